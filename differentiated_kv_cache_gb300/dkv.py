@@ -20,11 +20,14 @@ DKV_ERR_NO_PAGES, DKV_ERR_TABLE_FULL, DKV_ERR_TIMEOUT, DKV_ERR_CHECK, DKV_ERR_UN
 DKV_ERR_SCRATCH = -9
 DKV_ATTN_STATIC_SCRATCH_BYTES = 64 << 20
 DKV_PROMPT, DKV_DECODE = 0, 1
+DKV_F16, DKV_BF16 = 0, 1
+DKV_E4M3, DKV_INT8 = 0, 1
 
 EXPORTED = ("dkv_pool_create", "dkv_pool_destroy", "dkv_pool_geometry", "dkv_compact_step",
             "dkv_decode_attention", "dkv_decode_attention_static", "dkv_free_request", "dkv_pool_status", "dkv_pool_clear_error",
             "dkv_pool_export", "dkv_pool_set_thresholds", "dkv_pool_set_mid_thresholds", "dkv_prefill_attention",
-            "dkv_compact_step_prefilled", "dkv_strerror")
+            "dkv_compact_step_prefilled", "dkv_cache8_workspace", "dkv_cache8_append", "dkv_cache8_attention",
+            "dkv_cache8_prefill", "dkv_strerror")
 
 
 class dkv_config(C.Structure):
@@ -54,6 +57,16 @@ class dkv_status(C.Structure):
 class dkv_snapshot(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in ("pages", "free_list", "table", "head_counts", "req_state",
                                           "pointers")]
+
+
+class dkv_cache8(C.Structure):
+    """Descriptor of a uniform 8-bit cache (make_cache8 fills it and keeps the
+    tensors it points to)."""
+    _fields_ = [(n, C.c_int32) for n in ("n_kv_heads", "group_size", "head_dim", "block_tokens", "elem_type",
+                                         "code_type", "n_pages", "n_slots", "table_width", "rotary_dim",
+                                         "rotary_interleaved", "device")] + \
+        [(n, C.c_void_p) for n in ("pages", "scales", "tail", "page_table", "status", "workspace")] + \
+        [("workspace_bytes", C.c_int64)]
 
 
 class DkvError(RuntimeError):
@@ -90,6 +103,11 @@ def load() -> C.CDLL:
         L.dkv_pool_status.argtypes = [P, C.POINTER(dkv_status)]
         L.dkv_pool_clear_error.argtypes = [P]
         L.dkv_pool_export.argtypes = [P, C.POINTER(dkv_snapshot)]
+        L64, C8 = C.c_int64, C.POINTER(dkv_cache8)
+        L.dkv_cache8_workspace.argtypes = [C8, I, C.POINTER(C.c_int64)]
+        L.dkv_cache8_append.argtypes = [C8, I, P, P, P, P, L64, P, L64, P, L64, P, I, P, P, P]
+        L.dkv_cache8_attention.argtypes = [C8, I, P, P, P, L64, P, I, I, P]
+        L.dkv_cache8_prefill.argtypes = [C8, I, P, P, L64, P, L64, P, L64, P, I, I, P]
         L.dkv_strerror.argtypes = [C.c_int]
         L.dkv_strerror.restype = C.c_char_p
         for f in EXPORTED:
@@ -278,3 +296,151 @@ def dkv_pool_export(pool, cfg: dict, table_len: int, pages: bool = True, count_s
     snap.pages = out["pages"].ctypes.data if pages else None
     _check(load().dkv_pool_export(pool, C.byref(snap)), "dkv_pool_export")
     return out
+
+
+# ---- uniform 8-bit cache ----------------------------------------------------
+
+def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: int = 0, rotary_interleaved: bool = False,
+                max_req: int | None = None, status=None, workspace=None) -> dkv_cache8:
+    """Descriptor of a layer's uniform 8-bit cache over the caller's tensors:
+    pages [n_pages][Hkv][T/16][2][2048] (torch.float8_e4m3fn or torch.int8),
+    scales fp32 [n_pages][Hkv][2], tail [n_slots][Hkv][T/16][2][2048] (float16
+    or bfloat16), page_table int32 [n_slots][width]. The status words and the
+    workspace for attention calls of up to max_req requests (default: one a
+    slot, at most 1024) are allocated here unless given; layers whose calls are
+    ordered on one stream may share a workspace."""
+    import torch
+    codes = {torch.float8_e4m3fn: DKV_E4M3, torch.int8: DKV_INT8}
+    elems = {torch.float16: DKV_F16, torch.bfloat16: DKV_BF16}
+    if pages.dtype not in codes:
+        raise TypeError(f"pages must be torch.float8_e4m3fn or torch.int8, got {pages.dtype}")
+    if tail.dtype not in elems:
+        raise TypeError(f"tail must be float16 or bfloat16, got {tail.dtype}")
+    if pages.dim() != 5 or tail.dim() != 5 or page_table.dim() != 2:
+        raise ValueError("pages and tail have 5 dimensions, page_table has 2")
+    n_pages, hkv, sub = pages.shape[:3]
+    if tuple(pages.shape[3:]) != (2, 2048) or tuple(tail.shape[1:]) != (hkv, sub, 2, 2048):
+        raise ValueError("pages are [n_pages][Hkv][T/16][2][2048] and tail [n_slots][Hkv][T/16][2][2048]")
+    if tuple(scales.shape) != (n_pages, hkv, 2) or page_table.shape[0] != tail.shape[0]:
+        raise ValueError("scales are [n_pages][Hkv][2] and page_table [n_slots][width]")
+    c = dkv_cache8()
+    c.n_kv_heads, c.group_size, c.head_dim, c.block_tokens = hkv, group_size, 128, 16 * sub
+    c.elem_type, c.code_type = elems[tail.dtype], codes[pages.dtype]
+    c.n_pages, c.n_slots, c.table_width = n_pages, tail.shape[0], page_table.shape[1]
+    c.rotary_dim, c.rotary_interleaved = rotary_dim, int(bool(rotary_interleaved))
+    c.device = pages.device.index if pages.device.index is not None else 0
+    if status is None:
+        status = torch.zeros(2, dtype=torch.int32, device=pages.device)
+    if workspace is None:
+        n = C.c_int64()
+        _check(load().dkv_cache8_workspace(C.byref(c), min(c.n_slots, 1024) if max_req is None else int(max_req),
+                                           C.byref(n)), "dkv_cache8_workspace")
+        workspace = torch.zeros(n.value, dtype=torch.uint8, device=pages.device)
+    c.pages, c.scales = _on(c, pages, None, "pages"), _on(c, scales, torch.float32, "scales")
+    c.tail, c.page_table = _on(c, tail, None, "tail"), _on(c, page_table, torch.int32, "page_table")
+    c.status, c.workspace = _on(c, status, torch.int32, "status"), _on(c, workspace, torch.uint8, "workspace")
+    if status.numel() < 2:
+        raise ValueError("status has two words")
+    c.workspace_bytes = workspace.numel()
+    c.elem_dtype, c.status_words = tail.dtype, status
+    c.tensors = (pages, scales, tail, page_table, status, workspace)
+    return c
+
+
+def _on(cache, t, dtype, name):
+    """Address of a contiguous tensor on the cache's device (None -> NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device.index != cache.device:
+        raise TypeError(f"{name} must be a CUDA tensor on device {cache.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(cache, t, heads, n, name):
+    """Address and row stride of vectors [n][heads][128] of the cache's type."""
+    if not t.is_cuda or t.device.index != cache.device:
+        raise TypeError(f"{name} must be a CUDA tensor on device {cache.device}")
+    if t.dtype != cache.elem_dtype:
+        raise TypeError(f"{name} must be {cache.elem_dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be [{'tokens' if n is None else n}][{heads}][128], got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != 128):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), s[0] if t.shape[0] > 1 else max(s[0], heads * 128)
+
+
+def _stream8(cache, stream):
+    import torch
+    return (torch.cuda.current_stream(cache.device) if stream is None else stream).cuda_stream
+
+
+def dkv_cache8_append(cache: dkv_cache8, before, k, v, rope=None, n_new=None, slots=None, q=None, k_rot=None,
+                      q_rot=None, stream=None, check: bool = True) -> int:
+    """Append tokens to a uniform 8-bit cache: before (device int32 [n_req])
+    tokens are stored, n_new (host; None: one each) more come, keys and queries
+    turned by rope (fp32 [positions][rotary_dim / 2][2], cos and sin). k_rot and
+    q_rot receive the turned vectors."""
+    import torch
+    n_req = before.shape[0]
+    lens = None if n_new is None else _i32(n_new)
+    if lens is not None and lens.size != n_req:
+        raise ValueError("n_new and before have one entry per request")
+    total = n_req if lens is None else int(lens.sum(dtype=np.int64))
+    hkv, hq = cache.n_kv_heads, cache.n_kv_heads * cache.group_size
+    kp, ks = _rows(cache, k, hkv, total, "k")
+    vp, vs = _rows(cache, v, hkv, total, "v")
+    qp, qs = (None, 0) if q is None else _rows(cache, q, hq, total, "q")
+    if rope is not None and (rope.dim() != 3 or rope.shape[1] != cache.rotary_dim // 2 or rope.shape[2] != 2):
+        raise ValueError(f"rope must be [positions][{cache.rotary_dim // 2}][2]")
+    for t, like, name in ((k_rot, k, "k_rot"), (q_rot, q, "q_rot")):
+        if t is not None and (like is None or t.shape != like.shape):
+            raise ValueError(f"{name} must be shaped like its input")
+    if slots is not None and slots.numel() != n_req:
+        raise ValueError("slots and before have one entry per request")
+    rc = load().dkv_cache8_append(
+        C.byref(cache), n_req, None if lens is None else lens.ctypes.data, _on(cache, slots, torch.int32, "slots"),
+        _on(cache, before, torch.int32, "before"), kp, ks, vp, vs, qp, qs, _on(cache, rope, torch.float32, "rope"),
+        0 if rope is None else rope.shape[0], _on(cache, k_rot, cache.elem_dtype, "k_rot"),
+        _on(cache, q_rot, cache.elem_dtype, "q_rot"), _stream8(cache, stream))
+    return _check(rc, "dkv_cache8_append") if check else rc
+
+
+def dkv_cache8_attention(cache: dkv_cache8, seq_lens, q, out, window: int = 0, sinks: int = 0, slots=None,
+                         stream=None, check: bool = True) -> int:
+    """Decode attention of one query token per request over a uniform 8-bit
+    cache: seq_lens (device int32 [n_req]) tokens are stored; window = 0 sees
+    them all, else the last `window` and the first `sinks`."""
+    import torch
+    n_req, hq = seq_lens.shape[0], cache.n_kv_heads * cache.group_size
+    qp, qs = _rows(cache, q, hq, n_req, "q")
+    if out.shape != q.shape:
+        raise ValueError("out must be shaped like q")
+    if slots is not None and slots.numel() != n_req:
+        raise ValueError("slots and seq_lens have one entry per request")
+    rc = load().dkv_cache8_attention(C.byref(cache), n_req, _on(cache, slots, torch.int32, "slots"),
+                                     _on(cache, seq_lens, torch.int32, "seq_lens"), qp, qs,
+                                     _on(cache, out, cache.elem_dtype, "out"), window, sinks,
+                                     _stream8(cache, stream))
+    return _check(rc, "dkv_cache8_attention") if check else rc
+
+
+def dkv_cache8_prefill(cache: dkv_cache8, seq_lens, q, k, v, out, window: int = 0, sinks: int = 0, stream=None,
+                       check: bool = True) -> int:
+    """Causal attention over whole prompts (host lengths, requests back to
+    back) with an optional sliding window and first tokens that stay visible."""
+    lens = _i32(seq_lens)
+    total = int(lens.sum(dtype=np.int64))
+    hkv, hq = cache.n_kv_heads, cache.n_kv_heads * cache.group_size
+    qp, qs = _rows(cache, q, hq, total, "q")
+    kp, ks = _rows(cache, k, hkv, total, "k")
+    vp, vs = _rows(cache, v, hkv, total, "v")
+    if out.shape != q.shape:
+        raise ValueError("out must be shaped like q")
+    rc = load().dkv_cache8_prefill(C.byref(cache), lens.size, lens.ctypes.data, qp, qs, kp, ks, vp, vs,
+                                   _on(cache, out, cache.elem_dtype, "out"), window, sinks, _stream8(cache, stream))
+    return _check(rc, "dkv_cache8_prefill") if check else rc

@@ -395,6 +395,143 @@ int dkv_pool_clear_error(dkv_pool* pool);
 /* Synchronise and copy the device state into host buffers (see dkv_snapshot). */
 int dkv_pool_export(dkv_pool* pool, dkv_snapshot* out);
 
+/* ---- uniform 8-bit cache ---------------------------------------------------
+ * The cache without differentiation, for layers that are not worth
+ * compacting and as the baseline next to the pool: every token is kept, keys
+ * and values in 8 bits with one scale per (block of tokens, KV head), read in
+ * full or through a sliding window with a few first tokens that stay visible.
+ * Nothing is pruned, so page numbers follow from the lengths alone and the
+ * caller grants them; the calls therefore take a descriptor of buffers that
+ * the caller owns instead of a pool.
+ *
+ *  - A block is block_tokens = T tokens of one request. While it is incomplete
+ *    its tokens lie in the request's tail in 16 bits; the call that completes
+ *    it quantises it once, from the same 16-bit values, into its page. What
+ *    pages and open blocks hold does not depend on how tokens were cut into
+ *    calls. An append may step back (before[i] below the tokens stored so
+ *    far, e.g. after rejected guesses) as far as the open block's first
+ *    token: the 16-bit values of complete blocks are gone.
+ *  - Codes, per block, head and operand (K or V), fp32 arithmetic correctly
+ *    rounded: amax = the largest finite |x| of the T x 128 values,
+ *    s = max(fdiv(amax, Q), 2^-100) with Q = 448 (e4m3) or 127 (int8),
+ *    inv = fdiv(1, s), y = clamp(fmul(x, inv), -Q, Q), code = y rounded to
+ *    the nearest e4m3 value or integer, ties to even. The stored value is
+ *    s * code. Infinite inputs saturate; a NaN stays NaN (e4m3) or becomes 0
+ *    (int8). Other tokens of the block keep their values either way.
+ *  - A tile holds 16 consecutive tokens of one head: 2048 K entries, then
+ *    2048 V entries, of 8 bits (pages) or 16 bits (tails). Token i < 16,
+ *    feature f < 128: with (r, c, m) = (i, f % 16, f / 16) for K and
+ *    (f % 16, i, f / 16) for V, L = 4 (r % 8) + (c % 8) / 2 and
+ *    w = 4 (r / 8) + 2 (c / 8) + c % 2, the entry lies at
+ *      pages  (m / 2) 512 + 16 L + 8 (m % 2) + w
+ *      tails  256 m + 8 L + w
+ *    (the operand registers of a 16 x 16 matrix instruction, so that a warp
+ *    reads its operands with 16-byte loads and no transposition).
+ *  - slots, before and seq_lens are device arrays, read when the work runs: a
+ *    captured call can be replayed with other contents. A request with
+ *    before < 0 is skipped (padding); slots of one append must differ.
+ *  - Errors that only the device sees latch in status[0] (the first one;
+ *    status[1] = the request's index in the call): DKV_ERR_ARG (a slot
+ *    outside [0, n_slots), a slot given twice to an append, a position
+ *    outside the rotation table), DKV_ERR_TABLE_FULL (a length above
+ *    table_width * T), DKV_ERR_CHECK (a page number outside [0, n_pages)),
+ *    DKV_ERR_TIMEOUT. No bad index is followed. The call that latches an
+ *    error leaves its outputs undefined; while status[0] is non-zero, later
+ *    calls are device no-ops. The caller zeroes both words to go on.
+ *  - Calls on one cache must be ordered on one stream (or synchronised by the
+ *    caller). Attention calls that may overlap (two streams, two replayed
+ *    graphs) need a workspace each; appends and prompt attention use none. */
+#define DKV_F16  0   /* elem_type: k, v, q, out and tails are IEEE binary16 */
+#define DKV_BF16 1   /* elem_type: bfloat16                                  */
+#define DKV_E4M3 0   /* code_type: 8-bit floating point (4 exponent bits)    */
+#define DKV_INT8 1   /* code_type: signed integers in [-127, 127]            */
+
+typedef struct dkv_cache8 {
+  int32_t n_kv_heads;          /* Hkv                                          */
+  int32_t group_size;          /* G = query heads per KV head, 1..8            */
+  int32_t head_dim;            /* must be 128                                  */
+  int32_t block_tokens;        /* T: 16, 32, 64 or 128                         */
+  int32_t elem_type;           /* DKV_F16 or DKV_BF16                          */
+  int32_t code_type;           /* DKV_E4M3 or DKV_INT8                         */
+  int32_t n_pages;             /* pages (blocks of T tokens, every KV head)    */
+  int32_t n_slots;             /* request slots, at most 2^18                  */
+  int32_t table_width;         /* page-table entries of a slot                 */
+  int32_t rotary_dim;          /* features turned at the append: 0, or a
+                                  multiple of 16 up to 128                     */
+  int32_t rotary_interleaved;  /* 0: feature i turns with i + rotary_dim / 2;
+                                  1: feature 2i turns with 2i + 1              */
+  int32_t device;              /* CUDA device of every buffer                  */
+  void* pages;                 /* [n_pages][Hkv][T/16][2][2048] codes          */
+  float* scales;               /* [n_pages][Hkv][2]: K's and V's s             */
+  void* tail;                  /* [n_slots][Hkv][T/16][2][2048] elem_type      */
+  const int32_t* page_table;   /* [n_slots][table_width]                       */
+  int32_t* status;             /* [2], zeroed by the caller                    */
+  void* workspace;             /* dkv_cache8_workspace bytes, zeroed once by
+                                  the caller (every call leaves the zeros
+                                  that it found); NULL if no attention         */
+  int64_t workspace_bytes;
+} dkv_cache8;
+
+/* Bytes of workspace that dkv_cache8_attention needs for calls of up to
+ * max_req requests. The pointers of the descriptor may still be NULL. */
+int dkv_cache8_workspace(const dkv_cache8* cache, int32_t max_req, int64_t* bytes);
+
+/* Append tokens of n_req requests to a layer's cache, turning keys and queries
+ * on the way. Request i: slot slots[i] (slots device int32 [n_req], NULL: slot
+ * i), before[i] tokens stored so far (device int32 [n_req]), n_new[i] >= 1 new
+ * ones (host; NULL: one each) at positions before[i] .. before[i] + n_new[i]-1.
+ *   k, v    device [sum(n_new)][Hkv][128], requests back to back in call order;
+ *           token rows k_stride / v_stride elements apart (multiples of 8, at
+ *           least Hkv * 128), so that they may be parts of one projection.
+ *   q       NULL, or device [sum(n_new)][Hkv * G][128], rows q_stride apart.
+ *   rope    device fp32 [rope_len][rotary_dim / 2][2]: cos and sin of every
+ *           position's angles; NULL if and only if rotary_dim = 0. A turned pair
+ *           is (a c - b s, b c + a s) in fp32, every operation rounded, then
+ *           rounded to elem_type. Other features pass unchanged.
+ *   k_rot   NULL, or [sum(n_new)][Hkv][128] contiguous: the turned keys, e.g.
+ *           for dkv_cache8_prefill. q_rot: the same for q (both or neither).
+ *           k_rot = k and q_rot = q are allowed for contiguous k and q; the
+ *           buffers may overlap in no other way.
+ * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED (host, nothing queued);
+ * DKV_ERR_CUDA. */
+int dkv_cache8_append(const dkv_cache8* cache, int32_t n_req, const int32_t* n_new, const int32_t* slots,
+                      const int32_t* before, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                      const void* q, int64_t q_stride, const float* rope, int32_t rope_len, void* k_rot,
+                      void* q_rot, void* stream);
+
+/* Decode attention of one query token per request over the cache [Bkg-Attn]:
+ * with N = seq_lens[i] (device int32 [n_req]) tokens stored in slot slots[i]
+ * (device; NULL: slot i; a slot may occur more than once),
+ *   out[i][h] = sum_j softmax_j(q[i][h] . k^_j / sqrt(128)) v^_j
+ * over the visible tokens j < N: every one if window = 0, else the last
+ * `window` and the first `sinks` (j >= N - window or j < sinks). k^, v^ are
+ * the stored values (codes times scale in pages, 16 bits in the tail). A
+ * request with N <= 0 gets zeros. Tokens that are not visible are not read
+ * into the result, whatever they hold.
+ *   q       device [n_req][Hkv * G][128], rows q_stride elements apart.
+ *   out     device [n_req][Hkv * G][128] of elem_type, contiguous.
+ * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED, DKV_ERR_SCRATCH (workspace_bytes
+ * below dkv_cache8_workspace for n_req) (host, nothing queued); DKV_ERR_CUDA. */
+int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* slots, const int32_t* seq_lens,
+                         const void* q, int64_t q_stride, void* out, int32_t window, int32_t sinks,
+                         void* stream);
+
+/* Causal attention over whole prompts with the same window and first tokens:
+ * position p of request i (seq_lens[i] >= 1 tokens, host; back to back in call
+ * order) sees j <= p with window = 0, j > p - window or j < sinks. The cache
+ * supplies the head layout, elem_type, device and status only.
+ *   q, k, v  device [sum(seq_lens)][heads][128], token rows *_stride elements
+ *            apart (multiples of 8); out contiguous, of elem_type.
+ * Products accumulate in fp32; probabilities enter the value product rounded
+ * to elem_type. Values of other requests never enter a result; inside one
+ * request k and v must be finite (a non-finite v reaches the rows before it
+ * that share its 128-token tile).
+ * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED (host, nothing queued);
+ * DKV_ERR_CUDA. */
+int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* seq_lens, const void* q,
+                       int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       void* out, int32_t window, int32_t sinks, void* stream);
+
 /* Static description of an error code. */
 const char* dkv_strerror(int code);
 

@@ -1,0 +1,607 @@
+"""GPU tests of the uniform 8-bit cache (append with rotation, decode attention,
+prompt attention) against the plain reference of tests/cache8_ref.py: stored
+state bit for bit, attention against 64 bits within the bound derived in
+cache8_ref.tolerance."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from tests import cache8_ref as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+E4M3, INT8, F16, BF16 = torch.float8_e4m3fn, torch.int8, torch.float16, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    _dkv().build.build()
+    _dkv().load()
+
+
+def _dkv():
+    import differentiated_kv_cache_gb300 as dkv
+    return dkv
+
+
+class Cache:
+    """Tensors of a layer's cache, the descriptor and the reference beside them."""
+
+    def __init__(self, hkv, G, T, slots, width, elem, code, rot=0, inter=False, seed=0, fill=None, spare=3):
+        rng = np.random.default_rng(seed)
+        n = slots * width + spare
+        self.hkv, self.G, self.T, self.elem, self.slots = hkv, G, T, elem, slots
+        self.pages = torch.zeros((n, hkv, T // 16, 2, 2048), dtype=torch.uint8, device="cuda").view(code)
+        self.scales = torch.zeros((n, hkv, 2), device="cuda")
+        self.tail = torch.zeros((slots, hkv, T // 16, 2, 2048), dtype=elem, device="cuda")
+        if fill is not None:
+            self.tail.fill_(fill)
+        self.table = torch.from_numpy(rng.permutation(n)[:slots * width].astype(np.int32).reshape(slots, width)).cuda()
+        self.rot, self.inter = rot, inter
+        self.c = _dkv().make_cache8(self.pages, self.scales, self.tail, self.table, group_size=G, rotary_dim=rot,
+                                    rotary_interleaved=inter)
+        self.ref = ref.RefCache(self.pages, self.scales, self.tail, self.table, rot, inter)
+        ang = np.arange(width * T)[:, None] * 10000.0 ** (-np.arange(0, rot, 2) / max(rot, 1))
+        self.rope_np = np.stack([np.cos(ang), np.sin(ang)], -1).astype(np.float32) if rot else None
+        self.rope = torch.from_numpy(self.rope_np).cuda() if rot else None
+
+    def vec(self, rng, n, heads, scale=1.0):
+        x = rng.standard_normal((n, heads, 128)).astype(np.float32) * scale
+        x[:, :, rng.integers(0, 128, 3)] *= 8
+        return torch.from_numpy(x).to(self.elem).cuda()
+
+    def append(self, slots, before, new, k, v, q=None, k_rot=None, q_rot=None, step=False, **kw):
+        i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+        rc = _dkv().dkv_cache8_append(self.c, i32(before), k, v, rope=self.rope, n_new=None if step else new,
+                                      slots=None if slots is None else i32(slots), q=q, k_rot=k_rot, q_rot=q_rot, **kw)
+        at, turned = 0, []
+        kn, vn = ref.elem_np(k), ref.elem_np(v)
+        for s, b, n in zip(slots if slots is not None else range(len(before)), before, new):
+            if b >= 0:
+                turned.append(self.ref.append(s, b, kn[at:at + n], vn[at:at + n], self.rope_np))
+            else:
+                turned.append(None)
+            at += n
+        return rc, turned
+
+    def check(self):
+        torch.cuda.synchronize()
+        assert self.c.status_words.tolist() == [0, 0]
+        self.ref.check(self.pages, self.scales, self.tail)
+
+    def attend(self, slots, lens, q, window=0, sinks=0, out=None, **kw):
+        i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+        out = torch.full_like(q, float("nan"), memory_format=torch.contiguous_format) if out is None else out
+        _dkv().dkv_cache8_attention(self.c, i32(lens), q, out, window=window, sinks=sinks,
+                                    slots=None if slots is None else i32(slots), **kw)
+        return out
+
+    def check_attention(self, out, slots, lens, q, window=0, sinks=0):
+        got, qn = out.double().cpu().numpy(), q.double().cpu().numpy()
+        for i, (s, n) in enumerate(zip(slots, lens)):
+            see = ref.visible(max(n, 0), window, sinks)
+            for h in range(self.hkv):
+                k, v = self.ref.values(s, max(n, 0), h)
+                g = slice(h * self.G, (h + 1) * self.G)
+                want, pv, qk, vm = ref.attend(qn[i, g], k[see], v[see])
+                tol = ref.tolerance(want, pv, qk, vm, len(see), self.elem, 2.0 ** -11)
+                err = np.abs(got[i, g] - want)
+                assert (err <= tol).all(), (i, h, n, float((err / tol).max()))
+
+
+# ------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("elem,code", [(F16, E4M3), (F16, INT8), (BF16, E4M3), (BF16, INT8)])
+@pytest.mark.parametrize("T", [16, 32, 64, 128])
+def test_append_in_pieces_gives_the_same_state(elem, code, T):
+    """One token, odd pieces across block borders and whole blocks, two requests
+    in crossed slots; the other places of the tails (NaN here) stay."""
+    rng = np.random.default_rng(T)
+    c = Cache(2, 3, T, 4, 5, elem, code, rot=64, inter=T % 64 == 0, fill=float("nan"), seed=T)
+    at = {3: 0, 1: 0}
+    for a, b in [(1, T - 1), (T // 2 + 1, 1), (1, 2), (2 * T, T), (3, T + 5), (T // 2, 1)]:
+        n = a + b
+        k, v, q = c.vec(rng, n, 2), c.vec(rng, n, 2), c.vec(rng, n, 6)
+        kr, qr = torch.full_like(k, 7.0), torch.full_like(q, 7.0)
+        rc, turned = c.append([3, 1], [at[3], at[1]], [a, b], k, v, q, kr, qr)
+        assert rc == 0
+        assert np.array_equal(ref.elem_np(kr), np.concatenate(turned))
+        pos = np.concatenate([np.arange(at[3], at[3] + a), np.arange(at[1], at[1] + b)])
+        assert np.array_equal(ref.elem_np(qr), ref.rotate(ref.elem_np(q), pos, c.rope_np, 64, c.inter, elem))
+        at[3] += a
+        at[1] += b
+        c.check()
+
+
+@pytest.mark.parametrize("elem,code", [(F16, E4M3), (BF16, INT8)])
+def test_steps_equal_one_call(elem, code):
+    """130 calls of one token and one call of 130 tokens leave the same bits."""
+    rng = np.random.default_rng(5)
+    a, b = (Cache(3, 2, 32, 2, 6, elem, code, rot=128, seed=9) for _ in range(2))
+    k, v = a.vec(rng, 260, 3), a.vec(rng, 260, 3)
+    b.append(None, [0, 0], [130, 130], k, v)
+    for p in range(130):
+        rows = torch.tensor([p, 130 + p], device="cuda")
+        a.append(None, [p, p], [1, 1], k[rows], v[rows], step=True)
+    a.check()
+    b.check()
+    # what stays in a tail after its block is complete depends on the calls;
+    # the pages, scales and open blocks do not
+    assert torch.equal(a.pages.view(torch.uint8), b.pages.view(torch.uint8)) and torch.equal(a.scales, b.scales)
+    open_k = [ref.from_tiles(ref.elem_np(x.tail)[1, 2], 16)[:, :130 % 32] for x in (a, b)]
+    assert np.array_equal(*open_k)
+
+
+@pytest.mark.parametrize("rot,inter", [(0, False), (16, False), (16, True), (48, False), (96, True), (128, False), (128, True)])
+@pytest.mark.parametrize("G", [1, 7])
+def test_rotations(rot, inter, G):
+    rng = np.random.default_rng(rot)
+    for elem in (F16, BF16):
+        c = Cache(2, G, 16, 3, 20, elem, E4M3, rot=rot, inter=inter)
+        n = [70, 1, 33]
+        k, v, q = c.vec(rng, sum(n), 2), c.vec(rng, sum(n), 2), c.vec(rng, sum(n), 2 * G)
+        qr, kr = torch.empty_like(q), torch.empty_like(k)
+        _, turned = c.append([2, 0, 1], [0, 0, 0], n, k, v, q, kr, qr)
+        c.check()
+        pos = np.concatenate([np.arange(x) for x in n])
+        assert np.array_equal(ref.elem_np(qr), ref.rotate(ref.elem_np(q), pos, c.rope_np, rot, inter, elem))
+        assert np.array_equal(ref.elem_np(kr), np.concatenate(turned))
+
+
+def test_parts_of_one_projection_and_in_place():
+    """q, k, v as parts of one [tokens][q | k | v] projection; contiguous q and k
+    turned in place."""
+    rng = np.random.default_rng(3)
+    c = Cache(2, 4, 32, 2, 4, BF16, E4M3, rot=128)
+    qkv = c.vec(rng, 50, 12)
+    q, k, v = qkv[:, :8], qkv[:, 8:10], qkv[:, 10:]
+    qr = torch.empty((50, 8, 128), dtype=BF16, device="cuda")
+    c.append(None, [0, 0], [20, 30], k, v, q, None, qr)
+    c.check()
+    d = Cache(2, 4, 32, 2, 4, BF16, E4M3, rot=128)
+    q2, k2 = q.contiguous(), k.contiguous()
+    kn = ref.elem_np(k2)
+    before = torch.zeros(2, dtype=torch.int32, device="cuda")
+    _dkv().dkv_cache8_append(d.c, before, k2, v, rope=d.rope, n_new=[20, 30], q=q2, k_rot=k2, q_rot=q2)
+    torch.cuda.synchronize()
+    assert torch.equal(q2, qr)
+    assert torch.equal(c.pages.view(torch.uint8), d.pages.view(torch.uint8)) and torch.equal(c.tail, d.tail)
+    pos = np.concatenate([np.arange(20), np.arange(30)])
+    assert np.array_equal(ref.elem_np(k2), ref.rotate(kn, pos, d.rope_np, 128, False, BF16))
+
+
+@pytest.mark.parametrize("elem,code", [(F16, E4M3), (F16, INT8), (BF16, E4M3), (BF16, INT8)])
+def test_special_values(elem, code):
+    """Zero blocks, tiny and huge values, infinities and NaN: codes as the header
+    says, other tokens of the block undisturbed."""
+    c = Cache(1, 1, 16, 1, 8, elem, code)
+    big = torch.finfo(elem).max
+    x = torch.randn((8 * 16, 1, 128), generator=torch.Generator().manual_seed(1)).to(elem)
+    x[16:32] = 0
+    x[32:48] *= torch.finfo(elem).tiny
+    x[48:64] *= big / 8
+    x[70, 0, 3], x[71, 0, 4], x[72, 0, 5] = float("inf"), float("-inf"), float("nan")
+    x[80:96] = float("nan")
+    x[100] = -0.0
+    x[112:] = float("inf")
+    y = x.flip(0).contiguous()
+    c.append(None, [0], [128], x.cuda(), y.cuda())
+    c.check()
+
+
+def test_padding_rows_are_skipped():
+    rng = np.random.default_rng(8)
+    c = Cache(2, 2, 16, 5, 4, F16, E4M3, rot=32, fill=3.0)
+    n = [4, 1, 20]
+    k, v, q = c.vec(rng, 25, 2), c.vec(rng, 25, 2), c.vec(rng, 25, 4)
+    qr = torch.full_like(q, 9.0)
+    c.append([4, 4, 0], [0, -1, 0], n, k, v, q, None, qr)
+    c.check()
+    assert (qr[4] == 9).all() and not (qr[5:] == 9).all()
+    c.append([4, 4, 0], [4, -1, 20], [1, 1, 1], k[:3], v[:3], step=True)
+    c.check()
+
+
+# ------------------------------------------------------------------ attention
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200, 255, 256, 257, 383, 500]
+
+
+def filled(hkv, G, T, elem, code, lens, seed=0, scale=1.0, fill=float("nan")):
+    rng = np.random.default_rng(seed)
+    c = Cache(hkv, G, T, len(lens), max(1, -(-max(lens) // T)), elem, code, seed=seed, fill=fill)
+    slots = [int(x) for x in rng.permutation(len(lens))]
+    some = [i for i, n in enumerate(lens) if n > 0]
+    new = [lens[i] for i in some]
+    k, v = c.vec(rng, sum(new), hkv, scale), c.vec(rng, sum(new), hkv)
+    c.append([slots[i] for i in some], [0] * len(some), new, k, v)
+    return c, slots, c.vec(rng, len(lens), hkv * G)
+
+
+@pytest.mark.parametrize("T,G,elem,code", [(16, 4, F16, E4M3), (32, 1, F16, INT8), (64, 8, BF16, E4M3), (128, 5, BF16, INT8),
+                                           (64, 4, F16, E4M3), (128, 7, F16, INT8), (16, 2, BF16, INT8), (32, 3, BF16, E4M3)])
+def test_attention_lengths(T, G, elem, code):
+    """Every length at block and tile borders, from empty; unwritten tail places
+    hold NaN."""
+    c, slots, q = filled(2, G, T, elem, code, LENS, seed=G)
+    out = c.attend(slots, LENS, q)
+    c.check()
+    c.check_attention(out, slots, LENS, q)
+    assert (out[0] == 0).all()
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 3), (16, 0), (17, 4), (64, 64), (100, 16), (100, 33), (250, 200),
+                                          (499, 1), (500, 7), (10000, 4), (0, 9)])
+def test_attention_window_and_first_tokens(window, sinks):
+    for T, G, elem, code in ((32, 4, F16, E4M3), (128, 6, BF16, INT8)):
+        c, slots, q = filled(2, G, T, elem, code, LENS, seed=window)
+        out = c.attend(slots, LENS, q, window, sinks)
+        torch.cuda.synchronize()
+        assert c.c.status_words.tolist() == [0, 0]
+        c.check_attention(out, slots, LENS, q, window, sinks)
+
+
+def test_attention_ignores_what_is_not_visible():
+    """Tokens outside the window and the first ones hold infinities and NaN, in
+    blocks that a visible token shares too: the result does not change."""
+    T, lens, window, sinks = 32, [150, 149, 97, 40], 21, 3
+    rng = np.random.default_rng(4)
+    for elem, code in ((F16, E4M3), (BF16, E4M3), (BF16, INT8)):
+        outs = []
+        base = Cache(1, 4, T, 4, 5, elem, code)
+        k, v, q = base.vec(rng, sum(lens), 1), base.vec(rng, sum(lens), 1), base.vec(rng, 4, 4)
+        for bad in (False, True):
+            c = Cache(1, 4, T, 4, 5, elem, code)
+            kk, vv = k.clone(), v.clone()
+            at = 0
+            for n in lens:
+                hidden = [j for j in range(n) if j not in set(ref.visible(n, window, sinks))]
+                if bad:
+                    kk[at + np.array(hidden[::2])], vv[at + np.array(hidden[::2])] = float("nan"), float("inf")
+                    kk[at + np.array(hidden[1::2])], vv[at + np.array(hidden[1::2])] = float("-inf"), float("nan")
+                else:
+                    kk[at + np.array(hidden)] = vv[at + np.array(hidden)] = 0.0
+                at += n
+            c.append(None, [0] * 4, lens, kk, vv)
+            outs.append(c.attend(None, lens, q, window, sinks))
+            c.check_attention(outs[-1], range(4), lens, q, window, sinks)
+        assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("scale", [1e-3, 30.0])
+def test_attention_of_flat_and_sharp_rows(scale):
+    """Near-uniform weights and rows that one token takes alone, with V blocks of
+    very different scales and V rows of zeros."""
+    for elem, code in ((F16, E4M3), (BF16, INT8)):
+        rng = np.random.default_rng(6)
+        lens = [700, 64, 333]
+        c = Cache(2, 4, 64, 3, 11, elem, code)
+        k, v, q = c.vec(rng, sum(lens), 2, scale), c.vec(rng, sum(lens), 2), c.vec(rng, 3, 8)
+        f = torch.ones(sum(lens), 1, 1, device="cuda")
+        f[64:128], f[128:192], f[200:300], f[300:310] = 1e-4, 0.0, 100.0, 1e-6
+        v = (v.float() * f).to(elem)
+        c.append(None, [0, 0, 0], lens, k, v)
+        out = c.attend(None, lens, q)
+        c.check_attention(out, range(3), lens, q)
+
+
+@pytest.mark.parametrize("amp", [1e-30, 1e-12, 1e12])
+def test_attention_bf16_amplitudes(amp):
+    """Values far from 1 in every block and in the tail (bf16's range)."""
+    rng = np.random.default_rng(2)
+    lens = [100, 40, 7]
+    c = Cache(1, 3, 32, 3, 4, BF16, E4M3)
+    k = c.vec(rng, sum(lens), 1)
+    v = (c.vec(rng, sum(lens), 1).float() * amp).to(BF16)
+    q = (c.vec(rng, 3, 3).float() * 1e-3).to(BF16)
+    k = (k.float() * 1e3).to(BF16)
+    c.append(None, [0] * 3, lens, k, v)
+    out = c.attend(None, lens, q)
+    c.check_attention(out, range(3), lens, q)
+
+
+def test_attention_strided_queries_same_slot_twice_and_longer_batch():
+    """Rows of a projection as q; a slot given twice with other lengths; rows of
+    out behind the batch untouched."""
+    c, slots, _ = filled(2, 4, 32, F16, E4M3, [300, 90, 10], seed=1)
+    rng = np.random.default_rng(1)
+    wide = c.vec(rng, 4, 12)
+    q = wide[:, :8]
+    who, lens = [slots[0], slots[1], slots[0], slots[2]], [300, 77, 256, 10]
+    # 256 tokens of the first slot end at a block border; 77 of 90: the tail
+    # holds tokens 64..89
+    out = torch.full((6, 8, 128), 5.0, dtype=F16, device="cuda")
+    c.attend(who, lens, q, out=out[:4])
+    c.check_attention(out[:4], who, lens, q)
+    assert (out[4:] == 5).all()
+
+
+def test_long_context_and_many_requests():
+    lens = [5000] + [int(x) for x in np.random.default_rng(0).integers(1, 90, 60)]
+    c, slots, q = filled(1, 4, 64, F16, INT8, lens, seed=3)
+    for window, sinks in ((0, 0), (1000, 5)):
+        out = c.attend(slots, lens, q, window, sinks)
+        c.check_attention(out, slots, lens, q, window, sinks)
+
+
+def test_calls_repeat_bit_for_bit():
+    lens = [1500, 20, 700, 1, 333]
+    c, slots, q = filled(4, 7, 32, BF16, E4M3, lens, seed=3)
+    first = c.attend(slots, lens, q)
+    for _ in range(20):
+        assert torch.equal(first, c.attend(slots, lens, q))
+
+
+# ------------------------------------------------------------------ errors
+
+def test_device_errors_latch_and_stop_later_calls():
+    dkv = _dkv()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(1)
+
+    def fresh():
+        c = Cache(2, 2, 16, 3, 3, F16, E4M3, rot=32)
+        k, v = c.vec(rng, 9, 2), c.vec(rng, 9, 2)
+        return c, k, v
+
+    def state(c):
+        torch.cuda.synchronize()
+        return c.c.status_words.tolist()
+
+    for slots, before, n_new, want in (([0, 3], [0, 0], [3, 6], [dkv.DKV_ERR_ARG, 1]),
+                                       ([-1, 2], [0, 0], [3, 6], [dkv.DKV_ERR_ARG, 0]),
+                                       ([0, 1], [0, 43], [3, 6], [dkv.DKV_ERR_TABLE_FULL, 1]),
+                                       ([0, 1], [0, 2 ** 31 - 1], [3, 6], [dkv.DKV_ERR_TABLE_FULL, 1])):
+        c, k, v = fresh()
+        dkv.dkv_cache8_append(c.c, i32(before), k, v, rope=c.rope, n_new=n_new, slots=i32(slots))
+        assert state(c) == want
+        # nothing else runs until the words are zeroed
+        pages, tail = c.pages.clone(), c.tail.clone()
+        dkv.dkv_cache8_append(c.c, i32([0]), k[:5], v[:5], rope=c.rope, n_new=[5])
+        out = torch.full((1, 4, 128), 3.0, dtype=F16, device="cuda")
+        dkv.dkv_cache8_attention(c.c, i32([0]), torch.cat((k[:1], v[:1]), 1), out)
+        dkv.dkv_cache8_prefill(c.c, [1], out.clone(), k[:1], v[:1], out)
+        assert state(c) == want and (out == 3).all()
+        assert torch.equal(c.tail, tail) and torch.equal(c.pages.view(torch.uint8), pages.view(torch.uint8))
+        c.c.status_words.zero_()
+        dkv.dkv_cache8_attention(c.c, i32([0]), torch.cat((k[:1], v[:1]), 1), out)
+        assert state(c) == [0, 0] and (out == 0).all()
+    for step in (False, True):
+        c, k, v = fresh()
+        dkv.dkv_cache8_append(c.c, i32([0, 0]), k[:2], v[:2], rope=c.rope, n_new=None if step else [1, 1], slots=i32([2, 2]))
+        assert state(c) == [dkv.DKV_ERR_ARG, state(c)[1]] and state(c)[1] in (0, 1)
+    c, k, v = fresh()
+    dkv.dkv_cache8_append(c.c, i32([40]), k, v, rope=c.rope[:44], n_new=[9])     # a table of 44 positions
+    assert state(c)[0] in (dkv.DKV_ERR_ARG, dkv.DKV_ERR_TABLE_FULL)
+    c, k, v = fresh()
+    dkv.dkv_cache8_append(c.c, i32([30]), k, v, rope=c.rope[:38], n_new=[9])
+    assert state(c) == [dkv.DKV_ERR_ARG, 0]
+    for bad in (-1, 12, 2 ** 30):
+        c, k, v = fresh()
+        c.table[1, 0] = bad
+        dkv.dkv_cache8_append(c.c, i32([0, 8]), k[:9], v[:9], rope=c.rope, n_new=[1, 8])
+        assert state(c) == [dkv.DKV_ERR_CHECK, 1]
+        c.c.status_words.zero_()
+        out = torch.empty((2, 4, 128), dtype=F16, device="cuda")
+        dkv.dkv_cache8_attention(c.c, i32([1, 20]), torch.randn((2, 4, 128), device="cuda").half(), out)
+        assert state(c) == [dkv.DKV_ERR_CHECK, 1]
+    for slots, lens, want in (([0, 3], [1, 1], dkv.DKV_ERR_ARG), ([0, 1], [1, 49], dkv.DKV_ERR_TABLE_FULL),
+                              ([0, 1], [1, 2 ** 31 - 1], dkv.DKV_ERR_TABLE_FULL)):
+        c, k, v = fresh()
+        out = torch.empty((2, 4, 128), dtype=F16, device="cuda")
+        dkv.dkv_cache8_attention(c.c, i32(lens), torch.randn((2, 4, 128), device="cuda").half(), out, slots=i32(slots))
+        assert state(c) == [want, 1]
+
+
+def test_short_workspace_and_binding_checks():
+    dkv = _dkv()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    c = Cache(2, 2, 16, 4, 3, F16, E4M3)
+    q = torch.zeros((4, 4, 128), dtype=F16, device="cuda")
+    c.c.workspace_bytes -= 1
+    assert dkv.dkv_cache8_attention(c.c, i32([0] * 4), q, torch.empty_like(q), check=False) == dkv.DKV_ERR_SCRATCH
+    c.c.workspace_bytes += 1
+    k = torch.zeros((4, 2, 128), dtype=F16, device="cuda")
+    with pytest.raises(TypeError):
+        dkv.dkv_cache8_append(c.c, i32([0] * 4), k.bfloat16(), k)
+    with pytest.raises(TypeError):
+        dkv.dkv_cache8_append(c.c, i32([0] * 4).cpu(), k, k)
+    with pytest.raises(TypeError):
+        dkv.dkv_cache8_append(c.c, i32([0] * 4).long(), k, k)
+    with pytest.raises(ValueError):
+        dkv.dkv_cache8_append(c.c, i32([0] * 4), k[:3], k)
+    with pytest.raises(ValueError):
+        dkv.dkv_cache8_append(c.c, i32([0] * 4), k, k.transpose(0, 1).contiguous().transpose(0, 1))
+    with pytest.raises(ValueError):
+        dkv.dkv_cache8_append(c.c, i32([0] * 4), k, k, slots=i32([0]))
+    with pytest.raises(ValueError):
+        dkv.dkv_cache8_attention(c.c, i32([0] * 4), k, torch.empty_like(q))
+    with pytest.raises(ValueError):
+        dkv.dkv_cache8_attention(c.c, i32([0] * 4), q, torch.empty((4, 8, 128), dtype=F16, device="cuda")[:, ::2])
+    with pytest.raises(ValueError):
+        dkv.dkv_cache8_prefill(c.c, [2, 1], q, k, k, torch.empty_like(q))
+    with pytest.raises(ValueError):
+        dkv.make_cache8(c.pages, c.scales[:2], c.tail, c.table, group_size=2)
+
+
+# ------------------------------------------------------------------ prompt attention
+
+def prefill_case(hkv, G, lens, elem, window, sinks, seed=0, bad=None):
+    rng = np.random.default_rng(seed)
+    c = Cache(hkv, G, 16, 1, 1, elem, E4M3)
+    n = sum(lens)
+    q, k, v = c.vec(rng, n, hkv * G), c.vec(rng, n, hkv), c.vec(rng, n, hkv)
+    if bad is not None:       # one request's keys and values are not finite
+        a = sum(lens[:bad])
+        k[a:a + lens[bad]], v[a:a + lens[bad]] = float("nan"), float("inf")
+    out = torch.full_like(q, float("nan"))
+    _dkv().dkv_cache8_prefill(c.c, lens, q, k, v, out, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert c.c.status_words.tolist() == [0, 0]
+    qn, kn, vn, got = (x.double().cpu().numpy() for x in (q, k, v, out))
+    at = 0
+    for i, m in enumerate(lens):
+        rows = range(m) if m <= 300 else sorted({0, 1, 15, 16, 31, 32, 63, 64, 127, 128, 129, 255, 256, m // 2, m - 129,
+                                                 m - 128, m - 2, m - 1, window - 1, window, window + 1} & set(range(m)))
+        for p in rows if i != bad else ():
+            see = at + ref.visible(p + 1, window, sinks)
+            for h in range(hkv):
+                g = slice(h * G, (h + 1) * G)
+                want, pv, qk, vm = ref.attend(qn[at + p, g], kn[see, h], vn[see, h])
+                tol = ref.tolerance(want, pv, qk, vm, len(see), elem, torch.finfo(elem).eps / 2)
+                err = np.abs(got[at + p, g] - want)
+                assert (err <= tol).all(), (i, p, h, float((err / tol).max()))
+        at += m
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("elem", [F16, BF16])
+def test_prefill_groups(G, elem):
+    prefill_case(2, G, [1, 37, 130, 260], elem, 0, 0, seed=G)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 3), (31, 0), (64, 4), (128, 0), (129, 130), (200, 300), (255, 1),
+                                          (400, 16), (5000, 4)])
+def test_prefill_windows(window, sinks):
+    prefill_case(1, 4, [300, 17, 640, 2], F16, window, sinks, seed=window)
+    prefill_case(2, 5, [129, 290], BF16, window, sinks, seed=window)
+
+
+def test_prefill_long():
+    prefill_case(1, 8, [3000, 2049], F16, 0, 0)
+    prefill_case(1, 8, [3000, 2049], BF16, 700, 5)
+
+
+def test_prefill_requests_do_not_touch_each_other():
+    for bad in (0, 1, 2):
+        prefill_case(1, 4, [100, 77, 150], F16, 0, 0, seed=bad, bad=bad)
+        prefill_case(1, 7, [100, 77, 150], BF16, 40, 3, seed=bad, bad=bad)
+
+
+def test_prefill_parts_of_one_projection():
+    rng = np.random.default_rng(3)
+    c = Cache(2, 4, 16, 1, 1, F16, E4M3)
+    qkv = c.vec(rng, 333, 12)
+    q, k, v = qkv[:, :8], qkv[:, 8:10], qkv[:, 10:]
+    a, b = torch.empty((333, 8, 128), dtype=F16, device="cuda"), torch.empty((333, 8, 128), dtype=F16, device="cuda")
+    _dkv().dkv_cache8_prefill(c.c, [300, 33], q, k, v, a, window=100, sinks=2)
+    _dkv().dkv_cache8_prefill(c.c, [300, 33], q.contiguous(), k.contiguous(), v.contiguous(), b, window=100, sinks=2)
+    assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("elem,code,window,sinks", [(F16, E4M3, 0, 0), (BF16, INT8, 90, 4)])
+def test_prompt_then_generation(elem, code, window, sinks):
+    """Append with rotation, prompt attention over the turned vectors, then 70
+    generation steps (append, attention) queued without a wait between them."""
+    rng = np.random.default_rng(12)
+    hkv, G, T, lens, steps = 2, 4, 32, [150, 64, 31], 70
+    c = Cache(hkv, G, T, 3, 8, elem, code, rot=128)
+    n = sum(lens)
+    q, k, v = c.vec(rng, n, 8), c.vec(rng, n, 2), c.vec(rng, n, 2)
+    kr, qr, out = torch.empty_like(k), torch.empty_like(q), torch.empty_like(q)
+    slots = [1, 2, 0]
+    _, turned = c.append(slots, [0, 0, 0], lens, k, v, q, kr, qr)
+    _dkv().dkv_cache8_prefill(c.c, lens, qr, kr, v, out, window=window, sinks=sinks)
+    kn, vn, qn, got = (x.double().cpu().numpy() for x in (kr, v, qr, out))
+    at = 0
+    for m in lens:
+        for p in (0, m // 2, m - 1):
+            see = at + ref.visible(p + 1, window, sinks)
+            for h in range(hkv):
+                want, pv, qk, vm = ref.attend(qn[at + p, 4 * h:4 * h + 4], kn[see, h], vn[see, h])
+                tol = ref.tolerance(want, pv, qk, vm, len(see), elem, torch.finfo(elem).eps / 2)
+                assert (np.abs(got[at + p, 4 * h:4 * h + 4] - want) <= tol).all()
+        at += m
+    # the steps are queued first, then followed in the reference
+    data, outs = [], []
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    for s in range(steps):
+        x = [c.vec(rng, 3, 8), c.vec(rng, 3, 2), c.vec(rng, 3, 2)]
+        data.append((x, i32([m + s for m in lens]), i32([m + s + 1 for m in lens]), torch.empty_like(x[0])))
+        outs.append(torch.empty_like(x[0]))
+    sl = i32(slots)
+    torch.cuda.synchronize()
+    for (x, before, now, q_rot), o in zip(data, outs):
+        _dkv().dkv_cache8_append(c.c, before, x[1], x[2], rope=c.rope, slots=sl, q=x[0], q_rot=q_rot)
+        _dkv().dkv_cache8_attention(c.c, now, q_rot, o, window=window, sinks=sinks, slots=sl)
+    torch.cuda.synchronize()
+    for s, ((x, _, _, q_rot), o) in enumerate(zip(data, outs)):
+        for i, sl_i in enumerate(slots):
+            c.ref.append(sl_i, lens[i] + s, ref.elem_np(x[1])[i:i + 1], ref.elem_np(x[2])[i:i + 1], c.rope_np)
+        if s % 9 == 0 or s == steps - 1:
+            c.check_attention(o, slots, [m + s + 1 for m in lens], q_rot, window, sinks)
+    c.check()
+
+
+def test_captured_step_replays_with_other_contents():
+    """One captured append + attention, replayed over a generation with lengths,
+    slots and vectors written between the replays; a padded row skips."""
+    dkv = _dkv()
+    rng = np.random.default_rng(7)
+    c = Cache(2, 4, 16, 4, 6, F16, E4M3, rot=64)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    q, k, v = c.vec(rng, 3, 8), c.vec(rng, 3, 2), c.vec(rng, 3, 2)
+    before, now, slots, qr, out = i32([-1] * 3), i32([0] * 3), i32([0, 1, 2]), torch.empty_like(q), torch.empty_like(q)
+
+    def step():
+        dkv.dkv_cache8_append(c.c, before, k, v, rope=c.rope, slots=slots, q=q, q_rot=qr)
+        dkv.dkv_cache8_attention(c.c, now, qr, out, slots=slots, window=40, sinks=2)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    at = {0: 0, 1: 0, 2: 0, 3: 0}
+    for s in range(60):
+        who = [int(x) for x in rng.permutation(4)[:3]]
+        live = [s % 5 != 2, True, s % 7 != 3]
+        x = [c.vec(rng, 3, 8), c.vec(rng, 3, 2), c.vec(rng, 3, 2)]
+        for dst, src in zip((q, k, v), x):
+            dst.copy_(src)
+        slots.copy_(i32(who))
+        before.copy_(i32([at[w] if a else -1 for w, a in zip(who, live)]))
+        now.copy_(i32([at[w] + 1 if a else 0 for w, a in zip(who, live)]))
+        g.replay()
+        torch.cuda.synchronize()
+        for i, (w, a) in enumerate(zip(who, live)):
+            if a:
+                c.ref.append(w, at[w], ref.elem_np(x[1])[i:i + 1], ref.elem_np(x[2])[i:i + 1], c.rope_np)
+                at[w] += 1
+            else:
+                assert (out[i] == 0).all()
+        live_i = [i for i in range(3) if live[i]]
+        c.check_attention(out[live_i], [who[i] for i in live_i], [at[who[i]] for i in live_i], qr[live_i], 40, 2)
+    c.check()
+
+
+def test_other_streams_and_workspaces():
+    """Two caches on two streams at once, and one cache read by two streams with a
+    workspace each."""
+    dkv = _dkv()
+    lens = [900, 100, 1300]
+    c, slots, q = filled(4, 4, 64, F16, E4M3, lens, seed=1)
+    want = c.attend(slots, lens, q)
+    torch.cuda.synchronize()
+    other = dkv.make_cache8(c.pages, c.scales, c.tail, c.table, group_size=4)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    sl, ln = i32(slots), i32(lens)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.empty_like(q) for _ in range(40)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for a, b in zip(*outs):
+        dkv.dkv_cache8_attention(c.c, ln, q, a, slots=sl, stream=streams[0])
+        with torch.cuda.stream(streams[1]):
+            dkv.dkv_cache8_attention(other, ln, q, b, slots=sl)
+    torch.cuda.synchronize()
+    for o in outs[0] + outs[1]:
+        assert torch.equal(o, want)
