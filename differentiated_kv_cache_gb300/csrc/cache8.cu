@@ -2,6 +2,7 @@
 // (include/dkv.h) and the append kernels: rotation of keys and queries,
 // 16-bit tails, quantisation of completed blocks.
 #include <algorithm>
+#include <type_traits>
 
 #include "cache8.cuh"
 #include "dkv_kernels.cuh"
@@ -13,10 +14,10 @@ namespace {
 // first job and the number of blocks a request can touch.
 constexpr int kAppendReq = 1024;
 struct AppendCall {
-  int n_req;
   int tok0[kAppendReq + 1];
   int blk0[kAppendReq + 1];
 };
+struct StepCall {};              // one token each: nothing to pass
 
 // Four pair slots of a 128-feature row: features a0..a0+3 turn with
 // b0..b0+3 (rows split in halves) or the pairs lie inside a0..b0+3
@@ -205,20 +206,22 @@ __device__ __forceinline__ void put_v(uint16_t* buf, int i, int f0, uint4 v) {
 // STEP: one token per request, job = request. The block's 16-bit entries
 // gather in shared memory if this call completes it, else the new ones go to
 // the tail. The G query heads of the KV head turn with the same angles.
-template <int ELEM, int CODE, bool STEP>
-__global__ void k_append8(Cache8View c, Append8Args a, int n_req, const __grid_constant__ AppendCall call) {
+template <int ELEM, int CODE, typename Call>
+__global__ void k_append8(Cache8View c, Append8Args a, int n_req, const __grid_constant__ Call call) {
+  constexpr bool STEP = std::is_same<Call, StepCall>::value;
   extern __shared__ __align__(16) uint8_t sm[];
   pdl_launch_dependents();
   pdl_wait();
   if (c.noop()) return;
-  const int jobs = STEP ? n_req : call.blk0[n_req];
+  int jobs = n_req;
+  if constexpr (!STEP) jobs = call.blk0[n_req];
   if ((int)blockIdx.x == jobs * c.hkv) {
     check_slots(c, a, n_req, reinterpret_cast<uint32_t*>(sm));
     return;
   }
   const int job = blockIdx.x / c.hkv, h = blockIdx.x % c.hkv;
   int i = job, row0 = job, n = 1, jb = 0;
-  if (!STEP) {
+  if constexpr (!STEP) {
     int lo = 0, hi = n_req;      // the request whose jobs hold this one
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -301,25 +304,26 @@ __global__ void k_append8(Cache8View c, Append8Args a, int n_req, const __grid_c
 
 template <int ELEM, int CODE>
 cudaError_t append_typed(const Cache8View& c, const Append8Args& a, int n_req, const int32_t* n_new, cudaStream_t st) {
-  AppendCall call;
-  call.n_req = n_req;
-  long long jobs = n_req;
-  if (n_new) {
-    call.tok0[0] = call.blk0[0] = 0;
-    long long blk = 0;
-    for (int i = 0; i < n_req; i++) {
-      call.tok0[i + 1] = call.tok0[i] + n_new[i];
-      blk += (n_new[i] + c.T - 2) / c.T + 1;     // blocks that n tokens can touch
-      call.blk0[i + 1] = (int)blk;
-    }
-    jobs = blk;
-  }
   const size_t smem = std::max<size_t>((size_t)c.T * 4 * kD + 256, a.slots ? (size_t)(c.n_slots + 31) / 32 * 4 : 0);
-  auto kernel = n_new ? k_append8<ELEM, CODE, false> : k_append8<ELEM, CODE, true>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   const int threads = n_new ? std::min(512, 8 * c.T) : 128;
-  return launch_dependent(kernel, dim3((unsigned)(jobs * c.hkv + 1)), dim3(threads), smem, st, c, a, n_req, call);
+  const unsigned hkv = (unsigned)c.hkv;
+  cudaError_t e = cudaSuccess;
+  if (!n_new) {
+    auto kernel = k_append8<ELEM, CODE, StepCall>;
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kernel, dim3(n_req * hkv + 1), dim3(threads), smem, st, c, a, n_req, StepCall{});
+  }
+  AppendCall call;
+  call.tok0[0] = call.blk0[0] = 0;
+  for (int i = 0; i < n_req; i++) {
+    call.tok0[i + 1] = call.tok0[i] + n_new[i];
+    call.blk0[i + 1] = call.blk0[i] + (n_new[i] + c.T - 2) / c.T + 1;     // blocks that n tokens can touch
+  }
+  auto kernel = k_append8<ELEM, CODE, AppendCall>;
+  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kernel, dim3(call.blk0[n_req] * hkv + 1), dim3(threads), smem, st, c, a, n_req, call);
 }
 
 }  // namespace

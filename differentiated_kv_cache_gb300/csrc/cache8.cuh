@@ -70,8 +70,10 @@ __device__ __forceinline__ float amax_finite(float m, float x) {
   return a < INFINITY ? fmaxf(m, a) : m;      // false for infinities and NaN
 }
 
+// amax times the fp32 nearest 1 / Q (a code can then exceed Q by a rounding:
+// code_pair clamps it)
 __device__ __forceinline__ float block_scale(float amax, int code_type) {
-  return fmaxf(__fdiv_rn(amax, code_type == DKV_E4M3 ? 448.0f : 127.0f), kScaleFloor);
+  return fmaxf(__fmul_rn(amax, code_type == DKV_E4M3 ? 1.0f / 448.0f : 1.0f / 127.0f), kScaleFloor);
 }
 
 // Codes of two values (the first in the lower byte).

@@ -103,11 +103,11 @@ def load() -> C.CDLL:
         L.dkv_pool_status.argtypes = [P, C.POINTER(dkv_status)]
         L.dkv_pool_clear_error.argtypes = [P]
         L.dkv_pool_export.argtypes = [P, C.POINTER(dkv_snapshot)]
-        L64, C8 = C.c_int64, C.POINTER(dkv_cache8)
-        L.dkv_cache8_workspace.argtypes = [C8, I, C.POINTER(C.c_int64)]
-        L.dkv_cache8_append.argtypes = [C8, I, P, P, P, P, L64, P, L64, P, L64, P, I, P, P, P]
-        L.dkv_cache8_attention.argtypes = [C8, I, P, P, P, L64, P, I, I, P]
-        L.dkv_cache8_prefill.argtypes = [C8, I, P, P, L64, P, L64, P, L64, P, I, I, P]
+        L64 = C.c_int64
+        L.dkv_cache8_workspace.argtypes = [P, I, C.POINTER(C.c_int64)]
+        L.dkv_cache8_append.argtypes = [P, I, P, P, P, P, L64, P, L64, P, L64, P, I, P, P, P]
+        L.dkv_cache8_attention.argtypes = [P, I, P, P, P, L64, P, I, I, P]
+        L.dkv_cache8_prefill.argtypes = [P, I, P, P, L64, P, L64, P, L64, P, I, I, P]
         L.dkv_strerror.argtypes = [C.c_int]
         L.dkv_strerror.restype = C.c_char_p
         for f in EXPORTED:
@@ -343,6 +343,8 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
         raise ValueError("status has two words")
     c.workspace_bytes = workspace.numel()
     c.elem_dtype, c.status_words = tail.dtype, status
+    # plain copies of what every call reads
+    c.address, c.dev, c.heads, c.q_heads, c.pairs = C.addressof(c), c.device, hkv, hkv * group_size, rotary_dim // 2
     c.tensors = (pages, scales, tail, page_table, status, workspace)
     return c
 
@@ -351,9 +353,9 @@ def _on(cache, t, dtype, name):
     """Address of a contiguous tensor on the cache's device (None -> NULL)."""
     if t is None:
         return None
-    if not t.is_cuda or t.device.index != cache.device:
+    if t.get_device() != cache.device:
         raise TypeError(f"{name} must be a CUDA tensor on device {cache.device}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -362,21 +364,19 @@ def _on(cache, t, dtype, name):
 
 def _rows(cache, t, heads, n, name):
     """Address and row stride of vectors [n][heads][128] of the cache's type."""
-    if not t.is_cuda or t.device.index != cache.device:
-        raise TypeError(f"{name} must be a CUDA tensor on device {cache.device}")
-    if t.dtype != cache.elem_dtype:
-        raise TypeError(f"{name} must be {cache.elem_dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 128 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be [{'tokens' if n is None else n}][{heads}][128], got {tuple(t.shape)}")
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != 128):
+    if t.dtype is not cache.elem_dtype or t.get_device() != cache.dev:
+        raise TypeError(f"{name} must be a {cache.elem_dtype} tensor on device {cache.dev}, got {t.dtype} on {t.device}")
+    if t.shape != (n, heads, 128):
+        raise ValueError(f"{name} must be [{n}][{heads}][128], got {tuple(t.shape)}")
+    row, head, one = t.stride()
+    if one != 1 or (head != 128 and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), s[0] if t.shape[0] > 1 else max(s[0], heads * 128)
+    return t.data_ptr(), row if n > 1 else heads * 128
 
 
 def _stream8(cache, stream):
     import torch
-    return (torch.cuda.current_stream(cache.device) if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(cache.dev) if stream is None else stream.cuda_stream
 
 
 def dkv_cache8_append(cache: dkv_cache8, before, k, v, rope=None, n_new=None, slots=None, q=None, k_rot=None,
@@ -386,25 +386,25 @@ def dkv_cache8_append(cache: dkv_cache8, before, k, v, rope=None, n_new=None, sl
     turned by rope (fp32 [positions][rotary_dim / 2][2], cos and sin). k_rot and
     q_rot receive the turned vectors."""
     import torch
-    n_req = before.shape[0]
-    lens = None if n_new is None else _i32(n_new)
-    if lens is not None and lens.size != n_req:
-        raise ValueError("n_new and before have one entry per request")
-    total = n_req if lens is None else int(lens.sum(dtype=np.int64))
-    hkv, hq = cache.n_kv_heads, cache.n_kv_heads * cache.group_size
-    kp, ks = _rows(cache, k, hkv, total, "k")
-    vp, vs = _rows(cache, v, hkv, total, "v")
-    qp, qs = (None, 0) if q is None else _rows(cache, q, hq, total, "q")
-    if rope is not None and (rope.dim() != 3 or rope.shape[1] != cache.rotary_dim // 2 or rope.shape[2] != 2):
-        raise ValueError(f"rope must be [positions][{cache.rotary_dim // 2}][2]")
-    for t, like, name in ((k_rot, k, "k_rot"), (q_rot, q, "q_rot")):
-        if t is not None and (like is None or t.shape != like.shape):
-            raise ValueError(f"{name} must be shaped like its input")
+    n_req, i32 = before.numel(), torch.int32
+    lens, total = None, n_req
+    if n_new is not None:
+        lens = _i32(n_new)
+        total = int(lens.sum(dtype=np.int64))
+        if lens.size != n_req:
+            raise ValueError("n_new and before have one entry per request")
+    kp, ks = _rows(cache, k, cache.heads, total, "k")
+    vp, vs = _rows(cache, v, cache.heads, total, "v")
+    qp, qs = (None, 0) if q is None else _rows(cache, q, cache.q_heads, total, "q")
+    if k_rot is not None and k_rot.shape != k.shape or q_rot is not None and (q is None or q_rot.shape != q.shape):
+        raise ValueError("k_rot and q_rot must be shaped like k and q")
     if slots is not None and slots.numel() != n_req:
         raise ValueError("slots and before have one entry per request")
+    if rope is not None and rope.shape[1:] != (cache.pairs, 2):
+        raise ValueError(f"rope must be [positions][{cache.pairs}][2]")
     rc = load().dkv_cache8_append(
-        C.byref(cache), n_req, None if lens is None else lens.ctypes.data, _on(cache, slots, torch.int32, "slots"),
-        _on(cache, before, torch.int32, "before"), kp, ks, vp, vs, qp, qs, _on(cache, rope, torch.float32, "rope"),
+        cache.address, n_req, None if lens is None else lens.ctypes.data, _on(cache, slots, i32, "slots"),
+        _on(cache, before, i32, "before"), kp, ks, vp, vs, qp, qs, _on(cache, rope, torch.float32, "rope"),
         0 if rope is None else rope.shape[0], _on(cache, k_rot, cache.elem_dtype, "k_rot"),
         _on(cache, q_rot, cache.elem_dtype, "q_rot"), _stream8(cache, stream))
     return _check(rc, "dkv_cache8_append") if check else rc
@@ -416,13 +416,13 @@ def dkv_cache8_attention(cache: dkv_cache8, seq_lens, q, out, window: int = 0, s
     cache: seq_lens (device int32 [n_req]) tokens are stored; window = 0 sees
     them all, else the last `window` and the first `sinks`."""
     import torch
-    n_req, hq = seq_lens.shape[0], cache.n_kv_heads * cache.group_size
-    qp, qs = _rows(cache, q, hq, n_req, "q")
+    n_req = seq_lens.numel()
+    qp, qs = _rows(cache, q, cache.q_heads, n_req, "q")
     if out.shape != q.shape:
         raise ValueError("out must be shaped like q")
     if slots is not None and slots.numel() != n_req:
         raise ValueError("slots and seq_lens have one entry per request")
-    rc = load().dkv_cache8_attention(C.byref(cache), n_req, _on(cache, slots, torch.int32, "slots"),
+    rc = load().dkv_cache8_attention(cache.address, n_req, _on(cache, slots, torch.int32, "slots"),
                                      _on(cache, seq_lens, torch.int32, "seq_lens"), qp, qs,
                                      _on(cache, out, cache.elem_dtype, "out"), window, sinks,
                                      _stream8(cache, stream))
@@ -435,12 +435,11 @@ def dkv_cache8_prefill(cache: dkv_cache8, seq_lens, q, k, v, out, window: int = 
     back) with an optional sliding window and first tokens that stay visible."""
     lens = _i32(seq_lens)
     total = int(lens.sum(dtype=np.int64))
-    hkv, hq = cache.n_kv_heads, cache.n_kv_heads * cache.group_size
-    qp, qs = _rows(cache, q, hq, total, "q")
-    kp, ks = _rows(cache, k, hkv, total, "k")
-    vp, vs = _rows(cache, v, hkv, total, "v")
+    qp, qs = _rows(cache, q, cache.q_heads, total, "q")
+    kp, ks = _rows(cache, k, cache.heads, total, "k")
+    vp, vs = _rows(cache, v, cache.heads, total, "v")
     if out.shape != q.shape:
         raise ValueError("out must be shaped like q")
-    rc = load().dkv_cache8_prefill(C.byref(cache), lens.size, lens.ctypes.data, qp, qs, kp, ks, vp, vs,
+    rc = load().dkv_cache8_prefill(cache.address, lens.size, lens.ctypes.data, qp, qs, kp, ks, vp, vs,
                                    _on(cache, out, cache.elem_dtype, "out"), window, sinks, _stream8(cache, stream))
     return _check(rc, "dkv_cache8_prefill") if check else rc

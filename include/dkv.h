@@ -413,8 +413,8 @@ int dkv_pool_export(dkv_pool* pool, dkv_snapshot* out);
  *    token: the 16-bit values of complete blocks are gone.
  *  - Codes, per block, head and operand (K or V), fp32 arithmetic correctly
  *    rounded: amax = the largest finite |x| of the T x 128 values,
- *    s = max(fdiv(amax, Q), 2^-100) with Q = 448 (e4m3) or 127 (int8),
- *    inv = fdiv(1, s), y = clamp(fmul(x, inv), -Q, Q), code = y rounded to
+ *    s = max(fmul(amax, fdiv(1, Q)), 2^-100) with Q = 448 (e4m3) or 127
+ *    (int8), inv = fdiv(1, s), y = clamp(fmul(x, inv), -Q, Q), code = y rounded to
  *    the nearest e4m3 value or integer, ties to even. The stored value is
  *    s * code. Infinite inputs saturate; a NaN stays NaN (e4m3) or becomes 0
  *    (int8). Other tokens of the block keep their values either way.

@@ -66,7 +66,7 @@ def rotate(x, pos, rope, rotary_dim, interleaved, dtype):
 def quantise(x, code):
     """One operand's block [T][128] float32 -> (code bytes, scale)."""
     fin = np.where(np.isfinite(x), np.abs(x), np.float32(0))
-    s = np.float32(max(np.float32(fin.max()) / QMAX[code], np.float32(2.0 ** -100)))
+    s = np.float32(max(np.float32(fin.max()) * (np.float32(1) / QMAX[code]), np.float32(2.0 ** -100)))
     inv = np.float32(1.0) / s
     with np.errstate(invalid="ignore", over="ignore"):
         y = np.clip(x * inv, -QMAX[code], QMAX[code])
