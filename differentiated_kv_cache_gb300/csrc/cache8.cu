@@ -212,7 +212,7 @@ __global__ void k_append8(Cache8View c, Append8Args a, int n_req, const __grid_c
   extern __shared__ __align__(16) uint8_t sm[];
   pdl_launch_dependents();
   pdl_wait();
-  if (c.noop()) return;
+  if (c.stopped()) return;
   int jobs = n_req;
   if constexpr (!STEP) jobs = call.blk0[n_req];
   if ((int)blockIdx.x == jobs * c.hkv) {

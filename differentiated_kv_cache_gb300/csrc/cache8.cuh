@@ -32,7 +32,11 @@ struct Cache8View {
   __device__ __forceinline__ size_t tail_head(int slot, int h) const {
     return ((size_t)slot * hkv + h) * ((size_t)T * 4 * kD);
   }
-  __device__ __forceinline__ bool noop() const { return *(volatile int*)status != 0; }
+  // an error of an earlier call; the same for every thread of the block,
+  // whatever other blocks latch meanwhile
+  __device__ __forceinline__ bool stopped() const {
+    return __syncthreads_or(threadIdx.x == 0 && *(volatile int*)status != 0);
+  }
   __device__ __forceinline__ void latch(int code, int info) const {
     if (atomicCAS(status, 0, code) == 0) status[1] = info;
   }

@@ -2,8 +2,15 @@
 // or through a sliding window with first tokens that stay visible
 // (include/dkv.h: dkv_cache8_attention).
 //
-// One CTA per (request, KV head); its warps take 16-token tiles in turn and
-// join their partial results in shared memory.
+// The tiles of all (request, KV head) units, 16 tokens of 4 KB of codes each,
+// form one sequence that is cut into equal contiguous ranges, one per CTA of a
+// persistent grid and of those one per warp: a long unit spreads over the GPU,
+// short ones share a warp, and lengths are read on the device (a captured call
+// replays with others). A warp streams its tiles through a ring of bulk
+// copies; a unit inside one warp's range is written by it, one inside a CTA is
+// joined in shared memory, and one that crosses CTAs leaves a partial per CTA
+// in the workspace, which the CTA that arrives last joins in order (the result
+// does not depend on who that is).
 //
 // A warp's step on a tile of codes, S^T = K Q^T and O^T += V^T P^T with
 // mma.sync m16n8k16 (tokens / features on M, the G <= 8 queries on N; at most
@@ -20,13 +27,19 @@
 // Tiles of the 16-bit tail take s_k = 1 and, for s_v, the power of two below
 // their largest |v|, by which their values are divided (exact but for values
 // 2^-14 and less of the largest).
+#include <algorithm>
+
 #include "cache8.cuh"
 #include "dkv_kernels.cuh"
 
 namespace dkv {
 namespace {
 
-constexpr int kA8Warps = 8;
+constexpr int kA8Warps = 12;
+constexpr int kA8Stages = 3;        // ring entries of a warp
+constexpr int kA8Entry = 2 * kTile; // 4 KB: K and V codes of a tile, or K or V of a tail tile
+constexpr int kA8Row = kD + 4;      // floats of a query's row in a shared partial (no bank conflicts)
+constexpr int kA8Cta = 2 * kA8Warps;    // tiles that make a CTA worth its start
 constexpr float kA8Lazy = 8.0f;
 
 struct Attn8Args {
@@ -35,6 +48,8 @@ struct Attn8Args {
   long long qs;      // bytes
   uint8_t* out;
   int n_req, window, sinks;
+  unsigned* count;   // arrivals of CTAs, per query row; zero between calls
+  float* part;       // [CTA][2]: G rows of 128, then 8 maxima, 8 sums
 };
 
 // Tiles of one request: [0, head) from its start, [win, end) behind them; the
@@ -284,107 +299,398 @@ __device__ __forceinline__ void half_q(const uint32_t (&raw)[16], int lane, uint
   scale[1] = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
 }
 
-template <int ELEM, int CODE>
-__global__ void __launch_bounds__(kA8Warps * 32)
-    k_attention8(Cache8View c, Attn8Args a) {
-  __shared__ float s_o[kA8Warps][kMaxG][kD];
-  __shared__ float s_m[kA8Warps][kMaxG], s_l[kA8Warps][kMaxG];
-  pdl_launch_dependents();
-  pdl_wait();
-  if (c.noop()) return;
-  const int i = blockIdx.x / c.hkv, h = blockIdx.x % c.hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t4 = lane & 3, g4 = lane >> 2;
-  int slot = a.slots ? a.slots[i] : i, N = max(a.seq_lens[i], 0);
-  int err = 0;
-  if ((unsigned)slot >= (unsigned)c.n_slots) err = DKV_ERR_ARG;
-  else if ((long long)N > (long long)c.width * c.T) err = DKV_ERR_TABLE_FULL;
-  if (err) {
-    if (threadIdx.x == 0) c.latch(err, i);
-    return;
-  }
-  const Tiles tl = tiles_of(N, c.T, a.window, a.sinks);
-  uint32_t raw[16], qf[16];
-  float qs[2] = {1.0f, 1.0f};
-  load_q<ELEM>(a.q + i * a.qs + (size_t)h * c.G * (2 * kD), c.G, lane, raw);
-  if (ELEM == DKV_BF16) {
-    half_q(raw, lane, qf, qs);
-  } else {
+// Tiles from shared memory: K and V of codes lie one behind the other.
+template <int CODE>
+__device__ __forceinline__ void load_codes(const uint8_t* p, uint4 (&w)[4]) {
 #pragma unroll
-    for (int e = 0; e < 16; e++) qf[e] = raw[e];
-  }
-  State s;
-  s.clear();
-  const int per = c.T / kSub;
-  for (int x = warp; x < tl.count; x += kA8Warps) {
-    const int tile = x < tl.head ? x : x - tl.head + tl.win;
-    const See see = see_of(tile * kSub, N, a.window, a.sinks, lane);
-    if (tile < tl.full) {
-      int page = c.table[(size_t)slot * c.width + tile / per];
-      if ((unsigned)page >= (unsigned)c.n_pages) {
-        if (lane == 0) c.latch(DKV_ERR_CHECK, i);
-        page = 0;
-      }
-      const float* sc = c.scales + 2 * ((size_t)page * c.hkv + h);
-      const float sk = sc[0], sv = sc[1];
-      const uint4* p = reinterpret_cast<const uint4*>(c.pages + c.page_head(page, h) + (size_t)(tile % per) * 2 * kTile) + lane;
-      uint4 kw[4], vw[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        kw[j] = p[32 * j];
-        vw[j] = p[128 + 32 * j];
-      }
-      const float ks[2] = {sk * kLogitScale * qs[0], sk * kLogitScale * qs[1]};
-      code_tile<CODE>(s, qf, kw, vw, see, ks, log2f(sv), __fdiv_rn(1.0f, sv));
-    } else {
-      const uint8_t* p = c.tail + c.tail_head(slot, h) + (size_t)(tile - tl.full) * 4 * kTile + 16 * lane;
-      tail_tile<ELEM>(s, raw, p, p + 2 * kTile, see, kLogitScale);
-    }
-  }
-#pragma unroll
-  for (int d = 4; d <= 16; d <<= 1) {
-    s.l[0] += __shfl_xor_sync(0xffffffffu, s.l[0], d);
-    s.l[1] += __shfl_xor_sync(0xffffffffu, s.l[1], d);
-  }
-  if (g4 == 0) {
-    s_m[warp][2 * t4] = s.m[0];
-    s_m[warp][2 * t4 + 1] = s.m[1];
-    s_l[warp][2 * t4] = s.l[0];
-    s_l[warp][2 * t4 + 1] = s.l[1];
-  }
+  for (int j = 0; j < 4; j++) w[j] = *reinterpret_cast<const uint4*>(p + 512 * j);
+}
+
+// A unit that one warp holds whole: out = O / l, two features a store.
+template <int ELEM>
+__device__ __forceinline__ void write_unit(const State& s, uint8_t* out, int G, int lane) {
+  const int g = lane >> 2, t = lane & 3, odd = g & 1, q = 2 * t + odd;
+  const float ia = __fdiv_rn(1.0f, s.l[0]), ib = __fdiv_rn(1.0f, s.l[1]);
 #pragma unroll
   for (int m = 0; m < 8; m++)
 #pragma unroll
-    for (int e = 0; e < 4; e++) s_o[warp][2 * t4 + (e & 1)][16 * m + g4 + 8 * (e >> 1)] = s.o[m][e];
-  __syncthreads();
-  for (int x = threadIdx.x; x < c.G * kD / 2; x += blockDim.x) {
-    const int g = x / (kD / 2), f = 2 * (x % (kD / 2));
-    float M = -INFINITY;
-    for (int w = 0; w < kA8Warps; w++) M = fmaxf(M, s_m[w][g]);
-    float u = 0.0f, v = 0.0f, l = 0.0f;
-    for (int w = 0; w < kA8Warps; w++) {
-      const float fw = s_m[w][g] == M ? 1.0f : fast_exp2(s_m[w][g] - M);   // 0 for a warp without tiles
-      u = fmaf(s_o[w][g][f], fw, u);
-      v = fmaf(s_o[w][g][f + 1], fw, v);
-      l = fmaf(s_l[w][g], fw, l);
+    for (int e = 0; e < 2; e++) {
+      const float a = s.o[m][2 * e] * ia, b = s.o[m][2 * e + 1] * ib;
+      const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 4);
+      if (q < G)
+        *reinterpret_cast<uint32_t*>(out + (size_t)q * (2 * kD) + 2 * (16 * m + 8 * e + g - odd)) =
+            odd ? pack_elems<ELEM>(other, b) : pack_elems<ELEM>(a, other);
     }
-    const bool none = tl.count == 0;
-    reinterpret_cast<uint32_t*>(a.out)[(((size_t)i * c.hkv + h) * c.G + g) * (kD / 2) + f / 2] =
-        none ? 0u : pack_elems<ELEM>(__fdiv_rn(u, l), __fdiv_rn(v, l));
+}
+
+// A partial in shared memory: G rows of kA8Row, then 8 maxima and 8 sums.
+__device__ __forceinline__ void put_partial(const State& s, float* p, int G, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int m = 0; m < 8; m++)
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (2 * t + (e & 1) < G) p[(2 * t + (e & 1)) * kA8Row + 16 * m + g + 8 * (e >> 1)] = s.o[m][e];
+  if (g == 0) {
+    float* ml = p + G * kA8Row;
+    ml[2 * t] = s.m[0];
+    ml[2 * t + 1] = s.m[1];
+    ml[8 + 2 * t] = s.l[0];
+    ml[8 + 2 * t + 1] = s.l[1];
   }
+}
+// weight of a partial with maximum m under the joint maximum M: 1 where they
+// are equal, infinite ones too
+__device__ __forceinline__ float join(float m, float M) { return m == M ? 1.0f : fast_exp2(m - M); }
+
+template <int ELEM>
+__device__ __forceinline__ void write_row(uint8_t* out, int lane, float4 o, float l) {
+  const float inv = __fdiv_rn(1.0f, l);
+  *reinterpret_cast<uint2*>(out + 8 * lane) =
+      make_uint2(pack_elems<ELEM>(o.x * inv, o.y * inv), pack_elems<ELEM>(o.z * inv, o.w * inv));
+}
+
+// What a lane finds out about one tile of the sequence.
+struct Desc {
+  const uint8_t* src;    // its 4 KB of codes, or its 8 KB of the tail
+  float sk, sv;
+  int tile, unit;        // tile | kA8Tail: of the tail
+};
+constexpr int kA8Tail = 1 << 30;
+
+template <int ELEM, int CODE>
+__global__ void __launch_bounds__(kA8Warps * 32)
+    k_attention8(Cache8View c, Attn8Args a) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ int s_pre[kMaxCallReq + 1], s_len[kMaxCallReq], s_slot[kMaxCallReq], s_scan[32];
+  __shared__ int s_unit[2 * kA8Warps];
+  __shared__ __align__(8) uint64_t s_bar[kA8Warps * kA8Stages];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = c.G, hkv = c.hkv;
+  uint8_t* ring = sm + warp * (kA8Stages * kA8Entry);
+  float* first_part = reinterpret_cast<float*>(sm + kA8Warps * kA8Stages * kA8Entry) + warp * (G * kA8Row + 16);
+  const uint32_t bar0 = smem_u32(s_bar + warp * kA8Stages);
+  if (lane == 0) {
+    for (int s = 0; s < kA8Stages; s++) mbar_init(bar0 + 8 * s, 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 2 * kA8Warps) s_unit[threadIdx.x] = -1;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (c.stopped()) return;
+
+  // ---- lengths, and the prefix sums of the requests' tiles over all heads ----
+  for (int base = 0, carry = 0; base < a.n_req; base += blockDim.x) {
+    const int i = base + threadIdx.x;
+    int n = 0, cost = 0;
+    if (i < a.n_req) {
+      n = max(a.seq_lens[i], 0);
+      const int slot = a.slots ? a.slots[i] : i;
+      int err = 0;
+      if ((unsigned)slot >= (unsigned)c.n_slots) err = DKV_ERR_ARG;
+      else if ((long long)n > (long long)c.width * c.T) err = DKV_ERR_TABLE_FULL;
+      if (err) {
+        c.latch(err, i);
+        n = 0;
+      }
+      s_len[i] = n;
+      s_slot[i] = slot;
+      cost = tiles_of(n, c.T, a.window, a.sinks).count * hkv;
+    }
+    int x = cost;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    int before = carry, all = carry;
+    for (int w = 0; w < kA8Warps; w++) {
+      if (w < warp) before += s_scan[w];
+      all += s_scan[w];
+    }
+    if (i < a.n_req) s_pre[i] = before + x - cost;
+    carry = all;
+    if (threadIdx.x == 0) s_pre[min(base + (int)blockDim.x, a.n_req)] = all;
+    __syncthreads();
+  }
+  const int total = s_pre[a.n_req], units = a.n_req * hkv;
+  // CTAs that take part: not so many that warps have no tile, but one a unit
+  // (and no CTA without a tile: the join counts on that)
+  const int ctas = max(1, min(min((int)gridDim.x, total), max(units, (total + kA8Cta - 1) / kA8Cta)));
+
+  // requests without tokens: zeros
+  for (int i = blockIdx.x; i < a.n_req; i += gridDim.x)
+    if (s_pre[i + 1] == s_pre[i])
+      for (int x = threadIdx.x; x < hkv * G * (kD / 8); x += blockDim.x)
+        reinterpret_cast<uint4*>(a.out + (size_t)i * hkv * G * (2 * kD))[x] = make_uint4(0, 0, 0, 0);
+  if ((int)blockIdx.x >= ctas) return;
+
+  auto start_of = [&](int cta) { return (int)((long long)total * cta / ctas); };
+  auto cta_of = [&](int pos) { return (int)((((long long)pos + 1) * ctas - 1) / total); };
+  const int lo = start_of(blockIdx.x), hi = start_of(blockIdx.x + 1);
+  const int w0 = lo + (int)((long long)(hi - lo) * warp / kA8Warps);
+  const int w1 = lo + (int)((long long)(hi - lo) * (warp + 1) / kA8Warps);
+  const int per = __ffs(c.T / kSub) - 1;     // log2 of the tiles of a block
+
+  auto request_of = [&](int pos) {
+    int r = 0, end = a.n_req;
+    while (end - r > 1) {
+      const int mid = (r + end) >> 1;
+      if (s_pre[mid] <= pos) r = mid; else end = mid;
+    }
+    return r;
+  };
+  // first position and tiles of a unit
+  auto unit_start = [&](int u, int& count) {
+    const int r = u / hkv;
+    count = (s_pre[r + 1] - s_pre[r]) / hkv;
+    return s_pre[r] + (u - r * hkv) * count;
+  };
+  auto describe = [&](int pos) {
+    Desc d;
+    d.src = nullptr;
+    d.sk = d.sv = 1.0f;
+    d.tile = d.unit = 0;
+    if (pos >= w1) return d;
+    const int r = request_of(pos), n = s_len[r], slot = s_slot[r];
+    const Tiles t = tiles_of(n, c.T, a.window, a.sinks);
+    const int rem = pos - s_pre[r], h = rem / t.count, x = rem - h * t.count;
+    d.unit = r * hkv + h;
+    d.tile = x < t.head ? x : x - t.head + t.win;
+    if (d.tile < t.full) {
+      int page = c.table[(size_t)slot * c.width + (d.tile >> per)];
+      if ((unsigned)page >= (unsigned)c.n_pages) {
+        c.latch(DKV_ERR_CHECK, r);
+        page = 0;
+      }
+      const float2 sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * hkv + h));
+      d.sk = sc.x;
+      d.sv = sc.y;
+      d.src = c.pages + c.page_head(page, h) + (size_t)(d.tile & ((1 << per) - 1)) * (2 * kTile);
+    } else {
+      d.src = c.tail + c.tail_head(slot, h) + (size_t)(d.tile - t.full) * (4 * kTile);
+      d.tile |= kA8Tail;
+    }
+    return d;
+  };
+
+  // ---- the warp's tiles ----
+  Desc cur = describe(w0 + lane), nxt = cur;
+  bool ok = true;
+  int issued = 0, taken = 0;           // ring entries
+  int at = w0, half = 0;               // next entry to issue: tile, and which half of a tail tile
+  int base = w0;                       // first tile of `cur`
+  auto issue = [&]() {
+    if (at >= w1 || !ok) return;
+    const bool in = at - base < 32;
+    const unsigned long long src =
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(in ? cur.src : nxt.src), (at - w0) & 31);
+    const bool tail = __shfl_sync(0xffffffffu, in ? cur.tile : nxt.tile, (at - w0) & 31) & kA8Tail;
+    if (lane == 0) {
+      const int s = issued % kA8Stages;
+      mbar_expect_tx(bar0 + 8 * s, kA8Entry);
+      bulk_g2s(smem_u32(ring + s * kA8Entry), reinterpret_cast<const void*>(src + (half ? kA8Entry : 0)), kA8Entry,
+               bar0 + 8 * s);
+    }
+    issued++;
+    if (tail && !half) {
+      half = 1;
+    } else {
+      half = 0;
+      at++;
+    }
+  };
+  auto wait = [&]() {                  // the next entry, in shared memory
+    const int s = taken % kA8Stages;
+    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * s, (taken / kA8Stages) & 1))) {
+      ok = false;
+      if (lane == 0) c.latch(DKV_ERR_TIMEOUT, -1);
+    }
+    taken++;
+    return ring + s * kA8Entry + 16 * lane;
+  };
+  for (int s = 0; s < kA8Stages; s++) issue();
+  if (w1 - w0 > 32) nxt = describe(w0 + 32 + lane);
+
+  State s;
+  s.clear();
+  uint32_t raw[16], qf[16];
+  float qs[2] = {1.0f, 1.0f};
+  int unit = -1, N = 0, ustart = 0, ucount = 0;
+  // end of the warp's part of a unit
+  auto flush = [&](int pos) {
+#pragma unroll
+    for (int d = 4; d <= 16; d <<= 1) {
+      s.l[0] += __shfl_xor_sync(0xffffffffu, s.l[0], d);
+      s.l[1] += __shfl_xor_sync(0xffffffffu, s.l[1], d);
+    }
+    if (ustart >= w0 && pos == ustart + ucount) {
+      write_unit<ELEM>(s, a.out + (size_t)unit * G * (2 * kD), G, lane);
+      return;
+    }
+    // begun before the range: first slot; else it goes on behind the range and
+    // the ring is drained
+    const int slot = ustart < w0 ? 0 : 1;
+    put_partial(s, slot == 0 ? first_part : reinterpret_cast<float*>(ring), G, lane);
+    if (lane == 0) s_unit[2 * warp + slot] = unit;
+  };
+  for (int pos = w0; pos < w1; pos++) {
+    if (pos - base == 32) {
+      base = pos;
+      cur = nxt;
+      nxt = describe(base + 32 + lane);
+    }
+    const int from = (pos - w0) & 31;
+    const int u = __shfl_sync(0xffffffffu, cur.unit, from), tile = __shfl_sync(0xffffffffu, cur.tile, from);
+    const float sk = __shfl_sync(0xffffffffu, cur.sk, from), sv = __shfl_sync(0xffffffffu, cur.sv, from);
+    if (u != unit) {
+      if (unit >= 0) flush(pos);
+      unit = u;
+      ustart = unit_start(u, ucount);
+      const int r = u / hkv;
+      N = s_len[r];
+      s.clear();
+      load_q<ELEM>(a.q + r * a.qs + (size_t)(u - r * hkv) * G * (2 * kD), G, lane, raw);
+      if (ELEM == DKV_BF16) {
+        half_q(raw, lane, qf, qs);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; e++) qf[e] = raw[e];
+      }
+    }
+    const See see = see_of((tile & ~kA8Tail) * kSub, N, a.window, a.sinks, lane);
+    if (!(tile & kA8Tail)) {
+      const uint8_t* p = wait();
+      uint4 kw[4], vw[4];
+      load_codes<CODE>(p, kw);
+      load_codes<CODE>(p + kTile, vw);
+      const float ks[2] = {sk * kLogitScale * qs[0], sk * kLogitScale * qs[1]};
+      code_tile<CODE>(s, qf, kw, vw, see, ks, log2f(sv), __fdiv_rn(1.0f, sv));
+      __syncwarp();
+      issue();
+    } else {
+      const uint8_t *kp = wait(), *vp = wait();
+      tail_tile<ELEM>(s, raw, kp, vp, see, kLogitScale);
+      __syncwarp();
+      issue();
+      issue();
+    }
+  }
+  // a wait that gave up: no copy may still be in flight at the exit
+  if (!ok)
+    for (int e = max(issued - kA8Stages, 0); e < issued; e++)
+      mbar_wait_bounded(bar0 + 8 * (e % kA8Stages), (e / kA8Stages) & 1);
+  if (unit >= 0) flush(w1);
+  __syncthreads();
+
+  // ---- join the warps' parts, a query row of a unit per warp ----
+  const int mine = lane < 2 * kA8Warps ? s_unit[lane] : -1;
+  const unsigned same = __match_any_sync(0xffffffffu, mine);
+  unsigned leaders = __ballot_sync(0xffffffffu, mine >= 0 && __ffs(same) - 1 == lane);
+  auto part = [&](int slot) {
+    return (slot & 1) ? reinterpret_cast<const float*>(sm + (slot >> 1) * (kA8Stages * kA8Entry))
+                      : reinterpret_cast<const float*>(sm + kA8Warps * kA8Stages * kA8Entry) +
+                            (slot >> 1) * (G * kA8Row + 16);
+  };
+  for (int task = 0; leaders; leaders &= leaders - 1) {
+    const int lead = __ffs(leaders) - 1, u = __shfl_sync(0xffffffffu, mine, lead);
+    const unsigned set = __shfl_sync(0xffffffffu, same, lead);
+    for (int q = 0; q < G; q++, task++) {
+      if (task % kA8Warps != warp) continue;
+      const bool has = set >> lane & 1u;
+      const float* p = part(has ? lane : lead);
+      const float m = has ? p[G * kA8Row + q] : -INFINITY;
+      float M = m;
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      const float f = has ? join(m, M) : 0.0f;
+      float l = has ? f * p[G * kA8Row + 8 + q] : 0.0f;
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (unsigned b = set; b; b &= b - 1) {
+        const int x = __ffs(b) - 1;
+        const float g = __shfl_sync(0xffffffffu, f, x);
+        const float4 v = *reinterpret_cast<const float4*>(part(x) + q * kA8Row + 4 * lane);
+        o.x = fmaf(v.x, g, o.x);
+        o.y = fmaf(v.y, g, o.y);
+        o.z = fmaf(v.z, g, o.z);
+        o.w = fmaf(v.w, g, o.w);
+      }
+      uint8_t* out = a.out + ((size_t)u * G + q) * (2 * kD);
+      int count;
+      const int us = unit_start(u, count), ue = us + count;
+      if (us >= lo && ue <= hi) {
+        write_row<ELEM>(out, lane, o, l);
+        continue;
+      }
+      // ---- over CTAs: the one that arrives last joins the parts, in order ----
+      const size_t stride = (size_t)G * kD + 16;
+      float* dst = a.part + (2 * blockIdx.x + (us < lo ? 0 : 1)) * stride;
+      *reinterpret_cast<float4*>(dst + q * kD + 4 * lane) = o;
+      if (lane == 0) {
+        dst[G * kD + q] = M;
+        dst[G * kD + 8 + q] = l;
+      }
+      const int c0 = cta_of(us), c1 = cta_of(ue - 1);
+      __threadfence();
+      __syncwarp();
+      unsigned old = 0;
+      if (lane == 0) old = atomicInc(a.count + (size_t)u * G + q, (unsigned)(c1 - c0));   // back to zero by itself
+      if (__shfl_sync(0xffffffffu, old, 0) != (unsigned)(c1 - c0)) continue;
+      __threadfence();
+      auto cta_part = [&](int x) { return a.part + (2 * x + (x == c0 ? 1 : 0)) * stride; };
+      M = -INFINITY;
+      for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(cta_part(x) + G * kD + q));
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      l = 0.0f;
+      o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int x = c0; x <= c1; x++) {
+        const float* p = cta_part(x);
+        const float f = join(__ldcg(p + G * kD + q), M);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p + q * kD + 4 * lane));
+        l = fmaf(__ldcg(p + G * kD + 8 + q), f, l);
+        o.x = fmaf(v.x, f, o.x);
+        o.y = fmaf(v.y, f, o.y);
+        o.z = fmaf(v.z, f, o.z);
+        o.w = fmaf(v.w, f, o.w);
+      }
+      write_row<ELEM>(out, lane, o, l);
+    }
+  }
+}
+
+// a counter per query row: rows of one unit are joined apart
+size_t count_bytes(int hq, int n_req) { return ((size_t)hq * n_req * 4 + 255) / 256 * 256; }
+size_t attention8_smem(int G) {
+  return (size_t)kA8Warps * kA8Stages * kA8Entry + (size_t)kA8Warps * (G * kA8Row + 16) * 4;
 }
 
 }  // namespace
 
-size_t attention8_workspace(int, int, int, int) { return 256; }
+// The partials first: their place does not depend on the call's requests.
+size_t attention8_workspace(int hkv, int G, int max_req, int sm_count) {
+  return (size_t)sm_count * 2 * ((size_t)G * kD + 16) * 4 + count_bytes(hkv * G, max_req);
+}
 
-cudaError_t launch_attention8(const Cache8View& c, int elem, int code, int, const int* slots, const int* seq_lens,
-                              int n_req, const void* q, long long q_stride, void* out, int window, int sinks, void*,
-                              cudaStream_t st) {
+cudaError_t launch_attention8(const Cache8View& c, int elem, int code, int sm_count, const int* slots,
+                              const int* seq_lens, int n_req, const void* q, long long q_stride, void* out,
+                              int window, int sinks, void* workspace, cudaStream_t st) {
+  float* part = static_cast<float*>(workspace);
   const Attn8Args a{slots, seq_lens, static_cast<const uint8_t*>(q), 2 * q_stride, static_cast<uint8_t*>(out),
-                    n_req, window, sinks};
+                    n_req, window, sinks, reinterpret_cast<unsigned*>(part + (size_t)sm_count * 2 * (c.G * kD + 16)), part};
   auto kernel = elem == DKV_F16 ? (code == DKV_E4M3 ? k_attention8<DKV_F16, DKV_E4M3> : k_attention8<DKV_F16, DKV_INT8>)
                                 : (code == DKV_E4M3 ? k_attention8<DKV_BF16, DKV_E4M3> : k_attention8<DKV_BF16, DKV_INT8>);
-  return launch_dependent(kernel, dim3((unsigned)(n_req * c.hkv)), dim3(kA8Warps * 32), 0, st, c, a);
+  const size_t smem = attention8_smem(c.G);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  // no more CTAs than the longest lengths that the table holds could use
+  const long long units = (long long)n_req * c.hkv, tiles = units * ((long long)c.width * c.T / kSub);
+  const int grid = (int)std::min<long long>(sm_count, std::max(units, (tiles + kA8Cta - 1) / kA8Cta));
+  return launch_dependent(kernel, dim3(grid), dim3(kA8Warps * 32), smem, st, c, a);
 }
 
 }  // namespace dkv

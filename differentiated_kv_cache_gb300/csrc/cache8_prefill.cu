@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                const __grid_constant__ CUtensorMap tv, W8Args a, const __grid_constant__ W8Call call) {
   pdl_launch_dependents();
   pdl_wait();
-  if (c.noop()) return;
+  if (c.stopped()) return;
   const int G = c.G, h = blockIdx.x % c.hkv;
   const int qtile = call.tile0[call.n_req] - 1 - (int)(blockIdx.x / c.hkv);   // later rows first: more keys
   int i = 0;
