@@ -152,18 +152,16 @@ __device__ __forceinline__ void weights(State& s, float* x, float inv) {
 // Which tokens of a tile the query sees, for this lane: logits of tokens g and
 // g + 8, and the V entries of tokens 2t, 2t+1, 2t+8, 2t+9 (one byte each).
 struct See {
-  bool all, lo, hi;
+  bool lo, hi;
   uint32_t v;
 };
+// every token of a tile
+__device__ __forceinline__ bool sees_all(int pos0, int N, int window) {
+  return pos0 + kSub <= N && (window <= 0 || pos0 >= N - window);
+}
 __device__ __forceinline__ See see_of(int pos0, int N, int window, int sinks, int lane) {
   See s;
   const int from = window > 0 ? N - window : 0;
-  s.all = pos0 + kSub <= N && pos0 >= from;
-  if (s.all) {
-    s.lo = s.hi = true;
-    s.v = 0xffffffffu;
-    return s;
-  }
   auto sees = [&](int i) { return pos0 + i < N && (pos0 + i >= from || pos0 + i < sinks); };
   const int g = lane >> 2, t = lane & 3;
   s.lo = sees(g);
@@ -173,10 +171,19 @@ __device__ __forceinline__ See see_of(int pos0, int N, int window, int sinks, in
   return s;
 }
 
-// A tile of codes: kw, vw are the lane's 64 bytes of K and of V.
+// A lane's 64 bytes of K or V codes from shared memory.
+__device__ __forceinline__ void load_codes(const uint8_t* p, uint4 (&w)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; j++) w[j] = *reinterpret_cast<const uint4*>(p + 512 * j);
+}
+
+// A tile of codes at p (K, then V); edge: some token may not be visible.
 template <int CODE>
-__device__ __forceinline__ void code_tile(State& s, const uint32_t (&qf)[16], const uint4 (&kw)[4], const uint4 (&vw)[4],
-                                          const See& see, const float (&ks)[2], float lv, float inv) {
+__device__ __forceinline__ void code_tile(State& s, const uint32_t (&qf)[16], const uint8_t* p, bool edge,
+                                          const See& see, const float (&ks)[2], float lv) {
+  uint4 kw[4], vw[4];
+  load_codes(p, kw);
+  load_codes(p + kTile, vw);
   float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < 4; j++) {
@@ -189,18 +196,29 @@ __device__ __forceinline__ void code_tile(State& s, const uint32_t (&qf)[16], co
     mma16816(y, a, qf[4 * j + 2], qf[4 * j + 3]);
   }
 #pragma unroll
-  for (int e = 0; e < 4; e++) x[e] = (e < 2 ? see.lo : see.hi) ? fmaf(x[e] + y[e], ks[e & 1], lv) : -INFINITY;
+  for (int e = 0; e < 4; e++) x[e] = fmaf(x[e] + y[e], ks[e & 1], lv);
+  if (edge) {
+#pragma unroll
+    for (int e = 0; e < 4; e++) x[e] = (e < 2 ? see.lo : see.hi) ? x[e] : -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      vw[j].x &= see.v;
+      vw[j].y &= see.v;
+      vw[j].z &= see.v;
+      vw[j].w &= see.v;
+    }
+  }
   raise(s, x);
-  weights(s, x, inv);
+  weights(s, x, fast_exp2(-lv));
   const uint32_t b0 = movmatrix_trans(pack_half2(x[0], x[1])), b1 = movmatrix_trans(pack_half2(x[2], x[3]));
 #pragma unroll
   for (int j = 0; j < 4; j++) {
     uint32_t a[4];
-    code_halves<CODE>(see.all ? vw[j].x : vw[j].x & see.v, a[0], a[2]);
-    code_halves<CODE>(see.all ? vw[j].y : vw[j].y & see.v, a[1], a[3]);
+    code_halves<CODE>(vw[j].x, a[0], a[2]);
+    code_halves<CODE>(vw[j].y, a[1], a[3]);
     mma16816(s.o[2 * j], a, b0, b1);
-    code_halves<CODE>(see.all ? vw[j].z : vw[j].z & see.v, a[0], a[2]);
-    code_halves<CODE>(see.all ? vw[j].w : vw[j].w & see.v, a[1], a[3]);
+    code_halves<CODE>(vw[j].z, a[0], a[2]);
+    code_halves<CODE>(vw[j].w, a[1], a[3]);
     mma16816(s.o[2 * j + 1], a, b0, b1);
   }
 }
@@ -299,13 +317,6 @@ __device__ __forceinline__ void half_q(const uint32_t (&raw)[16], int lane, uint
   scale[1] = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
 }
 
-// Tiles from shared memory: K and V of codes lie one behind the other.
-template <int CODE>
-__device__ __forceinline__ void load_codes(const uint8_t* p, uint4 (&w)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; j++) w[j] = *reinterpret_cast<const uint4*>(p + 512 * j);
-}
-
 // A unit that one warp holds whole: out = O / l, two features a store.
 template <int ELEM>
 __device__ __forceinline__ void write_unit(const State& s, uint8_t* out, int G, int lane) {
@@ -353,10 +364,10 @@ __device__ __forceinline__ void write_row(uint8_t* out, int lane, float4 o, floa
 // What a lane finds out about one tile of the sequence.
 struct Desc {
   const uint8_t* src;    // its 4 KB of codes, or its 8 KB of the tail
-  float sk, sv;
-  int tile, unit;        // tile | kA8Tail: of the tail
+  float ks, lv;          // s_k log2(e) / sqrt(128) and log2(s_v)
+  int tile, unit;
+  bool tail, edge;
 };
-constexpr int kA8Tail = 1 << 30;
 
 template <int ELEM, int CODE>
 __global__ void __launch_bounds__(kA8Warps * 32)
@@ -450,8 +461,9 @@ __global__ void __launch_bounds__(kA8Warps * 32)
   auto describe = [&](int pos) {
     Desc d;
     d.src = nullptr;
-    d.sk = d.sv = 1.0f;
+    d.ks = d.lv = 0.0f;
     d.tile = d.unit = 0;
+    d.tail = d.edge = false;
     if (pos >= w1) return d;
     const int r = request_of(pos), n = s_len[r], slot = s_slot[r];
     const Tiles t = tiles_of(n, c.T, a.window, a.sinks);
@@ -465,53 +477,56 @@ __global__ void __launch_bounds__(kA8Warps * 32)
         page = 0;
       }
       const float2 sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * hkv + h));
-      d.sk = sc.x;
-      d.sv = sc.y;
+      d.ks = sc.x * kLogitScale;
+      d.lv = log2f(sc.y);
       d.src = c.pages + c.page_head(page, h) + (size_t)(d.tile & ((1 << per) - 1)) * (2 * kTile);
     } else {
       d.src = c.tail + c.tail_head(slot, h) + (size_t)(d.tile - t.full) * (4 * kTile);
-      d.tile |= kA8Tail;
+      d.tail = true;
     }
+    d.edge = !sees_all(d.tile * kSub, n, a.window);
     return d;
   };
 
-  // ---- the warp's tiles ----
+  // ---- the warp's tiles, 32 descriptors at a time, a lane each ----
   Desc cur = describe(w0 + lane), nxt = cur;
+  unsigned cur_tail = __ballot_sync(0xffffffffu, cur.tail), nxt_tail = 0;
   bool ok = true;
-  int issued = 0, taken = 0;           // ring entries
-  int at = w0, half = 0;               // next entry to issue: tile, and which half of a tail tile
+  int ahead = 0;                       // ring entry to fill next
+  int at = w0, half = 0;               // tile to issue next, and which half of a tail tile
   int base = w0;                       // first tile of `cur`
+  int stage = 0, parity = 0;           // ring entry to read next
+  // the lane that holds a tile's descriptor issues its copy
   auto issue = [&]() {
-    if (at >= w1 || !ok) return;
+    if (at >= w1) return;
     const bool in = at - base < 32;
-    const unsigned long long src =
-        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(in ? cur.src : nxt.src), (at - w0) & 31);
-    const bool tail = __shfl_sync(0xffffffffu, in ? cur.tile : nxt.tile, (at - w0) & 31) & kA8Tail;
-    if (lane == 0) {
-      const int s = issued % kA8Stages;
-      mbar_expect_tx(bar0 + 8 * s, kA8Entry);
-      bulk_g2s(smem_u32(ring + s * kA8Entry), reinterpret_cast<const void*>(src + (half ? kA8Entry : 0)), kA8Entry,
-               bar0 + 8 * s);
+    const int from = (at - w0) & 31;
+    const bool tail = (in ? cur_tail : nxt_tail) >> from & 1u;
+    if (lane == from && ok) {
+      mbar_expect_tx(bar0 + 8 * ahead, kA8Entry);
+      bulk_g2s(smem_u32(ring + ahead * kA8Entry), (in ? cur.src : nxt.src) + half * kA8Entry, kA8Entry, bar0 + 8 * ahead);
     }
-    issued++;
-    if (tail && !half) {
-      half = 1;
-    } else {
-      half = 0;
-      at++;
-    }
+    ahead = ahead == kA8Stages - 1 ? 0 : ahead + 1;
+    half = tail ? half ^ 1 : 0;
+    at += half ^ 1;
   };
   auto wait = [&]() {                  // the next entry, in shared memory
-    const int s = taken % kA8Stages;
-    if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * s, (taken / kA8Stages) & 1))) {
+    if (!mbar_try_wait(bar0 + 8 * stage, parity) && ok && !mbar_wait_bounded(bar0 + 8 * stage, parity)) {
       ok = false;
-      if (lane == 0) c.latch(DKV_ERR_TIMEOUT, -1);
+      c.latch(DKV_ERR_TIMEOUT, -1);
     }
-    taken++;
-    return ring + s * kA8Entry + 16 * lane;
+    const uint8_t* p = ring + stage * kA8Entry + 16 * lane;
+    if (++stage == kA8Stages) {
+      stage = 0;
+      parity ^= 1;
+    }
+    return p;
   };
   for (int s = 0; s < kA8Stages; s++) issue();
-  if (w1 - w0 > 32) nxt = describe(w0 + 32 + lane);
+  if (w1 - w0 > 32) {
+    nxt = describe(w0 + 32 + lane);
+    nxt_tail = __ballot_sync(0xffffffffu, nxt.tail);
+  }
 
   State s;
   s.clear();
@@ -535,52 +550,62 @@ __global__ void __launch_bounds__(kA8Warps * 32)
     put_partial(s, slot == 0 ? first_part : reinterpret_cast<float*>(ring), G, lane);
     if (lane == 0) s_unit[2 * warp + slot] = unit;
   };
-  for (int pos = w0; pos < w1; pos++) {
-    if (pos - base == 32) {
-      base = pos;
-      cur = nxt;
-      nxt = describe(base + 32 + lane);
-    }
-    const int from = (pos - w0) & 31;
-    const int u = __shfl_sync(0xffffffffu, cur.unit, from), tile = __shfl_sync(0xffffffffu, cur.tile, from);
-    const float sk = __shfl_sync(0xffffffffu, cur.sk, from), sv = __shfl_sync(0xffffffffu, cur.sv, from);
-    if (u != unit) {
-      if (unit >= 0) flush(pos);
-      unit = u;
-      ustart = unit_start(u, ucount);
-      const int r = u / hkv;
-      N = s_len[r];
-      s.clear();
-      load_q<ELEM>(a.q + r * a.qs + (size_t)(u - r * hkv) * G * (2 * kD), G, lane, raw);
-      if (ELEM == DKV_BF16) {
-        half_q(raw, lane, qf, qs);
-      } else {
+  for (; base < w1; base += 32) {
+    const int before = __shfl_up_sync(0xffffffffu, cur.unit, 1);
+    const unsigned edges = __ballot_sync(0xffffffffu, cur.edge);
+    const unsigned begins = __ballot_sync(0xffffffffu, cur.unit != (lane == 0 ? unit : before));
+    const int n = min(32, w1 - base);
+    for (int from = 0; from < n; from++) {
+      if (begins >> from & 1u) {
+        if (unit >= 0) flush(base + from);
+        unit = __shfl_sync(0xffffffffu, cur.unit, from);
+        ustart = unit_start(unit, ucount);
+        const int r = unit / hkv;
+        N = s_len[r];
+        s.clear();
+        load_q<ELEM>(a.q + r * a.qs + (size_t)(unit - r * hkv) * G * (2 * kD), G, lane, raw);
+        if (ELEM == DKV_BF16) {
+          half_q(raw, lane, qf, qs);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 16; e++) qf[e] = raw[e];
+          for (int e = 0; e < 16; e++) qf[e] = raw[e];
+        }
+      }
+      const float ks = __shfl_sync(0xffffffffu, cur.ks, from), lv = __shfl_sync(0xffffffffu, cur.lv, from);
+      const bool edge = edges >> from & 1u;
+      See see;
+      if (edge) see = see_of(__shfl_sync(0xffffffffu, cur.tile, from) * kSub, N, a.window, a.sinks, lane);
+      if (!(cur_tail >> from & 1u)) {
+        const float k2[2] = {ks * qs[0], ks * qs[1]};
+        code_tile<CODE>(s, qf, wait(), edge, see, k2, lv);
+        __syncwarp();
+        issue();
+      } else {
+        if (!edge) see = See{true, true, 0xffffffffu};
+        const uint8_t *kp = wait(), *vp = wait();
+        tail_tile<ELEM>(s, raw, kp, vp, see, kLogitScale);
+        __syncwarp();
+        issue();
+        issue();
       }
     }
-    const See see = see_of((tile & ~kA8Tail) * kSub, N, a.window, a.sinks, lane);
-    if (!(tile & kA8Tail)) {
-      const uint8_t* p = wait();
-      uint4 kw[4], vw[4];
-      load_codes<CODE>(p, kw);
-      load_codes<CODE>(p + kTile, vw);
-      const float ks[2] = {sk * kLogitScale * qs[0], sk * kLogitScale * qs[1]};
-      code_tile<CODE>(s, qf, kw, vw, see, ks, log2f(sv), __fdiv_rn(1.0f, sv));
-      __syncwarp();
-      issue();
-    } else {
-      const uint8_t *kp = wait(), *vp = wait();
-      tail_tile<ELEM>(s, raw, kp, vp, see, kLogitScale);
-      __syncwarp();
-      issue();
-      issue();
+    cur = nxt;
+    cur_tail = nxt_tail;
+    if (base + 64 < w1) {
+      nxt = describe(base + 64 + lane);
+      nxt_tail = __ballot_sync(0xffffffffu, nxt.tail);
     }
   }
   // a wait that gave up: no copy may still be in flight at the exit
   if (!ok)
-    for (int e = max(issued - kA8Stages, 0); e < issued; e++)
-      mbar_wait_bounded(bar0 + 8 * (e % kA8Stages), (e / kA8Stages) & 1);
+    for (int e = 0; e < kA8Stages; e++) {
+      mbar_wait_bounded(bar0 + 8 * stage, parity);
+      if (++stage == kA8Stages) {
+        stage = 0;
+        parity ^= 1;
+      }
+    }
+  __syncwarp();
   if (unit >= 0) flush(w1);
   __syncthreads();
 
