@@ -364,11 +364,29 @@ __device__ __forceinline__ void write_row(uint8_t* out, int lane, float4 o, floa
 // What a lane finds out about one tile of the sequence.
 struct Desc {
   const uint8_t* src;    // its 4 KB of codes, or its 8 KB of the tail
-  float ks, lv;          // s_k log2(e) / sqrt(128) and log2(s_v)
+  float2 sc;             // s_k, s_v
   int tile, unit;
   bool tail, edge;
 };
 
+// Copies of codes that no later work of this layer's step reads again: first
+// to leave L2, which keeps the tables, the scales and the kernel's own code.
+__device__ __forceinline__ uint64_t stream_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void bulk_g2s_hint(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;\n" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(pol)
+      : "memory");
+}
+__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
+
+// One kernel, and each of its phases once in the code: what runs once a call
+// (plan, descriptors, joins) is bound by instruction fetches that miss the
+// caches behind a cold L2.
 template <int ELEM, int CODE>
 __global__ void __launch_bounds__(kA8Warps * 32)
     k_attention8(Cache8View c, Attn8Args a) {
@@ -377,25 +395,30 @@ __global__ void __launch_bounds__(kA8Warps * 32)
   __shared__ int s_unit[2 * kA8Warps];
   __shared__ __align__(8) uint64_t s_bar[kA8Warps * kA8Stages];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = c.G, hkv = c.hkv;
+  const int first_off = kA8Warps * kA8Stages * kA8Entry, part_bytes = (G * kA8Row + 16) * 4;
   uint8_t* ring = sm + warp * (kA8Stages * kA8Entry);
-  float* first_part = reinterpret_cast<float*>(sm + kA8Warps * kA8Stages * kA8Entry) + warp * (G * kA8Row + 16);
   const uint32_t bar0 = smem_u32(s_bar + warp * kA8Stages);
   if (lane == 0) {
     for (int s = 0; s < kA8Stages; s++) mbar_init(bar0 + 8 * s, 1);
     fence_mbar_init();
   }
   if (threadIdx.x < 2 * kA8Warps) s_unit[threadIdx.x] = -1;
+  const uint64_t policy = stream_policy();
   pdl_launch_dependents();
   pdl_wait();
-  if (c.stopped()) return;
 
   // ---- lengths, and the prefix sums of the requests' tiles over all heads ----
-  for (int base = 0, carry = 0; base < a.n_req; base += blockDim.x) {
+  int carry = 0;
+  for (int base = 0; base < a.n_req; base += blockDim.x) {
     const int i = base + threadIdx.x;
-    int n = 0, cost = 0;
+    int n = 0, cost = 0, slot = i;
     if (i < a.n_req) {
-      n = max(a.seq_lens[i], 0);
-      const int slot = a.slots ? a.slots[i] : i;
+      n = a.seq_lens[i];
+      if (a.slots) slot = a.slots[i];
+    }
+    if (base == 0 && c.stopped()) return;       // its load is in flight with theirs
+    if (i < a.n_req) {
+      n = max(n, 0);
       int err = 0;
       if ((unsigned)slot >= (unsigned)c.n_slots) err = DKV_ERR_ARG;
       else if ((long long)n > (long long)c.width * c.T) err = DKV_ERR_TABLE_FULL;
@@ -415,103 +438,63 @@ __global__ void __launch_bounds__(kA8Warps * 32)
     }
     if (lane == 31) s_scan[warp] = x;
     __syncthreads();
-    int before = carry, all = carry;
-    for (int w = 0; w < kA8Warps; w++) {
-      if (w < warp) before += s_scan[w];
-      all += s_scan[w];
-    }
+    int sum = lane < kA8Warps ? s_scan[lane] : 0;
+    const int before = carry + __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0);
+    carry += __reduce_add_sync(0xffffffffu, sum);
     if (i < a.n_req) s_pre[i] = before + x - cost;
-    carry = all;
-    if (threadIdx.x == 0) s_pre[min(base + (int)blockDim.x, a.n_req)] = all;
+    if (threadIdx.x == 0) s_pre[min(base + (int)blockDim.x, a.n_req)] = carry;
     __syncthreads();
   }
-  const int total = s_pre[a.n_req], units = a.n_req * hkv;
+  const int total = carry, units = a.n_req * hkv;
   // CTAs that take part: not so many that warps have no tile, but one a unit
   // (and no CTA without a tile: the join counts on that)
   const int ctas = max(1, min(min((int)gridDim.x, total), max(units, (total + kA8Cta - 1) / kA8Cta)));
-
-  // requests without tokens: zeros
-  for (int i = blockIdx.x; i < a.n_req; i += gridDim.x)
-    if (s_pre[i + 1] == s_pre[i])
-      for (int x = threadIdx.x; x < hkv * G * (kD / 8); x += blockDim.x)
-        reinterpret_cast<uint4*>(a.out + (size_t)i * hkv * G * (2 * kD))[x] = make_uint4(0, 0, 0, 0);
-  if ((int)blockIdx.x >= ctas) return;
+  if ((int)blockIdx.x >= ctas && total > 0) return;
 
   auto start_of = [&](int cta) { return (int)((long long)total * cta / ctas); };
-  auto cta_of = [&](int pos) { return (int)((((long long)pos + 1) * ctas - 1) / total); };
   const int lo = start_of(blockIdx.x), hi = start_of(blockIdx.x + 1);
-  const int w0 = lo + (int)((long long)(hi - lo) * warp / kA8Warps);
-  const int w1 = lo + (int)((long long)(hi - lo) * (warp + 1) / kA8Warps);
+  const int w0 = lo + (int)((unsigned)(hi - lo) * warp / kA8Warps);
+  const int w1 = lo + (int)((unsigned)(hi - lo) * (warp + 1) / kA8Warps);
   const int per = __ffs(c.T / kSub) - 1;     // log2 of the tiles of a block
 
-  auto request_of = [&](int pos) {
-    int r = 0, end = a.n_req;
-    while (end - r > 1) {
-      const int mid = (r + end) >> 1;
-      if (s_pre[mid] <= pos) r = mid; else end = mid;
-    }
-    return r;
-  };
   // first position and tiles of a unit
   auto unit_start = [&](int u, int& count) {
     const int r = u / hkv;
     count = (s_pre[r + 1] - s_pre[r]) / hkv;
     return s_pre[r] + (u - r * hkv) * count;
   };
-  auto describe = [&](int pos) {
-    Desc d;
-    d.src = nullptr;
-    d.ks = d.lv = 0.0f;
-    d.tile = d.unit = 0;
-    d.tail = d.edge = false;
-    if (pos >= w1) return d;
-    const int r = request_of(pos), n = s_len[r], slot = s_slot[r];
-    const Tiles t = tiles_of(n, c.T, a.window, a.sinks);
-    const int rem = pos - s_pre[r], h = rem / t.count, x = rem - h * t.count;
-    d.unit = r * hkv + h;
-    d.tile = x < t.head ? x : x - t.head + t.win;
-    if (d.tile < t.full) {
-      int page = c.table[(size_t)slot * c.width + (d.tile >> per)];
-      if ((unsigned)page >= (unsigned)c.n_pages) {
-        c.latch(DKV_ERR_CHECK, r);
-        page = 0;
-      }
-      const float2 sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * hkv + h));
-      d.ks = sc.x * kLogitScale;
-      d.lv = log2f(sc.y);
-      d.src = c.pages + c.page_head(page, h) + (size_t)(d.tile & ((1 << per) - 1)) * (2 * kTile);
-    } else {
-      d.src = c.tail + c.tail_head(slot, h) + (size_t)(d.tile - t.full) * (4 * kTile);
-      d.tail = true;
-    }
-    d.edge = !sees_all(d.tile * kSub, n, a.window);
-    return d;
-  };
 
   // ---- the warp's tiles, 32 descriptors at a time, a lane each ----
-  Desc cur = describe(w0 + lane), nxt = cur;
-  unsigned cur_tail = __ballot_sync(0xffffffffu, cur.tail), nxt_tail = 0;
+  Desc cur, nxt;
+  nxt.src = nullptr;
+  nxt.unit = nxt.tile = 0;
+  nxt.tail = nxt.edge = false;
+  nxt.sc = make_float2(1.0f, 1.0f);
+  unsigned cur_tail = 0, nxt_tail = 0;
   bool ok = true;
   int ahead = 0;                       // ring entry to fill next
   int at = w0, half = 0;               // tile to issue next, and which half of a tail tile
   int base = w0;                       // first tile of `cur`
   int stage = 0, parity = 0;           // ring entry to read next
-  // the lane that holds a tile's descriptor issues its copy
-  auto issue = [&]() {
-    if (at >= w1) return;
-    const bool in = at - base < 32;
-    const int from = (at - w0) & 31;
-    const bool tail = (in ? cur_tail : nxt_tail) >> from & 1u;
-    if (lane == from && ok) {
-      mbar_expect_tx(bar0 + 8 * ahead, kA8Entry);
-      bulk_g2s(smem_u32(ring + ahead * kA8Entry), (in ? cur.src : nxt.src) + half * kA8Entry, kA8Entry, bar0 + 8 * ahead);
+  // The next `n` entries; the lane that holds a tile's descriptor issues its copy.
+  auto issue = [&](int n) {
+#pragma unroll 1
+    for (; n > 0 && at < w1; n--) {
+      const bool in = at - base < 32;
+      const int from = (at - w0) & 31;
+      const bool tail = (in ? cur_tail : nxt_tail) >> from & 1u;
+      if (lane == from && ok) {
+        mbar_expect_tx(bar0 + 8 * ahead, kA8Entry);
+        bulk_g2s_hint(smem_u32(ring + ahead * kA8Entry), (in ? cur.src : nxt.src) + half * kA8Entry, kA8Entry,
+                      bar0 + 8 * ahead, policy);
+      }
+      ahead = ahead == kA8Stages - 1 ? 0 : ahead + 1;
+      half = tail ? half ^ 1 : 0;
+      at += half ^ 1;
     }
-    ahead = ahead == kA8Stages - 1 ? 0 : ahead + 1;
-    half = tail ? half ^ 1 : 0;
-    at += half ^ 1;
   };
   auto wait = [&]() {                  // the next entry, in shared memory
-    if (!mbar_try_wait(bar0 + 8 * stage, parity) && ok && !mbar_wait_bounded(bar0 + 8 * stage, parity)) {
+    if (!mbar_try_wait(bar0 + 8 * stage, parity) && ok && !slow_wait(bar0 + 8 * stage, parity)) {
       ok = false;
       c.latch(DKV_ERR_TIMEOUT, -1);
     }
@@ -522,42 +505,84 @@ __global__ void __launch_bounds__(kA8Warps * 32)
     }
     return p;
   };
-  for (int s = 0; s < kA8Stages; s++) issue();
-  if (w1 - w0 > 32) {
-    nxt = describe(w0 + 32 + lane);
-    nxt_tail = __ballot_sync(0xffffffffu, nxt.tail);
-  }
 
   State s;
   s.clear();
   uint32_t raw[16], qf[16];
   float qs[2] = {1.0f, 1.0f};
   int unit = -1, N = 0, ustart = 0, ucount = 0;
-  // end of the warp's part of a unit
-  auto flush = [&](int pos) {
-#pragma unroll
-    for (int d = 4; d <= 16; d <<= 1) {
-      s.l[0] += __shfl_xor_sync(0xffffffffu, s.l[0], d);
-      s.l[1] += __shfl_xor_sync(0xffffffffu, s.l[1], d);
+#pragma unroll 1
+  for (int k = 0; w0 < w1; k++) {
+    // descriptors of batch k; the tiles of batch k - 1 follow
+    cur = nxt;
+    cur_tail = nxt_tail;
+    const int pos = w0 + 32 * k + lane;
+    nxt.tail = false;
+    if (pos < w1) {
+      int r = 0, end = a.n_req;        // the request: the last that starts at or before pos
+      while (end - r > 1) {
+        const int mid = (r + end) >> 1;
+        if (s_pre[mid] <= pos) r = mid; else end = mid;
+      }
+      const int n = s_len[r], slot = s_slot[r];
+      const Tiles t = tiles_of(n, c.T, a.window, a.sinks);
+      const int rem = pos - s_pre[r], h = (unsigned)rem / (unsigned)t.count, x = rem - h * t.count;
+      nxt.unit = r * hkv + h;
+      nxt.tile = x < t.head ? x : x - t.head + t.win;
+      nxt.edge = !sees_all(nxt.tile * kSub, n, a.window);
+      if (nxt.tile < t.full) {
+        int page = c.table[(size_t)slot * c.width + (nxt.tile >> per)];
+        if ((unsigned)page >= (unsigned)c.n_pages) {
+          c.latch(DKV_ERR_CHECK, r);
+          page = 0;
+        }
+        nxt.sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * hkv + h));
+        nxt.src = c.pages + c.page_head(page, h) + (size_t)(nxt.tile & ((1 << per) - 1)) * (2 * kTile);
+      } else {
+        nxt.src = c.tail + c.tail_head(slot, h) + (size_t)(nxt.tile - t.full) * (4 * kTile);
+        nxt.tail = true;
+      }
     }
-    if (ustart >= w0 && pos == ustart + ucount) {
-      write_unit<ELEM>(s, a.out + (size_t)unit * G * (2 * kD), G, lane);
-      return;
+    nxt_tail = __ballot_sync(0xffffffffu, nxt.tail);
+    if (k == 0) {
+      base = w0 - 32;                  // nothing in `cur` yet
+      issue(kA8Stages);
+      base = w0;
+      if (w1 - w0 > 32) continue;
+      cur = nxt;
+      cur_tail = nxt_tail;
+    } else if (k == 1) {
+      base = w0;
+    } else {
+      base += 32;
     }
-    // begun before the range: first slot; else it goes on behind the range and
-    // the ring is drained
-    const int slot = ustart < w0 ? 0 : 1;
-    put_partial(s, slot == 0 ? first_part : reinterpret_cast<float*>(ring), G, lane);
-    if (lane == 0) s_unit[2 * warp + slot] = unit;
-  };
-  for (; base < w1; base += 32) {
+    const float my_ks = cur.sc.x * kLogitScale, my_lv = log2f(cur.sc.y);
     const int before = __shfl_up_sync(0xffffffffu, cur.unit, 1);
     const unsigned edges = __ballot_sync(0xffffffffu, cur.edge);
     const unsigned begins = __ballot_sync(0xffffffffu, cur.unit != (lane == 0 ? unit : before));
     const int n = min(32, w1 - base);
-    for (int from = 0; from < n; from++) {
-      if (begins >> from & 1u) {
-        if (unit >= 0) flush(base + from);
+    const bool last = base + 32 >= w1;
+#pragma unroll 1
+    for (int from = 0; from < n + (last ? 1 : 0); from++) {
+      if (from == n || (begins >> from & 1u)) {
+        if (unit >= 0) {
+          // the end of the warp's part of a unit
+#pragma unroll
+          for (int d = 4; d <= 16; d <<= 1) {
+            s.l[0] += __shfl_xor_sync(0xffffffffu, s.l[0], d);
+            s.l[1] += __shfl_xor_sync(0xffffffffu, s.l[1], d);
+          }
+          if (ustart >= w0 && base + from == ustart + ucount) {
+            write_unit<ELEM>(s, a.out + (size_t)unit * G * (2 * kD), G, lane);
+          } else {
+            // begun before the range: a place of its own; else it goes on
+            // behind the range, and the ring is drained
+            const int slot = ustart < w0 ? 0 : 1;
+            put_partial(s, reinterpret_cast<float*>(slot ? ring : sm + first_off + warp * part_bytes), G, lane);
+            if (lane == 0) s_unit[2 * warp + slot] = unit;
+          }
+        }
+        if (from == n) break;
         unit = __shfl_sync(0xffffffffu, cur.unit, from);
         ustart = unit_start(unit, ucount);
         const int r = unit / hkv;
@@ -571,121 +596,127 @@ __global__ void __launch_bounds__(kA8Warps * 32)
           for (int e = 0; e < 16; e++) qf[e] = raw[e];
         }
       }
-      const float ks = __shfl_sync(0xffffffffu, cur.ks, from), lv = __shfl_sync(0xffffffffu, cur.lv, from);
-      const bool edge = edges >> from & 1u;
-      See see;
+      const float ks = __shfl_sync(0xffffffffu, my_ks, from), lv = __shfl_sync(0xffffffffu, my_lv, from);
+      const bool edge = edges >> from & 1u, tail = cur_tail >> from & 1u;
+      See see{true, true, 0xffffffffu};
       if (edge) see = see_of(__shfl_sync(0xffffffffu, cur.tile, from) * kSub, N, a.window, a.sinks, lane);
-      if (!(cur_tail >> from & 1u)) {
+      const uint8_t* p = wait();
+      if (!tail) {
         const float k2[2] = {ks * qs[0], ks * qs[1]};
-        code_tile<CODE>(s, qf, wait(), edge, see, k2, lv);
-        __syncwarp();
-        issue();
+        code_tile<CODE>(s, qf, p, edge, see, k2, lv);
       } else {
-        if (!edge) see = See{true, true, 0xffffffffu};
-        const uint8_t *kp = wait(), *vp = wait();
-        tail_tile<ELEM>(s, raw, kp, vp, see, kLogitScale);
-        __syncwarp();
-        issue();
-        issue();
+        tail_tile<ELEM>(s, raw, p, wait(), see, kLogitScale);
       }
+      __syncwarp();
+      issue(tail ? 2 : 1);
     }
-    cur = nxt;
-    cur_tail = nxt_tail;
-    if (base + 64 < w1) {
-      nxt = describe(base + 64 + lane);
-      nxt_tail = __ballot_sync(0xffffffffu, nxt.tail);
-    }
+    if (last) break;
   }
   // a wait that gave up: no copy may still be in flight at the exit
   if (!ok)
     for (int e = 0; e < kA8Stages; e++) {
-      mbar_wait_bounded(bar0 + 8 * stage, parity);
+      slow_wait(bar0 + 8 * stage, parity);
       if (++stage == kA8Stages) {
         stage = 0;
         parity ^= 1;
       }
     }
-  __syncwarp();
-  if (unit >= 0) flush(w1);
   __syncthreads();
 
-  // ---- join the warps' parts, a query row of a unit per warp ----
+  // ---- joins: a query row of a unit per warp, over the warps' parts and, if
+  // the unit crosses CTAs, again over the CTAs' by the one that arrives last ----
   const int mine = lane < 2 * kA8Warps ? s_unit[lane] : -1;
   const unsigned same = __match_any_sync(0xffffffffu, mine);
   unsigned leaders = __ballot_sync(0xffffffffu, mine >= 0 && __ffs(same) - 1 == lane);
-  auto part = [&](int slot) {
-    return (slot & 1) ? reinterpret_cast<const float*>(sm + (slot >> 1) * (kA8Stages * kA8Entry))
-                      : reinterpret_cast<const float*>(sm + kA8Warps * kA8Stages * kA8Entry) +
-                            (slot >> 1) * (G * kA8Row + 16);
-  };
-  for (int task = 0; leaders; leaders &= leaders - 1) {
-    const int lead = __ffs(leaders) - 1, u = __shfl_sync(0xffffffffu, mine, lead);
-    const unsigned set = __shfl_sync(0xffffffffu, same, lead);
-    for (int q = 0; q < G; q++, task++) {
-      if (task % kA8Warps != warp) continue;
+  const float* my_part = reinterpret_cast<const float*>(
+      sm + ((lane & 1) ? (lane >> 1) * (kA8Stages * kA8Entry) : first_off + (lane >> 1) * part_bytes));
+  const int stride = G * kD + 16;      // floats of a part in the workspace
+  for (int task = warp; task < __popc(leaders) * G; task += kA8Warps) {
+    unsigned rest = leaders;
+    for (int skip = task / G; skip > 0; skip--) rest &= rest - 1;
+    const int lead = __ffs(rest) - 1, q = task % G;
+    const int u = __shfl_sync(0xffffffffu, mine, lead);
+    int count;
+    const int us = unit_start(u, count), ue = us + count;
+    // rows of the parts: lane x holds part x of the round
+    unsigned set = __shfl_sync(0xffffffffu, same, lead);
+    const float* p = my_part;
+    int row = kA8Row, left = 1;
+    int c0 = 0, c1 = 0;
+    float M = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    while (true) {
       const bool has = set >> lane & 1u;
-      const float* p = part(has ? lane : lead);
-      const float m = has ? p[G * kA8Row + q] : -INFINITY;
-      float M = m;
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-      const float f = has ? join(m, M) : 0.0f;
-      float l = has ? f * p[G * kA8Row + 8 + q] : 0.0f;
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float m = has ? p[G * row + q] : -INFINITY, pl = has ? p[G * row + 8 + q] : 0.0f;
+      float now = M;
+      {
+        float x = m;
+#pragma unroll 1
+        for (int d = 16; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        now = fmaxf(now, x);
+      }
+      const float f = has ? join(m, now) : 0.0f, g = join(M, now);
+      M = now;
+      l *= g;
+      o.x *= g;
+      o.y *= g;
+      o.z *= g;
+      o.w *= g;
+#pragma unroll 1
       for (unsigned b = set; b; b &= b - 1) {
         const int x = __ffs(b) - 1;
-        const float g = __shfl_sync(0xffffffffu, f, x);
-        const float4 v = *reinterpret_cast<const float4*>(part(x) + q * kA8Row + 4 * lane);
-        o.x = fmaf(v.x, g, o.x);
-        o.y = fmaf(v.y, g, o.y);
-        o.z = fmaf(v.z, g, o.z);
-        o.w = fmaf(v.w, g, o.w);
+        const float w = __shfl_sync(0xffffffffu, f, x);
+        const float* src = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), x));
+        const float4 v = *reinterpret_cast<const float4*>(src + q * row + 4 * lane);
+        l = fmaf(__shfl_sync(0xffffffffu, pl, x), w, l);
+        o.x = fmaf(v.x, w, o.x);
+        o.y = fmaf(v.y, w, o.y);
+        o.z = fmaf(v.z, w, o.z);
+        o.w = fmaf(v.w, w, o.w);
       }
-      uint8_t* out = a.out + ((size_t)u * G + q) * (2 * kD);
-      int count;
-      const int us = unit_start(u, count), ue = us + count;
-      if (us >= lo && ue <= hi) {
-        write_row<ELEM>(out, lane, o, l);
+      if (--left > 0) {                // further CTAs, 32 at a time
+        c0 += 32;
+        set = c1 - c0 >= 31 ? 0xffffffffu : (1u << (c1 - c0 + 1)) - 1u;
+        p = a.part + (size_t)(2 * min(c0 + lane, c1)) * stride;
         continue;
       }
-      // ---- over CTAs: the one that arrives last joins the parts, in order ----
-      const size_t stride = (size_t)G * kD + 16;
-      float* dst = a.part + (2 * blockIdx.x + (us < lo ? 0 : 1)) * stride;
+      if (row == kD || (us >= lo && ue <= hi)) break;
+      // publish this CTA's part of the row; the last to arrive goes on
+      auto cta_of = [&](int x) { return (int)((((long long)x + 1) * ctas - 1) / total); };
+      c0 = cta_of(us);
+      c1 = cta_of(ue - 1);
+      float* dst = a.part + (size_t)(2 * blockIdx.x + (us < lo ? 0 : 1)) * stride;
       *reinterpret_cast<float4*>(dst + q * kD + 4 * lane) = o;
       if (lane == 0) {
         dst[G * kD + q] = M;
         dst[G * kD + 8 + q] = l;
       }
-      const int c0 = cta_of(us), c1 = cta_of(ue - 1);
       __threadfence();
       __syncwarp();
       unsigned old = 0;
       if (lane == 0) old = atomicInc(a.count + (size_t)u * G + q, (unsigned)(c1 - c0));   // back to zero by itself
-      if (__shfl_sync(0xffffffffu, old, 0) != (unsigned)(c1 - c0)) continue;
+      if (__shfl_sync(0xffffffffu, old, 0) != (unsigned)(c1 - c0)) {
+        row = 0;
+        break;
+      }
       __threadfence();
-      auto cta_part = [&](int x) { return a.part + (2 * x + (x == c0 ? 1 : 0)) * stride; };
+      row = kD;
+      left = (c1 - c0 + 32) / 32;
+      set = c1 - c0 >= 31 ? 0xffffffffu : (1u << (c1 - c0 + 1)) - 1u;
+      p = a.part + (size_t)(2 * min(c0 + lane, c1) + (lane == 0 ? 1 : 0)) * stride;
       M = -INFINITY;
-      for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, __ldcg(cta_part(x) + G * kD + q));
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
       l = 0.0f;
       o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int x = c0; x <= c1; x++) {
-        const float* p = cta_part(x);
-        const float f = join(__ldcg(p + G * kD + q), M);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(p + q * kD + 4 * lane));
-        l = fmaf(__ldcg(p + G * kD + 8 + q), f, l);
-        o.x = fmaf(v.x, f, o.x);
-        o.y = fmaf(v.y, f, o.y);
-        o.z = fmaf(v.z, f, o.z);
-        o.w = fmaf(v.w, f, o.w);
-      }
-      write_row<ELEM>(out, lane, o, l);
     }
+    if (row) write_row<ELEM>(a.out + ((size_t)u * G + q) * (2 * kD), lane, o, l);
   }
+
+  // requests without tokens: zeros
+  for (int i = blockIdx.x; i < a.n_req; i += ctas)
+    if (s_pre[i + 1] == s_pre[i])
+      for (int x = threadIdx.x; x < hkv * G * (kD / 8); x += blockDim.x)
+        reinterpret_cast<uint4*>(a.out + (size_t)i * hkv * G * (2 * kD))[x] = make_uint4(0, 0, 0, 0);
 }
 
 // a counter per query row: rows of one unit are joined apart
