@@ -24,9 +24,10 @@
 // x_j exceeds it by more than 8: w stays below 2^8, in fp16's range. w enters
 // the second product rounded to fp16 (relative 2^-11, the size of the
 // output's own rounding); l sums the unrounded fp32 values.
-// Tiles of the 16-bit tail take s_k = 1 and, for s_v, the power of two below
-// their largest |v|, by which their values are divided (exact but for values
-// 2^-14 and less of the largest).
+// Tiles of the 16-bit tail take s_k = 1 and, for s_v, the power of two that
+// brings their largest |v| to [128, 256), the size of codes, so that equal
+// weights stand for equal contributions; their values are divided by it (exact
+// but for values 2^-20 and less of the largest).
 #include <algorithm>
 
 #include "cache8.cuh"
@@ -36,7 +37,7 @@ namespace dkv {
 namespace {
 
 constexpr int kA8Warps = 12;
-constexpr int kA8Stages = 3;        // ring entries of a warp
+constexpr int kA8Stages = 2;        // ring entries of a warp
 constexpr int kA8Entry = 2 * kTile; // 4 KB: K and V codes of a tile, or K or V of a tail tile
 constexpr int kA8Row = kD + 4;      // floats of a query's row in a shared partial (no bank conflicts)
 constexpr int kA8Cta = 2 * kA8Warps;    // tiles that make a CTA worth its start
@@ -181,9 +182,8 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, uint4 (&w)[4]) {
 template <int CODE>
 __device__ __forceinline__ void code_tile(State& s, const uint32_t (&qf)[16], const uint8_t* p, bool edge,
                                           const See& see, const float (&ks)[2], float lv) {
-  uint4 kw[4], vw[4];
+  uint4 kw[4];
   load_codes(p, kw);
-  load_codes(p + kTile, vw);
   float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < 4; j++) {
@@ -197,6 +197,8 @@ __device__ __forceinline__ void code_tile(State& s, const uint32_t (&qf)[16], co
   }
 #pragma unroll
   for (int e = 0; e < 4; e++) x[e] = fmaf(x[e] + y[e], ks[e & 1], lv);
+  uint4 vw[4];
+  load_codes(p + kTile, vw);
   if (edge) {
 #pragma unroll
     for (int e = 0; e < 4; e++) x[e] = (e < 2 ? see.lo : see.hi) ? x[e] : -INFINITY;
@@ -233,22 +235,35 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t w, float f) {   // f: a 
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Query fragments of a (request, KV head).
+template <int ELEM>
+__device__ __forceinline__ void load_q(const uint8_t* q, int G, int lane, uint32_t (&raw)[16]) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int m = 0; m < 8; m++) {
+    const uint8_t* p = q + (size_t)g * (2 * kD) + 2 * (16 * m + 2 * t);
+    raw[2 * m] = g < G ? *reinterpret_cast<const uint32_t*>(p) : 0u;
+    raw[2 * m + 1] = g < G ? *reinterpret_cast<const uint32_t*>(p + 16) : 0u;
+  }
+}
+__device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
 // A tile of the 16-bit tail: kp, vp point to the lane's first 16 bytes of K
-// and V, the next steps 512 bytes on.
+// and V, the next steps 512 bytes on. qf: the queries in elem_type.
 template <int ELEM>
 __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], const uint8_t* kp, const uint8_t* vp,
                                           const See& see, float ks) {
-  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int m = 0; m < 8; m++) {
     const uint4 w = *reinterpret_cast<const uint4*>(kp + 512 * m);
     const uint32_t a[4] = {w.x, w.z, w.y, w.w};
-    mma_elem<ELEM>(x, a, qf[2 * m], qf[2 * m + 1]);
+    mma_elem<ELEM>(m & 1 ? y : x, a, qf[2 * m], qf[2 * m + 1]);
   }
   // entries of tokens that are not visible (unwritten ones too) become 0
   const uint32_t lo = prmt(see.v, 0, 0x1100u), hi = prmt(see.v, 0, 0x3322u);
   uint4 v[8];
-  float am = 0.0f;
+  uint32_t am2 = 0;        // magnitudes order like their bits
 #pragma unroll
   for (int m = 0; m < 8; m++) {
     v[m] = *reinterpret_cast<const uint4*>(vp + 512 * m);
@@ -256,19 +271,17 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
     v[m].y &= hi;
     v[m].z &= lo;
     v[m].w &= hi;
-    const uint32_t w[4] = {v[m].x, v[m].y, v[m].z, v[m].w};
-#pragma unroll
-    for (int e = 0; e < 4; e++) am = amax_finite(amax_finite(am, lo_elem<ELEM>(w[e])), hi_elem<ELEM>(w[e]));
+    am2 = umax2(umax2(am2, v[m].x & 0x7fff7fffu), umax2(umax2(v[m].y & 0x7fff7fffu, v[m].z & 0x7fff7fffu), v[m].w & 0x7fff7fffu));
   }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, d));
-  // power of two below am, its exponent within what fp16 factors (or the
-  // scale floor) allow
+  const uint32_t bits = __reduce_max_sync(0xffffffffu, max(am2 & 0xffffu, am2 >> 16));
+  const float am = elem_float<ELEM>((uint16_t)bits);
+  // exponents that fp16 factors (or the scale floor) allow; infinite or NaN
+  // values leave 1
   const int low = ELEM == DKV_F16 ? -14 : -100, high = ELEM == DKV_F16 ? 14 : 100;
-  const int ex = max(low, min(high, (int)(__float_as_uint(am) >> 23) - 127));
+  const int ex = am < INFINITY ? max(low, min(high, (int)(__float_as_uint(am) >> 23) - (127 + 7))) : 0;
   const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
-  for (int e = 0; e < 4; e++) x[e] = (e < 2 ? see.lo : see.hi) ? fmaf(x[e], ks, (float)ex) : -INFINITY;
+  for (int e = 0; e < 4; e++) x[e] = (e < 2 ? see.lo : see.hi) ? fmaf(x[e] + y[e], ks, (float)ex) : -INFINITY;
   raise(s, x);
   weights(s, x, inv);
   uint32_t p0 = pack_elems<ELEM>(x[0], x[1]), p1 = pack_elems<ELEM>(x[2], x[3]);
@@ -287,31 +300,20 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
   }
 }
 
-// Query fragments of a (request, KV head): raw, and for bf16 also as fp16
-// after division by the power of two below the row's largest |q| (8 bits fit;
-// what falls below fp16's range is under 2^-24 of that largest). scale: the
-// power of two of the lane's queries 2t, 2t + 1.
-template <int ELEM>
-__device__ __forceinline__ void load_q(const uint8_t* q, int G, int lane, uint32_t (&raw)[16]) {
-  const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int m = 0; m < 8; m++) {
-    const uint8_t* p = q + (size_t)g * (2 * kD) + 2 * (16 * m + 2 * t);
-    raw[2 * m] = g < G ? *reinterpret_cast<const uint32_t*>(p) : 0u;
-    raw[2 * m + 1] = g < G ? *reinterpret_cast<const uint32_t*>(p + 16) : 0u;
-  }
-}
-__device__ __forceinline__ void half_q(const uint32_t (&raw)[16], int lane, uint32_t (&qf)[16], float (&scale)[2]) {
+// bf16 queries as fp16 after division by the power of two below the row's
+// largest |q| (8 bits fit; what falls below fp16's range is under 2^-24 of that
+// largest). scale: the power of two of the lane's queries 2t, 2t + 1.
+__device__ __forceinline__ void half_q(uint32_t (&qf)[16], int lane, float (&scale)[2]) {
   float am = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; i++)
-    am = amax_finite(amax_finite(am, lo_elem<DKV_BF16>(raw[i])), hi_elem<DKV_BF16>(raw[i]));
+    am = amax_finite(amax_finite(am, lo_elem<DKV_BF16>(qf[i])), hi_elem<DKV_BF16>(qf[i]));
   am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
   am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
   const int ex = max(-100, min(100, (int)(__float_as_uint(am) >> 23) - 127));
   const float inv = __uint_as_float((uint32_t)(127 - ex) << 23), sc = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
-  for (int i = 0; i < 16; i++) qf[i] = pack_half2(lo_elem<DKV_BF16>(raw[i]) * inv, hi_elem<DKV_BF16>(raw[i]) * inv);
+  for (int i = 0; i < 16; i++) qf[i] = pack_half2(lo_elem<DKV_BF16>(qf[i]) * inv, hi_elem<DKV_BF16>(qf[i]) * inv);
   const int t = lane & 3;      // row of query 2t: lanes 4 (2t) ..
   scale[0] = __shfl_sync(0xffffffffu, sc, 8 * t);
   scale[1] = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
@@ -365,7 +367,9 @@ __device__ __forceinline__ void write_row(uint8_t* out, int lane, float4 o, floa
 struct Desc {
   const uint8_t* src;    // its 4 KB of codes, or its 8 KB of the tail
   float2 sc;             // s_k, s_v
-  int tile, unit;
+  int tile;
+  int head;              // request << 12 | KV head (4096 at most)
+  int start;             // first position of its unit
   bool tail, edge;
 };
 
@@ -382,6 +386,12 @@ __device__ __forceinline__ void bulk_g2s_hint(uint32_t dst, const void* src, uin
       "l"(src), "r"(bytes), "r"(bar), "l"(pol)
       : "memory");
 }
+// largest of the lanes' values, in one instruction (NaN is passed over)
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
 
 // One kernel, and each of its phases once in the code: what runs once a call
@@ -393,6 +403,7 @@ __global__ void __launch_bounds__(kA8Warps * 32)
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ int s_pre[kMaxCallReq + 1], s_len[kMaxCallReq], s_slot[kMaxCallReq], s_scan[32];
   __shared__ int s_unit[2 * kA8Warps];
+  __shared__ int2 s_span[2 * kA8Warps];     // its positions
   __shared__ __align__(8) uint64_t s_bar[kA8Warps * kA8Stages];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = c.G, hkv = c.hkv;
   const int first_off = kA8Warps * kA8Stages * kA8Entry, part_bytes = (G * kA8Row + 16) * 4;
@@ -457,17 +468,10 @@ __global__ void __launch_bounds__(kA8Warps * 32)
   const int w1 = lo + (int)((unsigned)(hi - lo) * (warp + 1) / kA8Warps);
   const int per = __ffs(c.T / kSub) - 1;     // log2 of the tiles of a block
 
-  // first position and tiles of a unit
-  auto unit_start = [&](int u, int& count) {
-    const int r = u / hkv;
-    count = (s_pre[r + 1] - s_pre[r]) / hkv;
-    return s_pre[r] + (u - r * hkv) * count;
-  };
-
   // ---- the warp's tiles, 32 descriptors at a time, a lane each ----
   Desc cur, nxt;
   nxt.src = nullptr;
-  nxt.unit = nxt.tile = 0;
+  nxt.head = nxt.tile = nxt.start = 0;
   nxt.tail = nxt.edge = false;
   nxt.sc = make_float2(1.0f, 1.0f);
   unsigned cur_tail = 0, nxt_tail = 0;
@@ -508,9 +512,10 @@ __global__ void __launch_bounds__(kA8Warps * 32)
 
   State s;
   s.clear();
-  uint32_t raw[16], qf[16];
+  uint32_t qf[16];
+  const uint8_t* q_at = nullptr;
   float qs[2] = {1.0f, 1.0f};
-  int unit = -1, N = 0, ustart = 0, ucount = 0;
+  int unit = -1, N = 0, ustart = 0, uend = 0, last_start = -1;
 #pragma unroll 1
   for (int k = 0; w0 < w1; k++) {
     // descriptors of batch k; the tiles of batch k - 1 follow
@@ -527,7 +532,8 @@ __global__ void __launch_bounds__(kA8Warps * 32)
       const int n = s_len[r], slot = s_slot[r];
       const Tiles t = tiles_of(n, c.T, a.window, a.sinks);
       const int rem = pos - s_pre[r], h = (unsigned)rem / (unsigned)t.count, x = rem - h * t.count;
-      nxt.unit = r * hkv + h;
+      nxt.head = r << 12 | h;
+      nxt.start = pos - x;
       nxt.tile = x < t.head ? x : x - t.head + t.win;
       nxt.edge = !sees_all(nxt.tile * kSub, n, a.window);
       if (nxt.tile < t.full) {
@@ -557,9 +563,9 @@ __global__ void __launch_bounds__(kA8Warps * 32)
       base += 32;
     }
     const float my_ks = cur.sc.x * kLogitScale, my_lv = log2f(cur.sc.y);
-    const int before = __shfl_up_sync(0xffffffffu, cur.unit, 1);
+    const int before = __shfl_up_sync(0xffffffffu, cur.start, 1);
     const unsigned edges = __ballot_sync(0xffffffffu, cur.edge);
-    const unsigned begins = __ballot_sync(0xffffffffu, cur.unit != (lane == 0 ? unit : before));
+    const unsigned begins = __ballot_sync(0xffffffffu, cur.start != (lane == 0 ? last_start : before));
     const int n = min(32, w1 - base);
     const bool last = base + 32 >= w1;
 #pragma unroll 1
@@ -572,29 +578,29 @@ __global__ void __launch_bounds__(kA8Warps * 32)
             s.l[0] += __shfl_xor_sync(0xffffffffu, s.l[0], d);
             s.l[1] += __shfl_xor_sync(0xffffffffu, s.l[1], d);
           }
-          if (ustart >= w0 && base + from == ustart + ucount) {
+          if (ustart >= w0 && base + from == uend) {
             write_unit<ELEM>(s, a.out + (size_t)unit * G * (2 * kD), G, lane);
           } else {
             // begun before the range: a place of its own; else it goes on
             // behind the range, and the ring is drained
             const int slot = ustart < w0 ? 0 : 1;
             put_partial(s, reinterpret_cast<float*>(slot ? ring : sm + first_off + warp * part_bytes), G, lane);
-            if (lane == 0) s_unit[2 * warp + slot] = unit;
+            if (lane == 0) {
+              s_unit[2 * warp + slot] = unit;
+              s_span[2 * warp + slot] = make_int2(ustart, uend);
+            }
           }
         }
         if (from == n) break;
-        unit = __shfl_sync(0xffffffffu, cur.unit, from);
-        ustart = unit_start(unit, ucount);
-        const int r = unit / hkv;
+        const int rh = __shfl_sync(0xffffffffu, cur.head, from), r = rh >> 12, h = rh & 4095;
+        ustart = last_start = __shfl_sync(0xffffffffu, cur.start, from);
+        unit = r * hkv + h;
         N = s_len[r];
+        uend = ustart + tiles_of(N, c.T, a.window, a.sinks).count;
         s.clear();
-        load_q<ELEM>(a.q + r * a.qs + (size_t)(unit - r * hkv) * G * (2 * kD), G, lane, raw);
-        if (ELEM == DKV_BF16) {
-          half_q(raw, lane, qf, qs);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; e++) qf[e] = raw[e];
-        }
+        q_at = a.q + r * a.qs + (size_t)h * G * (2 * kD);
+        load_q<ELEM>(q_at, G, lane, qf);
+        if (ELEM == DKV_BF16) half_q(qf, lane, qs);
       }
       const float ks = __shfl_sync(0xffffffffu, my_ks, from), lv = __shfl_sync(0xffffffffu, my_lv, from);
       const bool edge = edges >> from & 1u, tail = cur_tail >> from & 1u;
@@ -605,7 +611,14 @@ __global__ void __launch_bounds__(kA8Warps * 32)
         const float k2[2] = {ks * qs[0], ks * qs[1]};
         code_tile<CODE>(s, qf, p, edge, see, k2, lv);
       } else {
-        tail_tile<ELEM>(s, raw, p, wait(), see, kLogitScale);
+        const uint8_t* v = wait();
+        if (ELEM == DKV_F16) {
+          tail_tile<ELEM>(s, qf, p, v, see, kLogitScale);
+        } else {
+          uint32_t raw[16];    // the other tiles' fragments are scaled
+          load_q<ELEM>(q_at, G, lane, raw);
+          tail_tile<ELEM>(s, raw, p, v, see, kLogitScale);
+        }
       }
       __syncwarp();
       issue(tail ? 2 : 1);
@@ -636,8 +649,7 @@ __global__ void __launch_bounds__(kA8Warps * 32)
     for (int skip = task / G; skip > 0; skip--) rest &= rest - 1;
     const int lead = __ffs(rest) - 1, q = task % G;
     const int u = __shfl_sync(0xffffffffu, mine, lead);
-    int count;
-    const int us = unit_start(u, count), ue = us + count;
+    const int us = s_span[lead].x, ue = s_span[lead].y;
     // rows of the parts: lane x holds part x of the round
     unsigned set = __shfl_sync(0xffffffffu, same, lead);
     const float* p = my_part;
@@ -648,13 +660,7 @@ __global__ void __launch_bounds__(kA8Warps * 32)
     while (true) {
       const bool has = set >> lane & 1u;
       const float m = has ? p[G * row + q] : -INFINITY, pl = has ? p[G * row + 8 + q] : 0.0f;
-      float now = M;
-      {
-        float x = m;
-#pragma unroll 1
-        for (int d = 16; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-        now = fmaxf(now, x);
-      }
+      const float now = fmaxf(M, warp_max(m));
       const float f = has ? join(m, now) : 0.0f, g = join(M, now);
       M = now;
       l *= g;
@@ -662,18 +668,31 @@ __global__ void __launch_bounds__(kA8Warps * 32)
       o.y *= g;
       o.z *= g;
       o.w *= g;
+      // two parts at a time
 #pragma unroll 1
-      for (unsigned b = set; b; b &= b - 1) {
-        const int x = __ffs(b) - 1;
-        const float w = __shfl_sync(0xffffffffu, f, x);
-        const float* src = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), x));
-        const float4 v = *reinterpret_cast<const float4*>(src + q * row + 4 * lane);
-        l = fmaf(__shfl_sync(0xffffffffu, pl, x), w, l);
-        o.x = fmaf(v.x, w, o.x);
-        o.y = fmaf(v.y, w, o.y);
-        o.z = fmaf(v.z, w, o.z);
-        o.w = fmaf(v.w, w, o.w);
+      for (unsigned b = set; b;) {
+        const int x0 = __ffs(b) - 1;
+        b &= b - 1;
+        const int x1 = b ? __ffs(b) - 1 : x0;
+        const bool two = b != 0;
+        b &= b - 1;
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(p + q * row);
+        const float4 v0 = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, mine, x0))[lane];
+        const float4 v1 = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, mine, x1))[lane];
+        const float f0 = __shfl_sync(0xffffffffu, f, x0), l0 = __shfl_sync(0xffffffffu, pl, x0);
+        const float f1 = __shfl_sync(0xffffffffu, f, x1), l1 = __shfl_sync(0xffffffffu, pl, x1);
+        l = fmaf(l0, f0, l);
+        o.x = fmaf(v0.x, f0, o.x);
+        o.y = fmaf(v0.y, f0, o.y);
+        o.z = fmaf(v0.z, f0, o.z);
+        o.w = fmaf(v0.w, f0, o.w);
+        if (two) {
+          l = fmaf(l1, f1, l);
+          o.x = fmaf(v1.x, f1, o.x);
+          o.y = fmaf(v1.y, f1, o.y);
+          o.z = fmaf(v1.z, f1, o.z);
+          o.w = fmaf(v1.w, f1, o.w);
+        }
       }
       if (--left > 0) {                // further CTAs, 32 at a time
         c0 += 32;
