@@ -521,8 +521,10 @@ int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* se
   }
   Device8 dev(cache->device);
   if (!dev.ok) return DKV_ERR_CUDA;
+  const int sms = sm_count(cache->device);
+  if (!sms) return DKV_ERR_CUDA;
   const cudaError_t e = launch_prefill8(view(cache), cache->elem_type, seq_lens, n_req, q, q_stride, k, k_stride, v,
-                                        v_stride, out, window, sinks, reinterpret_cast<cudaStream_t>(stream));
+                                        v_stride, out, window, sinks, sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DKV_OK : DKV_ERR_CUDA;
 }
 

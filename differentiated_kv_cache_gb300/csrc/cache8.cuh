@@ -111,9 +111,8 @@ cudaError_t launch_attention8(const Cache8View& c, int elem, int code, int sm_co
                               const int* seq_lens, int n_req, const void* q, long long q_stride, void* out,
                               int window, int sinks, void* workspace, cudaStream_t st);
 size_t attention8_workspace(int hkv, int G, int max_req, int sm_count);
-struct Prefill8Args;
 cudaError_t launch_prefill8(const Cache8View& c, int elem, const int32_t* seq_lens, int n_req, const void* q,
                             long long qs, const void* k, long long ks, const void* v, long long vs, void* out,
-                            int window, int sinks, cudaStream_t st);
+                            int window, int sinks, int sm_count, cudaStream_t st);
 
 }  // namespace dkv

@@ -2,19 +2,27 @@
 // sliding window and first tokens that stay visible (include/dkv.h:
 // dkv_cache8_prefill), fp16 or bf16, on the fifth-generation tensor cores.
 //
-// A CTA takes 128 query rows of one request and KV head: row r is token
-// r / G of the CTA's floor(128 / G), query head r % G of the group, so one
-// K / V tile serves the whole group and a tile of rows spans few positions
-// (the keys that only part of its rows see stay few). Warp 0 issues the TMA
-// copies (the queries once, 128-key K and V tiles through two stages each),
-// warp 1 the MMAs, warps 2..5 run the softmax with one thread per row:
-//   S = Q K^T        tcgen05, D in tensor memory, three buffers
-//   P = 2^(S - m)    lazily raised row maximum, written over S in 16 bits
+// A work item is 256 query rows of one request and KV head in two halves of
+// 128: row r of a half is token r / G of its floor(128 / G), query head r % G of
+// the group, so one K / V tile serves the whole group twice and a half spans few
+// positions (keys that only part of its rows see stay few). Persistent CTAs, one
+// an SM; warp 0 issues the TMA copies (an item's queries, 128-key K and V tiles
+// through two stages each), warps 1 and 2 the MMAs of a half each, warps 4..7 and 8..11 run the softmax
+// of the halves with one thread per row (and most of the registers):
+//   S = Q K^T        tcgen05, D in tensor memory
+//   P = 2^(S - m)    written over S in 16 bits; m is a maximum of earlier keys,
+//                    raised (O, l rescaled) only when a row's P of a tile sum
+//                    to over 2^12, so that most tiles need no maximum at all
 //   O += P V         tcgen05, A = P from tensor memory, V MN-major
-// Only key tiles with a visible key are visited: [0, first) of the first
-// tokens, then the window's up to the diagonal. Every wait is bounded; on
-// expiry the kernel latches DKV_ERR_TIMEOUT, waits (bounded) for its own
-// copies and MMAs, frees its tensor memory and returns.
+// The halves do not wait for one another, so one half's products run while the
+// other half's softmax does, and the next item's first products while this
+// item's results are written. (Tensor memory is full with two S and two O, so P
+// lies over S, and the next S of a half is issued once its P V is done.)
+// Only key tiles with a visible key are visited, the window's from the diagonal
+// back (the nearest keys give a good first m), then the first tokens'; of each,
+// a half takes the 32-key parts that some of its rows may see. Every wait is bounded; on expiry
+// the kernel latches DKV_ERR_TIMEOUT, waits (bounded) for its own copies and
+// MMAs, frees its tensor memory and returns.
 #include <algorithm>
 #include <cudaTypedefs.h>
 
@@ -28,19 +36,19 @@ cudaError_t tma_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
 
 namespace {
 
-constexpr int kW8T = 128;                  // query rows per CTA, keys per tile
-constexpr int kW8Threads = 192;
+constexpr int kW8T = 128;                  // query rows of a half, keys of a tile
+constexpr int kW8Threads = 384;
+// registers a thread: launched with 168; 128 x 88 + 256 x 208 = 384 x 168
+constexpr int kW8RegsFew = 88, kW8RegsMany = 208;
 constexpr int kW8Half = kW8T * 128;        // 64 features of 128 rows: 16 KB
 constexpr int kW8Tile = 2 * kW8Half;
-constexpr int kW8Stages = 2;
-constexpr int kW8OffK = kW8Tile;
-constexpr int kW8OffV = kW8OffK + kW8Stages * kW8Tile;
-constexpr int kW8OffBar = kW8OffV + kW8Stages * kW8Tile;
+constexpr int kW8OffK = 2 * kW8Tile;       // after the queries of both halves
+constexpr int kW8OffV = kW8OffK + 2 * kW8Tile;
+constexpr int kW8OffBar = kW8OffV + 2 * kW8Tile;
 constexpr int kW8Smem = 1024 + kW8OffBar + 256;
-constexpr int kW8SBufs = 3;
-constexpr uint32_t kW8OCol = kW8SBufs * 128;
+constexpr uint32_t kW8OCol = 256;          // S of the halves, then O of the halves
 constexpr uint32_t kW8Cols = 512;
-constexpr float kW8Lazy = 8.0f;
+constexpr float kW8Most = 4096.0f;         // largest sum of a row's P of one tile (fp16 holds 65504)
 
 constexpr int kW8Req = 1024;
 struct W8Call {
@@ -51,8 +59,73 @@ struct W8Call {
 
 struct W8Args {
   uint8_t* out;
-  int window, sinks, tq;     // tq: tokens of a query tile
+  int window, sinks, tq;     // tq: tokens of a half
 };
+
+// A work item: 2 tq positions from p0 of request i (its tokens at row t0, n0 of
+// them) and KV head h; `near` key tiles back from `last`, then the first tiles,
+// `count` in all.
+struct Item {
+  int h, t0, n0, p0, last, near, count;
+  __device__ __forceinline__ int key(int j) const { return (j < near ? last - j : j - near) * kW8T; }
+};
+__device__ __forceinline__ Item item_of(int x, const Cache8View& c, const W8Args& a, const W8Call& call) {
+  Item it;
+  it.h = x % c.hkv;
+  const int qtile = call.tile0[call.n_req] - 1 - x / c.hkv;     // later rows first: more keys
+  int i = 0, hi = call.n_req;
+  while (hi - i > 1) {
+    const int mid = (i + hi) >> 1;
+    if (call.tile0[mid] <= qtile) i = mid; else hi = mid;
+  }
+  it.t0 = call.tok0[i];
+  it.n0 = call.tok0[i + 1] - it.t0;
+  it.p0 = (qtile - call.tile0[i]) * 2 * a.tq;
+  it.last = (min(it.p0 + 2 * a.tq, it.n0) - 1) / kW8T;
+  int from = 0, first = 0;
+  if (a.window > 0) {
+    from = max(it.p0 - a.window + 1, 0) / kW8T;
+    first = min((min(a.sinks, it.n0) + kW8T - 1) / kW8T, from);
+  }
+  it.near = it.last - from + 1;
+  it.count = it.near + first;
+  return it;
+}
+
+// The 32-key parts [c0, c1) of the tile at key kt that a half's rows may see
+// (one at least).
+struct Parts {
+  int c0, c1;
+};
+__device__ __forceinline__ Parts parts_of(const Item& it, const W8Args& a, int half, int kt) {
+  const int q0 = it.p0 + half * a.tq, q1 = max(min(q0 + a.tq, it.n0) - 1, q0);
+  const int hi = min(q1 - kt, kW8T - 1), lo = a.window > 0 ? max(q0 - a.window + 1 - kt, 0) : 0;
+  const int early = a.window > 0 ? min(a.sinks - kt, kW8T) : 0;
+  Parts p{4, 0};
+  if (lo <= hi) p = Parts{lo >> 5, (hi >> 5) + 1};
+  if (early > 0) p = Parts{0, max(p.c1, (early + 31) >> 5)};
+  if (p.c1 <= p.c0) p = Parts{0, 1};
+  return p;
+}
+
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// bits [0, n)
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+// Values of a tensor-memory load are used after the wait only.
+__device__ __forceinline__ void loaded32(float* v) {
+#pragma unroll
+  for (int e = 0; e < 32; e++) asm volatile("" : "+f"(v[e]));
+}
 
 template <int ELEM>
 __global__ void __launch_bounds__(kW8Threads, 1)
@@ -61,56 +134,28 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   pdl_launch_dependents();
   pdl_wait();
   if (c.stopped()) return;
-  const int G = c.G, h = blockIdx.x % c.hkv;
-  const int qtile = call.tile0[call.n_req] - 1 - (int)(blockIdx.x / c.hkv);   // later rows first: more keys
-  int i = 0;
-  {
-    int hi = call.n_req;
-    while (hi - i > 1) {
-      const int mid = (i + hi) >> 1;
-      if (call.tile0[mid] <= qtile) i = mid; else hi = mid;
-    }
-  }
-  const int t0 = call.tok0[i], n0 = call.tok0[i + 1] - t0;
-  const int p0 = (qtile - call.tile0[i]) * a.tq, p1 = min(p0 + a.tq, n0) - 1;   // positions of the CTA
-  // key tiles: [0, first), then [from, last]
-  const int last = p1 / kW8T;
-  int from = 0, first = 0;
-  if (a.window > 0) {
-    from = max(p0 - a.window + 1, 0) / kW8T;
-    first = min((min(a.sinks, n0) + kW8T - 1) / kW8T, from);
-  }
-  const int nkt = first + last - from + 1;
-  auto key_tile = [&](int j) { return j < first ? j : j - first + from; };
+  const int items = call.tile0[call.n_req] * c.hkv, G = c.G;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kW8OffBar);
   const uint32_t b0 = smem_u32(bars);
-  const uint32_t qfull = b0, ofull = b0 + 8u * 18;
-  auto kfull = [&](int s) { return b0 + 8u * (1 + s); };
-  auto kempty = [&](int s) { return b0 + 8u * (3 + s); };
-  auto vfull = [&](int s) { return b0 + 8u * (5 + s); };
-  auto vempty = [&](int s) { return b0 + 8u * (7 + s); };
-  auto sfull = [&](int b) { return b0 + 8u * (9 + b); };
-  auto pfull = [&](int b) { return b0 + 8u * (12 + b); };
-  auto pvdone = [&](int b) { return b0 + 8u * (15 + b); };
-  uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 19);
+  // A commit of MMAs costs the issuing thread hundreds of cycles: one a
+  // product. S and P V of step n (= tile n of the CTA's sequence) signal sdone
+  // and pvdone of (half, n & 1); a K (V) stage is free when both halves' S (P V)
+  // of its tile are done, the queries when both halves' last S of an item are.
+  const uint32_t qfull = b0;
+  auto kfull = [&](int s) { return b0 + 16u + 8u * s; };
+  auto vfull = [&](int s) { return b0 + 32u + 8u * s; };
+  auto pfull = [&](int h) { return b0 + 48u + 8u * h; };
+  auto sdone = [&](int h, int n) { return b0 + 64u + 16u * h + 8u * (n & 1); };
+  auto pvdone = [&](int h, int n) { return b0 + 96u + 16u * h + 8u * (n & 1); };
+  auto drain = [&](int h) { return b0 + 128u + 8u * h; };
+  uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 18);
   int* s_fail = reinterpret_cast<int*>(s_taddr + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(qfull, 1);
-    mbar_init(ofull, 1);
-    for (int s = 0; s < kW8Stages; s++) {
-      mbar_init(kfull(s), 1);
-      mbar_init(kempty(s), 1);
-      mbar_init(vfull(s), 1);
-      mbar_init(vempty(s), 1);
-    }
-    for (int b = 0; b < kW8SBufs; b++) {
-      mbar_init(sfull(b), 1);
-      mbar_init(pfull(b), 128);
-      mbar_init(pvdone(b), 1);
-    }
+    for (int s = 0; s < 18; s++) mbar_init(b0 + 8u * s, 1);
+    for (int h = 0; h < 2; h++) mbar_init(pfull(h), 4);        // a lane of each warp
     *s_fail = 0;
     fence_mbar_init();
   }
@@ -120,173 +165,226 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   tc_fence_after();
   const uint32_t tbase = *s_taddr;
   auto fail = [&]() {
-    c.latch(DKV_ERR_TIMEOUT, i);
+    c.latch(DKV_ERR_TIMEOUT, -1);
     *(volatile int*)s_fail = 1;
   };
   auto failed = [&]() { return *(volatile int*)s_fail != 0; };
 
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kW8RegsFew));
   if (warp == 0) {
+    // ---- copies: an item's first K tile, its queries, then K(j + 1) ahead of V(j) ----
     if (lane == 0) {
-      mbar_expect_tx(qfull, (uint32_t)(2 * 128 * a.tq * G));
-      for (int f = 0; f < 2; f++)
-        tma_load_3d(smem_u32(smem + f * kW8Half), &tq, 64 * f, h * G, t0 + p0, qfull);
-      int last_k[kW8Stages] = {-1, -1}, last_v[kW8Stages] = {-1, -1};
-      auto load = [&](int j, bool is_k) {
-        const int s = j & 1;
+      int nk = 0, nv = 0, nq = 0;      // K tiles, V tiles and items so far
+      bool ok = true;
+      auto load = [&](const Item& it, int j, bool is_k) {
+        const int t = is_k ? nk : nv, s = t & 1;
         const uint32_t full = is_k ? kfull(s) : vfull(s);
-        if (j >= 2 && !mbar_wait_bounded(is_k ? kempty(s) : vempty(s), ((j >> 1) - 1) & 1)) return false;
+        if (t >= 2)          // tile t - 2 of the stage is done with
+          for (int h = 0; h < 2; h++)
+            if (!mbar_wait_bounded(is_k ? sdone(h, t) : pvdone(h, t), ((t >> 1) - 1) & 1)) return false;
         mbar_expect_tx(full, kW8Tile);
         for (int f = 0; f < 2; f++)
           tma_load_3d(smem_u32(smem + (is_k ? kW8OffK : kW8OffV) + s * kW8Tile + f * kW8Half), is_k ? &tk : &tv,
-                      64 * f, h, t0 + key_tile(j) * kW8T, full);
-        (is_k ? last_k : last_v)[s] = j;
+                      64 * f, it.h, it.t0 + it.key(j), full);
+        (is_k ? nk : nv)++;
         return true;
       };
-      bool ok = load(0, true);
-      for (int j = 0; ok && j < nkt && !failed(); j++) {
-        if (j + 1 < nkt) ok = load(j + 1, true);
-        if (ok) ok = load(j, false);
+      for (int x = blockIdx.x; ok && x < items && !failed(); x += gridDim.x) {
+        const Item it = item_of(x, c, a, call);
+        const int t = nk - 1;          // the last tile of the item before
+        ok = load(it, 0, true);
+        if (nq > 0)
+          for (int h = 0; h < 2; h++) ok = ok && mbar_wait_bounded(sdone(h, t), (t >> 1) & 1);
+        if (!ok) break;
+        mbar_expect_tx(qfull, (uint32_t)(4 * 128 * a.tq * G));
+        for (int f = 0; f < 4; f++)
+          tma_load_3d(smem_u32(smem + f * kW8Half), &tq, 64 * (f & 1), it.h * G, it.t0 + it.p0 + (f >> 1) * a.tq, qfull);
+        nq++;
+        for (int j = 0; ok && j < it.count && !failed(); j++) {
+          if (j + 1 < it.count) ok = load(it, j + 1, true);
+          if (ok) ok = load(it, j, false);
+        }
       }
       if (!ok) fail();
       // no copy of this CTA may still be in flight when it exits
-      mbar_wait_bounded(qfull, 0);
-      for (int s = 0; s < kW8Stages; s++) {
-        if (last_k[s] >= 0) mbar_wait_bounded(kfull(s), (last_k[s] >> 1) & 1);
-        if (last_v[s] >= 0) mbar_wait_bounded(vfull(s), (last_v[s] >> 1) & 1);
-      }
+      if (nq > 0) mbar_wait_bounded(qfull, (nq - 1) & 1);
+      for (int t = max(nk - 2, 0); t < nk; t++) mbar_wait_bounded(kfull(t & 1), (t >> 1) & 1);
+      for (int t = max(nv - 2, 0); t < nv; t++) mbar_wait_bounded(vfull(t & 1), (t >> 1) & 1);
     }
-  } else if (warp == 1) {
+  } else if (warp < 3) {
+    // ---- MMAs of a half: S of step n once P V of step n - 1 is done, then P V ----
     if (lane == 0) {
       constexpr uint32_t type = ELEM == DKV_BF16 ? (1u << 7) | (1u << 10) : 0u;   // A and B formats
-      constexpr uint32_t id_qk = umma_idesc_f16(128, 128) | type;
       constexpr uint32_t id_pv = umma_idesc_f16(128, 128) | type | (1u << 16);   // B (V) MN-major
-      const uint32_t qs = smem_u32(smem);
-      bool ok = mbar_wait_bounded(qfull, 0);
-      auto issue_qk = [&](int t) {
-        const int b = t % kW8SBufs, s = t & 1;
-        if (t >= kW8SBufs && !mbar_wait_bounded(pvdone(b), ((t / kW8SBufs) - 1) & 1)) return false;
-        if (!mbar_wait_bounded(kfull(s), (t >> 1) & 1)) return false;
-        tc_fence_after();
-        const uint32_t ks = smem_u32(smem + kW8OffK + s * kW8Tile);
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-          const uint32_t off = (k >> 2) * kW8Half + (k & 3) * 32;
-          umma_f16(tbase + b * 128, umma_desc_sw128(qs + off), umma_desc_sw128(ks + off), id_qk, k > 0);
-        }
-        umma_commit(kempty(s));
-        umma_commit(sfull(b));
-        return true;
-      };
-      auto issue_pv = [&](int t) {
-        const int b = t % kW8SBufs, s = t & 1;
-        if (!mbar_wait_bounded(pfull(b), (t / kW8SBufs) & 1)) return false;
-        if (!mbar_wait_bounded(vfull(s), (t >> 1) & 1)) return false;
-        tc_fence_after();
-        const uint32_t vs = smem_u32(smem + kW8OffV + s * kW8Tile);
-#pragma unroll
-        for (int kk = 0; kk < 8; kk++)
-          umma_f16_tmem_a(tbase + kW8OCol, tbase + b * 128 + 8 * kk, umma_desc_sw128_mn(vs + kk * 2048, kW8Half), id_pv,
-                          t > 0 || kk > 0);
-        umma_commit(vempty(s));
-        umma_commit(pvdone(b));
-        return true;
-      };
-      if (ok && !issue_qk(0)) ok = false;
-      for (int j = 0; ok && j < nkt && !failed(); j++) {
-        if (j + 1 < nkt && !issue_qk(j + 1)) { ok = false; break; }
-        if (!issue_pv(j)) { ok = false; break; }
-      }
-      if (!ok) fail();
-      umma_commit(ofull);
-      mbar_wait_bounded(ofull, 0);
-    }
-  } else {
-    const int lg = warp & 3, row = 32 * lg + lane, pos = p0 + row / G;
-    const bool real = row < a.tq * G && pos < n0;
-    const uint32_t tl = tbase + ((uint32_t)(32 * lg) << 16);
-    float m = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int j = 0; j < nkt; j++) {
-      const int b = j % kW8SBufs, kt = key_tile(j) * kW8T;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(sfull(b), (j / kW8SBufs) & 1) && !failed());
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull(j & 1), (j >> 1) & 1));
-      if (!ok) break;
-      tc_fence_after();
-      if (kt + kW8T > n0) {
-        // V rows behind the request belong to others: zero them, whatever they
-        // hold (their weight is 0, but 0 * Inf is not)
-        uint8_t* vs = smem + kW8OffV + (j & 1) * kW8Tile;
-        for (int x = threadIdx.x - 64; x < 2 * (kt + kW8T - n0) * 8; x += 128) {
-          const int f = x & 1, r = n0 - kt + (x >> 4), o = (x >> 1) & 7;
-          *reinterpret_cast<uint4*>(vs + f * kW8Half + r * 128 + 16 * o) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
-      }
-      float x[128];
-#pragma unroll
-      for (int q = 0; q < 4; q++) tmem_ld32_nowait(tl + b * 128 + 32 * q, x + 32 * q);
-      tmem_wait_ld();
-      const bool edge = kt + kW8T - 1 > p0 || (a.window > 0 && kt <= p1 - a.window);
-      if (edge) {
-        // keys [lo, hi] of the window, or below the number of first tokens
-        const int hi = pos - kt, lo = a.window > 0 ? pos - a.window + 1 - kt : 0, early = a.window > 0 ? a.sinks - kt : 0;
-#pragma unroll
-        for (int q = 0; q < 128; q++)
-          if (q > hi || (q < lo && q >= early)) x[q] = -INFINITY;
-      }
-      float mx = x[0];
-#pragma unroll
-      for (int q = 1; q < 128; q++) mx = fmaxf(mx, x[q]);
-      const float mxs = mx * kLogitScale;
-      if (__any_sync(0xffffffffu, mxs > m + kW8Lazy)) {
-        const float mn = fmaxf(m, mxs);
-        if (j > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone((j - 1) % kW8SBufs), ((j - 1) / kW8SBufs) & 1));
+      const int h = warp - 1;
+      const uint32_t ts = tbase + h * 128, to = tbase + kW8OCol + h * 128;
+      const uint64_t qd = umma_desc_sw128(smem_u32(smem + h * kW8Tile));
+      const uint64_t kd = umma_desc_sw128(smem_u32(smem + kW8OffK)), vd = umma_desc_sw128_mn(smem_u32(smem + kW8OffV), kW8Half);
+      int n = 0, ii = 0;
+      bool ok = true;
+      for (int x = blockIdx.x; ok && x < items; x += gridDim.x, ii++) {
+        const Item it = item_of(x, c, a, call);
+        ok = mbar_wait_bounded(qfull, ii & 1);
+        for (int j = 0; ok && j < it.count; j++, n++) {
+          const Parts p = parts_of(it, a, h, it.key(j));
+          const int s = n & 1, par = (n >> 1) & 1;
+          const uint32_t id = umma_idesc_f16(128, 32 * (p.c1 - p.c0)) | type;
+          uint64_t ad = qd, bd = kd + ((s * kW8Tile + 4096 * p.c0) >> 4);
+          ok = mbar_wait_bounded(kfull(s), par) && (n == 0 || mbar_wait_bounded(pvdone(h, n - 1), ((n - 1) >> 1) & 1));
           if (!ok) break;
           tc_fence_after();
-          const float f = mn == -INFINITY ? 1.0f : fast_exp2(m - mn);
-          l *= f;
-#pragma unroll 1
-          for (int q = 0; q < 4; q++) {
-            float o[32];
-            tmem_ld32_nowait(tl + kW8OCol + 32 * q, o);
-            tmem_wait_ld();
-            uint32_t w[32];
 #pragma unroll
-            for (int e = 0; e < 32; e++) w[e] = __float_as_uint(o[e] * f);
-            tmem_st32(tl + kW8OCol + 32 * q, w);
+          for (int k = 0; k < 8; k++) {
+            umma_f16(ts + 32 * p.c0, ad, bd, id, k > 0);
+            const int step = (k == 3 ? kW8Half - 96 : 32) >> 4;      // 16 features on; the second half's after four
+            ad += step;
+            bd += step;
           }
-          tmem_wait_st();
+          umma_commit(sdone(h, n));
+          bd = vd + ((s * kW8Tile + 4096 * p.c0) >> 4);
+          ok = mbar_wait_bounded(vfull(s), par) && mbar_wait_bounded(pfull(h), n & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 2
+          for (int kk = 2 * p.c0; kk < 2 * p.c1; kk++, bd += 2048 >> 4)
+            umma_f16_tmem_a(to, ts + 8 * kk, bd, id_pv, j > 0 || kk > 2 * p.c0);
+          umma_commit(pvdone(h, n));
         }
-        m = mn;
       }
-      const float mr = m == -INFINITY ? 0.0f : m;     // no visible key so far
-#pragma unroll
-      for (int q = 0; q < 4; q++) {
-        uint32_t ph[16];
-#pragma unroll
-        for (int e = 0; e < 16; e++) {
-          const float u = fast_exp2(fmaf(x[32 * q + 2 * e], kLogitScale, -mr));
-          const float v = fast_exp2(fmaf(x[32 * q + 2 * e + 1], kLogitScale, -mr));
-          l += u + v;
-          ph[e] = pack_elems<ELEM>(u, v);
-        }
-        tmem_st16(tl + b * 128 + 16 * q, ph);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(pfull(b));
+      if (!ok) fail();
+      umma_commit(drain(h));                   // every MMA issued so far has completed
+      mbar_wait_bounded(drain(h), 0);
     }
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(ofull, 0) && !failed());
-    if (ok) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kW8RegsMany));
+    // ---- softmax: a thread per row of a half ----
+    const int half = warp >= 8 ? 1 : 0, lg = warp & 3, row = 32 * lg + lane, token = row / G;
+    const uint32_t tl = tbase + ((uint32_t)(32 * lg) << 16);
+    const uint32_t ts = tl + half * 128, to = tl + kW8OCol + half * 128;
+    int n = 0;
+    bool ok = true;
+    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
+      const Item it = item_of(x, c, a, call);
+      const int q0 = it.p0 + half * a.tq, q1 = max(min(q0 + a.tq, it.n0) - 1, q0), pos = q0 + token;
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < it.count; j++, n++) {
+        const int kt = it.key(j);
+        const Parts p = parts_of(it, a, half, kt);
+        const bool inside = kt + 32 * p.c1 - 1 <= q0 &&
+                            (a.window <= 0 || kt + 32 * p.c0 > q1 - a.window || kt + 32 * p.c1 <= a.sinks);
+        // keys [lo, hi] of the window, or below the number of first tokens
+        const int hi = pos - kt, lo = a.window > 0 ? pos - a.window + 1 - kt : 0, early = a.window > 0 ? a.sinks - kt : 0;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(sdone(half, n), (n >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after();
+        if (kt + kW8T > it.n0) {
+          // V rows behind the request belong to others: zero them, whatever they
+          // hold (their weight is 0, but 0 * Inf is not). Both halves do, each
+          // ahead of its own product
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull(n & 1), (n >> 1) & 1));
+          if (!ok) break;
+          uint8_t* vs = smem + kW8OffV + (n & 1) * kW8Tile;
+          for (int y = row; y < 2 * (kt + kW8T - it.n0) * 8; y += 128) {
+            const int f = y & 1, r = it.n0 - kt + (y >> 4), o = (y >> 1) & 7;
+            *reinterpret_cast<uint4*>(vs + f * kW8Half + r * 128 + 16 * o) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+        }
+        auto hide = [&](float* s, int q) {
+          if (inside) return;
+          const uint32_t see = below(hi + 1 - 32 * q) & (~below(lo - 32 * q) | below(early - 32 * q));
+#pragma unroll
+          for (int e = 0; e < 32; e++) s[e] = see & (1u << e) ? s[e] : -INFINITY;
+        };
+        uint32_t ph[64];
+        float sum;
+        bool raise = __any_sync(0xffffffffu, m == -INFINITY);
+#pragma unroll 1
+        while (true) {
+          if (raise) {
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int q = p.c0; q < p.c1; q++) {
+              float s[32];
+              tmem_ld32_nowait(ts + 32 * q, s);
+              tmem_wait_ld();
+              loaded32(s);
+              hide(s, q);
+              float y[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+              for (int e = 4; e < 32; e++) y[e & 3] = fmaxf(y[e & 3], s[e]);
+              mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+            }
+            const float mn = fmaxf(m, mx * kLogitScale);
+            if (j > 0) {       // S of this step was issued after the last P V was done: O is still
+              const float f = mn == -INFINITY ? 1.0f : fast_exp2(m - mn);
+              l *= f;
+#pragma unroll 1
+              for (int q = 0; q < 4; q++) {
+                float o[32];
+                tmem_ld32_nowait(to + 32 * q, o);
+                tmem_wait_ld();
+                loaded32(o);
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; e++) w[e] = __float_as_uint(o[e] * f);
+                tmem_st32(to + 32 * q, w);
+              }
+              tmem_wait_st();
+            }
+            m = mn;
+          }
+          const float mr = m == -INFINITY ? 0.0f : m;     // no visible key so far
+          const uint64_t sc2 = f32x2(kLogitScale, kLogitScale), nm2 = f32x2(-mr, -mr);
+          uint64_t l2[4] = {0, 0, 0, 0};
+          // part q + 1 is on its way while part q is taken
+          float s[2][32];
+#pragma unroll
+          for (int q = 0; q < 4; q++)
+            if (q == p.c0) tmem_ld32_nowait(ts + 32 * q, s[q & 1]);
+#pragma unroll
+          for (int q = 0; q < 4; q++)
+            if (q >= p.c0 && q < p.c1) {
+              tmem_wait_ld();
+              loaded32(s[q & 1]);
+              if (q + 1 < p.c1) tmem_ld32_nowait(ts + 32 * q + 32, s[(q + 1) & 1]);
+              hide(s[q & 1], q);
+#pragma unroll
+              for (int e = 0; e < 16; e++) {
+                const uint64_t y = fma_f32x2(f32x2(s[q & 1][2 * e], s[q & 1][2 * e + 1]), sc2, nm2);
+                const float u = fast_exp2(__uint_as_float((uint32_t)y)), v = fast_exp2(__uint_as_float((uint32_t)(y >> 32)));
+                l2[e & 3] = add_f32x2(l2[e & 3], f32x2(u, v));
+                ph[16 * q + e] = pack_elems<ELEM>(u, v);
+              }
+            }
+          const uint64_t t2 = add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3]));
+          sum = __uint_as_float((uint32_t)t2) + __uint_as_float((uint32_t)(t2 >> 32));
+          if (raise || !__any_sync(0xffffffffu, !(sum <= kW8Most))) break;
+          raise = true;
+        }
+        l += sum;
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+          if (q >= p.c0 && q < p.c1) tmem_st16(ts + 16 * q, ph + 16 * q);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull(half));
+      }
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, n - 1), ((n - 1) >> 1) & 1));
+      if (!ok) break;
       tc_fence_after();
       const float inv = __fdiv_rn(1.0f, l);
-      uint8_t* dst = a.out + (((size_t)(t0 + pos) * c.hkv + h) * G + row % G) * (2 * kD);
+      const bool real = token < a.tq && pos < it.n0;
+      uint8_t* dst = a.out + (((size_t)(it.t0 + pos) * c.hkv + it.h) * G + row % G) * (2 * kD);
 #pragma unroll 1
       for (int q = 0; q < 4; q++) {
         float o[32];
-        tmem_ld32_nowait(tl + kW8OCol + 32 * q, o);
+        tmem_ld32_nowait(to + 32 * q, o);
         tmem_wait_ld();
+        loaded32(o);
         if (real) {
           uint4* d4 = reinterpret_cast<uint4*>(dst + 64 * q);
 #pragma unroll
@@ -297,7 +395,9 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                                pack_elems<ELEM>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
         }
       }
+      tc_fence_before();
     }
+    if (!ok) fail();
   }
   tc_fence_before();
   __syncthreads();
@@ -327,7 +427,7 @@ cudaError_t rows_map(PFN_cuTensorMapEncodeTiled_v12000 enc, int elem, const void
 
 cudaError_t launch_prefill8(const Cache8View& c, int elem, const int32_t* seq_lens, int n_req, const void* q,
                             long long qs, const void* k, long long ks, const void* v, long long vs, void* out,
-                            int window, int sinks, cudaStream_t st) {
+                            int window, int sinks, int sm_count, cudaStream_t st) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   cudaError_t e = tma_encoder(&enc);
   if (e != cudaSuccess) return e;
@@ -337,7 +437,7 @@ cudaError_t launch_prefill8(const Cache8View& c, int elem, const int32_t* seq_le
   const int tq = kW8T / c.G;
   for (int i = 0; i < n_req; i++) {
     call.tok0[i + 1] = call.tok0[i] + seq_lens[i];
-    call.tile0[i + 1] = call.tile0[i] + (seq_lens[i] + tq - 1) / tq;
+    call.tile0[i + 1] = call.tile0[i] + (seq_lens[i] + 2 * tq - 1) / (2 * tq);
   }
   const long long n = call.tok0[n_req];
   CUtensorMap mq, mk, mv;
@@ -347,7 +447,8 @@ cudaError_t launch_prefill8(const Cache8View& c, int elem, const int32_t* seq_le
   auto kernel = elem == DKV_F16 ? k_prefill8<DKV_F16> : k_prefill8<DKV_BF16>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kernel, dim3((unsigned)call.tile0[n_req] * c.hkv), dim3(kW8Threads), kW8Smem, st, c, mq, mk,
+  const int grid = std::min(call.tile0[n_req] * c.hkv, sm_count);
+  return launch_dependent(kernel, dim3(grid), dim3(kW8Threads), kW8Smem, st, c, mq, mk,
                           mv, W8Args{static_cast<uint8_t*>(out), window, sinks, tq}, call);
 }
 
