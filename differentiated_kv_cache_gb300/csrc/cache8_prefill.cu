@@ -9,15 +9,17 @@
 // an SM; warp 0 issues the TMA copies (an item's queries, 128-key K and V tiles
 // through two stages each), warps 1 and 2 the MMAs of a half each, warps 4..7 and 8..11 run the softmax
 // of the halves with one thread per row (and most of the registers):
-//   S = Q K^T        tcgen05, D in tensor memory
+//   S = Q K^T        tcgen05, D in tensor memory, 64 keys a step, two buffers
 //   P = 2^(S - m)    written over S in 16 bits; m is a maximum of earlier keys,
-//                    raised (O, l rescaled) only when a row's P of a tile sum
-//                    to over 2^12, so that most tiles need no maximum at all
+//                    raised (O, l rescaled) only when a row's P of a step sum
+//                    to over 2^12, so that most steps need no maximum at all
 //   O += P V         tcgen05, A = P from tensor memory, V MN-major
-// The halves do not wait for one another, so one half's products run while the
-// other half's softmax does, and the next item's first products while this
-// item's results are written. (Tensor memory is full with two S and two O, so P
-// lies over S, and the next S of a half is issued once its P V is done.)
+// S of step n + 2 is issued once P V of step n is done, while the softmax takes
+// step n + 1, and the halves do not wait for one another: products run while
+// either half's softmax does, and the next item's first products while this
+// item's results are written. (Tensor memory holds two S of 64 columns and an O
+// of 128 for each half; with one S of 128 columns a half, each softmax waited
+// for P V and the next S in turn: 4900 cycles for 128 keys instead of XXXX.)
 // Only key tiles with a visible key are visited, the window's from the diagonal
 // back (the nearest keys give a good first m), then the first tokens'; of each,
 // a half takes the 32-key parts that some of its rows may see. Every wait is bounded; on expiry
@@ -44,7 +46,8 @@ constexpr int kW8Half = kW8T * 128;        // 64 features of 128 rows: 16 KB
 constexpr int kW8Tile = 2 * kW8Half;
 constexpr int kW8OffK = 2 * kW8Tile;       // after the queries of both halves
 constexpr int kW8OffV = kW8OffK + 2 * kW8Tile;
-constexpr int kW8OffBar = kW8OffV + 2 * kW8Tile;
+constexpr int kW8OffOut = kW8OffV + 2 * kW8Tile;      // 4 KB a softmax warp, to write whole lines
+constexpr int kW8OffBar = kW8OffOut + 8 * 4096;
 constexpr int kW8Smem = 1024 + kW8OffBar + 256;
 constexpr uint32_t kW8OCol = 256;          // S of the halves, then O of the halves
 constexpr uint32_t kW8Cols = 512;
@@ -92,16 +95,16 @@ __device__ __forceinline__ Item item_of(int x, const Cache8View& c, const W8Args
   return it;
 }
 
-// The 32-key parts [c0, c1) of the tile at key kt that a half's rows may see
+// The 32-key parts [c0, c1) of the 64 keys from kt that a half's rows may see
 // (one at least).
 struct Parts {
   int c0, c1;
 };
 __device__ __forceinline__ Parts parts_of(const Item& it, const W8Args& a, int half, int kt) {
   const int q0 = it.p0 + half * a.tq, q1 = max(min(q0 + a.tq, it.n0) - 1, q0);
-  const int hi = min(q1 - kt, kW8T - 1), lo = a.window > 0 ? max(q0 - a.window + 1 - kt, 0) : 0;
-  const int early = a.window > 0 ? min(a.sinks - kt, kW8T) : 0;
-  Parts p{4, 0};
+  const int hi = min(q1 - kt, 63), lo = a.window > 0 ? max(q0 - a.window + 1 - kt, 0) : 0;
+  const int early = a.window > 0 ? min(a.sinks - kt, 64) : 0;
+  Parts p{2, 0};
   if (lo <= hi) p = Parts{lo >> 5, (hi >> 5) + 1};
   if (early > 0) p = Parts{0, max(p.c1, (early + 31) >> 5)};
   if (p.c1 <= p.c0) p = Parts{0, 1};
@@ -139,23 +142,24 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kW8OffBar);
   const uint32_t b0 = smem_u32(bars);
-  // A commit of MMAs costs the issuing thread hundreds of cycles: one a
-  // product. S and P V of step n (= tile n of the CTA's sequence) signal sdone
-  // and pvdone of (half, n & 1); a K (V) stage is free when both halves' S (P V)
-  // of its tile are done, the queries when both halves' last S of an item are.
+  // S and P V of step n (64 keys, tile n / 2 of the CTA's sequence) signal sdone
+  // and pvdone of (half, n & 3); a K (V) stage is free when both halves' S (P V)
+  // of its tile's second step are done, the queries when both halves' last S of
+  // an item are. (Four of each: a barrier cannot run on by two phases before
+  // everyone has seen the first.)
   const uint32_t qfull = b0;
   auto kfull = [&](int s) { return b0 + 16u + 8u * s; };
   auto vfull = [&](int s) { return b0 + 32u + 8u * s; };
-  auto pfull = [&](int h) { return b0 + 48u + 8u * h; };
-  auto sdone = [&](int h, int n) { return b0 + 64u + 16u * h + 8u * (n & 1); };
-  auto pvdone = [&](int h, int n) { return b0 + 96u + 16u * h + 8u * (n & 1); };
-  auto drain = [&](int h) { return b0 + 128u + 8u * h; };
-  uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 18);
+  auto pfull = [&](int h, int n) { return b0 + 48u + 16u * h + 8u * (n & 1); };
+  auto sdone = [&](int h, int n) { return b0 + 80u + 32u * h + 8u * (n & 3); };
+  auto pvdone = [&](int h, int n) { return b0 + 144u + 32u * h + 8u * (n & 3); };
+  auto drain = [&](int h) { return b0 + 208u + 8u * h; };
+  uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 28);
   int* s_fail = reinterpret_cast<int*>(s_taddr + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 18; s++) mbar_init(b0 + 8u * s, 1);
-    for (int h = 0; h < 2; h++) mbar_init(pfull(h), 4);        // a lane of each warp
+    for (int s = 0; s < 28; s++)      // pfull: a lane of each warp
+      mbar_init(b0 + 8u * s, s >= 6 && s < 10 ? 4 : 1);
     *s_fail = 0;
     fence_mbar_init();
   }
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         const uint32_t full = is_k ? kfull(s) : vfull(s);
         if (t >= 2)          // tile t - 2 of the stage is done with
           for (int h = 0; h < 2; h++)
-            if (!mbar_wait_bounded(is_k ? sdone(h, t) : pvdone(h, t), ((t >> 1) - 1) & 1)) return false;
+            if (!mbar_wait_bounded(is_k ? sdone(h, 2 * t + 1) : pvdone(h, 2 * t + 1), ((t >> 1) - 1) & 1)) return false;
         mbar_expect_tx(full, kW8Tile);
         for (int f = 0; f < 2; f++)
           tma_load_3d(smem_u32(smem + (is_k ? kW8OffK : kW8OffV) + s * kW8Tile + f * kW8Half), is_k ? &tk : &tv,
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         const int t = nk - 1;          // the last tile of the item before
         ok = load(it, 0, true);
         if (nq > 0)
-          for (int h = 0; h < 2; h++) ok = ok && mbar_wait_bounded(sdone(h, t), (t >> 1) & 1);
+          for (int h = 0; h < 2; h++) ok = ok && mbar_wait_bounded(sdone(h, 2 * t + 1), (t >> 1) & 1);
         if (!ok) break;
         mbar_expect_tx(qfull, (uint32_t)(4 * 128 * a.tq * G));
         for (int f = 0; f < 4; f++)
@@ -221,35 +225,47 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       const uint32_t ts = tbase + h * 128, to = tbase + kW8OCol + h * 128;
       const uint64_t qd = umma_desc_sw128(smem_u32(smem + h * kW8Tile));
       const uint64_t kd = umma_desc_sw128(smem_u32(smem + kW8OffK)), vd = umma_desc_sw128_mn(smem_u32(smem + kW8OffV), kW8Half);
-      int n = 0, ii = 0;
+      Item it{};
+      int n = 0, ii = 0;                       // steps and items so far
+      // S of step n + d, the item's step j; false: given up
+      auto issue_s = [&](int d, int j) {
+        const Parts p = parts_of(it, a, h, it.key(j >> 1) + 64 * (j & 1));
+        const int sn = n + d, st = (sn >> 1) & 1;
+        const uint32_t id = umma_idesc_f16(128, 32 * (p.c1 - p.c0)) | type;
+        uint64_t ad = qd, bd = kd + ((st * kW8Tile + (sn & 1) * 8192 + 4096 * p.c0) >> 4);
+        if (!mbar_wait_bounded(kfull(st), (sn >> 2) & 1)) return false;
+        if (sn >= 2 && !mbar_wait_bounded(pvdone(h, sn - 2), ((sn - 2) >> 2) & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+          umma_f16(ts + 64 * (sn & 1) + 32 * p.c0, ad, bd, id, k > 0);
+          const int step = (k == 3 ? kW8Half - 96 : 32) >> 4;      // 16 features on; the second half's after four
+          ad += step;
+          bd += step;
+        }
+        umma_commit(sdone(h, sn));
+        return true;
+      };
       bool ok = true;
       for (int x = blockIdx.x; ok && x < items; x += gridDim.x, ii++) {
-        const Item it = item_of(x, c, a, call);
+        it = item_of(x, c, a, call);
         ok = mbar_wait_bounded(qfull, ii & 1);
-        for (int j = 0; ok && j < it.count; j++, n++) {
-          const Parts p = parts_of(it, a, h, it.key(j));
-          const int s = n & 1, par = (n >> 1) & 1;
-          const uint32_t id = umma_idesc_f16(128, 32 * (p.c1 - p.c0)) | type;
-          uint64_t ad = qd, bd = kd + ((s * kW8Tile + 4096 * p.c0) >> 4);
-          ok = mbar_wait_bounded(kfull(s), par) && (n == 0 || mbar_wait_bounded(pvdone(h, n - 1), ((n - 1) >> 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < 8; k++) {
-            umma_f16(ts + 32 * p.c0, ad, bd, id, k > 0);
-            const int step = (k == 3 ? kW8Half - 96 : 32) >> 4;      // 16 features on; the second half's after four
-            ad += step;
-            bd += step;
-          }
-          umma_commit(sdone(h, n));
-          bd = vd + ((s * kW8Tile + 4096 * p.c0) >> 4);
-          ok = mbar_wait_bounded(vfull(s), par) && mbar_wait_bounded(pfull(h), n & 1);
-          if (!ok) break;
-          tc_fence_after();
+        // (one call site: S runs two steps ahead)
+        for (int j = -2; ok && j < 2 * it.count; j++) {
+          if (j >= 0) {
+            const Parts p = parts_of(it, a, h, it.key(j >> 1) + 64 * (j & 1));
+            const int st = (n >> 1) & 1;
+            uint64_t bd = vd + ((st * kW8Tile + (n & 1) * 8192 + 4096 * p.c0) >> 4);
+            ok = mbar_wait_bounded(vfull(st), (n >> 2) & 1) && mbar_wait_bounded(pfull(h, n), (n >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 2
-          for (int kk = 2 * p.c0; kk < 2 * p.c1; kk++, bd += 2048 >> 4)
-            umma_f16_tmem_a(to, ts + 8 * kk, bd, id_pv, j > 0 || kk > 2 * p.c0);
-          umma_commit(pvdone(h, n));
+            for (int kk = 2 * p.c0; kk < 2 * p.c1; kk++, bd += 2048 >> 4)
+              umma_f16_tmem_a(to, ts + 64 * (n & 1) + 8 * kk, bd, id_pv, j > 0 || kk > 2 * p.c0);
+            umma_commit(pvdone(h, n));
+          }
+          if (j + 2 < 2 * it.count) ok = issue_s(j < 0 ? j + 2 : 2, j + 2);
+          if (j >= 0) n++;
         }
       }
       if (!ok) fail();
@@ -269,25 +285,28 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       const Item it = item_of(x, c, a, call);
       const int q0 = it.p0 + half * a.tq, q1 = max(min(q0 + a.tq, it.n0) - 1, q0), pos = q0 + token;
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < it.count; j++, n++) {
-        const int kt = it.key(j);
+      for (int j = 0; j < 2 * it.count; j++, n++) {
+        const int kt = it.key(j >> 1) + 64 * (j & 1);
         const Parts p = parts_of(it, a, half, kt);
+        const uint32_t tb = ts + 64 * (n & 1);
         const bool inside = kt + 32 * p.c1 - 1 <= q0 &&
                             (a.window <= 0 || kt + 32 * p.c0 > q1 - a.window || kt + 32 * p.c1 <= a.sinks);
         // keys [lo, hi] of the window, or below the number of first tokens
         const int hi = pos - kt, lo = a.window > 0 ? pos - a.window + 1 - kt : 0, early = a.window > 0 ? a.sinks - kt : 0;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(sdone(half, n), (n >> 1) & 1));
+        bool raise = __any_sync(0xffffffffu, m == -INFINITY);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(sdone(half, n), (n >> 2) & 1));
         if (!ok) break;
         tc_fence_after();
-        if (kt + kW8T > it.n0) {
+        if (kt + 64 > it.n0) {
           // V rows behind the request belong to others: zero them, whatever they
           // hold (their weight is 0, but 0 * Inf is not). Both halves do, each
           // ahead of its own product
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull(n & 1), (n >> 1) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull((n >> 1) & 1), (n >> 2) & 1));
           if (!ok) break;
-          uint8_t* vs = smem + kW8OffV + (n & 1) * kW8Tile;
-          for (int y = row; y < 2 * (kt + kW8T - it.n0) * 8; y += 128) {
-            const int f = y & 1, r = it.n0 - kt + (y >> 4), o = (y >> 1) & 7;
+          const int first = max(it.n0 - kt, 0);
+          uint8_t* vs = smem + kW8OffV + ((n >> 1) & 1) * kW8Tile + (n & 1) * 8192;
+          for (int y = row; y < 2 * (64 - first) * 8; y += 128) {
+            const int f = y & 1, r = first + (y >> 4), o = (y >> 1) & 7;
             *reinterpret_cast<uint4*>(vs + f * kW8Half + r * 128 + 16 * o) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
@@ -298,9 +317,8 @@ __global__ void __launch_bounds__(kW8Threads, 1)
 #pragma unroll
           for (int e = 0; e < 32; e++) s[e] = see & (1u << e) ? s[e] : -INFINITY;
         };
-        uint32_t ph[64];
+        uint32_t ph[32];
         float sum;
-        bool raise = __any_sync(0xffffffffu, m == -INFINITY);
 #pragma unroll 1
         while (true) {
           if (raise) {
@@ -308,7 +326,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
 #pragma unroll 1
             for (int q = p.c0; q < p.c1; q++) {
               float s[32];
-              tmem_ld32_nowait(ts + 32 * q, s);
+              tmem_ld32_nowait(tb + 32 * q, s);
               tmem_wait_ld();
               loaded32(s);
               hide(s, q);
@@ -318,7 +336,10 @@ __global__ void __launch_bounds__(kW8Threads, 1)
               mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
             }
             const float mn = fmaxf(m, mx * kLogitScale);
-            if (j > 0) {       // S of this step was issued after the last P V was done: O is still
+            if (j > 0) {       // O is still once the last P V is done
+              ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, n - 1), ((n - 1) >> 2) & 1));
+              if (!ok) break;
+              tc_fence_after();
               const float f = mn == -INFINITY ? 1.0f : fast_exp2(m - mn);
               l *= f;
 #pragma unroll 1
@@ -339,21 +360,19 @@ __global__ void __launch_bounds__(kW8Threads, 1)
           const float mr = m == -INFINITY ? 0.0f : m;     // no visible key so far
           const uint64_t sc2 = f32x2(kLogitScale, kLogitScale), nm2 = f32x2(-mr, -mr);
           uint64_t l2[4] = {0, 0, 0, 0};
-          // part q + 1 is on its way while part q is taken
           float s[2][32];
 #pragma unroll
-          for (int q = 0; q < 4; q++)
-            if (q == p.c0) tmem_ld32_nowait(ts + 32 * q, s[q & 1]);
+          for (int q = 0; q < 2; q++)
+            if (q >= p.c0 && q < p.c1) tmem_ld32_nowait(tb + 32 * q, s[q]);
+          tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < 4; q++)
+          for (int q = 0; q < 2; q++)
             if (q >= p.c0 && q < p.c1) {
-              tmem_wait_ld();
-              loaded32(s[q & 1]);
-              if (q + 1 < p.c1) tmem_ld32_nowait(ts + 32 * q + 32, s[(q + 1) & 1]);
-              hide(s[q & 1], q);
+              loaded32(s[q]);
+              hide(s[q], q);
 #pragma unroll
               for (int e = 0; e < 16; e++) {
-                const uint64_t y = fma_f32x2(f32x2(s[q & 1][2 * e], s[q & 1][2 * e + 1]), sc2, nm2);
+                const uint64_t y = fma_f32x2(f32x2(s[q][2 * e], s[q][2 * e + 1]), sc2, nm2);
                 const float u = fast_exp2(__uint_as_float((uint32_t)y)), v = fast_exp2(__uint_as_float((uint32_t)(y >> 32)));
                 l2[e & 3] = add_f32x2(l2[e & 3], f32x2(u, v));
                 ph[16 * q + e] = pack_elems<ELEM>(u, v);
@@ -364,36 +383,50 @@ __global__ void __launch_bounds__(kW8Threads, 1)
           if (raise || !__any_sync(0xffffffffu, !(sum <= kW8Most))) break;
           raise = true;
         }
+        if (!ok) break;
         l += sum;
 #pragma unroll
-        for (int q = 0; q < 4; q++)
-          if (q >= p.c0 && q < p.c1) tmem_st16(ts + 16 * q, ph + 16 * q);
+        for (int q = 0; q < 2; q++)
+          if (q >= p.c0 && q < p.c1) tmem_st16(tb + 16 * q, ph + 16 * q);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull(half));
+        if (lane == 0) mbar_arrive(pfull(half, n));
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, n - 1), ((n - 1) >> 1) & 1));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, n - 1), ((n - 1) >> 2) & 1));
       if (!ok) break;
       tc_fence_after();
       const float inv = __fdiv_rn(1.0f, l);
       const bool real = token < a.tq && pos < it.n0;
-      uint8_t* dst = a.out + (((size_t)(it.t0 + pos) * c.hkv + it.h) * G + row % G) * (2 * kD);
+      // through shared memory, 64 features at a time: eight lanes write a line
+      const unsigned long long dst = real ? reinterpret_cast<unsigned long long>(a.out) +
+          (((size_t)(it.t0 + pos) * c.hkv + it.h) * G + row % G) * (2 * kD) : 0ull;
+      uint8_t* stage = smem + kW8OffOut + (warp - 4) * 4096;
 #pragma unroll 1
-      for (int q = 0; q < 4; q++) {
-        float o[32];
-        tmem_ld32_nowait(to + 32 * q, o);
-        tmem_wait_ld();
-        loaded32(o);
-        if (real) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + 64 * q);
+      for (int q = 0; q < 2; q++) {
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          float o[32];
+          tmem_ld32_nowait(to + 64 * q + 32 * r, o);
+          tmem_wait_ld();
+          loaded32(o);
 #pragma unroll
           for (int e = 0; e < 4; e++)
-            d4[e] = make_uint4(pack_elems<ELEM>(o[8 * e] * inv, o[8 * e + 1] * inv),
-                               pack_elems<ELEM>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                               pack_elems<ELEM>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                               pack_elems<ELEM>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * r + e) ^ (lane & 7)) << 4)) =
+                make_uint4(pack_elems<ELEM>(o[8 * e] * inv, o[8 * e + 1] * inv),
+                           pack_elems<ELEM>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                           pack_elems<ELEM>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                           pack_elems<ELEM>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
         }
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const int r = 4 * e + (lane >> 3);
+          const unsigned long long to_row = __shfl_sync(0xffffffffu, dst, r);
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (to_row) *reinterpret_cast<uint4*>(to_row + 128 * q + 16 * (lane & 7)) = w;
+        }
+        __syncwarp();
       }
       tc_fence_before();
     }
