@@ -70,7 +70,10 @@ struct W8Args {
 // `count` in all.
 struct Item {
   int h, t0, n0, p0, last, near, count;
+  int lo, hi, early;   // keys that some row sees: [lo, hi], and below early
   __device__ __forceinline__ int key(int j) const { return (j < near ? last - j : j - near) * kW8T; }
+  // 64 keys from kt; every tile of an item has such a step
+  __device__ __forceinline__ bool step(int kt) const { return (kt <= hi && kt + 63 >= lo) || kt < early; }
 };
 __device__ __forceinline__ Item item_of(int x, const Cache8View& c, const W8Args& a, const W8Call& call) {
   Item it;
@@ -84,16 +87,38 @@ __device__ __forceinline__ Item item_of(int x, const Cache8View& c, const W8Args
   it.t0 = call.tok0[i];
   it.n0 = call.tok0[i + 1] - it.t0;
   it.p0 = (qtile - call.tile0[i]) * 2 * a.tq;
-  it.last = (min(it.p0 + 2 * a.tq, it.n0) - 1) / kW8T;
-  int from = 0, first = 0;
-  if (a.window > 0) {
-    from = max(it.p0 - a.window + 1, 0) / kW8T;
-    first = min((min(a.sinks, it.n0) + kW8T - 1) / kW8T, from);
-  }
+  it.hi = min(it.p0 + 2 * a.tq, it.n0) - 1;
+  it.last = it.hi / kW8T;
+  it.lo = a.window > 0 ? max(it.p0 - a.window + 1, 0) : 0;
+  it.early = a.window > 0 ? min(a.sinks, it.n0) : 0;
+  const int from = it.lo / kW8T, first = min((it.early + kW8T - 1) / kW8T, from);
   it.near = it.last - from + 1;
   it.count = it.near + first;
   return it;
 }
+
+// The steps of an item in order: its tiles, and in each the 64-key halves that
+// some row sees. n: steps, t: tiles of the CTA's sequence so far.
+struct Cursor {
+  int j, u, n, t;
+  __device__ __forceinline__ int key(const Item& it) const { return it.key(j) + 64 * u; }
+  __device__ __forceinline__ void begin(const Item& it) {
+    j = 0;
+    u = it.step(it.key(0)) ? 0 : 1;
+  }
+  // to the next step; false (with the tile counted): the item's last one it was
+  __device__ __forceinline__ bool next(const Item& it) {
+    n++;
+    if (u == 0 && it.step(it.key(j) + 64)) {
+      u = 1;
+      return true;
+    }
+    t++;
+    if (++j == it.count) return false;
+    u = it.step(it.key(j)) ? 0 : 1;
+    return true;
+  }
+};
 
 // The 32-key parts [c0, c1) of the 64 keys from kt that a half's rows may see
 // (one at least).
@@ -142,11 +167,11 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kW8OffBar);
   const uint32_t b0 = smem_u32(bars);
-  // S and P V of step n (64 keys, tile n / 2 of the CTA's sequence) signal sdone
-  // and pvdone of (half, n & 3); a K (V) stage is free when both halves' S (P V)
-  // of its tile's second step are done, the queries when both halves' last S of
-  // an item are. (Four of each: a barrier cannot run on by two phases before
-  // everyone has seen the first.)
+  // S and P V of step n (64 keys) signal sdone and pvdone of (half, n & 3); a K
+  // (V) stage is free when both halves' S (P V) of its tile's last step are done,
+  // the queries when both halves' last S of an item are. (Four of each: step
+  // n + 4 needs a tile or queries that are not loaded before everyone has seen
+  // step n's phase.)
   const uint32_t qfull = b0;
   auto kfull = [&](int s) { return b0 + 16u + 8u * s; };
   auto vfull = [&](int s) { return b0 + 32u + 8u * s; };
@@ -180,26 +205,37 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     // ---- copies: an item's first K tile, its queries, then K(j + 1) ahead of V(j) ----
     if (lane == 0) {
       int nk = 0, nv = 0, nq = 0;      // K tiles, V tiles and items so far
+      int done = 0;                    // steps of the tiles whose K is loaded
+      int end[2] = {0, 0};             // last step of the latest tile of each stage
+      int vend[2] = {0, 0};
       bool ok = true;
       auto load = [&](const Item& it, int j, bool is_k) {
         const int t = is_k ? nk : nv, s = t & 1;
         const uint32_t full = is_k ? kfull(s) : vfull(s);
+        const int e = is_k ? end[s] : vend[s];
         if (t >= 2)          // tile t - 2 of the stage is done with
           for (int h = 0; h < 2; h++)
-            if (!mbar_wait_bounded(is_k ? sdone(h, 2 * t + 1) : pvdone(h, 2 * t + 1), ((t >> 1) - 1) & 1)) return false;
+            if (!mbar_wait_bounded(is_k ? sdone(h, e) : pvdone(h, e), (e >> 2) & 1)) return false;
         mbar_expect_tx(full, kW8Tile);
         for (int f = 0; f < 2; f++)
           tma_load_3d(smem_u32(smem + (is_k ? kW8OffK : kW8OffV) + s * kW8Tile + f * kW8Half), is_k ? &tk : &tv,
                       64 * f, it.h, it.t0 + it.key(j), full);
-        (is_k ? nk : nv)++;
+        if (is_k) {
+          nk++;
+          done += (it.step(it.key(j)) ? 1 : 0) + (it.step(it.key(j) + 64) ? 1 : 0);
+          end[s] = done - 1;
+        } else {
+          nv++;
+          vend[s] = end[s];            // K of the tile after next is not loaded yet
+        }
         return true;
       };
       for (int x = blockIdx.x; ok && x < items && !failed(); x += gridDim.x) {
         const Item it = item_of(x, c, a, call);
-        const int t = nk - 1;          // the last tile of the item before
+        const int last = done - 1;     // the last step of the item before
         ok = load(it, 0, true);
         if (nq > 0)
-          for (int h = 0; h < 2; h++) ok = ok && mbar_wait_bounded(sdone(h, 2 * t + 1), (t >> 1) & 1);
+          for (int h = 0; h < 2; h++) ok = ok && mbar_wait_bounded(sdone(h, last), (last >> 2) & 1);
         if (!ok) break;
         mbar_expect_tx(qfull, (uint32_t)(4 * 128 * a.tq * G));
         for (int f = 0; f < 4; f++)
@@ -225,47 +261,49 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       const uint32_t ts = tbase + h * 128, to = tbase + kW8OCol + h * 128;
       const uint64_t qd = umma_desc_sw128(smem_u32(smem + h * kW8Tile));
       const uint64_t kd = umma_desc_sw128(smem_u32(smem + kW8OffK)), vd = umma_desc_sw128_mn(smem_u32(smem + kW8OffV), kW8Half);
-      Item it{};
-      int n = 0, ii = 0;                       // steps and items so far
-      // S of step n + d, the item's step j; false: given up
-      auto issue_s = [&](int d, int j) {
-        const Parts p = parts_of(it, a, h, it.key(j >> 1) + 64 * (j & 1));
-        const int sn = n + d, st = (sn >> 1) & 1;
-        const uint32_t id = umma_idesc_f16(128, 32 * (p.c1 - p.c0)) | type;
-        uint64_t ad = qd, bd = kd + ((st * kW8Tile + (sn & 1) * 8192 + 4096 * p.c0) >> 4);
-        if (!mbar_wait_bounded(kfull(st), (sn >> 2) & 1)) return false;
-        if (sn >= 2 && !mbar_wait_bounded(pvdone(h, sn - 2), ((sn - 2) >> 2) & 1)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-          umma_f16(ts + 64 * (sn & 1) + 32 * p.c0, ad, bd, id, k > 0);
-          const int step = (k == 3 ? kW8Half - 96 : 32) >> 4;      // 16 features on; the second half's after four
-          ad += step;
-          bd += step;
-        }
-        umma_commit(sdone(h, sn));
-        return true;
-      };
+      Cursor sc{0, 0, 0, 0}, pc{0, 0, 0, 0};     // steps of S and, two behind, of P V
+      int ii = 0;
       bool ok = true;
       for (int x = blockIdx.x; ok && x < items; x += gridDim.x, ii++) {
-        it = item_of(x, c, a, call);
+        const Item it = item_of(x, c, a, call);
+        sc.begin(it);
+        pc.begin(it);
+        bool more_s = true, more_p = true;
         ok = mbar_wait_bounded(qfull, ii & 1);
-        // (one call site: S runs two steps ahead)
-        for (int j = -2; ok && j < 2 * it.count; j++) {
-          if (j >= 0) {
-            const Parts p = parts_of(it, a, h, it.key(j >> 1) + 64 * (j & 1));
-            const int st = (n >> 1) & 1;
-            uint64_t bd = vd + ((st * kW8Tile + (n & 1) * 8192 + 4096 * p.c0) >> 4);
-            ok = mbar_wait_bounded(vfull(st), (n >> 2) & 1) && mbar_wait_bounded(pfull(h, n), (n >> 1) & 1);
+        for (int ahead = 0; ok && more_p; ahead++) {
+          if (ahead >= 2) {
+            const Parts p = parts_of(it, a, h, pc.key(it));
+            const int st = pc.t & 1, n = pc.n;
+            const bool first = pc.j == 0 && ahead == 2;
+            uint64_t bd = vd + ((st * kW8Tile + pc.u * 8192 + 4096 * p.c0) >> 4);
+            ok = mbar_wait_bounded(vfull(st), (pc.t >> 1) & 1) && mbar_wait_bounded(pfull(h, n), (n >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 2
             for (int kk = 2 * p.c0; kk < 2 * p.c1; kk++, bd += 2048 >> 4)
-              umma_f16_tmem_a(to, ts + 64 * (n & 1) + 8 * kk, bd, id_pv, j > 0 || kk > 2 * p.c0);
+              umma_f16_tmem_a(to, ts + 64 * (n & 1) + 8 * kk, bd, id_pv, !first || kk > 2 * p.c0);
             umma_commit(pvdone(h, n));
+            more_p = pc.next(it);
           }
-          if (j + 2 < 2 * it.count) ok = issue_s(j < 0 ? j + 2 : 2, j + 2);
-          if (j >= 0) n++;
+          if (more_s) {
+            const Parts p = parts_of(it, a, h, sc.key(it));
+            const int st = sc.t & 1, n = sc.n;
+            const uint32_t id = umma_idesc_f16(128, 32 * (p.c1 - p.c0)) | type;
+            uint64_t ad = qd, bd = kd + ((st * kW8Tile + sc.u * 8192 + 4096 * p.c0) >> 4);
+            ok = mbar_wait_bounded(kfull(st), (sc.t >> 1) & 1) &&
+                 (n < 2 || mbar_wait_bounded(pvdone(h, n - 2), ((n - 2) >> 2) & 1));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+              umma_f16(ts + 64 * (n & 1) + 32 * p.c0, ad, bd, id, k > 0);
+              const int step = (k == 3 ? kW8Half - 96 : 32) >> 4;      // 16 features on; the second half's after four
+              ad += step;
+              bd += step;
+            }
+            umma_commit(sdone(h, n));
+            more_s = sc.next(it);
+          }
         }
       }
       if (!ok) fail();
@@ -279,14 +317,16 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     const int half = warp >= 8 ? 1 : 0, lg = warp & 3, row = 32 * lg + lane, token = row / G;
     const uint32_t tl = tbase + ((uint32_t)(32 * lg) << 16);
     const uint32_t ts = tl + half * 128, to = tl + kW8OCol + half * 128;
-    int n = 0;
+    Cursor cu{0, 0, 0, 0};
     bool ok = true;
     for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
       const Item it = item_of(x, c, a, call);
       const int q0 = it.p0 + half * a.tq, q1 = max(min(q0 + a.tq, it.n0) - 1, q0), pos = q0 + token;
       float m = -INFINITY, l = 0.0f;
-      for (int j = 0; j < 2 * it.count; j++, n++) {
-        const int kt = it.key(j >> 1) + 64 * (j & 1);
+      cu.begin(it);
+      bool first = true, more = true;
+      for (; more; first = false) {
+        const int kt = cu.key(it), n = cu.n;
         const Parts p = parts_of(it, a, half, kt);
         const uint32_t tb = ts + 64 * (n & 1);
         const bool inside = kt + 32 * p.c1 - 1 <= q0 &&
@@ -301,12 +341,12 @@ __global__ void __launch_bounds__(kW8Threads, 1)
           // V rows behind the request belong to others: zero them, whatever they
           // hold (their weight is 0, but 0 * Inf is not). Both halves do, each
           // ahead of its own product
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull((n >> 1) & 1), (n >> 2) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull(cu.t & 1), (cu.t >> 1) & 1));
           if (!ok) break;
-          const int first = max(it.n0 - kt, 0);
-          uint8_t* vs = smem + kW8OffV + ((n >> 1) & 1) * kW8Tile + (n & 1) * 8192;
-          for (int y = row; y < 2 * (64 - first) * 8; y += 128) {
-            const int f = y & 1, r = first + (y >> 4), o = (y >> 1) & 7;
+          const int own = max(it.n0 - kt, 0);
+          uint8_t* vs = smem + kW8OffV + (cu.t & 1) * kW8Tile + cu.u * 8192;
+          for (int y = row; y < 2 * (64 - own) * 8; y += 128) {
+            const int f = y & 1, r = own + (y >> 4), o = (y >> 1) & 7;
             *reinterpret_cast<uint4*>(vs + f * kW8Half + r * 128 + 16 * o) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
@@ -336,7 +376,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
               mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
             }
             const float mn = fmaxf(m, mx * kLogitScale);
-            if (j > 0) {       // O is still once the last P V is done
+            if (!first) {      // O is still once the last P V is done
               ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, n - 1), ((n - 1) >> 2) & 1));
               if (!ok) break;
               tc_fence_after();
@@ -392,8 +432,9 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull(half, n));
+        more = cu.next(it);
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, n - 1), ((n - 1) >> 2) & 1));
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, cu.n - 1), ((cu.n - 1) >> 2) & 1));
       if (!ok) break;
       tc_fence_after();
       const float inv = __fdiv_rn(1.0f, l);
