@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   auto drain = [&](int h) { return b0 + 208u + 8u * h; };
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 28);
   int* s_fail = reinterpret_cast<int*>(s_taddr + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (broadcasts: uniform over a warp for the compiler too)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 28; s++)      // pfull: a lane of each warp
       mbar_init(b0 + 8u * s, s >= 6 && s < 10 ? 4 : 1);
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *s_taddr;
+  const uint32_t tbase = __shfl_sync(0xffffffffu, *s_taddr, 0);
   auto fail = [&]() {
     c.latch(DKV_ERR_TIMEOUT, -1);
     *(volatile int*)s_fail = 1;
@@ -254,7 +255,9 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     }
   } else if (warp < 3) {
     // ---- MMAs of a half: S of step n once P V of step n - 1 is done, then P V ----
-    if (lane == 0) {
+    // The whole warp walks the steps, one lane issues: operands stay in uniform
+    // registers (with one lane in the loop an MMA took 100 cycles to issue).
+    {
       constexpr uint32_t type = ELEM == DKV_BF16 ? (1u << 7) | (1u << 10) : 0u;   // A and B formats
       constexpr uint32_t id_pv = umma_idesc_f16(128, 128) | type | (1u << 16);   // B (V) MN-major
       const int h = warp - 1;
@@ -269,46 +272,55 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         sc.begin(it);
         pc.begin(it);
         bool more_s = true, more_p = true;
-        ok = mbar_wait_bounded(qfull, ii & 1);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(qfull, ii & 1));
         for (int ahead = 0; ok && more_p; ahead++) {
           if (ahead >= 2) {
             const Parts p = parts_of(it, a, h, pc.key(it));
             const int st = pc.t & 1, n = pc.n;
-            const bool first = pc.j == 0 && ahead == 2;
-            uint64_t bd = vd + ((st * kW8Tile + pc.u * 8192 + 4096 * p.c0) >> 4);
-            ok = mbar_wait_bounded(vfull(st), (pc.t >> 1) & 1) && mbar_wait_bounded(pfull(h, n), (n >> 1) & 1);
+            const bool first = ahead == 2;
+            const uint64_t bd = vd + ((st * kW8Tile + pc.u * 8192) >> 4);
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull(st), (pc.t >> 1) & 1) &&
+                                             mbar_wait_bounded(pfull(h, n), (n >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 2
-            for (int kk = 2 * p.c0; kk < 2 * p.c1; kk++, bd += 2048 >> 4)
-              umma_f16_tmem_a(to, ts + 64 * (n & 1) + 8 * kk, bd, id_pv, !first || kk > 2 * p.c0);
-            umma_commit(pvdone(h, n));
+            if (lane == 0) {
+#pragma unroll
+              for (int kk = 0; kk < 4; kk++)
+                if (kk >= 2 * p.c0 && kk < 2 * p.c1)
+                  umma_f16_tmem_a(to, ts + 64 * (n & 1) + 8 * kk, bd + kk * (2048 >> 4), id_pv, !first || kk > 2 * p.c0);
+              umma_commit(pvdone(h, n));
+            }
+            __syncwarp();
             more_p = pc.next(it);
           }
           if (more_s) {
             const Parts p = parts_of(it, a, h, sc.key(it));
             const int st = sc.t & 1, n = sc.n;
             const uint32_t id = umma_idesc_f16(128, 32 * (p.c1 - p.c0)) | type;
-            uint64_t ad = qd, bd = kd + ((st * kW8Tile + sc.u * 8192 + 4096 * p.c0) >> 4);
-            ok = mbar_wait_bounded(kfull(st), (sc.t >> 1) & 1) &&
-                 (n < 2 || mbar_wait_bounded(pvdone(h, n - 2), ((n - 2) >> 2) & 1));
+            const uint64_t bd = kd + ((st * kW8Tile + sc.u * 8192 + 4096 * p.c0) >> 4);
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(kfull(st), (sc.t >> 1) & 1) &&
+                                             (n < 2 || mbar_wait_bounded(pvdone(h, n - 2), ((n - 2) >> 2) & 1)));
             if (!ok) break;
             tc_fence_after();
+            if (lane == 0) {
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-              umma_f16(ts + 64 * (n & 1) + 32 * p.c0, ad, bd, id, k > 0);
-              const int step = (k == 3 ? kW8Half - 96 : 32) >> 4;      // 16 features on; the second half's after four
-              ad += step;
-              bd += step;
+              for (int k = 0; k < 8; k++) {
+                const int off = ((k >> 2) * kW8Half + (k & 3) * 32) >> 4;      // half of the features, 16 of them
+                umma_f16(ts + 64 * (n & 1) + 32 * p.c0, qd + off, bd + off, id, k > 0);
+              }
+              umma_commit(sdone(h, n));
             }
-            umma_commit(sdone(h, n));
+            __syncwarp();
             more_s = sc.next(it);
           }
         }
       }
       if (!ok) fail();
-      umma_commit(drain(h));                   // every MMA issued so far has completed
-      mbar_wait_bounded(drain(h), 0);
+      if (lane == 0) {
+        umma_commit(drain(h));                 // every MMA issued so far has completed
+        mbar_wait_bounded(drain(h), 0);
+      }
+      __syncwarp();
     }
   }
   } else {
