@@ -19,7 +19,7 @@
 // either half's softmax does, and the next item's first products while this
 // item's results are written. (Tensor memory holds two S of 64 columns and an O
 // of 128 for each half; with one S of 128 columns a half, each softmax waited
-// for P V and the next S in turn: 4900 cycles for 128 keys instead of XXXX.)
+// for P V and the next S in turn: 4900 cycles for 128 keys instead of 3100.)
 // Only key tiles with a visible key are visited, the window's from the diagonal
 // back (the nearest keys give a good first m), then the first tokens'; of each,
 // a half takes the 32-key parts that some of its rows may see. Every wait is bounded; on expiry
@@ -136,6 +136,15 @@ __device__ __forceinline__ Parts parts_of(const Item& it, const W8Args& a, int h
   return p;
 }
 
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {     // without waiting
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
@@ -336,58 +345,56 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       const int q0 = it.p0 + half * a.tq, q1 = max(min(q0 + a.tq, it.n0) - 1, q0), pos = q0 + token;
       float m = -INFINITY, l = 0.0f;
       cu.begin(it);
-      bool first = true, more = true;
+      bool first = true, more = true, have = false, raise = true;
+      float s[64];
       for (; more; first = false) {
-        const int kt = cu.key(it), n = cu.n;
-        const Parts p = parts_of(it, a, half, kt);
+        const int kt = cu.key(it), n = cu.n, stage = cu.t & 1, stage_par = (cu.t >> 1) & 1, u = cu.u;
         const uint32_t tb = ts + 64 * (n & 1);
-        const bool inside = kt + 32 * p.c1 - 1 <= q0 &&
-                            (a.window <= 0 || kt + 32 * p.c0 > q1 - a.window || kt + 32 * p.c1 <= a.sinks);
-        // keys [lo, hi] of the window, or below the number of first tokens
-        const int hi = pos - kt, lo = a.window > 0 ? pos - a.window + 1 - kt : 0, early = a.window > 0 ? a.sinks - kt : 0;
-        bool raise = __any_sync(0xffffffffu, m == -INFINITY);
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(sdone(half, n), (n >> 2) & 1));
-        if (!ok) break;
-        tc_fence_after();
+        if (!have) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(sdone(half, n), (n >> 2) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          tmem_ld32_nowait(tb, s);
+          tmem_ld32_nowait(tb + 32, s + 32);
+        }
         if (kt + 64 > it.n0) {
           // V rows behind the request belong to others: zero them, whatever they
           // hold (their weight is 0, but 0 * Inf is not). Both halves do, each
           // ahead of its own product
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull(cu.t & 1), (cu.t >> 1) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull(stage), stage_par));
           if (!ok) break;
           const int own = max(it.n0 - kt, 0);
-          uint8_t* vs = smem + kW8OffV + (cu.t & 1) * kW8Tile + cu.u * 8192;
+          uint8_t* vs = smem + kW8OffV + stage * kW8Tile + u * 8192;
           for (int y = row; y < 2 * (64 - own) * 8; y += 128) {
             const int f = y & 1, r = own + (y >> 4), o = (y >> 1) & 7;
             *reinterpret_cast<uint4*>(vs + f * kW8Half + r * 128 + 16 * o) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async();
         }
-        auto hide = [&](float* s, int q) {
-          if (inside) return;
-          const uint32_t see = below(hi + 1 - 32 * q) & (~below(lo - 32 * q) | below(early - 32 * q));
+        tmem_wait_ld();
+        loaded32(s);
+        loaded32(s + 32);
+        // some row does not see all 64 keys: those of the window, or below the
+        // number of first tokens
+        if (!(kt + 63 <= q0 && (a.window <= 0 || kt > q1 - a.window || kt + 64 <= a.sinks))) {
+          const int hi = pos - kt + 1, lo = a.window > 0 ? pos - a.window + 1 - kt : 0, early = a.window > 0 ? a.sinks - kt : 0;
+          const uint32_t see0 = below(hi) & (~below(lo) | below(early));
+          const uint32_t see1 = below(hi - 32) & (~below(lo - 32) | below(early - 32));
 #pragma unroll
-          for (int e = 0; e < 32; e++) s[e] = see & (1u << e) ? s[e] : -INFINITY;
-        };
+          for (int e = 0; e < 32; e++) {
+            s[e] = see0 & (1u << e) ? s[e] : -INFINITY;
+            s[32 + e] = see1 & (1u << e) ? s[32 + e] : -INFINITY;
+          }
+        }
         uint32_t ph[32];
         float sum;
 #pragma unroll 1
-        while (true) {
-          if (raise) {
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int q = p.c0; q < p.c1; q++) {
-              float s[32];
-              tmem_ld32_nowait(tb + 32 * q, s);
-              tmem_wait_ld();
-              loaded32(s);
-              hide(s, q);
-              float y[4] = {s[0], s[1], s[2], s[3]};
+        for (bool again = raise;; again = true) {
+          if (again) {
+            float y[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-              for (int e = 4; e < 32; e++) y[e & 3] = fmaxf(y[e & 3], s[e]);
-              mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
-            }
-            const float mn = fmaxf(m, mx * kLogitScale);
+            for (int e = 4; e < 64; e++) y[e & 3] = fmaxf(y[e & 3], s[e]);
+            const float mn = fmaxf(m, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * kLogitScale);
             if (!first) {      // O is still once the last P V is done
               ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, n - 1), ((n - 1) >> 2) & 1));
               if (!ok) break;
@@ -408,43 +415,38 @@ __global__ void __launch_bounds__(kW8Threads, 1)
               tmem_wait_st();
             }
             m = mn;
+            raise = __any_sync(0xffffffffu, m == -INFINITY);     // a row that has seen no key so far
           }
-          const float mr = m == -INFINITY ? 0.0f : m;     // no visible key so far
+          const float mr = m == -INFINITY ? 0.0f : m;
           const uint64_t sc2 = f32x2(kLogitScale, kLogitScale), nm2 = f32x2(-mr, -mr);
           uint64_t l2[4] = {0, 0, 0, 0};
-          float s[2][32];
 #pragma unroll
-          for (int q = 0; q < 2; q++)
-            if (q >= p.c0 && q < p.c1) tmem_ld32_nowait(tb + 32 * q, s[q]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < 2; q++)
-            if (q >= p.c0 && q < p.c1) {
-              loaded32(s[q]);
-              hide(s[q], q);
-#pragma unroll
-              for (int e = 0; e < 16; e++) {
-                const uint64_t y = fma_f32x2(f32x2(s[q][2 * e], s[q][2 * e + 1]), sc2, nm2);
-                const float u = fast_exp2(__uint_as_float((uint32_t)y)), v = fast_exp2(__uint_as_float((uint32_t)(y >> 32)));
-                l2[e & 3] = add_f32x2(l2[e & 3], f32x2(u, v));
-                ph[16 * q + e] = pack_elems<ELEM>(u, v);
-              }
-            }
+          for (int e = 0; e < 32; e++) {
+            const uint64_t y = fma_f32x2(f32x2(s[2 * e], s[2 * e + 1]), sc2, nm2);
+            const float v0 = fast_exp2(__uint_as_float((uint32_t)y)), v1 = fast_exp2(__uint_as_float((uint32_t)(y >> 32)));
+            l2[e & 3] = add_f32x2(l2[e & 3], f32x2(v0, v1));
+            ph[e] = pack_elems<ELEM>(v0, v1);
+          }
           const uint64_t t2 = add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3]));
           sum = __uint_as_float((uint32_t)t2) + __uint_as_float((uint32_t)(t2 >> 32));
-          if (raise || !__any_sync(0xffffffffu, !(sum <= kW8Most))) break;
-          raise = true;
+          if (again || !__any_sync(0xffffffffu, !(sum <= kW8Most))) break;
         }
         if (!ok) break;
         l += sum;
-#pragma unroll
-        for (int q = 0; q < 2; q++)
-          if (q >= p.c0 && q < p.c1) tmem_st16(tb + 16 * q, ph + 16 * q);
+        tmem_st16(tb, ph);
+        tmem_st16(tb + 16, ph + 16);
+        // the next S, if it is there, comes while P goes
+        more = cu.next(it);
+        have = more && __all_sync(0xffffffffu, mbar_test(sdone(half, n + 1), ((n + 1) >> 2) & 1));
+        if (have) {
+          tc_fence_after();
+          tmem_ld32_nowait(ts + 64 * ((n + 1) & 1), s);
+          tmem_ld32_nowait(ts + 64 * ((n + 1) & 1) + 32, s + 32);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull(half, n));
-        more = cu.next(it);
       }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, cu.n - 1), ((cu.n - 1) >> 2) & 1));
       if (!ok) break;
