@@ -248,10 +248,11 @@ __device__ __forceinline__ void load_q(const uint8_t* q, int G, int lane, uint32
 }
 __device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
-// A tile of the 16-bit tail: kp, vp point to the lane's first 16 bytes of K
-// and V, the next steps 512 bytes on. qf: the queries in elem_type.
-template <int ELEM>
-__device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], const uint8_t* kp, const uint8_t* vp,
+// A tile of the 16-bit tail: kp points to the lane's first 16 bytes of K,
+// after_k() gives V's once K is read; the next steps lie 512 bytes on. qf: the
+// queries in elem_type.
+template <int ELEM, typename AfterK>
+__device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], const uint8_t* kp, AfterK after_k,
                                           const See& see, float ks) {
   float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -260,6 +261,7 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
     const uint32_t a[4] = {w.x, w.z, w.y, w.w};
     mma_elem<ELEM>(m & 1 ? y : x, a, qf[2 * m], qf[2 * m + 1]);
   }
+  const uint8_t* vp = after_k();
   // entries of tokens that are not visible (unwritten ones too) become 0
   const uint32_t lo = prmt(see.v, 0, 0x1100u), hi = prmt(see.v, 0, 0x3322u);
   uint4 v[8];
@@ -356,6 +358,59 @@ __device__ __forceinline__ void put_partial(const State& s, float* p, int G, int
 // are equal, infinite ones too
 __device__ __forceinline__ float join(float m, float M) { return m == M ? 1.0f : fast_exp2(m - M); }
 
+// largest of the lanes' values, in one instruction (NaN is passed over)
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// Row q of several parts: lane x holds the address of part x where bit x of set
+// is on; rows of `row` floats, then G maxima from G * row and G sums from
+// G * row + 8. Added to what r holds.
+struct Row {
+  float4 o;
+  float m, l;
+};
+__device__ __noinline__ Row join_row(Row r, unsigned set, const float* p, int row, int G, int q, int lane) {
+  const bool has = set >> lane & 1u;
+  const float m = has ? p[G * row + q] : -INFINITY, pl = has ? p[G * row + 8 + q] : 0.0f;
+  const float now = fmaxf(r.m, warp_max(m));
+  const float f = has ? join(m, now) : 0.0f, g = join(r.m, now);
+  r.m = now;
+  r.l *= g;
+  r.o.x *= g;
+  r.o.y *= g;
+  r.o.z *= g;
+  r.o.w *= g;
+  const unsigned long long mine = reinterpret_cast<unsigned long long>(p + q * row);
+  // two parts at a time
+#pragma unroll 1
+  while (set) {
+    const int x0 = __ffs(set) - 1;
+    set &= set - 1;
+    const int x1 = set ? __ffs(set) - 1 : x0;
+    const bool two = set != 0;
+    set &= set - 1;
+    const float4 v0 = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, mine, x0))[lane];
+    const float4 v1 = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, mine, x1))[lane];
+    const float f0 = __shfl_sync(0xffffffffu, f, x0), l0 = __shfl_sync(0xffffffffu, pl, x0);
+    const float f1 = __shfl_sync(0xffffffffu, f, x1), l1 = __shfl_sync(0xffffffffu, pl, x1);
+    r.l = fmaf(l0, f0, r.l);
+    r.o.x = fmaf(v0.x, f0, r.o.x);
+    r.o.y = fmaf(v0.y, f0, r.o.y);
+    r.o.z = fmaf(v0.z, f0, r.o.z);
+    r.o.w = fmaf(v0.w, f0, r.o.w);
+    if (two) {
+      r.l = fmaf(l1, f1, r.l);
+      r.o.x = fmaf(v1.x, f1, r.o.x);
+      r.o.y = fmaf(v1.y, f1, r.o.y);
+      r.o.z = fmaf(v1.z, f1, r.o.z);
+      r.o.w = fmaf(v1.w, f1, r.o.w);
+    }
+  }
+  return r;
+}
+
 template <int ELEM>
 __device__ __forceinline__ void write_row(uint8_t* out, int lane, float4 o, float l) {
   const float inv = __fdiv_rn(1.0f, l);
@@ -385,12 +440,6 @@ __device__ __forceinline__ void bulk_g2s_hint(uint32_t dst, const void* src, uin
       "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;\n" ::"r"(dst),
       "l"(src), "r"(bytes), "r"(bar), "l"(pol)
       : "memory");
-}
-// largest of the lanes' values, in one instruction (NaN is passed over)
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
-  return y;
 }
 __device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
 
@@ -611,17 +660,21 @@ __global__ void __launch_bounds__(kA8Warps * 32)
         const float k2[2] = {ks * qs[0], ks * qs[1]};
         code_tile<CODE>(s, qf, p, edge, see, k2, lv);
       } else {
-        const uint8_t* v = wait();
+        auto after_k = [&]() {      // the next tile's K follows while V is awaited
+          __syncwarp();
+          issue(1);
+          return wait();
+        };
         if (ELEM == DKV_F16) {
-          tail_tile<ELEM>(s, qf, p, v, see, kLogitScale);
+          tail_tile<ELEM>(s, qf, p, after_k, see, kLogitScale);
         } else {
           uint32_t raw[16];    // the other tiles' fragments are scaled
           load_q<ELEM>(q_at, G, lane, raw);
-          tail_tile<ELEM>(s, raw, p, v, see, kLogitScale);
+          tail_tile<ELEM>(s, raw, p, after_k, see, kLogitScale);
         }
       }
       __syncwarp();
-      issue(tail ? 2 : 1);
+      issue(1);
     }
     if (last) break;
   }
@@ -636,99 +689,60 @@ __global__ void __launch_bounds__(kA8Warps * 32)
     }
   __syncthreads();
 
-  // ---- joins: a query row of a unit per warp, over the warps' parts and, if
-  // the unit crosses CTAs, again over the CTAs' by the one that arrives last ----
+  // ---- joins: the rows of a unit that several warps hold parts of are shared
+  // out over warps; where the unit crosses CTAs, each leaves its part, and the
+  // CTA that arrives last joins those ----
   const int mine = lane < 2 * kA8Warps ? s_unit[lane] : -1;
   const unsigned same = __match_any_sync(0xffffffffu, mine);
   unsigned leaders = __ballot_sync(0xffffffffu, mine >= 0 && __ffs(same) - 1 == lane);
   const float* my_part = reinterpret_cast<const float*>(
       sm + ((lane & 1) ? (lane >> 1) * (kA8Stages * kA8Entry) : first_off + (lane >> 1) * part_bytes));
   const int stride = G * kD + 16;      // floats of a part in the workspace
-  for (int task = warp; task < __popc(leaders) * G; task += kA8Warps) {
-    unsigned rest = leaders;
-    for (int skip = task / G; skip > 0; skip--) rest &= rest - 1;
-    const int lead = __ffs(rest) - 1, q = task % G;
+  const int share = max(1, kA8Warps / max(1, __popc(leaders)));     // warps a unit
+  for (int at = 0; leaders; at++, leaders &= leaders - 1) {
+    if (at % (kA8Warps / share) != warp / share || warp / share >= kA8Warps / share) continue;
+    const int lead = __ffs(leaders) - 1, q0 = warp % share;
     const int u = __shfl_sync(0xffffffffu, mine, lead);
+    const unsigned set = __shfl_sync(0xffffffffu, same, lead);
     const int us = s_span[lead].x, ue = s_span[lead].y;
-    // rows of the parts: lane x holds part x of the round
-    unsigned set = __shfl_sync(0xffffffffu, same, lead);
-    const float* p = my_part;
-    int row = kA8Row, left = 1;
-    int c0 = 0, c1 = 0;
-    float M = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    while (true) {
-      const bool has = set >> lane & 1u;
-      const float m = has ? p[G * row + q] : -INFINITY, pl = has ? p[G * row + 8 + q] : 0.0f;
-      const float now = fmaxf(M, warp_max(m));
-      const float f = has ? join(m, now) : 0.0f, g = join(M, now);
-      M = now;
-      l *= g;
-      o.x *= g;
-      o.y *= g;
-      o.z *= g;
-      o.w *= g;
-      // two parts at a time
+    const bool whole = us >= lo && ue <= hi;
+    uint8_t* out = a.out + (size_t)u * G * (2 * kD);
+    float* dst = a.part + (size_t)(2 * blockIdx.x + (us < lo ? 0 : 1)) * stride;
 #pragma unroll 1
-      for (unsigned b = set; b;) {
-        const int x0 = __ffs(b) - 1;
-        b &= b - 1;
-        const int x1 = b ? __ffs(b) - 1 : x0;
-        const bool two = b != 0;
-        b &= b - 1;
-        const unsigned long long mine = reinterpret_cast<unsigned long long>(p + q * row);
-        const float4 v0 = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, mine, x0))[lane];
-        const float4 v1 = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, mine, x1))[lane];
-        const float f0 = __shfl_sync(0xffffffffu, f, x0), l0 = __shfl_sync(0xffffffffu, pl, x0);
-        const float f1 = __shfl_sync(0xffffffffu, f, x1), l1 = __shfl_sync(0xffffffffu, pl, x1);
-        l = fmaf(l0, f0, l);
-        o.x = fmaf(v0.x, f0, o.x);
-        o.y = fmaf(v0.y, f0, o.y);
-        o.z = fmaf(v0.z, f0, o.z);
-        o.w = fmaf(v0.w, f0, o.w);
-        if (two) {
-          l = fmaf(l1, f1, l);
-          o.x = fmaf(v1.x, f1, o.x);
-          o.y = fmaf(v1.y, f1, o.y);
-          o.z = fmaf(v1.z, f1, o.z);
-          o.w = fmaf(v1.w, f1, o.w);
+    for (int q = q0; q < G; q += share) {
+      const Row r = join_row(Row{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f}, set, my_part, kA8Row, G, q, lane);
+      if (whole) {
+        write_row<ELEM>(out + q * (2 * kD), lane, r.o, r.l);
+      } else {
+        *reinterpret_cast<float4*>(dst + q * kD + 4 * lane) = r.o;
+        if (lane == 0) {
+          dst[G * kD + q] = r.m;
+          dst[G * kD + 8 + q] = r.l;
         }
       }
-      if (--left > 0) {                // further CTAs, 32 at a time
-        c0 += 32;
-        set = c1 - c0 >= 31 ? 0xffffffffu : (1u << (c1 - c0 + 1)) - 1u;
-        p = a.part + (size_t)(2 * min(c0 + lane, c1)) * stride;
-        continue;
-      }
-      if (row == kD || (us >= lo && ue <= hi)) break;
-      // publish this CTA's part of the row; the last to arrive goes on
-      auto cta_of = [&](int x) { return (int)((((long long)x + 1) * ctas - 1) / total); };
-      c0 = cta_of(us);
-      c1 = cta_of(ue - 1);
-      float* dst = a.part + (size_t)(2 * blockIdx.x + (us < lo ? 0 : 1)) * stride;
-      *reinterpret_cast<float4*>(dst + q * kD + 4 * lane) = o;
-      if (lane == 0) {
-        dst[G * kD + q] = M;
-        dst[G * kD + 8 + q] = l;
-      }
-      __threadfence();
-      __syncwarp();
-      unsigned old = 0;
-      if (lane == 0) old = atomicInc(a.count + (size_t)u * G + q, (unsigned)(c1 - c0));   // back to zero by itself
-      if (__shfl_sync(0xffffffffu, old, 0) != (unsigned)(c1 - c0)) {
-        row = 0;
-        break;
-      }
-      __threadfence();
-      row = kD;
-      left = (c1 - c0 + 32) / 32;
-      set = c1 - c0 >= 31 ? 0xffffffffu : (1u << (c1 - c0 + 1)) - 1u;
-      p = a.part + (size_t)(2 * min(c0 + lane, c1) + (lane == 0 ? 1 : 0)) * stride;
-      M = -INFINITY;
-      l = 0.0f;
-      o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
-    if (row) write_row<ELEM>(a.out + ((size_t)u * G + q) * (2 * kD), lane, o, l);
+    if (whole) continue;
+    auto cta_of = [&](int x) { return (int)((((long long)x + 1) * ctas - 1) / total); };
+    const int c0 = cta_of(us), c1 = cta_of(ue - 1);
+    __threadfence();
+    __syncwarp();
+    // a counter per row, back to zero by itself; a lane each
+    const bool counts = lane < G && lane >= q0 && (lane - q0) % share == 0;
+    const unsigned old = counts ? atomicInc(a.count + (size_t)u * G + lane, (unsigned)(c1 - c0)) : 0u;
+    unsigned last = __ballot_sync(0xffffffffu, counts && old == (unsigned)(c1 - c0));
+    if (!last) continue;
+    __threadfence();
+#pragma unroll 1
+    for (; last; last &= last - 1) {
+      const int q = __ffs(last) - 1;
+      Row r{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
+      for (int x = c0; x <= c1; x += 32) {
+        const int n = min(c1 - x + 1, 32), cta = min(x + lane, c1);
+        r = join_row(r, n == 32 ? 0xffffffffu : (1u << n) - 1u, a.part + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * stride,
+                     kD, G, q, lane);
+      }
+      write_row<ELEM>(out + q * (2 * kD), lane, r.o, r.l);
+    }
   }
 
   // requests without tokens: zeros
