@@ -37,6 +37,7 @@ namespace dkv {
 namespace {
 
 constexpr int kA8Warps = 12;
+static_assert(kA8Warps == 12, "the joins share 12 warps out to 1, 2, 3, 4, 6 or 12 units");
 constexpr int kA8Stages = 2;        // ring entries of a warp
 constexpr int kA8Entry = 2 * kTile; // 4 KB: K and V codes of a tile, or K or V of a tail tile
 constexpr int kA8Row = kD + 4;      // floats of a query's row in a shared partial (no bank conflicts)
@@ -693,17 +694,23 @@ __global__ void __launch_bounds__(kA8Warps * 32)
   // out over warps; where the unit crosses CTAs, each leaves its part, and the
   // CTA that arrives last joins those ----
   const int mine = lane < 2 * kA8Warps ? s_unit[lane] : -1;
-  const unsigned same = __match_any_sync(0xffffffffu, mine);
-  unsigned leaders = __ballot_sync(0xffffffffu, mine >= 0 && __ffs(same) - 1 == lane);
+  // slots lie in the order of positions: those of a unit are neighbours
+  const unsigned used = __ballot_sync(0xffffffffu, mine >= 0), below = used & ((1u << lane) - 1u);
+  const int before = __shfl_sync(0xffffffffu, mine, below ? 31 - __clz(below) : lane);
+  unsigned leaders = __ballot_sync(0xffffffffu, mine >= 0 && (below == 0 || before != mine));
   const float* my_part = reinterpret_cast<const float*>(
       sm + ((lane & 1) ? (lane >> 1) * (kA8Stages * kA8Entry) : first_off + (lane >> 1) * part_bytes));
   const int stride = G * kD + 16;      // floats of a part in the workspace
-  const int share = max(1, kA8Warps / max(1, __popc(leaders)));     // warps a unit
-  for (int at = 0; leaders; at++, leaders &= leaders - 1) {
-    if (at % (kA8Warps / share) != warp / share || warp / share >= kA8Warps / share) continue;
-    const int lead = __ffs(leaders) - 1, q0 = warp % share;
+  // groups of warps, a unit each in turn
+  const int n_units = __popc(leaders);
+  const int groups = n_units <= 4 ? max(n_units, 1) : n_units <= 6 ? 6 : kA8Warps, share = kA8Warps / groups;
+  const int group = warp * groups / kA8Warps, q0 = warp - group * share;
+  for (int turn = 0; leaders; leaders &= leaders - 1, turn = turn + 1 == groups ? 0 : turn + 1) {
+    if (turn != group) continue;
+    const int lead = __ffs(leaders) - 1;
+    const unsigned next = leaders & (leaders - 1);
+    const unsigned set = used & ~((1u << lead) - 1u) & (next ? (next & -next) - 1u : 0xffffffffu);
     const int u = __shfl_sync(0xffffffffu, mine, lead);
-    const unsigned set = __shfl_sync(0xffffffffu, same, lead);
     const int us = s_span[lead].x, ue = s_span[lead].y;
     const bool whole = us >= lo && ue <= hi;
     uint8_t* out = a.out + (size_t)u * G * (2 * kD);
