@@ -561,7 +561,7 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
   if (n_req < 1 || n_req > kMaxCallReq || !seq_lens || !at(seq_lens, 4) || !at(slots, 4)) return DKV_ERR_ARG;
   if (!slots && n_req > cache->n_slots) return DKV_ERR_ARG;
   const int hkv = cache->n_kv_heads, hq = hkv * cache->group_size;
-  if (!rows_ok(q, q_stride, hq) || !out || !at(out, 16) || window < 0 || sinks < 0) return DKV_ERR_ARG;
+  if (!rows_ok(q, q_stride, hq) || !out || out == q || !at(out, 16) || window < 0 || sinks < 0) return DKV_ERR_ARG;
   // tiles of the whole call are numbered in 32 bits
   if ((long long)n_req * hkv * ((long long)cache->table_width * cache->block_tokens / kSub + 1) > 0x7ffffff0ll)
     return DKV_ERR_ARG;
@@ -571,6 +571,8 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
   const int sms = sm_count(cache->device);
   if (!sms) return DKV_ERR_CUDA;
   if (cache->workspace_bytes < (int64_t)attention8_workspace(hkv, cache->group_size, n_req, sms)) return DKV_ERR_SCRATCH;
+  // a window that no length exceeds is none (and positions minus it stay in 32 bits)
+  if (window >= (long long)cache->table_width * cache->block_tokens) window = 0;
   const cudaError_t e =
       launch_attention8(view(cache), cache->elem_type, cache->code_type, sms, slots, seq_lens, n_req, q, q_stride, out,
                         window, sinks, cache->workspace, reinterpret_cast<cudaStream_t>(stream));
@@ -585,11 +587,13 @@ int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* se
   if (n_req < 1 || n_req > kMaxCallReq || !seq_lens || window < 0 || sinks < 0) return DKV_ERR_ARG;
   const int hkv = cache->n_kv_heads, hq = hkv * cache->group_size;
   if (!rows_ok(q, q_stride, hq) || !rows_ok(k, k_stride, hkv) || !rows_ok(v, v_stride, hkv)) return DKV_ERR_ARG;
-  if (!out || !at(out, 16)) return DKV_ERR_ARG;
+  if (!out || !at(out, 16) || out == q || out == k || out == v) return DKV_ERR_ARG;
   long long tok = 0, tiles = 0;
+  int longest = 0;
   const int tq = 128 / cache->group_size;
   for (int i = 0; i < n_req; i++) {
     if (seq_lens[i] < 1) return DKV_ERR_ARG;
+    longest = std::max(longest, seq_lens[i]);
     tok += seq_lens[i];
     tiles += (seq_lens[i] + (long long)tq - 1) / tq;
     if (tok > 0x7fffff00ll || tiles * hkv > 0x7ffffff0ll) return DKV_ERR_ARG;   // rows and tiles are 32-bit
@@ -598,6 +602,7 @@ int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* se
   if (!dev.ok) return DKV_ERR_CUDA;
   const int sms = sm_count(cache->device);
   if (!sms) return DKV_ERR_CUDA;
+  if (window >= longest) window = 0;   // as above
   const cudaError_t e = launch_prefill8(view(cache), cache->elem_type, seq_lens, n_req, q, q_stride, k, k_stride, v,
                                         v_stride, out, window, sinks, sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? DKV_OK : DKV_ERR_CUDA;

@@ -307,8 +307,8 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
     scales fp32 [n_pages][Hkv][2], tail [n_slots][Hkv][T/16][2][2048] (float16
     or bfloat16), page_table int32 [n_slots][width]. The status words and the
     workspace for attention calls of up to max_req requests (default: one a
-    slot, at most 1024) are allocated here unless given; layers whose calls are
-    ordered on one stream may share a workspace."""
+    slot, at most 1024) are allocated here unless given; layers of one head layout
+    whose calls are ordered on one stream may share a workspace."""
     import torch
     codes = {torch.float8_e4m3fn: DKV_E4M3, torch.int8: DKV_INT8}
     elems = {torch.float16: DKV_F16, torch.bfloat16: DKV_BF16}

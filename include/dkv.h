@@ -440,7 +440,8 @@ int dkv_pool_export(dkv_pool* pool, dkv_snapshot* out);
  *    calls are device no-ops. The caller zeroes both words to go on.
  *  - Calls on one cache must be ordered on one stream (or synchronised by the
  *    caller). Attention calls that may overlap (two streams, two replayed
- *    graphs) need a workspace each; appends and prompt attention use none. */
+ *    graphs) need a workspace each; others may share one if n_kv_heads and
+ *    group_size are the same. Appends and prompt attention use none. */
 #define DKV_F16  0   /* elem_type: k, v, q, out and tails are IEEE binary16 */
 #define DKV_BF16 1   /* elem_type: bfloat16                                  */
 #define DKV_E4M3 0   /* code_type: 8-bit floating point (4 exponent bits)    */
@@ -509,7 +510,9 @@ int dkv_cache8_append(const dkv_cache8* cache, int32_t n_req, const int32_t* n_n
  * request with N <= 0 gets zeros. Tokens that are not visible are not read
  * into the result, whatever they hold.
  *   q       device [n_req][Hkv * G][128], rows q_stride elements apart.
- *   out     device [n_req][Hkv * G][128] of elem_type, contiguous.
+ *   out     device [n_req][Hkv * G][128] of elem_type, contiguous, apart from q.
+ * The call is split over the GPU by the lengths that it finds on the device;
+ * the same inputs give the same bits whatever order its blocks run in.
  * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED, DKV_ERR_SCRATCH (workspace_bytes
  * below dkv_cache8_workspace for n_req) (host, nothing queued); DKV_ERR_CUDA. */
 int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* slots, const int32_t* seq_lens,
@@ -521,7 +524,8 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
  * order) sees j <= p with window = 0, j > p - window or j < sinks. The cache
  * supplies the head layout, elem_type, device and status only.
  *   q, k, v  device [sum(seq_lens)][heads][128], token rows *_stride elements
- *            apart (multiples of 8); out contiguous, of elem_type.
+ *            apart (multiples of 8); out contiguous, of elem_type, apart from
+ *            them.
  * Products accumulate in fp32; probabilities enter the value product rounded
  * to elem_type. Values of other requests never enter a result; inside one
  * request k and v must be finite (a non-finite v reaches the rows before it

@@ -64,12 +64,12 @@ def append(c, n_req=2, n_new=None, slots=None, before=A, k=A, ks=256, v=A, vs=25
                                         slots, before, k, ks, v, vs, q, qs, rope, rope_len, k_rot, q_rot, None)
 
 
-def attention(c, n_req=2, slots=None, lens=A, q=A, qs=1024, out=A, window=0, sinks=0):
+def attention(c, n_req=2, slots=None, lens=A, q=A, qs=1024, out=2 * A, window=0, sinks=0):
     return dkv.load().dkv_cache8_attention(None if c is None else C.byref(c), n_req, slots, lens, q, qs, out, window,
                                            sinks, None)
 
 
-def prefill(c, n_req=2, lens=(3, 4), q=A, qs=1024, k=A, ks=256, v=A, vs=256, out=A, window=0, sinks=0):
+def prefill(c, n_req=2, lens=(3, 4), q=A, qs=1024, k=A, ks=256, v=A, vs=256, out=2 * A, window=0, sinks=0):
     ln = None if lens is None else np.asarray(lens, np.int32)
     return dkv.load().dkv_cache8_prefill(None if c is None else C.byref(c), n_req, None if ln is None else ln.ctypes.data,
                                          q, qs, k, ks, v, vs, out, window, sinks, None)
@@ -116,7 +116,8 @@ def test_rope_is_given_with_a_rotary_dimension_only():
 
 @pytest.mark.parametrize("kw", [
     dict(n_req=0), dict(n_req=1025), dict(n_req=5), dict(lens=None), dict(lens=A + 2), dict(slots=A + 3), dict(q=None),
-    dict(q=A + 2), dict(qs=1023), dict(qs=1028), dict(qs=512), dict(out=None), dict(out=A + 4), dict(window=-1),
+    dict(q=A + 2), dict(qs=1023), dict(qs=1028), dict(qs=512), dict(out=None), dict(out=A + 4), dict(out=A),
+    dict(window=-1, out=2 * A),
     dict(sinks=-1)])
 def test_bad_attention_arguments_are_refused(kw):
     dkv.build.build()
@@ -134,7 +135,7 @@ def test_attention_needs_a_workspace_and_32_bit_tile_numbers():
 @pytest.mark.parametrize("kw", [
     dict(n_req=0), dict(n_req=1025), dict(lens=None), dict(lens=(3, 0)), dict(lens=(-1, 3)), dict(q=None), dict(k=None),
     dict(v=None), dict(out=None), dict(q=A + 2), dict(qs=1020), dict(ks=252), dict(vs=128), dict(out=A + 8),
-    dict(window=-5), dict(sinks=-1), dict(lens=(2 ** 31 - 1, 2 ** 31 - 1))])
+    dict(window=-5), dict(sinks=-1), dict(lens=(2 ** 31 - 1, 2 ** 31 - 1)), dict(out=A)])
 def test_bad_prefill_arguments_are_refused(kw):
     dkv.build.build()
     refused(prefill(cache(), **kw))

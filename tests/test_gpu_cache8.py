@@ -584,6 +584,123 @@ def test_captured_step_replays_with_other_contents():
     c.check()
 
 
+def test_captured_prompt_attention():
+    """A captured prompt attention, replayed over other vectors, beside an append."""
+    rng = np.random.default_rng(5)
+    c = Cache(2, 4, 32, 2, 8, BF16, E4M3, rot=128)
+    lens = [100, 150]
+    q, k, v = c.vec(rng, 250, 8), c.vec(rng, 250, 2), c.vec(rng, 250, 2)
+    kr, qr, out, before = torch.empty_like(k), torch.empty_like(q), torch.empty_like(q), torch.zeros(2, dtype=torch.int32, device="cuda")
+
+    def run(o):
+        _dkv().dkv_cache8_append(c.c, before, k, v, rope=c.rope, n_new=lens, q=q, k_rot=kr, q_rot=qr)
+        _dkv().dkv_cache8_prefill(c.c, lens, qr, kr, v, o, window=60, sinks=3)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(out)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(out)
+    for _ in range(3):
+        for t, h in ((q, 8), (k, 2), (v, 2)):
+            t.copy_(c.vec(rng, 250, h))
+        g.replay()
+        again = torch.empty_like(out)
+        got = out.clone()
+        run(again)
+        assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 64, 700])
+def test_windows_beyond_every_length(window):
+    """As no window, whatever the number of first tokens."""
+    for sinks in (0, 5, 2 ** 31 - 1):
+        prefill_case(1, 4, [300, 17], F16, window, sinks)
+        c, slots, q = filled(2, 4, 32, F16, E4M3, [300, 77, 0], seed=2)
+        assert torch.equal(c.attend(slots, [300, 77, 0], q), c.attend(slots, [300, 77, 0], q, window, sinks))
+
+
+def test_first_tokens_beyond_every_length():
+    prefill_case(1, 4, [300, 17, 130], BF16, 9, 2 ** 31 - 1)
+    c, slots, q = filled(2, 4, 32, F16, E4M3, [300, 77, 0], seed=2)
+    assert torch.equal(c.attend(slots, [300, 77, 0], q), c.attend(slots, [300, 77, 0], q, 9, 2 ** 31 - 1))
+
+
+@pytest.mark.parametrize("elem,code", [(F16, E4M3), (BF16, E4M3), (F16, INT8)])
+def test_attention_of_values_that_are_not_finite(elem, code):
+    """A visible NaN key makes its heads' rows NaN, an infinite value in the tail
+    its feature infinite, and nothing else."""
+    rng = np.random.default_rng(9)
+    c = Cache(2, 2, 32, 3, 3, elem, code)
+    k, v, q = c.vec(rng, 120, 2), c.vec(rng, 120, 2), c.vec(rng, 3, 4)
+    k[3, 0, 7] = float("nan")            # request 0, head 0: in a page (e4m3 keeps it, int8 holds 0)
+    v[79, 1, 5] = float("inf")           # request 1 (tokens 40..79), head 1: in the tail
+    c.append(None, [0, 0, 0], [40, 40, 40], k, v)
+    out = c.attend(None, [40, 40, 40], q).float().cpu().numpy()
+    assert np.isnan(out[0, :2]).all() == (code == E4M3) and np.isfinite(out[0, 2:]).all()
+    assert np.isposinf(out[1, 2:, 5]).all()
+    assert np.isfinite(np.delete(out[1], 5, axis=1)).all() and np.isfinite(out[1, :2]).all() and np.isfinite(out[2]).all()
+
+
+def test_stepping_back_inside_the_open_block():
+    """Rejected tokens are written over; the state is that of the tokens kept."""
+    rng = np.random.default_rng(2)
+    a, b = (Cache(2, 2, 32, 1, 4, BF16, E4M3, rot=32, seed=3) for _ in range(2))
+    k, v = a.vec(rng, 90, 2), a.vec(rng, 90, 2)
+    bad = a.vec(rng, 12, 2)
+    a.append(None, [0], [70], k[:70], v[:70])
+    a.append(None, [70], [12], bad, bad)
+    a.append(None, [70], [20], k[70:], v[70:])
+    b.append(None, [0], [90], k, v)
+    torch.cuda.synchronize()
+    assert torch.equal(a.pages.view(torch.uint8), b.pages.view(torch.uint8)) and torch.equal(a.scales, b.scales)
+    assert np.array_equal(*(ref.from_tiles(ref.elem_np(x.tail)[0, 1], 16)[:, :90 % 32] for x in (a, b)))
+
+
+def test_largest_batch():
+    """1024 requests in one call of each kind, ragged, some padded."""
+    rng = np.random.default_rng(4)
+    n = 1024
+    c = Cache(1, 1, 16, n, 3, F16, INT8, rot=16)
+    lens = [int(x) for x in rng.integers(1, 40, n)]
+    order = [int(x) for x in rng.permutation(n)]
+    k, v, q = c.vec(rng, sum(lens), 1), c.vec(rng, sum(lens), 1), c.vec(rng, n, 1)
+    c.append(order, [0] * n, lens, k, v)
+    live = [m if i % 7 else 0 for i, m in enumerate(lens)]
+    out = c.attend(order, live, q)
+    c.check()
+    c.check_attention(out, order, live, q)
+    step = [m if i % 5 else -1 for i, m in enumerate(lens)]
+    c.append(order, step, [1] * n, k[:n], v[:n], step=True)
+    c.check()
+    got = torch.empty((sum(lens), 1, 128), dtype=F16, device="cuda")
+    q2 = c.vec(rng, sum(lens), 1)
+    _dkv().dkv_cache8_prefill(c.c, lens, q2, k, v, got, window=11, sinks=2)
+    qn, kn, vn, gn = (x.double().cpu().numpy() for x in (q2, k, v, got))
+    at = 0
+    for m in lens:
+        see = at + ref.visible(m, 11, 2)
+        want, pv, qk, vm = ref.attend(qn[at + m - 1], kn[see, 0], vn[see, 0])
+        assert (np.abs(gn[at + m - 1] - want) <= ref.tolerance(want, pv, qk, vm, len(see), F16, 2.0 ** -11)).all()
+        at += m
+
+
+def test_shared_workspace_of_two_layers():
+    """Two layers of one head layout take turns with one workspace."""
+    dkv = _dkv()
+    lens = [700, 3, 90]
+    c, slots, q = filled(2, 4, 32, F16, E4M3, lens, seed=1)
+    d, _, q2 = filled(2, 4, 64, BF16, INT8, lens, seed=1)
+    want = c.attend(slots, lens, q), d.attend(slots, lens, q2)
+    e = dkv.make_cache8(d.pages, d.scales, d.tail, d.table, group_size=4, workspace=c.c.tensors[5])
+    d.c = e
+    for _ in range(5):
+        assert torch.equal(c.attend(slots, lens, q), want[0]) and torch.equal(d.attend(slots, lens, q2), want[1])
+
+
 def test_other_streams_and_workspaces():
     """Two caches on two streams at once, and one cache read by two streams with a
     workspace each."""
