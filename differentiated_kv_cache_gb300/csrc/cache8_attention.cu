@@ -24,10 +24,11 @@
 // x_j exceeds it by more than 8: w stays below 2^8, in fp16's range. w enters
 // the second product rounded to fp16 (relative 2^-11, the size of the
 // output's own rounding); l sums the unrounded fp32 values.
-// Tiles of the 16-bit tail take s_k = 1 and, for s_v, the power of two that
-// brings their largest |v| to [128, 256), the size of codes, so that equal
-// weights stand for equal contributions; their values are divided by it (exact
-// but for values 2^-20 and less of the largest).
+// Tiles of the 16-bit tail take s_k = s_v = 1 where there are no codes to mix
+// with; else s_v is the power of two that brings their largest |v| to
+// [128, 256), the size of codes, so that equal weights stand for equal
+// contributions; their values are divided by it (exact but for values 2^-20 and
+// less of the largest).
 #include <algorithm>
 
 #include "cache8.cuh"
@@ -254,7 +255,7 @@ __device__ __forceinline__ uint32_t umax2(uint32_t a, uint32_t b) { return __vma
 // queries in elem_type.
 template <int ELEM, typename AfterK>
 __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], const uint8_t* kp, AfterK after_k,
-                                          const See& see, float ks) {
+                                          bool edge, const See& see, bool mixed, float ks) {
   float x[4] = {0.0f, 0.0f, 0.0f, 0.0f}, y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int m = 0; m < 8; m++) {
@@ -263,28 +264,46 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
     mma_elem<ELEM>(m & 1 ? y : x, a, qf[2 * m], qf[2 * m + 1]);
   }
   const uint8_t* vp = after_k();
-  // entries of tokens that are not visible (unwritten ones too) become 0
-  const uint32_t lo = prmt(see.v, 0, 0x1100u), hi = prmt(see.v, 0, 0x3322u);
   uint4 v[8];
-  uint32_t am2 = 0;        // magnitudes order like their bits
 #pragma unroll
-  for (int m = 0; m < 8; m++) {
-    v[m] = *reinterpret_cast<const uint4*>(vp + 512 * m);
-    v[m].x &= lo;
-    v[m].y &= hi;
-    v[m].z &= lo;
-    v[m].w &= hi;
-    am2 = umax2(umax2(am2, v[m].x & 0x7fff7fffu), umax2(umax2(v[m].y & 0x7fff7fffu, v[m].z & 0x7fff7fffu), v[m].w & 0x7fff7fffu));
+  for (int m = 0; m < 8; m++) v[m] = *reinterpret_cast<const uint4*>(vp + 512 * m);
+#pragma unroll
+  for (int e = 0; e < 4; e++) x[e] = (x[e] + y[e]) * ks;
+  if (edge) {
+    // entries of tokens that are not visible (unwritten ones too) become 0
+    const uint32_t lo = prmt(see.v, 0, 0x1100u), hi = prmt(see.v, 0, 0x3322u);
+#pragma unroll
+    for (int m = 0; m < 8; m++) {
+      v[m].x &= lo;
+      v[m].y &= hi;
+      v[m].z &= lo;
+      v[m].w &= hi;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++) x[e] = (e < 2 ? see.lo : see.hi) ? x[e] : -INFINITY;
   }
-  const uint32_t bits = __reduce_max_sync(0xffffffffu, max(am2 & 0xffffu, am2 >> 16));
-  const float am = elem_float<ELEM>((uint16_t)bits);
-  // exponents that fp16 factors (or the scale floor) allow; infinite or NaN
-  // values leave 1
-  const int low = ELEM == DKV_F16 ? -14 : -100, high = ELEM == DKV_F16 ? 14 : 100;
-  const int ex = am < INFINITY ? max(low, min(high, (int)(__float_as_uint(am) >> 23) - (127 + 7))) : 0;
-  const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+  float inv = 1.0f;
+  if (mixed) {
+    uint32_t am2 = 0;        // magnitudes order like their bits
 #pragma unroll
-  for (int e = 0; e < 4; e++) x[e] = (e < 2 ? see.lo : see.hi) ? fmaf(x[e] + y[e], ks, (float)ex) : -INFINITY;
+    for (int m = 0; m < 8; m++)
+      am2 = umax2(umax2(am2, v[m].x & 0x7fff7fffu), umax2(umax2(v[m].y & 0x7fff7fffu, v[m].z & 0x7fff7fffu), v[m].w & 0x7fff7fffu));
+    const float am = elem_float<ELEM>((uint16_t)__reduce_max_sync(0xffffffffu, max(am2 & 0xffffu, am2 >> 16)));
+    // exponents that fp16 factors (or the scale floor) allow; infinite or NaN
+    // values leave 1
+    const int low = ELEM == DKV_F16 ? -14 : -100, high = ELEM == DKV_F16 ? 14 : 100;
+    const int ex = am < INFINITY ? max(low, min(high, (int)(__float_as_uint(am) >> 23) - (127 + 7))) : 0;
+    inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+#pragma unroll
+    for (int e = 0; e < 4; e++) x[e] += (float)ex;
+#pragma unroll
+    for (int m = 0; m < 8; m++) {
+      v[m].x = scale_pair<ELEM>(v[m].x, inv);
+      v[m].y = scale_pair<ELEM>(v[m].y, inv);
+      v[m].z = scale_pair<ELEM>(v[m].z, inv);
+      v[m].w = scale_pair<ELEM>(v[m].w, inv);
+    }
+  }
   raise(s, x);
   weights(s, x, inv);
   uint32_t p0 = pack_elems<ELEM>(x[0], x[1]), p1 = pack_elems<ELEM>(x[2], x[3]);
@@ -296,8 +315,7 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
   }
 #pragma unroll
   for (int m = 0; m < 8; m++) {
-    const uint32_t a[4] = {scale_pair<ELEM>(v[m].x, inv), scale_pair<ELEM>(v[m].z, inv), scale_pair<ELEM>(v[m].y, inv),
-                           scale_pair<ELEM>(v[m].w, inv)};
+    const uint32_t a[4] = {v[m].x, v[m].z, v[m].y, v[m].w};
     mma_elem<ELEM>(s.o[m], a, b0, b1);
     if (ELEM == DKV_BF16) mma_elem<ELEM>(s.o[m], a, r0, r1);
   }
@@ -565,6 +583,7 @@ __global__ void __launch_bounds__(kA8Warps * 32)
   uint32_t qf[16];
   const uint8_t* q_at = nullptr;
   float qs[2] = {1.0f, 1.0f};
+  bool mixed = false;                  // the unit may have tiles of codes
   int unit = -1, N = 0, ustart = 0, uend = 0, last_start = -1;
 #pragma unroll 1
   for (int k = 0; w0 < w1; k++) {
@@ -646,6 +665,7 @@ __global__ void __launch_bounds__(kA8Warps * 32)
         ustart = last_start = __shfl_sync(0xffffffffu, cur.start, from);
         unit = r * hkv + h;
         N = s_len[r];
+        mixed = N >= c.T;
         uend = ustart + tiles_of(N, c.T, a.window, a.sinks).count;
         s.clear();
         q_at = a.q + r * a.qs + (size_t)h * G * (2 * kD);
@@ -667,11 +687,11 @@ __global__ void __launch_bounds__(kA8Warps * 32)
           return wait();
         };
         if (ELEM == DKV_F16) {
-          tail_tile<ELEM>(s, qf, p, after_k, see, kLogitScale);
+          tail_tile<ELEM>(s, qf, p, after_k, edge, see, mixed, kLogitScale);
         } else {
           uint32_t raw[16];    // the other tiles' fragments are scaled
           load_q<ELEM>(q_at, G, lane, raw);
-          tail_tile<ELEM>(s, raw, p, after_k, see, kLogitScale);
+          tail_tile<ELEM>(s, raw, p, after_k, edge, see, mixed, kLogitScale);
         }
       }
       __syncwarp();
