@@ -203,8 +203,10 @@ __device__ __forceinline__ void put_v(uint16_t* buf, int i, int f0, uint4 v) {
 
 // One token per request, a block per request and KV head: 16 threads turn a row
 // (K, V, then the G query heads) of 8 features each, so that every row's load is
-// in flight at once. The call is bound by its chain of dependent loads (request,
-// angles; tail and page where a block is complete), not by bytes.
+// in flight at once. The call is bound by its launch and its chain of dependent
+// loads (request, angles; tail and page where a block is complete), not by
+// bytes: one request 2.1 us, 128 with 28 / 4 heads 5.8 us (7.5 with a row after
+// the other).
 constexpr int kStepThreads = 160;     // 16 x (2 + G) at most
 template <int ELEM, int CODE>
 __global__ void __launch_bounds__(kStepThreads) k_append8_step(Cache8View c, Append8Args a, int n_req) {

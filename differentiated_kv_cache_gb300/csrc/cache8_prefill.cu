@@ -7,8 +7,9 @@
 // the group, so one K / V tile serves the whole group twice and a half spans few
 // positions (keys that only part of its rows see stay few). Persistent CTAs, one
 // an SM; warp 0 issues the TMA copies (an item's queries, 128-key K and V tiles
-// through two stages each), warps 1 and 2 the MMAs of a half each, warps 4..7 and 8..11 run the softmax
-// of the halves with one thread per row (and most of the registers):
+// through two stages each), warps 1 and 2 the MMAs of a half each, warps 4..7
+// and 8..11 run the softmax of the halves with one thread per row (and most of
+// the registers):
 //   S = Q K^T        tcgen05, D in tensor memory, 64 keys a step, two buffers
 //   P = 2^(S - m)    written over S in 16 bits; m is a maximum of earlier keys,
 //                    raised (O, l rescaled) only when a row's P of a step sum
@@ -22,9 +23,22 @@
 // for P V and the next S in turn: 4900 cycles for 128 keys instead of 3100.)
 // Only key tiles with a visible key are visited, the window's from the diagonal
 // back (the nearest keys give a good first m), then the first tokens'; of each,
-// a half takes the 32-key parts that some of its rows may see. Every wait is bounded; on expiry
-// the kernel latches DKV_ERR_TIMEOUT, waits (bounded) for its own copies and
-// MMAs, frees its tensor memory and returns.
+// a half takes the 32-key parts that some of its rows may see.
+//
+// Bound by the tensor cores: 32 prompts of 4096 tokens, 32 / 8 heads, window
+// 1024 take 1.78 ms (1.93 TFLOP, 55% of the measured bf16 burst rate; the steps
+// at the window's edges and the diagonal add 18% to the products), 16384 tokens
+// with 64 / 8 heads and window 4096 take 1.46 ms (68%). In a step of 64 keys the
+// products of both halves take about 1400 of 1650 cycles; S has N = 64, for
+// which the queries are read from shared memory again (48 instead of 32 cycles
+// an MMA), the price of the second S buffer. With one thread in the MMA warps'
+// loop, whose operands then are no uniform registers, an MMA took 100 cycles to
+// issue (2.25 ms); results written by warps of their own left the softmax too
+// few registers (2.25 ms); queries fetched per half, the second half started a
+// step late: no difference.
+//
+// Every wait is bounded; on expiry the kernel latches DKV_ERR_TIMEOUT, waits
+// (bounded) for its own copies and MMAs, frees its tensor memory and returns.
 #include <algorithm>
 #include <cudaTypedefs.h>
 
@@ -265,7 +279,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   } else if (warp < 3) {
     // ---- MMAs of a half: S of step n once P V of step n - 1 is done, then P V ----
     // The whole warp walks the steps, one lane issues: operands stay in uniform
-    // registers (with one lane in the loop an MMA took 100 cycles to issue).
+    // registers.
     {
       constexpr uint32_t type = ELEM == DKV_BF16 ? (1u << 7) | (1u << 10) : 0u;   // A and B formats
       constexpr uint32_t id_pv = umma_idesc_f16(128, 128) | type | (1u << 16);   // B (V) MN-major
