@@ -37,6 +37,11 @@
 // few registers (2.25 ms); queries fetched per half, the second half started a
 // step late: no difference.
 //
+// 0 * Inf is not 0: an infinite or NaN value makes NaN of every row of its step,
+// those that do not see it too. A second kernel computes rows that came out so
+// again, one by one over the keys that they see (in this kernel the code for it
+// cost 3%, though it never ran, and a look at V ahead of the products 5%).
+//
 // Every wait is bounded; on expiry the kernel latches DKV_ERR_TIMEOUT, waits
 // (bounded) for its own copies and MMAs, frees its tensor memory and returns.
 #include <algorithm>
@@ -172,6 +177,17 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 
 // bits [0, n)
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+// acc + 0 * x: NaN from the first infinite or NaN value on.
+template <int ELEM>
+__device__ __forceinline__ void find_not_finite(uint32_t (&acc)[4], uint4 x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if (ELEM == DKV_F16) asm("fma.rn.f16x2 %0, %1, %2, %0;\n" : "+r"(acc[i]) : "r"(w[i]), "r"(0u));
+    else asm("fma.rn.bf16x2 %0, %1, %2, %0;\n" : "+r"(acc[i]) : "r"(w[i]), "r"(0u));
+  }
+}
+
 // Values of a tensor-memory load are used after the wait only.
 __device__ __forceinline__ void loaded32(float* v) {
 #pragma unroll
@@ -471,6 +487,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       const unsigned long long dst = real ? reinterpret_cast<unsigned long long>(a.out) +
           (((size_t)(it.t0 + pos) * c.hkv + it.h) * G + row % G) * (2 * kD) : 0ull;
       uint8_t* stage = smem + kW8OffOut + (warp - 4) * 4096;
+      uint32_t bad[4] = {0, 0, 0, 0};
 #pragma unroll 1
       for (int q = 0; q < 2; q++) {
 #pragma unroll
@@ -480,12 +497,14 @@ __global__ void __launch_bounds__(kW8Threads, 1)
           tmem_wait_ld();
           loaded32(o);
 #pragma unroll
-          for (int e = 0; e < 4; e++)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * r + e) ^ (lane & 7)) << 4)) =
-                make_uint4(pack_elems<ELEM>(o[8 * e] * inv, o[8 * e + 1] * inv),
-                           pack_elems<ELEM>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                           pack_elems<ELEM>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                           pack_elems<ELEM>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          for (int e = 0; e < 4; e++) {
+            const uint4 w = make_uint4(pack_elems<ELEM>(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                       pack_elems<ELEM>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                       pack_elems<ELEM>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                       pack_elems<ELEM>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            find_not_finite<ELEM>(bad, w);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * r + e) ^ (lane & 7)) << 4)) = w;
+          }
         }
         __syncwarp();
 #pragma unroll
@@ -497,6 +516,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         }
         __syncwarp();
       }
+      if (real && ((bad[0] | bad[1] | bad[2] | bad[3]) & 0x7fff7fffu)) c.status[2] = 1;
       tc_fence_before();
     }
     if (!ok) fail();
@@ -507,6 +527,78 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tbase, kW8Cols);
+  }
+}
+
+// Rows that came out infinite or NaN in this call (or, while status[2] is on, may
+// have): a warp each, four features a lane, from the definition, over the keys
+// that the row sees, the nearest first, until what it sees has left none of its
+// doubtful features finite. Other features stay as they are. A quarter of the SMs:
+// the launch that finds nothing adds 1.6 us to a call, four blocks an SM 2.8.
+struct Again8 {
+  uint8_t* out;
+  const uint8_t *q, *k, *v;
+  long long qs, ks, vs;      // row strides in bytes
+  int window, sinks;
+};
+template <int ELEM>
+__global__ void __launch_bounds__(512) k_prefill8_again(Cache8View c, Again8 a, const __grid_constant__ W8Call call) {
+  pdl_launch_dependents();
+  pdl_wait();
+  if (c.stopped() || *(volatile int*)(c.status + 2) == 0) return;
+  const int lane = threadIdx.x & 31, hq = c.hkv * c.G;
+  const long long rows = (long long)call.tok0[call.n_req] * hq, step = (long long)gridDim.x * (blockDim.x / 32);
+  auto finite = [](float x) { return fabsf(x) < INFINITY; };
+  auto four = [](const uint8_t* p, float (&x)[4]) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    x[0] = lo_elem<ELEM>(w.x);
+    x[1] = hi_elem<ELEM>(w.x);
+    x[2] = lo_elem<ELEM>(w.y);
+    x[3] = hi_elem<ELEM>(w.y);
+  };
+  for (long long r = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += step) {
+    uint8_t* out = a.out + r * (2 * kD) + 8 * lane;
+    float was[4];
+    four(out, was);
+    bool doubt[4], any = false;
+#pragma unroll
+    for (int e = 0; e < 4; e++) any |= doubt[e] = !finite(was[e]);
+    if (!__any_sync(0xffffffffu, any)) continue;
+    const int tok = (int)(r / hq), head = (int)(r - (long long)tok * hq);
+    int i = 0;
+    for (int end = call.n_req; end - i > 1;) {
+      const int mid = (i + end) >> 1;
+      if (call.tok0[mid] <= tok) i = mid; else end = mid;
+    }
+    const int t0 = call.tok0[i], pos = tok - t0, lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+    const int early = a.window > 0 ? min(a.sinks, lo) : 0;
+    const uint8_t* k = a.k + t0 * a.ks + (head / c.G) * (2 * kD) + 8 * lane;
+    const uint8_t* v = a.v + t0 * a.vs + (head / c.G) * (2 * kD) + 8 * lane;
+    float q[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
+    four(a.q + tok * a.qs + head * (2 * kD) + 8 * lane, q);
+    for (int j = pos; j >= 0; j = j == lo ? early - 1 : j - 1) {
+      float y[4], z[4];
+      four(k + j * a.ks, y);
+      four(v + j * a.vs, z);
+      float x = fmaf(q[3], y[3], fmaf(q[2], y[2], fmaf(q[1], y[1], q[0] * y[0])));
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+      x *= kLogitScale;
+      const float mn = fmaxf(m, x), f = m == mn ? 1.0f : fast_exp2(m - mn), p = fast_exp2(x - mn);
+      m = mn;
+      l = fmaf(l, f, p);
+      bool open = false;
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        o[e] = fmaf(p, z[e], o[e] * f);
+        open |= doubt[e] && finite(o[e]);
+      }
+      if (!finite(l) || !__any_sync(0xffffffffu, open)) break;
+    }
+    const float inv = __fdiv_rn(1.0f, l);
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (doubt[e]) reinterpret_cast<uint16_t*>(out)[e] = float_elem<ELEM>(o[e] * inv);
   }
 }
 
@@ -550,8 +642,13 @@ cudaError_t launch_prefill8(const Cache8View& c, int elem, const int32_t* seq_le
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
   if (e != cudaSuccess) return e;
   const int grid = std::min(call.tile0[n_req] * c.hkv, sm_count);
-  return launch_dependent(kernel, dim3(grid), dim3(kW8Threads), kW8Smem, st, c, mq, mk,
-                          mv, W8Args{static_cast<uint8_t*>(out), window, sinks, tq}, call);
+  e = launch_dependent(kernel, dim3(grid), dim3(kW8Threads), kW8Smem, st, c, mq, mk, mv,
+                       W8Args{static_cast<uint8_t*>(out), window, sinks, tq}, call);
+  if (e != cudaSuccess) return e;
+  const Again8 again{static_cast<uint8_t*>(out),       static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(k),
+                     static_cast<const uint8_t*>(v), 2 * qs, 2 * ks, 2 * vs, window, sinks};
+  return launch_dependent(elem == DKV_F16 ? k_prefill8_again<DKV_F16> : k_prefill8_again<DKV_BF16>, dim3(std::max(1, sm_count / 4)),
+                          dim3(512), 0, st, c, again, call);
 }
 
 }  // namespace dkv

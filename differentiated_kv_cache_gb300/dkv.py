@@ -330,7 +330,7 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
     c.rotary_dim, c.rotary_interleaved = rotary_dim, int(bool(rotary_interleaved))
     c.device = pages.device.index if pages.device.index is not None else 0
     if status is None:
-        status = torch.zeros(2, dtype=torch.int32, device=pages.device)
+        status = torch.zeros(4, dtype=torch.int32, device=pages.device)
     if workspace is None:
         n = C.c_int64()
         _check(load().dkv_cache8_workspace(C.byref(c), min(c.n_slots, 1024) if max_req is None else int(max_req),
@@ -339,10 +339,10 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
     c.pages, c.scales = _on(c, pages, None, "pages"), _on(c, scales, torch.float32, "scales")
     c.tail, c.page_table = _on(c, tail, None, "tail"), _on(c, page_table, torch.int32, "page_table")
     c.status, c.workspace = _on(c, status, torch.int32, "status"), _on(c, workspace, torch.uint8, "workspace")
-    if status.numel() < 2:
-        raise ValueError("status has two words")
+    if status.numel() < 4:
+        raise ValueError("status has four words")
     c.workspace_bytes = workspace.numel()
-    c.elem_dtype, c.status_words = tail.dtype, status
+    c.elem_dtype, c.status_words = tail.dtype, status[:2]     # error and its request
     # plain copies of what every call reads
     c.address, c.dev, c.heads, c.q_heads, c.pairs = C.addressof(c), c.device, hkv, hkv * group_size, rotary_dim // 2
     c.tensors = (pages, scales, tail, page_table, status, workspace)

@@ -437,7 +437,7 @@ int dkv_pool_export(dkv_pool* pool, dkv_snapshot* out);
  *    table_width * T), DKV_ERR_CHECK (a page number outside [0, n_pages)),
  *    DKV_ERR_TIMEOUT. No bad index is followed. The call that latches an
  *    error leaves its outputs undefined; while status[0] is non-zero, later
- *    calls are device no-ops. The caller zeroes both words to go on.
+ *    calls are device no-ops. The caller zeroes the words to go on.
  *  - Calls on one cache must be ordered on one stream (or synchronised by the
  *    caller). Attention calls that may overlap (two streams, two replayed
  *    graphs) need a workspace each; others may share one if n_kv_heads and
@@ -466,7 +466,7 @@ typedef struct dkv_cache8 {
   float* scales;               /* [n_pages][Hkv][2]: K's and V's s             */
   void* tail;                  /* [n_slots][Hkv][T/16][2][2048] elem_type      */
   const int32_t* page_table;   /* [n_slots][table_width]                       */
-  int32_t* status;             /* [2], zeroed by the caller                    */
+  int32_t* status;             /* [4], zeroed by the caller                    */
   void* workspace;             /* dkv_cache8_workspace bytes, zeroed once by
                                   the caller (every call leaves the zeros
                                   that it found); NULL if no attention         */
@@ -527,9 +527,10 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
  *            apart (multiples of 8); out contiguous, of elem_type, apart from
  *            them.
  * Products accumulate in fp32; probabilities enter the value product rounded
- * to elem_type. Values of other requests never enter a result; inside one
- * request k and v must be finite (a non-finite v reaches the rows before it
- * that share its 128-token tile).
+ * to elem_type. What a row does not see never enters its result, whatever it
+ * holds: rows that come out infinite or NaN are computed again by themselves,
+ * and status[2] goes on; while it is on, every call looks through its whole
+ * result for such rows (until the caller zeroes it).
  * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED (host, nothing queued);
  * DKV_ERR_CUDA. */
 int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* seq_lens, const void* q,

@@ -482,6 +482,65 @@ def test_prefill_requests_do_not_touch_each_other():
         prefill_case(1, 7, [100, 77, 150], BF16, 40, 3, seed=bad, bad=bad)
 
 
+@pytest.mark.parametrize("elem", [F16, BF16])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3), (130, 70)])
+def test_prefill_of_values_that_are_not_finite(elem, window, sinks):
+    """Infinite and NaN keys and values reach the rows that see them, feature by
+    feature, and no other."""
+    rng = np.random.default_rng(window)
+    lens, G, hkv = [210, 333, 70], 3, 2
+    c = Cache(hkv, G, 16, 1, 1, elem, E4M3)
+    n = sum(lens)
+    q, k, v = c.vec(rng, n, hkv * G), c.vec(rng, n, hkv), c.vec(rng, n, hkv)
+    clean = [x.double().cpu().numpy() for x in (q, k, v)]
+    v[5, 0, 17] = float("inf")                 # a first token
+    v[100, 0, 3], v[101, 1, 3] = float("-inf"), float("nan")
+    v[210 + 64, :, 100] = float("nan")
+    v[210 + 200, 1] = float("inf")
+    k[210 + 300, 0, 9] = float("nan")
+    bad = [x.double().cpu().numpy() for x in (q, k, v)]
+    out = torch.full_like(q, 7.0)
+    _dkv().dkv_cache8_prefill(c.c, lens, q, k, v, out, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert c.c.status_words.tolist() == [0, 0]
+    got, at = out.double().cpu().numpy(), 0
+    for m in lens:
+        for p in range(m):
+            see = at + ref.visible(p + 1, window, sinks)
+            for h in range(hkv):
+                g = slice(h * G, (h + 1) * G)
+                want, pv, qk, vm = ref.attend(clean[0][at + p, g], clean[1][see, h], clean[2][see, h])
+                tol = ref.tolerance(want, pv, qk, vm, len(see), elem, torch.finfo(elem).eps / 2)
+                vb, kb = bad[2][see, h], bad[1][see, h]
+                hit = ~np.isfinite(vb).all(axis=0) | ~np.isfinite(kb).all()
+                x = got[at + p, g]
+                assert not np.isfinite(x[:, hit]).any(), (p, h)
+                assert (np.abs(x - want) <= tol)[:, ~hit].all(), (p, h)
+        at += m
+
+
+def test_prefill_after_values_that_are_not_finite():
+    """While status[2] is on, finite results stay bit for bit; no error latches."""
+    rng = np.random.default_rng(1)
+    c = Cache(2, 4, 16, 1, 1, BF16, E4M3)
+    q, k, v = c.vec(rng, 500, 8), c.vec(rng, 500, 2), c.vec(rng, 500, 2)
+    a, b, d = (torch.empty_like(q) for _ in range(3))
+    _dkv().dkv_cache8_prefill(c.c, [400, 100], q, k, v, a, window=50, sinks=1)
+    torch.cuda.synchronize()
+    words = c.c.tensors[4]
+    assert words.tolist() == [0, 0, 0, 0]
+    bad = v.clone()
+    bad[77] = float("inf")
+    _dkv().dkv_cache8_prefill(c.c, [400, 100], q, k, bad, b, window=50, sinks=1)
+    torch.cuda.synchronize()
+    assert words.tolist() == [0, 0, 1, 0]
+    sees = torch.zeros(500, dtype=torch.bool, device="cuda")
+    sees[77:77 + 50] = True
+    assert not torch.isfinite(b[sees].float()).any() and torch.isfinite(b[~sees].float()).all()
+    _dkv().dkv_cache8_prefill(c.c, [400, 100], q, k, v, d, window=50, sinks=1)
+    assert torch.equal(a, d)
+
+
 def test_prefill_parts_of_one_projection():
     rng = np.random.default_rng(3)
     c = Cache(2, 4, 16, 1, 1, F16, E4M3)
