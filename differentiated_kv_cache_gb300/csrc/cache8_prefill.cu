@@ -26,9 +26,9 @@
 // a half takes the 32-key parts that some of its rows may see.
 //
 // Bound by the tensor cores: 32 prompts of 4096 tokens, 32 / 8 heads, window
-// 1024 take 1.78 ms (1.93 TFLOP, 55% of the measured bf16 burst rate; the steps
+// 1024 take 1.80 ms (1.93 TFLOP, 55% of the measured bf16 burst rate; the steps
 // at the window's edges and the diagonal add 18% to the products), 16384 tokens
-// with 64 / 8 heads and window 4096 take 1.46 ms (68%). In a step of 64 keys the
+// with 64 / 8 heads and window 4096 take 1.47 ms (68%). In a step of 64 keys the
 // products of both halves take about 1400 of 1650 cycles; S has N = 64, for
 // which the queries are read from shared memory again (48 instead of 32 cycles
 // an MMA), the price of the second S buffer. With one thread in the MMA warps'

@@ -328,7 +328,9 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
     c.elem_type, c.code_type = elems[tail.dtype], codes[pages.dtype]
     c.n_pages, c.n_slots, c.table_width = n_pages, tail.shape[0], page_table.shape[1]
     c.rotary_dim, c.rotary_interleaved = rotary_dim, int(bool(rotary_interleaved))
-    c.device = pages.device.index if pages.device.index is not None else 0
+    c.device = c.dev = pages.get_device()
+    if c.dev < 0:
+        raise TypeError("the cache's tensors must be CUDA tensors")
     if status is None:
         status = torch.zeros(4, dtype=torch.int32, device=pages.device)
     if workspace is None:
@@ -336,29 +338,28 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
         _check(load().dkv_cache8_workspace(C.byref(c), min(c.n_slots, 1024) if max_req is None else int(max_req),
                                            C.byref(n)), "dkv_cache8_workspace")
         workspace = torch.zeros(n.value, dtype=torch.uint8, device=pages.device)
-    c.pages, c.scales = _on(c, pages, None, "pages"), _on(c, scales, torch.float32, "scales")
-    c.tail, c.page_table = _on(c, tail, None, "tail"), _on(c, page_table, torch.int32, "page_table")
+    c.pages, c.scales = _on(c, pages, pages.dtype, "pages"), _on(c, scales, torch.float32, "scales")
+    c.tail, c.page_table = _on(c, tail, tail.dtype, "tail"), _on(c, page_table, torch.int32, "page_table")
     c.status, c.workspace = _on(c, status, torch.int32, "status"), _on(c, workspace, torch.uint8, "workspace")
     if status.numel() < 4:
         raise ValueError("status has four words")
     c.workspace_bytes = workspace.numel()
     c.elem_dtype, c.status_words = tail.dtype, status[:2]     # error and its request
     # plain copies of what every call reads
-    c.address, c.dev, c.heads, c.q_heads, c.pairs = C.addressof(c), c.device, hkv, hkv * group_size, rotary_dim // 2
+    c.address, c.heads, c.q_heads, c.pairs = C.addressof(c), hkv, hkv * group_size, rotary_dim // 2
     c.tensors = (pages, scales, tail, page_table, status, workspace)
     return c
 
 
-def _on(cache, t, dtype, name):
-    """Address of a contiguous tensor on the cache's device (None -> NULL)."""
+def _on(cache, t, dtype, name, n=None):
+    """Address of a contiguous tensor (of n elements) on the cache's device
+    (None -> NULL)."""
     if t is None:
         return None
-    if t.get_device() != cache.device:
-        raise TypeError(f"{name} must be a CUDA tensor on device {cache.device}")
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.dtype is not dtype or t.get_device() != cache.dev:
+        raise TypeError(f"{name} must be a {dtype} tensor on device {cache.dev}, got {t.dtype} on {t.device}")
+    if not t.is_contiguous() or n is not None and t.numel() != n:
+        raise ValueError(f"{name} must be contiguous" + (f" and have {n} elements" if n is not None else ""))
     return t.data_ptr()
 
 
@@ -396,17 +397,17 @@ def dkv_cache8_append(cache: dkv_cache8, before, k, v, rope=None, n_new=None, sl
     kp, ks = _rows(cache, k, cache.heads, total, "k")
     vp, vs = _rows(cache, v, cache.heads, total, "v")
     qp, qs = (None, 0) if q is None else _rows(cache, q, cache.q_heads, total, "q")
-    if k_rot is not None and k_rot.shape != k.shape or q_rot is not None and (q is None or q_rot.shape != q.shape):
-        raise ValueError("k_rot and q_rot must be shaped like k and q")
-    if slots is not None and slots.numel() != n_req:
-        raise ValueError("slots and before have one entry per request")
-    if rope is not None and rope.shape[1:] != (cache.pairs, 2):
-        raise ValueError(f"rope must be [positions][{cache.pairs}][2]")
+    positions = 0
+    if rope is not None:
+        positions, pairs, two = rope.shape
+        if pairs != cache.pairs or two != 2:
+            raise ValueError(f"rope must be [positions][{cache.pairs}][2]")
+    elem, heads = cache.elem_dtype, 128 * total
     rc = load().dkv_cache8_append(
-        cache.address, n_req, None if lens is None else lens.ctypes.data, _on(cache, slots, i32, "slots"),
+        cache.address, n_req, None if lens is None else lens.ctypes.data, _on(cache, slots, i32, "slots", n_req),
         _on(cache, before, i32, "before"), kp, ks, vp, vs, qp, qs, _on(cache, rope, torch.float32, "rope"),
-        0 if rope is None else rope.shape[0], _on(cache, k_rot, cache.elem_dtype, "k_rot"),
-        _on(cache, q_rot, cache.elem_dtype, "q_rot"), _stream8(cache, stream))
+        positions, _on(cache, k_rot, elem, "k_rot", heads * cache.heads),
+        _on(cache, q_rot, elem, "q_rot", heads * cache.q_heads), _stream8(cache, stream))
     return _check(rc, "dkv_cache8_append") if check else rc
 
 
@@ -418,13 +419,9 @@ def dkv_cache8_attention(cache: dkv_cache8, seq_lens, q, out, window: int = 0, s
     import torch
     n_req = seq_lens.numel()
     qp, qs = _rows(cache, q, cache.q_heads, n_req, "q")
-    if out.shape != q.shape:
-        raise ValueError("out must be shaped like q")
-    if slots is not None and slots.numel() != n_req:
-        raise ValueError("slots and seq_lens have one entry per request")
-    rc = load().dkv_cache8_attention(cache.address, n_req, _on(cache, slots, torch.int32, "slots"),
+    rc = load().dkv_cache8_attention(cache.address, n_req, _on(cache, slots, torch.int32, "slots", n_req),
                                      _on(cache, seq_lens, torch.int32, "seq_lens"), qp, qs,
-                                     _on(cache, out, cache.elem_dtype, "out"), window, sinks,
+                                     _on(cache, out, cache.elem_dtype, "out", n_req * cache.q_heads * 128), window, sinks,
                                      _stream8(cache, stream))
     return _check(rc, "dkv_cache8_attention") if check else rc
 
@@ -438,8 +435,7 @@ def dkv_cache8_prefill(cache: dkv_cache8, seq_lens, q, k, v, out, window: int = 
     qp, qs = _rows(cache, q, cache.q_heads, total, "q")
     kp, ks = _rows(cache, k, cache.heads, total, "k")
     vp, vs = _rows(cache, v, cache.heads, total, "v")
-    if out.shape != q.shape:
-        raise ValueError("out must be shaped like q")
     rc = load().dkv_cache8_prefill(cache.address, lens.size, lens.ctypes.data, qp, qs, kp, ks, vp, vs,
-                                   _on(cache, out, cache.elem_dtype, "out"), window, sinks, _stream8(cache, stream))
+                                   _on(cache, out, cache.elem_dtype, "out", total * cache.q_heads * 128), window, sinks,
+                                   _stream8(cache, stream))
     return _check(rc, "dkv_cache8_prefill") if check else rc
