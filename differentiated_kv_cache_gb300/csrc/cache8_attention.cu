@@ -497,6 +497,7 @@ __global__ void __launch_bounds__(kA8Warps * 32)
 
   // ---- lengths, and the prefix sums of the requests' tiles over all heads ----
   int carry = 0;
+  bool stopped = false;
   for (int base = 0; base < a.n_req; base += blockDim.x) {
     const int i = base + threadIdx.x;
     int n = 0, cost = 0, slot = i;
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(kA8Warps * 32)
       n = a.seq_lens[i];
       if (a.slots) slot = a.slots[i];
     }
-    if (base == 0 && c.stopped()) return;       // its load is in flight with theirs
+    if (base == 0) stopped = c.stopped();       // its load is in flight with theirs
     if (i < a.n_req) {
       n = max(n, 0);
       int err = 0;
@@ -543,6 +544,24 @@ __global__ void __launch_bounds__(kA8Warps * 32)
   const int lo = start_of(blockIdx.x), hi = start_of(blockIdx.x + 1);
   const int w0 = lo + (int)((unsigned)(hi - lo) * warp / kA8Warps);
   const int w1 = lo + (int)((unsigned)(hi - lo) * (warp + 1) / kA8Warps);
+  auto cta_of = [&](int x) { return (int)((((long long)x + 1) * ctas - 1) / total); };
+  if (stopped) {
+    // The error may be one of this call, and CTAs that began before it count on
+    // this one's arrival for the units that cross its ends: that is all it does.
+    if (warp < 2 && total > 0 && lane < G) {
+      const int pos = warp ? hi - 1 : lo;
+      int r = 0, end = a.n_req;
+      while (end - r > 1) {
+        const int mid = (r + end) >> 1;
+        if (s_pre[mid] <= pos) r = mid; else end = mid;
+      }
+      const int n = tiles_of(s_len[r], c.T, a.window, a.sinks).count, h = (pos - s_pre[r]) / n;
+      const int us = s_pre[r] + h * n, ue = us + n;
+      if (warp ? us >= lo && ue > hi : us < lo)
+        atomicInc(a.count + ((size_t)r * hkv + h) * G + lane, (unsigned)(cta_of(ue - 1) - cta_of(us)));
+    }
+    return;
+  }
   const int per = __ffs(c.T / kSub) - 1;     // log2 of the tiles of a block
 
   // ---- the warp's tiles, 32 descriptors at a time, a lane each ----
@@ -758,7 +777,6 @@ __global__ void __launch_bounds__(kA8Warps * 32)
       }
     }
     if (whole) continue;
-    auto cta_of = [&](int x) { return (int)((((long long)x + 1) * ctas - 1) / total); };
     const int c0 = cta_of(us), c1 = cta_of(ue - 1);
     __threadfence();
     __syncwarp();

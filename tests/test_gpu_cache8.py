@@ -760,6 +760,44 @@ def test_shared_workspace_of_two_layers():
         assert torch.equal(c.attend(slots, lens, q), want[0]) and torch.equal(d.attend(slots, lens, q2), want[1])
 
 
+def test_workspace_after_a_call_that_latched_an_error():
+    """Blocks of a call may begin long apart beside another stream's work: those
+    that find an error of their own call already latched still leave the
+    workspace as the next call needs it."""
+    dkv = _dkv()
+    lens = [700, 3000, 1500, 2300]
+    c, slots, q = filled(4, 4, 64, F16, E4M3, lens, seed=2)
+    apart = dkv.make_cache8(c.pages, c.scales, c.tail, c.table, group_size=4)
+    rng = np.random.default_rng(3)
+    # one prompt whose blocks hold their multiprocessors for very different times
+    p = Cache(1, 8, 64, 1, 1, F16, E4M3)
+    pq, pk, pv = (p.vec(rng, 4500, n) for n in (8, 1, 1))
+    pout, out = torch.empty_like(pq), torch.empty_like(q)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    sl, ln = i32(slots), i32(lens)
+    side = torch.cuda.Stream()
+    good = c.table.clone()
+    # arrivals lie behind the partial results, two a multiprocessor
+    count = c.c.tensors[5][torch.cuda.get_device_properties(0).multi_processor_count * 2 * (4 * 128 + 16) * 4:]
+    assert count.numel() >= 16 * len(lens) * 4
+    for bad in (0, 1, 2, 3) * 5:
+        c.table.copy_(good)
+        c.table[slots[bad], 0] = -1
+        torch.cuda.synchronize()
+        dkv.dkv_cache8_prefill(p.c, [4500], pq, pk, pv, pout, stream=side)
+        dkv.dkv_cache8_attention(c.c, ln, q, out, slots=sl)
+        torch.cuda.synchronize()
+        assert c.c.status_words.tolist() == [dkv.DKV_ERR_CHECK, bad]
+        assert not count.any()
+        c.table.copy_(good)
+        q = c.vec(rng, len(lens), 16)
+        want = torch.empty_like(q)
+        dkv.dkv_cache8_attention(apart, ln, q, want, slots=sl)
+        c.attend(slots, lens, q)          # stopped
+        c.c.status_words.zero_()
+        assert torch.equal(c.attend(slots, lens, q), want) and c.c.status_words.tolist() == [0, 0]
+
+
 def test_other_streams_and_workspaces():
     """Two caches on two streams at once, and one cache read by two streams with a
     workspace each."""
