@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kA8Warps * 32)
     if (i < a.n_req) {
       n = max(n, 0);
       int err = 0;
-      if ((unsigned)slot >= (unsigned)c.n_slots) err = DKV_ERR_ARG;
+      if (n > 0 && (unsigned)slot >= (unsigned)c.n_slots) err = DKV_ERR_ARG;
       else if ((long long)n > (long long)c.width * c.T) err = DKV_ERR_TABLE_FULL;
       if (err) {
         c.latch(err, i);

@@ -429,7 +429,8 @@ int dkv_pool_export(dkv_pool* pool, dkv_snapshot* out);
  *    reads its operands with 16-byte loads and no transposition).
  *  - slots, before and seq_lens are device arrays, read when the work runs: a
  *    captured call can be replayed with other contents. A request with
- *    before < 0 is skipped (padding); slots of one append must differ.
+ *    before < 0 is skipped (padding; its slot may be any number); the other
+ *    slots of one append must differ.
  *  - Errors that only the device sees latch in status[0] (the first one;
  *    status[1] = the request's index in the call): DKV_ERR_ARG (a slot
  *    outside [0, n_slots), a slot given twice to an append, a position
@@ -507,8 +508,8 @@ int dkv_cache8_append(const dkv_cache8* cache, int32_t n_req, const int32_t* n_n
  * over the visible tokens j < N: every one if window = 0, else the last
  * `window` and the first `sinks` (j >= N - window or j < sinks). k^, v^ are
  * the stored values (codes times scale in pages, 16 bits in the tail). A
- * request with N <= 0 gets zeros. Tokens that are not visible are not read
- * into the result, whatever they hold.
+ * request with N <= 0 (padding; its slot may be any number) gets zeros. Tokens
+ * that are not visible are not read into the result, whatever they hold.
  *   q       device [n_req][Hkv * G][128], rows q_stride elements apart.
  *   out     device [n_req][Hkv * G][128] of elem_type, contiguous, apart from q.
  * The call is split over the GPU by the lengths that it finds on the device;

@@ -760,6 +760,25 @@ def test_shared_workspace_of_two_layers():
         assert torch.equal(c.attend(slots, lens, q), want[0]) and torch.equal(d.attend(slots, lens, q2), want[1])
 
 
+def test_padding_rows_with_any_slot():
+    dkv = _dkv()
+    lens = [70, 0, 33, -5, 16]
+    c, slots, q = filled(2, 4, 16, F16, E4M3, [70, 1, 33, 1, 16], seed=6)
+    for any_slot in (-1, 5, 2 ** 31 - 1, -2 ** 31):
+        who = [s if n > 0 else any_slot for s, n in zip(slots, lens)]
+        out = c.attend(who, lens, q)
+        c.check_attention(out, slots, lens, q)
+        assert (out[1] == 0).all() and (out[3] == 0).all()
+        rng = np.random.default_rng(4)
+        k, v = c.vec(rng, 5, 2), c.vec(rng, 5, 2)
+        tail = c.tail.clone()
+        i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+        for n_new in (None, [1] * 5):
+            dkv.dkv_cache8_append(c.c, i32([-1] * 5), k, v, n_new=n_new, slots=i32([any_slot] * 5))
+        torch.cuda.synchronize()
+        assert torch.equal(c.tail.view(torch.int16), tail.view(torch.int16)) and c.c.status_words.tolist() == [0, 0]
+
+
 def test_workspace_after_a_call_that_latched_an_error():
     """Blocks of a call may begin long apart beside another stream's work: those
     that find an error of their own call already latched still leave the
