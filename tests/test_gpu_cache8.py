@@ -760,6 +760,42 @@ def test_shared_workspace_of_two_layers():
         assert torch.equal(c.attend(slots, lens, q), want[0]) and torch.equal(d.attend(slots, lens, q2), want[1])
 
 
+def test_offsets_beyond_32_bits():
+    """Pages, slots and rows behind the first 4 GB give what near ones give."""
+    dkv = _dkv()
+    hkv, G, T, lens = 2, 4, 64, [200, 64, 130]
+    rng = np.random.default_rng(9)
+    near = Cache(hkv, G, T, 3, 4, F16, E4M3)
+    n_pages, n_slots = 2 ** 33 // (hkv * T * 256) + 1, 2 ** 33 // (hkv * T * 512) + 1
+    pages = torch.empty((n_pages, hkv, T // 16, 2, 2048), dtype=E4M3, device="cuda")
+    tail = torch.empty((n_slots, hkv, T // 16, 2, 2048), dtype=F16, device="cuda")
+    scales = torch.empty((n_pages, hkv, 2), device="cuda")
+    table = torch.zeros((n_slots, 4), dtype=torch.int32, device="cuda")
+    slots = torch.tensor([n_slots - 1, n_slots // 2 + 1, n_slots - 7], dtype=torch.int32, device="cuda")
+    table[slots.long()] = torch.arange(n_pages - 12, n_pages, dtype=torch.int32, device="cuda").reshape(3, 4)
+    far = dkv.make_cache8(pages, scales, tail, table, group_size=G)
+    total = sum(lens)
+    wide = 2 ** 32 // total // 8 * 8 + 8          # rows lie over 8 GB
+    space = torch.empty((total, wide), dtype=F16, device="cuda")
+    q, k, v = near.vec(rng, total, hkv * G), near.vec(rng, total, hkv), near.vec(rng, total, hkv)
+    rows = []
+    for i, x in enumerate((q, k, v)):
+        y = space[:, 2048 * i:2048 * i + x.shape[1] * 128].view(total, x.shape[1], 128)
+        y.copy_(x)
+        rows.append(y)
+    zero, ln = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = []
+    for c, sl, (a, b, d) in ((near.c, None, (q, k, v)), (far, slots, rows)):
+        kr, qr, out, dec = torch.empty_like(k), torch.empty_like(q), torch.empty_like(q), torch.empty_like(q[:3])
+        dkv.dkv_cache8_append(c, zero, b, d, n_new=lens, slots=sl, q=a, k_rot=kr, q_rot=qr)
+        dkv.dkv_cache8_prefill(c, lens, a, b, d, out, window=100, sinks=4)
+        dkv.dkv_cache8_attention(c, ln, a[-3:], dec, slots=sl)
+        assert c.status_words.tolist() == [0, 0]
+        got.append((kr, qr, out, dec))
+    for x, y in zip(*got):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
+
+
 def test_padding_rows_with_any_slot():
     dkv = _dkv()
     lens = [70, 0, 33, -5, 16]
