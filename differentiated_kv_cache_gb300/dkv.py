@@ -375,6 +375,19 @@ def _rows(cache, t, heads, n, name):
     return t.data_ptr(), row if n > 1 else heads * 128
 
 
+def _lens8(x):
+    """Host lengths as a C array: the array (its owner keeps it alive), its
+    address, entries and sum. A list of ints is converted without numpy."""
+    if type(x) is list:
+        try:
+            a = (C.c_int32 * len(x))(*x)
+            return a, C.addressof(a), len(x), sum(x)
+        except TypeError:
+            pass
+    a = _i32(x)
+    return a, a.ctypes.data, a.size, int(a.sum(dtype=np.int64))
+
+
 def _stream8(cache, stream):
     import torch
     return torch._C._cuda_getCurrentRawStream(cache.dev) if stream is None else stream.cuda_stream
@@ -390,9 +403,8 @@ def dkv_cache8_append(cache: dkv_cache8, before, k, v, rope=None, n_new=None, sl
     n_req, i32 = before.numel(), torch.int32
     lens, total = None, n_req
     if n_new is not None:
-        lens = _i32(n_new)
-        total = int(lens.sum(dtype=np.int64))
-        if lens.size != n_req:
+        keep, lens, size, total = _lens8(n_new)
+        if size != n_req:
             raise ValueError("n_new and before have one entry per request")
     kp, ks = _rows(cache, k, cache.heads, total, "k")
     vp, vs = _rows(cache, v, cache.heads, total, "v")
@@ -404,7 +416,7 @@ def dkv_cache8_append(cache: dkv_cache8, before, k, v, rope=None, n_new=None, sl
             raise ValueError(f"rope must be [positions][{cache.pairs}][2]")
     elem, heads = cache.elem_dtype, 128 * total
     rc = load().dkv_cache8_append(
-        cache.address, n_req, None if lens is None else lens.ctypes.data, _on(cache, slots, i32, "slots", n_req),
+        cache.address, n_req, lens, _on(cache, slots, i32, "slots", n_req),
         _on(cache, before, i32, "before"), kp, ks, vp, vs, qp, qs, _on(cache, rope, torch.float32, "rope"),
         positions, _on(cache, k_rot, elem, "k_rot", heads * cache.heads),
         _on(cache, q_rot, elem, "q_rot", heads * cache.q_heads), _stream8(cache, stream))
@@ -430,12 +442,11 @@ def dkv_cache8_prefill(cache: dkv_cache8, seq_lens, q, k, v, out, window: int = 
                        check: bool = True) -> int:
     """Causal attention over whole prompts (host lengths, requests back to
     back) with an optional sliding window and first tokens that stay visible."""
-    lens = _i32(seq_lens)
-    total = int(lens.sum(dtype=np.int64))
+    keep, lens, n_req, total = _lens8(seq_lens)
     qp, qs = _rows(cache, q, cache.q_heads, total, "q")
     kp, ks = _rows(cache, k, cache.heads, total, "k")
     vp, vs = _rows(cache, v, cache.heads, total, "v")
-    rc = load().dkv_cache8_prefill(cache.address, lens.size, lens.ctypes.data, qp, qs, kp, ks, vp, vs,
+    rc = load().dkv_cache8_prefill(cache.address, n_req, lens, qp, qs, kp, ks, vp, vs,
                                    _on(cache, out, cache.elem_dtype, "out", total * cache.q_heads * 128), window, sinks,
                                    _stream8(cache, stream))
     return _check(rc, "dkv_cache8_prefill") if check else rc

@@ -148,3 +148,10 @@ def test_bad_workspace_requests_are_refused():
     for r in (0, -1, 1025):
         refused(dkv.load().dkv_cache8_workspace(C.byref(cache()), r, C.byref(n)))
     refused(dkv.load().dkv_cache8_workspace(C.byref(cache()), 4, None))
+
+
+@pytest.mark.parametrize("given", [[3, 1, 40], (3, 1, 40), np.array([3, 1, 40]), np.array([3, 1, 40], np.int32)[::1],
+                                   np.array([3, 9, 1, 9, 40, 9], np.int32)[::2], [np.int64(3), 1, np.int32(40)], [3.0, 1, 40]])
+def test_host_lengths(given):
+    keep, address, n, total = dkv.dkv._lens8(given)
+    assert (n, total) == (3, 44) and list((C.c_int32 * 3).from_address(address)) == [3, 1, 40]
