@@ -760,6 +760,15 @@ def test_shared_workspace_of_two_layers():
         assert torch.equal(c.attend(slots, lens, q), want[0]) and torch.equal(d.attend(slots, lens, q2), want[1])
 
 
+@pytest.mark.parametrize("lens", [[40000], [13000, 30001], [24576, 50, 25000]])
+def test_unit_over_more_than_32_blocks_of_the_grid(lens):
+    c, slots, q = filled(1, 3, 64, BF16, E4M3, lens, seed=3)
+    out = c.attend(slots, lens, q)
+    c.check_attention(out, slots, lens, q)
+    out = c.attend(slots, lens, q, 30000, 5)
+    c.check_attention(out, slots, lens, q, 30000, 5)
+
+
 def test_offsets_beyond_32_bits():
     """Pages, slots and rows behind the first 4 GB give what near ones give."""
     dkv = _dkv()
