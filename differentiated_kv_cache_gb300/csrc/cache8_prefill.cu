@@ -5,8 +5,11 @@
 // A work item is 256 query rows of one request and KV head in two halves of
 // 128: row r of a half is token r / G of its floor(128 / G), query head r % G of
 // the group, so one K / V tile serves the whole group twice and a half spans few
-// positions (keys that only part of its rows see stay few). Persistent CTAs, one
-// an SM; warp 0 issues the TMA copies (an item's queries, 128-key K and V tiles
+// positions (keys that only part of its rows see stay few). The grid has a CTA an
+// item; one is on each SM, and when it comes to its item it asks for one whose
+// CTA has not begun (clusterlaunchcontrol), the latest rows first: items differ
+// much in their keys (8 x 4096 tokens with 56 / 8 heads 1.57 ms, dealt out in turn
+// 1.80; one prompt of 8192 0.41 and 0.46). warp 0 issues the TMA copies (an item's queries, 128-key K and V tiles
 // through two stages each), warps 1 and 2 the MMAs of a half each, warps 4..7
 // and 8..11 run the softmax of the halves with one thread per row (and most of
 // the registers):
@@ -26,9 +29,9 @@
 // a half takes the 32-key parts that some of its rows may see.
 //
 // Bound by the tensor cores: 32 prompts of 4096 tokens, 32 / 8 heads, window
-// 1024 take 1.80 ms (1.93 TFLOP, 55% of the measured bf16 burst rate; the steps
+// 1024 take 1.77 ms (1.93 TFLOP, 56% of the measured bf16 burst rate; the steps
 // at the window's edges and the diagonal add 18% to the products), 16384 tokens
-// with 64 / 8 heads and window 4096 take 1.47 ms (68%). In a step of 64 keys the
+// with 64 / 8 heads and window 4096 take 1.45 ms (69%). In a step of 64 keys the
 // products of both halves take about 1400 of 1650 cycles; S has N = 64, for
 // which the queries are read from shared memory again (48 instead of 32 cycles
 // an MMA), the price of the second S buffer. With one thread in the MMA warps'
@@ -67,7 +70,9 @@ constexpr int kW8OffK = 2 * kW8Tile;       // after the queries of both halves
 constexpr int kW8OffV = kW8OffK + 2 * kW8Tile;
 constexpr int kW8OffOut = kW8OffV + 2 * kW8Tile;      // 4 KB a softmax warp, to write whole lines
 constexpr int kW8OffBar = kW8OffOut + 8 * 4096;
-constexpr int kW8Smem = 1024 + kW8OffBar + 256;
+constexpr int kW8Next = 8;                 // places of the ring of items
+constexpr int kW8OffNext = kW8OffBar + 256;           // their barriers, then the answers of 16 bytes
+constexpr int kW8Smem = 1024 + kW8OffNext + 24 * kW8Next;
 constexpr uint32_t kW8OCol = 256;          // S of the halves, then O of the halves
 constexpr uint32_t kW8Cols = 512;
 constexpr float kW8Most = 4096.0f;         // largest sum of a row's P of one tile (fp16 holds 65504)
@@ -164,6 +169,26 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {     /
       : "memory");
   return ok != 0;
 }
+// A block of the grid that has not begun yet is asked for, so that this one does
+// its work; the answer (16 bytes) completes the barrier.
+__device__ __forceinline__ void ask_item(uint32_t answer, uint32_t bar) {
+  mbar_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(answer),
+               "r"(bar)
+               : "memory");
+}
+// The block's index, -1 if every block has begun (then none may be asked for again).
+__device__ __forceinline__ int told_item(uint32_t answer) {
+  int x;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 h;\n ld.shared.b128 h, [%1];\n mov.s32 %0, -1;\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n}\n"
+      : "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
+}
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
@@ -201,7 +226,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   pdl_launch_dependents();
   pdl_wait();
   if (c.stopped()) return;
-  const int items = call.tile0[call.n_req] * c.hkv, G = c.G;
+  const int G = c.G;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kW8OffBar);
@@ -218,6 +243,16 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   auto sdone = [&](int h, int n) { return b0 + 80u + 32u * h + 8u * (n & 3); };
   auto pvdone = [&](int h, int n) { return b0 + 144u + 32u * h + 8u * (n & 3); };
   auto drain = [&](int h) { return b0 + 208u + 8u * h; };
+  // Item r + 1 of this CTA (item 0 is its own block): place r & 7. Its index is
+  // asked for when item r begins, whose first K tile waits for S of the tile
+  // two before; every warp has then read the indices up to item r - 3, so a
+  // place is free long before it is used again.
+  auto told = [&](int r) { return b0 + 256u + 8u * (r & (kW8Next - 1)); };
+  auto answer = [&](int r) { return b0 + 256u + 8u * kW8Next + 16u * (r & (kW8Next - 1)); };
+  auto item_told = [&](int r, bool& ok) {      // the same for every lane
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(told(r), (r / kW8Next) & 1));
+    return ok ? told_item(answer(r)) : -1;
+  };
   uint32_t* s_taddr = reinterpret_cast<uint32_t*>(bars + 28);
   int* s_fail = reinterpret_cast<int*>(s_taddr + 1);
   // (broadcasts: uniform over a warp for the compiler too)
@@ -225,6 +260,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 28; s++)      // pfull: a lane of each warp
       mbar_init(b0 + 8u * s, s >= 6 && s < 10 ? 4 : 1);
+    for (int r = 0; r < kW8Next; r++) mbar_init(told(r), 1);
     *s_fail = 0;
     fence_mbar_init();
   }
@@ -270,7 +306,11 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         }
         return true;
       };
-      for (int x = blockIdx.x; ok && x < items && !failed(); x += gridDim.x) {
+      int asked = 0;
+      for (int x = blockIdx.x; x >= 0 && !failed();) {
+        fence_proxy_async();
+        ask_item(answer(asked), told(asked));
+        asked++;
         const Item it = item_of(x, c, a, call);
         const int last = done - 1;     // the last step of the item before
         ok = load(it, 0, true);
@@ -285,9 +325,14 @@ __global__ void __launch_bounds__(kW8Threads, 1)
           if (j + 1 < it.count) ok = load(it, j + 1, true);
           if (ok) ok = load(it, j, false);
         }
+        if (!ok) break;
+        ok = mbar_wait_bounded(told(asked - 1), ((asked - 1) / kW8Next) & 1);
+        if (!ok) break;
+        x = told_item(answer(asked - 1));
       }
       if (!ok) fail();
-      // no copy of this CTA may still be in flight when it exits
+      // no copy of this CTA, and no answer, may still be in flight when it exits
+      if (asked > 0) mbar_wait_bounded(told(asked - 1), ((asked - 1) / kW8Next) & 1);
       if (nq > 0) mbar_wait_bounded(qfull, (nq - 1) & 1);
       for (int t = max(nk - 2, 0); t < nk; t++) mbar_wait_bounded(kfull(t & 1), (t >> 1) & 1);
       for (int t = max(nv - 2, 0); t < nv; t++) mbar_wait_bounded(vfull(t & 1), (t >> 1) & 1);
@@ -306,7 +351,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       Cursor sc{0, 0, 0, 0}, pc{0, 0, 0, 0};     // steps of S and, two behind, of P V
       int ii = 0;
       bool ok = true;
-      for (int x = blockIdx.x; ok && x < items; x += gridDim.x, ii++) {
+      for (int x = blockIdx.x, next = -1; x >= 0; x = ok ? next : -1, ii++) {
         const Item it = item_of(x, c, a, call);
         sc.begin(it);
         pc.begin(it);
@@ -351,6 +396,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
             }
             __syncwarp();
             more_s = sc.next(it);
+            if (!more_s) next = item_told(ii, ok);     // while its P is awaited
           }
         }
       }
@@ -370,9 +416,13 @@ __global__ void __launch_bounds__(kW8Threads, 1)
     const uint32_t ts = tl + half * 128, to = tl + kW8OCol + half * 128;
     Cursor cu{0, 0, 0, 0};
     bool ok = true;
-    for (int x = blockIdx.x; ok && x < items; x += gridDim.x) {
-      const Item it = item_of(x, c, a, call);
+    int ii = 0;
+    Item it = item_of(blockIdx.x, c, a, call);
+    for (int next = 0; next >= 0; ii++) {
       const int q0 = it.p0 + half * a.tq, q1 = max(min(q0 + a.tq, it.n0) - 1, q0), pos = q0 + token;
+      // rows behind the request, or of no token, hold what happened to be there:
+      // they take no part in what the warp decides
+      const bool real = token < a.tq && pos < it.n0;
       float m = -INFINITY, l = 0.0f;
       cu.begin(it);
       bool first = true, more = true, have = false, raise = true;
@@ -478,11 +528,13 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull(half, n));
       }
+      // the next item, while P V of the last step is awaited
+      next = ok ? item_told(ii, ok) : -1;
+      const Item then = next >= 0 ? item_of(next, c, a, call) : it;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone(half, cu.n - 1), ((cu.n - 1) >> 2) & 1));
       if (!ok) break;
       tc_fence_after();
       const float inv = __fdiv_rn(1.0f, l);
-      const bool real = token < a.tq && pos < it.n0;
       // through shared memory, 64 features at a time: eight lanes write a line
       const unsigned long long dst = real ? reinterpret_cast<unsigned long long>(a.out) +
           (((size_t)(it.t0 + pos) * c.hkv + it.h) * G + row % G) * (2 * kD) : 0ull;
@@ -517,6 +569,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         __syncwarp();
       }
       if (real && ((bad[0] | bad[1] | bad[2] | bad[3]) & 0x7fff7fffu)) c.status[2] = 1;
+      it = then;
       tc_fence_before();
     }
     if (!ok) fail();
@@ -641,8 +694,7 @@ cudaError_t launch_prefill8(const Cache8View& c, int elem, const int32_t* seq_le
   auto kernel = elem == DKV_F16 ? k_prefill8<DKV_F16> : k_prefill8<DKV_BF16>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8Smem);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(call.tile0[n_req] * c.hkv, sm_count);
-  e = launch_dependent(kernel, dim3(grid), dim3(kW8Threads), kW8Smem, st, c, mq, mk, mv,
+  e = launch_dependent(kernel, dim3(call.tile0[n_req] * c.hkv), dim3(kW8Threads), kW8Smem, st, c, mq, mk, mv,
                        W8Args{static_cast<uint8_t*>(out), window, sinks, tq}, call);
   if (e != cudaSuccess) return e;
   const Again8 again{static_cast<uint8_t*>(out),       static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(k),
