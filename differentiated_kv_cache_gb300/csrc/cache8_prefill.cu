@@ -8,7 +8,7 @@
 // positions (keys that only part of its rows see stay few). The grid has a CTA an
 // item; one is on each SM, and when it comes to its item it asks for one whose
 // CTA has not begun (clusterlaunchcontrol), the latest rows first: items differ
-// much in their keys (8 x 4096 tokens with 56 / 8 heads 1.57 ms, dealt out in turn
+// much in their keys (8 x 4096 tokens with 56 / 8 heads 1.51 ms, dealt out in turn
 // 1.80; one prompt of 8192 0.41 and 0.46). warp 0 issues the TMA copies (an item's queries, 128-key K and V tiles
 // through two stages each), warps 1 and 2 the MMAs of a half each, warps 4..7
 // and 8..11 run the softmax of the halves with one thread per row (and most of
@@ -29,9 +29,9 @@
 // a half takes the 32-key parts that some of its rows may see.
 //
 // Bound by the tensor cores: 32 prompts of 4096 tokens, 32 / 8 heads, window
-// 1024 take 1.77 ms (1.93 TFLOP, 56% of the measured bf16 burst rate; the steps
+// 1024 take 1.76 ms (1.93 TFLOP, 56% of the measured bf16 burst rate; the steps
 // at the window's edges and the diagonal add 18% to the products), 16384 tokens
-// with 64 / 8 heads and window 4096 take 1.45 ms (69%). In a step of 64 keys the
+// with 64 / 8 heads and window 4096 take 1.44 ms (69%). In a step of 64 keys the
 // products of both halves take about 1400 of 1650 cycles; S has N = 64, for
 // which the queries are read from shared memory again (48 instead of 32 cycles
 // an MMA), the price of the second S buffer. With one thread in the MMA warps'
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
               tmem_wait_st();
             }
             m = mn;
-            raise = __any_sync(0xffffffffu, m == -INFINITY);     // a row that has seen no key so far
+            raise = __any_sync(0xffffffffu, real && m == -INFINITY);     // a row that has seen no key so far
           }
           const float mr = m == -INFINITY ? 0.0f : m;
           const uint64_t sc2 = f32x2(kLogitScale, kLogitScale), nm2 = f32x2(-mr, -mr);
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
           }
           const uint64_t t2 = add_f32x2(add_f32x2(l2[0], l2[1]), add_f32x2(l2[2], l2[3]));
           sum = __uint_as_float((uint32_t)t2) + __uint_as_float((uint32_t)(t2 >> 32));
-          if (again || !__any_sync(0xffffffffu, !(sum <= kW8Most))) break;
+          if (again || !__any_sync(0xffffffffu, real && !(sum <= kW8Most))) break;
         }
         if (!ok) break;
         l += sum;

@@ -528,10 +528,11 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
  *            apart (multiples of 8); out contiguous, of elem_type, apart from
  *            them.
  * Products accumulate in fp32; probabilities enter the value product rounded
- * to elem_type. What a row does not see never enters its result, whatever it
- * holds: rows that come out infinite or NaN are computed again by themselves,
- * and status[2] goes on; while it is on, every call looks through its whole
- * result for such rows (until the caller zeroes it).
+ * to elem_type; the same inputs give the same bits, whatever else is in the
+ * call. What a row does not see never enters its result, whatever it holds:
+ * rows that come out infinite or NaN are computed again by themselves, and
+ * status[2] goes on; while it is on, every call looks through its whole result
+ * for such rows (until the caller zeroes it).
  * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED (host, nothing queued);
  * DKV_ERR_CUDA. */
 int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* seq_lens, const void* q,

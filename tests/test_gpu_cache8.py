@@ -862,6 +862,42 @@ def test_workspace_after_a_call_that_latched_an_error():
         assert torch.equal(c.attend(slots, lens, q), want) and c.c.status_words.tolist() == [0, 0]
 
 
+def test_prompt_attention_of_two_streams_at_once():
+    """Blocks share their items out as they come free: whoever takes which, beside
+    whatever else runs, alone and replayed, the results are the same bits."""
+    dkv = _dkv()
+    rng = np.random.default_rng(12)
+    cases = []
+    for hkv, G, elem, window, sinks in ((4, 4, F16, 0, 0), (2, 7, BF16, 300, 5)):
+        c = Cache(hkv, G, 16, 1, 1, elem, E4M3)
+        lens = [int(x) for x in rng.integers(1, 3000, 12)] + [64, 1]
+        q, k, v = (c.vec(rng, sum(lens), n) for n in (hkv * G, hkv, hkv))
+        want = torch.full_like(q, float("nan"))
+        dkv.dkv_cache8_prefill(c.c, lens, q, k, v, want, window=window, sinks=sinks)
+        assert torch.isfinite(want).all()
+        cases.append((c, lens, q, k, v, want, window, sinks))
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.full_like(x[5], float("nan")) for _ in range(6)] for x in cases]
+    graphs = []
+    torch.cuda.synchronize()
+    for x, s, o in zip(cases, streams, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            dkv.dkv_cache8_prefill(x[0].c, *x[1:5], o[0], window=x[6], sinks=x[7])
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for i in range(1, 6):
+        for x, s, o, g in zip(cases, streams, outs, graphs):
+            dkv.dkv_cache8_prefill(x[0].c, *x[1:5], o[i], window=x[6], sinks=x[7], stream=s)
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for x, o in zip(cases, outs):
+        assert x[0].c.status_words.tolist() == [0, 0]
+        for y in o:
+            assert torch.equal(y, x[5])
+
+
 def test_other_streams_and_workspaces():
     """Two caches on two streams at once, and one cache read by two streams with a
     workspace each."""
