@@ -125,35 +125,44 @@ __device__ void check_slots(const Cache8View& c, const Append8Args& a, int n_req
 // Quantise a complete block of one head from its 16-bit entries (tile order)
 // in shared memory and write codes and scales. All threads of the block.
 template <int ELEM, int CODE>
-__device__ void quantise_block(const Cache8View& c, const uint16_t* buf, int page, int h, float* red) {
+__device__ void quantise_block(const Cache8View& c, const uint16_t* buf, int page, int h, uint32_t* red) {
   const int nt = blockDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = nt >> 5;
   const int per = c.T * kD;      // entries of one operand
-  float m[2] = {0.0f, 0.0f};
-  for (int x = 8 * threadIdx.x; x < 2 * per; x += 8 * nt) {
-    const uint4 w = *reinterpret_cast<const uint4*>(buf + x);
-    const int o = (x / kTile) & 1;
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-    float mm = 0.0f;
+  // magnitudes order like their bits: packed maxima of every value, and again of
+  // the finite ones only where the first pass finds that some are not
+  constexpr uint32_t kInf = ELEM == DKV_F16 ? 0x7c00u : 0x7f80u;
+  uint32_t top[2];
+#pragma unroll 1
+  for (bool all = true;; all = false) {
+    uint32_t m[2] = {0, 0};
+    for (int x = 8 * threadIdx.x; x < 2 * per; x += 8 * nt) {
+      const uint4 w = *reinterpret_cast<const uint4*>(buf + x);
+      const int o = (x / kTile) & 1;
+      uint32_t v[4] = {w.x & 0x7fff7fffu, w.y & 0x7fff7fffu, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu};
+      if (!all) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) mm = amax_finite(amax_finite(mm, lo_elem<ELEM>(v[i])), hi_elem<ELEM>(v[i]));
-    m[0] = o == 0 ? fmaxf(m[0], mm) : m[0];
-    m[1] = o == 1 ? fmaxf(m[1], mm) : m[1];
-  }
+        for (int i = 0; i < 4; i++) v[i] &= ~__vcmpgeu2(v[i], kInf << 16 | kInf);
+      }
+      const uint32_t mm = __vmaxu2(__vmaxu2(v[0], v[1]), __vmaxu2(v[2], v[3]));
+      if (o == 0) m[0] = __vmaxu2(m[0], mm);
+      else m[1] = __vmaxu2(m[1], mm);
+    }
 #pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) {
-    m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], s));
-    m[1] = fmaxf(m[1], __shfl_xor_sync(0xffffffffu, m[1], s));
+    for (int o = 0; o < 2; o++) {
+      const uint32_t r = __reduce_max_sync(0xffffffffu, max(m[o] & 0xffffu, m[o] >> 16));
+      if (lane == 0) red[32 * o + warp] = r;
+    }
+    __syncthreads();
+    top[0] = top[1] = 0;
+    for (int w = 0; w < nw; w++) {
+      top[0] = max(top[0], red[w]);
+      top[1] = max(top[1], red[32 + w]);
+    }
+    if (!all || max(top[0], top[1]) < kInf) break;
+    __syncthreads();
   }
-  if (lane == 0) {
-    red[warp] = m[0];
-    red[32 + warp] = m[1];
-  }
-  __syncthreads();
-  for (int w = 0; w < nw; w++) {
-    m[0] = fmaxf(m[0], red[w]);
-    m[1] = fmaxf(m[1], red[32 + w]);
-  }
-  const float s0 = block_scale(m[0], CODE), s1 = block_scale(m[1], CODE);
+  const float s0 = block_scale(elem_float<ELEM>((uint16_t)top[0]), CODE);
+  const float s1 = block_scale(elem_float<ELEM>((uint16_t)top[1]), CODE);
   const float i0 = __fdiv_rn(1.0f, s0), i1 = __fdiv_rn(1.0f, s1);
   if (threadIdx.x == 0) {
     float* sc = c.scales + 2 * ((size_t)page * c.hkv + h);
@@ -267,7 +276,7 @@ __global__ void __launch_bounds__(kStepThreads) k_append8_step(Cache8View c, App
   }
   if (full) {
     __syncthreads();
-    quantise_block<ELEM, CODE>(c, buf, page, h, reinterpret_cast<float*>(sm + (size_t)T * 4 * kD));
+    quantise_block<ELEM, CODE>(c, buf, page, h, reinterpret_cast<uint32_t*>(sm + (size_t)T * 4 * kD));
   }
 }
 
@@ -373,7 +382,7 @@ __global__ void __launch_bounds__(512, 2)
     }
     if (full) {
       __syncthreads();
-      quantise_block<ELEM, CODE>(c, buf, page, h, reinterpret_cast<float*>(sm + (size_t)T * 4 * kD));
+      quantise_block<ELEM, CODE>(c, buf, page, h, reinterpret_cast<uint32_t*>(sm + (size_t)T * 4 * kD));
     }
     if (!both || b != first) return;
     b = open;
