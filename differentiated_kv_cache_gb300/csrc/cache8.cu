@@ -2,6 +2,7 @@
 // (include/dkv.h) and the append kernels: rotation of keys and queries,
 // 16-bit tails, quantisation of completed blocks.
 #include <algorithm>
+#include <type_traits>
 
 #include "cache8.cuh"
 #include "dkv_kernels.cuh"
@@ -132,8 +133,9 @@ __device__ void quantise_block(const Cache8View& c, const uint16_t* buf, int pag
   // the finite ones only where the first pass finds that some are not
   constexpr uint32_t kInf = ELEM == DKV_F16 ? 0x7c00u : 0x7f80u;
   uint32_t top[2];
+  bool all = true;
 #pragma unroll 1
-  for (bool all = true;; all = false) {
+  for (;; all = false) {
     uint32_t m[2] = {0, 0};
     for (int x = 8 * threadIdx.x; x < 2 * per; x += 8 * nt) {
       const uint4 w = *reinterpret_cast<const uint4*>(buf + x);
@@ -171,21 +173,30 @@ __device__ void quantise_block(const Cache8View& c, const uint16_t* buf, int pag
   }
   uint8_t* dst = c.pages + c.page_head(page, h);
   // 16 codes a thread: m-steps 2j and 2j + 1 of one lane's operands
-  for (int g = threadIdx.x; g < 2 * per / 16; g += nt) {
-    const int tile = g >> 7, j = (g >> 5) & 3, l = g & 31;
-    const float inv = tile & 1 ? i1 : i0;
-    const uint16_t* src = buf + tile * kTile + 512 * j + 8 * l;
-    uint32_t r[4];
+  auto encode = [&](auto finite) {
+    constexpr bool FINITE = decltype(finite)::value;
+    for (int g = threadIdx.x; g < 2 * per / 16; g += nt) {
+      const int tile = g >> 7, j = (g >> 5) & 3, l = g & 31;
+      const float inv = tile & 1 ? i1 : i0;
+      const uint16_t* src = buf + tile * kTile + 512 * j + 8 * l;
+      uint32_t r[4];
 #pragma unroll
-    for (int e = 0; e < 2; e++) {
-      const uint4 w = *reinterpret_cast<const uint4*>(src + 256 * e);
-      r[2 * e] = code_pair<CODE>(lo_elem<ELEM>(w.x), hi_elem<ELEM>(w.x), inv) |
-                 code_pair<CODE>(lo_elem<ELEM>(w.y), hi_elem<ELEM>(w.y), inv) << 16;
-      r[2 * e + 1] = code_pair<CODE>(lo_elem<ELEM>(w.z), hi_elem<ELEM>(w.z), inv) |
-                     code_pair<CODE>(lo_elem<ELEM>(w.w), hi_elem<ELEM>(w.w), inv) << 16;
+      for (int e = 0; e < 2; e++) {
+        const uint4 w = *reinterpret_cast<const uint4*>(src + 256 * e);
+        const uint32_t x = code_pair<CODE, FINITE>(lo_elem<ELEM>(w.x), hi_elem<ELEM>(w.x), inv);
+        const uint32_t y = code_pair<CODE, FINITE>(lo_elem<ELEM>(w.y), hi_elem<ELEM>(w.y), inv);
+        const uint32_t z = code_pair<CODE, FINITE>(lo_elem<ELEM>(w.z), hi_elem<ELEM>(w.z), inv);
+        const uint32_t u = code_pair<CODE, FINITE>(lo_elem<ELEM>(w.w), hi_elem<ELEM>(w.w), inv);
+        r[2 * e] = FINITE ? prmt(x, y, 0x5410u) : x | y << 16;
+        r[2 * e + 1] = FINITE ? prmt(z, u, 0x5410u) : z | u << 16;
+      }
+      *reinterpret_cast<uint4*>(dst + tile * kTile + 512 * j + 16 * l) = make_uint4(r[0], r[1], r[2], r[3]);
     }
-    *reinterpret_cast<uint4*>(dst + tile * kTile + 512 * j + 16 * l) = make_uint4(r[0], r[1], r[2], r[3]);
-  }
+  };
+  // integers of finite values need no conversion instruction: 16 x 4096 tokens
+  // with 8 / 8 heads 176 us, 196 with
+  if (CODE == DKV_INT8 && all) encode(std::true_type());
+  else encode(std::false_type());
 }
 
 // Entries of one token's quad: K (rows = tokens) or V (columns = tokens) of a
@@ -214,7 +225,7 @@ __device__ __forceinline__ void put_v(uint16_t* buf, int i, int f0, uint4 v) {
 // (K, V, then the G query heads) of 8 features each, so that every row's load is
 // in flight at once. The call is bound by its launch and its chain of dependent
 // loads (request, angles; tail and page where a block is complete), not by
-// bytes: one request 2.1 us, 128 with 28 / 4 heads 5.8 us (7.5 with a row after
+// bytes: one request 2.1 us, 128 with 28 / 4 heads 5.2 us (7.5 with a row after
 // the other).
 constexpr int kStepThreads = 160;     // 16 x (2 + G) at most
 template <int ELEM, int CODE>
@@ -283,11 +294,13 @@ __global__ void __launch_bounds__(kStepThreads) k_append8_step(Cache8View c, App
 // One block of one KV head: a job takes the call's tokens that fall into it. The
 // block's 16-bit entries gather in shared memory if this call completes it, else
 // the new ones go to the tail. The G query heads of the KV head turn with the
-// same angles. Bound by bytes: 32 x 4096 tokens (3.22 GB) take 490 us, 97% of
+// same angles. Bound by bytes: 32 x 4096 tokens (3.22 GB) take 479 us, 99% of
 // the measured copy rate, with 4 T threads and the loads of K, V and four query
 // rows in flight together (8 T threads: 786 us, two blocks an SM do not cover
 // each other's barriers; 2 T threads: 635 us). Half of the query heads in a block of
-// their own: 555 us, and 143 us instead of 126 us for ragged pieces in blocks of 128.
+// their own: 555 us instead of 490, and 143 us instead of 126 us for ragged pieces
+// in blocks of 128; V's neighbouring tokens exchanged to store pairs: 531 us
+// instead of 479 (spills).
 template <int ELEM, int CODE>
 __global__ void __launch_bounds__(512, 2)
     k_append8(Cache8View c, Append8Args a, int n_req, const __grid_constant__ AppendCall call) {

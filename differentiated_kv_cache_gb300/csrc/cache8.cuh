@@ -80,8 +80,10 @@ __device__ __forceinline__ float block_scale(float amax, int code_type) {
   return fmaxf(__fmul_rn(amax, code_type == DKV_E4M3 ? 1.0f / 448.0f : 1.0f / 127.0f), kScaleFloor);
 }
 
-// Codes of two values (the first in the lower byte).
-template <int CODE>
+// Codes of two values (the first in the lower byte; FINITE leaves the upper half
+// undefined). FINITE: neither is infinite or NaN, and |x inv| exceeds Q by a
+// rounding at most.
+template <int CODE, bool FINITE>
 __device__ __forceinline__ uint32_t code_pair(float a, float b, float inv) {
   a = __fmul_rn(a, inv);
   b = __fmul_rn(b, inv);
@@ -89,6 +91,10 @@ __device__ __forceinline__ uint32_t code_pair(float a, float b, float inv) {
     uint16_t r;   // round to nearest even, saturating; NaN stays NaN
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(b), "f"(a));
     return r;
+  }
+  if (FINITE) {   // the sum's ulp is 1: rounds to nearest even, the low byte is the code
+    const float big = 12582912.0f;
+    return prmt(__float_as_uint(__fadd_rn(a, big)), __float_as_uint(__fadd_rn(b, big)), 0x0040u);
   }
   // NaN gives 0
   const int x = a == a ? (int)rintf(fminf(fmaxf(a, -127.0f), 127.0f)) : 0;
