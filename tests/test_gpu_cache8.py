@@ -898,6 +898,33 @@ def test_prompt_attention_of_two_streams_at_once():
             assert torch.equal(y, x[5])
 
 
+def test_generation_on_a_stream_of_higher_priority_beside_prompts():
+    """Blocks of the prompt attention that cannot have another block's item (work of
+    higher priority waits) end; what they leave begins later."""
+    dkv = _dkv()
+    rng = np.random.default_rng(21)
+    lens = [900, 100, 1300, 5000]
+    d, slots, dq = filled(4, 4, 64, F16, E4M3, lens, seed=1)
+    dwant = d.attend(slots, lens, dq)
+    p = Cache(8, 4, 64, 1, 1, F16, E4M3)
+    prompts = [4000, 1500, 2500, 700]
+    q, k, v = (p.vec(rng, sum(prompts), n) for n in (32, 8, 8))
+    want = torch.empty_like(q)
+    dkv.dkv_cache8_prefill(p.c, prompts, q, k, v, want)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    sl, ln = i32(slots), i32(lens)
+    low, high = torch.cuda.Stream(priority=0), torch.cuda.Stream(priority=-1)
+    outs, douts = [torch.full_like(q, float("nan")) for _ in range(6)], [torch.empty_like(dq) for _ in range(200)]
+    torch.cuda.synchronize()
+    for o in outs:
+        dkv.dkv_cache8_prefill(p.c, prompts, q, k, v, o, stream=low)
+    for o in douts:
+        dkv.dkv_cache8_attention(d.c, ln, dq, o, slots=sl, stream=high)
+    torch.cuda.synchronize()
+    assert p.c.status_words.tolist() == [0, 0] and d.c.status_words.tolist() == [0, 0]
+    assert all(torch.equal(o, want) for o in outs) and all(torch.equal(o, dwant) for o in douts)
+
+
 def test_other_streams_and_workspaces():
     """Two caches on two streams at once, and one cache read by two streams with a
     workspace each."""
