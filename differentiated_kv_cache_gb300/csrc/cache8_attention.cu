@@ -26,14 +26,17 @@
 // mma.sync m16n8k16 (tokens / features on M, the G <= 8 queries on N; at most
 // 8 rows of queries cannot fill a tcgen05 tile, and the kernel is bound by
 // memory, not by matrix rate):
-//   x_j  = s_k (q . code_j) log2(e) / sqrt(128) + log2(s_v)
+//   y_j  = s_k (q . code_j) log2(e) / sqrt(128),   x_j = y_j + log2(s_v)
 //   w_j  = 2^(x_j - m)        the probability times V's scale, up to 2^-m
-//   O   += w_j code_j,   l += w_j / s_v,   out = O / l
-// so that one running maximum m serves both and blocks with different V
-// scales need no rescaling of O. m is raised (O, l rescaled) only when some
-// x_j exceeds it by more than 8: w stays below 2^8, in fp16's range. w enters
-// the second product rounded to fp16 (relative 2^-11, the size of the
-// output's own rounding); l sums the unrounded fp32 values.
+//   O   += w_j code_j,   l += 2^(y_j - u),   out = O 2^(m - u) / l
+// so that blocks with different V scales need no rescaling of O. m and u are
+// running maxima of x and y. Each sum has its own: s_v lies in 2^-100 .. 2^121,
+// and a block of zeros, which adds nothing to O, has its full weight in l beside
+// blocks of any size. They are raised (O, l rescaled) only when some x_j exceeds m
+// by more than 8 (w stays below 2^8, in fp16's range) or some y_j exceeds u by
+// more than 5 (2^(m - u) stays below 2^127). w enters the second product rounded
+// to fp16 (relative 2^-11, the size of the output's own rounding); l sums the
+// unrounded fp32 values.
 // Tiles of the 16-bit tail take s_k = s_v = 1 where there are no codes to mix
 // with; else s_v is the power of two that brings their largest |v| to
 // [128, 256), the size of codes, so that equal weights stand for equal
@@ -52,7 +55,7 @@ constexpr int kA8Stages = 2;        // ring entries of a warp
 constexpr int kA8Entry = 2 * kTile; // 4 KB: K and V codes of a tile, or K or V of a tail tile
 constexpr int kA8Row = kD + 4;      // floats of a query's row in a shared partial (no bank conflicts)
 constexpr int kA8Cta = 2 * kA8Warps;    // tiles that make a CTA worth its start
-constexpr float kA8Lazy = 8.0f;
+constexpr float kA8Lazy = 8.0f, kA8LazySum = 5.0f;     // how far x may pass m, y pass u
 
 struct Attn8Args {
   const int *slots, *seq_lens;
@@ -114,33 +117,38 @@ __device__ __forceinline__ void mma_elem(float* c, const uint32_t* a, uint32_t b
 // queries 2t, 2t + 1; O rows are features 16 m + g and 16 m + g + 8.
 struct State {
   float o[8][4];
-  float m[2], l[2];
+  float m[2], u[2], l[2];
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < 8; i++)
 #pragma unroll
       for (int e = 0; e < 4; e++) o[i][e] = 0.0f;
-    m[0] = m[1] = -INFINITY;
+    m[0] = m[1] = u[0] = u[1] = -INFINITY;
     l[0] = l[1] = 0.0f;
   }
 };
 
-// Raise the running maxima where some x exceeds them by more than the slack.
-// x: tokens g (x[0], x[1]) and g + 8 (x[2], x[3]) for the lane's two queries.
-__device__ __forceinline__ void raise(State& s, const float* x) {
+// Raise the running maxima where some x or y = x - lv exceeds them by more than
+// the slack. x: tokens g (x[0], x[1]) and g + 8 (x[2], x[3]) for the lane's two
+// queries.
+__device__ __forceinline__ void raise(State& s, const float* x, float lv) {
   float a = fmaxf(x[0], x[2]), b = fmaxf(x[1], x[3]);
-  if (!__any_sync(0xffffffffu, a > s.m[0] + kA8Lazy || b > s.m[1] + kA8Lazy)) return;
+  if (!__any_sync(0xffffffffu, a > fminf(s.m[0] + kA8Lazy, s.u[0] + (lv + kA8LazySum)) ||
+                                   b > fminf(s.m[1] + kA8Lazy, s.u[1] + (lv + kA8LazySum))))
+    return;
 #pragma unroll
   for (int d = 4; d <= 16; d <<= 1) {
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
     b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
   }
-  const float na = fmaxf(s.m[0], a), nb = fmaxf(s.m[1], b);
-  const float fa = na == -INFINITY ? 1.0f : fast_exp2(s.m[0] - na), fb = nb == -INFINITY ? 1.0f : fast_exp2(s.m[1] - nb);
-  s.m[0] = na;
-  s.m[1] = nb;
-  s.l[0] *= fa;
-  s.l[1] *= fb;
+  auto up = [](float& top, float x) {      // the factor of what was summed below the old maximum
+    const float old = top;
+    top = fmaxf(old, x);
+    return top == -INFINITY ? 1.0f : fast_exp2(old - top);
+  };
+  const float fa = up(s.m[0], a), fb = up(s.m[1], b);
+  s.l[0] *= up(s.u[0], a - lv);
+  s.l[1] *= up(s.u[1], b - lv);
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     s.o[i][0] *= fa;
@@ -150,15 +158,15 @@ __device__ __forceinline__ void raise(State& s, const float* x) {
   }
 }
 
-// w = 2^(x - m) in place of x, summed into l.
-__device__ __forceinline__ void weights(State& s, float* x, float inv) {
-  const float ma = s.m[0] == -INFINITY ? 0.0f : s.m[0], mb = s.m[1] == -INFINITY ? 0.0f : s.m[1];
-  x[0] = fast_exp2(x[0] - ma);
-  x[1] = fast_exp2(x[1] - mb);
-  x[2] = fast_exp2(x[2] - ma);
-  x[3] = fast_exp2(x[3] - mb);
-  s.l[0] = fmaf(x[0] + x[2], inv, s.l[0]);
-  s.l[1] = fmaf(x[1] + x[3], inv, s.l[1]);
+// w = 2^(x - m) in place of x, and 2^(x - lv - u) summed into l.
+__device__ __forceinline__ void weights(State& s, float* x, float lv) {
+#pragma unroll
+  for (int e = 0; e < 2; e++) {
+    const float m = s.m[e] == -INFINITY ? 0.0f : s.m[e], u = s.u[e] == -INFINITY ? 0.0f : s.u[e] + lv;
+    s.l[e] += fast_exp2(x[e] - u) + fast_exp2(x[e + 2] - u);
+    x[e] = fast_exp2(x[e] - m);
+    x[e + 2] = fast_exp2(x[e + 2] - m);
+  }
 }
 
 // Which tokens of a tile the query sees, for this lane: logits of tokens g and
@@ -221,8 +229,8 @@ __device__ __forceinline__ void code_tile(State& s, const uint32_t (&qf)[16], co
       vw[j].w &= see.v;
     }
   }
-  raise(s, x);
-  weights(s, x, fast_exp2(-lv));
+  raise(s, x, lv);
+  weights(s, x, lv);
   const uint32_t b0 = movmatrix_trans(pack_half2(x[0], x[1])), b1 = movmatrix_trans(pack_half2(x[2], x[3]));
 #pragma unroll
   for (int j = 0; j < 4; j++) {
@@ -291,7 +299,7 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
 #pragma unroll
     for (int e = 0; e < 4; e++) x[e] = (e < 2 ? see.lo : see.hi) ? x[e] : -INFINITY;
   }
-  float inv = 1.0f;
+  float lv = 0.0f;
   if (mixed) {
     uint32_t am2 = 0;        // magnitudes order like their bits
 #pragma unroll
@@ -302,9 +310,10 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
     // values leave 1
     const int low = ELEM == DKV_F16 ? -14 : -100, high = ELEM == DKV_F16 ? 14 : 100;
     const int ex = am < INFINITY ? max(low, min(high, (int)(__float_as_uint(am) >> 23) - (127 + 7))) : 0;
-    inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+    const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+    lv = (float)ex;
 #pragma unroll
-    for (int e = 0; e < 4; e++) x[e] += (float)ex;
+    for (int e = 0; e < 4; e++) x[e] += lv;
 #pragma unroll
     for (int m = 0; m < 8; m++) {
       v[m].x = scale_pair<ELEM>(v[m].x, inv);
@@ -313,8 +322,8 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
       v[m].w = scale_pair<ELEM>(v[m].w, inv);
     }
   }
-  raise(s, x);
-  weights(s, x, inv);
+  raise(s, x, lv);
+  weights(s, x, lv);
   uint32_t p0 = pack_elems<ELEM>(x[0], x[1]), p1 = pack_elems<ELEM>(x[2], x[3]);
   const uint32_t b0 = movmatrix_trans(p0), b1 = movmatrix_trans(p1);
   uint32_t r0 = 0, r1 = 0;
@@ -349,11 +358,11 @@ __device__ __forceinline__ void half_q(uint32_t (&qf)[16], int lane, float (&sca
   scale[1] = __shfl_sync(0xffffffffu, sc, 8 * t + 4);
 }
 
-// A unit that one warp holds whole: out = O / l, two features a store.
+// A unit that one warp holds whole: out = O 2^(m - u) / l, two features a store.
 template <int ELEM>
 __device__ __forceinline__ void write_unit(const State& s, uint8_t* out, int G, int lane) {
   const int g = lane >> 2, t = lane & 3, odd = g & 1, q = 2 * t + odd;
-  const float ia = __fdiv_rn(1.0f, s.l[0]), ib = __fdiv_rn(1.0f, s.l[1]);
+  const float ia = __fdiv_rn(fast_exp2(s.m[0] - s.u[0]), s.l[0]), ib = __fdiv_rn(fast_exp2(s.m[1] - s.u[1]), s.l[1]);
 #pragma unroll
   for (int m = 0; m < 8; m++)
 #pragma unroll
@@ -366,20 +375,37 @@ __device__ __forceinline__ void write_unit(const State& s, uint8_t* out, int G, 
     }
 }
 
-// A partial in shared memory: G rows of kA8Row, then 8 maxima and 8 sums.
+// A partial: the part's own result, so that its size is that of its values, and
+// its weight as l 2^m with l in [2^-9, 2^-8): a row's weights sum to less than 2
+// under their joint maximum (304 parts at most), values of any size stay in
+// fp32's range times them. l = 0: no visible token with a logit above -Inf.
+__device__ __forceinline__ void split_weight(float& m, float& l) {
+  if (l > 0.0f && l < INFINITY) {
+    const int e = (int)(__float_as_uint(l) >> 23) - (127 - 9);      // l: of the order of 1 and more, never subnormal
+    m += (float)e;
+    l = __uint_as_float(__float_as_uint(l) - ((uint32_t)e << 23));
+  }
+}
+// In shared memory: G rows of kA8Row, then 8 maxima and 8 sums.
 __device__ __forceinline__ void put_partial(const State& s, float* p, int G, int lane) {
   const int g = lane >> 2, t = lane & 3;
+  float f[2], m[2] = {s.u[0], s.u[1]}, l[2] = {s.l[0], s.l[1]};
 #pragma unroll
-  for (int m = 0; m < 8; m++)
+  for (int e = 0; e < 2; e++) {
+    f[e] = l[e] == 0.0f ? 0.0f : __fdiv_rn(fast_exp2(s.m[e] - s.u[e]), l[e]);
+    split_weight(m[e], l[e]);
+  }
+#pragma unroll
+  for (int m8 = 0; m8 < 8; m8++)
 #pragma unroll
     for (int e = 0; e < 4; e++)
-      if (2 * t + (e & 1) < G) p[(2 * t + (e & 1)) * kA8Row + 16 * m + g + 8 * (e >> 1)] = s.o[m][e];
+      if (2 * t + (e & 1) < G) p[(2 * t + (e & 1)) * kA8Row + 16 * m8 + g + 8 * (e >> 1)] = s.o[m8][e] * f[e & 1];
   if (g == 0) {
     float* ml = p + G * kA8Row;
-    ml[2 * t] = s.m[0];
-    ml[2 * t + 1] = s.m[1];
-    ml[8 + 2 * t] = s.l[0];
-    ml[8 + 2 * t + 1] = s.l[1];
+    ml[2 * t] = m[0];
+    ml[2 * t + 1] = m[1];
+    ml[8 + 2 * t] = l[0];
+    ml[8 + 2 * t + 1] = l[1];
   }
 }
 // weight of a partial with maximum m under the joint maximum M: 1 where they
@@ -394,22 +420,16 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 // Row q of several parts: lane x holds the address of part x where bit x of set
 // is on; rows of `row` floats, then G maxima from G * row and G sums from
-// G * row + 8. Added to what r holds.
+// G * row + 8. o is the sum of the parts' results by weight, l of the weights.
 struct Row {
   float4 o;
   float m, l;
 };
-__device__ __noinline__ Row join_row(Row r, unsigned set, const float* p, int row, int G, int q, int lane) {
+__device__ __noinline__ Row join_row(unsigned set, const float* p, int row, int G, int q, int lane) {
   const bool has = set >> lane & 1u;
   const float m = has ? p[G * row + q] : -INFINITY, pl = has ? p[G * row + 8 + q] : 0.0f;
-  const float now = fmaxf(r.m, warp_max(m));
-  const float f = has ? join(m, now) : 0.0f, g = join(r.m, now);
-  r.m = now;
-  r.l *= g;
-  r.o.x *= g;
-  r.o.y *= g;
-  r.o.z *= g;
-  r.o.w *= g;
+  Row r{make_float4(0.0f, 0.0f, 0.0f, 0.0f), warp_max(m), 0.0f};
+  const float f = has ? pl * join(m, r.m) : 0.0f;
   const unsigned long long mine = reinterpret_cast<unsigned long long>(p + q * row);
   // two parts at a time
 #pragma unroll 1
@@ -421,15 +441,14 @@ __device__ __noinline__ Row join_row(Row r, unsigned set, const float* p, int ro
     set &= set - 1;
     const float4 v0 = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, mine, x0))[lane];
     const float4 v1 = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, mine, x1))[lane];
-    const float f0 = __shfl_sync(0xffffffffu, f, x0), l0 = __shfl_sync(0xffffffffu, pl, x0);
-    const float f1 = __shfl_sync(0xffffffffu, f, x1), l1 = __shfl_sync(0xffffffffu, pl, x1);
-    r.l = fmaf(l0, f0, r.l);
+    const float f0 = __shfl_sync(0xffffffffu, f, x0), f1 = __shfl_sync(0xffffffffu, f, x1);
+    r.l += f0;
     r.o.x = fmaf(v0.x, f0, r.o.x);
     r.o.y = fmaf(v0.y, f0, r.o.y);
     r.o.z = fmaf(v0.z, f0, r.o.z);
     r.o.w = fmaf(v0.w, f0, r.o.w);
     if (two) {
-      r.l = fmaf(l1, f1, r.l);
+      r.l += f1;
       r.o.x = fmaf(v1.x, f1, r.o.x);
       r.o.y = fmaf(v1.y, f1, r.o.y);
       r.o.z = fmaf(v1.z, f1, r.o.z);
@@ -460,7 +479,7 @@ __device__ __noinline__ Row join_far(const float* part, int stride, int c0, int 
     };
     load(0);
     const float now = fmaxf(r.m, warp_max(m));
-    const float f = lane < n ? join(m, now) : 0.0f, g = join(r.m, now);
+    const float f = lane < n ? pl * join(m, now) : 0.0f, g = join(r.m, now);
     r.m = now;
     r.l *= g;
     r.o.x *= g;
@@ -471,9 +490,9 @@ __device__ __noinline__ Row join_far(const float* part, int stride, int c0, int 
     for (int b = 0;;) {
 #pragma unroll
       for (int i = 0; i < kFar; i++) {
-        const float fi = __shfl_sync(0xffffffffu, f, min(b + i, 31)), li = __shfl_sync(0xffffffffu, pl, min(b + i, 31));
+        const float fi = __shfl_sync(0xffffffffu, f, min(b + i, 31));
         if (b + i < n) {
-          r.l = fmaf(li, fi, r.l);
+          r.l += fi;
           r.o.x = fmaf(v[i].x, fi, r.o.x);
           r.o.y = fmaf(v[i].y, fi, r.o.y);
           r.o.z = fmaf(v[i].z, fi, r.o.z);
@@ -814,9 +833,12 @@ __global__ void __launch_bounds__(kA8Warps * 32)
     const int u = __shfl_sync(0xffffffffu, mine, lead);
     const int us = s_span[lead].x, ue = s_span[lead].y;
     uint8_t* out = a.out + ((size_t)u * G + q) * (2 * kD);
-    Row r = join_row(Row{make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f}, set, my_part, kA8Row, G, q, lane);
+    Row r = join_row(set, my_part, kA8Row, G, q, lane);
     if (us < lo || ue > hi) {
       float* dst = a.part + (size_t)(2 * blockIdx.x + (us < lo ? 0 : 1)) * stride;
+      const float inv = r.l == 0.0f ? 0.0f : __fdiv_rn(1.0f, r.l);
+      r.o = make_float4(r.o.x * inv, r.o.y * inv, r.o.z * inv, r.o.w * inv);
+      split_weight(r.m, r.l);
       *reinterpret_cast<float4*>(dst + q * kD + 4 * lane) = r.o;
       if (lane == 0) {
         dst[G * kD + q] = r.m;

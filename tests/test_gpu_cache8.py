@@ -946,3 +946,51 @@ def test_other_streams_and_workspaces():
     torch.cuda.synchronize()
     for o in outs[0] + outs[1]:
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("amp", [1e9, 4e10, 1e12, 1e30, 3e38])
+def test_attention_of_zero_values_beside_huge_ones(code, amp):
+    """Tokens whose values are zero keep their weight beside blocks of any finite
+    size: in pages and in the tail, inside one warp's tiles, over the warps of a
+    block and over blocks of the grid."""
+    lens = [64, 70, 90, 500, 9000, 5]
+    rng = np.random.default_rng(8)
+    c = Cache(1, 3, 32, len(lens), 9000 // 32 + 1, BF16, code, fill=float("nan"))
+    n = sum(lens)
+    k, q = (c.vec(rng, n, 1).float() * 1e-2).to(BF16), c.vec(rng, len(lens), 3)
+    v = torch.full((n, 1, 128), amp, device="cuda")
+    at = 0
+    for i, m in enumerate(lens):
+        f = torch.ones(m, 1, 1, device="cuda")
+        if i % 2 == 0:
+            f[:m // 2 // 32 * 32 or 2] = 0.0           # the first half
+        else:
+            f[m // 2 // 32 * 32:] = 0.0                # the second, the open block with it
+        v[at:at + m] *= f
+        at += m
+    v = v.to(BF16)
+    c.append(None, [0] * len(lens), lens, k, v)
+    for window, sinks in ((0, 0), (60, 33)):
+        out = c.attend(None, lens, q, window, sinks)
+        assert torch.isfinite(out).all()
+        c.check_attention(out, range(len(lens)), lens, q, window, sinks)
+
+
+def test_attention_of_many_light_tokens_of_zero_values():
+    """fp16: thousands of zero values, 2^-20 of the largest weight each, beside one
+    value of the type's largest size."""
+    for lens in ([4200], [4200, 900, 4100]):
+        c = Cache(1, 2, 64, len(lens), 70, F16, INT8)
+        n = sum(lens)
+        k, v = (torch.zeros((n, 1, 128), dtype=F16, device="cuda") for _ in range(2))
+        q = torch.zeros((len(lens), 2, 128), dtype=F16, device="cuda")
+        q[:, :, 0] = 8.0
+        at = 0
+        for m in lens:
+            p = at + m - 100
+            k[p, 0, 0], v[p] = 20.0, 65504.0       # 160 / sqrt(128) is 20.4 in powers of two
+            at += m
+        c.append(None, [0] * len(lens), lens, k, v)
+        out = c.attend(None, lens, q)
+        c.check_attention(out, range(len(lens)), lens, q)
