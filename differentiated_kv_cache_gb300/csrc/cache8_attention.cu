@@ -884,13 +884,14 @@ cudaError_t launch_attention8(const Cache8View& c, int elem, int code, int sm_co
                     n_req, window, sinks, reinterpret_cast<unsigned*>(part + (size_t)sm_count * 2 * (c.G * kD + 16)), part};
   auto kernel = elem == DKV_F16 ? (code == DKV_E4M3 ? k_attention8<DKV_F16, DKV_E4M3> : k_attention8<DKV_F16, DKV_INT8>)
                                 : (code == DKV_E4M3 ? k_attention8<DKV_BF16, DKV_E4M3> : k_attention8<DKV_BF16, DKV_INT8>);
-  const size_t smem = attention8_smem(c.G);
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the limit belongs to the kernel, which calls of other group sizes on other
+  // host threads launch too: always the largest
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)attention8_smem(kMaxG));
   if (e != cudaSuccess) return e;
   // no more CTAs than the longest lengths that the table holds could use
   const long long units = (long long)n_req * c.hkv, tiles = units * ((long long)c.width * c.T / kSub);
   const int grid = (int)std::min<long long>(sm_count, std::max(units, (tiles + kA8Cta - 1) / kA8Cta));
-  return launch_dependent(kernel, dim3(grid), dim3(kA8Warps * 32), smem, st, c, a);
+  return launch_dependent(kernel, dim3(grid), dim3(kA8Warps * 32), attention8_smem(c.G), st, c, a);
 }
 
 }  // namespace dkv

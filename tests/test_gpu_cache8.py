@@ -994,3 +994,55 @@ def test_attention_of_many_light_tokens_of_zero_values():
         c.append(None, [0] * len(lens), lens, k, v)
         out = c.attend(None, lens, q)
         c.check_attention(out, range(len(lens)), lens, q)
+
+
+def test_group_sizes_on_two_host_threads(tmp_path):
+    """Caches of the smallest and the largest group, each served by a host thread and
+    a stream of its own: calls of the C entry without Python between them."""
+    import ctypes as C
+    import subprocess
+    dkv = _dkv()
+    (tmp_path / "two.c").write_text("""
+#include <pthread.h>
+#include "dkv.h"
+typedef int (*entry)(const dkv_cache8*, int32_t, const int32_t*, const int32_t*, const void*, int64_t, void*, int32_t,
+                     int32_t, void*);
+struct job { entry f; const dkv_cache8* c; const int32_t *slots, *lens; const void* q; void *out, *stream; int32_t n_req;
+             int32_t calls, failed; };
+static void* serve(void* p) {
+  struct job* j = p;
+  for (int i = 0; i < j->calls; i++)
+    j->failed += j->f(j->c, j->n_req, j->slots, j->lens, j->q, (int64_t)j->c->n_kv_heads * j->c->group_size * 128, j->out, 0,
+                      0, j->stream) != 0;
+  return 0;
+}
+void two(struct job* a, struct job* b) {
+  pthread_t t;
+  pthread_create(&t, 0, serve, a);
+  serve(b);
+  pthread_join(t, 0);
+}
+""")
+    so = str(tmp_path / "two.so")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-pthread", "-I", str(dkv.build.INCLUDE), "-o", so, str(tmp_path / "two.c")],
+                   check=True)
+
+    class Job(C.Structure):
+        _fields_ = [(n, C.c_void_p) for n in ("f", "c", "slots", "lens", "q", "out", "stream")] + \
+            [(n, C.c_int32) for n in ("n_req", "calls", "failed")]
+
+    lens = [100, 33]
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    keep, jobs = [], []
+    for G in (1, 8):
+        c, slots, q = filled(1, G, 32, F16, E4M3, lens, seed=G)
+        sl, ln, out, stream = i32(slots), i32(lens), torch.empty_like(q), torch.cuda.Stream()
+        keep.append((c, sl, ln, q, out, stream, c.attend(slots, lens, q)))
+        jobs.append(Job(C.cast(dkv.load().dkv_cache8_attention, C.c_void_p), c.c.address, sl.data_ptr(), ln.data_ptr(),
+                        q.data_ptr(), out.data_ptr(), stream.cuda_stream, 2, 50000, 0))
+    torch.cuda.synchronize()
+    C.CDLL(so).two(C.byref(jobs[0]), C.byref(jobs[1]))
+    torch.cuda.synchronize()
+    assert [j.failed for j in jobs] == [0, 0]
+    for c, _, _, _, out, _, want in keep:
+        assert torch.equal(out, want) and c.c.status_words.tolist() == [0, 0]
