@@ -637,7 +637,8 @@ __global__ void __launch_bounds__(512) k_prefill8_again(Cache8View c, Again8 a, 
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
       x *= kLogitScale;
-      const float mn = fmaxf(m, x), f = m == mn ? 1.0f : fast_exp2(m - mn), p = fast_exp2(x - mn);
+      const float mn = fmaxf(m, x), f = m == mn ? 1.0f : fast_exp2(m - mn);
+      const float p = x == -INFINITY ? 0.0f : fast_exp2(x - mn);      // the nearest key's may be -Inf, m then too
       m = mn;
       l = fmaf(l, f, p);
       bool open = false;

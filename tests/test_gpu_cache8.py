@@ -1046,3 +1046,27 @@ void two(struct job* a, struct job* b) {
     assert [j.failed for j in jobs] == [0, 0]
     for c, _, _, _, out, _, want in keep:
         assert torch.equal(out, want) and c.c.status_words.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("elem", [F16, BF16])
+def test_prefill_of_own_keys_of_infinite_weight_zero(elem):
+    """A row whose own key's logit is -Inf (weight 0) and that does not see the NaN
+    beside it has the result of its other keys."""
+    rng = np.random.default_rng(3)
+    n, G = 150, 2
+    c = Cache(1, G, 16, 1, 1, elem, E4M3)
+    q, k, v = c.vec(rng, n, G), c.vec(rng, n, 1), c.vec(rng, n, 1)
+    q[:, :, 9] = q[:, :, 9].abs() + 0.5
+    k[[10, 90], 0, 9] = float("-inf")
+    v[[12, 100], 0, ::3] = float("nan")
+    out = torch.empty_like(q)
+    _dkv().dkv_cache8_prefill(c.c, [n], q, k, v, out, window=30, sinks=2)
+    torch.cuda.synchronize()
+    got, qn, kn, vn = (x.double().cpu().numpy() for x in (out, q, k, v))
+    for p in range(n):
+        see = ref.visible(p + 1, 30, 2)
+        hit = ~np.isfinite(vn[see, 0]).all(axis=0)
+        see = see[np.isfinite(kn[see, 0]).all(axis=1)]      # the others have no weight
+        want, pv, qk, vm = ref.attend(qn[p], kn[see, 0], np.nan_to_num(vn[see, 0]))
+        tol = ref.tolerance(want, pv, qk, vm, len(see), elem, torch.finfo(elem).eps / 2)
+        assert np.isnan(got[p][:, hit]).all() and (np.abs(got[p] - want) <= tol)[:, ~hit].all(), p
