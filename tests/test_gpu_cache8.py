@@ -1070,3 +1070,30 @@ def test_prefill_of_own_keys_of_infinite_weight_zero(elem):
         want, pv, qk, vm = ref.attend(qn[p], kn[see, 0], np.nan_to_num(vn[see, 0]))
         tol = ref.tolerance(want, pv, qk, vm, len(see), elem, torch.finfo(elem).eps / 2)
         assert np.isnan(got[p][:, hit]).all() and (np.abs(got[p] - want) <= tol)[:, ~hit].all(), p
+
+
+@pytest.mark.parametrize("elem", [F16, BF16])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (70, 20)])
+def test_prefill_of_infinite_values_of_both_signs(elem, window, sinks):
+    """Infinite values give their feature their sign, both signs give NaN, whichever
+    is nearer, and a NaN gives NaN."""
+    rng = np.random.default_rng(4)
+    n, G = 300, 2
+    c = Cache(1, G, 16, 1, 1, elem, E4M3)
+    q, k, v = c.vec(rng, n, G), c.vec(rng, n, 1), c.vec(rng, n, 1)
+    inf = float("inf")
+    v[10, 0, 3], v[200, 0, 3] = inf, -inf
+    v[5, 0, 4], v[180, 0, 4] = -inf, inf
+    v[8, 0, 5], v[100, 0, 5] = float("nan"), inf
+    v[[0, 130], 0, 6] = -inf
+    out = torch.empty_like(q)
+    _dkv().dkv_cache8_prefill(c.c, [n], q, k, v, out, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    got, vn = out.double().cpu().numpy(), v.double().cpu().numpy()
+    for p in range(n):
+        x = vn[ref.visible(p + 1, window, sinks), 0]
+        up, down, nan = (x == inf).any(axis=0), (x == -inf).any(axis=0), np.isnan(x).any(axis=0)
+        nan |= up & down
+        g = got[p]
+        assert np.isnan(g[:, nan]).all() and (g[:, up & ~nan] == inf).all() and (g[:, down & ~nan] == -inf).all(), p
+        assert np.isfinite(g[:, ~(up | down | nan)]).all(), p
