@@ -68,6 +68,20 @@ __device__ __forceinline__ float lo_elem(uint32_t w) { return elem_float<ELEM>((
 template <int ELEM>
 __device__ __forceinline__ float hi_elem(uint32_t w) { return elem_float<ELEM>((uint16_t)(w >> 16)); }
 
+// c += a b, 16 x 16 by 16 x 8 (mma.sync), fp32 sums
+template <int ELEM>
+__device__ __forceinline__ void mma_elem(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (ELEM == DKV_F16) {
+    mma16816(c, a, b0, b1);
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
 // largest finite |x| so far
 __device__ __forceinline__ float amax_finite(float m, float x) {
   const float a = fabsf(x);

@@ -100,19 +100,6 @@ __device__ __forceinline__ void code_halves(uint32_t w, uint32_t& lo, uint32_t& 
   }
 }
 
-template <int ELEM>
-__device__ __forceinline__ void mma_elem(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  if (ELEM == DKV_F16) {
-    mma16816(c, a, b0, b1);
-  } else {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};\n"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  }
-}
-
 // Running state of a warp for one (request, KV head): lane 4g + t holds
 // queries 2t, 2t + 1; O rows are features 16 m + g and 16 m + g + 8.
 struct State {

@@ -42,8 +42,8 @@
 //
 // 0 * Inf is not 0: an infinite or NaN value makes NaN of every row of its step,
 // those that do not see it too. A second kernel computes rows that came out so
-// again, one by one over the keys that they see (in this kernel the code for it
-// cost 3%, though it never ran, and a look at V ahead of the products 5%).
+// again over what they see (in this kernel the code for it cost 3%, though it
+// never ran, and a look at V ahead of the products 5%).
 //
 // Every wait is bounded; on expiry the kernel latches DKV_ERR_TIMEOUT, waits
 // (bounded) for its own copies and MMAs, frees its tensor memory and returns.
@@ -583,76 +583,366 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   }
 }
 
-// Rows that came out infinite or NaN in this call (or, while status[2] is on, may
-// have): a warp each, four features a lane, from the definition, over the keys
-// that the row sees, the nearest first, until what it sees has made NaN of all its
-// doubtful features. Other features stay as they are. A quarter of the SMs:
-// the launch that finds nothing adds 1.6 us to a call, four blocks an SM 2.8.
+// ---- Rows that came out NaN ----
+// A feature of a row is NaN by right where the row sees a NaN value of it,
+// infinite ones of both signs, an infinite one under a weight of 0, or a key whose
+// logit is NaN or +Inf. It is wrong where a value that the row does not see, in a
+// step beside its keys, made 0 * NaN or 0 * Inf of it, and where an infinite value
+// that it does see met a weight that rounds to 0 in 16 bits. (What is infinite is
+// right: nothing makes a number of NaN again.)
+//
+// A block takes the halves of the kernel above in turn (128 / G tokens, all heads
+// of a group). Of one that holds NaN it looks through the keys and values that its
+// rows see, and those that the steps beside them hold, for what is not finite, 512
+// keys at a time, the first ones first and then from the diagonal back, until
+// every NaN is seen to be right. Where some are not, it computes the half again
+// with mma.sync, with zeros for the values that are not finite, and writes the
+// features that are not right, and only those. So a call that meets such a value
+// costs a look through its results, and through keys and values as far as that
+// value; and each value the computing of the few halves that hold it in a step but
+// not in their rows' sight. 16384 tokens, 64 / 8 heads, window 4096 + 64, bf16 (1.45
+// ms without such a value): one NaN in a first token's key or value 1.95 ms, in the
+// middle 2.1, a feature infinite in every token 10.8, one value in 10^4 NaN 10.4
+// (with 64 / 64 heads 20.8: every half again, at 110 TFLOP/s). A walk of a warp a
+// row through its keys, nearest first, took 244 ms for one NaN in 4096 tokens with
+// window 1024 (0.14 ms without).
+//
+// The launch that finds nothing adds 1.5 us to a call.
 struct Again8 {
   uint8_t* out;
   const uint8_t *q, *k, *v;
   long long qs, ks, vs;      // row strides in bytes
-  int window, sinks;
+  W8Args w;
 };
+constexpr int kAgThreads = 256;            // a warp for 16 rows
+constexpr int kAgKeys = 64;                // keys of a tile
+constexpr int kAgLook = 512;               // keys between two looks at what is left
+
+// Bits of features: NaN by right, +Inf and -Inf among the values that are seen.
+enum { kNan, kUp, kDown, kKinds };
+struct AgShared {
+  uint4 k[kAgKeys * 16], v[kAgKeys * 16];          // 16-byte pieces, swizzled by row % 8
+  uint32_t seen[kKinds][kW8T][4];                  // by a token
+  uint32_t all[kKinds][4];                         // by every token
+  uint32_t unseen[4];                              // any value that some token does not see
+  uint32_t need[kW8T][4];                          // per row: NaN, then what is to be computed again
+};
+// Bits of eight 16-bit values w: those in which `is` is on in the 16 bits of m.
+__device__ __forceinline__ uint32_t bits8(uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3) {
+  auto two = [](uint32_t m) { return (m & 1u) | (m >> 31 << 1); };
+  return two(m0) | two(m1) << 2 | two(m2) << 4 | two(m3) << 6;
+}
 template <int ELEM>
-__global__ void __launch_bounds__(512) k_prefill8_again(Cache8View c, Again8 a, const __grid_constant__ W8Call call) {
+struct Elem {
+  static constexpr uint32_t kInf = ELEM == DKV_F16 ? 0x7c007c00u : 0x7f807f80u;
+  static __device__ __forceinline__ uint32_t mag(uint32_t w) { return w & 0x7fff7fffu; }
+  static __device__ __forceinline__ bool all_finite(uint4 w) {
+    return (__vcmpgeu2(mag(w.x), kInf) | __vcmpgeu2(mag(w.y), kInf) | __vcmpgeu2(mag(w.z), kInf) | __vcmpgeu2(mag(w.w), kInf)) == 0;
+  }
+  static __device__ __forceinline__ uint32_t nans(uint4 w) {
+    return bits8(__vcmpgtu2(mag(w.x), kInf), __vcmpgtu2(mag(w.y), kInf), __vcmpgtu2(mag(w.z), kInf), __vcmpgtu2(mag(w.w), kInf));
+  }
+  static __device__ __forceinline__ uint32_t equal(uint4 w, uint32_t x) {
+    return bits8(__vcmpeq2(w.x, x), __vcmpeq2(w.y, x), __vcmpeq2(w.z, x), __vcmpeq2(w.w, x));
+  }
+  // zeros in place of what is not finite
+  static __device__ __forceinline__ uint4 finite_of(uint4 w) {
+    return make_uint4(w.x & __vcmpltu2(mag(w.x), kInf), w.y & __vcmpltu2(mag(w.y), kInf), w.z & __vcmpltu2(mag(w.z), kInf),
+                      w.w & __vcmpltu2(mag(w.w), kInf));
+  }
+};
+
+// Keys [0, first) and [lo, hi), numbered in a row.
+struct AgKeys {
+  int first, lo, total;
+  __device__ __forceinline__ AgKeys(int first_, int lo_, int hi) : first(min(first_, lo_)), lo(lo_), total(first + hi - lo_) {}
+  __device__ __forceinline__ int operator()(int x) const { return x < first ? x : lo + x - first; }
+};
+
+// The bits of piece c (eight features) of key j, for the tokens that see it.
+// Seldom reached.
+__device__ __noinline__ void mark(AgShared& sh, int q0, int nt, const W8Args& a, int j, int c, uint32_t nan, uint32_t up,
+                                  uint32_t down) {
+  const int word = c >> 2, shift = 8 * (c & 3);
+  const uint32_t b[kKinds] = {nan << shift, up << shift, down << shift};
+  auto put = [](uint32_t& w, uint32_t x) {
+    if ((*(volatile uint32_t*)&w & x) != x) atomicOr(&w, x);
+  };
+  const int t0 = max(j - q0, 0);      // the tokens [t0, t1) see it
+  const int t1 = a.window <= 0 || j < a.sinks ? nt : (int)min((long long)nt, (long long)j - q0 + a.window);
+  const bool all = t0 == 0 && t1 == nt;
+  if (!all) put(sh.unseen[word], b[kNan] | b[kUp] | b[kDown]);
+  for (int i = 0; i < kKinds; i++)
+    if (all) put(sh.all[i][word], b[i]);
+    else if (b[i])
+      for (int t = t0; t < t1; t++) put(sh.seen[i][t][word], b[i]);
+}
+struct AgRow {
+  uint32_t nan, up, down;
+};
+// Of a word of features of a token.
+__device__ __forceinline__ AgRow row_of(const AgShared& sh, int t, int w) {
+  AgRow r{sh.seen[kNan][t][w] | sh.all[kNan][w], sh.seen[kUp][t][w] | sh.all[kUp][w], sh.seen[kDown][t][w] | sh.all[kDown][w]};
+  r.nan |= r.up & r.down;
+  return r;
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// The half again: S = Q K^T and O += P V with mma.sync m16n8k16, 16 rows a warp,
+// in the manner and the types of the kernel above.
+template <int ELEM>
+__device__ __noinline__ void half_again(AgShared& sh, const Cache8View& c, const Again8& a, const Item& it, int q0, int nt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = c.G;
+  const int window = a.w.window, q1 = q0 + nt - 1;
+  const AgKeys key(window > 0 ? min(a.w.sinks, it.n0) : 0, window > 0 ? max(q0 - window + 1, 0) : 0, q1 + 1);
+  const uint32_t* need = sh.need[16 * warp + (lane & 15)];
+  const bool mine = __any_sync(0xffffffffu, (need[0] | need[1] | need[2] | need[3]) != 0);
+  int pos[2];
+  long long row[2];            // of the output and the queries: token, head
+  uint32_t qf[8][4];
+#pragma unroll
+  for (int e = 0; e < 2; e++) {
+    const int r = 16 * warp + g + 8 * e;
+    pos[e] = q0 + r / G;
+    const bool in = r < nt * G;
+    const long long tok = (long long)it.t0 + pos[e];
+    row[e] = in ? (tok * c.hkv + it.h) * G + r % G : -1;
+    const uint8_t* p = a.q + tok * a.qs + ((size_t)it.h * G + r % G) * (2 * kD) + 4 * t;
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      qf[k][e] = in ? *reinterpret_cast<const uint32_t*>(p + 32 * k) : 0u;
+      qf[k][2 + e] = in ? *reinterpret_cast<const uint32_t*>(p + 32 * k + 16) : 0u;
+    }
+  }
+  float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 16; i++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) o[i][e] = 0.0f;
+  const uint32_t ks = smem_u32(sh.k), vs = smem_u32(sh.v);
+  auto piece = [](uint32_t base, int r, int ch) { return base + 16 * (16 * r + (ch ^ (r & 7))); };
+#pragma unroll 1
+  for (int base = 0; base < key.total; base += kAgKeys) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kAgKeys * 16; i += kAgThreads) {
+      const int r = i >> 4, ch = i & 15, at = 16 * r + (ch ^ (r & 7));
+      uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
+      const int j = key(min(base + r, key.total - 1));
+      if (base + r < key.total) {
+        kw = *reinterpret_cast<const uint4*>(a.k + ((long long)it.t0 + j) * a.ks + it.h * (2 * kD) + 16 * ch);
+        vw = *reinterpret_cast<const uint4*>(a.v + ((long long)it.t0 + j) * a.vs + it.h * (2 * kD) + 16 * ch);
+      }
+      sh.k[at] = kw;
+      sh.v[at] = Elem<ELEM>::finite_of(vw);
+    }
+    __syncthreads();
+    if (!mine) continue;
+    float s[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; n++) {
+#pragma unroll
+      for (int e = 0; e < 4; e++) s[n][e] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        uint32_t b[4];
+        ldmatrix_x4(b, piece(ks, 8 * n + (lane & 7), 4 * k + (lane >> 3)));
+        mma_elem<ELEM>(s[n], qf[2 * k], b[0], b[1]);
+        mma_elem<ELEM>(s[n], qf[2 * k + 1], b[2], b[3]);
+      }
+    }
+    float top[2] = {m[0], m[1]};
+    const int j0 = key(base), j1 = key(base + kAgKeys - 1);
+    if (base + kAgKeys > key.total || j1 > q0 || !(window <= 0 || j0 > q1 - window || j1 < a.w.sinks)) {
+#pragma unroll
+      for (int n = 0; n < 8; n++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {        // some token does not see every key
+          const int x = base + 8 * n + 2 * t + (e & 1), j = key(x), p = pos[e >> 1];
+          if (!(x < key.total && j <= p && (window <= 0 || j > p - window || j < a.w.sinks))) s[n][e] = -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 8; n++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        s[n][e] *= kLogitScale;
+        top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+      }
+    float f[2], off[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+      top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+      top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
+      f[e] = top[e] == -INFINITY ? 1.0f : fast_exp2(m[e] - top[e]);
+      off[e] = top[e] == -INFINITY ? 0.0f : top[e];
+      m[e] = top[e];
+      l[e] *= f[e];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[i][e] *= f[e >> 1];
+#pragma unroll
+    for (int n = 0; n < 8; n++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        s[n][e] = fast_exp2(s[n][e] - off[e >> 1]);
+        l[e >> 1] += s[n][e];
+      }
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const uint32_t p[4] = {pack_elems<ELEM>(s[2 * k][0], s[2 * k][1]), pack_elems<ELEM>(s[2 * k][2], s[2 * k][3]),
+                             pack_elems<ELEM>(s[2 * k + 1][0], s[2 * k + 1][1]), pack_elems<ELEM>(s[2 * k + 1][2], s[2 * k + 1][3])};
+#pragma unroll
+      for (int n = 0; n < 8; n++) {
+        uint32_t b[4];
+        ldmatrix_x4_trans(b, piece(vs, 16 * k + (lane & 15), 2 * n + (lane >> 4)));
+        mma_elem<ELEM>(o[2 * n], p, b[0], b[1]);
+        mma_elem<ELEM>(o[2 * n + 1], p, b[2], b[3]);
+      }
+    }
+  }
+  if (!mine) return;
+#pragma unroll
+  for (int e = 0; e < 2; e++) {
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+    l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+    if (row[e] < 0) continue;
+    const int r = 16 * warp + g + 8 * e;
+    const float inv = __fdiv_rn(1.0f, l[e]);
+    uint16_t* out = reinterpret_cast<uint16_t*>(a.out + row[e] * (2 * kD));
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const int w = i >> 2;
+      if ((sh.need[r][w] >> (8 * (i & 3)) & 0xffu) == 0) continue;
+      const AgRow x = row_of(sh, r / G, w);
+#pragma unroll
+      for (int y = 0; y < 2; y++) {
+        const int at = 8 * (i & 3) + 2 * t + y;
+        if (!((sh.need[r][w] & ~x.nan) >> at & 1u)) continue;
+        // an infinite sum is infinite, unless the weights are NaN
+        const float v = (x.up | x.down) >> at & 1u ? (x.up >> at & 1u ? INFINITY : -INFINITY) * inv : o[i][2 * e + y] * inv;
+        out[8 * i + 2 * t + y] = float_elem<ELEM>(v);
+      }
+    }
+  }
+}
+
+template <int ELEM>
+__global__ void __launch_bounds__(kAgThreads, 1) k_prefill8_again(Cache8View c, Again8 a, const __grid_constant__ W8Call call) {
   pdl_launch_dependents();
   pdl_wait();
   if (c.stopped() || *(volatile int*)(c.status + 2) == 0) return;
-  const int lane = threadIdx.x & 31, hq = c.hkv * c.G;
-  const long long rows = (long long)call.tok0[call.n_req] * hq, step = (long long)gridDim.x * (blockDim.x / 32);
-  auto finite = [](float x) { return fabsf(x) < INFINITY; };
-  auto four = [](const uint8_t* p, float (&x)[4]) {
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    x[0] = lo_elem<ELEM>(w.x);
-    x[1] = hi_elem<ELEM>(w.x);
-    x[2] = lo_elem<ELEM>(w.y);
-    x[3] = hi_elem<ELEM>(w.y);
-  };
-  for (long long r = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += step) {
-    uint8_t* out = a.out + r * (2 * kD) + 8 * lane;
-    float was[4];
-    four(out, was);
-    bool doubt[4], any = false;
+  __shared__ AgShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x, G = c.G, tq = a.w.tq;
+  const long long halves = 2ll * call.tile0[call.n_req] * c.hkv;
+#pragma unroll 1
+  for (long long x = blockIdx.x; x < halves; x += gridDim.x) {
+    const Item it = item_of((int)(x >> 1), c, a.w, call);
+    const int q0 = it.p0 + (int)(x & 1) * tq, nt = min(tq, it.n0 - q0);      // its tokens
+    if (nt <= 0) continue;
+    // NaN in its rows
+    __syncthreads();           // the half before is done with
+    uint32_t some = 0;
+    uint4 w[8];
 #pragma unroll
-    for (int e = 0; e < 4; e++) any |= doubt[e] = !finite(was[e]);
-    if (!__any_sync(0xffffffffu, any)) continue;
-    const int tok = (int)(r / hq), head = (int)(r - (long long)tok * hq);
-    int i = 0;
-    for (int end = call.n_req; end - i > 1;) {
-      const int mid = (i + end) >> 1;
-      if (call.tok0[mid] <= tok) i = mid; else end = mid;
+    for (int i = 0; i < 8; i++) {
+      const int r = 16 * warp + 2 * i + (lane >> 4);
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (r < nt * G)
+        w[i] = *reinterpret_cast<const uint4*>(a.out + (((long long)(it.t0 + q0 + r / G) * c.hkv + it.h) * G + r % G) * (2 * kD) +
+                                               16 * (lane & 15));
     }
-    const int t0 = call.tok0[i], pos = tok - t0, lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-    const int early = a.window > 0 ? min(a.sinks, lo) : 0;
-    const uint8_t* k = a.k + t0 * a.ks + (head / c.G) * (2 * kD) + 8 * lane;
-    const uint8_t* v = a.v + t0 * a.vs + (head / c.G) * (2 * kD) + 8 * lane;
-    float q[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = -INFINITY, l = 0.0f;
-    four(a.q + tok * a.qs + head * (2 * kD) + 8 * lane, q);
-    for (int j = pos; j >= 0; j = j == lo ? early - 1 : j - 1) {
-      float y[4], z[4];
-      four(k + j * a.ks, y);
-      four(v + j * a.vs, z);
-      float x = fmaf(q[3], y[3], fmaf(q[2], y[2], fmaf(q[1], y[1], q[0] * y[0])));
 #pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      x *= kLogitScale;
-      const float mn = fmaxf(m, x), f = m == mn ? 1.0f : fast_exp2(m - mn);
-      const float p = x == -INFINITY ? 0.0f : fast_exp2(x - mn);      // the nearest key's may be -Inf, m then too
-      m = mn;
-      l = fmaf(l, f, p);
-      bool open = false;
+    for (int i = 0; i < 8; i++) {
+      const int r = 16 * warp + 2 * i + (lane >> 4);
+      uint32_t b = Elem<ELEM>::nans(w[i]) << (8 * (lane & 3));
+      some |= b;
+      b |= __shfl_xor_sync(0xffffffffu, b, 1);
+      b |= __shfl_xor_sync(0xffffffffu, b, 2);
+      if ((lane & 3) == 0) sh.need[r][lane >> 2 & 3] = b;
+    }
+    for (int i = tid; i < kKinds * kW8T * 4; i += kAgThreads) (&sh.seen[0][0][0])[i] = 0;
+    if (tid < kKinds * 4) (&sh.all[0][0])[tid] = 0;
+    if (tid < 4) sh.unseen[tid] = 0;
+    if (!__syncthreads_or(some != 0)) continue;
+    // what is not finite: of every key that some token sees, or that a step beside
+    // those holds (no step of the item's lies outside the tiles of 128 keys that its
+    // 2 tq rows see some of)
+    const int beside = 2 * tq + kW8T, q1 = q0 + nt - 1;
+    const int lo = a.w.window > 0 ? max(q0 - a.w.window + 1 - beside, 0) : 0;
+    const int first = a.w.window > 0 && a.w.sinks > 0 ? min(a.w.sinks, it.n0 - kW8T) + kW8T : 0;
+    const AgKeys key(first, lo, (int)min((long long)q1 + 1 + beside, (long long)it.n0));
+    const int looks = (key.total + kAgLook - 1) / kAgLook;
+    bool left = true;
+#pragma unroll 1
+    for (int n = 0; left && n < looks; n++) {
+      const int from = (n == 0 ? 0 : looks - n) * kAgLook, end = min(from + kAgLook, key.total);
+#pragma unroll 1
+      for (int y = from; y < end; y += 8 * (kAgThreads / 16)) {
+        uint4 z[8];
+        bool bad = false;
+        auto at = [&](int i) { return key(min(y + i * (kAgThreads / 16) + (tid >> 4), end - 1)); };   // the last one several times
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        o[e] = fmaf(p, z[e], o[e] * f);
-        open |= doubt[e] && o[e] == o[e];      // an infinite sum may still meet its opposite
+        for (int i = 0; i < 8; i++) {
+          const long long j = (long long)it.t0 + at(i);
+          w[i] = *reinterpret_cast<const uint4*>(a.k + j * a.ks + it.h * (2 * kD) + 16 * (tid & 15));
+          z[i] = *reinterpret_cast<const uint4*>(a.v + j * a.vs + it.h * (2 * kD) + 16 * (tid & 15));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) bad |= !Elem<ELEM>::all_finite(w[i]) || !Elem<ELEM>::all_finite(z[i]);
+        if (!__any_sync(0xffffffffu, bad)) continue;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          // of the whole key: a NaN makes its logit NaN, an infinite entry NaN or
+          // infinite, and then what it gives of an infinite value is NaN
+          const bool none = __ballot_sync(0xffffffffu, Elem<ELEM>::nans(w[i]) != 0) >> (lane & 16) & 0xffffu;
+          const bool odd = __ballot_sync(0xffffffffu, !Elem<ELEM>::all_finite(w[i])) >> (lane & 16) & 0xffffu;
+          uint32_t nan = Elem<ELEM>::nans(z[i]), up = Elem<ELEM>::equal(z[i], Elem<ELEM>::kInf);
+          uint32_t down = Elem<ELEM>::equal(z[i], Elem<ELEM>::kInf | 0x80008000u);
+          if (odd) nan |= up | down;
+          if (none) nan = 0xffu;
+          if (nan | up | down) mark(sh, q0, nt, a.w, at(i), tid & 15, nan, up, down);
+        }
       }
-      if (!finite(l) || !__any_sync(0xffffffffu, open)) break;
+      __syncthreads();
+      bool open = false;
+      if (tid < nt * G)
+        for (int e = 0; e < 4; e++) open |= (sh.need[tid][e] & ~row_of(sh, tid / G, e).nan) != 0;
+      left = __syncthreads_or(open);
     }
-    const float inv = __fdiv_rn(1.0f, l);
-#pragma unroll
-    for (int e = 0; e < 4; e++)
-      if (doubt[e]) reinterpret_cast<uint16_t*>(out)[e] = float_elem<ELEM>(o[e] * inv);
+    if (!left) continue;
+    bool again = false;
+    if (tid < nt * G) {
+      uint32_t* need = sh.need[tid];
+      // a row with a feature that is not NaN has weights that are not: what is
+      // infinite of it needs no computing
+      const bool sure = (need[0] & need[1] & need[2] & need[3]) != 0xffffffffu;
+      uint16_t* out = reinterpret_cast<uint16_t*>(
+          a.out + (((long long)(it.t0 + q0 + tid / G) * c.hkv + it.h) * G + tid % G) * (2 * kD));
+      for (int e = 0; e < 4; e++) {
+        const AgRow r = row_of(sh, tid / G, e);
+        uint32_t x = need[e] & ~r.nan, inf = x & (r.up | r.down);
+        if (sure) {
+          for (uint32_t f = inf; f; f &= f - 1) {
+            const int b = __ffs(f) - 1;
+            out[32 * e + b] = float_elem<ELEM>(r.up >> b & 1u ? INFINITY : -INFINITY);
+          }
+          x &= ~inf;
+          inf = 0;
+        }
+        need[e] = x & (inf | sh.unseen[e]);
+        again |= need[e] != 0;
+      }
+    }
+    if (!__syncthreads_or(again)) continue;
+    half_again<ELEM>(sh, c, a, it, q0, nt);
   }
 }
 
@@ -699,9 +989,9 @@ cudaError_t launch_prefill8(const Cache8View& c, int elem, const int32_t* seq_le
                        W8Args{static_cast<uint8_t*>(out), window, sinks, tq}, call);
   if (e != cudaSuccess) return e;
   const Again8 again{static_cast<uint8_t*>(out),       static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(k),
-                     static_cast<const uint8_t*>(v), 2 * qs, 2 * ks, 2 * vs, window, sinks};
-  return launch_dependent(elem == DKV_F16 ? k_prefill8_again<DKV_F16> : k_prefill8_again<DKV_BF16>, dim3(std::max(1, sm_count / 4)),
-                          dim3(512), 0, st, c, again, call);
+                     static_cast<const uint8_t*>(v), 2 * qs, 2 * ks, 2 * vs, W8Args{static_cast<uint8_t*>(out), window, sinks, tq}};
+  return launch_dependent(elem == DKV_F16 ? k_prefill8_again<DKV_F16> : k_prefill8_again<DKV_BF16>, dim3(sm_count),
+                          dim3(kAgThreads), 0, st, c, again, call);
 }
 
 }  // namespace dkv

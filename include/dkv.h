@@ -530,9 +530,12 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
  * Products accumulate in fp32; probabilities enter the value product rounded
  * to elem_type; the same inputs give the same bits, whatever else is in the
  * call. What a row does not see never enters its result, whatever it holds:
- * rows that come out infinite or NaN are computed again by themselves, and
- * status[2] goes on; while it is on, every call looks through its whole result
- * for such rows (until the caller zeroes it).
+ * where rows come out infinite or NaN, status[2] goes on, the call looks through
+ * its results, keys and values for the reason, and computes again what a value
+ * out of its sight has touched. One such value costs up to half the call's time
+ * again, such values in every few hundred tokens up to 14 times it. While
+ * status[2] is on, every call looks through its whole result for such rows (until
+ * the caller zeroes it).
  * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED (host, nothing queued);
  * DKV_ERR_CUDA. */
 int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* seq_lens, const void* q,

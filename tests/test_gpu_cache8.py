@@ -1097,3 +1097,85 @@ def test_prefill_of_infinite_values_of_both_signs(elem, window, sinks):
         g = got[p]
         assert np.isnan(g[:, nan]).all() and (g[:, up & ~nan] == inf).all() and (g[:, down & ~nan] == -inf).all(), p
         assert np.isfinite(g[:, ~(up | down | nan)]).all(), p
+
+
+def scattered(rng, x, share, kinds=(float("nan"), float("inf"), float("-inf"))):
+    """x with a share of its entries not finite."""
+    x = x.clone()
+    hit = torch.from_numpy(rng.random(tuple(x.shape)) < share).cuda()
+    x[hit] = torch.from_numpy(rng.choice(np.float32(kinds), int(hit.sum()))).to(x.dtype).cuda()
+    return x
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("elem,window,sinks,share", [(F16, 0, 0, 2e-4), (BF16, 50, 3, 2e-3), (F16, 129, 200, 2e-4), (BF16, 300, 0, 2e-5),
+                                                     (F16, 17, 70, 2e-2), (F16, 64, 1, 0.5)])
+def test_prefill_of_scattered_values_that_are_not_finite(G, elem, window, sinks, share):
+    """Every row against the definition, feature by feature: NaN, +Inf, -Inf or the
+    number that the keys which it sees give."""
+    rng = np.random.default_rng(1000 * G + window)
+    lens, hkv = [1, 290, 37, 405], 2
+    c = Cache(hkv, G, 16, 1, 1, elem, E4M3)
+    n = sum(lens)
+    q, k, v = c.vec(rng, n, hkv * G), c.vec(rng, n, hkv), c.vec(rng, n, hkv)
+    v = scattered(rng, v, share)
+    if share < 1e-3:
+        k = scattered(rng, k, 2e-5)
+        q[[5, 300], 1 % G] = float("nan")
+    out = torch.empty_like(q)
+    _dkv().dkv_cache8_prefill(c.c, lens, q, k, v, out, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert c.c.status_words.tolist() == [0, 0]
+    got, qn, kn, vn = (x.double().cpu().numpy() for x in (out, q, k, v))
+    at = 0
+    with np.errstate(invalid="ignore"):
+        for m in lens:
+            for p in range(m):
+                see = at + ref.visible(p + 1, window, sinks)
+                for h in range(hkv):
+                    x, kk = vn[see, h], kn[see, h]
+                    up, down = (x == np.inf).any(axis=0), (x == -np.inf).any(axis=0)
+                    for g in range(h * G, (h + 1) * G):
+                        s = kk @ qn[at + p, g] / np.sqrt(128)
+                        nan = np.isnan(x).any(axis=0) | (up & down) | np.isinf(x[s == -np.inf]).any(axis=0)
+                        use = s > -np.inf
+                        if np.isnan(s).any() or (s == np.inf).any() or not use.any():
+                            nan[:] = True
+                        r = got[at + p, g]
+                        assert np.isnan(r[nan]).all() and (r[up & ~nan] == np.inf).all() and (r[down & ~nan] == -np.inf).all(), (p, g)
+                        rest = ~(nan | up | down)
+                        if rest.any():
+                            y = np.where(np.isfinite(x[use]), x[use], 0)
+                            want, pv, qk, vm = ref.attend(qn[at + p, g:g + 1], kk[use], y)
+                            tol = ref.tolerance(want, pv, qk, vm, len(see), elem, torch.finfo(elem).eps / 2)
+                            assert (np.abs(r - want[0]) <= tol[0])[rest].all(), (p, g)
+            at += m
+
+
+def test_prefill_cost_of_one_value_that_is_not_finite():
+    """One NaN in a first token that every row sees, or in its key: no more than a
+    look through the results and the values beside the call itself."""
+    rng = np.random.default_rng(0)
+    n, hkv, G, window, sinks = 8192, 4, 8, 2048, 16
+    c = Cache(hkv, G, 16, 1, 1, F16, E4M3)
+    q, k, v = c.vec(rng, n, hkv * G), c.vec(rng, n, hkv), c.vec(rng, n, hkv)
+    out = torch.empty_like(q)
+    bad_v, bad_k = v.clone(), k.clone()
+    bad_v[3, :, 17], bad_k[3, :, 17] = float("nan"), float("nan")
+
+    def time_of(k, v):
+        best = []
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            c.c.tensors[4].zero_()
+            a.record()
+            _dkv().dkv_cache8_prefill(c.c, [n], q, k, v, out, window=window, sinks=sinks)
+            b.record()
+            torch.cuda.synchronize()
+            best.append(a.elapsed_time(b))
+        return min(best[1:])
+
+    clean = time_of(k, v)
+    for kk, vv in ((k, bad_v), (bad_k, v)):
+        assert time_of(kk, vv) < 3 * clean      # by a walk through every row's keys: hundreds
+        assert torch.isnan(out[3:]).any(dim=2).all()
