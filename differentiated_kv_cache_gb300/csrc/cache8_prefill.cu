@@ -77,6 +77,11 @@ constexpr uint32_t kW8OCol = 256;          // S of the halves, then O of the hal
 constexpr uint32_t kW8Cols = 512;
 constexpr float kW8Most = 4096.0f;         // largest sum of a row's P of one tile (fp16 holds 65504)
 
+// status[3], zero between calls: a row of this call came out infinite or NaN; the
+// blocks of the second kernel then count themselves in the bits below, and the last
+// one puts the zero back.
+constexpr int kLook = 1 << 30;
+
 constexpr int kW8Req = 1024;
 struct W8Call {
   int n_req;
@@ -568,7 +573,10 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         }
         __syncwarp();
       }
-      if (real && ((bad[0] | bad[1] | bad[2] | bad[3]) & 0x7fff7fffu)) c.status[2] = 1;
+      if (real && ((bad[0] | bad[1] | bad[2] | bad[3]) & 0x7fff7fffu)) {
+        c.status[2] = 1;
+        c.status[3] = kLook;
+      }
       it = then;
       tc_fence_before();
     }
@@ -838,7 +846,7 @@ template <int ELEM>
 __global__ void __launch_bounds__(kAgThreads, 1) k_prefill8_again(Cache8View c, Again8 a, const __grid_constant__ W8Call call) {
   pdl_launch_dependents();
   pdl_wait();
-  if (c.stopped() || *(volatile int*)(c.status + 2) == 0) return;
+  if (c.stopped() || (*(volatile int*)(c.status + 3) & kLook) == 0) return;
   __shared__ AgShared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x, G = c.G, tq = a.w.tq;
   const long long halves = 2ll * call.tile0[call.n_req] * c.hkv;
@@ -944,6 +952,8 @@ __global__ void __launch_bounds__(kAgThreads, 1) k_prefill8_again(Cache8View c, 
     if (!__syncthreads_or(again)) continue;
     half_again<ELEM>(sh, c, a, it, q0, nt);
   }
+  __syncthreads();             // every thread has read the word
+  if (tid == 0 && atomicAdd(c.status + 3, 1) == (kLook | ((int)gridDim.x - 1))) c.status[3] = 0;
 }
 
 // [n_tok][heads][128] 16-bit vectors, token rows `stride` elements apart; box

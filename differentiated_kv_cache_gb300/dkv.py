@@ -345,6 +345,7 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
         raise ValueError("status has four words")
     c.workspace_bytes = workspace.numel()
     c.elem_dtype, c.status_words = tail.dtype, status[:2]     # error and its request
+    c.not_finite = status[2:3]        # 1 once a row of prompt attention came out infinite or NaN; the caller may zero it
     # plain copies of what every call reads
     c.address, c.heads, c.q_heads, c.pairs = C.addressof(c), hkv, hkv * group_size, rotary_dim // 2
     c.tensors = (pages, scales, tail, page_table, status, workspace)

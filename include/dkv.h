@@ -442,7 +442,9 @@ int dkv_pool_export(dkv_pool* pool, dkv_snapshot* out);
  *  - Calls on one cache must be ordered on one stream (or synchronised by the
  *    caller). Attention calls that may overlap (two streams, two replayed
  *    graphs) need a workspace each; others may share one if n_kv_heads and
- *    group_size are the same. Appends and prompt attention use none. */
+ *    group_size are the same. Appends and prompt attention use none. The same
+ *    goes for the status words: caches whose prompt attention may overlap need
+ *    their own. */
 #define DKV_F16  0   /* elem_type: k, v, q, out and tails are IEEE binary16 */
 #define DKV_BF16 1   /* elem_type: bfloat16                                  */
 #define DKV_E4M3 0   /* code_type: 8-bit floating point (4 exponent bits)    */
@@ -467,7 +469,8 @@ typedef struct dkv_cache8 {
   float* scales;               /* [n_pages][Hkv][2]: K's and V's s             */
   void* tail;                  /* [n_slots][Hkv][T/16][2][2048] elem_type      */
   const int32_t* page_table;   /* [n_slots][table_width]                       */
-  int32_t* status;             /* [4], zeroed by the caller                    */
+  int32_t* status;             /* [4], zeroed by the caller: error, its request,
+                                  results not finite, the calls' own           */
   void* workspace;             /* dkv_cache8_workspace bytes, zeroed once by
                                   the caller (every call leaves the zeros
                                   that it found); NULL if no attention         */
@@ -533,9 +536,9 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
  * where rows come out infinite or NaN, status[2] goes on, the call looks through
  * its results, keys and values for the reason, and computes again what a value
  * out of its sight has touched. One such value costs up to half the call's time
- * again, such values in every few hundred tokens up to 14 times it. While
- * status[2] is on, every call looks through its whole result for such rows (until
- * the caller zeroes it).
+ * again, such values in every few hundred tokens up to 14 times it; calls without
+ * them cost the same before and after. status[2] stays on until the caller zeroes
+ * it (nothing reads it); status[3] is the call's own and zero between calls.
  * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED (host, nothing queued);
  * DKV_ERR_CUDA. */
 int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* seq_lens, const void* q,

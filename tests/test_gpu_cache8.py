@@ -1179,3 +1179,35 @@ def test_prefill_cost_of_one_value_that_is_not_finite():
     for kk, vv in ((k, bad_v), (bad_k, v)):
         assert time_of(kk, vv) < 3 * clean      # by a walk through every row's keys: hundreds
         assert torch.isnan(out[3:]).any(dim=2).all()
+
+
+def test_prefill_looks_for_values_that_are_not_finite_in_their_own_call_only():
+    """A call with an infinite value leaves a mark for the caller and no cost to later
+    calls (a look through their results would more than double this shape's time)."""
+    rng = np.random.default_rng(1)
+    lens, hkv, G = [4096] * 8, 8, 8
+    c = Cache(hkv, G, 16, 1, 1, BF16, E4M3)
+    q, k, v = (torch.randn((sum(lens), n, 128), device="cuda").to(BF16) for n in (hkv * G, hkv, hkv))
+    out, bad = torch.empty_like(q), v.clone()
+    bad[77] = float("inf")
+
+    def run(v):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        _dkv().dkv_cache8_prefill(c.c, lens, q, k, v, out, window=32)
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b)
+
+    before = min(run(v) for _ in range(10))
+    want = out.clone()
+    assert c.c.not_finite.item() == 0
+    run(bad)
+    assert c.c.not_finite.item() == 1 and c.c.tensors[4].tolist() == [0, 0, 1, 0]
+    after = min(run(v) for _ in range(10))
+    assert torch.equal(out, want) and c.c.tensors[4].tolist() == [0, 0, 1, 0]
+    assert after < 1.15 * before, (before, after)
+    c.c.not_finite.zero_()
+    run(bad)
+    assert c.c.tensors[4].tolist() == [0, 0, 1, 0] and not torch.isfinite(out[77:77 + 32]).any()
+    assert torch.isfinite(out[:77]).all() and torch.isfinite(out[77 + 32:]).all()
