@@ -307,8 +307,9 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
     scales fp32 [n_pages][Hkv][2], tail [n_slots][Hkv][T/16][2][2048] (float16
     or bfloat16), page_table int32 [n_slots][width]. The status words and the
     workspace for attention calls of up to max_req requests (default: one a
-    slot, at most 1024) are allocated here unless given; layers of one head layout
-    whose calls are ordered on one stream may share a workspace."""
+    slot, at most 1024) are allocated here unless given, and zero when this returns
+    (made while a graph is captured: by the graph); layers of one head layout whose
+    calls are ordered on one stream may share a workspace."""
     import torch
     codes = {torch.float8_e4m3fn: DKV_E4M3, torch.int8: DKV_INT8}
     elems = {torch.float16: DKV_F16, torch.bfloat16: DKV_BF16}
@@ -331,6 +332,7 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
     c.device = c.dev = pages.get_device()
     if c.dev < 0:
         raise TypeError("the cache's tensors must be CUDA tensors")
+    ours = status is None or workspace is None
     if status is None:
         status = torch.zeros(4, dtype=torch.int32, device=pages.device)
     if workspace is None:
@@ -338,6 +340,9 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
         _check(load().dkv_cache8_workspace(C.byref(c), min(c.n_slots, 1024) if max_req is None else int(max_req),
                                            C.byref(n)), "dkv_cache8_workspace")
         workspace = torch.zeros(n.value, dtype=torch.uint8, device=pages.device)
+    with torch.cuda.device(pages.device):      # the first call may be on any stream
+        if ours and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
     c.pages, c.scales = _on(c, pages, pages.dtype, "pages"), _on(c, scales, torch.float32, "scales")
     c.tail, c.page_table = _on(c, tail, tail.dtype, "tail"), _on(c, page_table, torch.int32, "page_table")
     c.status, c.workspace = _on(c, status, torch.int32, "status"), _on(c, workspace, torch.uint8, "workspace")

@@ -1211,3 +1211,23 @@ def test_prefill_looks_for_values_that_are_not_finite_in_their_own_call_only():
     run(bad)
     assert c.c.tensors[4].tolist() == [0, 0, 1, 0] and not torch.isfinite(out[77:77 + 32]).any()
     assert torch.isfinite(out[:77]).all() and torch.isfinite(out[77 + 32:]).all()
+
+
+def test_first_call_on_another_stream_than_the_descriptor_was_made_on():
+    """Status words and workspace are zero when make_cache8 returns, whatever the
+    stream that it ran on still has to do."""
+    dkv = _dkv()
+    lens = [3000, 700, 1]
+    c, slots, q = filled(4, 4, 64, F16, E4M3, lens, seed=1)
+    want = c.attend(slots, lens, q)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    sl, ln, out, side = i32(slots), i32(lens), torch.full_like(q, float("nan")), torch.cuda.Stream()
+    size = c.c.tensors[5].numel()
+    dirty = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (size, 16)]
+    torch.cuda.synchronize()
+    del dirty                            # the next allocations of these sizes
+    torch.cuda._sleep(100_000_000)       # some 50 ms
+    d = dkv.make_cache8(c.pages, c.scales, c.tail, c.table, group_size=4)
+    dkv.dkv_cache8_attention(d, ln, q, out, slots=sl, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and d.tensors[4].tolist() == [0] * 4 and not torch.isnan(out).any()
