@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from array import array
 
 import numpy as np
 
@@ -383,14 +384,21 @@ def _rows(cache, t, heads, n, name):
 
 def _lens8(x):
     """Host lengths as a C array: the array (its owner keeps it alive), its
-    address, entries and sum. A list of ints is converted without numpy."""
-    if type(x) is list:
-        try:
-            a = (C.c_int32 * len(x))(*x)
-            return a, C.addressof(a), len(x), sum(x)
-        except TypeError:
-            pass
-    a = _i32(x)
+    address, entries and sum. A list of ints is converted without numpy. What
+    32-bit integers do not hold is refused."""
+    try:
+        if type(x) is list:
+            try:
+                a = array("i", x)
+                return a, a.buffer_info()[0], len(x), sum(x)
+            except TypeError:
+                pass
+        with np.errstate(invalid="ignore"):
+            a = _i32(x)
+    except OverflowError as e:
+        raise ValueError(f"lengths are 32-bit integers: {e}") from None
+    if not np.array_equal(a, np.asarray(x).reshape(-1)):
+        raise ValueError("lengths are 32-bit integers")
     return a, a.ctypes.data, a.size, int(a.sum(dtype=np.int64))
 
 

@@ -155,3 +155,10 @@ def test_bad_workspace_requests_are_refused():
 def test_host_lengths(given):
     keep, address, n, total = dkv.dkv._lens8(given)
     assert (n, total) == (3, 44) and list((C.c_int32 * 3).from_address(address)) == [3, 1, 40]
+
+
+@pytest.mark.parametrize("given", [[2 ** 32 + 2, 1], [2 ** 32 + 2, -2 ** 32 + 1], [3, -2 ** 32 + 1], (2 ** 31, 1), [-2 ** 31 - 1],
+                                   np.array([2 ** 32 + 2, 1]), np.array([2.0 ** 31]), [2.5, 1], np.array([1.5])])
+def test_host_lengths_beyond_32_bits_are_refused(given):
+    with pytest.raises(ValueError):
+        dkv.dkv._lens8(given)
