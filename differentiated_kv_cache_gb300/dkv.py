@@ -402,6 +402,11 @@ def _lens8(x):
     return a, a.ctypes.data, a.size, int(a.sum(dtype=np.int64))
 
 
+def _window8(window, sinks):
+    if abs(window) | abs(sinks) > 0x7fffffff:       # ctypes would wrap them
+        raise ValueError("window and sinks are 32-bit integers")
+
+
 def _stream8(cache, stream):
     import torch
     return torch._C._cuda_getCurrentRawStream(cache.dev) if stream is None else stream.cuda_stream
@@ -443,6 +448,7 @@ def dkv_cache8_attention(cache: dkv_cache8, seq_lens, q, out, window: int = 0, s
     cache: seq_lens (device int32 [n_req]) tokens are stored; window = 0 sees
     them all, else the last `window` and the first `sinks`."""
     import torch
+    _window8(window, sinks)
     n_req = seq_lens.numel()
     qp, qs = _rows(cache, q, cache.q_heads, n_req, "q")
     rc = load().dkv_cache8_attention(cache.address, n_req, _on(cache, slots, torch.int32, "slots", n_req),
@@ -456,6 +462,7 @@ def dkv_cache8_prefill(cache: dkv_cache8, seq_lens, q, k, v, out, window: int = 
                        check: bool = True) -> int:
     """Causal attention over whole prompts (host lengths, requests back to
     back) with an optional sliding window and first tokens that stay visible."""
+    _window8(window, sinks)
     keep, lens, n_req, total = _lens8(seq_lens)
     qp, qs = _rows(cache, q, cache.q_heads, total, "q")
     kp, ks = _rows(cache, k, cache.heads, total, "k")

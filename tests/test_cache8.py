@@ -162,3 +162,11 @@ def test_host_lengths(given):
 def test_host_lengths_beyond_32_bits_are_refused(given):
     with pytest.raises(ValueError):
         dkv.dkv._lens8(given)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 32, 0), (2 ** 32 + 5, 4), (2 ** 31, 0), (5, 2 ** 32), (-2 ** 32, 0), (5, -2 ** 32 + 1)])
+def test_windows_beyond_32_bits_are_refused(window, sinks):
+    for call in (lambda: dkv.dkv_cache8_attention(None, None, None, None, window=window, sinks=sinks),
+                 lambda: dkv.dkv_cache8_prefill(None, None, None, None, None, None, window=window, sinks=sinks)):
+        with pytest.raises(ValueError):
+            call()
