@@ -460,6 +460,13 @@ struct Device8 {
   int want;
 };
 
+// The caller's own next check of CUDA's last error is not to find this call's.
+int result(cudaError_t e) {
+  if (e == cudaSuccess) return DKV_OK;
+  cudaGetLastError();
+  return DKV_ERR_CUDA;
+}
+
 bool at(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Shape fields only (the pointers may be NULL).
@@ -527,7 +534,7 @@ int dkv_cache8_workspace(const dkv_cache8* cache, int32_t max_req, int64_t* byte
   if (rc) return rc;
   if (!bytes || max_req < 1 || max_req > kMaxCallReq) return DKV_ERR_ARG;
   const int sms = sm_count(cache->device);
-  if (!sms) return DKV_ERR_CUDA;
+  if (!sms) return result(cudaErrorInvalidDevice);
   *bytes = (int64_t)attention8_workspace(cache->n_kv_heads, cache->group_size, max_req, sms);
   return DKV_OK;
 }
@@ -559,7 +566,7 @@ int dkv_cache8_append(const dkv_cache8* cache, int32_t n_req, const int32_t* n_n
     }
   }
   Device8 dev(cache->device);
-  if (!dev.ok) return DKV_ERR_CUDA;
+  if (!dev.ok) return result(cudaErrorInvalidDevice);
   Append8Args a;
   a.k = static_cast<const uint8_t*>(k);
   a.v = static_cast<const uint8_t*>(v);
@@ -575,7 +582,7 @@ int dkv_cache8_append(const dkv_cache8* cache, int32_t n_req, const int32_t* n_n
   a.before = before;
   const cudaError_t e = launch_append8(view(cache), cache->elem_type, cache->code_type, a, n_req, n_new,
                                        reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? DKV_OK : DKV_ERR_CUDA;
+  return result(e);
 }
 
 int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* slots, const int32_t* seq_lens,
@@ -592,16 +599,16 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
     return DKV_ERR_ARG;
   if (!cache->workspace || !at(cache->workspace, 16)) return DKV_ERR_ARG;
   Device8 dev(cache->device);
-  if (!dev.ok) return DKV_ERR_CUDA;
+  if (!dev.ok) return result(cudaErrorInvalidDevice);
   const int sms = sm_count(cache->device);
-  if (!sms) return DKV_ERR_CUDA;
+  if (!sms) return result(cudaErrorInvalidDevice);
   if (cache->workspace_bytes < (int64_t)attention8_workspace(hkv, cache->group_size, n_req, sms)) return DKV_ERR_SCRATCH;
   // a window that no length exceeds is none (and positions minus it stay in 32 bits)
   if (window >= (long long)cache->table_width * cache->block_tokens) window = 0;
   const cudaError_t e =
       launch_attention8(view(cache), cache->elem_type, cache->code_type, sms, slots, seq_lens, n_req, q, q_stride, out,
                         window, sinks, cache->workspace, reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? DKV_OK : DKV_ERR_CUDA;
+  return result(e);
 }
 
 int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* seq_lens, const void* q,
@@ -624,13 +631,13 @@ int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* se
     if (tok > 0x7fffff00ll || tiles * hkv > 0x7ffffff0ll) return DKV_ERR_ARG;   // rows and tiles are 32-bit
   }
   Device8 dev(cache->device);
-  if (!dev.ok) return DKV_ERR_CUDA;
+  if (!dev.ok) return result(cudaErrorInvalidDevice);
   const int sms = sm_count(cache->device);
-  if (!sms) return DKV_ERR_CUDA;
+  if (!sms) return result(cudaErrorInvalidDevice);
   if (window >= longest) window = 0;   // as above
   const cudaError_t e = launch_prefill8(view(cache), cache->elem_type, seq_lens, n_req, q, q_stride, k, k_stride, v,
                                         v_stride, out, window, sinks, sms, reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? DKV_OK : DKV_ERR_CUDA;
+  return result(e);
 }
 
 }  // extern "C"

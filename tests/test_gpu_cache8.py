@@ -1231,3 +1231,20 @@ def test_first_call_on_another_stream_than_the_descriptor_was_made_on():
     dkv.dkv_cache8_attention(d, ln, q, out, slots=sl, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and d.tensors[4].tolist() == [0] * 4 and not torch.isnan(out).any()
+
+
+def test_a_device_that_is_not_there_leaves_no_error_behind():
+    import ctypes as C
+    dkv = _dkv()
+    c = Cache(2, 2, 16, 4, 3, F16, E4M3)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    x, y, ln = (torch.zeros((4, n, 128), dtype=F16, device="cuda") for n in (4, 2, 1))
+    out, ln = torch.empty_like(x), i32([1] * 4)
+    n = C.c_int64()
+    c.c.device = torch.cuda.device_count()
+    for call in (lambda: dkv.load().dkv_cache8_workspace(c.c.address, 4, C.byref(n)),
+                 lambda: dkv.dkv_cache8_append(c.c, ln, y, y, check=False),
+                 lambda: dkv.dkv_cache8_attention(c.c, ln, x, out, check=False),
+                 lambda: dkv.dkv_cache8_prefill(c.c, [4], x, y, y, out, check=False)):
+        assert call() == dkv.DKV_ERR_CUDA
+        assert torch.ones(3, device="cuda").mul(2).sum().item() == 6      # raises what is left behind
