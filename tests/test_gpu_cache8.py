@@ -1248,3 +1248,37 @@ def test_a_device_that_is_not_there_leaves_no_error_behind():
                  lambda: dkv.dkv_cache8_prefill(c.c, [4], x, y, y, out, check=False)):
         assert call() == dkv.DKV_ERR_CUDA
         assert torch.ones(3, device="cuda").mul(2).sum().item() == 6      # raises what is left behind
+
+
+def test_which_error_and_which_request():
+    """One slot given to several requests, and a position behind the page table and the
+    rotation table both: one code each, of a request concerned."""
+    dkv = _dkv()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(2)
+    for step in (False, True):
+        c = Cache(2, 2, 16, 4, 3, F16, E4M3, rot=32)
+        k, v = c.vec(rng, 4, 2), c.vec(rng, 4, 2)
+        dkv.dkv_cache8_append(c.c, i32([0] * 4), k, v, rope=c.rope, n_new=None if step else [1] * 4, slots=i32([3, 1, 0, 1]))
+        torch.cuda.synchronize()
+        error, request = c.c.status_words.tolist()
+        assert error == dkv.DKV_ERR_ARG and request in (1, 3)
+    for before, want in ((40, dkv.DKV_ERR_TABLE_FULL), (39, dkv.DKV_ERR_ARG)):     # 49 and 48 tokens of 48 places, 44 positions
+        c = Cache(2, 2, 16, 1, 3, F16, E4M3, rot=32)
+        k, v = c.vec(rng, 9, 2), c.vec(rng, 9, 2)
+        dkv.dkv_cache8_append(c.c, i32([before]), k, v, rope=c.rope[:44], n_new=[9])
+        torch.cuda.synchronize()
+        assert c.c.status_words.tolist() == [want, 0]
+
+
+def test_lengths_below_what_is_stored():
+    """The open block holds the newest tokens: any length inside it is good, and any
+    end of a block; a slot may occur with several of them."""
+    stored, T = 150, 32
+    lens = [150, 149, 129, 128, 96, 64, 32, 0]
+    c, slots, _ = filled(2, 4, T, BF16, INT8, [stored, 20], seed=5)
+    q = c.vec(np.random.default_rng(5), len(lens), 8)
+    who = [slots[0]] * len(lens)
+    for window, sinks in ((0, 0), (40, 3)):
+        out = c.attend(who, lens, q, window, sinks)
+        c.check_attention(out, who, lens, q, window, sinks)
