@@ -282,71 +282,70 @@ __global__ void __launch_bounds__(kW8Threads, 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kW8RegsFew));
-  if (warp == 0) {
-    // ---- copies: an item's first K tile, its queries, then K(j + 1) ahead of V(j) ----
-    if (lane == 0) {
-      int nk = 0, nv = 0, nq = 0;      // K tiles, V tiles and items so far
-      int done = 0;                    // steps of the tiles whose K is loaded
-      int end[2] = {0, 0};             // last step of the latest tile of each stage
-      int vend[2] = {0, 0};
-      bool ok = true;
-      auto load = [&](const Item& it, int j, bool is_k) {
-        const int t = is_k ? nk : nv, s = t & 1;
-        const uint32_t full = is_k ? kfull(s) : vfull(s);
-        const int e = is_k ? end[s] : vend[s];
-        if (t >= 2)          // tile t - 2 of the stage is done with
-          for (int h = 0; h < 2; h++)
-            if (!mbar_wait_bounded(is_k ? sdone(h, e) : pvdone(h, e), (e >> 2) & 1)) return false;
-        mbar_expect_tx(full, kW8Tile);
-        for (int f = 0; f < 2; f++)
-          tma_load_3d(smem_u32(smem + (is_k ? kW8OffK : kW8OffV) + s * kW8Tile + f * kW8Half), is_k ? &tk : &tv,
-                      64 * f, it.h, it.t0 + it.key(j), full);
-        if (is_k) {
-          nk++;
-          done += (it.step(it.key(j)) ? 1 : 0) + (it.step(it.key(j) + 64) ? 1 : 0);
-          end[s] = done - 1;
-        } else {
-          nv++;
-          vend[s] = end[s];            // K of the tile after next is not loaded yet
+    if (warp == 0) {
+      // ---- copies: an item's first K tile, its queries, then K(j + 1) ahead of V(j) ----
+      if (lane == 0) {
+        int nk = 0, nv = 0, nq = 0;      // K tiles, V tiles and items so far
+        int done = 0;                    // steps of the tiles whose K is loaded
+        int end[2] = {0, 0};             // last step of the latest tile of each stage
+        int vend[2] = {0, 0};
+        bool ok = true;
+        auto load = [&](const Item& it, int j, bool is_k) {
+          const int t = is_k ? nk : nv, s = t & 1;
+          const uint32_t full = is_k ? kfull(s) : vfull(s);
+          const int e = is_k ? end[s] : vend[s];
+          if (t >= 2)          // tile t - 2 of the stage is done with
+            for (int h = 0; h < 2; h++)
+              if (!mbar_wait_bounded(is_k ? sdone(h, e) : pvdone(h, e), (e >> 2) & 1)) return false;
+          mbar_expect_tx(full, kW8Tile);
+          for (int f = 0; f < 2; f++)
+            tma_load_3d(smem_u32(smem + (is_k ? kW8OffK : kW8OffV) + s * kW8Tile + f * kW8Half), is_k ? &tk : &tv,
+                        64 * f, it.h, it.t0 + it.key(j), full);
+          if (is_k) {
+            nk++;
+            done += (it.step(it.key(j)) ? 1 : 0) + (it.step(it.key(j) + 64) ? 1 : 0);
+            end[s] = done - 1;
+          } else {
+            nv++;
+            vend[s] = end[s];            // K of the tile after next is not loaded yet
+          }
+          return true;
+        };
+        int asked = 0;
+        for (int x = blockIdx.x; x >= 0 && !failed();) {
+          fence_proxy_async();
+          ask_item(answer(asked), told(asked));
+          asked++;
+          const Item it = item_of(x, c, a, call);
+          const int last = done - 1;     // the last step of the item before
+          ok = load(it, 0, true);
+          if (nq > 0)
+            for (int h = 0; h < 2; h++) ok = ok && mbar_wait_bounded(sdone(h, last), (last >> 2) & 1);
+          if (!ok) break;
+          mbar_expect_tx(qfull, (uint32_t)(4 * 128 * a.tq * G));
+          for (int f = 0; f < 4; f++)
+            tma_load_3d(smem_u32(smem + f * kW8Half), &tq, 64 * (f & 1), it.h * G, it.t0 + it.p0 + (f >> 1) * a.tq, qfull);
+          nq++;
+          for (int j = 0; ok && j < it.count && !failed(); j++) {
+            if (j + 1 < it.count) ok = load(it, j + 1, true);
+            if (ok) ok = load(it, j, false);
+          }
+          if (!ok) break;
+          ok = mbar_wait_bounded(told(asked - 1), ((asked - 1) / kW8Next) & 1);
+          if (!ok) break;
+          x = told_item(answer(asked - 1));
         }
-        return true;
-      };
-      int asked = 0;
-      for (int x = blockIdx.x; x >= 0 && !failed();) {
-        fence_proxy_async();
-        ask_item(answer(asked), told(asked));
-        asked++;
-        const Item it = item_of(x, c, a, call);
-        const int last = done - 1;     // the last step of the item before
-        ok = load(it, 0, true);
-        if (nq > 0)
-          for (int h = 0; h < 2; h++) ok = ok && mbar_wait_bounded(sdone(h, last), (last >> 2) & 1);
-        if (!ok) break;
-        mbar_expect_tx(qfull, (uint32_t)(4 * 128 * a.tq * G));
-        for (int f = 0; f < 4; f++)
-          tma_load_3d(smem_u32(smem + f * kW8Half), &tq, 64 * (f & 1), it.h * G, it.t0 + it.p0 + (f >> 1) * a.tq, qfull);
-        nq++;
-        for (int j = 0; ok && j < it.count && !failed(); j++) {
-          if (j + 1 < it.count) ok = load(it, j + 1, true);
-          if (ok) ok = load(it, j, false);
-        }
-        if (!ok) break;
-        ok = mbar_wait_bounded(told(asked - 1), ((asked - 1) / kW8Next) & 1);
-        if (!ok) break;
-        x = told_item(answer(asked - 1));
+        if (!ok) fail();
+        // no copy of this CTA, and no answer, may still be in flight when it exits
+        if (asked > 0) mbar_wait_bounded(told(asked - 1), ((asked - 1) / kW8Next) & 1);
+        if (nq > 0) mbar_wait_bounded(qfull, (nq - 1) & 1);
+        for (int t = max(nk - 2, 0); t < nk; t++) mbar_wait_bounded(kfull(t & 1), (t >> 1) & 1);
+        for (int t = max(nv - 2, 0); t < nv; t++) mbar_wait_bounded(vfull(t & 1), (t >> 1) & 1);
       }
-      if (!ok) fail();
-      // no copy of this CTA, and no answer, may still be in flight when it exits
-      if (asked > 0) mbar_wait_bounded(told(asked - 1), ((asked - 1) / kW8Next) & 1);
-      if (nq > 0) mbar_wait_bounded(qfull, (nq - 1) & 1);
-      for (int t = max(nk - 2, 0); t < nk; t++) mbar_wait_bounded(kfull(t & 1), (t >> 1) & 1);
-      for (int t = max(nv - 2, 0); t < nv; t++) mbar_wait_bounded(vfull(t & 1), (t >> 1) & 1);
-    }
-  } else if (warp < 3) {
-    // ---- MMAs of a half: S of step n once P V of step n - 1 is done, then P V ----
-    // The whole warp walks the steps, one lane issues: operands stay in uniform
-    // registers.
-    {
+    } else if (warp < 3) {
+      // ---- MMAs of a half: S of step n once P V of step n - 1 is done, then P V ----
+      // The whole warp walks the steps, one lane issues: operands stay in uniform
+      // registers.
       constexpr uint32_t type = ELEM == DKV_BF16 ? (1u << 7) | (1u << 10) : 0u;   // A and B formats
       constexpr uint32_t id_pv = umma_idesc_f16(128, 128) | type | (1u << 16);   // B (V) MN-major
       const int h = warp - 1;
@@ -412,7 +411,6 @@ __global__ void __launch_bounds__(kW8Threads, 1)
       }
       __syncwarp();
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kW8RegsMany));
     // ---- softmax: a thread per row of a half ----
@@ -635,7 +633,7 @@ struct AgShared {
   uint32_t unseen[4];                              // any value that some token does not see
   uint32_t need[kW8T][4];                          // per row: NaN, then what is to be computed again
 };
-// Bits of eight 16-bit values w: those in which `is` is on in the 16 bits of m.
+// A bit for each of eight 16-bit places that are on in m0 .. m3.
 __device__ __forceinline__ uint32_t bits8(uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3) {
   auto two = [](uint32_t m) { return (m & 1u) | (m >> 31 << 1); };
   return two(m0) | two(m1) << 2 | two(m2) << 4 | two(m3) << 6;
