@@ -63,6 +63,20 @@ __device__ __forceinline__ uint32_t pack_elems(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+// A mean of values of the type whose weights were rounded on the way can come out
+// just above the type's largest: that largest value, unless it is infinite.
+template <int ELEM>
+__device__ __forceinline__ float in_range(float x) {
+  const float top = ELEM == DKV_F16 ? 65504.0f : 3.3895313892515355e38f;
+  return fabsf(x) < INFINITY ? fminf(fmaxf(x, -top), top) : x;
+}
+// acc + 0 * x: NaN from the first infinite or NaN value on (never in the sign).
+template <int ELEM>
+__device__ __forceinline__ void find_not_finite(uint32_t& acc, uint32_t x) {
+  if (ELEM == DKV_F16) asm("fma.rn.f16x2 %0, %1, %2, %0;\n" : "+r"(acc) : "r"(x), "r"(0u));
+  else asm("fma.rn.bf16x2 %0, %1, %2, %0;\n" : "+r"(acc) : "r"(x), "r"(0u));
+}
+__device__ __forceinline__ bool found_not_finite(uint32_t acc) { return (acc & 0x7fff7fffu) != 0; }
 template <int ELEM>
 __device__ __forceinline__ float lo_elem(uint32_t w) { return elem_float<ELEM>((uint16_t)(w & 0xffffu)); }
 template <int ELEM>

@@ -56,6 +56,10 @@ constexpr int kA8Entry = 2 * kTile; // 4 KB: K and V codes of a tile, or K or V 
 constexpr int kA8Row = kD + 4;      // floats of a query's row in a shared partial (no bank conflicts)
 constexpr int kA8Cta = 2 * kA8Warps;    // tiles that make a CTA worth its start
 constexpr float kA8Lazy = 8.0f, kA8LazySum = 5.0f;     // how far x may pass m, y pass u
+// bf16 values of a tail alone, which are not scaled: m lies this much above the
+// maximum, so that 127 weights of up to 2^8 sum to less than 1 and their
+// products stay in fp32's range
+constexpr float kA8Above = 15.0f;
 
 struct Attn8Args {
   const int *slots, *seq_lens;
@@ -117,11 +121,11 @@ struct State {
 
 // Raise the running maxima where some x or y = x - lv exceeds them by more than
 // the slack. x: tokens g (x[0], x[1]) and g + 8 (x[2], x[3]) for the lane's two
-// queries.
-__device__ __forceinline__ void raise(State& s, const float* x, float lv) {
+// queries; above: how far m lies above the maximum.
+__device__ __forceinline__ void raise(State& s, const float* x, float lv, float above) {
   float a = fmaxf(x[0], x[2]), b = fmaxf(x[1], x[3]);
-  if (!__any_sync(0xffffffffu, a > fminf(s.m[0] + kA8Lazy, s.u[0] + (lv + kA8LazySum)) ||
-                                   b > fminf(s.m[1] + kA8Lazy, s.u[1] + (lv + kA8LazySum))))
+  if (!__any_sync(0xffffffffu, a > fminf(s.m[0] + (kA8Lazy - above), s.u[0] + (lv + kA8LazySum)) ||
+                                   b > fminf(s.m[1] + (kA8Lazy - above), s.u[1] + (lv + kA8LazySum))))
     return;
 #pragma unroll
   for (int d = 4; d <= 16; d <<= 1) {
@@ -133,7 +137,7 @@ __device__ __forceinline__ void raise(State& s, const float* x, float lv) {
     top = fmaxf(old, x);
     return top == -INFINITY ? 1.0f : fast_exp2(old - top);
   };
-  const float fa = up(s.m[0], a), fb = up(s.m[1], b);
+  const float fa = up(s.m[0], a + above), fb = up(s.m[1], b + above);
   s.l[0] *= up(s.u[0], a - lv);
   s.l[1] *= up(s.u[1], b - lv);
 #pragma unroll
@@ -216,7 +220,7 @@ __device__ __forceinline__ void code_tile(State& s, const uint32_t (&qf)[16], co
       vw[j].w &= see.v;
     }
   }
-  raise(s, x, lv);
+  raise(s, x, lv, 0.0f);
   weights(s, x, lv);
   const uint32_t b0 = movmatrix_trans(pack_half2(x[0], x[1])), b1 = movmatrix_trans(pack_half2(x[2], x[3]));
 #pragma unroll
@@ -286,8 +290,9 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
 #pragma unroll
     for (int e = 0; e < 4; e++) x[e] = (e < 2 ? see.lo : see.hi) ? x[e] : -INFINITY;
   }
-  float lv = 0.0f;
+  float lv = 0.0f, above = ELEM == DKV_BF16 ? kA8Above : 0.0f;
   if (mixed) {
+    above = 0.0f;
     uint32_t am2 = 0;        // magnitudes order like their bits
 #pragma unroll
     for (int m = 0; m < 8; m++)
@@ -309,7 +314,7 @@ __device__ __forceinline__ void tail_tile(State& s, const uint32_t (&qf)[16], co
       v[m].w = scale_pair<ELEM>(v[m].w, inv);
     }
   }
-  raise(s, x, lv);
+  raise(s, x, lv, above);
   weights(s, x, lv);
   uint32_t p0 = pack_elems<ELEM>(x[0], x[1]), p1 = pack_elems<ELEM>(x[2], x[3]);
   const uint32_t b0 = movmatrix_trans(p0), b1 = movmatrix_trans(p1);
@@ -350,16 +355,28 @@ template <int ELEM>
 __device__ __forceinline__ void write_unit(const State& s, uint8_t* out, int G, int lane) {
   const int g = lane >> 2, t = lane & 3, odd = g & 1, q = 2 * t + odd;
   const float ia = __fdiv_rn(fast_exp2(s.m[0] - s.u[0]), s.l[0]), ib = __fdiv_rn(fast_exp2(s.m[1] - s.u[1]), s.l[1]);
+  uint32_t bad = 0;
 #pragma unroll
   for (int m = 0; m < 8; m++)
 #pragma unroll
     for (int e = 0; e < 2; e++) {
       const float a = s.o[m][2 * e] * ia, b = s.o[m][2 * e + 1] * ib;
       const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 4);
-      if (q < G)
-        *reinterpret_cast<uint32_t*>(out + (size_t)q * (2 * kD) + 2 * (16 * m + 8 * e + g - odd)) =
-            odd ? pack_elems<ELEM>(other, b) : pack_elems<ELEM>(a, other);
+      const uint32_t w = odd ? pack_elems<ELEM>(other, b) : pack_elems<ELEM>(a, other);
+      find_not_finite<ELEM>(bad, w);
+      if (q < G) *reinterpret_cast<uint32_t*>(out + (size_t)q * (2 * kD) + 2 * (16 * m + 8 * e + g - odd)) = w;
     }
+  if (__builtin_expect(__any_sync(0xffffffffu, found_not_finite(bad)), 0)) {
+    // seldom: each lane its own features, within the type's range
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < 8; m++)
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (2 * t + (e & 1) < G)
+          reinterpret_cast<uint16_t*>(out)[(2 * t + (e & 1)) * kD + 16 * m + 8 * (e >> 1) + g] =
+              float_elem<ELEM>(in_range<ELEM>(s.o[m][e] * (e & 1 ? ib : ia)));
+  }
 }
 
 // A partial: the part's own result, so that its size is that of its values, and
@@ -497,8 +514,14 @@ __device__ __noinline__ Row join_far(const float* part, int stride, int c0, int 
 template <int ELEM>
 __device__ __forceinline__ void write_row(uint8_t* out, int lane, float4 o, float l) {
   const float inv = __fdiv_rn(1.0f, l);
-  *reinterpret_cast<uint2*>(out + 8 * lane) =
-      make_uint2(pack_elems<ELEM>(o.x * inv, o.y * inv), pack_elems<ELEM>(o.z * inv, o.w * inv));
+  uint2 w = make_uint2(pack_elems<ELEM>(o.x * inv, o.y * inv), pack_elems<ELEM>(o.z * inv, o.w * inv));
+  uint32_t bad = 0;
+  find_not_finite<ELEM>(bad, w.x);
+  find_not_finite<ELEM>(bad, w.y);
+  if (__builtin_expect(found_not_finite(bad), 0))
+    w = make_uint2(pack_elems<ELEM>(in_range<ELEM>(o.x * inv), in_range<ELEM>(o.y * inv)),
+                   pack_elems<ELEM>(in_range<ELEM>(o.z * inv), in_range<ELEM>(o.w * inv)));
+  *reinterpret_cast<uint2*>(out + 8 * lane) = w;
 }
 
 // What a lane finds out about one tile of the sequence.

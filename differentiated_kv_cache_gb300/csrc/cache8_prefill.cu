@@ -207,17 +207,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 
 // bits [0, n)
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
-// acc + 0 * x: NaN from the first infinite or NaN value on.
-template <int ELEM>
-__device__ __forceinline__ void find_not_finite(uint32_t (&acc)[4], uint4 x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    if (ELEM == DKV_F16) asm("fma.rn.f16x2 %0, %1, %2, %0;\n" : "+r"(acc[i]) : "r"(w[i]), "r"(0u));
-    else asm("fma.rn.bf16x2 %0, %1, %2, %0;\n" : "+r"(acc[i]) : "r"(w[i]), "r"(0u));
-  }
-}
-
 // Values of a tensor-memory load are used after the wait only.
 __device__ __forceinline__ void loaded32(float* v) {
 #pragma unroll
@@ -557,7 +546,10 @@ __global__ void __launch_bounds__(kW8Threads, 1)
                                        pack_elems<ELEM>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
                                        pack_elems<ELEM>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
                                        pack_elems<ELEM>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-            find_not_finite<ELEM>(bad, w);
+            find_not_finite<ELEM>(bad[0], w.x);
+            find_not_finite<ELEM>(bad[1], w.y);
+            find_not_finite<ELEM>(bad[2], w.z);
+            find_not_finite<ELEM>(bad[3], w.w);
             *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * r + e) ^ (lane & 7)) << 4)) = w;
           }
         }
@@ -571,7 +563,7 @@ __global__ void __launch_bounds__(kW8Threads, 1)
         }
         __syncwarp();
       }
-      if (real && ((bad[0] | bad[1] | bad[2] | bad[3]) & 0x7fff7fffu)) {
+      if (real && found_not_finite(bad[0] | bad[1] | bad[2] | bad[3])) {
         c.status[2] = 1;
         c.status[3] = kLook;
       }

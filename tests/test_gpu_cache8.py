@@ -1282,3 +1282,20 @@ def test_lengths_below_what_is_stored():
     for window, sinks in ((0, 0), (40, 3)):
         out = c.attend(who, lens, q, window, sinks)
         c.check_attention(out, who, lens, q, window, sinks)
+
+
+@pytest.mark.parametrize("elem,code", [(F16, E4M3), (F16, INT8), (BF16, E4M3), (BF16, INT8)])
+def test_attention_of_the_largest_values(elem, code):
+    """Means of values of the type's largest size do not round to infinite ones."""
+    rng = np.random.default_rng(7)
+    lens = [2000, 992, 300, 50]
+    c = Cache(1, 4, 64, len(lens), 2000 // 64 + 1, elem, code)
+    k = c.vec(rng, sum(lens), 1)
+    sign = torch.from_numpy(np.where(rng.random((1, 1, 128)) < 0.5, -1.0, 1.0)).cuda()
+    v = (sign * torch.finfo(elem).max).expand(sum(lens), 1, 128).to(elem).contiguous()
+    c.append(None, [0] * len(lens), lens, k, v)
+    for scale in [0.5, 1.0, 2.0, 4.0] * 25:
+        q = c.vec(rng, len(lens), 4, scale)
+        out = c.attend(None, lens, q)
+        assert torch.isfinite(out).all()
+    c.check_attention(out, range(len(lens)), lens, q)
