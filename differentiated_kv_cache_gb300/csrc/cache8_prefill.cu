@@ -581,19 +581,22 @@ __global__ void __launch_bounds__(kW8Threads, 1)
   }
 }
 
-// ---- Rows that came out NaN ----
+// ---- Rows that came out infinite or NaN ----
 // A feature of a row is NaN by right where the row sees a NaN value of it,
 // infinite ones of both signs, an infinite one under a weight of 0, or a key whose
 // logit is NaN or +Inf. It is wrong where a value that the row does not see, in a
 // step beside its keys, made 0 * NaN or 0 * Inf of it, and where an infinite value
-// that it does see met a weight that rounds to 0 in 16 bits. (What is infinite is
-// right: nothing makes a number of NaN again.)
+// that it does see met a weight that rounds to 0 in 16 bits. What is infinite is
+// right where the row sees an infinite value of that feature (nothing makes a
+// number of NaN again). Else a mean of values of the type's largest size was
+// rounded up, or a sum of bf16 values left fp32's range: weights of up to 2^12 make
+// that possible above 2^122 / tokens.
 //
 // A block takes the halves of the kernel above in turn (128 / G tokens, all heads
-// of a group). Of one that holds NaN it looks through the keys and values that its
+// of a group). Of one that holds such a feature it looks through the keys and values that its
 // rows see, and those that the steps beside them hold, for what is not finite, 512
 // keys at a time, the first ones first and then from the diagonal back, until
-// every NaN is seen to be right. Where some are not, it computes the half again
+// all is seen to be right. Where some are not, it computes the half again
 // with mma.sync, with zeros for the values that are not finite, and writes the
 // features that are not right, and only those. So a call that meets such a value
 // costs a look through its results, and through keys and values as far as that
@@ -623,7 +626,7 @@ struct AgShared {
   uint32_t seen[kKinds][kW8T][4];                  // by a token
   uint32_t all[kKinds][4];                         // by every token
   uint32_t unseen[4];                              // any value that some token does not see
-  uint32_t need[kW8T][4];                          // per row: NaN, then what is to be computed again
+  uint32_t need[kW8T][4], inf[kW8T][4];            // per row: infinite or NaN, then what is to be computed again; infinite
 };
 // A bit for each of eight 16-bit places that are on in m0 .. m3.
 __device__ __forceinline__ uint32_t bits8(uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3) {
@@ -693,9 +696,10 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t addr) {
 }
 
 // The half again: S = Q K^T and O += P V with mma.sync m16n8k16, 16 rows a warp,
-// in the manner and the types of the kernel above.
+// in the manner and the types of the kernel above; weights are at most 2^-above.
 template <int ELEM>
-__device__ __noinline__ void half_again(AgShared& sh, const Cache8View& c, const Again8& a, const Item& it, int q0, int nt) {
+__device__ __noinline__ void half_again(AgShared& sh, const Cache8View& c, const Again8& a, const Item& it, int q0, int nt,
+                                        float above) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = c.G;
   const int window = a.w.window, q1 = q0 + nt - 1;
   const AgKeys key(window > 0 ? min(a.w.sinks, it.n0) : 0, window > 0 ? max(q0 - window + 1, 0) : 0, q1 + 1);
@@ -778,7 +782,7 @@ __device__ __noinline__ void half_again(AgShared& sh, const Cache8View& c, const
       top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
       top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2));
       f[e] = top[e] == -INFINITY ? 1.0f : fast_exp2(m[e] - top[e]);
-      off[e] = top[e] == -INFINITY ? 0.0f : top[e];
+      off[e] = top[e] == -INFINITY ? 0.0f : top[e] + above;
       m[e] = top[e];
       l[e] *= f[e];
     }
@@ -826,7 +830,7 @@ __device__ __noinline__ void half_again(AgShared& sh, const Cache8View& c, const
         if (!((sh.need[r][w] & ~x.nan) >> at & 1u)) continue;
         // an infinite sum is infinite, unless the weights are NaN
         const float v = (x.up | x.down) >> at & 1u ? (x.up >> at & 1u ? INFINITY : -INFINITY) * inv : o[i][2 * e + y] * inv;
-        out[8 * i + 2 * t + y] = float_elem<ELEM>(v);
+        out[8 * i + 2 * t + y] = float_elem<ELEM>(in_range<ELEM>(v));
       }
     }
   }
@@ -845,7 +849,7 @@ __global__ void __launch_bounds__(kAgThreads, 1) k_prefill8_again(Cache8View c, 
     const Item it = item_of((int)(x >> 1), c, a.w, call);
     const int q0 = it.p0 + (int)(x & 1) * tq, nt = min(tq, it.n0 - q0);      // its tokens
     if (nt <= 0) continue;
-    // NaN in its rows
+    // what its rows hold
     __syncthreads();           // the half before is done with
     uint32_t some = 0;
     uint4 w[8];
@@ -860,11 +864,18 @@ __global__ void __launch_bounds__(kAgThreads, 1) k_prefill8_again(Cache8View c, 
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       const int r = 16 * warp + 2 * i + (lane >> 4);
-      uint32_t b = Elem<ELEM>::nans(w[i]) << (8 * (lane & 3));
+      uint32_t inf = (Elem<ELEM>::equal(w[i], Elem<ELEM>::kInf) | Elem<ELEM>::equal(w[i], Elem<ELEM>::kInf | 0x80008000u)) << (8 * (lane & 3));
+      uint32_t b = inf | Elem<ELEM>::nans(w[i]) << (8 * (lane & 3));
       some |= b;
-      b |= __shfl_xor_sync(0xffffffffu, b, 1);
-      b |= __shfl_xor_sync(0xffffffffu, b, 2);
-      if ((lane & 3) == 0) sh.need[r][lane >> 2 & 3] = b;
+#pragma unroll
+      for (int d = 1; d <= 2; d <<= 1) {
+        b |= __shfl_xor_sync(0xffffffffu, b, d);
+        inf |= __shfl_xor_sync(0xffffffffu, inf, d);
+      }
+      if ((lane & 3) == 0) {
+        sh.need[r][lane >> 2 & 3] = b;
+        sh.inf[r][lane >> 2 & 3] = inf;
+      }
     }
     for (int i = tid; i < kKinds * kW8T * 4; i += kAgThreads) (&sh.seen[0][0][0])[i] = 0;
     if (tid < kKinds * 4) (&sh.all[0][0])[tid] = 0;
@@ -912,35 +923,43 @@ __global__ void __launch_bounds__(kAgThreads, 1) k_prefill8_again(Cache8View c, 
       __syncthreads();
       bool open = false;
       if (tid < nt * G)
-        for (int e = 0; e < 4; e++) open |= (sh.need[tid][e] & ~row_of(sh, tid / G, e).nan) != 0;
+        for (int e = 0; e < 4; e++) {
+          const AgRow r = row_of(sh, tid / G, e);
+          open |= (sh.need[tid][e] & ~r.nan & ~(sh.inf[tid][e] & (r.up | r.down))) != 0;
+        }
       left = __syncthreads_or(open);
     }
     if (!left) continue;
-    bool again = false;
+    bool again = false, wide = false;
     if (tid < nt * G) {
       uint32_t* need = sh.need[tid];
       // a row with a feature that is not NaN has weights that are not: what is
-      // infinite of it needs no computing
-      const bool sure = (need[0] & need[1] & need[2] & need[3]) != 0xffffffffu;
+      // infinite of it needs no computing, and other NaN came of sums
+      bool sure = false;
+      for (int e = 0; e < 4; e++) sure |= (need[e] & ~sh.inf[tid][e]) != 0xffffffffu;
       uint16_t* out = reinterpret_cast<uint16_t*>(
           a.out + (((long long)(it.t0 + q0 + tid / G) * c.hkv + it.h) * G + tid % G) * (2 * kD));
       for (int e = 0; e < 4; e++) {
         const AgRow r = row_of(sh, tid / G, e);
-        uint32_t x = need[e] & ~r.nan, inf = x & (r.up | r.down);
+        const uint32_t x = need[e] & ~r.nan & ~(sh.inf[tid][e] & (r.up | r.down)), inf = x & (r.up | r.down);
         if (sure) {
           for (uint32_t f = inf; f; f &= f - 1) {
             const int b = __ffs(f) - 1;
             out[32 * e + b] = float_elem<ELEM>(r.up >> b & 1u ? INFINITY : -INFINITY);
           }
-          x &= ~inf;
-          inf = 0;
+          need[e] = x & ~inf;
+          wide |= (need[e] & (sh.inf[tid][e] | ~sh.unseen[e])) != 0;
+        } else {
+          need[e] = x & (inf | sh.unseen[e]);
         }
-        need[e] = x & (inf | sh.unseen[e]);
         again |= need[e] != 0;
       }
     }
     if (!__syncthreads_or(again)) continue;
-    half_again<ELEM>(sh, c, a, it, q0, nt);
+    // 2^32 tokens' weights of 2^-32 sum to 1 (bf16 keeps them whole); fp16 values
+    // need no such room
+    wide = __syncthreads_or(wide) && ELEM == DKV_BF16;
+    half_again<ELEM>(sh, c, a, it, q0, nt, wide ? 32.0f : 0.0f);
   }
   __syncthreads();             // every thread has read the word
   if (tid == 0 && atomicAdd(c.status + 3, 1) == (kLook | ((int)gridDim.x - 1))) c.status[3] = 0;

@@ -539,6 +539,9 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
  * again, such values in every few hundred tokens up to 14 times it; calls without
  * them cost the same before and after. status[2] stays on until the caller zeroes
  * it (nothing reads it); status[3] is the call's own and zero between calls.
+ * Means of finite values are finite: one that rounds to an infinite number is the
+ * type's largest. (bf16 values above 2^122 / seq_lens[i]: where every feature of a
+ * row left fp32's range with both signs, the row stays NaN.)
  * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED (host, nothing queued);
  * DKV_ERR_CUDA. */
 int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* seq_lens, const void* q,

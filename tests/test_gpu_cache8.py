@@ -1299,3 +1299,34 @@ def test_attention_of_the_largest_values(elem, code):
         out = c.attend(None, lens, q)
         assert torch.isfinite(out).all()
     c.check_attention(out, range(len(lens)), lens, q)
+
+
+@pytest.mark.parametrize("elem", [F16, BF16])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (100, 5)])
+def test_prefill_of_the_largest_values(elem, window, sinks):
+    """Means of values of the type's largest size do not come out infinite, beside
+    infinite ones that are and NaN out of sight."""
+    rng = np.random.default_rng(8)
+    lens, G = [3000, 40], 4
+    c = Cache(1, G, 16, 1, 1, elem, E4M3)
+    n, top = sum(lens), torch.finfo(elem).max
+    q, k = c.vec(rng, n, G, 1.5), c.vec(rng, n, 1)
+    sign = torch.from_numpy(np.where(rng.random((1, 1, 128)) < 0.5, -1.0, 1.0)).cuda()
+    v = (sign * top).expand(n, 1, 128).to(elem).contiguous()
+    inf = float("inf")
+    v[700, 0, 5], v[900, 0, 6], v[1300, 0, 7], v[2999, 0, 8] = inf, -inf, float("nan"), inf
+    out = torch.empty_like(q)
+    _dkv().dkv_cache8_prefill(c.c, lens, q, k, v, out, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    got, vn, sign = out.double().cpu().numpy(), v.double().cpu().numpy(), sign.cpu().numpy()[0]
+    at = 0
+    for m in lens:
+        for p in range(m):
+            x = vn[at + ref.visible(p + 1, window, sinks), 0]
+            want = np.where(np.isfinite(x).all(axis=0), sign * top, x.max(axis=0) + x.min(axis=0))[0]      # Inf + top, Inf - Inf, NaN
+            r = got[at + p]
+            fin = np.isfinite(want)
+            assert (np.isnan(r) == np.isnan(want)).all() and (r == want)[:, np.isinf(want)].all(), p
+            # weights off by half a step each, and half a step of the result
+            assert np.isfinite(r[:, fin]).all() and (np.abs(r[:, fin] - want[fin]) <= 1.1 * torch.finfo(elem).eps * top).all(), p
+        at += m
