@@ -1330,3 +1330,16 @@ def test_prefill_of_the_largest_values(elem, window, sinks):
             # weights off by half a step each, and half a step of the result
             assert np.isfinite(r[:, fin]).all() and (np.abs(r[:, fin] - want[fin]) <= 1.1 * torch.finfo(elem).eps * top).all(), p
         at += m
+
+
+def test_prefill_of_the_largest_values_in_many_rows():
+    """fp16 weights round up enough in one row of some thousands."""
+    rng = np.random.default_rng(0)
+    n, G = 3000, 4
+    c = Cache(1, G, 16, 1, 1, F16, E4M3)
+    v = torch.full((n, 1, 128), 65504.0, dtype=F16, device="cuda")
+    for _ in range(12):
+        q, k = c.vec(rng, n, G), c.vec(rng, n, 1)
+        out = torch.empty_like(q)
+        _dkv().dkv_cache8_prefill(c.c, [n], q, k, v, out)
+        assert torch.isfinite(out).all() and (out >= 65504 * (1 - 2.0 ** -10)).all()
