@@ -13,14 +13,16 @@
 // does not depend on who that is).
 //
 // Bound by DRAM: 32 requests of 4096 tokens with 8 KV heads (273 MB) take 48 us,
-// 5.7 TB/s or 83% of the measured copy rate; 35 of them stream at 7.7 TB/s, the
+// 5.7 TB/s or 84% of the measured copy rate; 35 of them stream at 7.7 TB/s, the
 // rest is launch, the chain lengths - page table - first tile (3.5 us), CTAs
 // that DRAM serves at uneven rates (4 us) and the joins (3 us). 8 x 32768 with 64
 // query heads: 89 us, 89%. One CTA of 12 warps with two 4 KB copies each on
 // their way: three copies queue up at DRAM and part the CTAs' ends further
 // (50.4 us), 8 warps leave the matrix and conversion chain of a tile exposed
 // (54 us), 16 have too few registers (52 us, 8 x 32768: 119 us). One CTA per
-// (request, KV head) took 52 and 297 us.
+// (request, KV head) took 52 and 297 us. Both sums under one maximum, which loses
+// tokens of zero values beside large ones, took 0.3 us less (269 instructions a tile
+// instead of 289).
 //
 // A warp's step on a tile of codes, S^T = K Q^T and O^T += V^T P^T with
 // mma.sync m16n8k16 (tokens / features on M, the G <= 8 queries on N; at most
@@ -821,8 +823,8 @@ __global__ void __launch_bounds__(kA8Warps * 32)
   // that arrives last joins those. The rows of such units, which are the CTA's
   // first or last, come first: each waits through a fence, an atomic and loads, a
   // few us in which the other warps do the rest (200 requests of 2 tiles with 8 KV
-  // heads and G = 5 take 13 us, with a warp a unit 16; 200 of 1 .. 160 tokens 21
-  // and 23) ----
+  // heads and G = 5 take 13 us, with a warp a unit 16; 200 of 1 .. 160 tokens 20
+  // and 23; but 8 x 32768 tokens, with few units of many parts, 89.2 and 87.8) ----
   const int mine = lane < 2 * kA8Warps ? s_unit[lane] : -1;
   // slots lie in the order of positions: those of a unit are neighbours
   const unsigned used = __ballot_sync(0xffffffffu, mine >= 0), below = used & ((1u << lane) - 1u);

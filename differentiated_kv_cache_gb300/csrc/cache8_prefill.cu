@@ -22,16 +22,18 @@
 // step n + 1, and the halves do not wait for one another: products run while
 // either half's softmax does, and the next item's first products while this
 // item's results are written. (Tensor memory holds two S of 64 columns and an O
-// of 128 for each half; with one S of 128 columns a half, each softmax waited
-// for P V and the next S in turn: 4900 cycles for 128 keys instead of 3100.)
+// of 128 for each half. With one S of 128 columns a half, each softmax waited
+// for P V and the next S in turn; that layout was timed only while an MMA took
+// 100 cycles to issue, see below, so there is no figure for it as things are.)
 // Only key tiles with a visible key are visited, the window's from the diagonal
 // back (the nearest keys give a good first m), then the first tokens'; of each,
 // a half takes the 32-key parts that some of its rows may see.
 //
 // Bound by the tensor cores: 32 prompts of 4096 tokens, 32 / 8 heads, window
-// 1024 take 1.76 ms (1.93 TFLOP, 56% of the measured bf16 burst rate; the steps
-// at the window's edges and the diagonal add 18% to the products), 16384 tokens
-// with 64 / 8 heads and window 4096 take 1.44 ms (69%). In a step of 64 keys the
+// 1024 take 1.85 ms (1.93 TFLOP, 53% of the measured bf16 burst rate; the steps
+// at the window's edges and the diagonal add 5% to the columns of the products),
+// 16384 tokens with 64 / 8 heads and window 4096 take 1.50 ms (66%; 0.8%). (Other
+// runs of the same code: 1.76 and 1.44.) In a step of 64 keys the
 // products of both halves take about 1400 of 1650 cycles; S has N = 64, for
 // which the queries are read from shared memory again (48 instead of 32 cycles
 // an MMA), the price of the second S buffer. With one thread in the MMA warps'

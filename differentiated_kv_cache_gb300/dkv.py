@@ -415,8 +415,8 @@ def _stream8(cache, stream):
 def dkv_cache8_append(cache: dkv_cache8, before, k, v, rope=None, n_new=None, slots=None, q=None, k_rot=None,
                       q_rot=None, stream=None, check: bool = True) -> int:
     """Append tokens to a uniform 8-bit cache: before (device int32 [n_req])
-    tokens are stored, n_new (host; None: one each) more come, keys and queries
-    turned by rope (fp32 [positions][rotary_dim / 2][2], cos and sin). k_rot and
+    tokens are stored, n_new (host; None: one each, the form of a generation step)
+    more come, keys and queries turned by rope (fp32 [positions][rotary_dim / 2][2], cos and sin). k_rot and
     q_rot receive the turned vectors."""
     import torch
     n_req, i32 = before.numel(), torch.int32
@@ -445,8 +445,9 @@ def dkv_cache8_append(cache: dkv_cache8, before, k, v, rope=None, n_new=None, sl
 def dkv_cache8_attention(cache: dkv_cache8, seq_lens, q, out, window: int = 0, sinks: int = 0, slots=None,
                          stream=None, check: bool = True) -> int:
     """Decode attention of one query token per request over a uniform 8-bit
-    cache: seq_lens (device int32 [n_req]) tokens are stored; window = 0 sees
-    them all, else the last `window` and the first `sinks`."""
+    cache: seq_lens (device int32 [n_req]) tokens are stored (fewer: a multiple of
+    the block, or inside the open one); window = 0 sees them all, else the last
+    `window` and the first `sinks`."""
     import torch
     _window8(window, sinks)
     n_req = seq_lens.numel()
@@ -461,7 +462,8 @@ def dkv_cache8_attention(cache: dkv_cache8, seq_lens, q, out, window: int = 0, s
 def dkv_cache8_prefill(cache: dkv_cache8, seq_lens, q, k, v, out, window: int = 0, sinks: int = 0, stream=None,
                        check: bool = True) -> int:
     """Causal attention over whole prompts (host lengths, requests back to
-    back) with an optional sliding window and first tokens that stay visible."""
+    back) with an optional sliding window and first tokens that stay visible
+    (in full and fp16, dkv_prefill_attention is the slower and more exact form)."""
     _window8(window, sinks)
     keep, lens, n_req, total = _lens8(seq_lens)
     qp, qs = _rows(cache, q, cache.q_heads, total, "q")

@@ -411,6 +411,8 @@ int dkv_pool_export(dkv_pool* pool, dkv_snapshot* out);
  *    calls. An append may step back (before[i] below the tokens stored so
  *    far, e.g. after rejected guesses) as far as the open block's first
  *    token: the 16-bit values of complete blocks are gone.
+ *  - Keys are turned by the position that they were appended at, and first
+ *    tokens that stay visible keep it when the window moves on.
  *  - Codes, per block, head and operand (K or V), fp32 arithmetic correctly
  *    rounded: amax = the largest finite |x| of the T x 128 values,
  *    s = max(fmul(amax, fdiv(1, Q)), 2^-100) with Q = 448 (e4m3) or 127
@@ -485,6 +487,8 @@ int dkv_cache8_workspace(const dkv_cache8* cache, int32_t max_req, int64_t* byte
  * on the way. Request i: slot slots[i] (slots device int32 [n_req], NULL: slot
  * i), before[i] tokens stored so far (device int32 [n_req]), n_new[i] >= 1 new
  * ones (host; NULL: one each) at positions before[i] .. before[i] + n_new[i]-1.
+ * NULL is the generation step's form: the same results as an array of ones,
+ * sooner.
  *   k, v    device [sum(n_new)][Hkv][128], requests back to back in call order;
  *           token rows k_stride / v_stride elements apart (multiples of 8, at
  *           least Hkv * 128), so that they may be parts of one projection.
@@ -510,11 +514,20 @@ int dkv_cache8_append(const dkv_cache8* cache, int32_t n_req, const int32_t* n_n
  *   out[i][h] = sum_j softmax_j(q[i][h] . k^_j / sqrt(128)) v^_j
  * over the visible tokens j < N: every one if window = 0, else the last
  * `window` and the first `sinks` (j >= N - window or j < sinks). k^, v^ are
- * the stored values (codes times scale in pages, 16 bits in the tail). A
- * request with N <= 0 (padding; its slot may be any number) gets zeros. Tokens
- * that are not visible are not read into the result, whatever they hold.
+ * the stored values (codes times scale in pages, 16 bits in the tail). N may be
+ * less than what is stored where it is a multiple of T or lies in the open
+ * block; inside a block that is complete since, the tail holds other tokens and
+ * the result is undefined. A request with N <= 0 (padding; its slot may be any
+ * number) gets zeros. Tokens that are not visible are not read into the result,
+ * whatever they hold.
+ * Sums are in fp32. Weights enter the value product rounded to fp16 (relative
+ * 2^-11; in the tail of a bf16 cache as a pair of bf16), the sum of weights
+ * unrounded; bf16 queries meet codes as fp16 after division by a power of two
+ * (what lies below 2^-24 of the row's largest entry is lost). An infinite value
+ * under a weight that rounds to 0 gives NaN.
  *   q       device [n_req][Hkv * G][128], rows q_stride elements apart.
  *   out     device [n_req][Hkv * G][128] of elem_type, contiguous, apart from q.
+ *   n_req * Hkv * (table_width * T / 16 + 1) is at most 2^31 - 16.
  * The call is split over the GPU by the lengths that it finds on the device;
  * the same inputs give the same bits whatever order its blocks run in.
  * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED, DKV_ERR_SCRATCH (workspace_bytes
@@ -526,7 +539,12 @@ int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* 
 /* Causal attention over whole prompts with the same window and first tokens:
  * position p of request i (seq_lens[i] >= 1 tokens, host; back to back in call
  * order) sees j <= p with window = 0, j > p - window or j < sinks. The cache
- * supplies the head layout, elem_type, device and status only.
+ * supplies the head layout, elem_type, device and status only. With window = 0
+ * and fp16, dkv_prefill_attention computes the same with probabilities as a pair
+ * (22 bits), an fp32 result and the observation rows' log-sum-exps that the
+ * pool's compaction takes; where those are not wanted, this call takes about 0.6
+ * of its time and its result is off by fp16 steps (1e-3 where that one's is by
+ * 1e-6, for normal values).
  *   q, k, v  device [sum(seq_lens)][heads][128], token rows *_stride elements
  *            apart (multiples of 8); out contiguous, of elem_type, apart from
  *            them.
