@@ -29,18 +29,17 @@
 // back (the nearest keys give a good first m), then the first tokens'; of each,
 // a half takes the 32-key parts that some of its rows may see.
 //
-// Bound by the tensor cores: 32 prompts of 4096 tokens, 32 / 8 heads, window
-// 1024 take 1.85 ms (1.93 TFLOP, 53% of the measured bf16 burst rate; the steps
-// at the window's edges and the diagonal add 5% to the columns of the products),
-// 16384 tokens with 64 / 8 heads and window 4096 take 1.50 ms (66%; 0.8%). (Other
-// runs of the same code: 1.76 and 1.44.) In a step of 64 keys the
-// products of both halves take about 1400 of 1650 cycles; S has N = 64, for
-// which the queries are read from shared memory again (48 instead of 32 cycles
-// an MMA), the price of the second S buffer. With one thread in the MMA warps'
-// loop, whose operands then are no uniform registers, an MMA took 100 cycles to
-// issue (2.25 ms); results written by warps of their own left the softmax too
-// few registers (2.25 ms); queries fetched per half, the second half started a
-// step late: no difference.
+// Bound by the tensor cores: 32 prompts of 4096 tokens, 32 / 8 heads, window 1024
+// take 1.85 ms (1.93 TFLOP, 53% of the measured bf16 burst rate; the steps at the
+// window's edges and the diagonal add 5% to the columns of the products), 16384
+// tokens with 64 / 8 heads and window 4096 take 1.50 ms (66%; 0.8%). (Other runs
+// of the same code: 1.76 and 1.44.) In a step of 64 keys the products of both
+// halves take about 1400 of 1650 cycles; S has N = 64, for which the queries are
+// read from shared memory again (48 instead of 32 cycles an MMA), the price of the
+// second S buffer. With one thread in the MMA warps' loop, whose operands then are
+// no uniform registers, an MMA took 100 cycles to issue (2.25 ms); results written
+// by warps of their own left the softmax too few registers (2.25 ms); queries
+// fetched per half, the second half started a step late: no difference.
 //
 // 0 * Inf is not 0: an infinite or NaN value makes NaN of every row of its step,
 // those that do not see it too. A second kernel computes rows that came out so
@@ -595,15 +594,15 @@ __global__ void __launch_bounds__(kW8Threads, 1)
 // that possible above 2^122 / tokens.
 //
 // A block takes the halves of the kernel above in turn (128 / G tokens, all heads
-// of a group). Of one that holds such a feature it looks through the keys and values that its
-// rows see, and those that the steps beside them hold, for what is not finite, 512
-// keys at a time, the first ones first and then from the diagonal back, until
-// all is seen to be right. Where some are not, it computes the half again
-// with mma.sync, with zeros for the values that are not finite, and writes the
-// features that are not right, and only those. So a call that meets such a value
-// costs a look through its results, and through keys and values as far as that
-// value; and each value the computing of the few halves that hold it in a step but
-// not in their rows' sight. 16384 tokens, 64 / 8 heads, window 4096 + 64, bf16 (1.45
+// of a group). Of one that holds such a feature it looks through the keys and
+// values that its rows see, and those that the steps beside them hold, for what is
+// not finite, 512 keys at a time, the first ones first and then from the diagonal
+// back, until all is seen to be right. Where some is not, it computes the half
+// again with mma.sync, with zeros for the values that are not finite, and writes
+// the features that are not right, and only those. So a call that meets such a
+// value costs a look through its results, and through keys and values as far as
+// that value; and each value the computing of the few halves that hold it in a step
+// but not in their rows' sight. 16384 tokens, 64 / 8 heads, window 4096 + 64, bf16 (1.45
 // ms without such a value): one NaN in a first token's key or value 1.95 ms, in the
 // middle 2.1, a feature infinite in every token 10.8, one value in 10^4 NaN 10.4
 // (with 64 / 64 heads 20.8: every half again, at 110 TFLOP/s). A walk of a warp a
