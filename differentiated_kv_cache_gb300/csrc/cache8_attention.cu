@@ -343,7 +343,7 @@ __device__ __forceinline__ void half_q(uint32_t (&qf)[16], int lane, float (&sca
     am = amax_finite(amax_finite(am, lo_elem<DKV_BF16>(qf[i])), hi_elem<DKV_BF16>(qf[i]));
   am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
   am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-  const int ex = max(-100, min(100, (int)(__float_as_uint(am) >> 23) - 127));
+  const int ex = max(-126, min(126, (int)(__float_as_uint(am) >> 23) - 127));     // both powers are normal numbers
   const float inv = __uint_as_float((uint32_t)(127 - ex) << 23), sc = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
   for (int i = 0; i < 16; i++) qf[i] = pack_half2(lo_elem<DKV_BF16>(qf[i]) * inv, hi_elem<DKV_BF16>(qf[i]) * inv);

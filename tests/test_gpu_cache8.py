@@ -1343,3 +1343,26 @@ def test_prefill_of_the_largest_values_in_many_rows():
         out = torch.empty_like(q)
         _dkv().dkv_cache8_prefill(c.c, [n], q, k, v, out)
         assert torch.isfinite(out).all() and (out >= 65504 * (1 - 2.0 ** -10)).all()
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("amp", [1e-37, 1e-20, 1e20, 1e35, 3e38])
+def test_attention_of_bf16_queries_of_any_size(code, amp):
+    """Queries over bf16's whole range beside keys of zero and (where the logits stay in
+    fp32's range) others."""
+    rng = np.random.default_rng(4)
+    lens = [150, 64, 20]
+    c = Cache(1, 4, 32, len(lens), 5, BF16, code)
+    v, n = c.vec(rng, sum(lens), 1), sum(lens)
+    for zero in (True, False):
+        if not zero and amp > 1e35:
+            continue
+        k = torch.zeros((n, 1, 128), dtype=BF16, device="cuda")
+        if not zero:
+            k = (c.vec(rng, n, 1).float() * min(1.0, 1e30 / amp)).to(BF16)
+        q = c.vec(rng, len(lens), 4).float()
+        q = (q / q.abs().max() * amp).to(BF16)
+        c.append(None, [0] * len(lens), lens, k, v)
+        out = c.attend(None, lens, q)
+        assert torch.isfinite(out).all()
+        c.check_attention(out, range(len(lens)), lens, q)
