@@ -1,6 +1,7 @@
 // cache8.cu — host side of the uniform 8-bit cache's entry points
-// (include/dkv.h) and the append kernels: rotation of keys and queries,
-// 16-bit tails, quantisation of completed blocks.
+// (include/dkv.h) and the append kernels: rotation of keys and queries by one
+// position or one of each axis, 16-bit tails, quantisation of completed blocks,
+// accepted drafts.
 #include <algorithm>
 #include <type_traits>
 
@@ -52,6 +53,33 @@ __device__ __forceinline__ Rot4 load_rot(const float2* rope, int rot, int pos, c
   return r;
 }
 
+// The same with a position of its own for each pair (four axes in the bytes of
+// axes, pairs pair0 onwards): token `row` of the call. Pairs of one axis, the usual
+// case where axes take parts of the head, lie together in the table.
+__device__ __forceinline__ Rot4 load_rot_at(const Cache8View& c, const Append8Args& a, uint32_t axes, long long row,
+                                            int info, const Quad& x) {
+  Rot4 r = {};
+  if (!x.turn) return r;
+  auto position = [&](int i) {
+    int p = __ldg(a.pos + (axes >> (8 * i) & 0xffu) * a.n_tok + row);
+    if ((unsigned)p >= (unsigned)a.rope_len) {
+      c.latch(DKV_ERR_ARG, info);
+      p = 0;
+    }
+    return p;
+  };
+  if (axes == (axes & 0xffu) * 0x01010101u) return load_rot(a.rope, c.rot, position(0), x);
+  int p[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) p[i] = position(i);
+#pragma unroll
+  for (int i = 0; i < 4; i++) r.cs[i] = __ldg(a.rope + (size_t)p[i] * (c.rot / 2) + x.pair0 + i);
+  return r;
+}
+__device__ __forceinline__ uint32_t axes_of(const Append8Args& a, int j) {
+  return *reinterpret_cast<const uint32_t*>(a.axis + 4 * j);
+}
+
 // (a c - b s, b c + a s), every operation rounded by itself
 __device__ __forceinline__ void turn_pair(float& a, float& b, float2 cs) {
   const float y = __fsub_rn(__fmul_rn(a, cs.x), __fmul_rn(b, cs.y));
@@ -100,7 +128,7 @@ __device__ __forceinline__ bool valid(const Cache8View& c, const Append8Args& a,
     c.latch(DKV_ERR_TABLE_FULL, i);
     return false;
   }
-  if (c.rot && end > a.rope_len) {
+  if (c.rot && !a.pos && end > a.rope_len) {
     c.latch(DKV_ERR_ARG, i);
     return false;
   }
@@ -228,7 +256,7 @@ __device__ __forceinline__ void put_v(uint16_t* buf, int i, int f0, uint4 v) {
 // bytes: one request 2.1 us, 128 with 28 / 4 heads 5.2 us (7.5 with a row after
 // the other).
 constexpr int kStepThreads = 160;     // 16 x (2 + G) at most
-template <int ELEM, int CODE>
+template <int ELEM, int CODE, bool AT>
 __global__ void __launch_bounds__(kStepThreads) k_append8_step(Cache8View c, Append8Args a, int n_req) {
   extern __shared__ __align__(16) uint8_t sm[];
   pdl_launch_dependents();
@@ -256,7 +284,7 @@ __global__ void __launch_bounds__(kStepThreads) k_append8_step(Cache8View c, App
   const bool full = p == T - 1;
   uint16_t* tail = reinterpret_cast<uint16_t*>(c.tail + c.tail_head(w.slot, h));
   uint16_t* buf = reinterpret_cast<uint16_t*>(sm);
-  const Rot4 rot = load_rot(a.rope, c.rot, w.before, qd);
+  const Rot4 rot = AT ? load_rot_at(c, a, axes_of(a, j), i, i, qd) : load_rot(a.rope, c.rot, w.before, qd);
   int page = 0;
   if (full) {
     page = c.table[(size_t)w.slot * c.width + b];
@@ -301,7 +329,7 @@ __global__ void __launch_bounds__(kStepThreads) k_append8_step(Cache8View c, App
 // their own: 555 us instead of 490, and 143 us instead of 126 us for ragged pieces
 // in blocks of 128; V's neighbouring tokens exchanged to store pairs: 531 us
 // instead of 479 (spills).
-template <int ELEM, int CODE>
+template <int ELEM, int CODE, bool AT>
 __global__ void __launch_bounds__(512, 2)
     k_append8(Cache8View c, Append8Args a, int n_req, const __grid_constant__ AppendCall call) {
   extern __shared__ __align__(16) uint8_t sm[];
@@ -331,6 +359,7 @@ __global__ void __launch_bounds__(512, 2)
   const int gq = a.q ? c.G : 0;
   uint16_t* tail = reinterpret_cast<uint16_t*>(c.tail + c.tail_head(w.slot, h));
   uint16_t* buf = reinterpret_cast<uint16_t*>(sm);
+  const uint32_t axes = AT ? axes_of(a, threadIdx.x & 15) : 0u;
   while (true) {
     const int start = b * T;
     // tokens of this call inside the block: places [lo, hi)
@@ -357,7 +386,7 @@ __global__ void __launch_bounds__(512, 2)
       const int p = lo + (x >> 4), j = x & 15;
       const long long row = r0 + p;
       const Quad qd = quad_of(j, c.rot, c.inter);
-      const Rot4 rot = load_rot(a.rope, c.rot, start + p, qd);
+      const Rot4 rot = AT ? load_rot_at(c, a, axes, row, i, qd) : load_rot(a.rope, c.rot, start + p, qd);
       const uint8_t* ks = a.k + row * a.ks + h * (2 * kD);
       const uint8_t* qs = a.q + row * a.qs + (size_t)h * c.G * (2 * kD);
       uint8_t* dq = a.q_rot + (row * c.hkv + h) * (size_t)c.G * (2 * kD);
@@ -403,13 +432,126 @@ __global__ void __launch_bounds__(512, 2)
   }
 }
 
+// Accepted drafts: a block of threads per request, KV head and block of tokens that
+// a path can touch; the keys are turned already. Bound by latency: request, path,
+// rows, then tail or page.
+constexpr int kAcceptThreads = 256;
+constexpr int kStoreSmem = 128 * 4 * kD + 256;      // the largest block
 template <int ELEM, int CODE>
+__global__ void __launch_bounds__(kAcceptThreads) k_accept8(Cache8View c, Accept8Args a, int n_req, int jobs) {
+  extern __shared__ __align__(16) uint8_t sm[];
+  pdl_launch_dependents();
+  pdl_wait();
+  if (c.stopped()) return;
+  const int h = blockIdx.x % c.hkv, job = blockIdx.x / c.hkv, i = job / jobs, jb = job - i * jobs;
+  Append8Args slots_of;
+  slots_of.slots = a.slots;
+  slots_of.before = a.before;
+  if (i == n_req) {
+    check_slots(c, slots_of, n_req, reinterpret_cast<uint32_t*>(sm));
+    return;
+  }
+  int n = a.n_path ? a.n_path[i] : a.width;
+  const int before = a.before[i], slot = a.slots ? a.slots[i] : i;
+  if (before < 0 || n <= 0) return;
+  int err = 0;
+  if ((unsigned)slot >= (unsigned)c.n_slots || n > a.width) err = DKV_ERR_ARG;
+  else if ((long long)before + n > (long long)c.width * c.T) err = DKV_ERR_TABLE_FULL;
+  if (err) {
+    c.latch(err, i);
+    return;
+  }
+  const int T = c.T, first = before / T, open = (before + n) / T, used = before - first * T;
+  int b = first + jb;
+  const bool both = used > 0 && open > first;     // as in k_append8
+  if (both && b == open) return;
+  uint16_t* tail = reinterpret_cast<uint16_t*>(c.tail + c.tail_head(slot, h));
+  uint16_t* buf = reinterpret_cast<uint16_t*>(sm);
+  while (true) {
+    const int start = b * T, lo = max(before - start, 0), hi = min(before + n - start, T);
+    if (hi <= lo) return;
+    const bool full = hi == T;
+    int page = 0;
+    if (full) {
+      page = c.table[(size_t)slot * c.width + b];
+      if ((unsigned)page >= (unsigned)c.n_pages) {
+        if (threadIdx.x == 0) c.latch(DKV_ERR_CHECK, i);
+        return;
+      }
+      if (lo > 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(tail);
+        uint4* dst = reinterpret_cast<uint4*>(buf);
+        for (int x = threadIdx.x; x < T * 2 * kD / 8; x += blockDim.x) dst[x] = src[x];
+        __syncthreads();
+      }
+    }
+    uint16_t* to = full ? buf : tail;
+    for (int x = threadIdx.x; x < (hi - lo) * 16; x += blockDim.x) {
+      const int p = lo + (x >> 4), j = x & 15;
+      int node = a.path[(size_t)i * a.width + (start + p - before)];
+      if ((unsigned)node >= (unsigned)a.max_nodes) {
+        c.latch(DKV_ERR_ARG, i);
+        node = 0;
+      }
+      const long long row = (long long)i * a.max_nodes + node;
+      const uint4 u = *reinterpret_cast<const uint4*>(a.k + row * a.ks + h * (2 * kD) + 16 * j);
+      const uint4 v = *reinterpret_cast<const uint4*>(a.v + row * a.vs + h * (2 * kD) + 16 * j);
+      put_k(to, p, quad_of(j, 0, 0), make_uint2(u.x, u.y), make_uint2(u.z, u.w));
+      put_v(to, p, 8 * j, v);
+    }
+    if (full) {
+      __syncthreads();
+      quantise_block<ELEM, CODE>(c, buf, page, h, reinterpret_cast<uint32_t*>(sm + (size_t)T * 4 * kD));
+    }
+    if (!both || b != first) return;
+    b = open;
+    __syncthreads();
+  }
+}
+
+// Keys and queries turned without being stored: 16 threads a token, each with the
+// angles of eight features for kRotHeads heads, whose loads are in flight together.
+constexpr int kRotHeads = 8, kRotThreads = 256;
+template <int ELEM>
+__global__ void __launch_bounds__(kRotThreads) k_rotate8(Cache8View c, Append8Args a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  if (c.stopped()) return;
+  const int hk = a.k ? c.hkv : 0, heads = hk + (a.q ? c.hkv * c.G : 0), parts = (heads + kRotHeads - 1) / kRotHeads;
+  const int j = threadIdx.x & 15;
+  const long long row = (long long)(blockIdx.x / parts) * (kRotThreads / 16) + (threadIdx.x >> 4);
+  const int h0 = (blockIdx.x % parts) * kRotHeads;
+  if (row >= a.n_tok || a.pos[row] < 0) return;       // below 0: padding
+  const Quad qd = quad_of(j, c.rot, c.inter);
+  uint2 u[kRotHeads], v[kRotHeads];
+  auto place = [&](int h, const uint8_t* k, long long ks, const uint8_t* q, long long qs) {
+    return h < hk ? k + row * ks + h * (2 * kD) : q + row * qs + (h - hk) * (2 * kD);
+  };
+#pragma unroll
+  for (int e = 0; e < kRotHeads; e++)
+    if (h0 + e < heads) {
+      const uint8_t* p = place(h0 + e, a.k, a.ks, a.q, a.qs);
+      u[e] = ld8(p + 2 * qd.a0);
+      v[e] = ld8(p + 2 * qd.b0);
+    }
+  const Rot4 rot = load_rot_at(c, a, axes_of(a, j), row, (int)min(row, 0x7fffffffll), qd);
+#pragma unroll
+  for (int e = 0; e < kRotHeads; e++)
+    if (h0 + e < heads) {
+      turn_quad<ELEM>(u[e], v[e], qd, rot, c.inter);
+      uint8_t* p = const_cast<uint8_t*>(place(h0 + e, a.k_rot, c.hkv * (2 * kD), a.q_rot, (long long)c.hkv * c.G * (2 * kD)));
+      st8(p + 2 * qd.a0, u[e]);
+      st8(p + 2 * qd.b0, v[e]);
+    }
+}
+
+template <int ELEM, int CODE, bool AT>
 cudaError_t append_typed(const Cache8View& c, const Append8Args& a, int n_req, const int32_t* n_new, cudaStream_t st) {
   const size_t smem = std::max<size_t>((size_t)c.T * 4 * kD + 256, a.slots ? (size_t)(c.n_slots + 31) / 32 * 4 : 0);
   const unsigned hkv = (unsigned)c.hkv;
   cudaError_t e = cudaSuccess;
   if (!n_new) {
-    auto kernel = k_append8_step<ELEM, CODE>;
+    auto kernel = k_append8_step<ELEM, CODE, AT>;
     if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, dim3(n_req * hkv + 1), dim3(kStepThreads), smem, st, c, a, n_req);
@@ -420,10 +562,28 @@ cudaError_t append_typed(const Cache8View& c, const Append8Args& a, int n_req, c
     call.tok0[i + 1] = call.tok0[i] + n_new[i];
     call.blk0[i + 1] = call.blk0[i] + (n_new[i] + c.T - 2) / c.T + 1;     // blocks that n tokens can touch
   }
-  auto kernel = k_append8<ELEM, CODE>;
+  auto kernel = k_append8<ELEM, CODE, AT>;
   if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kernel, dim3(call.blk0[n_req] * hkv + 1), dim3(4 * c.T), smem, st, c, a, n_req, call);
+}
+
+template <int ELEM, int CODE>
+cudaError_t append_typed(const Cache8View& c, const Append8Args& a, int n_req, const int32_t* n_new, cudaStream_t st) {
+  return a.pos ? append_typed<ELEM, CODE, true>(c, a, n_req, n_new, st)
+               : append_typed<ELEM, CODE, false>(c, a, n_req, n_new, st);
+}
+
+template <int ELEM, int CODE>
+cudaError_t accept_typed(const Cache8View& c, const Accept8Args& a, int n_req, cudaStream_t st) {
+  const int jobs = (a.width + c.T - 2) / c.T + 1;     // blocks that a path can touch
+  const size_t smem = std::max<size_t>((size_t)c.T * 4 * kD + 256, a.slots ? (size_t)(c.n_slots + 31) / 32 * 4 : 0);
+  auto kernel = k_accept8<ELEM, CODE>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStoreSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dependent(kernel, dim3((unsigned)(n_req * jobs * c.hkv + 1)), dim3(kAcceptThreads), smem, st, c, a, n_req, jobs);
 }
 
 }  // namespace
@@ -435,6 +595,19 @@ cudaError_t launch_append8(const Cache8View& c, int elem, int code, const Append
                             : append_typed<DKV_F16, DKV_INT8>(c, a, n_req, n_new, st);
   return code == DKV_E4M3 ? append_typed<DKV_BF16, DKV_E4M3>(c, a, n_req, n_new, st)
                           : append_typed<DKV_BF16, DKV_INT8>(c, a, n_req, n_new, st);
+}
+
+cudaError_t launch_accept8(const Cache8View& c, int elem, int code, const Accept8Args& a, int n_req, cudaStream_t st) {
+  if (elem == DKV_F16)
+    return code == DKV_E4M3 ? accept_typed<DKV_F16, DKV_E4M3>(c, a, n_req, st) : accept_typed<DKV_F16, DKV_INT8>(c, a, n_req, st);
+  return code == DKV_E4M3 ? accept_typed<DKV_BF16, DKV_E4M3>(c, a, n_req, st) : accept_typed<DKV_BF16, DKV_INT8>(c, a, n_req, st);
+}
+
+cudaError_t launch_rotate8(const Cache8View& c, int elem, const Append8Args& a, cudaStream_t st) {
+  const int heads = (a.k ? c.hkv : 0) + (a.q ? c.hkv * c.G : 0);
+  const long long tokens = (a.n_tok + kRotThreads / 16 - 1) / (kRotThreads / 16), parts = (heads + kRotHeads - 1) / kRotHeads;
+  return launch_dependent(elem == DKV_F16 ? k_rotate8<DKV_F16> : k_rotate8<DKV_BF16>, dim3((unsigned)(tokens * parts)),
+                          dim3(kRotThreads), 0, st, c, a);
 }
 
 }  // namespace dkv
@@ -520,9 +693,80 @@ Cache8View view(const dkv_cache8* c) {
   return v;
 }
 
+// Positions of a call's tokens and the axis of each pair of features.
+struct Turn {
+  const int32_t* positions;
+  int32_t n_axes;
+  const uint8_t* pair_axis;
+  int fill(const dkv_cache8* c, long long n_tok, Append8Args& a) const {
+    if (!c->rotary_dim || !positions || !at(positions, 4) || n_axes < 1 || n_axes > kMaxAxes || (n_axes > 1 && !pair_axis))
+      return DKV_ERR_ARG;
+    for (int i = 0; i < kD / 2; i++) a.axis[i] = 0;
+    for (int i = 0; pair_axis && i < c->rotary_dim / 2; i++) {
+      if (pair_axis[i] >= n_axes) return DKV_ERR_ARG;
+      a.axis[i] = pair_axis[i];
+    }
+    a.pos = positions;
+    a.n_tok = n_tok;
+    return DKV_OK;
+  }
+};
+
 int sm_count(int device) {
   int n = 0;
   return cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) == cudaSuccess ? n : 0;
+}
+
+int append(const dkv_cache8* cache, int32_t n_req, const int32_t* n_new, const int32_t* slots, const int32_t* before,
+           const Turn* turn, const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+           int64_t q_stride, const float* rope, int32_t rope_len, void* k_rot, void* q_rot, void* stream) {
+  const int rc = check_cache(cache, true);
+  if (rc) return rc;
+  if (n_req < 1 || n_req > kMaxCallReq || !before || !at(before, 4) || !at(slots, 4)) return DKV_ERR_ARG;
+  if (!slots && n_req > cache->n_slots) return DKV_ERR_ARG;
+  const int hkv = cache->n_kv_heads, hq = hkv * cache->group_size;
+  if (!rows_ok(k, k_stride, hkv) || !rows_ok(v, v_stride, hkv)) return DKV_ERR_ARG;
+  if ((q != nullptr) != (q_rot != nullptr) || (q && !rows_ok(q, q_stride, hq))) return DKV_ERR_ARG;
+  if (!at(k_rot, 16) || !at(q_rot, 16)) return DKV_ERR_ARG;
+  if (k_rot == k && k_stride != (int64_t)hkv * kD) return DKV_ERR_ARG;
+  if (q && q_rot == q && q_stride != (int64_t)hq * kD) return DKV_ERR_ARG;
+  if ((cache->rotary_dim != 0) != (rope != nullptr) || !at(rope, 16)) return DKV_ERR_ARG;
+  if (rope && rope_len < 1) return DKV_ERR_ARG;
+  long long tok = n_req, blk = 0;
+  if (n_new) {
+    tok = 0;
+    const int t = cache->block_tokens;
+    for (int i = 0; i < n_req; i++) {
+      if (n_new[i] < 1 || n_new[i] > (long long)cache->table_width * t) return DKV_ERR_ARG;
+      tok += n_new[i];
+      blk += (n_new[i] + t - 2) / t + 1;
+      if (tok > 0x7fffffffll || blk * hkv > 0x7ffffff0ll) return DKV_ERR_ARG;   // rows and jobs are 32-bit
+    }
+  }
+  Append8Args a;
+  if (turn) {
+    const int e = turn->fill(cache, tok, a);
+    if (e) return e;
+  } else {
+    a.pos = nullptr;
+  }
+  Device8 dev(cache->device);
+  if (!dev.ok) return result(cudaErrorInvalidDevice);
+  a.k = static_cast<const uint8_t*>(k);
+  a.v = static_cast<const uint8_t*>(v);
+  a.q = static_cast<const uint8_t*>(q);
+  a.ks = 2 * k_stride;
+  a.vs = 2 * v_stride;
+  a.qs = 2 * q_stride;
+  a.rope = reinterpret_cast<const float2*>(rope);
+  a.rope_len = rope_len;
+  a.k_rot = static_cast<uint8_t*>(k_rot);
+  a.q_rot = static_cast<uint8_t*>(q_rot);
+  a.slots = slots;
+  a.before = before;
+  const cudaError_t e = launch_append8(view(cache), cache->elem_type, cache->code_type, a, n_req, n_new,
+                                       reinterpret_cast<cudaStream_t>(stream));
+  return result(e);
 }
 
 }  // namespace
@@ -543,46 +787,107 @@ int dkv_cache8_append(const dkv_cache8* cache, int32_t n_req, const int32_t* n_n
                       const int32_t* before, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                       const void* q, int64_t q_stride, const float* rope, int32_t rope_len, void* k_rot,
                       void* q_rot, void* stream) {
-  const int rc = check_cache(cache, true);
+  return append(cache, n_req, n_new, slots, before, nullptr, k, k_stride, v, v_stride, q, q_stride, rope, rope_len, k_rot,
+                q_rot, stream);
+}
+
+int dkv_cache8_append_at(const dkv_cache8* cache, int32_t n_req, const int32_t* n_new, const int32_t* slots,
+                         const int32_t* before, const int32_t* positions, int32_t n_axes, const uint8_t* pair_axis,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                         const float* rope, int32_t rope_len, void* k_rot, void* q_rot, void* stream) {
+  const Turn turn{positions, n_axes, pair_axis};
+  return append(cache, n_req, n_new, slots, before, &turn, k, k_stride, v, v_stride, q, q_stride, rope, rope_len, k_rot,
+                q_rot, stream);
+}
+
+int dkv_cache8_rotate(const dkv_cache8* cache, int32_t n_tok, const int32_t* positions, int32_t n_axes,
+                      const uint8_t* pair_axis, const void* k, int64_t k_stride, const void* q, int64_t q_stride,
+                      const float* rope, int32_t rope_len, void* k_rot, void* q_rot, void* stream) {
+  const int rc = check_cache(cache, false);
   if (rc) return rc;
-  if (n_req < 1 || n_req > kMaxCallReq || !before || !at(before, 4) || !at(slots, 4)) return DKV_ERR_ARG;
-  if (!slots && n_req > cache->n_slots) return DKV_ERR_ARG;
   const int hkv = cache->n_kv_heads, hq = hkv * cache->group_size;
-  if (!rows_ok(k, k_stride, hkv) || !rows_ok(v, v_stride, hkv)) return DKV_ERR_ARG;
-  if ((q != nullptr) != (q_rot != nullptr) || (q && !rows_ok(q, q_stride, hq))) return DKV_ERR_ARG;
-  if (!at(k_rot, 16) || !at(q_rot, 16)) return DKV_ERR_ARG;
-  if (k_rot == k && k_stride != (int64_t)hkv * kD) return DKV_ERR_ARG;
+  if (n_tok < 1 || (!k && !q) || (k != nullptr) != (k_rot != nullptr) || (q != nullptr) != (q_rot != nullptr)) return DKV_ERR_ARG;
+  if ((k && !rows_ok(k, k_stride, hkv)) || (q && !rows_ok(q, q_stride, hq)) || !at(k_rot, 16) || !at(q_rot, 16)) return DKV_ERR_ARG;
+  if (k && k_rot == k && k_stride != (int64_t)hkv * kD) return DKV_ERR_ARG;
   if (q && q_rot == q && q_stride != (int64_t)hq * kD) return DKV_ERR_ARG;
-  if ((cache->rotary_dim != 0) != (rope != nullptr) || !at(rope, 16)) return DKV_ERR_ARG;
-  if (rope && rope_len < 1) return DKV_ERR_ARG;
-  if (n_new) {
-    long long tok = 0, blk = 0;
-    const int t = cache->block_tokens;
-    for (int i = 0; i < n_req; i++) {
-      if (n_new[i] < 1 || n_new[i] > (long long)cache->table_width * t) return DKV_ERR_ARG;
-      tok += n_new[i];
-      blk += (n_new[i] + t - 2) / t + 1;
-      if (tok > 0x7fffffffll || blk * hkv > 0x7ffffff0ll) return DKV_ERR_ARG;   // rows and jobs are 32-bit
-    }
-  }
+  if (!rope || !at(rope, 16) || rope_len < 1) return DKV_ERR_ARG;
+  // blocks of 16 tokens and 8 heads are numbered in 32 bits
+  if (((long long)n_tok / 16 + 1) * ((hkv + hq) / 8 + 1) > 0x7ffffff0ll) return DKV_ERR_ARG;
+  Append8Args a;
+  const int e = Turn{positions, n_axes, pair_axis}.fill(cache, n_tok, a);
+  if (e) return e;
   Device8 dev(cache->device);
   if (!dev.ok) return result(cudaErrorInvalidDevice);
-  Append8Args a;
   a.k = static_cast<const uint8_t*>(k);
-  a.v = static_cast<const uint8_t*>(v);
+  a.v = nullptr;
   a.q = static_cast<const uint8_t*>(q);
   a.ks = 2 * k_stride;
-  a.vs = 2 * v_stride;
+  a.vs = 0;
   a.qs = 2 * q_stride;
   a.rope = reinterpret_cast<const float2*>(rope);
   a.rope_len = rope_len;
   a.k_rot = static_cast<uint8_t*>(k_rot);
   a.q_rot = static_cast<uint8_t*>(q_rot);
-  a.slots = slots;
-  a.before = before;
-  const cudaError_t e = launch_append8(view(cache), cache->elem_type, cache->code_type, a, n_req, n_new,
-                                       reinterpret_cast<cudaStream_t>(stream));
-  return result(e);
+  a.slots = a.before = nullptr;
+  return result(launch_rotate8(view(cache), cache->elem_type, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dkv_cache8_accept(const dkv_cache8* cache, int32_t n_req, const int32_t* slots, const int32_t* before,
+                      int32_t max_nodes, const int32_t* path, int32_t path_width, const int32_t* n_path, const void* k,
+                      int64_t k_stride, const void* v, int64_t v_stride, void* stream) {
+  const int rc = check_cache(cache, true);
+  if (rc) return rc;
+  if (n_req < 1 || n_req > kMaxCallReq || !before || !at(before, 4) || !at(slots, 4)) return DKV_ERR_ARG;
+  if (!slots && n_req > cache->n_slots) return DKV_ERR_ARG;
+  if (max_nodes < 1 || max_nodes > kMaxNodes || path_width < 1 || path_width > kMaxNodes) return DKV_ERR_ARG;
+  if (!path || !at(path, 4) || !at(n_path, 4)) return DKV_ERR_ARG;
+  const int hkv = cache->n_kv_heads;
+  if (!rows_ok(k, k_stride, hkv) || !rows_ok(v, v_stride, hkv)) return DKV_ERR_ARG;
+  Device8 dev(cache->device);
+  if (!dev.ok) return result(cudaErrorInvalidDevice);
+  const Accept8Args a{static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v), 2 * k_stride, 2 * v_stride,
+                      slots, before, path, n_path, max_nodes, path_width};
+  return result(launch_accept8(view(cache), cache->elem_type, cache->code_type, a, n_req, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dkv_cache8_tree_workspace(const dkv_cache8* cache, int32_t max_nodes, int64_t* bytes) {
+  const int rc = check_shape(cache);
+  if (rc) return rc;
+  if (!bytes || max_nodes < 1 || max_nodes > kMaxNodes) return DKV_ERR_ARG;
+  const int sms = sm_count(cache->device);
+  if (!sms) return result(cudaErrorInvalidDevice);
+  *bytes = (int64_t)tree8_workspace(cache->group_size, max_nodes, sms);
+  return DKV_OK;
+}
+
+int dkv_cache8_tree(const dkv_cache8* cache, int32_t n_req, const int32_t* slots, const int32_t* seq_lens,
+                    int32_t max_nodes, const int32_t* n_nodes, const int32_t* parents, const void* q, int64_t q_stride,
+                    const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* out, int32_t window,
+                    int32_t sinks, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int rc = check_cache(cache, true);
+  if (rc) return rc;
+  if (n_req < 1 || n_req > kMaxCallReq || !seq_lens || !at(seq_lens, 4) || !at(slots, 4)) return DKV_ERR_ARG;
+  if (!slots && n_req > cache->n_slots) return DKV_ERR_ARG;
+  if (max_nodes < 1 || max_nodes > kMaxNodes || !at(n_nodes, 4) || !at(parents, 4)) return DKV_ERR_ARG;
+  const int hkv = cache->n_kv_heads, hq = hkv * cache->group_size;
+  if (!rows_ok(q, q_stride, hq) || !rows_ok(k, k_stride, hkv) || !rows_ok(v, v_stride, hkv)) return DKV_ERR_ARG;
+  if (!out || !at(out, 16) || out == q || out == k || out == v || window < 0 || sinks < 0) return DKV_ERR_ARG;
+  const long long most = (long long)cache->table_width * cache->block_tokens;
+  // steps of 64 tokens of the whole call are numbered in 32 bits
+  const long long tiles = (max_nodes * cache->group_size + 127) / 128, steps = (most + 2 * kSub + max_nodes + 63) / 64 + 1;
+  if ((long long)n_req * hkv * tiles > 0x7ffffff0ll / steps) return DKV_ERR_ARG;
+  if (!workspace || !at(workspace, 16)) return DKV_ERR_ARG;
+  Device8 dev(cache->device);
+  if (!dev.ok) return result(cudaErrorInvalidDevice);
+  const int sms = sm_count(cache->device);
+  if (!sms) return result(cudaErrorInvalidDevice);
+  if (workspace_bytes < (int64_t)tree8_workspace(cache->group_size, max_nodes, sms)) return DKV_ERR_SCRATCH;
+  // a window that no position exceeds is none (and positions minus it stay in 32 bits)
+  if (window >= most + max_nodes) window = 0;
+  const Tree8Args a{slots, seq_lens, n_nodes, parents, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(k),
+                    static_cast<const uint8_t*>(v), 2 * q_stride, 2 * k_stride, 2 * v_stride, static_cast<uint8_t*>(out),
+                    n_req, max_nodes, window, sinks, static_cast<float*>(workspace)};
+  return result(launch_tree8(view(cache), cache->elem_type, cache->code_type, sms, a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dkv_cache8_attention(const dkv_cache8* cache, int32_t n_req, const int32_t* slots, const int32_t* seq_lens,

@@ -96,6 +96,21 @@ __device__ __forceinline__ void mma_elem(float* c, const uint32_t* a, uint32_t b
   }
 }
 
+// four codes as fp16, exact
+template <int CODE>
+__device__ __forceinline__ void code_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (CODE == DKV_E4M3) {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // byte b + 128 under the exponent of 1024, then 1152 off: exact
+    const uint32_t u = w ^ 0x80808080u;
+    lo = hsub2_u(prmt(u, 0x64646464u, 0x4140u), 0x64806480u);
+    hi = hsub2_u(prmt(u, 0x64646464u, 0x4342u), 0x64806480u);
+  }
+}
+
 // largest finite |x| so far
 __device__ __forceinline__ float amax_finite(float m, float x) {
   const float a = fabsf(x);
@@ -137,10 +152,39 @@ struct Append8Args {
   int rope_len;
   uint8_t *k_rot, *q_rot;
   const int *slots, *before;
+  // positions of the call's tokens, [axes][n_tok], and the axis of each pair of
+  // features (null: before[i] onwards)
+  const int* pos;
+  long long n_tok;
+  uint8_t axis[kD / 2];
 };
+
+// Drafted tokens on their way into the cache.
+struct Accept8Args {
+  const uint8_t *k, *v;
+  long long ks, vs;          // row strides in bytes
+  const int *slots, *before, *path, *n_path;
+  int max_nodes, width;      // rows of a request, entries of a path
+};
+
+// Attention for trees of drafted tokens.
+struct Tree8Args {
+  const int *slots, *seq_lens, *n_nodes, *parents;
+  const uint8_t *q, *k, *v;
+  long long qs, ks, vs;      // row strides in bytes
+  uint8_t* out;
+  int n_req, max_nodes, window, sinks;
+  float* part;
+};
+constexpr int kMaxNodes = 128;
+constexpr int kMaxAxes = 4;
 
 cudaError_t launch_append8(const Cache8View& c, int elem, int code, const Append8Args& a, int n_req,
                            const int32_t* n_new, cudaStream_t st);
+cudaError_t launch_rotate8(const Cache8View& c, int elem, const Append8Args& a, cudaStream_t st);
+cudaError_t launch_accept8(const Cache8View& c, int elem, int code, const Accept8Args& a, int n_req, cudaStream_t st);
+size_t tree8_workspace(int G, int max_nodes, int sm_count);
+cudaError_t launch_tree8(const Cache8View& c, int elem, int code, int sm_count, const Tree8Args& a, cudaStream_t st);
 cudaError_t launch_attention8(const Cache8View& c, int elem, int code, int sm_count, const int* slots,
                               const int* seq_lens, int n_req, const void* q, long long q_stride, void* out,
                               int window, int sinks, void* workspace, cudaStream_t st);

@@ -92,20 +92,6 @@ __device__ __forceinline__ Tiles tiles_of(int N, int T, int window, int sinks) {
   return t;
 }
 
-template <int CODE>
-__device__ __forceinline__ void code_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if (CODE == DKV_E4M3) {
-    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  } else {
-    // byte b + 128 under the exponent of 1024, then 1152 off: exact
-    const uint32_t u = w ^ 0x80808080u;
-    lo = hsub2_u(prmt(u, 0x64646464u, 0x4140u), 0x64806480u);
-    hi = hsub2_u(prmt(u, 0x64646464u, 0x4342u), 0x64806480u);
-  }
-}
-
 // Running state of a warp for one (request, KV head): lane 4g + t holds
 // queries 2t, 2t + 1; O rows are features 16 m + g and 16 m + g + 8.
 struct State {

@@ -28,7 +28,8 @@ EXPORTED = ("dkv_pool_create", "dkv_pool_destroy", "dkv_pool_geometry", "dkv_com
             "dkv_decode_attention", "dkv_decode_attention_static", "dkv_free_request", "dkv_pool_status", "dkv_pool_clear_error",
             "dkv_pool_export", "dkv_pool_set_thresholds", "dkv_pool_set_mid_thresholds", "dkv_prefill_attention",
             "dkv_compact_step_prefilled", "dkv_cache8_workspace", "dkv_cache8_append", "dkv_cache8_attention",
-            "dkv_cache8_prefill", "dkv_strerror")
+            "dkv_cache8_prefill", "dkv_cache8_append_at", "dkv_cache8_rotate", "dkv_cache8_tree",
+            "dkv_cache8_tree_workspace", "dkv_cache8_accept", "dkv_strerror")
 
 
 class dkv_config(C.Structure):
@@ -109,6 +110,11 @@ def load() -> C.CDLL:
         L.dkv_cache8_append.argtypes = [P, I, P, P, P, P, L64, P, L64, P, L64, P, I, P, P, P]
         L.dkv_cache8_attention.argtypes = [P, I, P, P, P, L64, P, I, I, P]
         L.dkv_cache8_prefill.argtypes = [P, I, P, P, L64, P, L64, P, L64, P, I, I, P]
+        L.dkv_cache8_append_at.argtypes = [P, I, P, P, P, P, I, P, P, L64, P, L64, P, L64, P, I, P, P, P]
+        L.dkv_cache8_rotate.argtypes = [P, I, P, I, P, P, L64, P, L64, P, I, P, P, P]
+        L.dkv_cache8_tree_workspace.argtypes = [P, I, C.POINTER(C.c_int64)]
+        L.dkv_cache8_tree.argtypes = [P, I, P, P, I, P, P, P, L64, P, L64, P, L64, P, I, I, P, L64, P]
+        L.dkv_cache8_accept.argtypes = [P, I, P, P, I, P, I, P, P, L64, P, L64, P]
         L.dkv_strerror.argtypes = [C.c_int]
         L.dkv_strerror.restype = C.c_char_p
         for f in EXPORTED:
@@ -302,7 +308,8 @@ def dkv_pool_export(pool, cfg: dict, table_len: int, pages: bool = True, count_s
 # ---- uniform 8-bit cache ----------------------------------------------------
 
 def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: int = 0, rotary_interleaved: bool = False,
-                max_req: int | None = None, status=None, workspace=None) -> dkv_cache8:
+                max_req: int | None = None, status=None, workspace=None, max_nodes: int = 0,
+                tree_workspace=None) -> dkv_cache8:
     """Descriptor of a layer's uniform 8-bit cache over the caller's tensors:
     pages [n_pages][Hkv][T/16][2][2048] (torch.float8_e4m3fn or torch.int8),
     scales fp32 [n_pages][Hkv][2], tail [n_slots][Hkv][T/16][2][2048] (float16
@@ -310,7 +317,9 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
     workspace for attention calls of up to max_req requests (default: one a
     slot, at most 1024) are allocated here unless given, and zero when this returns
     (made while a graph is captured: by the graph); layers of one head layout whose
-    calls are ordered on one stream may share a workspace."""
+    calls are ordered on one stream may share a workspace. max_nodes > 0: also a
+    tree_workspace for tree attention of up to so many drafts a request, unless
+    given; layers may share it in the same way."""
     import torch
     codes = {torch.float8_e4m3fn: DKV_E4M3, torch.int8: DKV_INT8}
     elems = {torch.float16: DKV_F16, torch.bfloat16: DKV_BF16}
@@ -354,7 +363,13 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
     c.not_finite = status[2:3]        # 1 once a row of prompt attention came out infinite or NaN; the caller may zero it
     # plain copies of what every call reads
     c.address, c.heads, c.q_heads, c.pairs = C.addressof(c), hkv, hkv * group_size, rotary_dim // 2
-    c.tensors = (pages, scales, tail, page_table, status, workspace)
+    if max_nodes and tree_workspace is None:
+        n = C.c_int64()
+        _check(load().dkv_cache8_tree_workspace(c.address, int(max_nodes), C.byref(n)), "dkv_cache8_tree_workspace")
+        tree_workspace = torch.empty(n.value, dtype=torch.uint8, device=pages.device)
+    c.tree_workspace = _on(c, tree_workspace, torch.uint8, "tree_workspace")
+    c.tree_bytes = 0 if tree_workspace is None else tree_workspace.numel()
+    c.tensors = (pages, scales, tail, page_table, status, workspace, tree_workspace)
     return c
 
 
@@ -440,6 +455,114 @@ def dkv_cache8_append(cache: dkv_cache8, before, k, v, rope=None, n_new=None, sl
         positions, _on(cache, k_rot, elem, "k_rot", heads * cache.heads),
         _on(cache, q_rot, elem, "q_rot", heads * cache.q_heads), _stream8(cache, stream))
     return _check(rc, "dkv_cache8_append") if check else rc
+
+
+def _axes8(cache, positions, pair_axis, n_tok):
+    """Address and number of axes of positions [axes][n_tok] (or [n_tok]: one), the
+    axis of each pair as bytes."""
+    import torch
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.shape not in ((axes, n_tok), (n_tok,)):
+        raise ValueError(f"positions must be [axes][{n_tok}], got {tuple(positions.shape)}")
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != cache.pairs:
+            raise ValueError(f"pair_axis has one entry for each of {cache.pairs} pairs")
+    return _on(cache, positions, torch.int32, "positions"), axes, pair_axis
+
+
+def dkv_cache8_append_at(cache: dkv_cache8, before, positions, k, v, rope, pair_axis=None, n_new=None, slots=None, q=None,
+                         k_rot=None, q_rot=None, stream=None, check: bool = True) -> int:
+    """dkv_cache8_append with positions of their own for the call's tokens: device
+    int32 [axes][tokens] (or [tokens]); pair_axis (host, one entry a pair of features)
+    names the axis that each pair turns by."""
+    import torch
+    n_req, i32 = before.numel(), torch.int32
+    lens, total = None, n_req
+    if n_new is not None:
+        keep, lens, size, total = _lens8(n_new)
+        if size != n_req:
+            raise ValueError("n_new and before have one entry per request")
+    at, axes, pair_axis = _axes8(cache, positions, pair_axis, total)
+    kp, ks = _rows(cache, k, cache.heads, total, "k")
+    vp, vs = _rows(cache, v, cache.heads, total, "v")
+    qp, qs = (None, 0) if q is None else _rows(cache, q, cache.q_heads, total, "q")
+    length, pairs, two = rope.shape
+    if pairs != cache.pairs or two != 2:
+        raise ValueError(f"rope must be [positions][{cache.pairs}][2]")
+    elem, heads = cache.elem_dtype, 128 * total
+    rc = load().dkv_cache8_append_at(
+        cache.address, n_req, lens, _on(cache, slots, i32, "slots", n_req), _on(cache, before, i32, "before"), at, axes,
+        pair_axis, kp, ks, vp, vs, qp, qs, _on(cache, rope, torch.float32, "rope"), length,
+        _on(cache, k_rot, elem, "k_rot", heads * cache.heads), _on(cache, q_rot, elem, "q_rot", heads * cache.q_heads),
+        _stream8(cache, stream))
+    return _check(rc, "dkv_cache8_append_at") if check else rc
+
+
+def dkv_cache8_rotate(cache: dkv_cache8, positions, rope, q=None, k=None, q_rot=None, k_rot=None, pair_axis=None, stream=None,
+                      check: bool = True) -> int:
+    """Turn queries and keys ([tokens][heads][128]) by positions (device int32
+    [axes][tokens] or [tokens]) without storing them; tokens of a negative position are
+    padding."""
+    import torch
+    n = positions.shape[-1]
+    at, axes, pair_axis = _axes8(cache, positions, pair_axis, n)
+    kp, ks = (None, 0) if k is None else _rows(cache, k, cache.heads, n, "k")
+    qp, qs = (None, 0) if q is None else _rows(cache, q, cache.q_heads, n, "q")
+    length, pairs, two = rope.shape
+    if pairs != cache.pairs or two != 2:
+        raise ValueError(f"rope must be [positions][{cache.pairs}][2]")
+    elem = cache.elem_dtype
+    rc = load().dkv_cache8_rotate(cache.address, n, at, axes, pair_axis, kp, ks, qp, qs, _on(cache, rope, torch.float32, "rope"),
+                                  length, _on(cache, k_rot, elem, "k_rot", 128 * n * cache.heads),
+                                  _on(cache, q_rot, elem, "q_rot", 128 * n * cache.q_heads), _stream8(cache, stream))
+    return _check(rc, "dkv_cache8_rotate") if check else rc
+
+
+def _drafts8(cache, n_req, rows):
+    """Drafts of a request where there are so many rows in all."""
+    nodes = rows // n_req if n_req else 0
+    if nodes < 1 or nodes * n_req != rows:
+        raise ValueError("drafts have the same number of rows for each request")
+    return nodes
+
+
+def dkv_cache8_tree(cache: dkv_cache8, seq_lens, parents, q, k, v, out, n_nodes=None, window: int = 0, sinks: int = 0,
+                    slots=None, stream=None, check: bool = True) -> int:
+    """Attention for trees of drafted tokens over a uniform 8-bit cache made with
+    max_nodes: seq_lens (device int32 [n_req]) tokens are stored, q, k, v and out hold
+    max_nodes rows a request, of which n_nodes (device; None: all) are drafts; parents
+    (device int32 [n_req][max_nodes], -1: the last stored token; None: chains)."""
+    import torch
+    _window8(window, sinks)
+    i32, n_req = torch.int32, seq_lens.numel()
+    rows = q.shape[0]
+    nodes = _drafts8(cache, n_req, rows)
+    qp, qs = _rows(cache, q, cache.q_heads, rows, "q")
+    kp, ks = _rows(cache, k, cache.heads, rows, "k")
+    vp, vs = _rows(cache, v, cache.heads, rows, "v")
+    rc = load().dkv_cache8_tree(cache.address, n_req, _on(cache, slots, i32, "slots", n_req), _on(cache, seq_lens, i32, "seq_lens"),
+                                nodes, _on(cache, n_nodes, i32, "n_nodes", n_req), _on(cache, parents, i32, "parents", rows),
+                                qp, qs, kp, ks, vp, vs, _on(cache, out, cache.elem_dtype, "out", rows * cache.q_heads * 128),
+                                window, sinks, cache.tree_workspace, cache.tree_bytes, _stream8(cache, stream))
+    return _check(rc, "dkv_cache8_tree") if check else rc
+
+
+def dkv_cache8_accept(cache: dkv_cache8, before, k, v, path, n_path=None, slots=None, stream=None, check: bool = True) -> int:
+    """Append accepted drafts: the rows path[i][0 .. n_path[i]) (device int32; None:
+    all) of request i's drafts in k and v (turned already) follow its before[i]
+    tokens."""
+    import torch
+    i32, n_req, rows = torch.int32, before.numel(), k.shape[0]
+    if path.dim() != 2 or path.shape[0] != n_req:
+        raise ValueError("path is [n_req][width]")
+    nodes = _drafts8(cache, n_req, rows)
+    kp, ks = _rows(cache, k, cache.heads, rows, "k")
+    vp, vs = _rows(cache, v, cache.heads, rows, "v")
+    rc = load().dkv_cache8_accept(cache.address, n_req, _on(cache, slots, i32, "slots", n_req), _on(cache, before, i32, "before"),
+                                  nodes, _on(cache, path, i32, "path"), path.shape[1], _on(cache, n_path, i32, "n_path", n_req),
+                                  kp, ks, vp, vs, _stream8(cache, stream))
+    return _check(rc, "dkv_cache8_accept") if check else rc
 
 
 def dkv_cache8_attention(cache: dkv_cache8, seq_lens, q, out, window: int = 0, sinks: int = 0, slots=None,

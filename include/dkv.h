@@ -566,6 +566,83 @@ int dkv_cache8_prefill(const dkv_cache8* cache, int32_t n_req, const int32_t* se
                        int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                        void* out, int32_t window, int32_t sinks, void* stream);
 
+/* Positions of their own, one per axis: `positions` is a device int32 array
+ * [n_axes][tokens] (1 <= n_axes <= 4; time, height and width of images and video;
+ * or one axis, where a token's position is not its place in the cache, as behind an
+ * image or in a tree of drafts), pair_axis a host array [rotary_dim / 2] that names
+ * the axis of each pair of features (NULL: every pair turns by axis 0; needed for
+ * more than one axis). Pair i of token t turns by row
+ * positions[pair_axis[i]][t] of the rotation table, with the arithmetic of
+ * dkv_cache8_append. pair_axis is copied before the call returns. A position outside
+ * [0, rope_len) latches DKV_ERR_ARG. The cache's rotary_dim must not be 0.
+ *
+ * dkv_cache8_append_at: dkv_cache8_append with such positions for the tokens of
+ * the call, which still lie at places before[i] .. of their request (places, not
+ * positions, decide on blocks and windows). rope_len is not related to the
+ * cache's length here. */
+int dkv_cache8_append_at(const dkv_cache8* cache, int32_t n_req, const int32_t* n_new, const int32_t* slots,
+                         const int32_t* before, const int32_t* positions, int32_t n_axes, const uint8_t* pair_axis,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                         int64_t q_stride, const float* rope, int32_t rope_len, void* k_rot, void* q_rot,
+                         void* stream);
+
+/* Turn keys and queries of n_tok tokens without storing them, e.g. drafted tokens
+ * ahead of dkv_cache8_tree. k and k_rot, q and q_rot as for dkv_cache8_append (both
+ * or neither of a pair; one pair at least). A token whose position on axis 0 is
+ * negative is padding: its rows of k_rot and q_rot stay as they were. The cache
+ * supplies the head layout, elem_type, rotary_dim, rotary_interleaved, device and
+ * status only; status[1] is the token's index.
+ * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED (host, nothing queued); DKV_ERR_CUDA. */
+int dkv_cache8_rotate(const dkv_cache8* cache, int32_t n_tok, const int32_t* positions, int32_t n_axes,
+                      const uint8_t* pair_axis, const void* k, int64_t k_stride, const void* q, int64_t q_stride,
+                      const float* rope, int32_t rope_len, void* k_rot, void* q_rot, void* stream);
+
+/* Attention for trees of drafted tokens over the cache: request i has N =
+ * seq_lens[i] tokens stored (as for dkv_cache8_attention; N <= 0: none) in slot
+ * slots[i] and n_nodes[i] drafts (device int32 [n_req], at most max_nodes <= 128;
+ * NULL: max_nodes each; <= 0: padding, its slot may be any number) in rows
+ * i * max_nodes .. of q, k, v and out. Node m hangs on node parents[i][m] < m or, for
+ * -1, on the last stored token (device int32 [n_req][max_nodes]; NULL: chains, node m
+ * on node m - 1). A node of d ancestors has position p = N + d and
+ *   out[m][h] = softmax(q[m][h] . k^ / sqrt(128)) v^
+ * over the stored tokens j with window = 0, j > p - window or j < sinks, over its
+ * ancestors by the same rule with their positions, and itself. k^, v^ are
+ * the stored values and the drafts' k and v as they are (keys and queries turned
+ * already). Rows behind a request's nodes are neither read nor written.
+ *   q, k, v  device [n_req * max_nodes][heads][128], token rows *_stride elements
+ *            apart (multiples of 8); out contiguous, of elem_type, apart from them.
+ *   workspace  device, 16-byte aligned, at least dkv_cache8_tree_workspace bytes; what
+ *            it holds does not matter. Calls that may overlap need one each.
+ * Sums are in fp32. Weights enter the value product rounded to fp16 (relative 2^-11;
+ * below 2^-21 of the row's largest weighted scale, off by up to 2^-32 of it), the
+ * sum of weights unrounded; bf16 queries, tail entries and drafts meet the products
+ * as fp16 after division by a power of two (of a query row, or of the K or V of 16
+ * tokens; what lies below 2^-24 of the largest is lost). What a row does
+ * not see never enters its result, whatever it holds: rows that come out infinite
+ * or NaN are computed again over what they see, a warp a row. Means of finite values
+ * are finite. The same inputs give the same bits.
+ * Errors that only the device sees: DKV_ERR_ARG (also a parent outside [-1, m), n_nodes
+ * above max_nodes), DKV_ERR_TABLE_FULL, DKV_ERR_CHECK, DKV_ERR_TIMEOUT.
+ * Errors: DKV_ERR_ARG, DKV_ERR_UNSUPPORTED, DKV_ERR_SCRATCH (host, nothing queued);
+ * DKV_ERR_CUDA. */
+int dkv_cache8_tree(const dkv_cache8* cache, int32_t n_req, const int32_t* slots, const int32_t* seq_lens,
+                    int32_t max_nodes, const int32_t* n_nodes, const int32_t* parents, const void* q, int64_t q_stride,
+                    const void* k, int64_t k_stride, const void* v, int64_t v_stride, void* out, int32_t window,
+                    int32_t sinks, void* workspace, int64_t workspace_bytes, void* stream);
+int dkv_cache8_tree_workspace(const dkv_cache8* cache, int32_t max_nodes, int64_t* bytes);
+
+/* Append accepted drafts: request i's tokens path[i][0 .. n_path[i]) (node numbers
+ * below max_nodes, device int32 [n_req][path_width], path_width <= 128; n_path device
+ * int32 [n_req], NULL: path_width each, 0: none) lie in rows i * max_nodes + node of k
+ * and v, the keys turned already, and follow the before[i] tokens stored so far.
+ * They leave the same state as an append of those rows to a cache without rotation.
+ * Counts and paths are read on the device, so a captured step replays. Other
+ * conditions as for dkv_cache8_append. Errors that only the device sees: also
+ * DKV_ERR_ARG for n_path above path_width or a node outside [0, max_nodes). */
+int dkv_cache8_accept(const dkv_cache8* cache, int32_t n_req, const int32_t* slots, const int32_t* before,
+                      int32_t max_nodes, const int32_t* path, int32_t path_width, const int32_t* n_path, const void* k,
+                      int64_t k_stride, const void* v, int64_t v_stride, void* stream);
+
 /* Static description of an error code. */
 const char* dkv_strerror(int code);
 
