@@ -111,6 +111,34 @@ __device__ __forceinline__ void code_halves(uint32_t w, uint32_t& lo, uint32_t& 
   }
 }
 
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {     // without waiting
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// bits [0, n)
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+// Values of a tensor-memory load are used after the wait only.
+__device__ __forceinline__ void loaded32(float* v) {
+#pragma unroll
+  for (int e = 0; e < 32; e++) asm volatile("" : "+f"(v[e]));
+}
+
 // largest finite |x| so far
 __device__ __forceinline__ float amax_finite(float m, float x) {
   const float a = fabsf(x);

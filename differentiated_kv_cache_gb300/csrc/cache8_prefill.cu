@@ -166,15 +166,6 @@ __device__ __forceinline__ Parts parts_of(const Item& it, const W8Args& a, int h
   return p;
 }
 
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {     // without waiting
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // A block of the grid that has not begun yet is asked for, so that this one does
 // its work; the answer (16 bytes) completes the barrier.
 __device__ __forceinline__ void ask_item(uint32_t answer, uint32_t bar) {
@@ -195,25 +186,6 @@ __device__ __forceinline__ int told_item(uint32_t answer) {
       : "memory");
   return x;
 }
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// bits [0, n)
-__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
-// Values of a tensor-memory load are used after the wait only.
-__device__ __forceinline__ void loaded32(float* v) {
-#pragma unroll
-  for (int e = 0; e < 32; e++) asm volatile("" : "+f"(v[e]));
-}
-
 template <int ELEM>
 __global__ void __launch_bounds__(kW8Threads, 1)
     k_prefill8(Cache8View c, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,

@@ -15,11 +15,16 @@ constexpr int kT8Step = 4;          // tiles of a step
 constexpr int kT8Least = 2;         // steps that make a CTA worth its start
 constexpr int kT8Conv = 7;          // warps that convert
 constexpr int kT8Threads = 32 * (8 + kT8Conv + 1);
-constexpr int kT8Stages = 5;
+// registers a thread: launched with 128; 256 x 168 + 256 x 88 = 512 x 128
+constexpr int kT8RegsFew = 88, kT8RegsMany = 168;
+constexpr int kT8Stages = 4;        // even: a stage is of one half, which has seen its phases
 constexpr int kT8Stage = 32768;     // K, then V of a step in 16 bits
-constexpr int kT8Descs = 64;        // ring of a converting warp
-constexpr float kT8Lazy = 8.0f, kT8LazySum = 5.0f;     // how far x may pass m, y pass u
-constexpr float kT8Up = 7.0f;       // log2 of a weight at its maximum
+constexpr int kT8Descs = 64;        // descriptors of a converting warp, a ring
+constexpr int kT8Ring = 2;          // copies that it has on their way
+constexpr int kT8Pitch = 272;       // bytes from draft row to draft row (no bank conflicts)
+constexpr int kT8Entry = 16 * kT8Pitch;     // K and V codes of a tile, or K or V of a 16-bit one
+constexpr float kT8Up = 7.0f;       // log2 of a weight at its row's maximum
+constexpr float kT8Most = 32768.0f; // largest sum of a row's weights of one tile (fp16 holds 65504)
 
 // A request of the call: N tokens stored, M drafts (0: padding).
 struct TreeReq {
@@ -51,7 +56,8 @@ struct TreeTiles {
 __device__ __forceinline__ TreeTiles tree_tiles(int N, int M, int T, int window, int sinks) {
   TreeTiles t;
   t.end = (N + kSub - 1) / kSub;
-  t.full = N / T * (T / kSub);
+  const int lt = __ffs(T) - 1;      // T is a power of two, at least 16
+  t.full = N >> lt << (lt - 4);
   t.head = t.win = 0;
   if (window > 0 && window <= N) {          // a root (position N) sees those above N - window
     const int from = N - window + 1;
@@ -93,8 +99,6 @@ __device__ __forceinline__ Node node_of(const Cache8View& c, const Tree8Args& a,
     if (a.window <= 0 || back < a.window || N + n.depth - back < a.sinks) sees(x);
   return n;
 }
-// bits [0, n)
-__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 // Which of the 16 stored tokens from pos0 on a node sees, as bits.
 __device__ __forceinline__ uint32_t sees_stored(const Tree8Args& a, int N, int depth, int pos0) {
   uint32_t s = below(min(N - pos0, kSub));
@@ -391,19 +395,16 @@ struct TreeSmem {
   float4 ex[2][kT8Rows];       // m, u, l of the halves
   TreePlan plan;
   int parents[kMaxNodes];
-  float qs[kT8Rows];
+  uint32_t qmax[2][kT8Rows];   // bits of the largest |q| of the features that a half's warps load
   int scan[32];
   uint64_t bar[2 * kT8Stages + 10];
+  uint64_t rbar[kT8Conv][kT8Ring];
   uint32_t taddr;
   int fail;
 };
-constexpr int kT8Smem = 1024 + kT8Stages * kT8Stage + (int)sizeof(TreeSmem);
+constexpr int kT8OffRing = kT8Stages * kT8Stage, kT8OffSmem = kT8OffRing + kT8Conv * kT8Ring * kT8Entry;
+constexpr int kT8Smem = 1024 + kT8OffSmem + (int)sizeof(TreeSmem);
 
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
 __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
@@ -412,10 +413,6 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint3
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
                : "memory");
-}
-__device__ __forceinline__ void loaded32(float* v) {
-#pragma unroll
-  for (int e = 0; e < 32; e++) asm volatile("" : "+f"(v[e]));
 }
 // largest finite magnitude of bf16 pairs, as bits
 __device__ __forceinline__ uint32_t amax2_finite(uint32_t m, uint32_t w) {
@@ -432,19 +429,107 @@ __device__ __forceinline__ uint32_t half_of_bf16(uint32_t w, float f) {
   return pack_half2(lo_elem<DKV_BF16>(w) * f, hi_elem<DKV_BF16>(w) * f);
 }
 
+// One lane of the warp. A branch on it, not on the lane's number, leaves the products'
+// operands in uniform registers: an M = 128, K = 16 product with A in tensor memory
+// takes 42 (N = 64) and 74 cycles (N = 128) to issue, and 100 otherwise.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
+
+// Tile x of a CTA whose range begins at step lo.
+__device__ __forceinline__ void describe_tile(const Cache8View& c, const Tree8Args& a, const TreePlan& plan, int lo, int x, TileDesc& out) {
+  const int pos = lo + x / kT8Step;
+  const TreeItem it = tree_item(c, a, plan, pos, pos + 1);
+  x = kT8Step * it.s0 + x % kT8Step;
+  TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4};
+  if (x < it.tiles.stored) {
+    const int tile = it.tiles.tile(x);
+    d.pos0 = tile * kSub;
+    if (tile < it.tiles.full) {
+      const int per = __ffs(c.T) - 5;      // log2 of a block's tiles
+      int page = c.table[(size_t)it.slot * c.width + (tile >> per)];
+      if ((unsigned)page >= (unsigned)c.n_pages) {
+        c.latch(DKV_ERR_CHECK, it.i);
+        page = 0;
+      }
+      const float2 sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * c.hkv + it.h));
+      d.src = c.pages + c.page_head(page, it.h) + (size_t)(tile & ((1 << per) - 1)) * (2 * kTile);
+      d.ks = sc.x * kLogitScale;
+      d.lv = log2f(sc.y);
+      // every depth sees all of it
+      d.kind = a.window <= 0 || d.pos0 >= it.N + it.M - a.window || d.pos0 + kSub <= a.sinks ? 0 : 1;
+    } else {
+      d.src = c.tail + c.tail_head(it.slot, it.h) + (size_t)(tile - it.tiles.full) * (4 * kTile);
+      d.req_head = it.i << 12 | it.h;
+      d.kind = 2;
+    }
+  } else if (x < it.tiles.count) {
+    d.pos0 = (x - it.tiles.stored) * kSub;
+    d.req_head = it.i << 12 | it.h;
+    d.kind = 3;
+  }
+  out = d;
+}
+
+// K (op 0) or V of a tile of the tail (op + 0) or of drafts (op + 2), n tokens of it valid,
+// from its copy `src` in shared memory to fp16 operands (`at`: the lane's row of the first
+// four matrices). Returns the exponent of the power of two that the values were divided by.
+template <int ELEM>
+__device__ __noinline__ int put_elems(const uint8_t* src, int op, int n, uint32_t at) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const bool v = op & 1, draft = op & 2;
+  uint32_t x[32];
+  int ex = 0;
+  if (!draft) {
+    // what lies behind the request's tokens becomes 0 (0 times what it may hold is not)
+    const uint32_t lo_t = v ? (2 * t < n ? 0xffffu : 0u) | (2 * t + 1 < n ? 0xffff0000u : 0u) : g < n ? 0xffffffffu : 0u;
+    const uint32_t hi_t = v ? (2 * t + 8 < n ? 0xffffu : 0u) | (2 * t + 9 < n ? 0xffff0000u : 0u) : g + 8 < n ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int f = 0; f < 8; f++) {
+      const uint4 y = *reinterpret_cast<const uint4*>(src + 512 * f + 16 * lane);
+      x[4 * f] = y.x & lo_t;
+      x[4 * f + 1] = y.y & (v ? hi_t : lo_t);
+      x[4 * f + 2] = y.z & (v ? lo_t : hi_t);
+      x[4 * f + 3] = y.w & hi_t;
+    }
+  } else {
+#pragma unroll
+    for (int f = 0; f < 32; f++) {      // rows g, g + 8; features 16 m + 8 e + 2 t
+      const int row = g + 8 * (f >> 1 & 1);
+      const uint32_t y = *reinterpret_cast<const uint32_t*>(src + row * kT8Pitch + 2 * (16 * (f >> 2) + 8 * (f & 1) + 2 * t));
+      x[f] = row < n ? y : 0u;
+    }
+  }
+  if (ELEM == DKV_BF16) {
+    uint32_t am = 0;
+#pragma unroll
+    for (int f = 0; f < 32; f++) am = amax2_finite(am, x[f]);
+    ex = scale_exp(am);
+    const float inv = pow2(-ex);
+#pragma unroll
+    for (int f = 0; f < 32; f++) x[f] = half_of_bf16(x[f], inv);
+  }
+#pragma unroll
+  for (int f = 0; f < 8; f++) {
+    if (!v)
+      stmatrix4((at + (f >> 2) * 8192) ^ ((f & 3) << 5), x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
+    else if (!draft)
+      stmatrix4(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
+    else
+      stmatrix4_trans(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
+  }
+  return ex;
+}
+
 template <int ELEM, int CODE>
-__global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args a, int part_rows) {
+__global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__ Cache8View c, const __grid_constant__ Tree8Args a, int part_rows) {
   pdl_launch_dependents();
-  pdl_wait();
-  if (c.stopped()) return;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  TreeSmem& sm = *reinterpret_cast<TreeSmem*>(smem + kT8Stages * kT8Stage);
-  const int total = make_plan(c, a, sm.plan, sm.scan);
-  if (total == 0) return;
-  const int ctas = tree_ctas(total, gridDim.x);
-  if ((int)blockIdx.x >= ctas) return;
-  const int lo = range_start(total, blockIdx.x, ctas), hi = range_start(total, blockIdx.x + 1, ctas);
+  TreeSmem& sm = *reinterpret_cast<TreeSmem*>(smem + kT8OffSmem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, G = c.G;
   // step j of the CTA: half j & 1, its step j >> 1, stage j % kT8Stages
   const uint32_t b0 = smem_u32(sm.bar);
@@ -468,13 +553,24 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args
     }
     mbar_init(ready, 8);
     mbar_init(drain, 1);
+    for (int w = 0; w < kT8Conv * kT8Ring; w++) mbar_init(smem_u32(&sm.rbar[0][0]) + 8 * w, 1);
     sm.fail = 0;
     fence_mbar_init();
   }
   if (warp == 8 + kT8Conv) tmem_alloc(smem_u32(&sm.taddr), 512);
+  pdl_wait();
+  // an error of an earlier call (its load is in flight with the plan's)
+  const int halted = threadIdx.x == 0 ? *(volatile int*)c.status : 0;
+  const int total = make_plan(c, a, sm.plan, sm.scan);
   tc_fence_before();
-  __syncthreads();
+  const bool stopped = __syncthreads_or(halted);
   tc_fence_after();
+  const int ctas = tree_ctas(total, gridDim.x);
+  if (stopped || total == 0 || (int)blockIdx.x >= ctas) {
+    if (warp == 8 + kT8Conv) tmem_dealloc(__shfl_sync(0xffffffffu, sm.taddr, 0), 512);
+    return;
+  }
+  const int lo = range_start(total, blockIdx.x, ctas), hi = range_start(total, blockIdx.x + 1, ctas);
   const uint32_t tbase = __shfl_sync(0xffffffffu, sm.taddr, 0);
   // O of the halves, S of the halves, P of the halves, Q
   auto t_o = [&](int h) { return tbase + 128u * h; };
@@ -486,68 +582,96 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args
     *(volatile int*)&sm.fail = 1;
   };
   auto wait = [&](uint32_t bar, int phase) {       // the same for every lane
-    return __all_sync(0xffffffffu, *(volatile int*)&sm.fail == 0 && mbar_wait_bounded(bar, phase & 1)) != 0;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1))) return true;
+    return __all_sync(0xffffffffu, *(volatile int*)&sm.fail == 0 && wait_long(bar, phase & 1)) != 0;
   };
   bool ok = true;
 
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kT8RegsMany));
     // ---- softmax: a thread per query row, a half takes every other step ----
     const int half = warp >> 2, lg = warp & 3, r = 32 * lg + lane;
     const uint32_t tl = (uint32_t)(32 * lg) << 16;
     Node node;
-    int have_i = -1, have_t = -1;
-    for (int pos = lo, j0 = 0; pos < hi;) {
-      const TreeItem it = tree_item(c, a, sm.plan, pos, hi);
-      const int rows = it.M * G - it.t * kT8Rows, row = it.t * kT8Rows + r, m = row / G;
-      const bool real = r < rows, busy = 32 * lg < rows;
-      const bool fresh = it.i != have_i || it.t != have_t;
-      have_i = it.i;
-      have_t = it.t;
-      if (fresh && half == 1 && r < it.M && a.parents) sm.parents[r] = a.parents[(size_t)it.i * a.max_nodes + r];
-      if (half == 0 && busy) {
-        // the queries as fp16 (bf16: over a power of two of their row)
-        uint32_t q[64];
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + ((long long)it.i * a.max_nodes + m) * a.qs +
-                                                          ((size_t)it.h * G + (row - m * G)) * (2 * kD));
+    TreeItem it = tree_item(c, a, sm.plan, lo, hi);
+    int last_i = -1, last_t = -1, parent = 0;
+    uint4 qr[8];              // 64 features of the row, the other half's warps have the others
+    auto row_of = [&](const TreeItem& x) { return x.t * kT8Rows + r; };
+    auto real_of = [&](const TreeItem& x) { return row_of(x) < x.M * G; };
+    auto q_of = [&](const TreeItem& x) {
+      const int row = row_of(x), m = row / G;
+      return a.q + ((long long)x.i * a.max_nodes + m) * a.qs + ((size_t)x.h * G + (row - m * G)) * (2 * kD) + 128 * half;
+    };
+    auto load_row = [&](const TreeItem& x) {
+      const uint4* src = reinterpret_cast<const uint4*>(q_of(x));
+      const bool real = real_of(x);
 #pragma unroll
-        for (int e = 0; e < 16; e++) {
-          const uint4 w = real ? src[e] : make_uint4(0, 0, 0, 0);
-          q[4 * e] = w.x;
-          q[4 * e + 1] = w.y;
-          q[4 * e + 2] = w.z;
-          q[4 * e + 3] = w.w;
+      for (int e = 0; e < 8; e++) qr[e] = real ? src[e] : make_uint4(0, 0, 0, 0);
+      if (half == 1 && a.parents && r < x.M) parent = a.parents[(size_t)x.i * a.max_nodes + r];
+    };
+    load_row(it);
+    for (int pos = lo, j0 = 0;;) {
+      const int row = row_of(it), m = row / G;
+      const bool real = real_of(it), busy = 32 * lg + it.t * kT8Rows < it.M * G;
+      if (half == 1 && r < it.M) sm.parents[r] = parent;
+      if (ELEM == DKV_BF16) {
+        uint32_t am = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e++) am = amax2_finite(amax2_finite(amax2_finite(amax2_finite(am, qr[e].x), qr[e].y), qr[e].z), qr[e].w);
+        sm.qmax[half][r] = max(am & 0xffffu, am >> 16);
+      }
+      named_sync(1, 256);
+      // the queries as fp16 (bf16: over a power of two of their row)
+      float scale = 1.0f, inv = 1.0f;
+      if (ELEM == DKV_BF16) {
+        const int ex = max(-126, min(126, (int)(max(sm.qmax[0][r], sm.qmax[1][r]) >> 7) - 127));
+        inv = pow2(-ex);
+        scale = pow2(ex);
+      }
+      if (busy) {
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+          uint32_t q[16];
+#pragma unroll
+          for (int x = 0; x < 4; x++) {
+            q[4 * x] = qr[4 * e + x].x;
+            q[4 * x + 1] = qr[4 * e + x].y;
+            q[4 * x + 2] = qr[4 * e + x].z;
+            q[4 * x + 3] = qr[4 * e + x].w;
+          }
+          if (ELEM == DKV_BF16) {
+#pragma unroll
+            for (int x = 0; x < 16; x++) q[x] = half_of_bf16(q[x], inv);
+          }
+          tmem_st16(t_q + tl + 32 * half + 16 * e, q);
         }
-        if (ELEM == DKV_BF16) {
-          uint32_t am = 0;
-#pragma unroll
-          for (int e = 0; e < 64; e++) am = amax2_finite(am, q[e]);
-          const int ex = max(-126, min(126, (int)(max(am & 0xffffu, am >> 16) >> 7) - 127));
-          const float inv = pow2(-ex);
-          sm.qs[r] = pow2(ex);
-#pragma unroll
-          for (int e = 0; e < 64; e++) q[e] = half_of_bf16(q[e], inv);
-        }
-        tmem_st32(t_q + tl, q);
-        tmem_st32(t_q + tl + 32, q + 32);
         tmem_wait_st();
       }
       tc_fence_before();
-      named_sync(1, 256);
+      __syncwarp();
       if (lane == 0) mbar_arrive(ready);
-      if (fresh && real) node = node_of(c, a, a.parents ? sm.parents : nullptr, it.i, it.N, m);
-      const float scale = ELEM == DKV_BF16 && real ? sm.qs[r] : 1.0f;
+      if (real && (it.i != last_i || it.t != last_t)) node = node_of(c, a, a.parents ? sm.parents : nullptr, it.i, it.N, m);
+      last_i = it.i;
+      last_t = it.t;
       float mx = -INFINITY, u = -INFINITY, l = 0.0f;
-      int j = j0 + ((j0 & 1) != half), n = j >> 1;
+      int j = j0 + ((j0 & 1) != half), n = j >> 1, stage = j % kT8Stages;
       const int end = j0 + it.n;
-      bool first = true;
-      for (; ok && j < end; j += 2, n++) {
-        ok = wait(sfull(half), n);
-        if (!ok) break;
-        float s[64];
+      bool first = true, raise = true, have = false;
+      float s[64];
+      auto load_s = [&]() {
         tc_fence_after();
         if (busy) {
           tmem_ld32_nowait(t_s(half) + tl, s);
           tmem_ld32_nowait(t_s(half) + tl + 32, s + 32);
+        }
+      };
+      for (; ok && j < end; j += 2, n++) {
+        if (!have) {
+          ok = wait(sfull(half), n);
+          if (!ok) break;
+          load_s();
+        }
+        if (busy) {
           tmem_wait_ld();
           loaded32(s);
           loaded32(s + 32);
@@ -557,8 +681,8 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args
         if (lane == 0) mbar_arrive(sfree(half));
         uint32_t p[32];
         if (busy) {
-          const TileMeta* meta = sm.meta[j % kT8Stages];
-          float f[4], lv[4], ym[4];
+          const TileMeta* meta = sm.meta[stage];
+          float f[4], lv[4];
 #pragma unroll
           for (int b = 0; b < 4; b++) {
             const TileMeta d = meta[b];
@@ -574,58 +698,78 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args
 #pragma unroll
               for (int e = 0; e < 16; e++) s[16 * b + e] = see & (1u << e) ? s[16 * b + e] : -INFINITY;
             }
-            float y0 = s[16 * b], y1 = s[16 * b + 1];
-#pragma unroll
-            for (int e = 2; e < 16; e += 2) {
-              y0 = fmaxf(y0, s[16 * b + e]);
-              y1 = fmaxf(y1, s[16 * b + e + 1]);
-            }
-            ym[b] = fmaxf(y0, y1) * f[b];
           }
-          const float yt = fmaxf(fmaxf(ym[0], ym[1]), fmaxf(ym[2], ym[3]));
-          const float xt = fmaxf(fmaxf(ym[0] + lv[0], ym[1] + lv[1]), fmaxf(ym[2] + lv[2], ym[3] + lv[3]));
-          if (__any_sync(0xffffffffu, real && (xt > mx + kT8Lazy || yt > u + kT8LazySum))) {
-            const float nm = fmaxf(mx, xt), nu = fmaxf(u, yt);
-            l *= nu == -INFINITY ? 1.0f : fast_exp2(u - nu);
-            if (!first) {
-              ok = wait(pvdone(half), n - 1);
-              if (!ok) break;
-              tc_fence_after();
-              const float fo = nm == -INFINITY ? 1.0f : fast_exp2(mx - nm);
+          float sum;
 #pragma unroll 1
-              for (int q = 0; q < 8; q++) {
-                float o[16];
-                tmem_ld16_nowait(t_o(half) + tl + 16 * q, o);
-                tmem_wait_ld();
-                uint32_t w[16];
+          for (bool again = raise;; again = true) {
+            if (again) {
+              float ym[4];
 #pragma unroll
-                for (int e = 0; e < 16; e++) {
-                  asm volatile("" : "+f"(o[e]));
-                  w[e] = __float_as_uint(o[e] * fo);
+              for (int b = 0; b < 4; b++) {
+                float y0 = s[16 * b], y1 = s[16 * b + 1];
+#pragma unroll
+                for (int e = 2; e < 16; e += 2) {
+                  y0 = fmaxf(y0, s[16 * b + e]);
+                  y1 = fmaxf(y1, s[16 * b + e + 1]);
                 }
-                tmem_st16(t_o(half) + tl + 16 * q, w);
+                ym[b] = fmaxf(y0, y1) * f[b];
               }
-              tmem_wait_st();
-            }
-            mx = nm;
-            u = nu;
-          }
-          const float ur = u == -INFINITY ? 0.0f : u, mr = mx == -INFINITY ? 0.0f : mx;
-          float sum = 0.0f;
+              const float nu = fmaxf(u, fmaxf(fmaxf(ym[0], ym[1]), fmaxf(ym[2], ym[3])));
+              const float nm = fmaxf(mx, fmaxf(fmaxf(ym[0] + lv[0], ym[1] + lv[1]), fmaxf(ym[2] + lv[2], ym[3] + lv[3])));
+              l *= nu == -INFINITY ? 1.0f : fast_exp2(u - nu);
+              if (!first) {        // O is still once the last product is done
+                ok = wait(pvdone(half), n - 1);
+                if (!ok) break;
+                tc_fence_after();
+                const float fo = nm == -INFINITY ? 1.0f : fast_exp2(mx - nm);
+#pragma unroll 1
+                for (int q = 0; q < 8; q++) {
+                  float o[16];
+                  tmem_ld16_nowait(t_o(half) + tl + 16 * q, o);
+                  tmem_wait_ld();
+                  uint32_t w[16];
 #pragma unroll
-          for (int b = 0; b < 4; b++) {
-            const float g = fast_exp2(fminf(ur + lv[b] - mr + kT8Up, 127.0f));
-            float part = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-              const float p0 = fast_exp2(fmaf(s[16 * b + 2 * e], f[b], -ur)), p1 = fast_exp2(fmaf(s[16 * b + 2 * e + 1], f[b], -ur));
-              part += p0 + p1;
-              p[8 * b + e] = pack_half2(p0 * g, p1 * g);
+                  for (int e = 0; e < 16; e++) {
+                    asm volatile("" : "+f"(o[e]));
+                    w[e] = __float_as_uint(o[e] * fo);
+                  }
+                  tmem_st16(t_o(half) + tl + 16 * q, w);
+                }
+                tmem_wait_st();
+              }
+              mx = nm;
+              u = nu;
+              raise = __any_sync(0xffffffffu, real && u == -INFINITY);      // a row that has seen nothing so far
             }
-            sum += part;
+            const float ur = u == -INFINITY ? 0.0f : u, up = kT8Up + ur - (mx == -INFINITY ? 0.0f : mx);
+            float most = 0.0f;
+            sum = 0.0f;
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+              const float g = fast_exp2(fminf(up + lv[b], 127.0f));
+              const uint64_t f2 = f32x2(f[b], f[b]), u2 = f32x2(-ur, -ur), g2 = f32x2(g, g);
+              uint64_t part[2] = {0, 0};
+#pragma unroll
+              for (int e = 0; e < 8; e++) {
+                const uint64_t y = fma_f32x2(f32x2(s[16 * b + 2 * e], s[16 * b + 2 * e + 1]), f2, u2);
+                const uint64_t pr = f32x2(fast_exp2(__uint_as_float((uint32_t)y)), fast_exp2(__uint_as_float((uint32_t)(y >> 32))));
+                part[e & 1] = add_f32x2(part[e & 1], pr);
+                const uint64_t w = mul_f32x2(pr, g2);
+                p[8 * b + e] = pack_half2(__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32)));
+              }
+              part[0] = add_f32x2(part[0], part[1]);
+              const float tile = __uint_as_float((uint32_t)part[0]) + __uint_as_float((uint32_t)(part[0] >> 32));
+              sum += tile;
+              most = tile * g <= kT8Most ? most : INFINITY;
+            }
+            if (again || !__any_sync(0xffffffffu, real && most != 0.0f)) break;
           }
+          if (!ok) break;
           l += sum;
         }
+        // the next S, if it is there, comes while P goes
+        have = j + 2 < end && __all_sync(0xffffffffu, mbar_test(sfull(half), (n + 1) & 1));
+        if (have) load_s();
         // P of the step before is read, and its arrivals are complete (warps without rows
         // are here early)
         if (n > 0) ok = wait(pvdone(half), n - 1);
@@ -639,7 +783,14 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args
         __syncwarp();
         if (lane == 0) mbar_arrive(pfull(half));
         first = false;
+        stage += 2;
+        if (stage >= kT8Stages) stage -= kT8Stages;
       }
+      // the next item's queries, while the last product is awaited
+      pos += it.n;
+      j0 += it.n;
+      const TreeItem then = pos < hi ? tree_item(c, a, sm.plan, pos, hi) : it;
+      if (pos < hi && real_of(then)) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(q_of(then)));
       if (ok && !first) ok = wait(pvdone(half), n - 1);
       if (!ok) fail();
       sm.ex[half][r] = make_float4(mx, u, l, first ? 0.0f : 1.0f);
@@ -658,7 +809,8 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args
         const float f0 = factor(e0), f1 = factor(e1);
         const bool whole = it.n == it.per, two0 = e0.w != 0.0f, two1 = e1.w != 0.0f;
         uint8_t* out = a.out + (((long long)it.i * a.max_nodes + m) * c.hkv * G + (size_t)it.h * G + (row - m * G)) * (2 * kD) + 128 * half;
-        float* part = a.part + (size_t)(2 * blockIdx.x + (it.s0 > 0 ? 0 : 1)) * part_rows * (kD + 2);
+        // a part: [feature / 4][row][4], whose lanes' stores are neighbours, then (u, l) of the rows
+        float4* part = reinterpret_cast<float4*>(a.part + (size_t)(2 * blockIdx.x + (it.s0 > 0 ? 0 : 1)) * part_rows * (kD + 2));
 #pragma unroll 1
         for (int q = 0; q < 4; q++) {
           float o0[16], o1[16];
@@ -687,17 +839,19 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args
           } else if (real) {
 #pragma unroll
             for (int e = 0; e < 4; e++)
-              reinterpret_cast<float4*>(part + r * kD + 64 * half + 16 * q)[e] =
-                  make_float4(o0[4 * e], o0[4 * e + 1], o0[4 * e + 2], o0[4 * e + 3]);
+              part[(16 * half + 4 * q + e) * part_rows + r] = make_float4(o0[4 * e], o0[4 * e + 1], o0[4 * e + 2], o0[4 * e + 3]);
           }
         }
-        if (real && !whole && half == 0) reinterpret_cast<float2*>(part + part_rows * kD)[r] = make_float2(top, lsum);
+        if (real && !whole && half == 0) reinterpret_cast<float2*>(part + part_rows * (kD / 4))[r] = make_float2(top, lsum);
       }
       tc_fence_before();
-      pos += it.n;
-      j0 += it.n;
+      if (pos >= hi) break;
+      it = then;
+      load_row(it);
     }
-  } else if (warp < 8 + kT8Conv) {
+  } else {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kT8RegsFew));
+  if (warp < 8 + kT8Conv) {
     // ---- codes, tails and drafts to 16-bit operands: the tiles of the steps are dealt
     // out to the warps in turn ----
     const int cw = warp - 8;
@@ -707,63 +861,81 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args
     TileDesc* desc = sm.desc[cw];
     auto describe = [&](int batch) {       // tiles 32 batch ..: a lane each
       const int k = 32 * batch + lane;
-      if (k < steps) {
-        const int tile_of = cw + kT8Conv * k, pos = lo + tile_of / kT8Step;
-        const TreeItem it = tree_item(c, a, sm.plan, pos, pos + 1);
-        const int x = kT8Step * it.s0 + tile_of % kT8Step;
-        TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4};
-        if (x < it.tiles.stored) {
-          const int tile = it.tiles.tile(x);
-          d.pos0 = tile * kSub;
-          if (tile < it.tiles.full) {
-            const int per = c.T / kSub;
-            int page = c.table[(size_t)it.slot * c.width + tile / per];
-            if ((unsigned)page >= (unsigned)c.n_pages) {
-              c.latch(DKV_ERR_CHECK, it.i);
-              page = 0;
-            }
-            const float2 sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * c.hkv + it.h));
-            d.src = c.pages + c.page_head(page, it.h) + (size_t)(tile % per) * (2 * kTile);
-            d.ks = sc.x * kLogitScale;
-            d.lv = log2f(sc.y);
-            // every depth sees all of it
-            d.kind = a.window <= 0 || d.pos0 >= it.N + it.M - a.window || d.pos0 + kSub <= a.sinks ? 0 : 1;
-          } else {
-            d.src = c.tail + c.tail_head(it.slot, it.h) + (size_t)(tile - it.tiles.full) * (4 * kTile);
-            d.req_head = it.i << 12 | it.h;
-            d.kind = 2;
-          }
-        } else if (x < it.tiles.count) {
-          d.pos0 = (x - it.tiles.stored) * kSub;
-          d.req_head = it.i << 12 | it.h;
-          d.kind = 3;
-        }
-        desc[k & (kT8Descs - 1)] = d;
-      }
+      if (k < steps) describe_tile(c, a, sm.plan, lo, cw + kT8Conv * k, desc[k & (kT8Descs - 1)]);
       __syncwarp();
     };
-    auto fetch = [&](int k, uint4 (&w)[8]) {
-      if (k >= steps) return;
-      const TileDesc d = desc[k & (kT8Descs - 1)];
-      if (d.kind > 1) return;
-#pragma unroll
-      for (int e = 0; e < 8; e++) w[e] = ld_stream(d.src + 512 * e + 16 * lane);
+    // The next copy: codes of a tile, or K, then V of a 16-bit one.
+    uint8_t* ring = smem + kT8OffRing + cw * (kT8Ring * kT8Entry);
+    const uint32_t rbar = smem_u32(sm.rbar[cw]);
+    int at = 0, at_v = 0, ahead = 0, entry = 0, parity = 0, flying = 0;
+    auto issue = [&]() {
+      TileDesc d;
+      for (;; at++) {
+        if (at >= steps) return;
+        d = desc[at & (kT8Descs - 1)];
+        if (d.kind < 4) break;
+      }
+      const uint32_t dst = smem_u32(ring + ahead * kT8Entry), bar = rbar + 8 * ahead;
+      if (d.kind <= 2) {
+        if (lane == 0) {
+          mbar_expect_tx(bar, 2 * kTile);
+          bulk_g2s(dst, d.src + at_v * (2 * kTile), 2 * kTile, bar);
+        }
+      } else {
+        const int i = d.req_head >> 12, h = d.req_head & 4095, n = min(sm.plan.M[i] - d.pos0, kSub);
+        const long long row = (long long)i * a.max_nodes + d.pos0 + lane;
+        if (lane == 0) mbar_expect_tx(bar, n * (2 * kD));
+        __syncwarp();
+        if (lane < n)
+          bulk_g2s(dst + lane * kT8Pitch, (at_v ? a.v + row * a.vs : a.k + row * a.ks) + h * (2 * kD), 2 * kD, bar);
+      }
+      flying++;
+      ahead = ahead == kT8Ring - 1 ? 0 : ahead + 1;
+      at_v = d.kind >= 2 ? at_v ^ 1 : 0;
+      at += at_v ^ 1;
     };
-    auto put = [&](int k, const uint4 (&w)[8]) {
+    auto arrived = [&]() {               // the next copy
+      const uint8_t* p = ring + entry * kT8Entry;
+      ok = wait(rbar + 8 * entry, parity);
+      if (!ok) return p;
+      flying--;
+      if (++entry == kT8Ring) {
+        entry = 0;
+        parity ^= 1;
+      }
+      return p;
+    };
+    int described = 0;
+    if (steps > 0) {
+      describe(0);
+      for (int e = 0; e < kT8Ring; e++) issue();
+    }
+#pragma unroll 1
+    for (int k = 0; ok && k < steps; k++) {
+      // descriptors up to 32 tiles ahead
+      if (32 * (described + 1) < steps && k >= 32 * described + 4 * cw) describe(++described);
       const int tile_of = cw + kT8Conv * k, j = tile_of / kT8Step, sub = tile_of % kT8Step, stage = j % kT8Stages;
+      // (P V of step j - 8, the phase before, is done: this warp's last tile was of step
+      // j - 1 or j - 2, so P V of j - 5, whose S waited for it, or of j - 6 is)
       if (j >= kT8Stages) ok = wait(empty(stage), j / kT8Stages - 1);
-      if (!ok) return;
+      if (!ok) break;
       const uint32_t base = stage0 + stage * kT8Stage;
       // the lane's row of the four 8 x 8 matrices of a store: K, V, V of drafts
-      const uint32_t k_off = (2 * sub + ms) * 1024 + mrow * 128 + ((me ^ mrow) << 4);
-      const uint32_t v_off = 16384 + ms * 1024 + mrow * 128 + (((2 * sub + me) ^ mrow) << 4);
-      const uint32_t vt_off = 16384 + me * 1024 + mrow * 128 + (((2 * sub + ms) ^ mrow) << 4);
+      const uint32_t k_at = base + (2 * sub + ms) * 1024 + mrow * 128 + ((me ^ mrow) << 4);
+      const uint32_t v_at = base + 16384 + ms * 1024 + mrow * 128 + (((2 * sub + me) ^ mrow) << 4);
       const TileDesc d = desc[k & (kT8Descs - 1)];
-      TileMeta meta{d.ks, d.lv, d.pos0, d.kind > 2 ? d.kind - 1 : d.kind == 2 ? 1 : d.kind};
+      TileMeta meta{d.ks, d.lv, d.pos0, d.kind < 2 ? d.kind : d.kind - 1};
       if (d.kind <= 1) {
+        const uint8_t* p = arrived() + 16 * lane;
+        if (!ok) break;
+        uint4 w[8];
+#pragma unroll
+        for (int e = 0; e < 8; e++) w[e] = *reinterpret_cast<const uint4*>(p + 512 * e);
+        __syncwarp();
+        issue();
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-          const uint32_t at0 = e < 4 ? base + ((k_off + (e >> 1) * 8192) ^ ((e & 1) << 6)) : base + v_off + (e - 4) * 4096;
+          const uint32_t at0 = e < 4 ? (k_at + (e >> 1) * 8192) ^ ((e & 1) << 6) : v_at + (e - 4) * 4096;
           const uint32_t at1 = e < 4 ? at0 ^ 32u : at0 + 2048;
           uint32_t x[4];
           code_halves<CODE>(w[e].x, x[0], x[1]);
@@ -774,134 +946,119 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(Cache8View c, Tree8Args
           stmatrix4(at1, x[0], x[1], x[2], x[3]);
         }
       } else if (d.kind <= 3) {
-        const int i = d.req_head >> 12, h = d.req_head & 4095, g = lane >> 2, t = lane & 3;
-        const int n = min(d.kind == 2 ? sm.plan.N[i] - d.pos0 : sm.plan.M[i] - d.pos0, kSub);      // valid tokens
-        meta.lv = 0.0f;
-        uint32_t x[32];
-        const long long drow = (long long)i * a.max_nodes + d.pos0;
-#pragma unroll 1
-        for (int op = 0; op < 2; op++) {
-          if (d.kind == 2) {
-            // what lies behind the request's tokens becomes 0 (0 times what it may hold is not)
-            const bool v = op == 1;
-            const uint32_t lo_t = v ? (2 * t < n ? 0xffffu : 0u) | (2 * t + 1 < n ? 0xffff0000u : 0u) : g < n ? 0xffffffffu : 0u;
-            const uint32_t hi_t = v ? (2 * t + 8 < n ? 0xffffu : 0u) | (2 * t + 9 < n ? 0xffff0000u : 0u) : g + 8 < n ? 0xffffffffu : 0u;
-#pragma unroll
-            for (int f = 0; f < 8; f++) {
-              const uint4 y = *reinterpret_cast<const uint4*>(d.src + 2 * op * kTile + 512 * f + 16 * lane);
-              x[4 * f] = y.x & lo_t;
-              x[4 * f + 1] = y.y & (v ? hi_t : lo_t);
-              x[4 * f + 2] = y.z & (v ? lo_t : hi_t);
-              x[4 * f + 3] = y.w & hi_t;
-            }
-          } else {
-            const uint8_t* p = op == 0 ? a.k + drow * a.ks : a.v + drow * a.vs;
-            const long long stride = op == 0 ? a.ks : a.vs;
-#pragma unroll
-            for (int f = 0; f < 32; f++) {      // rows g, g + 8; features 16 m + 8 e + 2 t
-              const int row = g + 8 * (f >> 1 & 1);
-              x[f] = row < n ? *reinterpret_cast<const uint32_t*>(p + row * stride + h * (2 * kD) + 2 * (16 * (f >> 2) + 8 * (f & 1) + 2 * t))
-                             : 0u;
-            }
-          }
-          if (ELEM == DKV_BF16) {
-            uint32_t am = 0;
-#pragma unroll
-            for (int f = 0; f < 32; f++) am = amax2_finite(am, x[f]);
-            const int ex = scale_exp(am);
-            const float inv = pow2(-ex);
-#pragma unroll
-            for (int f = 0; f < 32; f++) x[f] = half_of_bf16(x[f], inv);
-            if (op == 0) meta.ks = kLogitScale * pow2(ex);
-            else meta.lv = (float)ex;
-          }
-#pragma unroll
-          for (int f = 0; f < 8; f++) {
-            if (op == 0)
-              stmatrix4(base + ((k_off + (f >> 2) * 8192) ^ ((f & 3) << 5)), x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
-            else if (d.kind == 2)
-              stmatrix4(base + v_off + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
-            else
-              stmatrix4_trans(base + vt_off + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
-          }
-        }
+        const int i = d.req_head >> 12, draft = d.kind == 3 ? 2 : 0;
+        const int n = min((draft ? sm.plan.M[i] : sm.plan.N[i]) - d.pos0, kSub);      // valid tokens
+        const uint8_t* p = arrived();
+        if (!ok) break;
+        meta.ks = kLogitScale * pow2(put_elems<ELEM>(p, draft, n, k_at));
+        __syncwarp();
+        issue();
+        p = arrived();
+        if (!ok) break;
+        const uint32_t vt_at = base + 16384 + me * 1024 + mrow * 128 + (((2 * sub + ms) ^ mrow) << 4);
+        meta.lv = (float)put_elems<ELEM>(p, draft + 1, n, draft ? vt_at : v_at);
+        __syncwarp();
+        issue();
       }
       if (lane == 0) sm.meta[stage][sub] = meta;
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(full(stage));
-    };
-    if (steps > 0) {
-      uint4 w0[8], w1[8];
-      describe(0);
-      fetch(0, w0);
-      fetch(1, w1);
-#pragma unroll 1
-      for (int k = 0; ok && k < steps; k += 2) {
-        if ((k & 31) == 0) describe((k >> 5) + 1);
-        put(k, w0);
-        fetch(k + 2, w0);
-        if (ok && k + 1 < steps) {
-          put(k + 1, w1);
-          fetch(k + 3, w1);
-        }
+    }
+    if (!ok) fail();
+    // no copy may be in flight at the exit
+    for (; flying > 0; flying--) {
+      wait_long(rbar + 8 * entry, parity);
+      if (++entry == kT8Ring) {
+        entry = 0;
+        parity ^= 1;
       }
-      if (!ok) fail();
     }
   } else {
     // ---- products: S of the steps to come, then O += P V; the whole warp walks, one
-    // lane issues ----
+    // lane issues (counters, so that operands stay in uniform registers) ----
     constexpr uint32_t id_s = umma_idesc_f16(128, 64), id_pv = umma_idesc_f16(128, 128);
     const uint64_t kd = umma_desc_sw128(smem_u32(smem)), vd = umma_desc_sw128(smem_u32(smem + 16384));
-    auto product_s = [&](int j) {
-      const int h = j & 1, n = j >> 1, stage = j % kT8Stages;
-      ok = wait(full(stage), j / kT8Stages) && (n == 0 || wait(sfree(h), n - 1));
-      if (!ok) return;
-      tc_fence_after();
-      if (lane == 0) {
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-          umma_f16_tmem_a(t_s(h), t_q + 8 * e, kd + ((stage * kT8Stage + (e >> 2) * 8192 + (e & 3) * 32) >> 4), id_s, e > 0);
-        umma_commit(sfull(h));
-      }
-      __syncwarp();
+    // Of each half: steps whose S, whose P V are issued, whose P V are done, and their
+    // stages. Whatever can be issued is, but S of step j waits for P V of step j - 3, so that
+    // stages are freed nearly in order (a converting warp waits for those of its tiles only).
+    int ns[2] = {0, 0}, nv[2] = {0, 0}, done[2] = {0, 0}, s_stage[2] = {0, 1}, s_round[2] = {0, 0}, v_stage[2] = {0, 1};
+    auto test = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0; };
+    auto next = [](int& stage) {          // two steps on; true behind the last stage
+      stage += 2;
+      if (stage < kT8Stages) return false;
+      stage -= kT8Stages;
+      return true;
     };
-    auto product_v = [&](int j, int tiles, bool start) {
-      const int h = j & 1, n = j >> 1, stage = j % kT8Stages;
-      ok = wait(pfull(h), n);
-      if (!ok) return;
-      tc_fence_after();
-      if (lane == 0) {
-#pragma unroll
-        for (int e = 0; e < kT8Step; e++)
-          if (e < tiles)
-            umma_f16_tmem_a(t_o(h), t_p(h) + 8 * e, vd + ((stage * kT8Stage + e * 32) >> 4), id_pv, !start || e > 0);
-        umma_commit(pvdone(h));
-        umma_commit(empty(stage));
-      }
-      __syncwarp();
-    };
-    int item = 0;
-    for (int pos = lo, j0 = 0; ok && pos < hi; item++) {
+    int item = 0, j0 = 0;
+    for (int pos = lo; ok && pos < hi; item++) {
       const TreeItem it = tree_item(c, a, sm.plan, pos, hi);
+      const int n = __shfl_sync(0xffffffffu, it.n, 0);
+      // tiles of the part's last step
+      const int rest = __shfl_sync(0xffffffffu, min(kT8Step, it.tiles.count - kT8Step * (it.s0 + it.n - 1)), 0);
+      const int begin[2] = {(j0 + 1) >> 1, j0 >> 1};
+      j0 += n;
+      pos += n;
+      const int end[2] = {(j0 + 1) >> 1, j0 >> 1};
       ok = wait(ready, item);
       if (!ok) break;
       tc_fence_after();
-      product_s(j0);
-      if (ok && it.n > 1) product_s(j0 + 1);
-      for (int x = 0; ok && x < it.n; x++) {
-        if (x + 2 < it.n) product_s(j0 + x + 2);
-        if (ok) product_v(j0 + x, min(kT8Step, it.tiles.count - kT8Step * (it.s0 + x)), x < 2);
+      long long since = 0;
+      int idle = 0;
+#pragma unroll 1
+      while (nv[0] < end[0] || nv[1] < end[1]) {
+        bool none = true;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          if (done[h] < nv[h] && test(pvdone(h), nv[h] - 1)) done[h] = nv[h];
+          if (ns[h] < end[h] && done[h ^ 1] >= ns[h] - 1 + h && test(full(s_stage[h]), s_round[h]) && (ns[h] == 0 || test(sfree(h), ns[h] - 1))) {
+            tc_fence_after();
+            if (elected()) {
+              const uint64_t bd = kd + s_stage[h] * (kT8Stage >> 4);
+#pragma unroll
+              for (int e = 0; e < 8; e++)
+                umma_f16_tmem_a(t_s(h), t_q + 8 * e, bd + (((e >> 2) * 8192 + (e & 3) * 32) >> 4), id_s, e > 0);
+              umma_commit(sfull(h));
+            }
+            __syncwarp();
+            ns[h]++;
+            if (next(s_stage[h])) s_round[h] ^= 1;
+            none = false;
+          }
+          if (nv[h] < ns[h] && test(pfull(h), nv[h])) {
+            tc_fence_after();
+            const bool start = nv[h] == begin[h];
+            const int tiles = 2 * nv[h] + h == j0 - 1 ? rest : kT8Step;
+            if (elected()) {
+              const uint64_t bd = vd + v_stage[h] * (kT8Stage >> 4);
+#pragma unroll
+              for (int e = 0; e < kT8Step; e++)
+                if (e < tiles) umma_f16_tmem_a(t_o(h), t_p(h) + 8 * e, bd + (e * 32 >> 4), id_pv, !start || e > 0);
+              umma_commit(pvdone(h));
+              umma_commit(empty(v_stage[h]));
+            }
+            __syncwarp();
+            done[h] = nv[h]++;       // P came after the step before was done
+            next(v_stage[h]);
+            none = false;
+          }
+        }
+        // bounded: about a second without anything to issue
+        if (!none) idle = 0;
+        else if (++idle == 1) since = clock64();
+        else if ((idle & 1023) == 0 && __any_sync(0xffffffffu, *(volatile int*)&sm.fail != 0 || clock64() - since > 2000000000LL)) {
+          ok = false;
+          break;
+        }
       }
-      pos += it.n;
-      j0 += it.n;
     }
     if (!ok) fail();
-    if (lane == 0) {
+    if (elected()) {
       umma_commit(drain);                // every MMA issued so far has completed
       mbar_wait_bounded(drain, 0);
     }
     __syncwarp();
+  }
   }
   tc_fence_before();
   __syncthreads();
@@ -966,7 +1123,7 @@ __global__ void __launch_bounds__(32 * kT8Walkers) k_tree8_join(Cache8View c, Tr
         const int n = min(c1 - b + 1, 32);
 #pragma unroll 4
         for (int e = 0; e < n; e++) {
-          const float4 v = reinterpret_cast<const float4*>(part(b + e) + r * kD)[lane];
+          const float4 v = reinterpret_cast<const float4*>(part(b + e))[lane * part_rows + r];
           const float fe = __shfl_sync(0xffffffffu, f, e);
           o.x = fmaf(v.x, fe, o.x);
           o.y = fmaf(v.y, fe, o.y);
