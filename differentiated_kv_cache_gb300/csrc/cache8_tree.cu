@@ -11,20 +11,20 @@ namespace {
 
 constexpr int kT8Rows = 128;        // query rows of a unit: (node, head of the group), nodes first
 constexpr int kT8Walkers = 8;       // warps of a block of the second kernel
-constexpr int kT8Step = 4;          // tiles of a step
-constexpr int kT8Least = 2;         // steps that make a CTA worth its start
+constexpr int kT8Step = 8;          // tiles of a step, in two parts of four
+constexpr int kT8Least = 1;         // steps that make a CTA worth its start
 constexpr int kT8Conv = 7;          // warps that convert
 constexpr int kT8Threads = 32 * (8 + kT8Conv + 1);
-// registers a thread: launched with 128; 256 x 168 + 256 x 88 = 512 x 128
-constexpr int kT8RegsFew = 88, kT8RegsMany = 168;
-constexpr int kT8Stages = 4;        // even: a stage is of one half, which has seen its phases
-constexpr int kT8Stage = 32768;     // K, then V of a step in 16 bits
+// registers a thread: launched with 128; 256 x 184 + 256 x 72 = 512 x 128
+constexpr int kT8RegsFew = 72, kT8RegsMany = 184;
+constexpr int kT8Slots = 4;         // parts whose K (V) is kept as operands
+constexpr int kT8Slot = 16384;      // K or V of a part in 16 bits
 constexpr int kT8Descs = 64;        // descriptors of a converting warp, a ring
-constexpr int kT8Ring = 2;          // copies that it has on their way
-constexpr int kT8Pitch = 272;       // bytes from draft row to draft row (no bank conflicts)
-constexpr int kT8Entry = 16 * kT8Pitch;     // K and V codes of a tile, or K or V of a 16-bit one
+constexpr int kT8Ring = 4;          // copies that it has on their way
+constexpr int kT8Entry = kTile;     // K or V codes of a tile
 constexpr float kT8Up = 7.0f;       // log2 of a weight at its row's maximum
 constexpr float kT8Most = 32768.0f; // largest sum of a row's weights of one tile (fp16 holds 65504)
+constexpr float kT8Far = 60.0f;     // log2 of how far weights may be from probabilities
 
 // A request of the call: N tokens stored, M drafts (0: padding).
 struct TreeReq {
@@ -391,18 +391,20 @@ struct TileMeta {
 
 struct TreeSmem {
   TileDesc desc[kT8Conv][kT8Descs];
-  TileMeta meta[kT8Stages][kT8Step];
-  float4 ex[2][kT8Rows];       // m, u, l of the halves
+  TileMeta meta[2 * kT8Slots][4];      // K of a part comes before the softmax has read that of part x - 4, not of x - 8
   TreePlan plan;
   int parents[kMaxNodes];
-  uint32_t qmax[2][kT8Rows];   // bits of the largest |q| of the features that a half's warps load
+  float2 pair[2][2][kT8Rows];      // what the two warps of a row tell each other
   int scan[32];
-  uint64_t bar[2 * kT8Stages + 10];
+  // K, V of a part there, no longer needed; S, P, P V of a step there, queries there (two of
+  // each); drain
+  uint64_t bar[4 * kT8Slots + 9];
   uint64_t rbar[kT8Conv][kT8Ring];
   uint32_t taddr;
   int fail;
 };
-constexpr int kT8OffRing = kT8Stages * kT8Stage, kT8OffSmem = kT8OffRing + kT8Conv * kT8Ring * kT8Entry;
+constexpr int kT8OffV = kT8Slots * kT8Slot, kT8OffRing = 2 * kT8Slots * kT8Slot;
+constexpr int kT8OffSmem = kT8OffRing + kT8Conv * kT8Ring * kT8Entry;
 constexpr int kT8Smem = 1024 + kT8OffSmem + (int)sizeof(TreeSmem);
 
 __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -474,17 +476,12 @@ __device__ __forceinline__ void describe_tile(const Cache8View& c, const Tree8Ar
   out = d;
 }
 
-// K (op 0) or V of a tile of the tail (op + 0) or of drafts (op + 2), n tokens of it valid,
-// from its copy `src` in shared memory to fp16 operands (`at`: the lane's row of the first
-// four matrices). Returns the exponent of the power of two that the values were divided by.
-template <int ELEM>
-__device__ __noinline__ int put_elems(const uint8_t* src, int op, int n, uint32_t at) {
+// A lane's words of K or V (op 0, 1) of a tile of the tail (draft 0) or of drafts (rows of
+// `stride` bytes from src), of which n tokens are valid. What lies behind those becomes 0 (0
+// times what it may hold is not). Words 4 m + (0 .. 3): the 8 x 8 matrices of m-step m.
+__device__ __forceinline__ void load_elems(const uint8_t* src, bool v, bool draft, int n, long long stride, uint32_t (&x)[32]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const bool v = op & 1, draft = op & 2;
-  uint32_t x[32];
-  int ex = 0;
   if (!draft) {
-    // what lies behind the request's tokens becomes 0 (0 times what it may hold is not)
     const uint32_t lo_t = v ? (2 * t < n ? 0xffffu : 0u) | (2 * t + 1 < n ? 0xffff0000u : 0u) : g < n ? 0xffffffffu : 0u;
     const uint32_t hi_t = v ? (2 * t + 8 < n ? 0xffffu : 0u) | (2 * t + 9 < n ? 0xffff0000u : 0u) : g + 8 < n ? 0xffffffffu : 0u;
 #pragma unroll
@@ -496,18 +493,29 @@ __device__ __noinline__ int put_elems(const uint8_t* src, int op, int n, uint32_
       x[4 * f + 3] = y.w & hi_t;
     }
   } else {
+    // rows g, g + 8; features 16 m + 8 e + 2 t
+    const uint8_t *p0 = src + g * stride + 4 * t, *p1 = p0 + 8 * stride;
 #pragma unroll
-    for (int f = 0; f < 32; f++) {      // rows g, g + 8; features 16 m + 8 e + 2 t
-      const int row = g + 8 * (f >> 1 & 1);
-      const uint32_t y = *reinterpret_cast<const uint32_t*>(src + row * kT8Pitch + 2 * (16 * (f >> 2) + 8 * (f & 1) + 2 * t));
-      x[f] = row < n ? y : 0u;
+    for (int f = 0; f < 32; f++) {
+      const int off = 32 * (f >> 2) + 16 * (f & 1);
+      x[f] = (f & 2 ? g + 8 : g) < n ? *reinterpret_cast<const uint32_t*>((f & 2 ? p1 : p0) + off) : 0u;
     }
   }
-  if (ELEM == DKV_BF16) {
-    uint32_t am = 0;
+}
+// The exponent of the power of two that bf16 values are divided by.
+__device__ __noinline__ int elems_exp(const uint8_t* src, bool v, bool draft, int n, long long stride) {
+  uint32_t x[32], am = 0;
+  load_elems(src, v, draft, n, stride, x);
 #pragma unroll
-    for (int f = 0; f < 32; f++) am = amax2_finite(am, x[f]);
-    ex = scale_exp(am);
+  for (int f = 0; f < 32; f++) am = amax2_finite(am, x[f]);
+  return scale_exp(am);
+}
+// ... as fp16 operands; at: the lane's row of the first four matrices.
+template <int ELEM>
+__device__ __noinline__ void put_elems(const uint8_t* src, bool v, bool draft, int n, long long stride, int ex, uint32_t at) {
+  uint32_t x[32];
+  load_elems(src, v, draft, n, stride, x);
+  if (ELEM == DKV_BF16) {
     const float inv = pow2(-ex);
 #pragma unroll
     for (int f = 0; f < 32; f++) x[f] = half_of_bf16(x[f], inv);
@@ -521,7 +529,6 @@ __device__ __noinline__ int put_elems(const uint8_t* src, int op, int n, uint32_
     else
       stmatrix4_trans(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
   }
-  return ex;
 }
 
 template <int ELEM, int CODE>
@@ -531,27 +538,30 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TreeSmem& sm = *reinterpret_cast<TreeSmem*>(smem + kT8OffSmem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, G = c.G;
-  // step j of the CTA: half j & 1, its step j >> 1, stage j % kT8Stages
+  // part x = 2 j + (0, 1) of step j of the CTA: slot x & 3; S and P of step j: place j & 1
   const uint32_t b0 = smem_u32(sm.bar);
-  auto full = [&](int s) { return b0 + 8u * s; };
-  auto empty = [&](int s) { return b0 + 8u * (kT8Stages + s); };
-  auto sfull = [&](int h) { return b0 + 8u * (2 * kT8Stages + h); };
-  auto sfree = [&](int h) { return b0 + 8u * (2 * kT8Stages + 2 + h); };
-  auto pfull = [&](int h) { return b0 + 8u * (2 * kT8Stages + 4 + h); };
-  auto pvdone = [&](int h) { return b0 + 8u * (2 * kT8Stages + 6 + h); };
-  const uint32_t ready = b0 + 8u * (2 * kT8Stages + 8), drain = ready + 8u;
+  auto kfull = [&](int s) { return b0 + 8u * s; };
+  auto kfree = [&](int s) { return b0 + 8u * (kT8Slots + s); };
+  auto vfull = [&](int s) { return b0 + 8u * (2 * kT8Slots + s); };
+  auto vfree = [&](int s) { return b0 + 8u * (3 * kT8Slots + s); };
+  auto sfull = [&](int s) { return b0 + 8u * (4 * kT8Slots + s); };
+  auto pfull = [&](int s) { return b0 + 8u * (4 * kT8Slots + 2 + s); };
+  auto qfull = [&](int s) { return b0 + 8u * (4 * kT8Slots + 4 + s); };
+  auto pvdone = [&](int s) { return b0 + 8u * (4 * kT8Slots + 6 + s); };
+  const uint32_t drain = b0 + 8u * (4 * kT8Slots + 8);
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kT8Stages; s++) {
-      mbar_init(full(s), kT8Step);
-      mbar_init(empty(s), 1);
+    for (int s = 0; s < kT8Slots; s++) {
+      mbar_init(kfull(s), 4);
+      mbar_init(kfree(s), 1);
+      mbar_init(vfull(s), 4);
+      mbar_init(vfree(s), 1);
     }
-    for (int h = 0; h < 2; h++) {
-      mbar_init(sfull(h), 1);
-      mbar_init(sfree(h), 4);
-      mbar_init(pfull(h), 4);
-      mbar_init(pvdone(h), 1);
+    for (int s = 0; s < 2; s++) {
+      mbar_init(sfull(s), 1);
+      mbar_init(pfull(s), 8);
+      mbar_init(qfull(s), 8);
+      mbar_init(pvdone(s), 1);
     }
-    mbar_init(ready, 8);
     mbar_init(drain, 1);
     for (int w = 0; w < kT8Conv * kT8Ring; w++) mbar_init(smem_u32(&sm.rbar[0][0]) + 8 * w, 1);
     sm.fail = 0;
@@ -572,138 +582,153 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   }
   const int lo = range_start(total, blockIdx.x, ctas), hi = range_start(total, blockIdx.x + 1, ctas);
   const uint32_t tbase = __shfl_sync(0xffffffffu, sm.taddr, 0);
-  // O of the halves, S of the halves, P of the halves, Q
-  auto t_o = [&](int h) { return tbase + 128u * h; };
-  auto t_s = [&](int h) { return tbase + 256u + 64u * h; };
-  auto t_p = [&](int h) { return tbase + 384u + 32u * h; };
-  const uint32_t t_q = tbase + 448u;
+  // O, two S (and P over them), two Q
+  const uint32_t t_o = tbase;
+  auto t_s = [&](int s) { return tbase + 128u + 128u * s; };
+  auto t_q = [&](int s) { return tbase + 384u + 64u * s; };
   auto fail = [&]() {
     c.latch(DKV_ERR_TIMEOUT, -1);
     *(volatile int*)&sm.fail = 1;
   };
   auto wait = [&](uint32_t bar, int phase) {       // the same for every lane
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1))) return true;
-    return __all_sync(0xffffffffu, *(volatile int*)&sm.fail == 0 && wait_long(bar, phase & 1)) != 0;
+    const bool there = __all_sync(0xffffffffu, *(volatile int*)&sm.fail == 0 && wait_long(bar, phase & 1)) != 0;
+    if (!there) fail();
+    return there;
   };
   bool ok = true;
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kT8RegsMany));
-    // ---- softmax: a thread per query row, a half takes every other step ----
-    const int half = warp >> 2, lg = warp & 3, r = 32 * lg + lane;
+    // ---- softmax: a thread per query row and part of a step, so two warps for 32 rows,
+    // which agree on the rows' maxima ----
+    const int part = warp >> 2, lg = warp & 3, r = 32 * lg + lane, pair_bar = 4 + lg;
     const uint32_t tl = (uint32_t)(32 * lg) << 16;
     Node node;
     TreeItem it = tree_item(c, a, sm.plan, lo, hi);
-    int last_i = -1, last_t = -1, parent = 0;
-    uint4 qr[8];              // 64 features of the row, the other half's warps have the others
+    int told = 0;              // place of `pair` to use next
     auto row_of = [&](const TreeItem& x) { return x.t * kT8Rows + r; };
     auto real_of = [&](const TreeItem& x) { return row_of(x) < x.M * G; };
-    auto q_of = [&](const TreeItem& x) {
+    auto busy_of = [&](const TreeItem& x) { return 32 * lg + x.t * kT8Rows < x.M * G; };
+    auto q_of = [&](const TreeItem& x) {         // 64 features of the row; the other warp has the others
       const int row = row_of(x), m = row / G;
-      return a.q + ((long long)x.i * a.max_nodes + m) * a.qs + ((size_t)x.h * G + (row - m * G)) * (2 * kD) + 128 * half;
+      return a.q + ((long long)x.i * a.max_nodes + m) * a.qs + ((size_t)x.h * G + (row - m * G)) * (2 * kD) + 128 * part;
     };
-    auto load_row = [&](const TreeItem& x) {
-      const uint4* src = reinterpret_cast<const uint4*>(q_of(x));
-      const bool real = real_of(x);
+    // The queries of item n (bf16: over a power of two of their row, which is returned).
+    auto put_row = [&](const TreeItem& x, int n) {
+      float scale = 1.0f;
+      if (busy_of(x)) {
+        const uint4* src = reinterpret_cast<const uint4*>(q_of(x));
+        const bool real = real_of(x);
+        uint4 qr[8];
 #pragma unroll
-      for (int e = 0; e < 8; e++) qr[e] = real ? src[e] : make_uint4(0, 0, 0, 0);
-      if (half == 1 && a.parents && r < x.M) parent = a.parents[(size_t)x.i * a.max_nodes + r];
-    };
-    load_row(it);
-    for (int pos = lo, j0 = 0;;) {
-      const int row = row_of(it), m = row / G;
-      const bool real = real_of(it), busy = 32 * lg + it.t * kT8Rows < it.M * G;
-      if (half == 1 && r < it.M) sm.parents[r] = parent;
-      if (ELEM == DKV_BF16) {
-        uint32_t am = 0;
+        for (int e = 0; e < 8; e++) qr[e] = real ? src[e] : make_uint4(0, 0, 0, 0);
+        float inv = 1.0f;
+        if (ELEM == DKV_BF16) {
+          uint32_t am = 0;
 #pragma unroll
-        for (int e = 0; e < 8; e++) am = amax2_finite(amax2_finite(amax2_finite(amax2_finite(am, qr[e].x), qr[e].y), qr[e].z), qr[e].w);
-        sm.qmax[half][r] = max(am & 0xffffu, am >> 16);
-      }
-      named_sync(1, 256);
-      // the queries as fp16 (bf16: over a power of two of their row)
-      float scale = 1.0f, inv = 1.0f;
-      if (ELEM == DKV_BF16) {
-        const int ex = max(-126, min(126, (int)(max(sm.qmax[0][r], sm.qmax[1][r]) >> 7) - 127));
-        inv = pow2(-ex);
-        scale = pow2(ex);
-      }
-      if (busy) {
+          for (int e = 0; e < 8; e++)
+            am = amax2_finite(amax2_finite(amax2_finite(amax2_finite(am, qr[e].x), qr[e].y), qr[e].z), qr[e].w);
+          const float mine = __uint_as_float(max(am & 0xffffu, am >> 16));
+          sm.pair[told][part][r].x = mine;
+          named_sync(pair_bar, 64);
+          const uint32_t most = max(__float_as_uint(mine), __float_as_uint(sm.pair[told][part ^ 1][r].x));
+          told ^= 1;
+          const int ex = max(-126, min(126, (int)(most >> 7) - 127));
+          inv = pow2(-ex);
+          scale = pow2(ex);
+        }
 #pragma unroll
         for (int e = 0; e < 2; e++) {
           uint32_t q[16];
 #pragma unroll
-          for (int x = 0; x < 4; x++) {
-            q[4 * x] = qr[4 * e + x].x;
-            q[4 * x + 1] = qr[4 * e + x].y;
-            q[4 * x + 2] = qr[4 * e + x].z;
-            q[4 * x + 3] = qr[4 * e + x].w;
+          for (int y = 0; y < 4; y++) {
+            q[4 * y] = qr[4 * e + y].x;
+            q[4 * y + 1] = qr[4 * e + y].y;
+            q[4 * y + 2] = qr[4 * e + y].z;
+            q[4 * y + 3] = qr[4 * e + y].w;
           }
           if (ELEM == DKV_BF16) {
 #pragma unroll
-            for (int x = 0; x < 16; x++) q[x] = half_of_bf16(q[x], inv);
+            for (int y = 0; y < 16; y++) q[y] = half_of_bf16(q[y], inv);
           }
-          tmem_st16(t_q + tl + 32 * half + 16 * e, q);
+          tmem_st16(t_q(n & 1) + tl + 32 * part + 16 * e, q);
         }
         tmem_wait_st();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ready);
-      if (real && (it.i != last_i || it.t != last_t)) node = node_of(c, a, a.parents ? sm.parents : nullptr, it.i, it.N, m);
-      last_i = it.i;
-      last_t = it.t;
+      if (lane == 0) mbar_arrive(qfull(n & 1));
+      return scale;
+    };
+    float scale = put_row(it, 0);
+    int last_i = -1, last_t = -1;
+    for (int pos = lo, j = 0, item = 0;; item++) {
+      const int row = row_of(it), m = row / G;
+      const bool real = real_of(it), busy = busy_of(it);
+      if (it.i != last_i || it.t != last_t) {      // the same for all eight warps
+        if (a.parents && it.i != last_i) {
+          named_sync(1, 256);
+          if (part == 1 && r < it.M) sm.parents[r] = a.parents[(size_t)it.i * a.max_nodes + r];
+          named_sync(1, 256);
+        }
+        if (real) node = node_of(c, a, a.parents ? sm.parents : nullptr, it.i, it.N, m);
+        last_i = it.i;
+        last_t = it.t;
+      }
+      pos += it.n;
+      TreeItem then = it;
+      if (pos < hi) {
+        then = tree_item(c, a, sm.plan, pos, hi);
+        if (real_of(then)) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(q_of(then)));
+      }
       float mx = -INFINITY, u = -INFINITY, l = 0.0f;
-      int j = j0 + ((j0 & 1) != half), n = j >> 1, stage = j % kT8Stages;
-      const int end = j0 + it.n;
-      bool first = true, raise = true, have = false;
-      float s[64];
-      auto load_s = [&]() {
+      const int end = j + it.n;
+      bool first = true, raise = true;
+      for (; j < end; j++) {
+        // (after a wait that gave up the warps walk on, through the same barriers)
+        ok = wait(sfull(j & 1), j >> 1) && ok;
+        if (j > 1) ok = wait(pvdone(j & 1), (j >> 1) - 1) && ok;      // long since: its phases are seen in turn
         tc_fence_after();
         if (busy) {
-          tmem_ld32_nowait(t_s(half) + tl, s);
-          tmem_ld32_nowait(t_s(half) + tl + 32, s + 32);
-        }
-      };
-      for (; ok && j < end; j += 2, n++) {
-        if (!have) {
-          ok = wait(sfull(half), n);
-          if (!ok) break;
-          load_s();
-        }
-        if (busy) {
-          tmem_wait_ld();
-          loaded32(s);
-          loaded32(s + 32);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sfree(half));
-        uint32_t p[32];
-        if (busy) {
-          const TileMeta* meta = sm.meta[stage];
+          float s[64];
+          const uint32_t ts = t_s(j & 1) + tl + 64 * part;
+          tmem_ld32_nowait(ts, s);
+          tmem_ld32_nowait(ts + 32, s + 32);
+          const TileMeta* meta = sm.meta[(2 * j + part) & (2 * kT8Slots - 1)];
           float f[4], lv[4];
+          int kind[4], pos0[4];
 #pragma unroll
           for (int b = 0; b < 4; b++) {
             const TileMeta d = meta[b];
             f[b] = d.ks * scale;
             lv[b] = d.lv;
-            if (d.kind != 0) {
-              uint32_t see = 0;
-              if (real && d.kind == 1) see = sees_stored(a, it.N, node.depth, d.pos0);
-              if (real && d.kind == 2) {
-                const int w = d.pos0 >> 5;
-                see = (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (d.pos0 & 31);
+            kind[b] = d.kind;
+            pos0[b] = d.pos0;
+          }
+          tmem_wait_ld();
+          loaded32(s);
+          loaded32(s + 32);
+          if (kind[0] | kind[1] | kind[2] | kind[3]) {
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+              uint32_t see = kind[b] == 0 ? 0xffffu : 0u;
+              if (real && kind[b] == 1) see = sees_stored(a, it.N, node.depth, pos0[b]);
+              if (real && kind[b] == 2) {
+                const int w = pos0[b] >> 5;
+                see = (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (pos0[b] & 31);
               }
 #pragma unroll
               for (int e = 0; e < 16; e++) s[16 * b + e] = see & (1u << e) ? s[16 * b + e] : -INFINITY;
             }
           }
+          uint32_t p[32];
           float sum;
 #pragma unroll 1
           for (bool again = raise;; again = true) {
             if (again) {
-              float ym[4];
+              // the rows' maxima over both parts
+              float yt = -INFINITY, xt = -INFINITY;
 #pragma unroll
               for (int b = 0; b < 4; b++) {
                 float y0 = s[16 * b], y1 = s[16 * b + 1];
@@ -712,20 +737,24 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
                   y0 = fmaxf(y0, s[16 * b + e]);
                   y1 = fmaxf(y1, s[16 * b + e + 1]);
                 }
-                ym[b] = fmaxf(y0, y1) * f[b];
+                y0 = fmaxf(y0, y1) * f[b];
+                yt = fmaxf(yt, y0);
+                xt = fmaxf(xt, y0 + lv[b]);
               }
-              const float nu = fmaxf(u, fmaxf(fmaxf(ym[0], ym[1]), fmaxf(ym[2], ym[3])));
-              const float nm = fmaxf(mx, fmaxf(fmaxf(ym[0] + lv[0], ym[1] + lv[1]), fmaxf(ym[2] + lv[2], ym[3] + lv[3])));
+              sm.pair[told][part][r] = make_float2(yt, xt);
+              named_sync(pair_bar, 64);
+              const float2 other = sm.pair[told][part ^ 1][r];
+              told ^= 1;
+              const float nu = fmaxf(u, fmaxf(yt, other.x)), nm = fmaxf(mx, fmaxf(xt, other.y));
               l *= nu == -INFINITY ? 1.0f : fast_exp2(u - nu);
               if (!first) {        // O is still once the last product is done
-                ok = wait(pvdone(half), n - 1);
-                if (!ok) break;
+                ok = wait(pvdone((j - 1) & 1), (j - 1) >> 1) && ok;
                 tc_fence_after();
                 const float fo = nm == -INFINITY ? 1.0f : fast_exp2(mx - nm);
 #pragma unroll 1
-                for (int q = 0; q < 8; q++) {
+                for (int q = 0; q < 4; q++) {
                   float o[16];
-                  tmem_ld16_nowait(t_o(half) + tl + 16 * q, o);
+                  tmem_ld16_nowait(t_o + tl + 64 * part + 16 * q, o);
                   tmem_wait_ld();
                   uint32_t w[16];
 #pragma unroll
@@ -733,313 +762,313 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
                     asm volatile("" : "+f"(o[e]));
                     w[e] = __float_as_uint(o[e] * fo);
                   }
-                  tmem_st16(t_o(half) + tl + 16 * q, w);
+                  tmem_st16(t_o + tl + 64 * part + 16 * q, w);
                 }
-                tmem_wait_st();
               }
               mx = nm;
               u = nu;
               raise = __any_sync(0xffffffffu, real && u == -INFINITY);      // a row that has seen nothing so far
             }
-            const float ur = u == -INFINITY ? 0.0f : u, up = kT8Up + ur - (mx == -INFINITY ? 0.0f : mx);
-            float most = 0.0f;
+            // weights 2^(x - m + kT8Up), to be rounded to fp16; their sum of a tile over
+            // 2^(kT8Up + u - m) s_v is that of the probabilities under u, except where these
+            // are so far apart that one of them may vanish
+            const float ur = u == -INFINITY ? 0.0f : u, mr = kT8Up - (mx == -INFINITY ? 0.0f : mx);
+            bool fits = true, far = false;
             sum = 0.0f;
 #pragma unroll
             for (int b = 0; b < 4; b++) {
-              const float g = fast_exp2(fminf(up + lv[b], 127.0f));
-              const uint64_t f2 = f32x2(f[b], f[b]), u2 = f32x2(-ur, -ur), g2 = f32x2(g, g);
-              uint64_t part[2] = {0, 0};
+              const float up = lv[b] + mr;
+              const uint64_t f2 = f32x2(f[b], f[b]), up2 = f32x2(up, up);
+              uint64_t acc[2] = {0, 0};
 #pragma unroll
               for (int e = 0; e < 8; e++) {
-                const uint64_t y = fma_f32x2(f32x2(s[16 * b + 2 * e], s[16 * b + 2 * e + 1]), f2, u2);
-                const uint64_t pr = f32x2(fast_exp2(__uint_as_float((uint32_t)y)), fast_exp2(__uint_as_float((uint32_t)(y >> 32))));
-                part[e & 1] = add_f32x2(part[e & 1], pr);
-                const uint64_t w = mul_f32x2(pr, g2);
-                p[8 * b + e] = pack_half2(__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32)));
+                const uint64_t y = fma_f32x2(f32x2(s[16 * b + 2 * e], s[16 * b + 2 * e + 1]), f2, up2);
+                const float w0 = fast_exp2(__uint_as_float((uint32_t)y)), w1 = fast_exp2(__uint_as_float((uint32_t)(y >> 32)));
+                acc[e & 1] = add_f32x2(acc[e & 1], f32x2(w0, w1));
+                p[8 * b + e] = pack_half2(w0, w1);
               }
-              part[0] = add_f32x2(part[0], part[1]);
-              const float tile = __uint_as_float((uint32_t)part[0]) + __uint_as_float((uint32_t)(part[0] >> 32));
-              sum += tile;
-              most = tile * g <= kT8Most ? most : INFINITY;
+              acc[0] = add_f32x2(acc[0], acc[1]);
+              const float tile = __uint_as_float((uint32_t)acc[0]) + __uint_as_float((uint32_t)(acc[0] >> 32));
+              const float back = up + ur;
+              sum = fmaf(tile, fast_exp2(-back), sum);
+              fits = fits && tile <= kT8Most;
+              far = far || !(fabsf(back) <= kT8Far);
             }
-            if (again || !__any_sync(0xffffffffu, real && most != 0.0f)) break;
+            if (__any_sync(0xffffffffu, real && far)) {
+              sum = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 64; e++) sum += fast_exp2(fmaf(s[e], f[e >> 4], -ur));
+            }
+            if (again || named_all(pair_bar, 64, fits || !real)) break;
           }
-          if (!ok) break;
           l += sum;
-        }
-        // the next S, if it is there, comes while P goes
-        have = j + 2 < end && __all_sync(0xffffffffu, mbar_test(sfull(half), (n + 1) & 1));
-        if (have) load_s();
-        // P of the step before is read, and its arrivals are complete (warps without rows
-        // are here early)
-        if (n > 0) ok = wait(pvdone(half), n - 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (busy) {
-          tmem_st32(t_p(half) + tl, p);
+          tmem_st32(ts, p);
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull(half));
+        if (lane == 0) mbar_arrive(pfull(j & 1));
         first = false;
-        stage += 2;
-        if (stage >= kT8Stages) stage -= kT8Stages;
       }
-      // the next item's queries, while the last product is awaited
-      pos += it.n;
-      j0 += it.n;
-      const TreeItem then = pos < hi ? tree_item(c, a, sm.plan, pos, hi) : it;
-      if (pos < hi && real_of(then)) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(q_of(then)));
-      if (ok && !first) ok = wait(pvdone(half), n - 1);
+      // the next item's queries ahead of this one's results
+      if (pos < hi) scale = put_row(then, item + 1);
+      ok = wait(pvdone((end - 1) & 1), (end - 1) >> 1) && ok;
       if (!ok) fail();
-      sm.ex[half][r] = make_float4(mx, u, l, first ? 0.0f : 1.0f);
-      tc_fence_before();
-      named_sync(2, 256);
-      tc_fence_after();
-      if (ok && busy) {
-        // both halves' rows, 64 features by each half's warps
-        const float4 e0 = sm.ex[0][r], e1 = sm.ex[1][r];
-        const float top = fmaxf(e0.y, e1.y);
-        auto weight = [&](const float4& e) { return e.z == 0.0f ? 0.0f : e.z * (e.y == top ? 1.0f : fast_exp2(e.y - top)); };
-        const float lsum = weight(e0) + weight(e1);
-        auto factor = [&](const float4& e) {
-          return e.z == 0.0f ? 0.0f : __fdiv_rn(fast_exp2(e.x - kT8Up - top), lsum);
-        };
-        const float f0 = factor(e0), f1 = factor(e1);
-        const bool whole = it.n == it.per, two0 = e0.w != 0.0f, two1 = e1.w != 0.0f;
-        uint8_t* out = a.out + (((long long)it.i * a.max_nodes + m) * c.hkv * G + (size_t)it.h * G + (row - m * G)) * (2 * kD) + 128 * half;
+      if (busy) {
+        tc_fence_after();
+        sm.pair[told][part][r].x = l;
+        named_sync(pair_bar, 64);
+        const float lsum = l + sm.pair[told][part ^ 1][r].x;
+        told ^= 1;
+        // a sum that left fp32's range: NaN, which the second kernel looks into
+        const float f = lsum == 0.0f ? 0.0f : lsum < INFINITY ? __fdiv_rn(fast_exp2(mx - kT8Up - u), lsum) : __uint_as_float(0x7fffffffu);
+        const bool whole = it.n == it.per;
+        uint8_t* out = a.out + (((long long)it.i * a.max_nodes + m) * c.hkv * G + (size_t)it.h * G + (row - m * G)) * (2 * kD) + 128 * part;
         // a part: [feature / 4][row][4], whose lanes' stores are neighbours, then (u, l) of the rows
-        float4* part = reinterpret_cast<float4*>(a.part + (size_t)(2 * blockIdx.x + (it.s0 > 0 ? 0 : 1)) * part_rows * (kD + 2));
+        float4* dst = reinterpret_cast<float4*>(a.part + (size_t)(2 * blockIdx.x + (it.s0 > 0 ? 0 : 1)) * part_rows * (kD + 2));
 #pragma unroll 1
         for (int q = 0; q < 4; q++) {
-          float o0[16], o1[16];
-          tmem_ld16_nowait(t_o(0) + tl + 64 * half + 16 * q, o0);
-          tmem_ld16_nowait(t_o(1) + tl + 64 * half + 16 * q, o1);
+          float o[16];
+          tmem_ld16_nowait(t_o + tl + 64 * part + 16 * q, o);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; e++) {
-            asm volatile("" : "+f"(o0[e]));
-            asm volatile("" : "+f"(o1[e]));
-            o0[e] = (two0 ? o0[e] * f0 : 0.0f) + (two1 ? o1[e] * f1 : 0.0f);
+            asm volatile("" : "+f"(o[e]));
+            o[e] *= f;
           }
           if (real && whole) {
             uint32_t w[8], bad = 0;
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-              w[e] = pack_elems<ELEM>(o0[2 * e], o0[2 * e + 1]);
+              w[e] = pack_elems<ELEM>(o[2 * e], o[2 * e + 1]);
               find_not_finite<ELEM>(bad, w[e]);
             }
             if (__builtin_expect(found_not_finite(bad), 0)) {
 #pragma unroll
-              for (int e = 0; e < 8; e++) w[e] = pack_elems<ELEM>(in_range<ELEM>(o0[2 * e]), in_range<ELEM>(o0[2 * e + 1]));
+              for (int e = 0; e < 8; e++) w[e] = pack_elems<ELEM>(in_range<ELEM>(o[2 * e]), in_range<ELEM>(o[2 * e + 1]));
             }
             reinterpret_cast<uint4*>(out)[2 * q] = make_uint4(w[0], w[1], w[2], w[3]);
             reinterpret_cast<uint4*>(out)[2 * q + 1] = make_uint4(w[4], w[5], w[6], w[7]);
           } else if (real) {
 #pragma unroll
             for (int e = 0; e < 4; e++)
-              part[(16 * half + 4 * q + e) * part_rows + r] = make_float4(o0[4 * e], o0[4 * e + 1], o0[4 * e + 2], o0[4 * e + 3]);
+              dst[(16 * part + 4 * q + e) * part_rows + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
-        if (real && !whole && half == 0) reinterpret_cast<float2*>(part + part_rows * (kD / 4))[r] = make_float2(top, lsum);
+        if (real && !whole && part == 0) reinterpret_cast<float2*>(dst + part_rows * (kD / 4))[r] = make_float2(u, lsum);
       }
       tc_fence_before();
       if (pos >= hi) break;
       it = then;
-      load_row(it);
     }
   } else {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kT8RegsFew));
-  if (warp < 8 + kT8Conv) {
-    // ---- codes, tails and drafts to 16-bit operands: the tiles of the steps are dealt
-    // out to the warps in turn ----
-    const int cw = warp - 8;
-    const int steps = (kT8Step * (hi - lo) - cw + kT8Conv - 1) / kT8Conv;      // tiles cw, cw + kT8Conv, ..
-    const int mat = lane >> 3, mrow = lane & 7, me = mat & 1, ms = mat >> 1;
-    const uint32_t stage0 = smem_u32(smem);
-    TileDesc* desc = sm.desc[cw];
-    auto describe = [&](int batch) {       // tiles 32 batch ..: a lane each
-      const int k = 32 * batch + lane;
-      if (k < steps) describe_tile(c, a, sm.plan, lo, cw + kT8Conv * k, desc[k & (kT8Descs - 1)]);
-      __syncwarp();
-    };
-    // The next copy: codes of a tile, or K, then V of a 16-bit one.
-    uint8_t* ring = smem + kT8OffRing + cw * (kT8Ring * kT8Entry);
-    const uint32_t rbar = smem_u32(sm.rbar[cw]);
-    int at = 0, at_v = 0, ahead = 0, entry = 0, parity = 0, flying = 0;
-    auto issue = [&]() {
-      TileDesc d;
-      for (;; at++) {
-        if (at >= steps) return;
-        d = desc[at & (kT8Descs - 1)];
-        if (d.kind < 4) break;
-      }
-      const uint32_t dst = smem_u32(ring + ahead * kT8Entry), bar = rbar + 8 * ahead;
-      if (d.kind <= 2) {
-        if (lane == 0) {
-          mbar_expect_tx(bar, 2 * kTile);
-          bulk_g2s(dst, d.src + at_v * (2 * kTile), 2 * kTile, bar);
-        }
-      } else {
-        const int i = d.req_head >> 12, h = d.req_head & 4095, n = min(sm.plan.M[i] - d.pos0, kSub);
-        const long long row = (long long)i * a.max_nodes + d.pos0 + lane;
-        if (lane == 0) mbar_expect_tx(bar, n * (2 * kD));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kT8RegsFew));
+    if (warp < 8 + kT8Conv) {
+      // ---- codes, tails and drafts to 16-bit operands: the tiles of the steps are dealt
+      // out to the warps in turn; K of a warp's next tile before V of this one, since S
+      // comes before P ----
+      const int cw = warp - 8;
+      const int tiles = (kT8Step * (hi - lo) - cw + kT8Conv - 1) / kT8Conv;      // tiles cw, cw + kT8Conv, ..
+      const int mat = lane >> 3, mrow = lane & 7, me = mat & 1, ms = mat >> 1;
+      const uint32_t slot0 = smem_u32(smem);
+      TileDesc* desc = sm.desc[cw];
+      auto describe = [&](int batch) {       // tiles 32 batch ..: a lane each
+        const int k = 32 * batch + lane;
+        if (k < tiles) describe_tile(c, a, sm.plan, lo, cw + kT8Conv * k, desc[k & (kT8Descs - 1)]);
         __syncwarp();
-        if (lane < n)
-          bulk_g2s(dst + lane * kT8Pitch, (at_v ? a.v + row * a.vs : a.k + row * a.ks) + h * (2 * kD), 2 * kD, bar);
+      };
+      // a job: K (op 0) or V of tile k
+      auto next_job = [&](int& k, int& op) {
+        if (op == 0) {
+          if (k == 0 && tiles > 1) k = 1;
+          else {
+            op = 1;
+            k = k > 0 ? k - 1 : 0;
+          }
+        } else if (k + 2 < tiles) {
+          k += 2;
+          op = 0;
+        } else {
+          k++;
+        }
+      };
+      uint8_t* ring = smem + kT8OffRing + cw * (kT8Ring * kT8Entry);
+      const uint32_t rbar = smem_u32(sm.rbar[cw]);
+      int at = 0, at_op = 0, ahead = 0, entry = 0, parity = 0, flying = 0;
+      auto issue = [&]() {                 // the next copy of codes
+        for (; at < tiles; next_job(at, at_op)) {
+          const TileDesc* d = desc + (at & (kT8Descs - 1));
+          if (d->kind > 1) continue;
+          if (lane == 0) {
+            mbar_expect_tx(rbar + 8 * ahead, kT8Entry);
+            bulk_g2s(smem_u32(ring + ahead * kT8Entry), d->src + at_op * kT8Entry, kT8Entry, rbar + 8 * ahead);
+          }
+          flying++;
+          ahead = (ahead + 1) & (kT8Ring - 1);
+          next_job(at, at_op);
+          return;
+        }
+      };
+      int described = 0;
+      if (tiles > 0) {
+        describe(0);
+        for (int e = 0; e < kT8Ring; e++) issue();
       }
-      flying++;
-      ahead = ahead == kT8Ring - 1 ? 0 : ahead + 1;
-      at_v = d.kind >= 2 ? at_v ^ 1 : 0;
-      at += at_v ^ 1;
-    };
-    auto arrived = [&]() {               // the next copy
-      const uint8_t* p = ring + entry * kT8Entry;
-      ok = wait(rbar + 8 * entry, parity);
-      if (!ok) return p;
-      flying--;
-      if (++entry == kT8Ring) {
-        entry = 0;
-        parity ^= 1;
-      }
-      return p;
-    };
-    int described = 0;
-    if (steps > 0) {
-      describe(0);
-      for (int e = 0; e < kT8Ring; e++) issue();
-    }
 #pragma unroll 1
-    for (int k = 0; ok && k < steps; k++) {
-      // descriptors up to 32 tiles ahead
-      if (32 * (described + 1) < steps && k >= 32 * described + 4 * cw) describe(++described);
-      const int tile_of = cw + kT8Conv * k, j = tile_of / kT8Step, sub = tile_of % kT8Step, stage = j % kT8Stages;
-      // (P V of step j - 8, the phase before, is done: this warp's last tile was of step
-      // j - 1 or j - 2, so P V of j - 5, whose S waited for it, or of j - 6 is)
-      if (j >= kT8Stages) ok = wait(empty(stage), j / kT8Stages - 1);
-      if (!ok) break;
-      const uint32_t base = stage0 + stage * kT8Stage;
-      // the lane's row of the four 8 x 8 matrices of a store: K, V, V of drafts
-      const uint32_t k_at = base + (2 * sub + ms) * 1024 + mrow * 128 + ((me ^ mrow) << 4);
-      const uint32_t v_at = base + 16384 + ms * 1024 + mrow * 128 + (((2 * sub + me) ^ mrow) << 4);
-      const TileDesc d = desc[k & (kT8Descs - 1)];
-      TileMeta meta{d.ks, d.lv, d.pos0, d.kind < 2 ? d.kind : d.kind - 1};
-      if (d.kind <= 1) {
-        const uint8_t* p = arrived() + 16 * lane;
+      for (int k = 0, op = 0; ok && k < tiles; next_job(k, op)) {
+        // descriptors up to 32 tiles ahead
+        if (op == 0 && 32 * (described + 1) < tiles && k >= 32 * described + 2 + 3 * cw) describe(++described);
+        const int tile = cw + kT8Conv * k, x = tile >> 2, sub = tile & 3, slot = x & (kT8Slots - 1);
+        // (the slot's phase before this one is over, too: products are issued in order, and
+        // this warp has waited for those of part x - 5 or x - 6 with its last tile)
+        if (x >= kT8Slots) ok = wait(op ? vfree(slot) : kfree(slot), x / kT8Slots - 1);
         if (!ok) break;
-        uint4 w[8];
+        const uint32_t base = slot0 + (op ? kT8OffV : 0) + slot * kT8Slot;
+        // the lane's row of the four 8 x 8 matrices of a store: K, V (row: feature) or V of
+        // drafts (row: feature, matrices the other way round)
+        const uint32_t k_at = base + (2 * sub + ms) * 1024 + mrow * 128 + ((me ^ mrow) << 4);
+        const uint32_t v_at = base + ms * 1024 + mrow * 128 + (((2 * sub + me) ^ mrow) << 4);
+        const TileDesc d = desc[k & (kT8Descs - 1)];
+        TileMeta meta{d.ks, d.lv, d.pos0, d.kind < 2 ? d.kind : d.kind - 1};
+        if (d.kind <= 1) {
+          ok = wait(rbar + 8 * entry, parity);
+          if (!ok) break;
+          const uint8_t* p = ring + entry * kT8Entry + 16 * lane;
+          uint4 w[4];
 #pragma unroll
-        for (int e = 0; e < 8; e++) w[e] = *reinterpret_cast<const uint4*>(p + 512 * e);
-        __syncwarp();
-        issue();
+          for (int e = 0; e < 4; e++) w[e] = *reinterpret_cast<const uint4*>(p + 512 * e);
+          flying--;
+          entry = (entry + 1) & (kT8Ring - 1);
+          parity ^= entry == 0;
+          __syncwarp();
+          issue();
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-          const uint32_t at0 = e < 4 ? (k_at + (e >> 1) * 8192) ^ ((e & 1) << 6) : v_at + (e - 4) * 4096;
-          const uint32_t at1 = e < 4 ? at0 ^ 32u : at0 + 2048;
-          uint32_t x[4];
-          code_halves<CODE>(w[e].x, x[0], x[1]);
-          code_halves<CODE>(w[e].y, x[2], x[3]);
-          stmatrix4(at0, x[0], x[1], x[2], x[3]);
-          code_halves<CODE>(w[e].z, x[0], x[1]);
-          code_halves<CODE>(w[e].w, x[2], x[3]);
-          stmatrix4(at1, x[0], x[1], x[2], x[3]);
+          for (int e = 0; e < 4; e++) {
+            const uint32_t at0 = op ? v_at + e * 4096 : (k_at + (e >> 1) * 8192) ^ ((e & 1) << 6);
+            const uint32_t at1 = op ? at0 + 2048 : at0 ^ 32u;
+            uint32_t y[4];
+            code_halves<CODE>(w[e].x, y[0], y[1]);
+            code_halves<CODE>(w[e].y, y[2], y[3]);
+            stmatrix4(at0, y[0], y[1], y[2], y[3]);
+            code_halves<CODE>(w[e].z, y[0], y[1]);
+            code_halves<CODE>(w[e].w, y[2], y[3]);
+            stmatrix4(at1, y[0], y[1], y[2], y[3]);
+          }
+        } else if (d.kind <= 3) {
+          const int i = d.req_head >> 12, h = d.req_head & 4095;
+          const bool draft = d.kind == 3;
+          const int n = min((draft ? sm.plan.M[i] : sm.plan.N[i]) - d.pos0, kSub);      // valid tokens
+          const long long first = (long long)i * a.max_nodes + d.pos0;
+          const uint8_t* ksrc = draft ? a.k + first * a.ks + h * (2 * kD) : d.src;
+          const uint8_t* vsrc = draft ? a.v + first * a.vs + h * (2 * kD) : d.src + 2 * kTile;
+          int ex = 0;
+          if (ELEM == DKV_BF16) {
+            ex = elems_exp(op ? vsrc : ksrc, op, draft, n, op ? a.vs : a.ks);
+            if (op == 0) {        // the softmax wants both with S
+              meta.ks = kLogitScale * pow2(ex);
+              meta.lv = (float)elems_exp(vsrc, true, draft, n, a.vs);
+            }
+          } else {
+            meta.lv = 0.0f;
+          }
+          const uint32_t vt_at = base + me * 1024 + mrow * 128 + (((2 * sub + ms) ^ mrow) << 4);
+          put_elems<ELEM>(op ? vsrc : ksrc, op, draft, n, op ? a.vs : a.ks, ex, op == 0 ? k_at : draft ? vt_at : v_at);
         }
-      } else if (d.kind <= 3) {
-        const int i = d.req_head >> 12, draft = d.kind == 3 ? 2 : 0;
-        const int n = min((draft ? sm.plan.M[i] : sm.plan.N[i]) - d.pos0, kSub);      // valid tokens
-        const uint8_t* p = arrived();
-        if (!ok) break;
-        meta.ks = kLogitScale * pow2(put_elems<ELEM>(p, draft, n, k_at));
+        if (op == 0 && lane == 0) sm.meta[x & (2 * kT8Slots - 1)][sub] = meta;
+        fence_proxy_async();
         __syncwarp();
-        issue();
-        p = arrived();
-        if (!ok) break;
-        const uint32_t vt_at = base + 16384 + me * 1024 + mrow * 128 + (((2 * sub + ms) ^ mrow) << 4);
-        meta.lv = (float)put_elems<ELEM>(p, draft + 1, n, draft ? vt_at : v_at);
-        __syncwarp();
-        issue();
+        if (lane == 0) mbar_arrive(op ? vfull(slot) : kfull(slot));
       }
-      if (lane == 0) sm.meta[stage][sub] = meta;
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full(stage));
-    }
-    if (!ok) fail();
-    // no copy may be in flight at the exit
-    for (; flying > 0; flying--) {
-      wait_long(rbar + 8 * entry, parity);
-      if (++entry == kT8Ring) {
-        entry = 0;
-        parity ^= 1;
+      if (!ok) fail();
+      // no copy may be in flight at the exit
+      for (; flying > 0; flying--) {
+        wait_long(rbar + 8 * entry, parity);
+        entry = (entry + 1) & (kT8Ring - 1);
+        parity ^= entry == 0;
       }
-    }
-  } else {
-    // ---- products: S of the steps to come, then O += P V; the whole warp walks, one
-    // lane issues (counters, so that operands stay in uniform registers) ----
-    constexpr uint32_t id_s = umma_idesc_f16(128, 64), id_pv = umma_idesc_f16(128, 128);
-    const uint64_t kd = umma_desc_sw128(smem_u32(smem)), vd = umma_desc_sw128(smem_u32(smem + 16384));
-    // Of each half: steps whose S, whose P V are issued, whose P V are done, and their
-    // stages. Whatever can be issued is, but S of step j waits for P V of step j - 3, so that
-    // stages are freed nearly in order (a converting warp waits for those of its tiles only).
-    int ns[2] = {0, 0}, nv[2] = {0, 0}, done[2] = {0, 0}, s_stage[2] = {0, 1}, s_round[2] = {0, 0}, v_stage[2] = {0, 1};
-    auto test = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0; };
-    auto next = [](int& stage) {          // two steps on; true behind the last stage
-      stage += 2;
-      if (stage < kT8Stages) return false;
-      stage -= kT8Stages;
-      return true;
-    };
-    int item = 0, j0 = 0;
-    for (int pos = lo; ok && pos < hi; item++) {
-      const TreeItem it = tree_item(c, a, sm.plan, pos, hi);
-      const int n = __shfl_sync(0xffffffffu, it.n, 0);
-      // tiles of the part's last step
-      const int rest = __shfl_sync(0xffffffffu, min(kT8Step, it.tiles.count - kT8Step * (it.s0 + it.n - 1)), 0);
-      const int begin[2] = {(j0 + 1) >> 1, j0 >> 1};
-      j0 += n;
-      pos += n;
-      const int end[2] = {(j0 + 1) >> 1, j0 >> 1};
-      ok = wait(ready, item);
-      if (!ok) break;
-      tc_fence_after();
-      long long since = 0;
+    } else {
+      // ---- products: S of the steps to come, O += P V; the whole warp walks, one lane
+      // issues (counters, so that operands stay in uniform registers). Products run in the
+      // order of their issue, so S may follow the P V that read its place ----
+      constexpr uint32_t id_s = umma_idesc_f16(128, 64), id_pv = umma_idesc_f16(128, 128);
+      const uint64_t kd = umma_desc_sw128(smem_u32(smem)), vd = umma_desc_sw128(smem_u32(smem + kT8OffV));
+      auto test = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0; };
+      auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      // the part of the sequence that S and that P V are in: its last step, the tiles of that
+      struct Run {
+        int pos, end, rest, item;
+      };
+      auto next_run = [&](Run& r) {
+        const TreeItem it = tree_item(c, a, sm.plan, lo + r.pos, hi);
+        r.end = uniform(r.pos + it.n);
+        r.rest = uniform(min(kT8Step, it.tiles.count - kT8Step * (it.s0 + it.n - 1)));
+        r.item++;
+      };
+      Run rs{0, 0, 0, -1}, rv{0, 0, 0, -1};
+      int js = 0, jv = 0;              // next step of S, of P V
+      bool begin = true, q_there = false;
+      next_run(rs);
+      next_run(rv);
+      const int steps = uniform(hi - lo);
       int idle = 0;
+      long long since = 0;
 #pragma unroll 1
-      while (nv[0] < end[0] || nv[1] < end[1]) {
+      while (jv < steps) {
         bool none = true;
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          if (done[h] < nv[h] && test(pvdone(h), nv[h] - 1)) done[h] = nv[h];
-          if (ns[h] < end[h] && done[h ^ 1] >= ns[h] - 1 + h && test(full(s_stage[h]), s_round[h]) && (ns[h] == 0 || test(sfree(h), ns[h] - 1))) {
+        if (js < steps && js < jv + 2) {
+          if (!q_there) q_there = test(qfull(rs.item & 1), rs.item >> 1);
+          const int x = 2 * js, s0 = x & (kT8Slots - 1), phase = x / kT8Slots;
+          if (q_there && test(kfull(s0), phase) && test(kfull(s0 + 1), phase)) {
             tc_fence_after();
+            const uint32_t d = uniform(t_s(js & 1)), q = uniform(t_q(rs.item & 1));
+            const int two = uniform(js < rs.end - 1 || rs.rest > 4), at = uniform(s0 * (kT8Slot >> 4));
             if (elected()) {
-              const uint64_t bd = kd + s_stage[h] * (kT8Stage >> 4);
+              const uint64_t bd = kd + at;
 #pragma unroll
               for (int e = 0; e < 8; e++)
-                umma_f16_tmem_a(t_s(h), t_q + 8 * e, bd + (((e >> 2) * 8192 + (e & 3) * 32) >> 4), id_s, e > 0);
-              umma_commit(sfull(h));
+                umma_f16_tmem_a(d, q + 8 * e, bd + (((e >> 2) * 8192 + (e & 3) * 32) >> 4), id_s, e > 0);
+              if (two) {
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                  umma_f16_tmem_a(d + 64, q + 8 * e, bd + ((kT8Slot + (e >> 2) * 8192 + (e & 3) * 32) >> 4), id_s, e > 0);
+              }
+              umma_commit(sfull(js & 1));
+              umma_commit(kfree(s0));
+              umma_commit(kfree(s0 + 1));
             }
             __syncwarp();
-            ns[h]++;
-            if (next(s_stage[h])) s_round[h] ^= 1;
+            if (++js == rs.end && js < steps) {
+              rs.pos = js;
+              next_run(rs);
+              q_there = false;
+            }
             none = false;
           }
-          if (nv[h] < ns[h] && test(pfull(h), nv[h])) {
+        }
+        if (jv < js) {
+          const int x = 2 * jv, s0 = x & (kT8Slots - 1), phase = x / kT8Slots;
+          if (test(pfull(jv & 1), jv >> 1) && test(vfull(s0), phase) && test(vfull(s0 + 1), phase)) {
             tc_fence_after();
-            const bool start = nv[h] == begin[h];
-            const int tiles = 2 * nv[h] + h == j0 - 1 ? rest : kT8Step;
+            const uint32_t p = uniform(t_s(jv & 1));
+            const int n = uniform(jv < rv.end - 1 ? kT8Step : rv.rest), go_on = uniform(!begin), at = uniform(s0 * (kT8Slot >> 4));
             if (elected()) {
-              const uint64_t bd = vd + v_stage[h] * (kT8Stage >> 4);
+              const uint64_t bd = vd + at;
 #pragma unroll
               for (int e = 0; e < kT8Step; e++)
-                if (e < tiles) umma_f16_tmem_a(t_o(h), t_p(h) + 8 * e, bd + (e * 32 >> 4), id_pv, !start || e > 0);
-              umma_commit(pvdone(h));
-              umma_commit(empty(v_stage[h]));
+                if (e < n)
+                  umma_f16_tmem_a(t_o, p + 64 * (e >> 2) + 8 * (e & 3), bd + (((e >> 2) * kT8Slot + (e & 3) * 32) >> 4), id_pv,
+                                  go_on || e > 0);
+              umma_commit(pvdone(jv & 1));
+              umma_commit(vfree(s0));
+              umma_commit(vfree(s0 + 1));
             }
             __syncwarp();
-            done[h] = nv[h]++;       // P came after the step before was done
-            next(v_stage[h]);
+            begin = false;
+            if (++jv == rv.end && jv < steps) {
+              rv.pos = jv;
+              next_run(rv);
+              begin = true;
+            }
             none = false;
           }
         }
@@ -1051,14 +1080,13 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           break;
         }
       }
+      if (!ok) fail();
+      if (elected()) {
+        umma_commit(drain);                // every MMA issued so far has completed
+        mbar_wait_bounded(drain, 0);
+      }
+      __syncwarp();
     }
-    if (!ok) fail();
-    if (elected()) {
-      umma_commit(drain);                // every MMA issued so far has completed
-      mbar_wait_bounded(drain, 0);
-    }
-    __syncwarp();
-  }
   }
   tc_fence_before();
   __syncthreads();
