@@ -13,15 +13,18 @@ constexpr int kT8Rows = 128;        // query rows of a unit: (node, head of the 
 constexpr int kT8Walkers = 8;       // warps of a block of the second kernel
 constexpr int kT8Step = 8;          // tiles of a step, in two parts of four
 constexpr int kT8Least = 1;         // steps that make a CTA worth its start
-constexpr int kT8Conv = 7;          // warps that convert
-constexpr int kT8Threads = 32 * (8 + kT8Conv + 1);
-// registers a thread: launched with 128; 256 x 184 + 256 x 72 = 512 x 128
-constexpr int kT8RegsFew = 72, kT8RegsMany = 184;
-constexpr int kT8Slots = 4;         // parts whose K (V) is kept as operands
-constexpr int kT8Slot = 16384;      // K or V of a part in 16 bits
-constexpr int kT8Descs = 64;        // descriptors of a converting warp, a ring
-constexpr int kT8Ring = 4;          // copies that it has on their way
-constexpr int kT8Entry = kTile;     // K or V codes of a tile
+// warps: 0 .. 7 softmax, 8 .. 11 convert K, 12 .. 15 V, 16 products, 17 lookups, 18
+// copies of K codes, 19 of V codes
+constexpr int kT8Threads = 640;
+// registers a thread: launched with 96; 256 x 144 + 384 x 64 = 640 x 96
+constexpr int kT8RegsFew = 64, kT8RegsMany = 144;
+constexpr int kT8Slots = 2;         // steps whose K (V) is kept as operands
+constexpr int kT8Ring = 2;          // steps whose K (V) codes are there or on their way
+constexpr int kT8Entry = kT8Step * kTile;   // K or V codes of a step
+constexpr int kT8Slot = 32768;      // K or V of a step in 16 bits
+constexpr int kT8Batch = 4;         // steps that are looked up at once
+constexpr int kT8Descs = 4 * kT8Batch;      // steps whose descriptors are kept, a ring
+constexpr int kT8Metas = 8;         // steps whose scales are kept for the softmax, a ring
 constexpr float kT8Up = 7.0f;       // log2 of a weight at its row's maximum
 constexpr float kT8Most = 32768.0f; // largest sum of a row's weights of one tile (fp16 holds 65504)
 constexpr float kT8Far = 60.0f;     // log2 of how far weights may be from probabilities
@@ -390,21 +393,23 @@ struct TileMeta {
 };
 
 struct TreeSmem {
-  TileDesc desc[kT8Conv][kT8Descs];
-  TileMeta meta[2 * kT8Slots][4];      // K of a part comes before the softmax has read that of part x - 4, not of x - 8
+  TileDesc desc[kT8Descs][kT8Step];
+  TileMeta meta[kT8Metas][kT8Step];    // (K of step j comes when the softmax has read that of step j - 5)
   TreePlan plan;
   int parents[kMaxNodes];
   float2 pair[2][2][kT8Rows];      // what the two warps of a row tell each other
   int scan[32];
-  // K, V of a part there, no longer needed; S, P, P V of a step there, queries there (two of
+  int2 runs[4];                    // ends of items of the products, the tiles of their last steps
+  // K, V of a step there, no longer needed; S, P, P V of a step there, queries there (two of
   // each); drain
   uint64_t bar[4 * kT8Slots + 9];
-  uint64_t rbar[kT8Conv][kT8Ring];
+  uint64_t rfull[2][kT8Ring], rfree[2][kT8Ring];      // copies of K, of V codes
+  uint64_t dfull[4], dfree[4];     // batches of descriptors
   uint32_t taddr;
   int fail;
 };
 constexpr int kT8OffV = kT8Slots * kT8Slot, kT8OffRing = 2 * kT8Slots * kT8Slot;
-constexpr int kT8OffSmem = kT8OffRing + kT8Conv * kT8Ring * kT8Entry;
+constexpr int kT8OffSmem = kT8OffRing + 2 * kT8Ring * kT8Entry;
 constexpr int kT8Smem = 1024 + kT8OffSmem + (int)sizeof(TreeSmem);
 
 __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -439,10 +444,10 @@ __device__ __forceinline__ bool elected() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p != 0;
 }
-__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity) { return mbar_wait_bounded(bar, parity); }
 
-// Tile x of a CTA whose range begins at step lo.
-__device__ __forceinline__ void describe_tile(const Cache8View& c, const Tree8Args& a, const TreePlan& plan, int lo, int x, TileDesc& out) {
+// Tile x of a CTA whose range begins at step lo, but for its page's scales.
+__device__ __forceinline__ TileDesc describe_tile(const Cache8View& c, const Tree8Args& a, const TreePlan& plan, int lo, int x,
+                                                  const float2*& scales) {
   const int pos = lo + x / kT8Step;
   const TreeItem it = tree_item(c, a, plan, pos, pos + 1);
   x = kT8Step * it.s0 + x % kT8Step;
@@ -457,10 +462,8 @@ __device__ __forceinline__ void describe_tile(const Cache8View& c, const Tree8Ar
         c.latch(DKV_ERR_CHECK, it.i);
         page = 0;
       }
-      const float2 sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * c.hkv + it.h));
+      scales = reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * c.hkv + it.h));
       d.src = c.pages + c.page_head(page, it.h) + (size_t)(tile & ((1 << per) - 1)) * (2 * kTile);
-      d.ks = sc.x * kLogitScale;
-      d.lv = log2f(sc.y);
       // every depth sees all of it
       d.kind = a.window <= 0 || d.pos0 >= it.N + it.M - a.window || d.pos0 + kSub <= a.sinks ? 0 : 1;
     } else {
@@ -473,7 +476,7 @@ __device__ __forceinline__ void describe_tile(const Cache8View& c, const Tree8Ar
     d.req_head = it.i << 12 | it.h;
     d.kind = 3;
   }
-  out = d;
+  return d;
 }
 
 // A lane's words of K or V (op 0, 1) of a tile of the tail (draft 0) or of drafts (rows of
@@ -523,7 +526,7 @@ __device__ __noinline__ void put_elems(const uint8_t* src, bool v, bool draft, i
 #pragma unroll
   for (int f = 0; f < 8; f++) {
     if (!v)
-      stmatrix4((at + (f >> 2) * 8192) ^ ((f & 3) << 5), x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
+      stmatrix4((at + (f >> 2) * 16384) ^ ((f & 3) << 5), x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
     else if (!draft)
       stmatrix4(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
     else
@@ -532,13 +535,14 @@ __device__ __noinline__ void put_elems(const uint8_t* src, bool v, bool draft, i
 }
 
 template <int ELEM, int CODE>
-__global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__ Cache8View c, const __grid_constant__ Tree8Args a, int part_rows) {
+__global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__ Cache8View c, const __grid_constant__ Tree8Args a, int part_rows,
+                                                         int* plan) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TreeSmem& sm = *reinterpret_cast<TreeSmem*>(smem + kT8OffSmem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, G = c.G;
-  // part x = 2 j + (0, 1) of step j of the CTA: slot x & 3; S and P of step j: place j & 1
+  // step j of the CTA: K and V in slot j % kT8Slots, S and P in place j & 1
   const uint32_t b0 = smem_u32(sm.bar);
   auto kfull = [&](int s) { return b0 + 8u * s; };
   auto kfree = [&](int s) { return b0 + 8u * (kT8Slots + s); };
@@ -563,11 +567,18 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       mbar_init(pvdone(s), 1);
     }
     mbar_init(drain, 1);
-    for (int w = 0; w < kT8Conv * kT8Ring; w++) mbar_init(smem_u32(&sm.rbar[0][0]) + 8 * w, 1);
+    for (int s = 0; s < 4; s++) {
+      mbar_init(smem_u32(&sm.dfull[s]), 1);
+      mbar_init(smem_u32(&sm.dfree[s]), 10);
+    }
+    for (int s = 0; s < 2 * kT8Ring; s++) {
+      mbar_init(smem_u32(&sm.rfull[0][0]) + 8 * s, 1);
+      mbar_init(smem_u32(&sm.rfree[0][0]) + 8 * s, 4);
+    }
     sm.fail = 0;
     fence_mbar_init();
   }
-  if (warp == 8 + kT8Conv) tmem_alloc(smem_u32(&sm.taddr), 512);
+  if (warp == 16) tmem_alloc(smem_u32(&sm.taddr), 512);
   pdl_wait();
   // an error of an earlier call (its load is in flight with the plan's)
   const int halted = threadIdx.x == 0 ? *(volatile int*)c.status : 0;
@@ -575,9 +586,11 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   tc_fence_before();
   const bool stopped = __syncthreads_or(halted);
   tc_fence_after();
+  if (blockIdx.x == 0)           // for the second kernel
+    for (int i = threadIdx.x; i <= a.n_req; i += blockDim.x) plan[i] = sm.plan.pre[i];
   const int ctas = tree_ctas(total, gridDim.x);
   if (stopped || total == 0 || (int)blockIdx.x >= ctas) {
-    if (warp == 8 + kT8Conv) tmem_dealloc(__shfl_sync(0xffffffffu, sm.taddr, 0), 512);
+    if (warp == 16) tmem_dealloc(__shfl_sync(0xffffffffu, sm.taddr, 0), 512);
     return;
   }
   const int lo = range_start(total, blockIdx.x, ctas), hi = range_start(total, blockIdx.x + 1, ctas);
@@ -586,15 +599,16 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   const uint32_t t_o = tbase;
   auto t_s = [&](int s) { return tbase + 128u + 128u * s; };
   auto t_q = [&](int s) { return tbase + 384u + 64u * s; };
-  auto fail = [&]() {
-    c.latch(DKV_ERR_TIMEOUT, -1);
-    *(volatile int*)&sm.fail = 1;
-  };
-  auto wait = [&](uint32_t bar, int phase) {       // the same for every lane
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1))) return true;
-    const bool there = __all_sync(0xffffffffu, *(volatile int*)&sm.fail == 0 && wait_long(bar, phase & 1)) != 0;
-    if (!there) fail();
-    return there;
+  // Bounded: 2^22 attempts of up to a microsecond each; then the block's other waits give
+  // up, too. The same for every lane. (Short: the kernel's hot code has to fit the
+  // instruction caches.)
+  auto wait = [&](uint32_t bar, int phase) {
+    for (int n = 1 << 22; !__all_sync(0xffffffffu, mbar_try_wait_hint(bar, phase & 1, 1000u)); n--)
+      if (n == 0 || ((n & 255) == 0 && *(volatile int*)&sm.fail)) {
+        *(volatile int*)&sm.fail = 1;
+        return false;
+      }
+    return true;
   };
   bool ok = true;
 
@@ -687,6 +701,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       bool first = true, raise = true;
       for (; j < end; j++) {
         // (after a wait that gave up the warps walk on, through the same barriers)
+        // (step -1, ahead of the first: the code comes to the caches, nothing is stored)
         ok = wait(sfull(j & 1), j >> 1) && ok;
         if (j > 1) ok = wait(pvdone(j & 1), (j >> 1) - 1) && ok;      // long since: its phases are seen in turn
         tc_fence_after();
@@ -695,7 +710,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           const uint32_t ts = t_s(j & 1) + tl + 64 * part;
           tmem_ld32_nowait(ts, s);
           tmem_ld32_nowait(ts + 32, s + 32);
-          const TileMeta* meta = sm.meta[(2 * j + part) & (2 * kT8Slots - 1)];
+          const TileMeta* meta = sm.meta[j & (kT8Metas - 1)] + 4 * part;
           float f[4], lv[4];
           int kind[4], pos0[4];
 #pragma unroll
@@ -813,7 +828,6 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       // the next item's queries ahead of this one's results
       if (pos < hi) scale = put_row(then, item + 1);
       ok = wait(pvdone((end - 1) & 1), (end - 1) >> 1) && ok;
-      if (!ok) fail();
       if (busy) {
         tc_fence_after();
         sm.pair[told][part][r].x = l;
@@ -863,224 +877,228 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kT8RegsFew));
-    if (warp < 8 + kT8Conv) {
-      // ---- codes, tails and drafts to 16-bit operands: the tiles of the steps are dealt
-      // out to the warps in turn; K of a warp's next tile before V of this one, since S
-      // comes before P ----
-      const int cw = warp - 8;
-      const int tiles = (kT8Step * (hi - lo) - cw + kT8Conv - 1) / kT8Conv;      // tiles cw, cw + kT8Conv, ..
+    const int steps = hi - lo;
+    if (warp < 16) {
+      // ---- codes, tails and drafts to 16-bit operands: a warp two tiles of each step ----
+      const int op = warp >= 12, first = 2 * (warp & 3);
       const int mat = lane >> 3, mrow = lane & 7, me = mat & 1, ms = mat >> 1;
-      const uint32_t slot0 = smem_u32(smem);
-      TileDesc* desc = sm.desc[cw];
-      auto describe = [&](int batch) {       // tiles 32 batch ..: a lane each
-        const int k = 32 * batch + lane;
-        if (k < tiles) describe_tile(c, a, sm.plan, lo, cw + kT8Conv * k, desc[k & (kT8Descs - 1)]);
-        __syncwarp();
+      // the lane's row of the four 8 x 8 matrices of a store, tile t of the step: K (rows of 64
+      // features, 16 KB on the others), V (rows: features, of 64 tokens), V of drafts (the
+      // matrices the other way round)
+      const uint32_t base = smem_u32(smem) + (op ? kT8OffV : 0);
+      auto place = [&](int t) {
+        return op ? base + (t >> 2) * 16384 + ms * 1024 + mrow * 128 + (((2 * (t & 3) + me) ^ mrow) << 4)
+                  : base + (2 * t + ms) * 1024 + mrow * 128 + ((me ^ mrow) << 4);
       };
-      // a job: K (op 0) or V of tile k
-      auto next_job = [&](int& k, int& op) {
-        if (op == 0) {
-          if (k == 0 && tiles > 1) k = 1;
-          else {
-            op = 1;
-            k = k > 0 ? k - 1 : 0;
-          }
-        } else if (k + 2 < tiles) {
-          k += 2;
-          op = 0;
-        } else {
-          k++;
-        }
-      };
-      uint8_t* ring = smem + kT8OffRing + cw * (kT8Ring * kT8Entry);
-      const uint32_t rbar = smem_u32(sm.rbar[cw]);
-      int at = 0, at_op = 0, ahead = 0, entry = 0, parity = 0, flying = 0;
-      auto issue = [&]() {                 // the next copy of codes
-        for (; at < tiles; next_job(at, at_op)) {
-          const TileDesc* d = desc + (at & (kT8Descs - 1));
-          if (d->kind > 1) continue;
-          if (lane == 0) {
-            mbar_expect_tx(rbar + 8 * ahead, kT8Entry);
-            bulk_g2s(smem_u32(ring + ahead * kT8Entry), d->src + at_op * kT8Entry, kT8Entry, rbar + 8 * ahead);
-          }
-          flying++;
-          ahead = (ahead + 1) & (kT8Ring - 1);
-          next_job(at, at_op);
-          return;
-        }
-      };
-      int described = 0;
-      if (tiles > 0) {
-        describe(0);
-        for (int e = 0; e < kT8Ring; e++) issue();
-      }
+      auto draft_place = [&](int t) { return base + (t >> 2) * 16384 + me * 1024 + mrow * 128 + (((2 * (t & 3) + ms) ^ mrow) << 4); };
+      const uint32_t full = op ? vfull(0) : kfull(0), free = op ? vfree(0) : kfree(0);
+      const uint8_t* ring = smem + kT8OffRing + op * (kT8Ring * kT8Entry) + first * kTile + 16 * lane;
+      const uint32_t rfull = smem_u32(sm.rfull[op]), rfree = smem_u32(sm.rfree[op]);
 #pragma unroll 1
-      for (int k = 0, op = 0; ok && k < tiles; next_job(k, op)) {
-        // descriptors up to 32 tiles ahead
-        if (op == 0 && 32 * (described + 1) < tiles && k >= 32 * described + 2 + 3 * cw) describe(++described);
-        const int tile = cw + kT8Conv * k, x = tile >> 2, sub = tile & 3, slot = x & (kT8Slots - 1);
-        // (the slot's phase before this one is over, too: products are issued in order, and
-        // this warp has waited for those of part x - 5 or x - 6 with its last tile)
-        if (x >= kT8Slots) ok = wait(op ? vfree(slot) : kfree(slot), x / kT8Slots - 1);
+      for (int j = 0; ok && j < steps; j++) {
+        // step -1 converts what happens to be there, so that the code is in the caches when
+        // the first codes come (cold, a step takes 4000 cycles longer)
+        const int slot = j & 1;
+        ok = wait(rfull + 8 * slot, j >> 1);         // (the descriptors are there, too)
+        if (ok && j >= kT8Slots) ok = wait(free + 8 * slot, (j >> 1) - 1);
         if (!ok) break;
-        const uint32_t base = slot0 + (op ? kT8OffV : 0) + slot * kT8Slot;
-        // the lane's row of the four 8 x 8 matrices of a store: K, V (row: feature) or V of
-        // drafts (row: feature, matrices the other way round)
-        const uint32_t k_at = base + (2 * sub + ms) * 1024 + mrow * 128 + ((me ^ mrow) << 4);
-        const uint32_t v_at = base + ms * 1024 + mrow * 128 + (((2 * sub + me) ^ mrow) << 4);
-        const TileDesc d = desc[k & (kT8Descs - 1)];
-        TileMeta meta{d.ks, d.lv, d.pos0, d.kind < 2 ? d.kind : d.kind - 1};
-        if (d.kind <= 1) {
-          ok = wait(rbar + 8 * entry, parity);
-          if (!ok) break;
-          const uint8_t* p = ring + entry * kT8Entry + 16 * lane;
-          uint4 w[4];
+        const uint32_t off = slot * kT8Slot;
+        const TileDesc* desc = sm.desc[j & (kT8Descs - 1)] + first;
 #pragma unroll
-          for (int e = 0; e < 4; e++) w[e] = *reinterpret_cast<const uint4*>(p + 512 * e);
-          flying--;
-          entry = (entry + 1) & (kT8Ring - 1);
-          parity ^= entry == 0;
-          __syncwarp();
-          issue();
+        for (int t = 0; t < 2; t++) {
+          TileDesc d = desc[t];
+          TileMeta meta{d.ks, d.lv, d.pos0, d.kind < 2 ? d.kind : d.kind - 1};
+          if (d.kind <= 1) {
+            uint4 w[4];
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const uint32_t at0 = op ? v_at + e * 4096 : (k_at + (e >> 1) * 8192) ^ ((e & 1) << 6);
-            const uint32_t at1 = op ? at0 + 2048 : at0 ^ 32u;
-            uint32_t y[4];
-            code_halves<CODE>(w[e].x, y[0], y[1]);
-            code_halves<CODE>(w[e].y, y[2], y[3]);
-            stmatrix4(at0, y[0], y[1], y[2], y[3]);
-            code_halves<CODE>(w[e].z, y[0], y[1]);
-            code_halves<CODE>(w[e].w, y[2], y[3]);
-            stmatrix4(at1, y[0], y[1], y[2], y[3]);
-          }
-        } else if (d.kind <= 3) {
-          const int i = d.req_head >> 12, h = d.req_head & 4095;
-          const bool draft = d.kind == 3;
-          const int n = min((draft ? sm.plan.M[i] : sm.plan.N[i]) - d.pos0, kSub);      // valid tokens
-          const long long first = (long long)i * a.max_nodes + d.pos0;
-          const uint8_t* ksrc = draft ? a.k + first * a.ks + h * (2 * kD) : d.src;
-          const uint8_t* vsrc = draft ? a.v + first * a.vs + h * (2 * kD) : d.src + 2 * kTile;
-          int ex = 0;
-          if (ELEM == DKV_BF16) {
-            ex = elems_exp(op ? vsrc : ksrc, op, draft, n, op ? a.vs : a.ks);
-            if (op == 0) {        // the softmax wants both with S
-              meta.ks = kLogitScale * pow2(ex);
-              meta.lv = (float)elems_exp(vsrc, true, draft, n, a.vs);
+            for (int e = 0; e < 4; e++) w[e] = *reinterpret_cast<const uint4*>(ring + slot * kT8Entry + t * kTile + 512 * e);
+            // K: 16 features on are 32 bytes of a row (swizzled); V: 2 KB
+            const uint32_t to = place(first + t) + off;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+              const uint32_t at0 = op ? to + e * 4096 : (to + (e >> 1) * 16384) ^ ((e & 1) << 6);
+              const uint32_t at1 = op ? at0 + 2048 : at0 ^ 32u;
+              uint32_t y[4];
+              code_halves<CODE>(w[e].x, y[0], y[1]);
+              code_halves<CODE>(w[e].y, y[2], y[3]);
+              stmatrix4(at0, y[0], y[1], y[2], y[3]);
+              code_halves<CODE>(w[e].z, y[0], y[1]);
+              code_halves<CODE>(w[e].w, y[2], y[3]);
+              stmatrix4(at1, y[0], y[1], y[2], y[3]);
             }
-          } else {
-            meta.lv = 0.0f;
+          } else if (d.kind <= 3) {
+            const int i = d.req_head >> 12, h = d.req_head & 4095;
+            const bool draft = d.kind == 3;
+            const int n = min((draft ? sm.plan.M[i] : sm.plan.N[i]) - d.pos0, kSub);      // valid tokens
+            const long long row0 = (long long)i * a.max_nodes + d.pos0;
+            const uint8_t* ksrc = draft ? a.k + row0 * a.ks + h * (2 * kD) : d.src;
+            const uint8_t* vsrc = draft ? a.v + row0 * a.vs + h * (2 * kD) : d.src + 2 * kTile;
+            int ex = 0;
+            if (ELEM == DKV_BF16) {
+              ex = elems_exp(op ? vsrc : ksrc, op, draft, n, op ? a.vs : a.ks);
+              if (op == 0) {        // the softmax wants both with S
+                meta.ks = kLogitScale * pow2(ex);
+                meta.lv = (float)elems_exp(vsrc, true, draft, n, a.vs);
+              }
+            } else {
+              meta.lv = 0.0f;
+            }
+            put_elems<ELEM>(op ? vsrc : ksrc, op, draft, n, op ? a.vs : a.ks, ex,
+                            (op && draft ? draft_place(first + t) : place(first + t)) + off);
           }
-          const uint32_t vt_at = base + me * 1024 + mrow * 128 + (((2 * sub + ms) ^ mrow) << 4);
-          put_elems<ELEM>(op ? vsrc : ksrc, op, draft, n, op ? a.vs : a.ks, ex, op == 0 ? k_at : draft ? vt_at : v_at);
+          if (op == 0 && lane == 0) sm.meta[j & (kT8Metas - 1)][first + t] = meta;
         }
-        if (op == 0 && lane == 0) sm.meta[x & (2 * kT8Slots - 1)][sub] = meta;
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(op ? vfull(slot) : kfull(slot));
+        if (lane == 0) {
+          mbar_arrive(full + 8 * slot);
+          mbar_arrive(rfree + 8 * slot);
+          if (j % kT8Batch == kT8Batch - 1) mbar_arrive(smem_u32(&sm.dfree[j / kT8Batch & 3]));
+        }
       }
-      if (!ok) fail();
+    } else if (warp == 17) {
+      // ---- where the tiles lie and what scales them, a lane a tile, a batch of steps at a
+      // time (at most four are kept) ----
+      const int batches = (steps + kT8Batch - 1) / kT8Batch;
+#pragma unroll 1
+      for (int b = 0; ok && b < batches; b++) {
+        const float2* scales = nullptr;
+        TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4};
+        const int x = kT8Step * kT8Batch * b + lane;
+        if (x < kT8Step * steps) d = describe_tile(c, a, sm.plan, lo, x, scales);
+        if (d.kind == 2)           // read without a copy
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(d.src), "r"(4 * kTile) : "memory");
+        if (scales) {
+          const float2 sc = *scales;
+          d.ks = sc.x * kLogitScale;
+          d.lv = log2f(sc.y);
+        }
+        if (b >= 4) ok = wait(smem_u32(&sm.dfree[b & 3]), (b >> 2) - 1);
+        if (!ok) break;
+        sm.desc[(kT8Batch * b + lane / kT8Step) & (kT8Descs - 1)][lane % kT8Step] = d;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.dfull[b & 3]));
+      }
+    } else if (warp >= 18) {
+      // ---- copies of codes ----
+      const int op = warp - 18;
+      const uint32_t ring = smem_u32(smem + kT8OffRing + op * (kT8Ring * kT8Entry));
+      int issued = 0;
+#pragma unroll 1
+      for (int j = 0; ok && j < steps; j++) {
+        if (j % kT8Batch == 0) ok = wait(smem_u32(&sm.dfull[j / kT8Batch & 3]), j / kT8Batch >> 2);
+        if (ok && j >= kT8Ring) ok = wait(smem_u32(&sm.rfree[op][j & 1]), (j >> 1) - 1);
+        if (!ok) break;
+        const TileDesc* d = &sm.desc[j & (kT8Descs - 1)][lane & (kT8Step - 1)];
+        const unsigned who = __ballot_sync(0xffffffffu, lane < kT8Step && d->kind <= 1);
+        const unsigned long long src = reinterpret_cast<unsigned long long>(d->src) + op * kTile;
+        const uint32_t bar = smem_u32(&sm.rfull[op][j & 1]), dst = ring + (j & 1) * kT8Entry;
+        if (lane == 0) {
+          if (who) mbar_expect_tx(bar, __popc(who) * kTile);
+          else mbar_arrive(bar);
+          if (j % kT8Batch == kT8Batch - 1) mbar_arrive(smem_u32(&sm.dfree[j / kT8Batch & 3]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < kT8Step; t++) {
+          const unsigned long long p = __shfl_sync(0xffffffffu, src, t);
+          if (who >> t & 1u)
+            if (elected()) bulk_g2s(dst + t * kTile, reinterpret_cast<const void*>(p), kTile, bar);
+        }
+        issued = j + 1;
+      }
       // no copy may be in flight at the exit
-      for (; flying > 0; flying--) {
-        wait_long(rbar + 8 * entry, parity);
-        entry = (entry + 1) & (kT8Ring - 1);
-        parity ^= entry == 0;
-      }
-    } else {
+      for (int j = max(issued - kT8Ring, 0); j < issued; j++) mbar_wait_bounded(smem_u32(&sm.rfull[op][j & 1]), j >> 1 & 1);
+    } else if (warp == 16) {
       // ---- products: S of the steps to come, O += P V; the whole warp walks, one lane
       // issues (counters, so that operands stay in uniform registers). Products run in the
       // order of their issue, so S may follow the P V that read its place ----
-      constexpr uint32_t id_s = umma_idesc_f16(128, 64), id_pv = umma_idesc_f16(128, 128);
+      constexpr uint32_t id_half = umma_idesc_f16(128, 64), id = umma_idesc_f16(128, 128);
       const uint64_t kd = umma_desc_sw128(smem_u32(smem)), vd = umma_desc_sw128(smem_u32(smem + kT8OffV));
       auto test = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0; };
       auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-      // the part of the sequence that S and that P V are in: its last step, the tiles of that
-      struct Run {
-        int pos, end, rest, item;
-      };
-      auto next_run = [&](Run& r) {
-        const TreeItem it = tree_item(c, a, sm.plan, lo + r.pos, hi);
-        r.end = uniform(r.pos + it.n);
-        r.rest = uniform(min(kT8Step, it.tiles.count - kT8Step * (it.s0 + it.n - 1)));
-        r.item++;
-      };
-      Run rs{0, 0, 0, -1}, rv{0, 0, 0, -1};
+      // S walks the items; their ends and the tiles of their last steps are kept for P V, which
+      // is at most two items behind
+      int s_end = 0, s_rest = 0, item = -1, v_end = 0, v_rest = 0, v_item = -1;
       int js = 0, jv = 0;              // next step of S, of P V
       bool begin = true, q_there = false;
-      next_run(rs);
-      next_run(rv);
-      const int steps = uniform(hi - lo);
-      int idle = 0;
+      const int last = uniform(steps);
+      int s_slot = 0, s_round = 0, v_slot = 0, v_round = 0, idle = 0;
+      auto next_slot = [](int& slot, int& round) {
+        if (++slot == kT8Slots) {
+          slot = 0;
+          round ^= 1;
+        }
+      };
       long long since = 0;
 #pragma unroll 1
-      while (jv < steps) {
+      while (jv < last) {
         bool none = true;
-        if (js < steps && js < jv + 2) {
-          if (!q_there) q_there = test(qfull(rs.item & 1), rs.item >> 1);
-          const int x = 2 * js, s0 = x & (kT8Slots - 1), phase = x / kT8Slots;
-          if (q_there && test(kfull(s0), phase) && test(kfull(s0 + 1), phase)) {
+        if (js < last && js < jv + 2) {
+          if (js == s_end) {
+            const TreeItem it = tree_item(c, a, sm.plan, lo + js, hi);
+            s_end = js + uniform(it.n);
+            s_rest = uniform(min(kT8Step, it.tiles.count - kT8Step * (it.s0 + it.n - 1)));
+            item++;
+            q_there = false;
+            if (lane == 0) sm.runs[item & 3] = make_int2(s_end, s_rest);
+            __syncwarp();
+          }
+          if (!q_there) q_there = test(qfull(item & 1), item >> 1);
+          if (q_there && test(kfull(s_slot), s_round)) {
             tc_fence_after();
-            const uint32_t d = uniform(t_s(js & 1)), q = uniform(t_q(rs.item & 1));
-            const int two = uniform(js < rs.end - 1 || rs.rest > 4), at = uniform(s0 * (kT8Slot >> 4));
+            const uint32_t d = uniform(t_s(js & 1)), q = uniform(t_q(item & 1));
+            const uint32_t kind = uniform(js < s_end - 1 || s_rest > 4 ? id : id_half);
+            const int at = uniform(s_slot * (kT8Slot >> 4)), bar_s = uniform(sfull(js & 1)), bar_k = uniform(kfree(s_slot));
             if (elected()) {
               const uint64_t bd = kd + at;
 #pragma unroll
               for (int e = 0; e < 8; e++)
-                umma_f16_tmem_a(d, q + 8 * e, bd + (((e >> 2) * 8192 + (e & 3) * 32) >> 4), id_s, e > 0);
-              if (two) {
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                  umma_f16_tmem_a(d + 64, q + 8 * e, bd + ((kT8Slot + (e >> 2) * 8192 + (e & 3) * 32) >> 4), id_s, e > 0);
-              }
-              umma_commit(sfull(js & 1));
-              umma_commit(kfree(s0));
-              umma_commit(kfree(s0 + 1));
+                umma_f16_tmem_a(d, q + 8 * e, bd + (((e >> 2) * 16384 + (e & 3) * 32) >> 4), kind, e > 0);
+              umma_commit(bar_s);
+              umma_commit(bar_k);
             }
             __syncwarp();
-            if (++js == rs.end && js < steps) {
-              rs.pos = js;
-              next_run(rs);
-              q_there = false;
-            }
+            next_slot(s_slot, s_round);
+            js++;
             none = false;
           }
         }
-        if (jv < js) {
-          const int x = 2 * jv, s0 = x & (kT8Slots - 1), phase = x / kT8Slots;
-          if (test(pfull(jv & 1), jv >> 1) && test(vfull(s0), phase) && test(vfull(s0 + 1), phase)) {
-            tc_fence_after();
-            const uint32_t p = uniform(t_s(jv & 1));
-            const int n = uniform(jv < rv.end - 1 ? kT8Step : rv.rest), go_on = uniform(!begin), at = uniform(s0 * (kT8Slot >> 4));
-            if (elected()) {
-              const uint64_t bd = vd + at;
+        if (jv < js && jv == v_end) {
+          const int2 run = sm.runs[++v_item & 3];
+          v_end = uniform(run.x);
+          v_rest = uniform(run.y);
+          begin = true;
+        }
+        if (jv < js && test(pfull(jv & 1), jv >> 1) && test(vfull(v_slot), v_round)) {
+          tc_fence_after();
+          const uint32_t p = uniform(t_s(jv & 1));
+          const int n = uniform(jv < v_end - 1 ? kT8Step : v_rest), go_on = uniform(!begin), at = uniform(v_slot * (kT8Slot >> 4));
+          const int bar_pv = uniform(pvdone(jv & 1)), bar_v = uniform(vfree(v_slot));
+          if (elected()) {
+            const uint64_t bd = vd + at;
 #pragma unroll
-              for (int e = 0; e < kT8Step; e++)
-                if (e < n)
-                  umma_f16_tmem_a(t_o, p + 64 * (e >> 2) + 8 * (e & 3), bd + (((e >> 2) * kT8Slot + (e & 3) * 32) >> 4), id_pv,
-                                  go_on || e > 0);
-              umma_commit(pvdone(jv & 1));
-              umma_commit(vfree(s0));
-              umma_commit(vfree(s0 + 1));
-            }
-            __syncwarp();
-            begin = false;
-            if (++jv == rv.end && jv < steps) {
-              rv.pos = jv;
-              next_run(rv);
-              begin = true;
-            }
-            none = false;
+            for (int e = 0; e < kT8Step; e++)
+              if (e < n)
+                umma_f16_tmem_a(t_o, p + 64 * (e >> 2) + 8 * (e & 3), bd + (((e >> 2) * 16384 + (e & 3) * 32) >> 4), id, go_on || e > 0);
+            umma_commit(bar_pv);
+            umma_commit(bar_v);
           }
+          __syncwarp();
+          next_slot(v_slot, v_round);
+          begin = false;
+          jv++;
+          none = false;
         }
         // bounded: about a second without anything to issue
         if (!none) idle = 0;
         else if (++idle == 1) since = clock64();
         else if ((idle & 1023) == 0 && __any_sync(0xffffffffu, *(volatile int*)&sm.fail != 0 || clock64() - since > 2000000000LL)) {
+          *(volatile int*)&sm.fail = 1;
           ok = false;
           break;
         }
       }
-      if (!ok) fail();
       if (elected()) {
         umma_commit(drain);                // every MMA issued so far has completed
         mbar_wait_bounded(drain, 0);
@@ -1090,35 +1108,37 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8 + kT8Conv) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
+    if (lane == 0 && sm.fail) c.latch(DKV_ERR_TIMEOUT, -1);
   }
 }
 
 // ---- rows of units that several CTAs hold parts of, and rows that came out infinite or
-// NaN: a warp a row ----
+// NaN: a warp a row. (Few registers, so that every row's loads are in flight: walks, which
+// are seldom, spill.) ----
 template <int ELEM, int CODE>
-__global__ void __launch_bounds__(32 * kT8Walkers) k_tree8_join(Cache8View c, Tree8Args a, int part_rows, int main_grid) {
-  __shared__ TreePlan plan;
-  __shared__ int scan[32];
+__global__ void __launch_bounds__(32 * kT8Walkers, 5) k_tree8_join(const __grid_constant__ Cache8View c, const __grid_constant__ Tree8Args a,
+                                                                   int part_rows, const int* plan, int main_grid) {
   pdl_launch_dependents();
-  pdl_wait();
-  if (c.stopped()) return;
-  const int total = make_plan(c, a, plan, scan);
-  if (total == 0) return;
-  const int ctas = tree_ctas(total, main_grid);
   const int lane = threadIdx.x & 31, G = c.G, hq = c.hkv * G;
-  const long long rows = (long long)a.n_req * a.max_nodes * hq;
+  const unsigned rows = (unsigned)a.n_req * a.max_nodes * hq;
+  pdl_wait();
+  // (an error of this call or an earlier one: results are undefined)
+  const int total = plan[a.n_req];
+  if (*(volatile int*)c.status != 0 || total == 0) return;
+  const int ctas = tree_ctas(total, main_grid);
 #pragma unroll 1
-  for (long long x = (long long)blockIdx.x * kT8Walkers + (threadIdx.x >> 5); x < rows; x += (long long)gridDim.x * kT8Walkers) {
-    const int q = (int)(x % hq), y = (int)(x / hq), i = y / a.max_nodes, m = y - i * a.max_nodes, h = q / G;
-    const TreeReq req{plan.N[i], plan.M[i], plan.slot[i]};
+  for (unsigned x = blockIdx.x * kT8Walkers + (threadIdx.x >> 5); x < rows; x += gridDim.x * kT8Walkers) {
+    const int q = x % hq, y = x / hq, i = y / a.max_nodes, m = y - i * a.max_nodes, h = q / G;
+    const int first = plan[i];
+    const TreeReq req = tree_req(c, a, i);
     if (m >= req.M) continue;
-    uint8_t* out = a.out + x * (2 * kD);
+    uint8_t* out = a.out + (size_t)x * (2 * kD);
     const TreeTiles tiles = tree_tiles(req.N, req.M, c.T, a.window, a.sinks);
     const int per = (tiles.count + kT8Step - 1) / kT8Step, row = m * G + (q - h * G), t = row / kT8Rows, r = row - t * kT8Rows;
-    const int us = plan.pre[i] + (h * unit_rows(req.M, G) + t) * per;
+    const int us = first + (h * unit_rows(req.M, G) + t) * per;
     const int c0 = range_of(total, us, ctas), c1 = range_of(total, us + per - 1, ctas);
     uint2 w;
     uint32_t bad = 0;
@@ -1126,11 +1146,14 @@ __global__ void __launch_bounds__(32 * kT8Walkers) k_tree8_join(Cache8View c, Tr
       w = *reinterpret_cast<const uint2*>(out + 8 * lane);
     } else {
       // the first part begins its unit (place 1), the others go on with it (place 0)
-      auto part = [&](int cta) { return a.part + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * part_rows * (kD + 2); };
+      const float4* parts = reinterpret_cast<const float4*>(a.part);
+      const size_t place = (size_t)part_rows * (kD + 2) / 4;
+      auto part = [&](int cta) { return parts + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * place; };
+      auto weight_of = [&](int cta) { return reinterpret_cast<const float2*>(part(cta) + part_rows * (kD / 4))[r]; };
       float top = -INFINITY, sum = 0.0f;
       for (int b = c0; b <= c1; b += 32) {
         float2 ul = make_float2(-INFINITY, 0.0f);
-        if (b + lane <= c1) ul = reinterpret_cast<const float2*>(part(b + lane) + part_rows * kD)[r];
+        if (b + lane <= c1) ul = weight_of(b + lane);
         float now = ul.x;
 #pragma unroll
         for (int d = 16; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
@@ -1145,13 +1168,13 @@ __global__ void __launch_bounds__(32 * kT8Walkers) k_tree8_join(Cache8View c, Tr
       for (int b = c0; b <= c1; b += 32) {
         float f = 0.0f;
         if (b + lane <= c1) {
-          const float2 ul = reinterpret_cast<const float2*>(part(b + lane) + part_rows * kD)[r];
+          const float2 ul = weight_of(b + lane);
           f = ul.y == 0.0f ? 0.0f : __fdiv_rn(ul.y * (ul.x == top ? 1.0f : fast_exp2(ul.x - top)), sum);
         }
         const int n = min(c1 - b + 1, 32);
-#pragma unroll 4
+#pragma unroll 2
         for (int e = 0; e < n; e++) {
-          const float4 v = reinterpret_cast<const float4*>(part(b + e))[lane * part_rows + r];
+          const float4 v = part(b + e)[lane * part_rows + r];
           const float fe = __shfl_sync(0xffffffffu, f, e);
           o.x = fmaf(v.x, fe, o.x);
           o.y = fmaf(v.y, fe, o.y);
@@ -1173,26 +1196,31 @@ __global__ void __launch_bounds__(32 * kT8Walkers) k_tree8_join(Cache8View c, Tr
 
 int part_rows_of(int G, int max_nodes) { return std::min(kT8Rows, (max_nodes * G + 31) / 32 * 32); }
 
+// The workspace: the plan's prefix sums, then two parts a CTA.
+constexpr size_t kT8PlanBytes = ((kMaxCallReq + 1) * 4 + 255) / 256 * 256;
+
 template <int ELEM, int CODE>
-cudaError_t tree_typed(const Cache8View& c, const Tree8Args& a, int sm_count, cudaStream_t st) {
+cudaError_t tree_typed(const Cache8View& c, Tree8Args a, int sm_count, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(k_tree8<ELEM, CODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kT8Smem);
   if (e != cudaSuccess) return e;
   const int part_rows = part_rows_of(c.G, a.max_nodes);
+  int* plan = reinterpret_cast<int*>(a.part);
+  a.part += kT8PlanBytes / 4;
   // no more CTAs than the longest lengths that the table holds could use
   const long long tiles = ((long long)c.width * c.T + a.max_nodes) / kSub + 3;
   const long long steps = (long long)a.n_req * c.hkv * ((a.max_nodes * c.G + kT8Rows - 1) / kT8Rows) * (tiles / kT8Step + 1);
   const int grid = (int)std::min<long long>(sm_count, (steps + kT8Least - 1) / kT8Least);
-  e = launch_dependent(k_tree8<ELEM, CODE>, dim3(grid), dim3(kT8Threads), kT8Smem, st, c, a, part_rows);
+  e = launch_dependent(k_tree8<ELEM, CODE>, dim3(grid), dim3(kT8Threads), kT8Smem, st, c, a, part_rows, plan);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)a.n_req * a.max_nodes * c.hkv * c.G;
-  const int blocks = (int)std::min<long long>((rows + kT8Walkers - 1) / kT8Walkers, (long long)sm_count * 6);
-  return launch_dependent(k_tree8_join<ELEM, CODE>, dim3(blocks), dim3(32 * kT8Walkers), 0, st, c, a, part_rows, grid);
+  const int blocks = (int)std::min<long long>((rows + kT8Walkers - 1) / kT8Walkers, (long long)sm_count * 20);
+  return launch_dependent(k_tree8_join<ELEM, CODE>, dim3(blocks), dim3(32 * kT8Walkers), 0, st, c, a, part_rows, plan, grid);
 }
 
 }  // namespace
 
 size_t tree8_workspace(int G, int max_nodes, int sm_count) {
-  return (size_t)sm_count * 2 * part_rows_of(G, max_nodes) * (kD + 2) * 4;
+  return kT8PlanBytes + (size_t)sm_count * 2 * part_rows_of(G, max_nodes) * (kD + 2) * 4;
 }
 
 cudaError_t launch_tree8(const Cache8View& c, int elem, int code, int sm_count, const Tree8Args& a, cudaStream_t st) {
