@@ -51,9 +51,12 @@ __device__ __forceinline__ TreeReq tree_req(const Cache8View& c, const Tree8Args
 
 // The 16-token tiles of a request in order: stored ones [0, head) and [win, end) of
 // which those from `full` on lie in the tail, then the drafts; `count` in all. A stored tile
-// is left out if no node of any depth sees a token of it.
+// is left out if no node of any depth sees a token of it. In the steps of the kernel below a
+// tile of 16-bit values takes two places (its copies need twice the room): places [0, codes)
+// hold the tiles of codes, which come first, those from `elems` on the others, every second one.
 struct TreeTiles {
   int head, win, end, full, stored, count;
+  int codes, elems, places;
   __device__ __forceinline__ int tile(int x) const { return x < head ? x : x - head + win; }
 };
 __device__ __forceinline__ TreeTiles tree_tiles(int N, int M, int T, int window, int sinks) {
@@ -69,6 +72,9 @@ __device__ __forceinline__ TreeTiles tree_tiles(int N, int M, int T, int window,
   }
   t.stored = t.head + t.end - t.win;
   t.count = t.stored + (M + kSub - 1) / kSub;
+  t.codes = t.full > t.win ? t.head + t.full - t.win : min(t.head, t.full);
+  t.elems = (t.codes + 1) & ~1;
+  t.places = t.elems + 2 * (t.count - t.codes);
   return t;
 }
 
@@ -325,7 +331,7 @@ __device__ __forceinline__ int make_plan(const Cache8View& c, const Tree8Args& a
       p.slot[i] = r.slot;
       if (r.M > 0) {
         const TreeTiles t = tree_tiles(r.N, r.M, c.T, a.window, a.sinks);
-        cost = c.hkv * unit_rows(r.M, c.G) * ((t.count + kT8Step - 1) / kT8Step);
+        cost = c.hkv * unit_rows(r.M, c.G) * ((t.places + kT8Step - 1) / kT8Step);
       }
     }
     int x = cost;
@@ -366,7 +372,7 @@ __device__ __forceinline__ TreeItem tree_item(const Cache8View& c, const Tree8Ar
   it.M = p.M[i];
   it.slot = p.slot[i];
   it.tiles = tree_tiles(it.N, it.M, c.T, a.window, a.sinks);
-  it.per = (it.tiles.count + kT8Step - 1) / kT8Step;
+  it.per = (it.tiles.places + kT8Step - 1) / kT8Step;
   const int x = pos - p.pre[i], unit = x / it.per, rt = unit_rows(it.M, c.G);
   it.s0 = x - unit * it.per;
   it.h = unit / rt;
@@ -375,16 +381,18 @@ __device__ __forceinline__ TreeItem tree_item(const Cache8View& c, const Tree8Ar
   return it;
 }
 
-// What a converting warp knows of one of its tiles. kind: of codes, of which every
-// node sees every token (0) or not (1), of the tail (2), drafts (3), none (4).
+// What is known of a tile. kind: of codes, of which every node sees every token (0) or not
+// (1), of the tail (2), drafts (3), none (4).
 struct TileDesc {
-  const uint8_t* src;
+  const uint8_t* src;       // (drafts: K)
   float ks;
   union {
     float lv;       // log2 of V's scale
-    int req_head;   // kinds 2 and 3: request << 12 | KV head
+    int req_head;   // kinds 2 and 3, until they are looked through: request << 12 | KV head
   };
   int pos0, kind;   // first token, first draft
+  int n, exps;      // kinds 2 and 3: valid tokens; exponents of the powers of two that K and V are divided by (K's in the lower half)
+  const uint8_t* vsrc;
 };
 // What the softmax has to know of it. kind: seen by all (0), stored (1), drafts (2), none (3).
 struct TileMeta {
@@ -394,15 +402,17 @@ struct TileMeta {
 
 struct TreeSmem {
   TileDesc desc[kT8Descs][kT8Step];
+  unsigned there[2 * kT8Descs];        // places of a step that hold a tile (the products are behind the conversion)
   TileMeta meta[kT8Metas][kT8Step];    // (K of step j comes when the softmax has read that of step j - 5)
   TreePlan plan;
   int parents[kMaxNodes];
   float2 pair[2][2][kT8Rows];      // what the two warps of a row tell each other
   int scan[32];
-  int2 runs[4];                    // ends of items of the products, the tiles of their last steps
+  int runs[4];                     // ends of items of the products
   // K, V of a step there, no longer needed; S, P, P V of a step there, queries there (two of
-  // each); drain
-  uint64_t bar[4 * kT8Slots + 9];
+  // each, of P V four: a wait is for the last of them, the one before in its place long over);
+  // drain
+  uint64_t bar[4 * kT8Slots + 11];
   uint64_t rfull[2][kT8Ring], rfree[2][kT8Ring];      // copies of K, of V codes
   uint64_t dfull[4], dfree[4];     // batches of descriptors
   uint32_t taddr;
@@ -445,36 +455,38 @@ __device__ __forceinline__ bool elected() {
   return p != 0;
 }
 
-// Tile x of a CTA whose range begins at step lo, but for its page's scales.
+// Place x of a CTA whose range begins at step lo, but for its page's scales.
 __device__ __forceinline__ TileDesc describe_tile(const Cache8View& c, const Tree8Args& a, const TreePlan& plan, int lo, int x,
                                                   const float2*& scales) {
   const int pos = lo + x / kT8Step;
   const TreeItem it = tree_item(c, a, plan, pos, pos + 1);
   x = kT8Step * it.s0 + x % kT8Step;
-  TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4};
-  if (x < it.tiles.stored) {
-    const int tile = it.tiles.tile(x);
+  TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4, 0, 0, nullptr};
+  if (x < it.tiles.codes) {
+    const int tile = it.tiles.tile(x), per = __ffs(c.T) - 5;      // log2 of a block's tiles
     d.pos0 = tile * kSub;
-    if (tile < it.tiles.full) {
-      const int per = __ffs(c.T) - 5;      // log2 of a block's tiles
-      int page = c.table[(size_t)it.slot * c.width + (tile >> per)];
-      if ((unsigned)page >= (unsigned)c.n_pages) {
-        c.latch(DKV_ERR_CHECK, it.i);
-        page = 0;
-      }
-      scales = reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * c.hkv + it.h));
-      d.src = c.pages + c.page_head(page, it.h) + (size_t)(tile & ((1 << per) - 1)) * (2 * kTile);
-      // every depth sees all of it
-      d.kind = a.window <= 0 || d.pos0 >= it.N + it.M - a.window || d.pos0 + kSub <= a.sinks ? 0 : 1;
-    } else {
-      d.src = c.tail + c.tail_head(it.slot, it.h) + (size_t)(tile - it.tiles.full) * (4 * kTile);
-      d.req_head = it.i << 12 | it.h;
-      d.kind = 2;
+    int page = c.table[(size_t)it.slot * c.width + (tile >> per)];
+    if ((unsigned)page >= (unsigned)c.n_pages) {
+      c.latch(DKV_ERR_CHECK, it.i);
+      page = 0;
     }
-  } else if (x < it.tiles.count) {
-    d.pos0 = (x - it.tiles.stored) * kSub;
+    scales = reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * c.hkv + it.h));
+    d.src = c.pages + c.page_head(page, it.h) + (size_t)(tile & ((1 << per) - 1)) * (2 * kTile);
+    // every depth sees all of it
+    d.kind = a.window <= 0 || d.pos0 >= it.N + it.M - a.window || d.pos0 + kSub <= a.sinks ? 0 : 1;
+  } else if (x >= it.tiles.elems && (x & 1) == 0) {
+    x = it.tiles.codes + ((x - it.tiles.elems) >> 1);
     d.req_head = it.i << 12 | it.h;
-    d.kind = 3;
+    if (x < it.tiles.stored) {
+      const int tile = it.tiles.tile(x);
+      d.pos0 = tile * kSub;
+      d.src = c.tail + c.tail_head(it.slot, it.h) + (size_t)(tile - it.tiles.full) * (4 * kTile);
+      d.kind = 2;
+    } else if (x < it.tiles.count) {
+      d.pos0 = (x - it.tiles.stored) * kSub;
+      d.src = a.k + ((long long)it.i * a.max_nodes + d.pos0) * a.ks + it.h * (2 * kD);
+      d.kind = 3;
+    }
   }
   return d;
 }
@@ -552,7 +564,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   auto pfull = [&](int s) { return b0 + 8u * (4 * kT8Slots + 2 + s); };
   auto qfull = [&](int s) { return b0 + 8u * (4 * kT8Slots + 4 + s); };
   auto pvdone = [&](int s) { return b0 + 8u * (4 * kT8Slots + 6 + s); };
-  const uint32_t drain = b0 + 8u * (4 * kT8Slots + 8);
+  const uint32_t drain = b0 + 8u * (4 * kT8Slots + 10);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kT8Slots; s++) {
       mbar_init(kfull(s), 4);
@@ -564,8 +576,8 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       mbar_init(sfull(s), 1);
       mbar_init(pfull(s), 8);
       mbar_init(qfull(s), 8);
-      mbar_init(pvdone(s), 1);
     }
+    for (int s = 0; s < 4; s++) mbar_init(pvdone(s), 1);
     mbar_init(drain, 1);
     for (int s = 0; s < 4; s++) {
       mbar_init(smem_u32(&sm.dfull[s]), 1);
@@ -703,7 +715,6 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         // (after a wait that gave up the warps walk on, through the same barriers)
         // (step -1, ahead of the first: the code comes to the caches, nothing is stored)
         ok = wait(sfull(j & 1), j >> 1) && ok;
-        if (j > 1) ok = wait(pvdone(j & 1), (j >> 1) - 1) && ok;      // long since: its phases are seen in turn
         tc_fence_after();
         if (busy) {
           float s[64];
@@ -763,7 +774,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
               const float nu = fmaxf(u, fmaxf(yt, other.x)), nm = fmaxf(mx, fmaxf(xt, other.y));
               l *= nu == -INFINITY ? 1.0f : fast_exp2(u - nu);
               if (!first) {        // O is still once the last product is done
-                ok = wait(pvdone((j - 1) & 1), (j - 1) >> 1) && ok;
+                ok = wait(pvdone((j - 1) & 3), (j - 1) >> 2) && ok;
                 tc_fence_after();
                 const float fo = nm == -INFINITY ? 1.0f : fast_exp2(mx - nm);
 #pragma unroll 1
@@ -807,14 +818,17 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
               const float back = up + ur;
               sum = fmaf(tile, fast_exp2(-back), sum);
               fits = fits && tile <= kT8Most;
-              far = far || !(fabsf(back) <= kT8Far);
+              far = far || !(fabsf(back) <= kT8Far);      // (these rows take the longer way every time)
             }
-            if (__any_sync(0xffffffffu, real && far)) {
-              sum = 0.0f;
+            if (again) {
+              if (__any_sync(0xffffffffu, real && far)) {
+                sum = 0.0f;
 #pragma unroll
-              for (int e = 0; e < 64; e++) sum += fast_exp2(fmaf(s[e], f[e >> 4], -ur));
+                for (int e = 0; e < 64; e++) sum += fast_exp2(fmaf(s[e], f[e >> 4], -ur));
+              }
+              break;
             }
-            if (again || named_all(pair_bar, 64, fits || !real)) break;
+            if (named_all(pair_bar, 64, (fits && !far) || !real)) break;
           }
           l += sum;
           tmem_st32(ts, p);
@@ -827,7 +841,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       }
       // the next item's queries ahead of this one's results
       if (pos < hi) scale = put_row(then, item + 1);
-      ok = wait(pvdone((end - 1) & 1), (end - 1) >> 1) && ok;
+      ok = wait(pvdone((end - 1) & 3), (end - 1) >> 2) && ok;
       if (busy) {
         tc_fence_after();
         sm.pair[told][part][r].x = l;
@@ -892,7 +906,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       };
       auto draft_place = [&](int t) { return base + (t >> 2) * 16384 + me * 1024 + mrow * 128 + (((2 * (t & 3) + ms) ^ mrow) << 4); };
       const uint32_t full = op ? vfull(0) : kfull(0), free = op ? vfree(0) : kfree(0);
-      const uint8_t* ring = smem + kT8OffRing + op * (kT8Ring * kT8Entry) + first * kTile + 16 * lane;
+      const uint8_t* ring = smem + kT8OffRing + op * (kT8Ring * kT8Entry) + first * kTile;
       const uint32_t rfull = smem_u32(sm.rfull[op]), rfree = smem_u32(sm.rfree[op]);
 #pragma unroll 1
       for (int j = 0; ok && j < steps; j++) {
@@ -902,51 +916,42 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         ok = wait(rfull + 8 * slot, j >> 1);         // (the descriptors are there, too)
         if (ok && j >= kT8Slots) ok = wait(free + 8 * slot, (j >> 1) - 1);
         if (!ok) break;
-        const uint32_t off = slot * kT8Slot;
+        const uint32_t to0 = place(first) + slot * kT8Slot, to1 = place(first + 1) + slot * kT8Slot;
         const TileDesc* desc = sm.desc[j & (kT8Descs - 1)] + first;
+        const int kind = desc->kind;
+        if (kind == 2 || kind == 3) {
+          // (the second place is none)
+          const TileDesc d = desc[0];
+          const bool draft = kind == 3;
+          put_elems<ELEM>(ring + slot * kT8Entry, op, draft, d.n, 2 * kD, op ? d.exps >> 16 : (int)(short)d.exps,
+                          op && draft ? draft_place(first) + slot * kT8Slot : to0);
+        } else {
 #pragma unroll
-        for (int t = 0; t < 2; t++) {
-          TileDesc d = desc[t];
-          TileMeta meta{d.ks, d.lv, d.pos0, d.kind < 2 ? d.kind : d.kind - 1};
-          if (d.kind <= 1) {
-            uint4 w[4];
+          for (int t = 0; t < 2; t++)
+            if (desc[t].kind <= 1) {
+              const uint8_t* p = ring + slot * kT8Entry + t * kTile + 16 * lane;
+              uint4 w[4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) w[e] = *reinterpret_cast<const uint4*>(ring + slot * kT8Entry + t * kTile + 512 * e);
-            // K: 16 features on are 32 bytes of a row (swizzled); V: 2 KB
-            const uint32_t to = place(first + t) + off;
+              for (int e = 0; e < 4; e++) w[e] = *reinterpret_cast<const uint4*>(p + 512 * e);
+              // K: 16 features on are 32 bytes of a row (swizzled); V: 2 KB
+              const uint32_t to = t ? to1 : to0;
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-              const uint32_t at0 = op ? to + e * 4096 : (to + (e >> 1) * 16384) ^ ((e & 1) << 6);
-              const uint32_t at1 = op ? at0 + 2048 : at0 ^ 32u;
-              uint32_t y[4];
-              code_halves<CODE>(w[e].x, y[0], y[1]);
-              code_halves<CODE>(w[e].y, y[2], y[3]);
-              stmatrix4(at0, y[0], y[1], y[2], y[3]);
-              code_halves<CODE>(w[e].z, y[0], y[1]);
-              code_halves<CODE>(w[e].w, y[2], y[3]);
-              stmatrix4(at1, y[0], y[1], y[2], y[3]);
-            }
-          } else if (d.kind <= 3) {
-            const int i = d.req_head >> 12, h = d.req_head & 4095;
-            const bool draft = d.kind == 3;
-            const int n = min((draft ? sm.plan.M[i] : sm.plan.N[i]) - d.pos0, kSub);      // valid tokens
-            const long long row0 = (long long)i * a.max_nodes + d.pos0;
-            const uint8_t* ksrc = draft ? a.k + row0 * a.ks + h * (2 * kD) : d.src;
-            const uint8_t* vsrc = draft ? a.v + row0 * a.vs + h * (2 * kD) : d.src + 2 * kTile;
-            int ex = 0;
-            if (ELEM == DKV_BF16) {
-              ex = elems_exp(op ? vsrc : ksrc, op, draft, n, op ? a.vs : a.ks);
-              if (op == 0) {        // the softmax wants both with S
-                meta.ks = kLogitScale * pow2(ex);
-                meta.lv = (float)elems_exp(vsrc, true, draft, n, a.vs);
+              for (int e = 0; e < 4; e++) {
+                const uint32_t at0 = op ? to + e * 4096 : (to + (e >> 1) * 16384) ^ ((e & 1) << 6);
+                const uint32_t at1 = op ? at0 + 2048 : at0 ^ 32u;
+                uint32_t y[4];
+                code_halves<CODE>(w[e].x, y[0], y[1]);
+                code_halves<CODE>(w[e].y, y[2], y[3]);
+                stmatrix4(at0, y[0], y[1], y[2], y[3]);
+                code_halves<CODE>(w[e].z, y[0], y[1]);
+                code_halves<CODE>(w[e].w, y[2], y[3]);
+                stmatrix4(at1, y[0], y[1], y[2], y[3]);
               }
-            } else {
-              meta.lv = 0.0f;
             }
-            put_elems<ELEM>(op ? vsrc : ksrc, op, draft, n, op ? a.vs : a.ks, ex,
-                            (op && draft ? draft_place(first + t) : place(first + t)) + off);
-          }
-          if (op == 0 && lane == 0) sm.meta[j & (kT8Metas - 1)][first + t] = meta;
+        }
+        if (op == 0 && lane < 2) {
+          const TileDesc* d = desc + lane;
+          sm.meta[j & (kT8Metas - 1)][first + lane] = TileMeta{d->ks, d->lv, d->pos0, d->kind < 2 ? d->kind : d->kind - 1};
         }
         fence_proxy_async();
         __syncwarp();
@@ -963,19 +968,44 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
 #pragma unroll 1
       for (int b = 0; ok && b < batches; b++) {
         const float2* scales = nullptr;
-        TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4};
+        TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4, 0, 0, nullptr};
         const int x = kT8Step * kT8Batch * b + lane;
         if (x < kT8Step * steps) d = describe_tile(c, a, sm.plan, lo, x, scales);
-        if (d.kind == 2)           // read without a copy
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(d.src), "r"(4 * kTile) : "memory");
         if (scales) {
           const float2 sc = *scales;
           d.ks = sc.x * kLogitScale;
           d.lv = log2f(sc.y);
         }
+        // tiles of the tail and drafts: bf16 ones are looked through for their largest values
+        const bool elems = d.kind == 2 || d.kind == 3;
+        if (elems) {
+          const int i = d.req_head >> 12, h = d.req_head & 4095;
+          d.n = min((d.kind == 2 ? sm.plan.N[i] : sm.plan.M[i]) - d.pos0, kSub);
+          d.vsrc = d.kind == 2 ? d.src + 2 * kTile : a.v + ((long long)i * a.max_nodes + d.pos0) * a.vs + h * (2 * kD);
+          d.lv = 0.0f;
+        }
+        if (ELEM == DKV_BF16) {
+          for (unsigned left = __ballot_sync(0xffffffffu, elems); left; left &= left - 1) {
+            const int who = __ffs(left) - 1;
+            const unsigned long long ks = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(d.src), who);
+            const unsigned long long vs = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(d.vsrc), who);
+            const int n = __shfl_sync(0xffffffffu, d.n, who);
+            const bool draft = __shfl_sync(0xffffffffu, d.kind, who) == 3;
+            const int ek = elems_exp(reinterpret_cast<const uint8_t*>(ks), false, draft, n, a.ks);
+            const int ev = elems_exp(reinterpret_cast<const uint8_t*>(vs), true, draft, n, a.vs);
+            if (lane == who) {
+              d.ks = kLogitScale * pow2(ek);
+              d.lv = (float)ev;
+              d.exps = (ek & 0xffff) | ev << 16;
+            }
+          }
+        }
         if (b >= 4) ok = wait(smem_u32(&sm.dfree[b & 3]), (b >> 2) - 1);
         if (!ok) break;
-        sm.desc[(kT8Batch * b + lane / kT8Step) & (kT8Descs - 1)][lane % kT8Step] = d;
+        const int at = (kT8Batch * b + lane / kT8Step) & (kT8Descs - 1);
+        sm.desc[at][lane % kT8Step] = d;
+        const unsigned there = __ballot_sync(0xffffffffu, d.kind < 4);
+        if (lane % kT8Step == 0) sm.there[(kT8Batch * b + lane / kT8Step) & (2 * kT8Descs - 1)] = there >> lane & 0xffu;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.dfull[b & 3]));
       }
@@ -990,21 +1020,32 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         if (ok && j >= kT8Ring) ok = wait(smem_u32(&sm.rfree[op][j & 1]), (j >> 1) - 1);
         if (!ok) break;
         const TileDesc* d = &sm.desc[j & (kT8Descs - 1)][lane & (kT8Step - 1)];
-        const unsigned who = __ballot_sync(0xffffffffu, lane < kT8Step && d->kind <= 1);
-        const unsigned long long src = reinterpret_cast<unsigned long long>(d->src) + op * kTile;
+        const int kind = d->kind;
+        const unsigned who = __ballot_sync(0xffffffffu, lane < kT8Step && kind <= 2);
+        // codes: 2 KB of a tile, K then V; the tail: 4 KB; drafts: their rows
+        const unsigned long long src = reinterpret_cast<unsigned long long>(d->src) + (kind == 2 ? 2 * op * kTile : op * kTile);
+        const int size = kind == 2 ? 2 * kTile : kind == 3 ? d->n * 2 * kD : kind < 2 ? kTile : 0;
+        const int bytes = __reduce_add_sync(0xffffffffu, lane < kT8Step ? size : 0);
         const uint32_t bar = smem_u32(&sm.rfull[op][j & 1]), dst = ring + (j & 1) * kT8Entry;
         if (lane == 0) {
-          if (who) mbar_expect_tx(bar, __popc(who) * kTile);
+          if (bytes) mbar_expect_tx(bar, bytes);
           else mbar_arrive(bar);
-          if (j % kT8Batch == kT8Batch - 1) mbar_arrive(smem_u32(&sm.dfree[j / kT8Batch & 3]));
         }
         __syncwarp();
 #pragma unroll
         for (int t = 0; t < kT8Step; t++) {
           const unsigned long long p = __shfl_sync(0xffffffffu, src, t);
+          const int n = __shfl_sync(0xffffffffu, size, t);
           if (who >> t & 1u)
-            if (elected()) bulk_g2s(dst + t * kTile, reinterpret_cast<const void*>(p), kTile, bar);
+            if (elected()) bulk_g2s(dst + t * kTile, reinterpret_cast<const void*>(p), n, bar);
         }
+        for (unsigned rows = __ballot_sync(0xffffffffu, lane < kT8Step && kind == 3); rows; rows &= rows - 1) {
+          const int t = __ffs(rows) - 1;
+          const TileDesc* e = &sm.desc[j & (kT8Descs - 1)][t];
+          if (lane < e->n) bulk_g2s(dst + t * kTile + lane * (2 * kD), op ? e->vsrc + lane * a.vs : e->src + lane * a.ks, 2 * kD, bar);
+        }
+        __syncwarp();
+        if (lane == 0 && j % kT8Batch == kT8Batch - 1) mbar_arrive(smem_u32(&sm.dfree[j / kT8Batch & 3]));
         issued = j + 1;
       }
       // no copy may be in flight at the exit
@@ -1017,9 +1058,8 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       const uint64_t kd = umma_desc_sw128(smem_u32(smem)), vd = umma_desc_sw128(smem_u32(smem + kT8OffV));
       auto test = [&](uint32_t bar, int phase) { return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0; };
       auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-      // S walks the items; their ends and the tiles of their last steps are kept for P V, which
-      // is at most two items behind
-      int s_end = 0, s_rest = 0, item = -1, v_end = 0, v_rest = 0, v_item = -1;
+      // S walks the items; their ends are kept for P V, which is at most two items behind
+      int s_end = 0, item = -1, v_end = 0, v_item = -1;
       int js = 0, jv = 0;              // next step of S, of P V
       bool begin = true, q_there = false;
       const int last = uniform(steps);
@@ -1038,17 +1078,16 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           if (js == s_end) {
             const TreeItem it = tree_item(c, a, sm.plan, lo + js, hi);
             s_end = js + uniform(it.n);
-            s_rest = uniform(min(kT8Step, it.tiles.count - kT8Step * (it.s0 + it.n - 1)));
             item++;
             q_there = false;
-            if (lane == 0) sm.runs[item & 3] = make_int2(s_end, s_rest);
+            if (lane == 0) sm.runs[item & 3] = s_end;
             __syncwarp();
           }
           if (!q_there) q_there = test(qfull(item & 1), item >> 1);
           if (q_there && test(kfull(s_slot), s_round)) {
             tc_fence_after();
             const uint32_t d = uniform(t_s(js & 1)), q = uniform(t_q(item & 1));
-            const uint32_t kind = uniform(js < s_end - 1 || s_rest > 4 ? id : id_half);
+            const uint32_t kind = uniform(sm.there[js & (2 * kT8Descs - 1)] >> 4 ? id : id_half);
             const int at = uniform(s_slot * (kT8Slot >> 4)), bar_s = uniform(sfull(js & 1)), bar_k = uniform(kfree(s_slot));
             if (elected()) {
               const uint64_t bd = kd + at;
@@ -1065,21 +1104,19 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           }
         }
         if (jv < js && jv == v_end) {
-          const int2 run = sm.runs[++v_item & 3];
-          v_end = uniform(run.x);
-          v_rest = uniform(run.y);
+          v_end = uniform(sm.runs[++v_item & 3]);
           begin = true;
         }
         if (jv < js && test(pfull(jv & 1), jv >> 1) && test(vfull(v_slot), v_round)) {
           tc_fence_after();
           const uint32_t p = uniform(t_s(jv & 1));
-          const int n = uniform(jv < v_end - 1 ? kT8Step : v_rest), go_on = uniform(!begin), at = uniform(v_slot * (kT8Slot >> 4));
-          const int bar_pv = uniform(pvdone(jv & 1)), bar_v = uniform(vfree(v_slot));
+          const int who = uniform(sm.there[jv & (2 * kT8Descs - 1)]), go_on = uniform(!begin), at = uniform(v_slot * (kT8Slot >> 4));
+          const int bar_pv = uniform(pvdone(jv & 3)), bar_v = uniform(vfree(v_slot));
           if (elected()) {
             const uint64_t bd = vd + at;
 #pragma unroll
             for (int e = 0; e < kT8Step; e++)
-              if (e < n)
+              if (who >> e & 1)       // (place 0 always holds a tile)
                 umma_f16_tmem_a(t_o, p + 64 * (e >> 2) + 8 * (e & 3), bd + (((e >> 2) * 16384 + (e & 3) * 32) >> 4), id, go_on || e > 0);
             umma_commit(bar_pv);
             umma_commit(bar_v);
@@ -1137,7 +1174,7 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 5) k_tree8_join(const __grid_
     if (m >= req.M) continue;
     uint8_t* out = a.out + (size_t)x * (2 * kD);
     const TreeTiles tiles = tree_tiles(req.N, req.M, c.T, a.window, a.sinks);
-    const int per = (tiles.count + kT8Step - 1) / kT8Step, row = m * G + (q - h * G), t = row / kT8Rows, r = row - t * kT8Rows;
+    const int per = (tiles.places + kT8Step - 1) / kT8Step, row = m * G + (q - h * G), t = row / kT8Rows, r = row - t * kT8Rows;
     const int us = first + (h * unit_rows(req.M, G) + t) * per;
     const int c0 = range_of(total, us, ctas), c1 = range_of(total, us + per - 1, ctas);
     uint2 w;
