@@ -551,7 +551,8 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
                                                          int* plan) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded pointer: the compiler still knows that this is shared memory)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   TreeSmem& sm = *reinterpret_cast<TreeSmem*>(smem + kT8OffSmem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, G = c.G;
   // step j of the CTA: K and V in slot j % kT8Slots, S and P in place j & 1
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   // up, too. The same for every lane. (Short: the kernel's hot code has to fit the
   // instruction caches.)
   auto wait = [&](uint32_t bar, int phase) {
-    for (int n = 1 << 22; !__all_sync(0xffffffffu, mbar_try_wait_hint(bar, phase & 1, 1000u)); n--)
+    for (int n = 1 << 25; !__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1)); n--)
       if (n == 0 || ((n & 255) == 0 && *(volatile int*)&sm.fail)) {
         *(volatile int*)&sm.fail = 1;
         return false;
@@ -753,6 +754,9 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
 #pragma unroll 1
           for (bool again = raise;; again = true) {
             if (again) {
+              // (the maxima are not to be taken ahead of the question)
+#pragma unroll
+              for (int e = 0; e < 64; e++) asm volatile("" : "+f"(s[e]));
               // the rows' maxima over both parts
               float yt = -INFINITY, xt = -INFINITY;
 #pragma unroll
@@ -1162,16 +1166,15 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 5) k_tree8_join(const __grid_
   const int lane = threadIdx.x & 31, G = c.G, hq = c.hkv * G;
   const unsigned rows = (unsigned)a.n_req * a.max_nodes * hq;
   pdl_wait();
-  // (an error of this call or an earlier one: results are undefined)
-  const int total = plan[a.n_req];
-  if (*(volatile int*)c.status != 0 || total == 0) return;
-  const int ctas = tree_ctas(total, main_grid);
+  const int total = plan[a.n_req], error = *(volatile int*)c.status;
 #pragma unroll 1
   for (unsigned x = blockIdx.x * kT8Walkers + (threadIdx.x >> 5); x < rows; x += gridDim.x * kT8Walkers) {
     const int q = x % hq, y = x / hq, i = y / a.max_nodes, m = y - i * a.max_nodes, h = q / G;
     const int first = plan[i];
     const TreeReq req = tree_req(c, a, i);
-    if (m >= req.M) continue;
+    // (an error of this call or an earlier one: results are undefined)
+    if (error != 0 || m >= req.M) continue;
+    const int ctas = tree_ctas(total, main_grid);
     uint8_t* out = a.out + (size_t)x * (2 * kD);
     const TreeTiles tiles = tree_tiles(req.N, req.M, c.T, a.window, a.sinks);
     const int per = (tiles.places + kT8Step - 1) / kT8Step, row = m * G + (q - h * G), t = row / kT8Rows, r = row - t * kT8Rows;
@@ -1187,6 +1190,11 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 5) k_tree8_join(const __grid_
       const size_t place = (size_t)part_rows * (kD + 2) / 4;
       auto part = [&](int cta) { return parts + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * place; };
       auto weight_of = [&](int cta) { return reinterpret_cast<const float2*>(part(cta) + part_rows * (kD / 4))[r]; };
+      // most units have few parts: their rows are on their way while the weights are
+      constexpr int kNear = 3;
+      float4 v[kNear];
+#pragma unroll
+      for (int e = 0; e < kNear; e++) v[e] = part(min(c0 + e, c1))[lane * part_rows + r];
       float top = -INFINITY, sum = 0.0f;
       for (int b = c0; b <= c1; b += 32) {
         float2 ul = make_float2(-INFINITY, 0.0f);
@@ -1202,6 +1210,12 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 5) k_tree8_join(const __grid_
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      auto add = [&](const float4& y, float f) {
+        o.x = fmaf(y.x, f, o.x);
+        o.y = fmaf(y.y, f, o.y);
+        o.z = fmaf(y.z, f, o.z);
+        o.w = fmaf(y.w, f, o.w);
+      };
       for (int b = c0; b <= c1; b += 32) {
         float f = 0.0f;
         if (b + lane <= c1) {
@@ -1209,15 +1223,14 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 5) k_tree8_join(const __grid_
           f = ul.y == 0.0f ? 0.0f : __fdiv_rn(ul.y * (ul.x == top ? 1.0f : fast_exp2(ul.x - top)), sum);
         }
         const int n = min(c1 - b + 1, 32);
-#pragma unroll 2
-        for (int e = 0; e < n; e++) {
-          const float4 v = part(b + e)[lane * part_rows + r];
-          const float fe = __shfl_sync(0xffffffffu, f, e);
-          o.x = fmaf(v.x, fe, o.x);
-          o.y = fmaf(v.y, fe, o.y);
-          o.z = fmaf(v.z, fe, o.z);
-          o.w = fmaf(v.w, fe, o.w);
+        int e = 0;
+        if (b == c0) {
+#pragma unroll
+          for (; e < kNear; e++)
+            if (e < n) add(v[e], __shfl_sync(0xffffffffu, f, e));
         }
+#pragma unroll 2
+        for (; e < n; e++) add(part(b + e)[lane * part_rows + r], __shfl_sync(0xffffffffu, f, e));
       }
       w = make_uint2(pack_elems<ELEM>(in_range<ELEM>(o.x), in_range<ELEM>(o.y)), pack_elems<ELEM>(in_range<ELEM>(o.z), in_range<ELEM>(o.w)));
       *reinterpret_cast<uint2*>(out + 8 * lane) = w;
