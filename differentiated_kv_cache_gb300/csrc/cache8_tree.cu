@@ -930,7 +930,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           put_elems<ELEM>(ring + slot * kT8Entry, op, draft, d.n, 2 * kD, op ? d.exps >> 16 : (int)(short)d.exps,
                           op && draft ? draft_place(first) + slot * kT8Slot : to0);
         } else {
-#pragma unroll
+#pragma unroll 1
           for (int t = 0; t < 2; t++)
             if (desc[t].kind <= 1) {
               const uint8_t* p = ring + slot * kT8Entry + t * kTile + 16 * lane;
