@@ -353,7 +353,12 @@ __device__ __forceinline__ int make_plan(const Cache8View& c, const Tree8Args& a
 }
 __device__ __forceinline__ int tree_ctas(int total, int grid) { return max(1, min(grid, (total + kT8Least - 1) / kT8Least)); }
 __device__ __forceinline__ int range_start(int total, int cta, int ctas) { return (int)((long long)total * cta / ctas); }
-__device__ __forceinline__ int range_of(int total, int pos, int ctas) { return (int)((((long long)pos + 1) * ctas - 1) / total); }
+__device__ __forceinline__ int range_of(int total, int pos, int ctas) {     // the CTA whose range holds pos
+  int x = min((int)((float)pos * ((float)ctas / (float)total)), ctas - 1);   // within a few of it
+  while (x > 0 && (long long)x * total > (long long)pos * ctas + (ctas - 1)) x--;
+  while (x < ctas - 1 && (long long)(x + 1) * total <= (long long)pos * ctas + (ctas - 1)) x++;
+  return x;
+}
 
 // Part of a unit in a CTA's range: steps s0 .. s0 + n - 1 of `per`.
 struct TreeItem {
@@ -858,9 +863,8 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         uint8_t* out = a.out + (((long long)it.i * a.max_nodes + m) * c.hkv * G + (size_t)it.h * G + (row - m * G)) * (2 * kD) + 128 * part;
         // a part: [feature / 4][row][4], whose lanes' stores are neighbours, then (u, l) of the rows
         float4* dst = reinterpret_cast<float4*>(a.part + (size_t)(2 * blockIdx.x + (it.s0 > 0 ? 0 : 1)) * part_rows * (kD + 2));
-#pragma unroll 1
-        for (int q = 0; q < 4; q++) {
-          float o[16];
+        // (loops, and short ones: code that runs once an item comes from far)
+        auto load = [&](int q, float (&o)[16]) {
           tmem_ld16_nowait(t_o + tl + 64 * part + 16 * q, o);
           tmem_wait_ld();
 #pragma unroll
@@ -868,26 +872,45 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
             asm volatile("" : "+f"(o[e]));
             o[e] *= f;
           }
-          if (real && whole) {
-            uint32_t w[8], bad = 0;
+        };
+        if (whole) {
+          uint32_t bad = 0;
+#pragma unroll 1
+          for (int q = 0; q < 4; q++) {
+            float o[16];
+            load(q, o);
+            uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; e++) {
               w[e] = pack_elems<ELEM>(o[2 * e], o[2 * e + 1]);
               find_not_finite<ELEM>(bad, w[e]);
             }
-            if (__builtin_expect(found_not_finite(bad), 0)) {
-#pragma unroll
-              for (int e = 0; e < 8; e++) w[e] = pack_elems<ELEM>(in_range<ELEM>(o[2 * e]), in_range<ELEM>(o[2 * e + 1]));
+            if (real) {
+              reinterpret_cast<uint4*>(out)[2 * q] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(out)[2 * q + 1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            reinterpret_cast<uint4*>(out)[2 * q] = make_uint4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<uint4*>(out)[2 * q + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-          } else if (real) {
+          }
+          if (__builtin_expect(__any_sync(0xffffffffu, real && found_not_finite(bad)), 0)) {
+#pragma unroll 1
+            for (int q = 0; q < 4; q++) {
+              float o[16];
+              load(q, o);
+#pragma unroll
+              for (int e = 0; e < 8; e++)
+                if (real) reinterpret_cast<uint32_t*>(out)[8 * q + e] = pack_elems<ELEM>(in_range<ELEM>(o[2 * e]), in_range<ELEM>(o[2 * e + 1]));
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < 4; q++) {
+            float o[16];
+            load(q, o);
 #pragma unroll
             for (int e = 0; e < 4; e++)
-              dst[(16 * part + 4 * q + e) * part_rows + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              if (real) dst[(16 * part + 4 * q + e) * part_rows + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
+          if (real && part == 0) reinterpret_cast<float2*>(dst + part_rows * (kD / 4))[r] = make_float2(u, lsum);
         }
-        if (real && !whole && part == 0) reinterpret_cast<float2*>(dst + part_rows * (kD / 4))[r] = make_float2(u, lsum);
       }
       tc_fence_before();
       if (pos >= hi) break;
