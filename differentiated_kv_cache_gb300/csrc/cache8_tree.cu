@@ -1,5 +1,32 @@
 // cache8_tree.cu — attention for trees of drafted tokens over the uniform 8-bit
 // cache (include/dkv.h: dkv_cache8_tree).
+//
+// o = sum_t w_t v_t / sum_t w_t, w_t = exp(q k_t / sqrt(128)), over the stored tokens in a
+// node's window and the drafts on its way to the root. All nodes of a request and all heads
+// of a group (M G query rows) read the same K and V, so the cache is read once for 128 rows;
+// the products, 4 * 128 operations a row and token, are for tcgen05 from about 32 rows on.
+// Both products take fp16 operands and sum in fp32: codes are exact in fp16 (e4m3's 4 and
+// int8's 8 bits of precision), tails, drafts and queries in bf16 are brought into fp16's range by a
+// power of two (one for 16 tokens, one for a query's row), which keeps their 8 bits down to 2^-17 of the
+// largest; K's scale joins the logits, V's joins the weights as an addend of their exponent.
+//
+// Units (request, KV head, 128 rows) of steps (128 tokens) follow one another; the sequence
+// of all is cut into equal ranges, one for each SM, so ragged batches and one long
+// request alike fill the GPU. A unit that is cut leaves parts (O over its sum, maximum, sum), which the
+// second kernel joins. In a step, of which several are in flight:
+//   lookups -> bulk copies of codes -> conversion to swizzled fp16 operands -> S = Q K^T
+//   -> weights -> O += P V, with Q, S, P and O in tensor memory.
+// A code costs 1 byte of traffic and 4 G M operations, and has to be converted once by
+// ordinary instructions. What bounds a step (2700 cycles at 128 rows): the weights, 16384
+// exponentials (4 cycles for a warp's 32, 512 of those a quarter of the SM: 2048 cycles), then the wait from P
+// through the product to the next S. Measured (int8, G = 4, 32 KV heads' worth as listed, all with tails):
+// 16 requests of 4096 tokens with 26 drafts 69 us (21 by bytes), 8 of 32768 with 64 drafts
+// 0.60 ms, 917 TFLOP/s (48 % of a plain matrix product's), 64 chains 128 us; one small tree
+// 12.5 us, of which 8 are the launches and the first loads' latencies.
+// Tried and slower: 64 tokens a step (8 x 32768: 0.92 ms); conversion by the softmax warps
+// (196 us for the chains); maxima of each step ahead of its weights (0.66 ms: now they are taken
+// when a weight could leave fp16's range); code unrolled over tiles (0.62 ms: it leaves the
+// instruction caches).
 #include <algorithm>
 
 #include "cache8.cuh"
@@ -10,9 +37,8 @@ namespace dkv {
 namespace {
 
 constexpr int kT8Rows = 128;        // query rows of a unit: (node, head of the group), nodes first
-constexpr int kT8Walkers = 8;       // warps of a block of the second kernel
+constexpr int kT8Walkers = 8;       // warps (and rows) of a block of the second kernel
 constexpr int kT8Step = 8;          // tiles of a step, in two parts of four
-constexpr int kT8Least = 1;         // steps that make a CTA worth its start
 // warps: 0 .. 7 softmax, 8 .. 11 convert K, 12 .. 15 V, 16 products, 17 lookups, 18
 // copies of K codes, 19 of V codes
 constexpr int kT8Threads = 640;
@@ -228,12 +254,13 @@ struct Walk {
     y += __shfl_xor_sync(0xffffffffu, y, 1);
     x += __shfl_xor_sync(0xffffffffu, x, 2);
     y += __shfl_xor_sync(0xffffffffu, y, 2);
-    const float f = p.sc.x * (1.0f / kIn) * kLogitScale * qs;
+    // (neither factor is infinite, nor x by the first: a logit is infinite only if the formula's is)
+    const float f = p.sc.x * kLogitScale, back = qs * (1.0f / kIn);
     const int g = lane >> 2;
-    return make_float2(p.see >> g & 1u ? x * f : -INFINITY, p.see >> (g + 8) & 1u ? y * f : -INFINITY);
+    return make_float2(p.see >> g & 1u ? x * f * back : -INFINITY, p.see >> (g + 8) & 1u ? y * f * back : -INFINITY);
   }
 
-  __device__ void row(int m, int g8, uint8_t* out) const {
+  __device__ __noinline__ void row(int m, int g8, uint8_t* out) const {
     const int g = lane >> 2, tt = lane & 3;
     const Node node = node_of(c, a, a.parents ? a.parents + (size_t)i * a.max_nodes : nullptr, i, r.N, m);
     float q[32], am = 0.0f;
@@ -249,7 +276,7 @@ struct Walk {
     if (ELEM == DKV_BF16) {
       am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
       am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-      const int ex = max(-126, min(126, (int)(__float_as_uint(am) >> 23) - 127));
+      const int ex = max(-126, min(118, (int)(__float_as_uint(am) >> 23) - 127));
       const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
       qs = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
@@ -311,7 +338,7 @@ struct Walk {
 };
 
 // ---- the call's plan, the same in every block: prefix sums of the requests' steps ----
-// A unit is a (request, KV head, 128 query rows); its steps of 64 tokens follow one
+// A unit is a (request, KV head, 128 query rows); its steps of 128 tokens follow one
 // another, and the units of all requests form one sequence that is cut into equal
 // ranges, one a CTA.
 struct TreePlan {
@@ -351,7 +378,7 @@ __device__ __forceinline__ int make_plan(const Cache8View& c, const Tree8Args& a
   }
   return carry;
 }
-__device__ __forceinline__ int tree_ctas(int total, int grid) { return max(1, min(grid, (total + kT8Least - 1) / kT8Least)); }
+__device__ __forceinline__ int tree_ctas(int total, int grid) { return max(1, min(grid, total)); }
 __device__ __forceinline__ int range_start(int total, int cta, int ctas) { return (int)((long long)total * cta / ctas); }
 __device__ __forceinline__ int range_of(int total, int pos, int ctas) {     // the CTA whose range holds pos
   int x = min((int)((float)pos * ((float)ctas / (float)total)), ctas - 1);   // within a few of it
@@ -617,9 +644,9 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   const uint32_t t_o = tbase;
   auto t_s = [&](int s) { return tbase + 128u + 128u * s; };
   auto t_q = [&](int s) { return tbase + 384u + 64u * s; };
-  // Bounded: 2^22 attempts of up to a microsecond each; then the block's other waits give
-  // up, too. The same for every lane. (Short: the kernel's hot code has to fit the
-  // instruction caches.)
+  // Bounded: by the products' warp, which gives up after a second without any, and by its own
+  // attempts; then the block's other waits give up, too. The same for every lane. (Short:
+  // the kernel's hot code has to fit the instruction caches.)
   auto wait = [&](uint32_t bar, int phase) {
     for (int n = 1 << 25; !__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1)); n--)
       if (n == 0 || ((n & 255) == 0 && *(volatile int*)&sm.fail)) {
@@ -666,7 +693,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           named_sync(pair_bar, 64);
           const uint32_t most = max(__float_as_uint(mine), __float_as_uint(sm.pair[told][part ^ 1][r].x));
           told ^= 1;
-          const int ex = max(-126, min(126, (int)(most >> 7) - 127));
+          const int ex = most ? max(-126, min(126, (int)(most >> 7) - 127)) : 0;
           inv = pow2(-ex);
           scale = pow2(ex);
         }
@@ -719,7 +746,6 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       bool first = true, raise = true;
       for (; j < end; j++) {
         // (after a wait that gave up the warps walk on, through the same barriers)
-        // (step -1, ahead of the first: the code comes to the caches, nothing is stored)
         ok = wait(sfull(j & 1), j >> 1) && ok;
         tc_fence_after();
         if (busy) {
@@ -937,8 +963,6 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       const uint32_t rfull = smem_u32(sm.rfull[op]), rfree = smem_u32(sm.rfree[op]);
 #pragma unroll 1
       for (int j = 0; ok && j < steps; j++) {
-        // step -1 converts what happens to be there, so that the code is in the caches when
-        // the first codes come (cold, a step takes 4000 cycles longer)
         const int slot = j & 1;
         ok = wait(rfull + 8 * slot, j >> 1);         // (the descriptors are there, too)
         if (ok && j >= kT8Slots) ok = wait(free + 8 * slot, (j >> 1) - 1);
@@ -1179,90 +1203,116 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   }
 }
 
-// ---- rows of units that several CTAs hold parts of, and rows that came out infinite or
-// NaN: a warp a row. (Few registers, so that every row's loads are in flight: walks, which
-// are seldom, spill.) ----
+// ---- units that several CTAs hold parts of, and rows that came out infinite or NaN ----
+// o = sum_p l_p 2^(u_p - u) o_p / sum_p l_p 2^(u_p - u) over a unit's parts p. A block takes
+// eight rows of a unit, a lane four features of one of them, so that the loads of a
+// warp are whole 128-byte lines (a warp for each row, with the part's rows 16 bytes a lane: 74
+// against 69 us for 16 requests of 4096 tokens with 26 drafts). It waits for memory, not for
+// its bandwidth: the first three parts are sent for before their weights are known, and four
+// blocks fit an SM (five spill: 70 us; three: 71 us). It takes 8 of those 69 us, and 2 of a
+// small call's 12.5.
 template <int ELEM, int CODE>
-__global__ void __launch_bounds__(32 * kT8Walkers, 5) k_tree8_join(const __grid_constant__ Cache8View c, const __grid_constant__ Tree8Args a,
-                                                                   int part_rows, const int* plan, int main_grid) {
+__global__ void __launch_bounds__(32 * kT8Walkers, 4) k_tree8_join(const __grid_constant__ Cache8View c, const __grid_constant__ Tree8Args a,
+                                                                   int part_rows, const int* plan, int main_grid, unsigned groups) {
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, G = c.G, hq = c.hkv * G;
-  const unsigned rows = (unsigned)a.n_req * a.max_nodes * hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane & 7, lq = lane >> 3, G = c.G, hq = c.hkv * G;
+  const unsigned per_head = (unsigned)(a.max_nodes * G + 7) / 8;
   pdl_wait();
   const int total = plan[a.n_req], error = *(volatile int*)c.status;
+  // (an error of this call or an earlier one: results are undefined)
+  if (error != 0) return;
+  const int ctas = tree_ctas(total, main_grid);
 #pragma unroll 1
-  for (unsigned x = blockIdx.x * kT8Walkers + (threadIdx.x >> 5); x < rows; x += gridDim.x * kT8Walkers) {
-    const int q = x % hq, y = x / hq, i = y / a.max_nodes, m = y - i * a.max_nodes, h = q / G;
+  for (unsigned x = blockIdx.x; x < groups; x += gridDim.x) {
+    const unsigned y = x / per_head, i = y / c.hkv;
+    const int h = y - i * c.hkv, row0 = 8 * (x - y * per_head), row = row0 + lr;
     const int first = plan[i];
     const TreeReq req = tree_req(c, a, i);
-    // (an error of this call or an earlier one: results are undefined)
-    if (error != 0 || m >= req.M) continue;
-    const int ctas = tree_ctas(total, main_grid);
-    uint8_t* out = a.out + (size_t)x * (2 * kD);
+    if (row0 >= req.M * G) continue;         // (the same for the block)
+    const bool real = row < req.M * G;
     const TreeTiles tiles = tree_tiles(req.N, req.M, c.T, a.window, a.sinks);
-    const int per = (tiles.places + kT8Step - 1) / kT8Step, row = m * G + (q - h * G), t = row / kT8Rows, r = row - t * kT8Rows;
+    const int per = (tiles.places + kT8Step - 1) / kT8Step, t = row0 / kT8Rows, r = row - t * kT8Rows;
     const int us = first + (h * unit_rows(req.M, G) + t) * per;
     const int c0 = range_of(total, us, ctas), c1 = range_of(total, us + per - 1, ctas);
-    uint2 w;
+    auto out_of = [&](int x) {
+      const int m = x / G;
+      return a.out + (((size_t)i * a.max_nodes + m) * hq + (size_t)h * G + (x - m * G)) * (2 * kD);
+    };
+    uint8_t* out = out_of(row) + 8 * (4 * warp + lq);
+    uint2 w = make_uint2(0, 0);
     uint32_t bad = 0;
     if (c0 == c1) {
-      w = *reinterpret_cast<const uint2*>(out + 8 * lane);
+      if (real) w = *reinterpret_cast<const uint2*>(out);
     } else {
       // the first part begins its unit (place 1), the others go on with it (place 0)
-      const float4* parts = reinterpret_cast<const float4*>(a.part);
       const size_t place = (size_t)part_rows * (kD + 2) / 4;
+      const float4* parts = reinterpret_cast<const float4*>(a.part) + (real ? r : 0);
       auto part = [&](int cta) { return parts + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * place; };
-      auto weight_of = [&](int cta) { return reinterpret_cast<const float2*>(part(cta) + part_rows * (kD / 4))[r]; };
+      auto weight_of = [&](int cta) {
+        const float4* p = reinterpret_cast<const float4*>(a.part) + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * place + part_rows * (kD / 4);
+        return reinterpret_cast<const float2*>(p)[real ? r : 0];
+      };
+      const int at = (4 * warp + lq) * part_rows;
       // most units have few parts: their rows are on their way while the weights are
       constexpr int kNear = 3;
       float4 v[kNear];
+      float2 ul[kNear];
 #pragma unroll
-      for (int e = 0; e < kNear; e++) v[e] = part(min(c0 + e, c1))[lane * part_rows + r];
-      float top = -INFINITY, sum = 0.0f;
-      for (int b = c0; b <= c1; b += 32) {
-        float2 ul = make_float2(-INFINITY, 0.0f);
-        if (b + lane <= c1) ul = weight_of(b + lane);
-        float now = ul.x;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
-        now = fmaxf(now, top);
-        sum = sum == 0.0f ? 0.0f : sum * (top == now ? 1.0f : fast_exp2(top - now));
-        sum += ul.y == 0.0f ? 0.0f : ul.y * (ul.x == now ? 1.0f : fast_exp2(ul.x - now));
-        top = now;
+      for (int e = 0; e < kNear; e++) {
+        v[e] = part(min(c0 + e, c1))[at];
+        ul[e] = weight_of(min(c0 + e, c1));
       }
+      float top = -INFINITY, sum = 0.0f;
+      auto more = [&](float2 z) {
+        const float now = fmaxf(top, z.x);
+        sum = sum == 0.0f ? 0.0f : sum * (top == now ? 1.0f : fast_exp2(top - now));
+        sum += z.y == 0.0f ? 0.0f : z.y * (z.x == now ? 1.0f : fast_exp2(z.x - now));
+        top = now;
+      };
+      if (c1 - c0 < kNear) {
 #pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        for (int e = 0; e < kNear; e++)
+          if (c0 + e <= c1) more(ul[e]);
+      } else {
+        for (int b = c0 + lq; b <= c1; b += 4) more(weight_of(b));
+#pragma unroll
+        for (int d = 8; d <= 16; d <<= 1) {
+          const float ot = __shfl_xor_sync(0xffffffffu, top, d), os = __shfl_xor_sync(0xffffffffu, sum, d);
+          more(make_float2(ot, os));
+        }
+      }
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      auto add = [&](const float4& y, float f) {
+      auto add = [&](const float4& y, const float2& z) {
+        const float f = z.y == 0.0f ? 0.0f : __fdiv_rn(z.y * (z.x == top ? 1.0f : fast_exp2(z.x - top)), sum);
         o.x = fmaf(y.x, f, o.x);
         o.y = fmaf(y.y, f, o.y);
         o.z = fmaf(y.z, f, o.z);
         o.w = fmaf(y.w, f, o.w);
       };
-      for (int b = c0; b <= c1; b += 32) {
-        float f = 0.0f;
-        if (b + lane <= c1) {
-          const float2 ul = weight_of(b + lane);
-          f = ul.y == 0.0f ? 0.0f : __fdiv_rn(ul.y * (ul.x == top ? 1.0f : fast_exp2(ul.x - top)), sum);
-        }
-        const int n = min(c1 - b + 1, 32);
-        int e = 0;
-        if (b == c0) {
 #pragma unroll
-          for (; e < kNear; e++)
-            if (e < n) add(v[e], __shfl_sync(0xffffffffu, f, e));
-        }
-#pragma unroll 2
-        for (; e < n; e++) add(part(b + e)[lane * part_rows + r], __shfl_sync(0xffffffffu, f, e));
-      }
+      for (int e = 0; e < kNear; e++)
+        if (c0 + e <= c1) add(v[e], ul[e]);
+#pragma unroll 4
+      for (int b = c0 + kNear; b <= c1; b++) add(part(b)[at], weight_of(b));
       w = make_uint2(pack_elems<ELEM>(in_range<ELEM>(o.x), in_range<ELEM>(o.y)), pack_elems<ELEM>(in_range<ELEM>(o.z), in_range<ELEM>(o.w)));
-      *reinterpret_cast<uint2*>(out + 8 * lane) = w;
+      if (real) *reinterpret_cast<uint2*>(out) = w;
     }
     find_not_finite<ELEM>(bad, w.x);
     find_not_finite<ELEM>(bad, w.y);
-    if (__any_sync(0xffffffffu, found_not_finite(bad))) {
-      const Walk<ELEM, CODE> walk{c, a, i, h, lane, req, tiles};
-      walk.row(m, q - h * G, out);
+    if (__builtin_expect(__syncthreads_or(real && found_not_finite(bad)), 0)) {
+      // a warp a row
+      uint8_t* mine = out_of(row0 + warp);
+      if (row0 + warp < req.M * G) {
+        const uint2 z = *reinterpret_cast<const uint2*>(mine + 8 * lane);
+        uint32_t b2 = 0;
+        find_not_finite<ELEM>(b2, z.x);
+        find_not_finite<ELEM>(b2, z.y);
+        if (__any_sync(0xffffffffu, found_not_finite(b2))) {
+          const int m = (row0 + warp) / G;
+          const Walk<ELEM, CODE> walk{c, a, (int)i, h, lane, req, tiles};
+          walk.row(m, row0 + warp - m * G, mine);
+        }
+      }
     }
   }
 }
@@ -1282,12 +1332,12 @@ cudaError_t tree_typed(const Cache8View& c, Tree8Args a, int sm_count, cudaStrea
   // no more CTAs than the longest lengths that the table holds could use
   const long long tiles = ((long long)c.width * c.T + a.max_nodes) / kSub + 3;
   const long long steps = (long long)a.n_req * c.hkv * ((a.max_nodes * c.G + kT8Rows - 1) / kT8Rows) * (tiles / kT8Step + 1);
-  const int grid = (int)std::min<long long>(sm_count, (steps + kT8Least - 1) / kT8Least);
+  const int grid = (int)std::min<long long>(sm_count, steps);
   e = launch_dependent(k_tree8<ELEM, CODE>, dim3(grid), dim3(kT8Threads), kT8Smem, st, c, a, part_rows, plan);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)a.n_req * a.max_nodes * c.hkv * c.G;
-  const int blocks = (int)std::min<long long>((rows + kT8Walkers - 1) / kT8Walkers, (long long)sm_count * 20);
-  return launch_dependent(k_tree8_join<ELEM, CODE>, dim3(blocks), dim3(32 * kT8Walkers), 0, st, c, a, part_rows, plan, grid);
+  const unsigned groups = (unsigned)a.n_req * c.hkv * ((a.max_nodes * c.G + 7) / 8);
+  const unsigned blocks = std::min(groups, (unsigned)sm_count * 20u);
+  return launch_dependent(k_tree8_join<ELEM, CODE>, dim3(blocks), dim3(32 * kT8Walkers), 0, st, c, a, part_rows, plan, grid, groups);
 }
 
 }  // namespace
