@@ -873,8 +873,8 @@ int dkv_cache8_tree(const dkv_cache8* cache, int32_t n_req, const int32_t* slots
   if (!rows_ok(q, q_stride, hq) || !rows_ok(k, k_stride, hkv) || !rows_ok(v, v_stride, hkv)) return DKV_ERR_ARG;
   if (!out || !at(out, 16) || out == q || out == k || out == v || window < 0 || sinks < 0) return DKV_ERR_ARG;
   const long long most = (long long)cache->table_width * cache->block_tokens;
-  // steps of 128 tokens and rows of the whole call are numbered in 32 bits
-  const long long tiles = (max_nodes * cache->group_size + 127) / 128, steps = (most + 2 * kSub + max_nodes + 63) / 64 + 1;
+  // steps of 128 tokens (and a few for each unit) and rows of the whole call are numbered in 32 bits
+  const long long tiles = (max_nodes * cache->group_size + 127) / 128, steps = (most + 2 * kSub + max_nodes + 63) / 64 + 8;
   if ((long long)n_req * hkv * tiles > 0x7ffffff0ll / steps || (long long)n_req * max_nodes * hq > 0x7ffffff0ll) return DKV_ERR_ARG;
   if (!workspace || !at(workspace, 16)) return DKV_ERR_ARG;
   Device8 dev(cache->device);

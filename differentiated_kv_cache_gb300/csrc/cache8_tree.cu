@@ -51,6 +51,7 @@ constexpr int kT8Slot = 32768;      // K or V of a step in 16 bits
 constexpr int kT8Batch = 4;         // steps that are looked up at once
 constexpr int kT8Descs = 4 * kT8Batch;      // steps whose descriptors are kept, a ring
 constexpr int kT8Metas = 8;         // steps whose scales are kept for the softmax, a ring
+constexpr int kT8Turn = 4;          // steps in whose time a CTA goes from one unit to the next
 constexpr float kT8Up = 7.0f;       // log2 of a weight at its row's maximum
 constexpr float kT8Most = 32768.0f; // largest sum of a row's weights of one tile (fp16 holds 65504)
 constexpr float kT8Far = 60.0f;     // log2 of how far weights may be from probabilities
@@ -337,20 +338,27 @@ struct Walk {
   }
 };
 
-// ---- the call's plan, the same in every block: prefix sums of the requests' steps ----
+// ---- the call's plan, the same in every block ----
 // A unit is a (request, KV head, 128 query rows); its steps of 128 tokens follow one
-// another, and the units of all requests form one sequence that is cut into equal
-// ranges, one a CTA.
+// another, and the units of all requests form one sequence that is cut into ranges, one a
+// CTA. For the cuts a unit counts `turn` steps more than it has, ahead of its first: what a CTA
+// spends on results, queries and first maxima between two units, at most a quarter of its range.
 struct TreePlan {
-  int pre[kMaxCallReq + 1], N[kMaxCallReq], M[kMaxCallReq], slot[kMaxCallReq];
+  int pre[kMaxCallReq + 1], units[kMaxCallReq + 1];      // steps, units of the requests before
+  int N[kMaxCallReq], M[kMaxCallReq], slot[kMaxCallReq];
+};
+struct TreeTotal {
+  int steps, units;
+  __device__ __forceinline__ int ctas(int grid) const { return max(1, min(grid, steps)); }
+  __device__ __forceinline__ int turn(int grid) const { return min(kT8Turn, steps / (4 * grid)); }
 };
 __device__ __forceinline__ int unit_rows(int M, int G) { return (M * G + kT8Rows - 1) / kT8Rows; }
-__device__ __forceinline__ int make_plan(const Cache8View& c, const Tree8Args& a, TreePlan& p, int* scan) {
+__device__ __forceinline__ TreeTotal make_plan(const Cache8View& c, const Tree8Args& a, TreePlan& p, int2* scan) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  int carry = 0;
+  TreeTotal carry{0, 0};
   for (int base = 0; base < a.n_req; base += blockDim.x) {
     const int i = base + threadIdx.x;
-    int cost = 0;
+    int cost = 0, units = 0;
     if (i < a.n_req) {
       const TreeReq r = tree_req(c, a, i);
       p.N[i] = r.N;
@@ -358,33 +366,57 @@ __device__ __forceinline__ int make_plan(const Cache8View& c, const Tree8Args& a
       p.slot[i] = r.slot;
       if (r.M > 0) {
         const TreeTiles t = tree_tiles(r.N, r.M, c.T, a.window, a.sinks);
-        cost = c.hkv * unit_rows(r.M, c.G) * ((t.places + kT8Step - 1) / kT8Step);
+        units = c.hkv * unit_rows(r.M, c.G);
+        cost = units * ((t.places + kT8Step - 1) / kT8Step);
       }
     }
-    int x = cost;
+    int x = cost, y = units;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
+      const int x2 = __shfl_up_sync(0xffffffffu, x, d), y2 = __shfl_up_sync(0xffffffffu, y, d);
+      if (lane >= d) {
+        x += x2;
+        y += y2;
+      }
     }
-    if (lane == 31) scan[warp] = x;
+    if (lane == 31) scan[warp] = make_int2(x, y);
     __syncthreads();
-    const int sum = lane < warps ? scan[lane] : 0;
-    const int before = carry + __reduce_add_sync(0xffffffffu, lane < warp ? sum : 0);
-    carry += __reduce_add_sync(0xffffffffu, sum);
-    if (i < a.n_req) p.pre[i] = before + x - cost;
-    if (threadIdx.x == 0) p.pre[min(base + (int)blockDim.x, a.n_req)] = carry;
+    const int2 sum = lane < warps ? scan[lane] : make_int2(0, 0);
+    const int before = carry.steps + __reduce_add_sync(0xffffffffu, lane < warp ? sum.x : 0);
+    const int units_before = carry.units + __reduce_add_sync(0xffffffffu, lane < warp ? sum.y : 0);
+    carry.steps += __reduce_add_sync(0xffffffffu, sum.x);
+    carry.units += __reduce_add_sync(0xffffffffu, sum.y);
+    if (i < a.n_req) {
+      p.pre[i] = before + x - cost;
+      p.units[i] = units_before + y - units;
+    }
+    if (threadIdx.x == 0) {
+      p.pre[min(base + (int)blockDim.x, a.n_req)] = carry.steps;
+      p.units[min(base + (int)blockDim.x, a.n_req)] = carry.units;
+    }
     __syncthreads();
   }
   return carry;
 }
-__device__ __forceinline__ int tree_ctas(int total, int grid) { return max(1, min(grid, total)); }
 __device__ __forceinline__ int range_start(int total, int cta, int ctas) { return (int)((long long)total * cta / ctas); }
 __device__ __forceinline__ int range_of(int total, int pos, int ctas) {     // the CTA whose range holds pos
   int x = min((int)((float)pos * ((float)ctas / (float)total)), ctas - 1);   // within a few of it
   while (x > 0 && (long long)x * total > (long long)pos * ctas + (ctas - 1)) x--;
   while (x < ctas - 1 && (long long)(x + 1) * total <= (long long)pos * ctas + (ctas - 1)) x++;
   return x;
+}
+// The first step at or behind a cut, which counts turns.
+__device__ __forceinline__ int step_at(const Cache8View& c, const Tree8Args& a, const TreePlan& p, const TreeTotal& all, int cut, int turn) {
+  if (turn == 0) return cut;
+  if (cut >= all.steps + turn * all.units) return all.steps;
+  int i = 0, end = a.n_req;
+  while (end - i > 1) {        // the last request that starts at or before the cut
+    const int mid = (i + end) >> 1;
+    if (p.pre[mid] + turn * p.units[mid] <= cut) i = mid; else end = mid;
+  }
+  const int per = (tree_tiles(p.N[i], p.M[i], c.T, a.window, a.sinks).places + kT8Step - 1) / kT8Step;
+  const int x = cut - p.pre[i] - turn * p.units[i], unit = x / (per + turn);
+  return p.pre[i] + unit * per + max(x - unit * (per + turn) - turn, 0);
 }
 
 // Part of a unit in a CTA's range: steps s0 .. s0 + n - 1 of `per`.
@@ -439,7 +471,7 @@ struct TreeSmem {
   TreePlan plan;
   int parents[kMaxNodes];
   float2 pair[2][2][kT8Rows];      // what the two warps of a row tell each other
-  int scan[32];
+  int2 scan[32];
   int runs[4];                     // ends of items of the products
   // K, V of a step there, no longer needed; S, P, P V of a step there, queries there (two of
   // each, of P V four: a wait is for the last of them, the one before in its place long over);
@@ -627,18 +659,26 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   pdl_wait();
   // an error of an earlier call (its load is in flight with the plan's)
   const int halted = threadIdx.x == 0 ? *(volatile int*)c.status : 0;
-  const int total = make_plan(c, a, sm.plan, sm.scan);
+  const TreeTotal all = make_plan(c, a, sm.plan, sm.scan);
   tc_fence_before();
   const bool stopped = __syncthreads_or(halted);
   tc_fence_after();
   if (blockIdx.x == 0)           // for the second kernel
-    for (int i = threadIdx.x; i <= a.n_req; i += blockDim.x) plan[i] = sm.plan.pre[i];
-  const int ctas = tree_ctas(total, gridDim.x);
-  if (stopped || total == 0 || (int)blockIdx.x >= ctas) {
+    for (int i = threadIdx.x; i <= a.n_req; i += blockDim.x) {
+      plan[i] = sm.plan.pre[i];
+      plan[kMaxCallReq + 1 + i] = sm.plan.units[i];
+    }
+  const int ctas = all.ctas(gridDim.x), turn = all.turn(gridDim.x);
+  int lo = 0, hi = 0;
+  if (all.steps > 0 && (int)blockIdx.x < ctas) {
+    const int mine = step_at(c, a, sm.plan, all, range_start(all.steps + turn * all.units, blockIdx.x + (lane & 1), ctas), turn);
+    lo = __shfl_sync(0xffffffffu, mine, 0);
+    hi = __shfl_sync(0xffffffffu, mine, 1);
+  }
+  if (stopped || lo == hi) {
     if (warp == 16) tmem_dealloc(__shfl_sync(0xffffffffu, sm.taddr, 0), 512);
     return;
   }
-  const int lo = range_start(total, blockIdx.x, ctas), hi = range_start(total, blockIdx.x + 1, ctas);
   const uint32_t tbase = __shfl_sync(0xffffffffu, sm.taddr, 0);
   // O, two S (and P over them), two Q
   const uint32_t t_o = tbase;
@@ -1218,21 +1258,22 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 4) k_tree8_join(const __grid_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane & 7, lq = lane >> 3, G = c.G, hq = c.hkv * G;
   const unsigned per_head = (unsigned)(a.max_nodes * G + 7) / 8;
   pdl_wait();
-  const int total = plan[a.n_req], error = *(volatile int*)c.status;
+  const TreeTotal all{plan[a.n_req], plan[kMaxCallReq + 1 + a.n_req]};
+  const int error = *(volatile int*)c.status;
   // (an error of this call or an earlier one: results are undefined)
   if (error != 0) return;
-  const int ctas = tree_ctas(total, main_grid);
+  const int ctas = all.ctas(main_grid), turn = all.turn(main_grid), total = all.steps + turn * all.units;
 #pragma unroll 1
   for (unsigned x = blockIdx.x; x < groups; x += gridDim.x) {
     const unsigned y = x / per_head, i = y / c.hkv;
     const int h = y - i * c.hkv, row0 = 8 * (x - y * per_head), row = row0 + lr;
-    const int first = plan[i];
+    const int first = plan[i], units = plan[kMaxCallReq + 1 + i];
     const TreeReq req = tree_req(c, a, i);
     if (row0 >= req.M * G) continue;         // (the same for the block)
     const bool real = row < req.M * G;
     const TreeTiles tiles = tree_tiles(req.N, req.M, c.T, a.window, a.sinks);
     const int per = (tiles.places + kT8Step - 1) / kT8Step, t = row0 / kT8Rows, r = row - t * kT8Rows;
-    const int us = first + (h * unit_rows(req.M, G) + t) * per;
+    const int unit = h * unit_rows(req.M, G) + t, us = first + unit * per + turn * (units + unit + 1);
     const int c0 = range_of(total, us, ctas), c1 = range_of(total, us + per - 1, ctas);
     auto out_of = [&](int x) {
       const int m = x / G;
@@ -1319,8 +1360,8 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 4) k_tree8_join(const __grid_
 
 int part_rows_of(int G, int max_nodes) { return std::min(kT8Rows, (max_nodes * G + 31) / 32 * 32); }
 
-// The workspace: the plan's prefix sums, then two parts a CTA.
-constexpr size_t kT8PlanBytes = ((kMaxCallReq + 1) * 4 + 255) / 256 * 256;
+// The workspace: the plan's two prefix sums, then two parts a CTA.
+constexpr size_t kT8PlanBytes = ((kMaxCallReq + 1) * 8 + 255) / 256 * 256;
 
 template <int ELEM, int CODE>
 cudaError_t tree_typed(const Cache8View& c, Tree8Args a, int sm_count, cudaStream_t st) {
