@@ -452,10 +452,10 @@ struct TileDesc {
   float ks;
   union {
     float lv;       // log2 of V's scale
-    int req_head;   // kinds 2 and 3, until they are looked through: request << 12 | KV head
+    int req_head;   // kinds 2 and 3, on the way: request << 12 | KV head
   };
   int pos0, kind;   // first token, first draft
-  int n, exps;      // kinds 2 and 3: valid tokens; exponents of the powers of two that K and V are divided by (K's in the lower half)
+  int n;            // kinds 2 and 3: valid tokens
   const uint8_t* vsrc;
 };
 // What the softmax has to know of it. kind: seen by all (0), stored (1), drafts (2), none (3).
@@ -525,7 +525,7 @@ __device__ __forceinline__ TileDesc describe_tile(const Cache8View& c, const Tre
   const int pos = lo + x / kT8Step;
   const TreeItem it = tree_item(c, a, plan, pos, pos + 1);
   x = kT8Step * it.s0 + x % kT8Step;
-  TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4, 0, 0, nullptr};
+  TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4, 0, nullptr};
   if (x < it.tiles.codes) {
     const int tile = it.tiles.tile(x), per = __ffs(c.T) - 5;      // log2 of a block's tiles
     d.pos0 = tile * kSub;
@@ -582,19 +582,26 @@ __device__ __forceinline__ void load_elems(const uint8_t* src, bool v, bool draf
   }
 }
 // The exponent of the power of two that bf16 values are divided by.
-__device__ __noinline__ int elems_exp(const uint8_t* src, bool v, bool draft, int n, long long stride) {
-  uint32_t x[32], am = 0;
-  load_elems(src, v, draft, n, stride, x);
+__device__ __forceinline__ int exp_of(const uint32_t (&x)[32]) {
+  uint32_t am = 0;
 #pragma unroll
   for (int f = 0; f < 32; f++) am = amax2_finite(am, x[f]);
   return scale_exp(am);
 }
-// ... as fp16 operands; at: the lane's row of the first four matrices.
-template <int ELEM>
-__device__ __noinline__ void put_elems(const uint8_t* src, bool v, bool draft, int n, long long stride, int ex, uint32_t at) {
+__device__ __noinline__ int elems_exp(const uint8_t* src, bool v, bool draft, int n, long long stride) {
   uint32_t x[32];
   load_elems(src, v, draft, n, stride, x);
+  return exp_of(x);
+}
+// ... as fp16 operands; at: the lane's row of the first four matrices. The exponent that they
+// were divided by.
+template <int ELEM>
+__device__ __noinline__ int put_elems(const uint8_t* src, bool v, bool draft, int n, long long stride, uint32_t at) {
+  uint32_t x[32];
+  int ex = 0;
+  load_elems(src, v, draft, n, stride, x);
   if (ELEM == DKV_BF16) {
+    ex = exp_of(x);
     const float inv = pow2(-ex);
 #pragma unroll
     for (int f = 0; f < 32; f++) x[f] = half_of_bf16(x[f], inv);
@@ -608,6 +615,7 @@ __device__ __noinline__ void put_elems(const uint8_t* src, bool v, bool draft, i
     else
       stmatrix4_trans(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
   }
+  return ex;
 }
 
 template <int ELEM, int CODE>
@@ -1004,18 +1012,23 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
 #pragma unroll 1
       for (int j = 0; ok && j < steps; j++) {
         const int slot = j & 1;
-        ok = wait(rfull + 8 * slot, j >> 1);         // (the descriptors are there, too)
+        const TileDesc* desc = sm.desc[j & (kT8Descs - 1)] + first;
+        // The softmax has to know V's exponents with S: K's warps find them themselves, from where
+        // the values lie, while the copies are on their way.
+        int ev = 0, ek = 0;
+        if (ELEM == DKV_BF16 && op == 0) {
+          if (j % kT8Batch == 0) ok = wait(smem_u32(&sm.dfull[j / kT8Batch & 3]), j / kT8Batch >> 2);
+          if (ok && (desc->kind == 2 || desc->kind == 3)) ev = elems_exp(desc->vsrc, true, desc->kind == 3, desc->n, a.vs);
+        }
+        ok = ok && wait(rfull + 8 * slot, j >> 1);         // (the descriptors are there, too)
         if (ok && j >= kT8Slots) ok = wait(free + 8 * slot, (j >> 1) - 1);
         if (!ok) break;
         const uint32_t to0 = place(first) + slot * kT8Slot, to1 = place(first + 1) + slot * kT8Slot;
-        const TileDesc* desc = sm.desc[j & (kT8Descs - 1)] + first;
         const int kind = desc->kind;
         if (kind == 2 || kind == 3) {
           // (the second place is none)
-          const TileDesc d = desc[0];
           const bool draft = kind == 3;
-          put_elems<ELEM>(ring + slot * kT8Entry, op, draft, d.n, 2 * kD, op ? d.exps >> 16 : (int)(short)d.exps,
-                          op && draft ? draft_place(first) + slot * kT8Slot : to0);
+          ek = put_elems<ELEM>(ring + slot * kT8Entry, op, draft, desc->n, 2 * kD, op && draft ? draft_place(first) + slot * kT8Slot : to0);
         } else {
 #pragma unroll 1
           for (int t = 0; t < 2; t++)
@@ -1042,7 +1055,9 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         }
         if (op == 0 && lane < 2) {
           const TileDesc* d = desc + lane;
-          sm.meta[j & (kT8Metas - 1)][first + lane] = TileMeta{d->ks, d->lv, d->pos0, d->kind < 2 ? d->kind : d->kind - 1};
+          const bool elems = ELEM == DKV_BF16 && (d->kind == 2 || d->kind == 3);
+          sm.meta[j & (kT8Metas - 1)][first + lane] =
+              TileMeta{elems ? kLogitScale * pow2(ek) : d->ks, elems ? (float)ev : d->lv, d->pos0, d->kind < 2 ? d->kind : d->kind - 1};
         }
         fence_proxy_async();
         __syncwarp();
@@ -1059,7 +1074,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
 #pragma unroll 1
       for (int b = 0; ok && b < batches; b++) {
         const float2* scales = nullptr;
-        TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4, 0, 0, nullptr};
+        TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4, 0, nullptr};
         const int x = kT8Step * kT8Batch * b + lane;
         if (x < kT8Step * steps) d = describe_tile(c, a, sm.plan, lo, x, scales);
         if (scales) {
@@ -1067,29 +1082,11 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           d.ks = sc.x * kLogitScale;
           d.lv = log2f(sc.y);
         }
-        // tiles of the tail and drafts: bf16 ones are looked through for their largest values
-        const bool elems = d.kind == 2 || d.kind == 3;
-        if (elems) {
+        if (d.kind == 2 || d.kind == 3) {
           const int i = d.req_head >> 12, h = d.req_head & 4095;
           d.n = min((d.kind == 2 ? sm.plan.N[i] : sm.plan.M[i]) - d.pos0, kSub);
           d.vsrc = d.kind == 2 ? d.src + 2 * kTile : a.v + ((long long)i * a.max_nodes + d.pos0) * a.vs + h * (2 * kD);
           d.lv = 0.0f;
-        }
-        if (ELEM == DKV_BF16) {
-          for (unsigned left = __ballot_sync(0xffffffffu, elems); left; left &= left - 1) {
-            const int who = __ffs(left) - 1;
-            const unsigned long long ks = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(d.src), who);
-            const unsigned long long vs = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(d.vsrc), who);
-            const int n = __shfl_sync(0xffffffffu, d.n, who);
-            const bool draft = __shfl_sync(0xffffffffu, d.kind, who) == 3;
-            const int ek = elems_exp(reinterpret_cast<const uint8_t*>(ks), false, draft, n, a.ks);
-            const int ev = elems_exp(reinterpret_cast<const uint8_t*>(vs), true, draft, n, a.vs);
-            if (lane == who) {
-              d.ks = kLogitScale * pow2(ek);
-              d.lv = (float)ev;
-              d.exps = (ek & 0xffff) | ev << 16;
-            }
-          }
         }
         if (b >= 4) ok = wait(smem_u32(&sm.dfree[b & 3]), (b >> 2) - 1);
         if (!ok) break;
