@@ -3,30 +3,35 @@
 //
 // o = sum_t w_t v_t / sum_t w_t, w_t = exp(q k_t / sqrt(128)), over the stored tokens in a
 // node's window and the drafts on its way to the root. All nodes of a request and all heads
-// of a group (M G query rows) read the same K and V, so the cache is read once for 128 rows;
-// the products, 4 * 128 operations a row and token, are for tcgen05 from about 32 rows on.
-// Both products take fp16 operands and sum in fp32: codes are exact in fp16 (e4m3's 4 and
-// int8's 8 bits of precision), tails, drafts and queries in bf16 are brought into fp16's range by a
-// power of two (one for 16 tokens, one for a query's row), which keeps their 8 bits down to 2^-17 of the
-// largest; K's scale joins the logits, V's joins the weights as an addend of their exponent.
+// of a group (M G query rows) read the same K and V, so the cache is read once for 128
+// rows; the products, 4 * 128 operations a row and token, go to tcgen05. Both take fp16
+// operands and sum in fp32: codes are exact in fp16; tails, drafts and queries in bf16 come
+// into its range by a power of two (one for 16 tokens, one for a query's row), which keeps
+// their 8 bits down to 2^-17 of the largest, and what is smaller to 2^-25 of it; K's scale joins
+// the logits, V's joins the weights as an addend of their exponent. Weights are rounded to
+// fp16 (2^-11), as probabilities are in the attention of single tokens.
 //
 // Units (request, KV head, 128 rows) of steps (128 tokens) follow one another; the sequence
-// of all is cut into equal ranges, one for each SM, so ragged batches and one long
-// request alike fill the GPU. A unit that is cut leaves parts (O over its sum, maximum, sum), which the
-// second kernel joins. In a step, of which several are in flight:
+// of all is cut into ranges of equal time, one for each SM, so ragged batches and one long
+// request alike fill the GPU. A unit that is cut leaves parts (O over its sum, maximum, sum),
+// which the second kernel joins. The way of a step, of which several are in flight:
 //   lookups -> bulk copies of codes -> conversion to swizzled fp16 operands -> S = Q K^T
 //   -> weights -> O += P V, with Q, S, P and O in tensor memory.
-// A code costs 1 byte of traffic and 4 G M operations, and has to be converted once by
-// ordinary instructions. What bounds a step (2700 cycles at 128 rows): the weights, 16384
-// exponentials (4 cycles for a warp's 32, 512 of those a quarter of the SM: 2048 cycles), then the wait from P
-// through the product to the next S. Measured (int8, G = 4, 32 KV heads' worth as listed, all with tails):
-// 16 requests of 4096 tokens with 26 drafts 69 us (21 by bytes), 8 of 32768 with 64 drafts
-// 0.60 ms, 917 TFLOP/s (48 % of a plain matrix product's), 64 chains 128 us; one small tree
-// 12.5 us, of which 8 are the launches and the first loads' latencies.
-// Tried and slower: 64 tokens a step (8 x 32768: 0.92 ms); conversion by the softmax warps
-// (196 us for the chains); maxima of each step ahead of its weights (0.66 ms: now they are taken
-// when a weight could leave fp16's range); code unrolled over tiles (0.62 ms: it leaves the
-// instruction caches).
+// What bounds a step of 128 rows (2400 cycles): its 16384 exponentials (4 cycles for a
+// warp's 32, a quarter of them for each quarter of an SM: 512 cycles; with sums, roundings and
+// masks 1300), and the wait from the weights through the products to the next S. Between two
+// units of a CTA lie 10000 cycles, ahead of the first step 20000: the launch, the plan, a
+// chain of four loads, and code that all SMs fetch at once. Measured:
+//   8 heads, G = 4, fp16, e4m3, 16 requests of 4096 tokens, 26 drafts    69 us (by bytes 21)
+//   8 heads, G = 8, bf16, int8, 8 of 32768, 64 drafts                   565 us, 976 TFLOP/s
+//     (51 % of a plain matrix product's rate)
+//   4 heads, G = 7, bf16, e4m3, 32 of 1024 to 16384, window 4096         63 us
+//   8 heads, G = 5, fp16, int8, 64 of 1 to 3000, chains of 5             99 us
+//   8 heads, G = 4, fp16, e4m3, one of 300 tokens, 8 drafts              12.5 us
+// Tried and slower: 64 tokens a step (the second: 0.92 ms); conversion by the softmax warps
+// (the chains: 196 us); maxima of each step ahead of its weights (the second: 0.66 ms; now
+// they are taken when a weight could leave fp16's range); conversion unrolled over its tiles
+// (0.62 ms: it leaves the instruction caches); ranges of equal steps (the chains: 126 us).
 #include <algorithm>
 
 #include "cache8.cuh"
@@ -51,7 +56,9 @@ constexpr int kT8Slot = 32768;      // K or V of a step in 16 bits
 constexpr int kT8Batch = 4;         // steps that are looked up at once
 constexpr int kT8Descs = 4 * kT8Batch;      // steps whose descriptors are kept, a ring
 constexpr int kT8Metas = 8;         // steps whose scales are kept for the softmax, a ring
-constexpr int kT8Turn = 4;          // steps in whose time a CTA goes from one unit to the next
+// steps in whose time a CTA goes from one unit to the next (0: 64 chains of 1 to 3000 tokens
+// take 126 us, 32 windows 76; 4: 100 and 68; 8: 103 and 68)
+constexpr int kT8Turn = 4;
 constexpr float kT8Up = 7.0f;       // log2 of a weight at its row's maximum
 constexpr float kT8Most = 32768.0f; // largest sum of a row's weights of one tile (fp16 holds 65504)
 constexpr float kT8Far = 60.0f;     // log2 of how far weights may be from probabilities
@@ -128,9 +135,11 @@ __device__ __forceinline__ Node node_of(const Cache8View& c, const Tree8Args& a,
       if (x >> 5 == w) n.over[w] |= 1u << (x & 31);
   };
   n.depth = 0;
+#pragma unroll 1
   for (int x = m; (x = up(x)) >= 0;) n.depth++;
   sees(m);
   int back = 1;
+#pragma unroll 1
   for (int x = m; (x = up(x)) >= 0; back++)
     if (a.window <= 0 || back < a.window || N + n.depth - back < a.sinks) sees(x);
   return n;
@@ -398,7 +407,10 @@ __device__ __forceinline__ TreeTotal make_plan(const Cache8View& c, const Tree8A
   }
   return carry;
 }
-__device__ __forceinline__ int range_start(int total, int cta, int ctas) { return (int)((long long)total * cta / ctas); }
+__device__ __forceinline__ int range_start(int total, int cta, int ctas) {       // floor(total * cta / ctas)
+  const int q = total / ctas;
+  return q * cta + (total - q * ctas) * cta / ctas;
+}
 __device__ __forceinline__ int range_of(int total, int pos, int ctas) {     // the CTA whose range holds pos
   int x = min((int)((float)pos * ((float)ctas / (float)total)), ctas - 1);   // within a few of it
   while (x > 0 && (long long)x * total > (long long)pos * ctas + (ctas - 1)) x--;
@@ -410,6 +422,7 @@ __device__ __forceinline__ int step_at(const Cache8View& c, const Tree8Args& a, 
   if (turn == 0) return cut;
   if (cut >= all.steps + turn * all.units) return all.steps;
   int i = 0, end = a.n_req;
+#pragma unroll 1
   while (end - i > 1) {        // the last request that starts at or before the cut
     const int mid = (i + end) >> 1;
     if (p.pre[mid] + turn * p.units[mid] <= cut) i = mid; else end = mid;
@@ -427,6 +440,7 @@ struct TreeItem {
 __device__ __forceinline__ TreeItem tree_item(const Cache8View& c, const Tree8Args& a, const TreePlan& p, int pos, int hi) {
   TreeItem it;
   int i = 0, end = a.n_req;
+#pragma unroll 1
   while (end - i > 1) {        // the last request that starts at or before pos
     const int mid = (i + end) >> 1;
     if (p.pre[mid] <= pos) i = mid; else end = mid;
@@ -696,6 +710,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   // attempts; then the block's other waits give up, too. The same for every lane. (Short:
   // the kernel's hot code has to fit the instruction caches.)
   auto wait = [&](uint32_t bar, int phase) {
+#pragma unroll 1
     for (int n = 1 << 25; !__all_sync(0xffffffffu, mbar_try_wait(bar, phase & 1)); n--)
       if (n == 0 || ((n & 255) == 0 && *(volatile int*)&sm.fail)) {
         *(volatile int*)&sm.fail = 1;
