@@ -342,7 +342,7 @@ def make_cache8(pages, scales, tail, page_table, group_size: int, rotary_dim: in
     c.device = c.dev = pages.get_device()
     if c.dev < 0:
         raise TypeError("the cache's tensors must be CUDA tensors")
-    ours = status is None or workspace is None
+    ours = status is None or workspace is None or bool(max_nodes) and tree_workspace is None
     if status is None:
         status = torch.zeros(4, dtype=torch.int32, device=pages.device)
     if workspace is None:

@@ -347,6 +347,108 @@ def test_two_streams_with_workspaces_of_their_own():
         assert torch.equal(o, w)
 
 
+@pytest.mark.parametrize("elem,n,hkv,G,M,longest", [(F16, 300, 4, 3, 3, 60), (BF16, 300, 4, 3, 3, 60), (F16, 1024, 1, 1, 1, 40)])
+def test_hundreds_of_short_requests(elem, n, hkv, G, M, longest):
+    """Many units of a step or two for each SM, a few long ones among them; some without
+    drafts."""
+    rng = np.random.default_rng(n + M)
+    lens = [int(x) for x in rng.integers(0, longest, n)]
+    lens[5], lens[n // 2], lens[n - 1] = 700, 431, 1300
+    c = make(hkv, G, 16, n, 1300 // 16 + 1, elem, E4M3, M, seed=3, fill=NAN)
+    who = [i for i in range(n) if lens[i] > 0]
+    new = [lens[i] for i in who]
+    c.append(who, [0] * len(who), new, c.vec(rng, sum(new), hkv), c.vec(rng, sum(new), hkv))
+    parents = [tref.random_tree(rng, M) for _ in range(n)]
+    n_nodes = [int(x) for x in rng.integers(0, M + 1, n)]
+    n_nodes[5] = n_nodes[n - 1] = M
+    q, k, v = drafts(c, rng, n, M, n_nodes)
+    out = run_tree(c, lens, parents, q, k, v, n_nodes)
+    check_tree(c, out, lens, parents, q, k, v, n_nodes)
+    again = run_tree(c, lens, parents, q, k, v, n_nodes)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.parametrize("n", [20, 300])
+def test_products_beyond_fp32_that_never_meet(n):
+    """bf16 queries and keys of 2^110 in different features: every logit is 0, so the
+    result is the mean of the values."""
+    rng = np.random.default_rng(12)
+    M = 7
+    c = make(2, 2, 16, 1, 24, BF16, INT8, M, seed=10)
+    k, v = torch.zeros((n, 2, 128), dtype=BF16, device="cuda"), c.vec(rng, n, 2)
+    k[:, :, 3] = 2.0 ** 110
+    c.append([0], [0], [n], k, v)
+    q, _, dv = drafts(c, rng, 1, M)
+    q[:] = 0
+    q[:, :, 4] = 2.0 ** 110
+    q[2] = 0                        # and a query of zeros
+    dk = torch.zeros_like(dv)
+    dk[:, :, 3] = 2.0 ** 110
+    parents = [[-1, 0, 0, 1, 2, -1, 5]]
+    out = run_tree(c, [n], parents, q, dk, dv)
+    check_tree(c, out, [n], parents, q, dk, dv, [M])
+
+
+@pytest.mark.parametrize("up", [-116, 116])
+def test_huge_keys_and_tiny_queries_computed_again(up):
+    """bf16 keys of 2^116 (2^-116) and queries that bring them back, with and without an
+    infinite value that rows do not see."""
+    rng = np.random.default_rng(13)
+    n, M = 150, 6
+    c = make(1, 4, 32, 1, 8, BF16, E4M3, M, seed=11)
+    k, v = c.vec(rng, n, 1), c.vec(rng, n, 1)
+    if up > 0:                      # (a block's smallest scale is 2^-100)
+        k *= 2.0 ** up
+    c.append([0], [0], [n], k, v)
+    q, dk, dv = drafts(c, rng, 1, M)
+    if up > 0:
+        q *= 2.0 ** -up
+        dk *= 2.0 ** up
+    else:
+        q[1] *= 2.0 ** up
+        dk[3] *= 2.0 ** up
+    parents = [[-1, 0, 0, 1, 1, 2]]
+    out = run_tree(c, [n], parents, q, dk, dv)
+    check_tree(c, out, [n], parents, q, dk, dv, [M])
+    dv[5, :, 9] = float("inf")
+    out = run_tree(c, [n], parents, q, dk, dv)
+    check_tree(c, out, [n], parents, q, dk, dv, [M], nodes=range(5))
+    assert torch.isinf(out[5, :, 9].float()).all() and torch.isfinite(out[5, :, :9].float()).all()
+
+
+def test_two_graphs_of_one_workspace_in_turn():
+    """Calls in the order of a stream may share a workspace: it holds nothing between
+    them."""
+    rng = np.random.default_rng(14)
+    M, lens = 9, [900, 70, 0]
+    cs, data = [], []
+    for s, hkv in ((1, 4), (2, 2)):
+        c = make(hkv, 4, 32, 3, 32, F16, INT8, M, seed=s)
+        fill(c, rng, lens)
+        cs.append(c)
+        data.append(([tref.random_tree(rng, M) for _ in lens], *drafts(c, rng, 3, M)))
+    cs[1].c = _dkv().make_cache8(cs[1].pages, cs[1].scales, cs[1].tail, cs[1].table, group_size=4, rotary_dim=0,
+                                 max_nodes=M, tree_workspace=cs[0].c.tensors[6])
+    want = [run_tree(c, lens, *d) for c, d in zip(cs, data)]
+    outs, graphs = [torch.full_like(w, NAN) for w in want], []
+    ln, par = i32(lens), [i32(d[0]) for d in data]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for c, d, o, p in zip(cs, data, outs, par):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            _dkv().dkv_cache8_tree(c.c, ln, p, *d[1:], o)
+        graphs.append(g)
+    for order in ((0, 1, 1, 0), (1, 0, 0, 1)):
+        for o in outs:
+            o.fill_(NAN)
+        for x in order:
+            graphs[x].replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o.view(torch.int16), w.view(torch.int16))
+
+
 # ------------------------------------------------------------------ accepted drafts
 
 @pytest.mark.parametrize("elem,code", [(F16, E4M3), (F16, INT8), (BF16, E4M3), (BF16, INT8)])
