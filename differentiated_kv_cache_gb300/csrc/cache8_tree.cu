@@ -112,36 +112,52 @@ __device__ __forceinline__ TreeTiles tree_tiles(int N, int M, int T, int window,
   return t;
 }
 
-// Which drafts a node sees (bits of 128) and its depth.
+// Which drafts a node sees (bits of 128) and its depth. By a whole warp, a node a lane (those
+// without one: m = -1): a walk up from lanes of their own, each with its own number of steps,
+// leaves the warp in pieces that run one after another (110 drafts in a chain: 350 us, 28 so).
 struct Node {
   uint32_t over[kMaxNodes / 32];
   int depth;
 };
 __device__ __forceinline__ Node node_of(const Cache8View& c, const Tree8Args& a, const int* parents, int i, int N, int m) {
   Node n;
+  n.depth = max(m, 0);
+  const int w = a.window > 0 ? a.window : kMaxNodes, first = a.window > 0 ? a.sinks - N : 0;   // of a path, besides the last w: those of depth under `first`
+  if (!parents) {              // a chain
 #pragma unroll
-  for (int w = 0; w < kMaxNodes / 32; w++) n.over[w] = 0;
-  auto up = [&](int x) {        // x's parent
-    int p = parents ? parents[x] : x - 1;
-    if (p < -1 || p >= x) {
+    for (int e = 0; e < kMaxNodes / 32; e++)
+      n.over[e] = m < 0 ? 0u : below(m + 1 - 32 * e) & (~below(m + 1 - w - 32 * e) | below(first - 32 * e));
+    return n;
+  }
+  auto up = [&](int x) {       // x's parent (-1: none)
+    int p = x >= 0 ? parents[x] : -1;
+    if (p < -1 || p >= max(x, 0)) {
       c.latch(DKV_ERR_ARG, i);
       p = -1;
     }
     return p;
   };
-  auto sees = [&](int x) {
+  // a path from its end: all of it where no window cuts it, else again once its length is known
+  int len = kMaxNodes;
+  bool whole = true;
+#pragma unroll 1
+  while (true) {
 #pragma unroll
-    for (int w = 0; w < kMaxNodes / 32; w++)
-      if (x >> 5 == w) n.over[w] |= 1u << (x & 31);
-  };
-  n.depth = 0;
+    for (int e = 0; e < kMaxNodes / 32; e++) n.over[e] = 0;
+    int back = 0;
 #pragma unroll 1
-  for (int x = m; (x = up(x)) >= 0;) n.depth++;
-  sees(m);
-  int back = 1;
-#pragma unroll 1
-  for (int x = m; (x = up(x)) >= 0; back++)
-    if (a.window <= 0 || back < a.window || N + n.depth - back < a.sinks) sees(x);
+    for (int x = m; __any_sync(0xffffffffu, x >= 0); x = up(x)) {
+      const bool see = x >= 0 && (whole || back < w || len - back < first);
+      const uint32_t bit = see ? 1u << (x & 31) : 0u;
+#pragma unroll
+      for (int e = 0; e < kMaxNodes / 32; e++) n.over[e] |= x >> 5 == e ? bit : 0u;
+      back += x >= 0;
+    }
+    len = back - 1;            // its depth
+    if (!whole || !__any_sync(0xffffffffu, back > w)) break;
+    whole = false;
+  }
+  n.depth = max(len, 0);
   return n;
 }
 // Which of the 16 stored tokens from pos0 on a node sees, as bits.
@@ -509,6 +525,12 @@ __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint3
                "r"(d)
                : "memory");
 }
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 // largest finite magnitude of bf16 pairs, as bits
 __device__ __forceinline__ uint32_t amax2_finite(uint32_t m, uint32_t w) {
   w &= 0x7fff7fffu;
@@ -569,30 +591,34 @@ __device__ __forceinline__ TileDesc describe_tile(const Cache8View& c, const Tre
   return d;
 }
 
-// A lane's words of K or V (op 0, 1) of a tile of the tail (draft 0) or of drafts (rows of
-// `stride` bytes from src), of which n tokens are valid. What lies behind those becomes 0 (0
-// times what it may hold is not). Words 4 m + (0 .. 3): the 8 x 8 matrices of m-step m.
-__device__ __forceinline__ void load_elems(const uint8_t* src, bool v, bool draft, int n, long long stride, uint32_t (&x)[32]) {
+// A lane's words of K or V of a tile of the tail, of which n tokens are valid: words 4 m +
+// (0 .. 3) are the 8 x 8 matrices of m-step m. What lies behind those tokens becomes 0 (0 times
+// what it may hold is not).
+__device__ __forceinline__ void load_tail(const uint8_t* src, bool v, int n, uint32_t (&x)[32]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  if (!draft) {
-    const uint32_t lo_t = v ? (2 * t < n ? 0xffffu : 0u) | (2 * t + 1 < n ? 0xffff0000u : 0u) : g < n ? 0xffffffffu : 0u;
-    const uint32_t hi_t = v ? (2 * t + 8 < n ? 0xffffu : 0u) | (2 * t + 9 < n ? 0xffff0000u : 0u) : g + 8 < n ? 0xffffffffu : 0u;
+  const uint32_t lo_t = v ? (2 * t < n ? 0xffffu : 0u) | (2 * t + 1 < n ? 0xffff0000u : 0u) : g < n ? 0xffffffffu : 0u;
+  const uint32_t hi_t = v ? (2 * t + 8 < n ? 0xffffu : 0u) | (2 * t + 9 < n ? 0xffff0000u : 0u) : g + 8 < n ? 0xffffffffu : 0u;
 #pragma unroll
-    for (int f = 0; f < 8; f++) {
-      const uint4 y = *reinterpret_cast<const uint4*>(src + 512 * f + 16 * lane);
-      x[4 * f] = y.x & lo_t;
-      x[4 * f + 1] = y.y & (v ? hi_t : lo_t);
-      x[4 * f + 2] = y.z & (v ? lo_t : hi_t);
-      x[4 * f + 3] = y.w & hi_t;
-    }
-  } else {
-    // rows g, g + 8; features 16 m + 8 e + 2 t
-    const uint8_t *p0 = src + g * stride + 4 * t, *p1 = p0 + 8 * stride;
+  for (int f = 0; f < 8; f++) {
+    const uint4 y = *reinterpret_cast<const uint4*>(src + 512 * f + 16 * lane);
+    x[4 * f] = y.x & lo_t;
+    x[4 * f + 1] = y.y & (v ? hi_t : lo_t);
+    x[4 * f + 2] = y.z & (v ? lo_t : hi_t);
+    x[4 * f + 3] = y.w & hi_t;
+  }
+}
+// ... of drafts (rows of `stride` bytes): words 4 e + (0 .. 3) are features 8 (lane % 16) + (0 .. 7)
+// of row 2 e + lane / 16.
+__device__ __forceinline__ void load_drafts(const uint8_t* src, int n, long long stride, uint32_t (&x)[32]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int f = 0; f < 32; f++) {
-      const int off = 32 * (f >> 2) + 16 * (f & 1);
-      x[f] = (f & 2 ? g + 8 : g) < n ? *reinterpret_cast<const uint32_t*>((f & 2 ? p1 : p0) + off) : 0u;
-    }
+  for (int e = 0; e < 8; e++) {
+    const int row = 2 * e + (lane >> 4);
+    const uint4 y = row < n ? *reinterpret_cast<const uint4*>(src + row * stride + 16 * (lane & 15)) : make_uint4(0, 0, 0, 0);
+    x[4 * e] = y.x;
+    x[4 * e + 1] = y.y;
+    x[4 * e + 2] = y.z;
+    x[4 * e + 3] = y.w;
   }
 }
 // The exponent of the power of two that bf16 values are divided by.
@@ -604,30 +630,65 @@ __device__ __forceinline__ int exp_of(const uint32_t (&x)[32]) {
 }
 __device__ __noinline__ int elems_exp(const uint8_t* src, bool v, bool draft, int n, long long stride) {
   uint32_t x[32];
-  load_elems(src, v, draft, n, stride, x);
+  if (draft) load_drafts(src, n, stride, x);
+  else load_tail(src, v, n, x);
   return exp_of(x);
 }
-// ... as fp16 operands; at: the lane's row of the first four matrices. The exponent that they
-// were divided by.
 template <int ELEM>
-__device__ __noinline__ int put_elems(const uint8_t* src, bool v, bool draft, int n, long long stride, uint32_t at) {
-  uint32_t x[32];
-  int ex = 0;
-  load_elems(src, v, draft, n, stride, x);
-  if (ELEM == DKV_BF16) {
-    ex = exp_of(x);
-    const float inv = pow2(-ex);
+__device__ __forceinline__ int to_half(uint32_t (&x)[32]) {      // (fp16 stays)
+  if (ELEM != DKV_BF16) return 0;
+  const int ex = exp_of(x);
+  const float inv = pow2(-ex);
 #pragma unroll
-    for (int f = 0; f < 32; f++) x[f] = half_of_bf16(x[f], inv);
-  }
+  for (int f = 0; f < 32; f++) x[f] = half_of_bf16(x[f], inv);
+  return ex;
+}
+// A tile of the tail as fp16 operands; at: the lane's row of the first four matrices. The
+// exponent that its values were divided by.
+template <int ELEM>
+__device__ __noinline__ int put_tail(const uint8_t* src, bool v, int n, uint32_t at) {
+  uint32_t x[32];
+  load_tail(src, v, n, x);
+  const int ex = to_half<ELEM>(x);
 #pragma unroll
   for (int f = 0; f < 8; f++) {
-    if (!v)
-      stmatrix4((at + (f >> 2) * 16384) ^ ((f & 3) << 5), x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
-    else if (!draft)
-      stmatrix4(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
-    else
-      stmatrix4_trans(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
+    if (!v) stmatrix4((at + (f >> 2) * 16384) ^ ((f & 3) << 5), x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
+    else stmatrix4(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
+  }
+  return ex;
+}
+// Drafts, whose rows of 256 bytes lie at src in shared memory. K's go to their operand rows as they
+// are (to: row 0); V's back to src, row r turned by r times 16 bytes so that the same features of
+// eight rows lie in different banks, and from there as transposed matrices (to: as for put_tail).
+// (Both by words straight from the rows, eight lanes on a bank: a step of four draft tiles 4000
+// cycles.)
+template <int ELEM>
+__device__ __noinline__ int put_drafts(uint32_t src, bool v, int n, uint32_t to) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  uint32_t x[32];
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    const int row = 2 * e + (lane >> 4);
+    x[4 * e] = x[4 * e + 1] = x[4 * e + 2] = x[4 * e + 3] = 0;
+    if (row < n) lds128(src + row * (2 * kD) + 16 * c, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+  }
+  const int ex = to_half<ELEM>(x);
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    const int row = 2 * e + (lane >> 4);
+    const uint32_t at = v ? src + row * (2 * kD) + (((c + row) & 15) << 4) : to + (c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4);
+    sts128(at, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+  }
+  if (v) {
+    __syncwarp();
+    const int row = (lane & 7) + 8 * (lane >> 4);      // matrices: features 0 .. 7, 8 .. 15 of rows 0 .. 7, of rows 8 .. 15
+#pragma unroll
+    for (int f = 0; f < 8; f++) {
+      uint32_t m[4];
+      ldmatrix_x4(m, src + row * (2 * kD) + (((2 * f + (lane >> 3 & 1) + row) & 15) << 4));
+      stmatrix4_trans(to + f * 2048, m[0], m[1], m[2], m[3]);
+    }
   }
   return ex;
 }
@@ -794,7 +855,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           if (part == 1 && r < it.M) sm.parents[r] = a.parents[(size_t)it.i * a.max_nodes + r];
           named_sync(1, 256);
         }
-        if (real) node = node_of(c, a, a.parents ? sm.parents : nullptr, it.i, it.N, m);
+        if (busy) node = node_of(c, a, a.parents ? sm.parents : nullptr, it.i, it.N, real ? m : -1);
         last_i = it.i;
         last_t = it.t;
       }
@@ -1042,8 +1103,8 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         const int kind = desc->kind;
         if (kind == 2 || kind == 3) {
           // (the second place is none)
-          const bool draft = kind == 3;
-          ek = put_elems<ELEM>(ring + slot * kT8Entry, op, draft, desc->n, 2 * kD, op && draft ? draft_place(first) + slot * kT8Slot : to0);
+          if (kind == 2) ek = put_tail<ELEM>(ring + slot * kT8Entry, op, desc->n, to0);
+          else ek = put_drafts<ELEM>(smem_u32(ring + slot * kT8Entry), op, desc->n, (op ? draft_place(first) : base + 2 * first * 1024) + slot * kT8Slot);
         } else {
 #pragma unroll 1
           for (int t = 0; t < 2; t++)
