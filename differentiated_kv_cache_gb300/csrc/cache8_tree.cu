@@ -475,6 +475,13 @@ __device__ __forceinline__ TreeItem tree_item(const Cache8View& c, const Tree8Ar
   return it;
 }
 
+// What a CTA leaves for the second kernel: whether it begins a unit that others go on with (1;
+// request, KV head, rows, the last of those others), and whether rows of whole units came out
+// infinite or NaN (2; its steps).
+struct __align__(16) TreeRecord {
+  int flags, i, h, t, M, last, lo, hi;
+};
+
 // What is known of a tile. kind: of codes, of which every node sees every token (0) or not
 // (1), of the tail (2), drafts (3), none (4).
 struct TileDesc {
@@ -503,6 +510,8 @@ struct TreeSmem {
   float2 pair[2][2][kT8Rows];      // what the two warps of a row tell each other
   int2 scan[32];
   int runs[4];                     // ends of items of the products
+  int begun[4];                    // the unit that the CTA's last item begins: 1, request, KV head, rows
+  int bad;
   // K, V of a step there, no longer needed; S, P, P V of a step there, queries there (two of
   // each, of P V four: a wait is for the last of them, the one before in its place long over);
   // drain
@@ -695,7 +704,7 @@ __device__ __noinline__ int put_drafts(uint32_t src, bool v, int n, uint32_t to)
 
 template <int ELEM, int CODE>
 __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__ Cache8View c, const __grid_constant__ Tree8Args a, int part_rows,
-                                                         int* plan) {
+                                                         int* plan, TreeRecord* records) {
   pdl_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   // (an offset, not a rounded pointer: the compiler still knows that this is shared memory)
@@ -735,7 +744,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       mbar_init(smem_u32(&sm.rfull[0][0]) + 8 * s, 1);
       mbar_init(smem_u32(&sm.rfree[0][0]) + 8 * s, 4);
     }
-    sm.fail = 0;
+    sm.fail = sm.bad = sm.begun[0] = 0;
     fence_mbar_init();
   }
   if (warp == 16) tmem_alloc(smem_u32(&sm.taddr), 512);
@@ -747,10 +756,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
   const bool stopped = __syncthreads_or(halted);
   tc_fence_after();
   if (blockIdx.x == 0)           // for the second kernel
-    for (int i = threadIdx.x; i <= a.n_req; i += blockDim.x) {
-      plan[i] = sm.plan.pre[i];
-      plan[kMaxCallReq + 1 + i] = sm.plan.units[i];
-    }
+    for (int i = threadIdx.x; i <= a.n_req; i += blockDim.x) plan[i] = sm.plan.pre[i];
   const int ctas = all.ctas(gridDim.x), turn = all.turn(gridDim.x);
   int lo = 0, hi = 0;
   if (all.steps > 0 && (int)blockIdx.x < ctas) {
@@ -759,6 +765,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
     hi = __shfl_sync(0xffffffffu, mine, 1);
   }
   if (stopped || lo == hi) {
+    if (threadIdx.x == 0) records[blockIdx.x] = TreeRecord{};
     if (warp == 16) tmem_dealloc(__shfl_sync(0xffffffffu, sm.taddr, 0), 512);
     return;
   }
@@ -1041,6 +1048,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
             }
           }
           if (__builtin_expect(__any_sync(0xffffffffu, real && found_not_finite(bad)), 0)) {
+            sm.bad = 1;
 #pragma unroll 1
             for (int q = 0; q < 4; q++) {
               float o[16];
@@ -1060,6 +1068,12 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
               if (real) dst[(16 * part + 4 * q + e) * part_rows + r] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           if (real && part == 0) reinterpret_cast<float2*>(dst + part_rows * (kD / 4))[r] = make_float2(u, lsum);
+          if (threadIdx.x == 0 && it.s0 == 0) {
+            sm.begun[0] = 1;
+            sm.begun[1] = it.i;
+            sm.begun[2] = it.h;
+            sm.begun[3] = it.t;
+          }
         }
       }
       tc_fence_before();
@@ -1313,128 +1327,136 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tbase, 512);
     if (lane == 0 && sm.fail) c.latch(DKV_ERR_TIMEOUT, -1);
+  } else if (threadIdx.x == 0) {
+    TreeRecord d{sm.begun[0] | sm.bad << 1, sm.begun[1], sm.begun[2], sm.begun[3], 0, 0, lo, hi};
+    if (sm.begun[0]) {
+      d.M = sm.plan.M[d.i];
+      const int per = (tree_tiles(sm.plan.N[d.i], d.M, c.T, a.window, a.sinks).places + kT8Step - 1) / kT8Step;
+      const int unit = d.h * unit_rows(d.M, G) + d.t;
+      d.last = range_of(all.steps + turn * all.units, sm.plan.pre[d.i] + unit * per + turn * (sm.plan.units[d.i] + unit + 1) + per - 1, ctas);
+    }
+    records[blockIdx.x] = d;
   }
 }
 
 // ---- units that several CTAs hold parts of, and rows that came out infinite or NaN ----
-// o = sum_p l_p 2^(u_p - u) o_p / sum_p l_p 2^(u_p - u) over a unit's parts p. A block takes
-// eight rows of a unit, a lane four features of one of them, so that the loads of a
-// warp are whole 128-byte lines (a warp for each row, with the part's rows 16 bytes a lane: 74
-// against 69 us for 16 requests of 4096 tokens with 26 drafts). It waits for memory, not for
-// its bandwidth: the first three parts are sent for before their weights are known, and four
-// blocks fit an SM (five spill: 70 us; three: 71 us). It takes 8 of those 69 us, and 2 of a
-// small call's 12.5.
+// o = sum_p l_p 2^(u_p - u) o_p / sum_p l_p 2^(u_p - u) over a unit's parts p. A block looks at what
+// one CTA has left and takes eight rows of the unit that it began, if others went on with it; a
+// lane four features of one of them, so that the loads of a warp are whole 128-byte lines (a warp
+// for each row, with the part's rows 16 bytes a lane: 5 us more for 16 requests of 4096 tokens with 26
+// drafts). It waits for memory, not for its bandwidth: the first three parts are sent for before
+// their weights are known, and four blocks fit an SM (five spill: 1.5 us more; three: 2 us).
 template <int ELEM, int CODE>
 __global__ void __launch_bounds__(32 * kT8Walkers, 4) k_tree8_join(const __grid_constant__ Cache8View c, const __grid_constant__ Tree8Args a,
-                                                                   int part_rows, const int* plan, int main_grid, unsigned groups) {
+                                                                   int part_rows, const int* plan, const TreeRecord* records) {
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane & 7, lq = lane >> 3, G = c.G, hq = c.hkv * G;
-  const unsigned per_head = (unsigned)(a.max_nodes * G + 7) / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane & 7, lq = lane >> 3, G = c.G;
+  const int octets = part_rows / 8, c0 = blockIdx.x / octets, o8 = 8 * (blockIdx.x - c0 * octets);
   pdl_wait();
-  const TreeTotal all{plan[a.n_req], plan[kMaxCallReq + 1 + a.n_req]};
-  const int error = *(volatile int*)c.status;
+  const TreeRecord rec = records[c0];
   // (an error of this call or an earlier one: results are undefined)
-  if (error != 0) return;
-  const int ctas = all.ctas(main_grid), turn = all.turn(main_grid), total = all.steps + turn * all.units;
-#pragma unroll 1
-  for (unsigned x = blockIdx.x; x < groups; x += gridDim.x) {
-    const unsigned y = x / per_head, i = y / c.hkv;
-    const int h = y - i * c.hkv, row0 = 8 * (x - y * per_head), row = row0 + lr;
-    const int first = plan[i], units = plan[kMaxCallReq + 1 + i];
-    const TreeReq req = tree_req(c, a, i);
-    if (row0 >= req.M * G) continue;         // (the same for the block)
-    const bool real = row < req.M * G;
-    const TreeTiles tiles = tree_tiles(req.N, req.M, c.T, a.window, a.sinks);
-    const int per = (tiles.places + kT8Step - 1) / kT8Step, t = row0 / kT8Rows, r = row - t * kT8Rows;
-    const int unit = h * unit_rows(req.M, G) + t, us = first + unit * per + turn * (units + unit + 1);
-    const int c0 = range_of(total, us, ctas), c1 = range_of(total, us + per - 1, ctas);
-    auto out_of = [&](int x) {
-      const int m = x / G;
-      return a.out + (((size_t)i * a.max_nodes + m) * hq + (size_t)h * G + (x - m * G)) * (2 * kD);
-    };
-    uint8_t* out = out_of(row) + 8 * (4 * warp + lq);
-    uint2 w = make_uint2(0, 0);
+  if (rec.flags == 0 || c.stopped()) return;
+  auto out_of = [&](int i, int h, int row) {
+    const int m = row / G;
+    return a.out + (((size_t)i * a.max_nodes + m) * (c.hkv * G) + (size_t)h * G + (row - m * G)) * (2 * kD);
+  };
+  // row `row`, if it is one, by a warp
+  auto again = [&](int i, int h, int row, const TreeReq& req, const TreeTiles& tiles) {
+    if (row >= req.M * G) return;
+    uint8_t* out = out_of(i, h, row);
+    const uint2 z = *reinterpret_cast<const uint2*>(out + 8 * lane);
     uint32_t bad = 0;
-    if (c0 == c1) {
-      if (real) w = *reinterpret_cast<const uint2*>(out);
-    } else {
-      // the first part begins its unit (place 1), the others go on with it (place 0)
-      const size_t place = (size_t)part_rows * (kD + 2) / 4;
-      const float4* parts = reinterpret_cast<const float4*>(a.part) + (real ? r : 0);
-      auto part = [&](int cta) { return parts + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * place; };
-      auto weight_of = [&](int cta) {
-        const float4* p = reinterpret_cast<const float4*>(a.part) + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * place + part_rows * (kD / 4);
-        return reinterpret_cast<const float2*>(p)[real ? r : 0];
-      };
-      const int at = (4 * warp + lq) * part_rows;
-      // most units have few parts: their rows are on their way while the weights are
-      constexpr int kNear = 3;
-      float4 v[kNear];
-      float2 ul[kNear];
+    find_not_finite<ELEM>(bad, z.x);
+    find_not_finite<ELEM>(bad, z.y);
+    if (!__any_sync(0xffffffffu, found_not_finite(bad))) return;
+    const Walk<ELEM, CODE> walk{c, a, i, h, lane, req, tiles};
+    walk.row(row / G, row % G, out);
+  };
+  const int row0 = rec.t * kT8Rows + o8, row = row0 + lr;
+  if ((rec.flags & 1) && row0 < rec.M * G) {
+    const int c1 = rec.last, r = o8 + lr;
+    const bool real = row < rec.M * G;
+    uint8_t* out = out_of(rec.i, rec.h, row) + 8 * (4 * warp + lq);
+    // the first part begins its unit (place 1), the others go on with it (place 0)
+    const size_t place = (size_t)part_rows * (kD + 2) / 4;
+    const float4* parts = reinterpret_cast<const float4*>(a.part);
+    auto part = [&](int cta) { return parts + (size_t)(2 * cta + (cta == c0 ? 1 : 0)) * place; };
+    auto weight_of = [&](int cta) { return reinterpret_cast<const float2*>(part(cta) + part_rows * (kD / 4))[real ? r : 0]; };
+    const int at = (4 * warp + lq) * part_rows + (real ? r : 0);
+    // most units have few parts: their rows are on their way while the weights are
+    constexpr int kNear = 3;
+    float4 v[kNear];
+    float2 ul[kNear];
 #pragma unroll
-      for (int e = 0; e < kNear; e++) {
-        v[e] = part(min(c0 + e, c1))[at];
-        ul[e] = weight_of(min(c0 + e, c1));
-      }
-      float top = -INFINITY, sum = 0.0f;
-      auto more = [&](float2 z) {
-        const float now = fmaxf(top, z.x);
-        sum = sum == 0.0f ? 0.0f : sum * (top == now ? 1.0f : fast_exp2(top - now));
-        sum += z.y == 0.0f ? 0.0f : z.y * (z.x == now ? 1.0f : fast_exp2(z.x - now));
-        top = now;
-      };
-      if (c1 - c0 < kNear) {
-#pragma unroll
-        for (int e = 0; e < kNear; e++)
-          if (c0 + e <= c1) more(ul[e]);
-      } else {
-        for (int b = c0 + lq; b <= c1; b += 4) more(weight_of(b));
-#pragma unroll
-        for (int d = 8; d <= 16; d <<= 1) {
-          const float ot = __shfl_xor_sync(0xffffffffu, top, d), os = __shfl_xor_sync(0xffffffffu, sum, d);
-          more(make_float2(ot, os));
-        }
-      }
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      auto add = [&](const float4& y, const float2& z) {
-        const float f = z.y == 0.0f ? 0.0f : __fdiv_rn(z.y * (z.x == top ? 1.0f : fast_exp2(z.x - top)), sum);
-        o.x = fmaf(y.x, f, o.x);
-        o.y = fmaf(y.y, f, o.y);
-        o.z = fmaf(y.z, f, o.z);
-        o.w = fmaf(y.w, f, o.w);
-      };
+    for (int e = 0; e < kNear; e++) {
+      v[e] = part(min(c0 + e, c1))[at];
+      ul[e] = weight_of(min(c0 + e, c1));
+    }
+    float top = -INFINITY, sum = 0.0f;
+    auto more = [&](float2 z) {
+      const float now = fmaxf(top, z.x);
+      sum = sum == 0.0f ? 0.0f : sum * (top == now ? 1.0f : fast_exp2(top - now));
+      sum += z.y == 0.0f ? 0.0f : z.y * (z.x == now ? 1.0f : fast_exp2(z.x - now));
+      top = now;
+    };
+    if (c1 - c0 < kNear) {
 #pragma unroll
       for (int e = 0; e < kNear; e++)
-        if (c0 + e <= c1) add(v[e], ul[e]);
-#pragma unroll 4
-      for (int b = c0 + kNear; b <= c1; b++) add(part(b)[at], weight_of(b));
-      w = make_uint2(pack_elems<ELEM>(in_range<ELEM>(o.x), in_range<ELEM>(o.y)), pack_elems<ELEM>(in_range<ELEM>(o.z), in_range<ELEM>(o.w)));
-      if (real) *reinterpret_cast<uint2*>(out) = w;
+        if (c0 + e <= c1) more(ul[e]);
+    } else {
+      for (int b = c0 + lq; b <= c1; b += 4) more(weight_of(b));
+#pragma unroll
+      for (int d = 8; d <= 16; d <<= 1) {
+        const float ot = __shfl_xor_sync(0xffffffffu, top, d), os = __shfl_xor_sync(0xffffffffu, sum, d);
+        more(make_float2(ot, os));
+      }
     }
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float4& y, const float2& z) {
+      const float f = z.y == 0.0f ? 0.0f : __fdiv_rn(z.y * (z.x == top ? 1.0f : fast_exp2(z.x - top)), sum);
+      o.x = fmaf(y.x, f, o.x);
+      o.y = fmaf(y.y, f, o.y);
+      o.z = fmaf(y.z, f, o.z);
+      o.w = fmaf(y.w, f, o.w);
+    };
+#pragma unroll
+    for (int e = 0; e < kNear; e++)
+      if (c0 + e <= c1) add(v[e], ul[e]);
+#pragma unroll 4
+    for (int b = c0 + kNear; b <= c1; b++) add(part(b)[at], weight_of(b));
+    const uint2 w = make_uint2(pack_elems<ELEM>(in_range<ELEM>(o.x), in_range<ELEM>(o.y)), pack_elems<ELEM>(in_range<ELEM>(o.z), in_range<ELEM>(o.w)));
+    if (real) *reinterpret_cast<uint2*>(out) = w;
+    uint32_t bad = 0;
     find_not_finite<ELEM>(bad, w.x);
     find_not_finite<ELEM>(bad, w.y);
     if (__builtin_expect(__syncthreads_or(real && found_not_finite(bad)), 0)) {
-      // a warp a row
-      uint8_t* mine = out_of(row0 + warp);
-      if (row0 + warp < req.M * G) {
-        const uint2 z = *reinterpret_cast<const uint2*>(mine + 8 * lane);
-        uint32_t b2 = 0;
-        find_not_finite<ELEM>(b2, z.x);
-        find_not_finite<ELEM>(b2, z.y);
-        if (__any_sync(0xffffffffu, found_not_finite(b2))) {
-          const int m = (row0 + warp) / G;
-          const Walk<ELEM, CODE> walk{c, a, (int)i, h, lane, req, tiles};
-          walk.row(m, row0 + warp - m * G, mine);
-        }
+      const TreeReq req = tree_req(c, a, rec.i);
+      again(rec.i, rec.h, row0 + warp, req, tree_tiles(req.N, req.M, c.T, a.window, a.sinks));
+    }
+  }
+  if (__builtin_expect(rec.flags & 2, 0)) {
+#pragma unroll 1
+    for (int pos = rec.lo; pos < rec.hi;) {
+      int i = 0, end = a.n_req;
+#pragma unroll 1
+      while (end - i > 1) {      // as in tree_item
+        const int mid = (i + end) >> 1;
+        if (plan[mid] <= pos) i = mid; else end = mid;
       }
+      const TreeReq req = tree_req(c, a, i);
+      const TreeTiles tiles = tree_tiles(req.N, req.M, c.T, a.window, a.sinks);
+      const int per = (tiles.places + kT8Step - 1) / kT8Step, x = pos - plan[i], unit = x / per, s0 = x - unit * per, n = min(per - s0, rec.hi - pos);
+      const int rt = unit_rows(req.M, G), h = unit / rt;
+      if (n == per) again(i, h, (unit - h * rt) * kT8Rows + o8 + warp, req, tiles);
+      pos += n;
     }
   }
 }
 
 int part_rows_of(int G, int max_nodes) { return std::min(kT8Rows, (max_nodes * G + 31) / 32 * 32); }
 
-// The workspace: the plan's two prefix sums, then two parts a CTA.
-constexpr size_t kT8PlanBytes = ((kMaxCallReq + 1) * 8 + 255) / 256 * 256;
+// The workspace: the steps' prefix sums, then a record and two parts a CTA.
+constexpr size_t kT8PlanBytes = ((kMaxCallReq + 1) * 4 + 255) / 256 * 256;
 
 template <int ELEM, int CODE>
 cudaError_t tree_typed(const Cache8View& c, Tree8Args a, int sm_count, cudaStream_t st) {
@@ -1442,22 +1464,21 @@ cudaError_t tree_typed(const Cache8View& c, Tree8Args a, int sm_count, cudaStrea
   if (e != cudaSuccess) return e;
   const int part_rows = part_rows_of(c.G, a.max_nodes);
   int* plan = reinterpret_cast<int*>(a.part);
-  a.part += kT8PlanBytes / 4;
+  TreeRecord* records = reinterpret_cast<TreeRecord*>(a.part + kT8PlanBytes / 4);
+  a.part += kT8PlanBytes / 4 + sm_count * (sizeof(TreeRecord) / 4);
   // no more CTAs than the longest lengths that the table holds could use
   const long long tiles = ((long long)c.width * c.T + a.max_nodes) / kSub + 3;
   const long long steps = (long long)a.n_req * c.hkv * ((a.max_nodes * c.G + kT8Rows - 1) / kT8Rows) * (tiles / kT8Step + 1);
   const int grid = (int)std::min<long long>(sm_count, steps);
-  e = launch_dependent(k_tree8<ELEM, CODE>, dim3(grid), dim3(kT8Threads), kT8Smem, st, c, a, part_rows, plan);
+  e = launch_dependent(k_tree8<ELEM, CODE>, dim3(grid), dim3(kT8Threads), kT8Smem, st, c, a, part_rows, plan, records);
   if (e != cudaSuccess) return e;
-  const unsigned groups = (unsigned)a.n_req * c.hkv * ((a.max_nodes * c.G + 7) / 8);
-  const unsigned blocks = std::min(groups, (unsigned)sm_count * 20u);
-  return launch_dependent(k_tree8_join<ELEM, CODE>, dim3(blocks), dim3(32 * kT8Walkers), 0, st, c, a, part_rows, plan, grid, groups);
+  return launch_dependent(k_tree8_join<ELEM, CODE>, dim3(grid * (part_rows / 8)), dim3(32 * kT8Walkers), 0, st, c, a, part_rows, plan, records);
 }
 
 }  // namespace
 
 size_t tree8_workspace(int G, int max_nodes, int sm_count) {
-  return kT8PlanBytes + (size_t)sm_count * 2 * part_rows_of(G, max_nodes) * (kD + 2) * 4;
+  return kT8PlanBytes + (size_t)sm_count * (sizeof(TreeRecord) + 2 * part_rows_of(G, max_nodes) * (kD + 2) * 4);
 }
 
 cudaError_t launch_tree8(const Cache8View& c, int elem, int code, int sm_count, const Tree8Args& a, cudaStream_t st) {
