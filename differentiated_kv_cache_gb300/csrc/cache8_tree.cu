@@ -22,16 +22,17 @@
 // masks 1300), and the wait from the weights through the products to the next S. Between two
 // units of a CTA lie 10000 cycles, ahead of the first step 20000: the launch, the plan, a
 // chain of four loads, and code that all SMs fetch at once. Measured:
-//   8 heads, G = 4, fp16, e4m3, 16 requests of 4096 tokens, 26 drafts    69 us (by bytes 21)
-//   8 heads, G = 8, bf16, int8, 8 of 32768, 64 drafts                   565 us, 976 TFLOP/s
-//     (51 % of a plain matrix product's rate)
-//   4 heads, G = 7, bf16, e4m3, 32 of 1024 to 16384, window 4096         63 us
-//   8 heads, G = 5, fp16, int8, 64 of 1 to 3000, chains of 5             99 us
-//   8 heads, G = 4, fp16, e4m3, one of 300 tokens, 8 drafts              12.5 us
+//   8 heads, G = 4, fp16, e4m3, 16 requests of 4096 tokens, 26 drafts    57 us (by bytes 21)
+//   8 heads, G = 8, bf16, int8, 8 of 32768, 64 drafts                   545 us, 1010 TFLOP/s
+//     (53 % of a plain matrix product's rate)
+//   4 heads, G = 7, bf16, e4m3, 32 of 1024 to 16384, window 4096         51 us
+//   8 heads, G = 5, fp16, int8, 64 of 1 to 3000, chains of 5             83 us
+//   8 heads, G = 4, fp16, e4m3, one of 300 tokens, 8 drafts              11.2 us
 // Tried and slower: 64 tokens a step (the second: 0.92 ms); conversion by the softmax warps
 // (the chains: 196 us); maxima of each step ahead of its weights (the second: 0.66 ms; now
 // they are taken when a weight could leave fp16's range); conversion unrolled over its tiles
-// (0.62 ms: it leaves the instruction caches); ranges of equal steps (the chains: 126 us).
+// (0.62 ms: it leaves the instruction caches); ranges of equal steps (the chains: 126 us); the
+// tails' and drafts' largest values looked for ahead of all copies (the third: 68 us).
 #include <algorithm>
 
 #include "cache8.cuh"
@@ -540,15 +541,14 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t& a, uint32_t& b, 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-// largest finite magnitude of bf16 pairs, as bits
-__device__ __forceinline__ uint32_t amax2_finite(uint32_t m, uint32_t w) {
-  w &= 0x7fff7fffu;
-  return __vmaxu2(m, w & ~__vcmpgeu2(w, 0x7f807f80u));
-}
-// exponent of the power of two that brings the largest magnitude (of a warp) to [128, 256)
-__device__ __forceinline__ int scale_exp(uint32_t m) {
-  const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-  return max(-120, (int)(top >> 7) - (127 + 7));
+// Largest finite magnitude of a lane's bf16 values, as bits: with the exponent's last bit added to
+// the bits of the magnitudes, infinities and NaN are negative numbers of 16 bits.
+template <int N>
+__device__ __forceinline__ uint32_t amax_bits(const uint32_t (&x)[N]) {
+  uint32_t m = 0x00800080u;
+#pragma unroll
+  for (int f = 0; f < N; f++) asm("max.s16x2 %0, %0, %1;\n" : "+r"(m) : "r"((x[f] & 0x7fff7fffu) + 0x00800080u));
+  return max(m & 0xffffu, m >> 16) - 0x80u;
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 __device__ __forceinline__ uint32_t half_of_bf16(uint32_t w, float f) {
@@ -630,12 +630,10 @@ __device__ __forceinline__ void load_drafts(const uint8_t* src, int n, long long
     x[4 * e + 3] = y.w;
   }
 }
-// The exponent of the power of two that bf16 values are divided by.
+// The exponent of the power of two that a tile's bf16 values are divided by: the largest
+// comes to [128, 256).
 __device__ __forceinline__ int exp_of(const uint32_t (&x)[32]) {
-  uint32_t am = 0;
-#pragma unroll
-  for (int f = 0; f < 32; f++) am = amax2_finite(am, x[f]);
-  return scale_exp(am);
+  return max(-120, (int)(__reduce_max_sync(0xffffffffu, amax_bits(x)) >> 7) - (127 + 7));
 }
 __device__ __noinline__ int elems_exp(const uint8_t* src, bool v, bool draft, int n, long long stride) {
   uint32_t x[32];
@@ -815,11 +813,15 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         for (int e = 0; e < 8; e++) qr[e] = real ? src[e] : make_uint4(0, 0, 0, 0);
         float inv = 1.0f;
         if (ELEM == DKV_BF16) {
-          uint32_t am = 0;
+          uint32_t x[32];
 #pragma unroll
-          for (int e = 0; e < 8; e++)
-            am = amax2_finite(amax2_finite(amax2_finite(amax2_finite(am, qr[e].x), qr[e].y), qr[e].z), qr[e].w);
-          const float mine = __uint_as_float(max(am & 0xffffu, am >> 16));
+          for (int e = 0; e < 8; e++) {
+            x[4 * e] = qr[e].x;
+            x[4 * e + 1] = qr[e].y;
+            x[4 * e + 2] = qr[e].z;
+            x[4 * e + 3] = qr[e].w;
+          }
+          const float mine = __uint_as_float(amax_bits(x));
           sm.pair[told][part][r].x = mine;
           named_sync(pair_bar, 64);
           const uint32_t most = max(__float_as_uint(mine), __float_as_uint(sm.pair[told][part ^ 1][r].x));
