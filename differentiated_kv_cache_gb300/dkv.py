@@ -465,7 +465,8 @@ def _axes8(cache, positions, pair_axis, n_tok):
     if positions.shape not in ((axes, n_tok), (n_tok,)):
         raise ValueError(f"positions must be [axes][{n_tok}], got {tuple(positions.shape)}")
     if pair_axis is not None:
-        pair_axis = bytes(pair_axis)
+        if type(pair_axis) is not bytes:
+            pair_axis = bytes(list(pair_axis))      # (not an array's raw bytes, not a number of zeros)
         if len(pair_axis) != cache.pairs:
             raise ValueError(f"pair_axis has one entry for each of {cache.pairs} pairs")
     return _on(cache, positions, torch.int32, "positions"), axes, pair_axis

@@ -122,3 +122,19 @@ def test_reference_trees():
 def test_windows_beyond_32_bits_are_refused():
     with pytest.raises(ValueError):
         dkv.dkv_cache8_tree(None, None, None, None, None, None, None, window=2 ** 32)
+
+
+def test_pair_axes_are_numbers_one_by_one():
+    import torch
+    from types import SimpleNamespace
+    cache = SimpleNamespace(pairs=8, dev=-1)
+    pos = torch.zeros((3, 5), dtype=torch.int32)
+    want = bytes([0, 1, 2, 2, 1, 0, 0, 1])
+    for given in (want, list(want), tuple(want), np.frombuffer(want, np.uint8).astype(np.int32), torch.tensor(list(want))):
+        at, axes, got = dkv.dkv._axes8(cache, pos, given, 5)
+        assert (axes, got) == (3, want)
+    for bad in (8, [0.5] * 8, [300] * 8, [-1] * 8, [0] * 7, np.zeros(2, np.int32)):
+        with pytest.raises((TypeError, ValueError)):
+            dkv.dkv._axes8(cache, pos, bad, 5)
+    with pytest.raises(ValueError):
+        dkv.dkv._axes8(cache, pos, want, 6)
