@@ -22,12 +22,12 @@
 // masks 1300), and the wait from the weights through the products to the next S. Between two
 // units of a CTA lie 10000 cycles, ahead of the first step 20000: the launch, the plan, a
 // chain of four loads, and code that all SMs fetch at once. Measured:
-//   8 heads, G = 4, fp16, e4m3, 16 requests of 4096 tokens, 26 drafts    57 us (by bytes 21)
-//   8 heads, G = 8, bf16, int8, 8 of 32768, 64 drafts                   545 us, 1010 TFLOP/s
+//   8 heads, G = 4, fp16, e4m3, 16 requests of 4096 tokens, 26 drafts    58 us (by bytes 21)
+//   8 heads, G = 8, bf16, int8, 8 of 32768, 64 drafts                   542 us, 1020 TFLOP/s
 //     (53 % of a plain matrix product's rate)
-//   4 heads, G = 7, bf16, e4m3, 32 of 1024 to 16384, window 4096         51 us
-//   8 heads, G = 5, fp16, int8, 64 of 1 to 3000, chains of 5             83 us
-//   8 heads, G = 4, fp16, e4m3, one of 300 tokens, 8 drafts              11.2 us
+//   4 heads, G = 7, bf16, e4m3, 32 of 1024 to 16384, window 4096         53 us
+//   8 heads, G = 5, fp16, int8, 64 of 1 to 3000, chains of 5             84 us
+//   8 heads, G = 4, fp16, e4m3, one of 300 tokens, 8 drafts              11.5 us
 // Tried and slower: 64 tokens a step (the second: 0.92 ms); conversion by the softmax warps
 // (the chains: 196 us); maxima of each step ahead of its weights (the second: 0.66 ms; now
 // they are taken when a weight could leave fp16's range); conversion unrolled over its tiles
@@ -168,198 +168,201 @@ __device__ __forceinline__ uint32_t sees_stored(const Tree8Args& a, int N, int d
   return s;
 }
 
-// ---- one row by one warp, from the formula: what the products below are checked
-// against, and what computes rows that come out infinite or NaN (a value that a row does
-// not see may have met its weight of 0) ----
-// A lane's share of a tile in the stored order, as values: K of tokens g and g + 8,
-// features 16 m + 2 t + {0, 1, 8, 9}; V of features 16 m + g, + 8 and tokens 2t, 2t + 1,
-// 2t + 8, 2t + 9.
+// ---- one row by a block of the second kernel, from the formula in fp32, over what the row sees:
+// rows that came out infinite or NaN (a code that a row does not see may have met its weight of
+// 0). A warp takes every eighth tile, 32 of which it looks up at once, a lane each; the eight join.
+// 4096 tokens take a row 55 us; a warp a row, its code unrolled over all kinds of tiles, took 3300:
+// a tile was 100 KB of instructions. ----
+// A lane's share of a tile in the stored order: K of tokens g and g + 8, features
+// 16 m + 2 t + {0, 1, 8, 9}; V of features 16 m + g, + 8 and tokens 2t, 2t + 1, 2t + 8, 2t + 9.
+struct WalkSmem {
+  float q[kD], o[kT8Walkers][kD], top[kT8Walkers], sum[kT8Walkers];
+};
 template <int ELEM, int CODE>
 struct Walk {
   const Cache8View& c;
   const Tree8Args& a;
-  int i, h, lane;
+  int i, h;
   TreeReq r;
   TreeTiles t;
 
-  // words of m-step m: [0], [1] row g, columns 2t and 2t + 8; [2], [3] row g + 8
-  __device__ __forceinline__ void words(const uint8_t* codes, const uint8_t* tail, int op, int m, float (&v)[8]) const {
-    if (codes) {
-      const uint2 w = *reinterpret_cast<const uint2*>(codes + op * kTile + 512 * (m >> 1) + 16 * lane + 8 * (m & 1));
-      uint32_t x[4];
-      code_halves<CODE>(w.x, x[0], x[1]);
-      code_halves<CODE>(w.y, x[2], x[3]);
+  // Words 4 m + (0 .. 3) of K or V (op): the four pairs of m-step m, in fp16 where they were codes.
+  __device__ __forceinline__ void words(unsigned long long at, int kind, int n, bool op, uint32_t (&x)[32]) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, tt = lane & 3;
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(at);
+    if (kind < 2) {
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        v[2 * e] = lo_elem<DKV_F16>(x[e]);
-        v[2 * e + 1] = hi_elem<DKV_F16>(x[e]);
+        const uint4 w = *reinterpret_cast<const uint4*>(p + op * kTile + 512 * e + 16 * lane);
+        code_halves<CODE>(w.x, x[8 * e], x[8 * e + 1]);
+        code_halves<CODE>(w.y, x[8 * e + 2], x[8 * e + 3]);
+        code_halves<CODE>(w.z, x[8 * e + 4], x[8 * e + 5]);
+        code_halves<CODE>(w.w, x[8 * e + 6], x[8 * e + 7]);
+      }
+    } else if (kind == 2) {
+#pragma unroll
+      for (int m = 0; m < 8; m++) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p + 2 * op * kTile + 512 * m + 16 * lane);
+        x[4 * m] = w.x;
+        x[4 * m + 1] = w.y;
+        x[4 * m + 2] = w.z;
+        x[4 * m + 3] = w.w;
+      }
+    } else if (!op) {             // drafts, of which those from n on are not read
+#pragma unroll
+      for (int f = 0; f < 32; f++) {
+        const int row = f & 2 ? g + 8 : g;
+        x[f] = row < n ? *reinterpret_cast<const uint32_t*>(p + row * a.ks + 32 * (f >> 2) + 16 * (f & 1) + 4 * tt) : 0u;
       }
     } else {
-      const uint4 w = *reinterpret_cast<const uint4*>(tail + 2 * op * kTile + 512 * m + 16 * lane);
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        v[2 * e] = lo_elem<ELEM>(x[e]);
-        v[2 * e + 1] = hi_elem<ELEM>(x[e]);
+      for (int f = 0; f < 32; f++) {
+        const int row = 2 * tt + 8 * (f & 1), at2 = 2 * (16 * (f >> 2) + 8 * (f >> 1 & 1) + g);
+        const uint32_t lo = row < n ? *reinterpret_cast<const uint16_t*>(p + row * a.vs + at2) : 0u;
+        const uint32_t hi = row + 1 < n ? *reinterpret_cast<const uint16_t*>(p + (row + 1) * a.vs + at2) : 0u;
+        x[f] = lo | hi << 16;
       }
     }
-  }
-  // the same of drafts, of which those from n on are not read
-  __device__ __forceinline__ void draft_k(int m0, int n, int m, float (&v)[8]) const {
-    const int g = lane >> 2, tt = lane & 3;
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-      const int x = g + 8 * (e >> 1);
-      uint32_t w = 0;
-      if (x < n)
-        w = *reinterpret_cast<const uint32_t*>(a.k + ((long long)i * a.max_nodes + m0 + x) * a.ks + h * (2 * kD) +
-                                               2 * (16 * m + 2 * tt + 8 * (e & 1)));
-      v[2 * e] = lo_elem<ELEM>(w);
-      v[2 * e + 1] = hi_elem<ELEM>(w);
-    }
-  }
-  __device__ __forceinline__ void draft_v(int m0, int n, int m, float (&v)[8]) const {
-    const int g = lane >> 2, tt = lane & 3;
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const int x = 2 * tt + (e & 1) + 8 * (e >> 1 & 1), f = 16 * m + g + 8 * (e >> 2);
-      v[e] = x < n ? elem_float<ELEM>(*reinterpret_cast<const uint16_t*>(
-                         a.v + ((long long)i * a.max_nodes + m0 + x) * a.vs + h * (2 * kD) + 2 * f))
-                   : 0.0f;
-    }
-  }
-  struct At {
-    const uint8_t *codes, *tail;
-    float2 sc;
-    int m0, n;        // drafts
-    uint32_t see;
-  };
-  __device__ __forceinline__ At at(int x, const Node& node) const {
-    At p{nullptr, nullptr, make_float2(1.0f, 1.0f), 0, 0, 0};
-    if (x >= t.stored) {
-      p.m0 = (x - t.stored) * kSub;
-      p.n = min(r.M - p.m0, kSub);
-      const int w = p.m0 >> 5;
-      p.see = (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (p.m0 & 31) & 0xffffu;
-      return p;
-    }
-    const int tile = t.tile(x);
-    p.see = sees_stored(a, r.N, node.depth, tile * kSub);
-    if (tile < t.full) {
-      const int per = c.T / kSub;
-      int page = c.table[(size_t)r.slot * c.width + tile / per];
-      if ((unsigned)page >= (unsigned)c.n_pages) {
-        c.latch(DKV_ERR_CHECK, i);
-        page = 0;
-      }
-      p.sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * c.hkv + h));
-      p.codes = c.pages + c.page_head(page, h) + (size_t)(tile % per) * (2 * kTile);
-    } else {
-      p.tail = c.tail + c.tail_head(r.slot, h) + (size_t)(tile - t.full) * (4 * kTile);
-    }
-    return p;
   }
 
-  // base-2 logits of tokens g and g + 8 (-Inf where they are not seen); q: the lane's
-  // features in the order of `words`, over a power of two that qs brings back
-  __device__ __forceinline__ float2 logits(const At& p, const float (&q)[32], float qs) const {
-    float x = 0.0f, y = 0.0f;
+  __device__ __noinline__ void row(int m, int g8, uint8_t* out, WalkSmem& sm) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tt = lane & 3;
+    const Node node = node_of(c, a, a.parents ? a.parents + (size_t)i * a.max_nodes : nullptr, i, r.N, m);
+    // the query over a power of two (bf16), which `back` brings back
+    const uint8_t* qp = a.q + ((long long)i * a.max_nodes + m) * a.qs + ((size_t)h * c.G + g8) * (2 * kD);
+    const uint2 qw = *reinterpret_cast<const uint2*>(qp + 8 * lane);
+    float q[4] = {lo_elem<ELEM>(qw.x), hi_elem<ELEM>(qw.x), lo_elem<ELEM>(qw.y), hi_elem<ELEM>(qw.y)}, qs = 1.0f;
     // bf16 keys may be as large as fp32: 2^-8 of them
     constexpr float kIn = ELEM == DKV_BF16 ? 0.00390625f : 1.0f;
-#pragma unroll
-    for (int m = 0; m < 8; m++) {
-      float v[8];
-      if (p.codes || p.tail) words(p.codes, p.tail, 0, m, v);
-      else draft_k(p.m0, p.n, m, v);
-#pragma unroll
-      for (int e = 0; e < 4; e++) {
-        x = fmaf(q[4 * m + e], v[e] * kIn, x);
-        y = fmaf(q[4 * m + e], v[4 + e] * kIn, y);
-      }
-    }
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    y += __shfl_xor_sync(0xffffffffu, y, 1);
-    x += __shfl_xor_sync(0xffffffffu, x, 2);
-    y += __shfl_xor_sync(0xffffffffu, y, 2);
-    // (neither factor is infinite, nor x by the first: a logit is infinite only if the formula's is)
-    const float f = p.sc.x * kLogitScale, back = qs * (1.0f / kIn);
-    const int g = lane >> 2;
-    return make_float2(p.see >> g & 1u ? x * f * back : -INFINITY, p.see >> (g + 8) & 1u ? y * f * back : -INFINITY);
-  }
-
-  __device__ __noinline__ void row(int m, int g8, uint8_t* out) const {
-    const int g = lane >> 2, tt = lane & 3;
-    const Node node = node_of(c, a, a.parents ? a.parents + (size_t)i * a.max_nodes : nullptr, i, r.N, m);
-    float q[32], am = 0.0f;
-    const uint8_t* qp = a.q + ((long long)i * a.max_nodes + m) * a.qs + ((size_t)h * c.G + g8) * (2 * kD);
-#pragma unroll
-    for (int e = 0; e < 16; e++) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(qp + 2 * (16 * (e >> 1) + 8 * (e & 1) + 2 * tt));
-      q[2 * e] = lo_elem<ELEM>(w);
-      q[2 * e + 1] = hi_elem<ELEM>(w);
-      am = amax_finite(amax_finite(am, q[2 * e]), q[2 * e + 1]);
-    }
-    float qs = 1.0f;
     if (ELEM == DKV_BF16) {
-      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-      am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-      const int ex = max(-126, min(118, (int)(__float_as_uint(am) >> 23) - 127));
+      const float am = amax_finite(amax_finite(amax_finite(amax_finite(0.0f, q[0]), q[1]), q[2]), q[3]);
+      const int ex = max(-126, min(118, (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(am)) >> 23) - 127));
       const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
       qs = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
-      for (int e = 0; e < 32; e++) q[e] *= inv;
+      for (int e = 0; e < 4; e++) q[e] *= inv;
     }
-    float top = -INFINITY, l = 0.0f;
-#pragma unroll 1
-    for (int x = 0; x < t.count; x++) {
-      const At p = at(x, node);
-      if (!p.see) continue;
-      const float2 y = logits(p, q, qs);
-      const float now = fmaxf(top, fmaxf(y.x, y.y));
-      if (now > -INFINITY) l = l * fast_exp2(top - now) + fast_exp2(y.x - now) + fast_exp2(y.y - now);
-      else l += y.x + y.y == -INFINITY ? 0.0f : y.x + y.y;      // NaN
-      top = now;
-    }
-    // the warp's maximum and sum: lanes of one t hold the tokens once
-    float all = top;
-#pragma unroll
-    for (int d = 4; d <= 16; d <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, d));
-    l = top == all ? l : l * fast_exp2(top - all);
-#pragma unroll
-    for (int d = 4; d <= 16; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    const float inv = __fdiv_rn(1.0f, l);
-    float o[16];
+    __syncthreads();             // (the row before has been written)
+    if (warp == 0) reinterpret_cast<float4*>(sm.q)[lane] = make_float4(q[0], q[1], q[2], q[3]);
+    __syncthreads();
+    const float back = qs * (1.0f / kIn);
+    float top = -INFINITY, l = 0.0f, o[16];
 #pragma unroll
     for (int e = 0; e < 16; e++) o[e] = 0.0f;
 #pragma unroll 1
-    for (int x = 0; x < t.count; x++) {
-      const At p = at(x, node);
-      if (!p.see) continue;
-      const float2 y = logits(p, q, qs);
-      const float px = fast_exp2(y.x - all) * inv, py = fast_exp2(y.y - all) * inv;
-      float w[4];
-      w[0] = __shfl_sync(0xffffffffu, px, 8 * tt);
-      w[1] = __shfl_sync(0xffffffffu, px, 8 * tt + 4);
-      w[2] = __shfl_sync(0xffffffffu, py, 8 * tt);
-      w[3] = __shfl_sync(0xffffffffu, py, 8 * tt + 4);
-      bool see[4];
+    for (int b = warp; b < t.count; b += 32 * kT8Walkers) {
+      // the lane's tile: where it lies, what scales it, which of its tokens the row sees
+      const int mine = b + kT8Walkers * lane;
+      unsigned long long k_at = 0, v_at = 0;
+      float2 sc = make_float2(1.0f, 1.0f);
+      uint32_t see = 0;
+      int kind = 2, n = kSub;
+      if (mine >= t.stored && mine < t.count) {
+        const int m0 = (mine - t.stored) * kSub, w = m0 >> 5;
+        kind = 3;
+        n = min(r.M - m0, kSub);
+        see = (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (m0 & 31) & 0xffffu;
+        k_at = reinterpret_cast<unsigned long long>(a.k + ((long long)i * a.max_nodes + m0) * a.ks + h * (2 * kD));
+        v_at = reinterpret_cast<unsigned long long>(a.v + ((long long)i * a.max_nodes + m0) * a.vs + h * (2 * kD));
+      } else if (mine < t.stored) {
+        const int tile = t.tile(mine), per = c.T / kSub;
+        see = sees_stored(a, r.N, node.depth, tile * kSub);
+        if (tile < t.full) {
+          int page = c.table[(size_t)r.slot * c.width + tile / per];
+          if ((unsigned)page >= (unsigned)c.n_pages) {
+            c.latch(DKV_ERR_CHECK, i);
+            page = 0;
+          }
+          kind = 0;
+          sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * c.hkv + h));
+          k_at = reinterpret_cast<unsigned long long>(c.pages + c.page_head(page, h) + (size_t)(tile % per) * (2 * kTile));
+        } else {
+          k_at = reinterpret_cast<unsigned long long>(c.tail + c.tail_head(r.slot, h) + (size_t)(tile - t.full) * (4 * kTile));
+        }
+        v_at = k_at;
+      }
+#pragma unroll 1
+      for (unsigned left = __ballot_sync(0xffffffffu, see != 0); left; left &= left - 1) {
+        const int who = __ffs(left) - 1;
+        const unsigned long long kp = __shfl_sync(0xffffffffu, k_at, who), vp = __shfl_sync(0xffffffffu, v_at, who);
+        const float ks = __shfl_sync(0xffffffffu, sc.x, who) * kLogitScale, vs = __shfl_sync(0xffffffffu, sc.y, who);
+        const uint32_t seen = __shfl_sync(0xffffffffu, see, who);
+        const int kd = __shfl_sync(0xffffffffu, kind, who), valid = __shfl_sync(0xffffffffu, n, who);
+        const bool halves = ELEM == DKV_F16 || kd < 2;
+        auto lo = [&](uint32_t w) { return halves ? lo_elem<DKV_F16>(w) : lo_elem<DKV_BF16>(w); };
+        auto hi = [&](uint32_t w) { return halves ? hi_elem<DKV_F16>(w) : hi_elem<DKV_BF16>(w); };
+        uint32_t x[32];
+        words(kp, kd, valid, false, x);
+        float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 4; e++) see[e] = p.see >> (2 * tt + (e & 1) + 8 * (e >> 1)) & 1u;
+        for (int f = 0; f < 16; f++) {            // pair f of the lane's features, tokens g and g + 8
+          const float2 qv = *reinterpret_cast<const float2*>(sm.q + 16 * (f >> 1) + 8 * (f & 1) + 2 * tt);
+          const uint32_t w0 = x[4 * (f >> 1) + (f & 1)], w1 = x[4 * (f >> 1) + 2 + (f & 1)];
+          y0 = fmaf(qv.y, hi(w0) * kIn, fmaf(qv.x, lo(w0) * kIn, y0));
+          y1 = fmaf(qv.y, hi(w1) * kIn, fmaf(qv.x, lo(w1) * kIn, y1));
+        }
+        words(vp, kd, valid, true, x);
+        y0 += __shfl_xor_sync(0xffffffffu, y0, 1);
+        y1 += __shfl_xor_sync(0xffffffffu, y1, 1);
+        y0 += __shfl_xor_sync(0xffffffffu, y0, 2);
+        y1 += __shfl_xor_sync(0xffffffffu, y1, 2);
+        // (neither factor is infinite, nor a sum by the first: a logit is infinite only if the formula's is)
+        y0 = seen >> g & 1u ? y0 * ks * back : -INFINITY;
+        y1 = seen >> (g + 8) & 1u ? y1 * ks * back : -INFINITY;
+        float now = fmaxf(top, fmaxf(y0, y1));
 #pragma unroll
-      for (int f = 0; f < 8; f++) {
-        float v[8];
-        if (p.codes || p.tail) words(p.codes, p.tail, 1, f, v);
-        else draft_v(p.m0, p.n, f, v);
+        for (int d = 4; d <= 16; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+        if (now > top) {
+          const float f = fast_exp2(top - now);
+          l *= f;
 #pragma unroll
-        for (int e = 0; e < 8; e++)
-          if (see[e & 3]) o[2 * f + (e >> 2)] = fmaf(w[e & 3], v[e] * p.sc.y, o[2 * f + (e >> 2)]);
+          for (int e = 0; e < 16; e++) o[e] *= f;
+          top = now;
+        }
+        const float under = top == -INFINITY ? 0.0f : top;
+        const float p0 = fast_exp2(y0 - under), p1 = fast_exp2(y1 - under);
+        l += p0 + p1;
+        float w[4];
+        w[0] = __shfl_sync(0xffffffffu, p0, 8 * tt) * vs;
+        w[1] = __shfl_sync(0xffffffffu, p0, 8 * tt + 4) * vs;
+        w[2] = __shfl_sync(0xffffffffu, p1, 8 * tt) * vs;
+        w[3] = __shfl_sync(0xffffffffu, p1, 8 * tt + 4) * vs;
+        const uint32_t at = seen >> (2 * tt);
+#pragma unroll
+        for (int f = 0; f < 16; f++) {            // features 16 (f / 2) + 8 (f % 2) + g
+          const uint32_t v0 = x[4 * (f >> 1) + 2 * (f & 1)], v1 = x[4 * (f >> 1) + 2 * (f & 1) + 1];
+          if (at & 1u) o[f] = fmaf(w[0], lo(v0), o[f]);
+          if (at & 2u) o[f] = fmaf(w[1], hi(v0), o[f]);
+          if (at & 256u) o[f] = fmaf(w[2], lo(v1), o[f]);
+          if (at & 512u) o[f] = fmaf(w[3], hi(v1), o[f]);
+        }
       }
     }
+    // lanes of one t hold the tokens once; lanes of one g a feature's tokens
+#pragma unroll
+    for (int d = 4; d <= 16; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
 #pragma unroll
     for (int e = 0; e < 16; e++) {
       o[e] += __shfl_xor_sync(0xffffffffu, o[e], 1);
       o[e] += __shfl_xor_sync(0xffffffffu, o[e], 2);
-      if (tt == (e & 3)) reinterpret_cast<uint16_t*>(out)[8 * e + g] = float_elem<ELEM>(in_range<ELEM>(o[e]));
+      if (tt == (e & 3)) sm.o[warp][8 * e + g] = o[e];
+    }
+    if (lane == 0) {
+      sm.top[warp] = top;
+      sm.sum[warp] = l;
+    }
+    __syncthreads();
+    if (threadIdx.x < kD) {
+      float all = -INFINITY, sum = 0.0f, y = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kT8Walkers; w++) all = fmaxf(all, sm.top[w]);
+#pragma unroll
+      for (int w = 0; w < kT8Walkers; w++) {
+        const float f = sm.top[w] == all ? 1.0f : fast_exp2(sm.top[w] - all);
+        sum = fmaf(sm.sum[w], f, sum);
+        if (sm.top[w] > -INFINITY || sm.sum[w] != 0.0f) y = fmaf(sm.o[w][threadIdx.x], f, y);
+      }
+      reinterpret_cast<uint16_t*>(out)[threadIdx.x] = float_elem<ELEM>(in_range<ELEM>(__fdiv_rn(y, sum)));
     }
   }
 };
@@ -512,7 +515,8 @@ struct TreeSmem {
   int2 scan[32];
   int runs[4];                     // ends of items of the products
   int begun[4];                    // the unit that the CTA's last item begins: 1, request, KV head, rows
-  int bad;
+  int bad, any_taken;
+  int2 taken[16][4];               // of a step's tiles of 16 bits: first token, kind << 16 | tokens whose V was taken out
   // K, V of a step there, no longer needed; S, P, P V of a step there, queries there (two of
   // each, of P V four: a wait is for the last of them, the one before in its place long over);
   // drain
@@ -650,34 +654,78 @@ __device__ __forceinline__ int to_half(uint32_t (&x)[32]) {      // (fp16 stays)
   for (int f = 0; f < 32; f++) x[f] = half_of_bf16(x[f], inv);
   return ex;
 }
-// A tile of the tail as fp16 operands; at: the lane's row of the first four matrices. The
-// exponent that its values were divided by.
+// V that is not finite would meet the weights of rows that do not see it, and 0 times it is not 0:
+// it becomes 0 where it lies in shared memory, and whoever sees its token (bits of 16) is computed
+// again. (Out of the way: instructions fetched with the usual case cost it 5%.)
 template <int ELEM>
-__device__ __noinline__ int put_tail(const uint8_t* src, bool v, int n, uint32_t at) {
-  uint32_t x[32];
-  load_tail(src, v, n, x);
+__device__ __forceinline__ bool none_to_take(const uint32_t (&x)[32]) {
+  uint32_t acc = 0;
+#pragma unroll
+  for (int f = 0; f < 32; f++) find_not_finite<ELEM>(acc, x[f]);
+  return __builtin_expect(!__any_sync(0xffffffffu, found_not_finite(acc)), 1);
+}
+template <int ELEM>
+__device__ __noinline__ uint32_t take_out(uint8_t* src, bool draft, int n) {
+  constexpr uint32_t kExp = ELEM == DKV_F16 ? 0x0400u : 0x0080u;
+  const int lane = threadIdx.x & 31;
+  uint32_t bits = 0;
+#pragma unroll 1
+  for (int e = 0; e < 32; e++) {             // word e % 4 of the lane's 16 bytes of 512
+    uint32_t* at = reinterpret_cast<uint32_t*>(src + 512 * (e >> 2) + 16 * lane) + (e & 3);
+    const int token = draft ? 2 * (e >> 2) + (lane >> 4) : 2 * (lane & 3) + 8 * (e & 1);
+    uint32_t w = *at;
+    if (((w & 0x7fffu) + kExp) & 0x8000u) {
+      w &= 0xffff0000u;
+      bits |= 1u << token;
+    }
+    if (((w >> 16 & 0x7fffu) + kExp) & 0x8000u) {
+      w &= 0xffffu;
+      bits |= 1u << (draft ? token : token + 1);
+    }
+    *at = w;
+  }
+  __syncwarp();
+  return __reduce_or_sync(0xffffffffu, bits) & below(n);
+}
+// A tile of the tail as fp16 operands; at: the lane's row of the first four matrices. Of K the
+// exponent that its values were divided by, of V the tokens with values that are not finite.
+template <int ELEM>
+__device__ __noinline__ int put_tail(uint8_t* src, bool v, int n, uint32_t at) {
+  uint32_t x[32], out = 0;
+#pragma unroll 1
+  while (true) {
+    load_tail(src, v, n, x);
+    if (!v || none_to_take<ELEM>(x)) break;
+    out = take_out<ELEM>(src, false, n);
+  }
   const int ex = to_half<ELEM>(x);
 #pragma unroll
   for (int f = 0; f < 8; f++) {
     if (!v) stmatrix4((at + (f >> 2) * 16384) ^ ((f & 3) << 5), x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
     else stmatrix4(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
   }
-  return ex;
+  return v ? (int)out : ex;
 }
-// Drafts, whose rows of 256 bytes lie at src in shared memory. K's go to their operand rows as they
-// are (to: row 0); V's back to src, row r turned by r times 16 bytes so that the same features of
+// Drafts, whose rows of 256 bytes lie in shared memory. K's go to their operand rows as they
+// are (to: row 0); V's back to there, row r turned by r times 16 bytes so that the same features of
 // eight rows lie in different banks, and from there as transposed matrices (to: as for put_tail).
 // (Both by words straight from the rows, eight lanes on a bank: a step of four draft tiles 4000
 // cycles.)
 template <int ELEM>
-__device__ __noinline__ int put_drafts(uint32_t src, bool v, int n, uint32_t to) {
+__device__ __noinline__ int put_drafts(uint8_t* rows, bool v, int n, uint32_t to) {
   const int lane = threadIdx.x & 31, c = lane & 15;
-  uint32_t x[32];
+  const uint32_t src = smem_u32(rows);
+  uint32_t x[32], out = 0;
+#pragma unroll 1
+  while (true) {
 #pragma unroll
-  for (int e = 0; e < 8; e++) {
-    const int row = 2 * e + (lane >> 4);
-    x[4 * e] = x[4 * e + 1] = x[4 * e + 2] = x[4 * e + 3] = 0;
-    if (row < n) lds128(src + row * (2 * kD) + 16 * c, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+    for (int e = 0; e < 8; e++) {
+      const int row = 2 * e + (lane >> 4);
+      x[4 * e] = x[4 * e + 1] = x[4 * e + 2] = x[4 * e + 3] = 0;
+      if (row < n) lds128(src + row * (2 * kD) + 16 * c, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+    }
+    if (!v || none_to_take<ELEM>(x)) break;
+    out = take_out<ELEM>(rows, true, n);
   }
   const int ex = to_half<ELEM>(x);
   __syncwarp();
@@ -697,7 +745,7 @@ __device__ __noinline__ int put_drafts(uint32_t src, bool v, int n, uint32_t to)
       stmatrix4_trans(to + f * 2048, m[0], m[1], m[2], m[3]);
     }
   }
-  return ex;
+  return v ? (int)out : ex;
 }
 
 template <int ELEM, int CODE>
@@ -742,7 +790,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       mbar_init(smem_u32(&sm.rfull[0][0]) + 8 * s, 1);
       mbar_init(smem_u32(&sm.rfree[0][0]) + 8 * s, 4);
     }
-    sm.fail = sm.bad = sm.begun[0] = 0;
+    sm.fail = sm.bad = sm.any_taken = sm.begun[0] = 0;
     fence_mbar_init();
   }
   if (warp == 16) tmem_alloc(smem_u32(&sm.taddr), 512);
@@ -1017,7 +1065,19 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         const float lsum = l + sm.pair[told][part ^ 1][r].x;
         told ^= 1;
         // a sum that left fp32's range: NaN, which the second kernel looks into
-        const float f = lsum == 0.0f ? 0.0f : lsum < INFINITY ? __fdiv_rn(fast_exp2(mx - kT8Up - u), lsum) : __uint_as_float(0x7fffffffu);
+        float f = lsum == 0.0f ? 0.0f : lsum < INFINITY ? __fdiv_rn(fast_exp2(mx - kT8Up - u), lsum) : __uint_as_float(0x7fffffffu);
+        if (__builtin_expect(*(volatile int*)&sm.any_taken, 0)) {
+          // tiles of 16 bits are a unit's last ones, in five steps at most
+#pragma unroll 1
+          for (int x = 4 * max(end - it.n, end - 8); x < 4 * end; x++) {
+            const int2 d = sm.taken[x >> 2 & 15][x & 3];
+            const int kind = d.y >> 16, w = d.x >> 5;
+            const uint32_t see = kind == 2 ? sees_stored(a, it.N, node.depth, d.x)
+                                 : kind == 3 ? (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (d.x & 31)
+                                             : 0u;
+            if (see & d.y & 0xffffu) f = __uint_as_float(0x7fffffffu);
+          }
+        }
         const bool whole = it.n == it.per;
         uint8_t* out = a.out + (((long long)it.i * a.max_nodes + m) * c.hkv * G + (size_t)it.h * G + (row - m * G)) * (2 * kD) + 128 * part;
         // a part: [feature / 4][row][4], whose lanes' stores are neighbours, then (u, l) of the rows
@@ -1099,7 +1159,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       };
       auto draft_place = [&](int t) { return base + (t >> 2) * 16384 + me * 1024 + mrow * 128 + (((2 * (t & 3) + ms) ^ mrow) << 4); };
       const uint32_t full = op ? vfull(0) : kfull(0), free = op ? vfree(0) : kfree(0);
-      const uint8_t* ring = smem + kT8OffRing + op * (kT8Ring * kT8Entry) + first * kTile;
+      uint8_t* ring = smem + kT8OffRing + op * (kT8Ring * kT8Entry) + first * kTile;
       const uint32_t rfull = smem_u32(sm.rfull[op]), rfree = smem_u32(sm.rfree[op]);
 #pragma unroll 1
       for (int j = 0; ok && j < steps; j++) {
@@ -1107,7 +1167,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         const TileDesc* desc = sm.desc[j & (kT8Descs - 1)] + first;
         // The softmax has to know V's exponents with S: K's warps find them themselves, from where
         // the values lie, while the copies are on their way.
-        int ev = 0, ek = 0;
+        int ev = 0, ek = 0, out = 0;
         if (ELEM == DKV_BF16 && op == 0) {
           if (j % kT8Batch == 0) ok = wait(smem_u32(&sm.dfull[j / kT8Batch & 3]), j / kT8Batch >> 2);
           if (ok && (desc->kind == 2 || desc->kind == 3)) ev = elems_exp(desc->vsrc, true, desc->kind == 3, desc->n, a.vs);
@@ -1119,8 +1179,11 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         const int kind = desc->kind;
         if (kind == 2 || kind == 3) {
           // (the second place is none)
-          if (kind == 2) ek = put_tail<ELEM>(ring + slot * kT8Entry, op, desc->n, to0);
-          else ek = put_drafts<ELEM>(smem_u32(ring + slot * kT8Entry), op, desc->n, (op ? draft_place(first) : base + 2 * first * 1024) + slot * kT8Slot);
+          int ex;
+          if (kind == 2) ex = put_tail<ELEM>(ring + slot * kT8Entry, op, desc->n, to0);
+          else ex = put_drafts<ELEM>(ring + slot * kT8Entry, op, desc->n, (op ? draft_place(first) : base + 2 * first * 1024) + slot * kT8Slot);
+          if (!op) ek = ex;
+          else out = ex;
         } else {
 #pragma unroll 1
           for (int t = 0; t < 2; t++)
@@ -1144,6 +1207,10 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
                 stmatrix4(at1, y[0], y[1], y[2], y[3]);
               }
             }
+        }
+        if (op && lane == 0) {
+          sm.taken[j & 15][warp & 3] = make_int2(desc->pos0, kind << 16 | out);
+          if (out) sm.any_taken = 1;
         }
         if (op == 0 && lane < 2) {
           const TileDesc* d = desc + lane;
@@ -1351,6 +1418,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
 template <int ELEM, int CODE>
 __global__ void __launch_bounds__(32 * kT8Walkers, 4) k_tree8_join(const __grid_constant__ Cache8View c, const __grid_constant__ Tree8Args a,
                                                                    int part_rows, const int* plan, const TreeRecord* records) {
+  __shared__ WalkSmem walk_sm;
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lr = lane & 7, lq = lane >> 3, G = c.G;
   const int octets = part_rows / 8, c0 = blockIdx.x / octets, o8 = 8 * (blockIdx.x - c0 * octets);
@@ -1362,17 +1430,12 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 4) k_tree8_join(const __grid_
     const int m = row / G;
     return a.out + (((size_t)i * a.max_nodes + m) * (c.hkv * G) + (size_t)h * G + (row - m * G)) * (2 * kD);
   };
-  // row `row`, if it is one, by a warp
-  auto again = [&](int i, int h, int row, const TreeReq& req, const TreeTiles& tiles) {
-    if (row >= req.M * G) return;
-    uint8_t* out = out_of(i, h, row);
-    const uint2 z = *reinterpret_cast<const uint2*>(out + 8 * lane);
-    uint32_t bad = 0;
-    find_not_finite<ELEM>(bad, z.x);
-    find_not_finite<ELEM>(bad, z.y);
-    if (!__any_sync(0xffffffffu, found_not_finite(bad))) return;
-    const Walk<ELEM, CODE> walk{c, a, i, h, lane, req, tiles};
-    walk.row(row / G, row % G, out);
+  // of eight rows from `first` on those that came out infinite or NaN, one by one
+  auto again = [&](int i, int h, int first, bool bad, const TreeReq& req, const TreeTiles& tiles) {
+    const Walk<ELEM, CODE> walk{c, a, i, h, req, tiles};
+#pragma unroll 1
+    for (int x = 0; x < 8; x++)
+      if (__syncthreads_or(bad && lr == x)) walk.row((first + x) / G, (first + x) % G, out_of(i, h, first + x), walk_sm);
   };
   const int row0 = rec.t * kT8Rows + o8, row = row0 + lr;
   if ((rec.flags & 1) && row0 < rec.M * G) {
@@ -1433,7 +1496,7 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 4) k_tree8_join(const __grid_
     find_not_finite<ELEM>(bad, w.y);
     if (__builtin_expect(__syncthreads_or(real && found_not_finite(bad)), 0)) {
       const TreeReq req = tree_req(c, a, rec.i);
-      again(rec.i, rec.h, row0 + warp, req, tree_tiles(req.N, req.M, c.T, a.window, a.sinks));
+      again(rec.i, rec.h, row0, real && found_not_finite(bad), req, tree_tiles(req.N, req.M, c.T, a.window, a.sinks));
     }
   }
   if (__builtin_expect(rec.flags & 2, 0)) {
@@ -1448,9 +1511,16 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 4) k_tree8_join(const __grid_
       const TreeReq req = tree_req(c, a, i);
       const TreeTiles tiles = tree_tiles(req.N, req.M, c.T, a.window, a.sinks);
       const int per = (tiles.places + kT8Step - 1) / kT8Step, x = pos - plan[i], unit = x / per, s0 = x - unit * per, n = min(per - s0, rec.hi - pos);
-      const int rt = unit_rows(req.M, G), h = unit / rt;
-      if (n == per) again(i, h, (unit - h * rt) * kT8Rows + o8 + warp, req, tiles);
+      const int rt = unit_rows(req.M, G), h = unit / rt, first = (unit - h * rt) * kT8Rows + o8;
       pos += n;
+      if (n < per) continue;
+      uint32_t bad = 0;
+      if (first + lr < req.M * G) {
+        const uint2 w = *reinterpret_cast<const uint2*>(out_of(i, h, first + lr) + 8 * (4 * warp + lq));
+        find_not_finite<ELEM>(bad, w.x);
+        find_not_finite<ELEM>(bad, w.y);
+      }
+      if (__syncthreads_or(found_not_finite(bad))) again(i, h, first, found_not_finite(bad), req, tiles);
     }
   }
 }

@@ -232,6 +232,67 @@ def test_what_is_not_seen_never_enters(elem, what, bad):
 
 
 @pytest.mark.parametrize("elem", [F16, BF16])
+@pytest.mark.parametrize("T,n,chain", [(64, 60, True), (64, 60, False), (16, 70, True), (128, 500, False)])
+def test_stored_values_not_finite_behind_the_window(elem, T, n, chain):
+    """A stored token (of the tail with T = 64 and 128, a code with T = 16) whose V is NaN: nodes
+    whose window does not reach it come out as if it were not there."""
+    rng = np.random.default_rng(T)
+    M, window, bad = 16, 12, n - 10                 # seen by depths 0 and 1
+    c = make(2, 3, T, 1, n // T + 1, elem, E4M3, M, seed=12, fill=NAN)
+    fill(c, rng, [n])
+    parents = [list(range(-1, M - 1)) if chain else tref.random_tree(rng, M, 8)]
+    q, k, v = drafts(c, rng, 1, M)
+    par = None if chain else parents
+    clean = run_tree(c, [n], par, q, k, v, window=window)
+    check_tree(c, clean, [n], parents, q, k, v, [M], window=window)
+    feature, token = 39, bad % 16
+    place = lambda bits: int(ref.PLACES[bits][1][token, feature])
+    if bad // T < n // T:
+        c.pages.view(torch.uint8)[int(c.table[0, bad // T]), 0, bad % T // 16, 1, place(8)] = 0x7f
+    else:
+        c.tail[0, 0, bad % T // 16, 1, place(16)] = NAN
+    out = run_tree(c, [n], par, q, k, v, window=window)
+    depth = np.array(tref.depths(parents[0]))
+    check_tree(c, out, [n], parents, q, k, v, [M], window=window, nodes=set(np.flatnonzero(depth > 1).tolist()))
+    hit = out.double().cpu().numpy()[depth <= 1][:, :3]
+    assert np.isnan(hit[..., feature]).all()
+    rest = np.arange(128) != feature
+    want = clean.double().cpu().numpy()[depth <= 1][:, :3][..., rest]
+    # recomputed rows round their weights otherwise: two roundings of weights and results apart
+    tol = 2 * (torch.finfo(elem).eps / 2) * np.abs(want) + 2 * 2.0 ** -10 * 40
+    assert (np.abs(hit[..., rest] - want) <= tol).all()
+
+
+@pytest.mark.parametrize("elem", [F16, BF16])
+def test_infinite_drafts_in_long_contexts_and_many_requests(elem):
+    """Leaves with infinite values in some of many requests, whose units are split and lie
+    behind one another: only rows that see them change."""
+    rng = np.random.default_rng(17)
+    lens, M = [1500, 3, 40, 900, 0, 333, 64, 17, 129, 700], 10
+    n = len(lens)
+    c = make(3, 4, 32, n, 1500 // 32 + 1, elem, INT8, M, seed=13, fill=NAN)
+    fill(c, rng, lens)
+    parents = [tref.random_tree(rng, M) for _ in range(n)]
+    q, k, v = drafts(c, rng, n, M)
+    clean = run_tree(c, lens, parents, q, k, v)
+    check_tree(c, clean, lens, parents, q, k, v, [M] * n)
+    leaf = M - 1
+    for i in (0, 3, 4, 7):
+        v[i * M + leaf, 1, 20] = float("-inf")
+    out = run_tree(c, lens, parents, q, k, v)
+    torch.cuda.synchronize()
+    assert c.c.status_words.tolist() == [0, 0]
+    same = torch.ones(n * M, 12, dtype=torch.bool)
+    for i in (0, 3, 4, 7):
+        same[i * M + leaf, 4:8] = False
+    o, w = out.float().cpu(), clean.float().cpu()
+    assert torch.isfinite(o[same]).all()
+    tol = 2 * (torch.finfo(elem).eps / 2) * w[same].abs() + 2 * 2.0 ** -10 * 40
+    assert ((o[same] - w[same]).abs() <= tol).all()
+    assert torch.isinf(o[~same][:, 20]).all() and torch.isfinite(o[~same][:, :20]).all()
+
+
+@pytest.mark.parametrize("elem", [F16, BF16])
 def test_values_at_the_edges_of_the_types(elem):
     """Zero blocks beside huge ones, values of the largest size, tiny ones, huge
     queries: finite means, the zero blocks' weights count."""
