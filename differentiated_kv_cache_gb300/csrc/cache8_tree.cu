@@ -57,8 +57,8 @@ constexpr int kT8Slot = 32768;      // K or V of a step in 16 bits
 constexpr int kT8Batch = 4;         // steps that are looked up at once
 constexpr int kT8Descs = 4 * kT8Batch;      // steps whose descriptors are kept, a ring
 constexpr int kT8Metas = 8;         // steps whose scales are kept for the softmax, a ring
-// steps in whose time a CTA goes from one unit to the next (0: 64 chains of 1 to 3000 tokens
-// take 126 us, 32 windows 76; 4: 100 and 68; 8: 103 and 68)
+// steps in whose time a CTA goes from one unit to the next (2: 64 chains of 1 to 3000 tokens take
+// 90 us, 32 windows 56; 3: 85 and 54; 4: 84 and 53; 6: 85 and 53)
 constexpr int kT8Turn = 4;
 constexpr float kT8Up = 7.0f;       // log2 of a weight at its row's maximum
 constexpr float kT8Most = 32768.0f; // largest sum of a row's weights of one tile (fp16 holds 65504)
