@@ -762,3 +762,83 @@ def test_rounds_of_guesses(elem, code):
         c.check()
     q1 = c.vec(rng, n, hkv * G)
     c.check_attention(c.attend(None, lens_h, q1), range(n), lens_h, q1)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages, slots and rows behind the first 4 GB give what near ones give, in all four
+    calls."""
+    dkv = _dkv()
+    hkv, G, T, lens, M, R = 2, 4, 64, [200, 64, 130], 7, 32
+    rng = np.random.default_rng(19)
+    near = make(hkv, G, T, 3, 4, F16, E4M3, M, rot=R)
+    n_pages, n_slots = 2 ** 33 // (hkv * T * 256) + 1, 2 ** 33 // (hkv * T * 512) + 1
+    pages = torch.empty((n_pages, hkv, T // 16, 2, 2048), dtype=E4M3, device="cuda")
+    tail = torch.empty((n_slots, hkv, T // 16, 2, 2048), dtype=F16, device="cuda")
+    scales = torch.empty((n_pages, hkv, 2), device="cuda")
+    table = torch.zeros((n_slots, 4), dtype=torch.int32, device="cuda")
+    slots = torch.tensor([n_slots - 1, n_slots // 2 + 1, n_slots - 7], dtype=torch.int32, device="cuda")
+    table[slots.long()] = torch.arange(n_pages - 12, n_pages, dtype=torch.int32, device="cuda").reshape(3, 4)
+    far = dkv.make_cache8(pages, scales, tail, table, group_size=G, rotary_dim=R, max_nodes=M)
+    total, rows = sum(lens), 3 * M
+
+    def apart(n, tensors):
+        wide = 2 ** 32 // n // 8 * 8 + 8                # rows lie over 8 GB
+        space, out = torch.empty((n, wide), dtype=F16, device="cuda"), []
+        for i, x in enumerate(tensors):
+            y = space[:, 2048 * i:2048 * i + x.shape[1] * 128].view(n, x.shape[1], 128)
+            y.copy_(x)
+            out.append(y)
+        return out
+
+    k, v = near.vec(rng, total, hkv), near.vec(rng, total, hkv)
+    qd, kd, vd = near.vec(rng, rows, hkv * G), near.vec(rng, rows, hkv), near.vec(rng, rows, hkv)
+    pos = torch.from_numpy(rng.integers(0, 4 * T, (2, total)).astype(np.int32)).cuda()
+    dpos = torch.from_numpy(rng.integers(0, 4 * T, (2, rows)).astype(np.int32)).cuda()
+    axes = bytes(i % 2 for i in range(R // 2))
+    zero, ln, par = i32([0] * 3), i32(lens), i32([tref.random_tree(rng, M) for _ in lens])
+    path = i32([[0, 1, 3], [2, 5, 0], [4, 6, 6]])
+    kept, got = [apart(total, (k, v)), apart(rows, (qd, kd, vd))], []
+    for c, sl, (a, b), (x, y, z) in ((near.c, None, (k, v), (qd, kd, vd)), (far, slots, *kept)):
+        dkv.dkv_cache8_append_at(c, zero, pos, a, b, near.rope, pair_axis=axes, n_new=lens, slots=sl)
+        qr, kr = torch.empty_like(qd), torch.empty_like(kd)
+        dkv.dkv_cache8_rotate(c, dpos, near.rope, q=x, k=y, q_rot=qr, k_rot=kr, pair_axis=axes)
+        outs = [torch.empty_like(qd) for _ in range(2)]
+        dkv.dkv_cache8_tree(c, ln, par, x, y, z, outs[0], slots=sl)
+        dkv.dkv_cache8_accept(c, ln, y, z, path, slots=sl)
+        dkv.dkv_cache8_tree(c, ln + 3, par, qr, kr, z, outs[1], window=150, sinks=3, slots=sl)
+        torch.cuda.synchronize()
+        assert c.status_words.tolist() == [0, 0]
+        got.append((qr, kr, *outs))
+    for x, y in zip(*got):
+        assert torch.isfinite(x.float()).all() and torch.equal(x.view(torch.int16), y.view(torch.int16))
+    assert torch.equal(near.pages.view(torch.uint8)[near.table.long()][0, :3], pages.view(torch.uint8)[table[slots.long()].long()][0, :3])
+
+
+def test_a_slot_of_two_requests():
+    """Reading calls may name a slot twice, with other lengths."""
+    rng = np.random.default_rng(20)
+    M = 5
+    c = make(2, 2, 32, 2, 8, BF16, INT8, M, seed=14, fill=NAN)
+    fill(c, rng, [192, 50])
+    lens, slots = [192, 64, 50, 192], [0, 0, 1, 0]
+    parents = [tref.random_tree(rng, M) for _ in lens]
+    q, k, v = drafts(c, rng, 4, M)
+    out = run_tree(c, lens, parents, q, k, v, slots=slots)
+    check_tree(c, out, lens, parents, q, k, v, [M] * 4, slots)
+
+
+def test_nothing_but_padding_then_something():
+    """A call without any draft writes nothing; the next one finds the workspace as it needs it."""
+    rng = np.random.default_rng(21)
+    M = 4
+    c = make(2, 4, 16, 3, 5, F16, E4M3, M, seed=15, fill=NAN)
+    fill(c, rng, [70, 0, 16])
+    parents = [tref.random_tree(rng, M) for _ in range(3)]
+    q, k, v = drafts(c, rng, 3, M, [0, 1, 0])
+    out = run_tree(c, [70, 0, 16], parents, q, k, v, [0, 0, -3], slots=[0, 7, -1])
+    torch.cuda.synchronize()
+    assert torch.isnan(out).all() and c.c.status_words.tolist() == [0, 0]
+    out = run_tree(c, [70, 0, 16], parents, q, k, v, [0, 1, 0])
+    check_tree(c, out, [70, 0, 16], parents, q, k, v, [0, 1, 0])
+    # a node alone sees itself: its value
+    assert torch.equal(out[M].view(2, 4, 128), v[M][:, None].expand(2, 4, 128))
