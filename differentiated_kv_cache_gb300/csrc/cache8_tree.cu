@@ -6,9 +6,10 @@
 // of a group (M G query rows) read the same K and V, so the cache is read once for 128
 // rows; the products, 4 * 128 operations a row and token, go to tcgen05. Both take fp16
 // operands and sum in fp32: codes are exact in fp16; tails, drafts and queries in bf16 come
-// into its range by a power of two (one for 16 tokens, one for a query's row), which keeps
-// their 8 bits down to 2^-17 of the largest, and what is smaller to 2^-25 of it; K's scale joins
-// the logits, V's joins the weights as an addend of their exponent. Weights are rounded to
+// into its range by a power of two: one for a query's row, whose 8 bits stay down to 2^-17 of the
+// largest (what lies under 2^-25 of it is lost), one for each token's K and V, whose bits stay
+// down to 2^-24 (lost under 2^-32). K's scale joins the logits, V's joins the weights as an addend
+// of their exponent. Weights are rounded to
 // fp16 (2^-11), as probabilities are in the attention of single tokens.
 //
 // Units (request, KV head, 128 rows) of steps (128 tokens) follow one another; the sequence
@@ -88,7 +89,8 @@ __device__ __forceinline__ TreeReq tree_req(const Cache8View& c, const Tree8Args
 // which those from `full` on lie in the tail, then the drafts; `count` in all. A stored tile
 // is left out if no node of any depth sees a token of it. In the steps of the kernel below a
 // tile of 16-bit values takes two places (its copies need twice the room): places [0, codes)
-// hold the tiles of codes, which come first, those from `elems` on the others, every second one.
+// hold the tiles of codes, which come first, those from `elems` on the others, every second one, so that the four
+// places of a softmax warp are of one kind.
 struct TreeTiles {
   int head, win, end, full, stored, count;
   int codes, elems, places;
@@ -108,7 +110,7 @@ __device__ __forceinline__ TreeTiles tree_tiles(int N, int M, int T, int window,
   t.stored = t.head + t.end - t.win;
   t.count = t.stored + (M + kSub - 1) / kSub;
   t.codes = t.full > t.win ? t.head + t.full - t.win : min(t.head, t.full);
-  t.elems = (t.codes + 1) & ~1;
+  t.elems = (t.codes + 3) & ~3;
   t.places = t.elems + 2 * (t.count - t.codes);
   return t;
 }
@@ -500,7 +502,7 @@ struct TileDesc {
   int n;            // kinds 2 and 3: valid tokens
   const uint8_t* vsrc;
 };
-// What the softmax has to know of it. kind: seen by all (0), stored (1), drafts (2), none (3).
+// What the softmax has to know of it; kind as above.
 struct TileMeta {
   float ks, lv;
   int pos0, kind;
@@ -510,6 +512,9 @@ struct TreeSmem {
   TileDesc desc[kT8Descs][kT8Step];
   unsigned there[2 * kT8Descs];        // places of a step that hold a tile (the products are behind the conversion)
   TileMeta meta[kT8Metas][kT8Step];    // (K of step j comes when the softmax has read that of step j - 5)
+  // of a step's tiles of 16 bits: K's powers of two, V's exponents (there with V, not with S)
+  uint16_t kexp[kT8Metas][kT8Step / 2][kSub];
+  float vexp[kT8Slots][kT8Step / 2][kSub];
   TreePlan plan;
   int parents[kMaxNodes];
   float2 pair[2][2][kT8Rows];      // what the two warps of a row tell each other
@@ -530,6 +535,7 @@ struct TreeSmem {
 constexpr int kT8OffV = kT8Slots * kT8Slot, kT8OffRing = 2 * kT8Slots * kT8Slot;
 constexpr int kT8OffSmem = kT8OffRing + 2 * kT8Ring * kT8Entry;
 constexpr int kT8Smem = 1024 + kT8OffSmem + (int)sizeof(TreeSmem);
+static_assert(kT8Smem <= 232448, "a block's shared memory");
 
 __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
@@ -538,6 +544,11 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b,
 __device__ __forceinline__ void stmatrix4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
@@ -605,66 +616,48 @@ __device__ __forceinline__ TileDesc describe_tile(const Cache8View& c, const Tre
   return d;
 }
 
-// A lane's words of K or V of a tile of the tail, of which n tokens are valid: words 4 m +
-// (0 .. 3) are the 8 x 8 matrices of m-step m. What lies behind those tokens becomes 0 (0 times
-// what it may hold is not).
-__device__ __forceinline__ void load_tail(const uint8_t* src, bool v, int n, uint32_t (&x)[32]) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t lo_t = v ? (2 * t < n ? 0xffffu : 0u) | (2 * t + 1 < n ? 0xffff0000u : 0u) : g < n ? 0xffffffffu : 0u;
-  const uint32_t hi_t = v ? (2 * t + 8 < n ? 0xffffu : 0u) | (2 * t + 9 < n ? 0xffff0000u : 0u) : g + 8 < n ? 0xffffffffu : 0u;
-#pragma unroll
-  for (int f = 0; f < 8; f++) {
-    const uint4 y = *reinterpret_cast<const uint4*>(src + 512 * f + 16 * lane);
-    x[4 * f] = y.x & lo_t;
-    x[4 * f + 1] = y.y & (v ? hi_t : lo_t);
-    x[4 * f + 2] = y.z & (v ? lo_t : hi_t);
-    x[4 * f + 3] = y.w & hi_t;
-  }
-}
-// ... of drafts (rows of `stride` bytes): words 4 e + (0 .. 3) are features 8 (lane % 16) + (0 .. 7)
-// of row 2 e + lane / 16.
-__device__ __forceinline__ void load_drafts(const uint8_t* src, int n, long long stride, uint32_t (&x)[32]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int e = 0; e < 8; e++) {
-    const int row = 2 * e + (lane >> 4);
-    const uint4 y = row < n ? *reinterpret_cast<const uint4*>(src + row * stride + 16 * (lane & 15)) : make_uint4(0, 0, 0, 0);
-    x[4 * e] = y.x;
-    x[4 * e + 1] = y.y;
-    x[4 * e + 2] = y.z;
-    x[4 * e + 3] = y.w;
-  }
-}
-// The exponent of the power of two that a tile's bf16 values are divided by: the largest
-// comes to [128, 256).
-__device__ __forceinline__ int exp_of(const uint32_t (&x)[32]) {
-  return max(-120, (int)(__reduce_max_sync(0xffffffffu, amax_bits(x)) >> 7) - (127 + 7));
-}
-__device__ __noinline__ int elems_exp(const uint8_t* src, bool v, bool draft, int n, long long stride) {
-  uint32_t x[32];
-  if (draft) load_drafts(src, n, stride, x);
-  else load_tail(src, v, n, x);
-  return exp_of(x);
+// ---- powers of two: K and V of each bf16 token are divided by one of their own, which brings the
+// token's largest value to [128, 256). (One for the tile: what a row does not see would set the
+// power for what it does. A sibling's V 2^30 above the others left rows that do not see it wrong
+// by 25 %, one 2^60 above left zeros.) ----
+template <int ELEM>
+constexpr bool kT8Own = ELEM == DKV_BF16;
+// Largest finite magnitudes so far of the low and of the high values: with the exponent's last
+// bit added to the bits of the magnitudes, infinities and NaN are negative numbers of 16 bits.
+template <int ELEM>
+constexpr uint32_t kT8Bias = ELEM == DKV_F16 ? 0x0400u : 0x0080u;
+__device__ __forceinline__ uint32_t max_s16x2(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.s16x2 %0, %1, %2;\n" : "=r"(m) : "r"(a), "r"(b));
+  return m;
 }
 template <int ELEM>
-__device__ __forceinline__ int to_half(uint32_t (&x)[32]) {      // (fp16 stays)
-  if (ELEM != DKV_BF16) return 0;
-  const int ex = exp_of(x);
-  const float inv = pow2(-ex);
-#pragma unroll
-  for (int f = 0; f < 32; f++) x[f] = half_of_bf16(x[f], inv);
-  return ex;
+__device__ __forceinline__ uint32_t top_pair(uint32_t m, uint32_t w) {
+  return max_s16x2(m, (w & 0x7fff7fffu) + kT8Bias<ELEM> * 0x10001u);
+}
+__device__ __forceinline__ uint32_t swap_halves(uint32_t x) { return prmt(x, x, 0x1032u); }
+// The exponent for one of the two.
+template <int ELEM>
+__device__ __forceinline__ int exp_of(uint32_t top) {
+  const uint32_t x = __float_as_uint(elem_float<ELEM>((uint16_t)((top & 0xffffu) - kT8Bias<ELEM>)));
+  return max(-120, (int)(x >> 23) - (127 + 7));
+}
+template <int ELEM>
+__device__ __forceinline__ uint32_t half_of(uint32_t w, float lo, float hi) {
+  return pack_half2(lo_elem<ELEM>(w) * lo, hi_elem<ELEM>(w) * hi);
+}
+// What the softmax has to know of the 16 tokens: K's powers of two, V's exponents.
+struct TileExps {
+  uint16_t* k;      // bf16
+  float* v;
+};
+__device__ __forceinline__ void put_exp(const TileExps& e, bool v, int token, int ex) {
+  if (v) e.v[token] = (float)ex;
+  else e.k[token] = (uint16_t)((127 + ex) << 7);
 }
 // V that is not finite would meet the weights of rows that do not see it, and 0 times it is not 0:
 // it becomes 0 where it lies in shared memory, and whoever sees its token (bits of 16) is computed
 // again. (Out of the way: instructions fetched with the usual case cost it 5%.)
-template <int ELEM>
-__device__ __forceinline__ bool none_to_take(const uint32_t (&x)[32]) {
-  uint32_t acc = 0;
-#pragma unroll
-  for (int f = 0; f < 32; f++) find_not_finite<ELEM>(acc, x[f]);
-  return __builtin_expect(!__any_sync(0xffffffffu, found_not_finite(acc)), 1);
-}
 template <int ELEM>
 __device__ __noinline__ uint32_t take_out(uint8_t* src, bool draft, int n) {
   constexpr uint32_t kExp = ELEM == DKV_F16 ? 0x0400u : 0x0080u;
@@ -688,65 +681,143 @@ __device__ __noinline__ uint32_t take_out(uint8_t* src, bool draft, int n) {
   __syncwarp();
   return __reduce_or_sync(0xffffffffu, bits) & below(n);
 }
-// A tile of the tail as fp16 operands; at: the lane's row of the first four matrices. Of K the
-// exponent that its values were divided by, of V the tokens with values that are not finite.
+// A tile of the tail as fp16 operands, of which n tokens are valid; at: the lane's row of the first
+// four matrices. Returns the tokens whose V has values that are not finite. Two passes over the
+// lane's 16 bytes of every m-step in short loops: this code runs once or twice a unit and comes from
+// far (unrolled, all eight m-steps at once: 59.9 us for the window, 57.3 so).
 template <int ELEM>
-__device__ __noinline__ int put_tail(uint8_t* src, bool v, int n, uint32_t at) {
-  uint32_t x[32], out = 0;
+__device__ __noinline__ uint32_t put_tail(uint8_t* src, bool v, int n, uint32_t at, TileExps exps) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // The four 8 x 8 matrices of m-step f, of K the first eight features' first: even words are of token
+  // g (K) or tokens 2t and 2t + 1 (V, low and high halves), odd ones of those eight tokens on. What
+  // lies behind the valid tokens becomes 0 (0 times what it may hold is not).
+  const uint32_t valid_a = v ? (2 * t < n ? 0xffffu : 0u) | (2 * t + 1 < n ? 0xffff0000u : 0u) : g < n ? 0xffffffffu : 0u;
+  const uint32_t valid_b = v ? (2 * t + 8 < n ? 0xffffu : 0u) | (2 * t + 9 < n ? 0xffff0000u : 0u) : g + 8 < n ? 0xffffffffu : 0u;
+  auto load = [&](int f) {
+    const uint4 y = *reinterpret_cast<const uint4*>(src + 512 * f + 16 * lane);
+    return make_uint4(y.x & valid_a, (v ? y.y : y.z) & valid_b, (v ? y.z : y.y) & valid_a, y.w & valid_b);
+  };
+  uint32_t a = 0, b = 0, out = 0;
 #pragma unroll 1
-  while (true) {
-    load_tail(src, v, n, x);
-    if (!v || none_to_take<ELEM>(x)) break;
+  while (v || ELEM == DKV_BF16) {          // (K in fp16 stays as it is)
+    uint32_t acc = 0;
+    a = b = kT8Bias<ELEM> * 0x10001u;
+#pragma unroll 2
+    for (int f = 0; f < 8; f++) {
+      const uint4 x = load(f);
+      a = top_pair<ELEM>(top_pair<ELEM>(a, x.x), x.z);
+      b = top_pair<ELEM>(top_pair<ELEM>(b, x.y), x.w);
+      find_not_finite<ELEM>(acc, x.x);
+      find_not_finite<ELEM>(acc, x.y);
+      find_not_finite<ELEM>(acc, x.z);
+      find_not_finite<ELEM>(acc, x.w);
+    }
+    if (!v || __builtin_expect(!__any_sync(0xffffffffu, found_not_finite(acc)), 1)) break;
     out = take_out<ELEM>(src, false, n);
   }
-  const int ex = to_half<ELEM>(x);
-#pragma unroll
-  for (int f = 0; f < 8; f++) {
-    if (!v) stmatrix4((at + (f >> 2) * 16384) ^ ((f & 3) << 5), x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
-    else stmatrix4(at + f * 2048, x[4 * f], x[4 * f + 1], x[4 * f + 2], x[4 * f + 3]);
+  float fa0 = 1.0f, fa1 = 1.0f, fb0 = 1.0f, fb1 = 1.0f;
+  if (kT8Own<ELEM>) {
+    if (!v) {
+      a = max_s16x2(a, swap_halves(a));
+      b = max_s16x2(b, swap_halves(b));
+    }
+#pragma unroll 1
+    for (int d = v ? 4 : 1; d < (v ? 32 : 4); d <<= 1) {
+      a = max_s16x2(a, __shfl_xor_sync(0xffffffffu, a, d));
+      b = max_s16x2(b, __shfl_xor_sync(0xffffffffu, b, d));
+    }
+    const int a0 = exp_of<ELEM>(a), a1 = exp_of<ELEM>(a >> 16), b0 = exp_of<ELEM>(b), b1 = exp_of<ELEM>(b >> 16);
+    if (v ? g == 0 : t == 0) {
+      put_exp(exps, v, v ? 2 * t : g, a0);
+      put_exp(exps, v, v ? 2 * t + 8 : g + 8, b0);
+      if (v) {
+        put_exp(exps, v, 2 * t + 1, a1);
+        put_exp(exps, v, 2 * t + 9, b1);
+      }
+    }
+    fa0 = pow2(-a0);
+    fa1 = pow2(-a1);
+    fb0 = pow2(-b0);
+    fb1 = pow2(-b1);
   }
-  return v ? (int)out : ex;
+#pragma unroll 2
+  for (int f = 0; f < 8; f++) {
+    uint4 x = load(f);
+    if (kT8Own<ELEM>) x = make_uint4(half_of<ELEM>(x.x, fa0, fa1), half_of<ELEM>(x.y, fb0, fb1), half_of<ELEM>(x.z, fa0, fa1), half_of<ELEM>(x.w, fb0, fb1));
+    if (!v) stmatrix4((at + (f >> 2) * 16384) ^ ((f & 3) << 5), x.x, x.z, x.y, x.w);
+    else stmatrix4(at + f * 2048, x.x, x.y, x.z, x.w);
+  }
+  return out;
 }
-// Drafts, whose rows of 256 bytes lie in shared memory. K's go to their operand rows as they
-// are (to: row 0); V's back to there, row r turned by r times 16 bytes so that the same features of
+// Drafts, whose rows of 256 bytes lie in shared memory: a lane half a row, 16 bytes at a time in an
+// order that keeps eight lanes apart in the banks, there (where column y lies in the same banks for
+// every row) and in the operand (where y xor the row does). K goes to its operand rows (to: row 0),
+// V back to where it was, then once more with row r turned by r times 16 bytes, so that the same features of
 // eight rows lie in different banks, and from there as transposed matrices (to: as for put_tail).
 // (Both by words straight from the rows, eight lanes on a bank: a step of four draft tiles 4000
 // cycles.)
 template <int ELEM>
-__device__ __noinline__ int put_drafts(uint8_t* rows, bool v, int n, uint32_t to) {
-  const int lane = threadIdx.x & 31, c = lane & 15;
+__device__ __noinline__ uint32_t put_drafts(uint8_t* rows, bool v, int n, uint32_t to, TileExps exps) {
+  const int lane = threadIdx.x & 31, row = lane & 15, half = lane >> 4, r = row & 7;
   const uint32_t src = smem_u32(rows);
-  uint32_t x[32], out = 0;
+  // y -> column, such that r -> column and r -> column xor r are one to one
+  const int turn = (r << 1 & 7) ^ (r & 4 ? 3 : 0);
+  const uint32_t mine = src + row * (2 * kD) + 128 * half;
+  auto load = [&](int y) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (row < n) lds128(mine + ((y ^ turn) << 4), x.x, x.y, x.z, x.w);
+    return x;
+  };
+  uint32_t top = 0, out = 0;
 #pragma unroll 1
-  while (true) {
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const int row = 2 * e + (lane >> 4);
-      x[4 * e] = x[4 * e + 1] = x[4 * e + 2] = x[4 * e + 3] = 0;
-      if (row < n) lds128(src + row * (2 * kD) + 16 * c, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+  while (v || ELEM == DKV_BF16) {
+    uint32_t acc = 0;
+    top = kT8Bias<ELEM> * 0x10001u;
+#pragma unroll 2
+    for (int y = 0; y < 8; y++) {
+      const uint4 x = load(y);
+      top = top_pair<ELEM>(top_pair<ELEM>(top_pair<ELEM>(top_pair<ELEM>(top, x.x), x.y), x.z), x.w);
+      find_not_finite<ELEM>(acc, x.x);
+      find_not_finite<ELEM>(acc, x.y);
+      find_not_finite<ELEM>(acc, x.z);
+      find_not_finite<ELEM>(acc, x.w);
     }
-    if (!v || none_to_take<ELEM>(x)) break;
+    if (!v || __builtin_expect(!__any_sync(0xffffffffu, found_not_finite(acc)), 1)) break;
     out = take_out<ELEM>(rows, true, n);
   }
-  const int ex = to_half<ELEM>(x);
-  __syncwarp();
-#pragma unroll
-  for (int e = 0; e < 8; e++) {
-    const int row = 2 * e + (lane >> 4);
-    const uint32_t at = v ? src + row * (2 * kD) + (((c + row) & 15) << 4) : to + (c >> 3) * 16384 + row * 128 + (((c ^ row) & 7) << 4);
-    sts128(at, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+  float f = 1.0f;
+  if (kT8Own<ELEM>) {
+    top = max_s16x2(top, swap_halves(top));
+    const int ex = exp_of<ELEM>(max_s16x2(top, __shfl_xor_sync(0xffffffffu, top, 16)));
+    if (half == 0) put_exp(exps, v, row, ex);
+    f = pow2(-ex);
+  }
+#pragma unroll 2
+  for (int y = 0; y < 8; y++) {
+    uint4 x = load(y);
+    if (kT8Own<ELEM>) x = make_uint4(half_of<ELEM>(x.x, f, f), half_of<ELEM>(x.y, f, f), half_of<ELEM>(x.z, f, f), half_of<ELEM>(x.w, f, f));
+    sts128(v ? mine + ((y ^ turn) << 4) : to + half * 16384 + row * 128 + ((y ^ turn ^ r) << 4), x.x, x.y, x.z, x.w);
   }
   if (v) {
+    const int c = lane & 15;
+    uint32_t x[32];
     __syncwarp();
-    const int row = (lane & 7) + 8 * (lane >> 4);      // matrices: features 0 .. 7, 8 .. 15 of rows 0 .. 7, of rows 8 .. 15
 #pragma unroll
-    for (int f = 0; f < 8; f++) {
-      uint32_t m[4];
-      ldmatrix_x4(m, src + row * (2 * kD) + (((2 * f + (lane >> 3 & 1) + row) & 15) << 4));
-      stmatrix4_trans(to + f * 2048, m[0], m[1], m[2], m[3]);
+    for (int e = 0; e < 8; e++) lds128(src + (2 * e + half) * (2 * kD) + 16 * c, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      sts128(src + (2 * e + half) * (2 * kD) + (((c + 2 * e + half) & 15) << 4), x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+    __syncwarp();
+    const int at = (lane & 7) + 8 * half;      // matrices: features 0 .. 7, 8 .. 15 of rows 0 .. 7, of rows 8 .. 15
+#pragma unroll 2
+    for (int m = 0; m < 8; m++) {
+      uint32_t w[4];
+      ldmatrix_x4(w, src + at * (2 * kD) + (((2 * m + (lane >> 3 & 1) + at) & 15) << 4));
+      stmatrix4_trans(to + m * 2048, w[0], w[1], w[2], w[3]);
     }
   }
-  return v ? (int)out : ex;
+  return out;
 }
 
 template <int ELEM, int CODE>
@@ -923,132 +994,203 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         then = tree_item(c, a, sm.plan, pos, hi);
         if (real_of(then)) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(q_of(then)));
       }
+      // which tokens of a tile the row sees
+      auto sees = [&](int kind, int pos0) {
+        const int w = pos0 >> 5;
+        return kind == 0 ? 0xffffu : kind == 1 || kind == 2 ? sees_stored(a, it.N, node.depth, pos0) : kind != 3 ? 0u
+               : (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (pos0 & 31);
+      };
       float mx = -INFINITY, u = -INFINITY, l = 0.0f;
       const int end = j + it.n;
       bool first = true, raise = true;
+      // The running maxima take in yt, xt of a step: all of them where one row's would leave its
+      // own by more than the slack.
+      auto raise_to = [&](float yt, float xt, int j, bool first, float slack_x, float slack_y) {
+        sm.pair[told][part][r] = make_float2(yt, xt);
+        named_sync(pair_bar, 64);
+        const float2 other = sm.pair[told][part ^ 1][r];
+        told ^= 1;
+        const float nu = fmaxf(u, fmaxf(yt, other.x)), nm = fmaxf(mx, fmaxf(xt, other.y));
+        // (the same for both warps of a row)
+        if (!__any_sync(0xffffffffu, nm > mx + slack_x || nu > u + slack_y)) return;
+        l *= nu == -INFINITY ? 1.0f : fast_exp2(u - nu);
+        if (!first) {        // O is still once the last product is done
+          ok = wait(pvdone((j - 1) & 3), (j - 1) >> 2) && ok;
+          tc_fence_after();
+          const float fo = nm == -INFINITY ? 1.0f : fast_exp2(mx - nm);
+#pragma unroll 1
+          for (int q = 0; q < 4; q++) {
+            float o[16];
+            tmem_ld16_nowait(t_o + tl + 64 * part + 16 * q, o);
+            tmem_wait_ld();
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; e++) {
+              asm volatile("" : "+f"(o[e]));
+              w[e] = __float_as_uint(o[e] * fo);
+            }
+            tmem_st16(t_o + tl + 64 * part + 16 * q, w);
+          }
+        }
+        mx = nm;
+        u = nu;
+        raise = __any_sync(0xffffffffu, real && u == -INFINITY);      // a row that has seen nothing so far
+      };
       for (; j < end; j++) {
         // (after a wait that gave up the warps walk on, through the same barriers)
         ok = wait(sfull(j & 1), j >> 1) && ok;
         tc_fence_after();
         if (busy) {
-          float s[64];
           const uint32_t ts = t_s(j & 1) + tl + 64 * part;
-          tmem_ld32_nowait(ts, s);
-          tmem_ld32_nowait(ts + 32, s + 32);
           const TileMeta* meta = sm.meta[j & (kT8Metas - 1)] + 4 * part;
-          float f[4], lv[4];
-          int kind[4], pos0[4];
+          float sum = 0.0f;
+          // a step with tiles of 16 bits, whose tokens have exponents of their own: the maxima are
+          // taken ahead of the weights there, which may then exceed them by the slack (a tile's weights
+          // sum to 2^15 at most, its probabilities under u to 2^64)
+          const int place = kT8Step * (it.s0 + it.n - (end - j));
+          const bool owned = kT8Own<ELEM> && place + kT8Step > it.tiles.elems;
+          const float slack_x = owned ? 4.0f : 0.0f, slack_y = owned ? kT8Far : 0.0f;
+          if (owned && place + 4 * part >= it.tiles.elems) {
+            // this warp's part holds two of them
+            float y[2][16], v[2][16], yt = -INFINITY, xt = -INFINITY;
+            bool is[2];
+            tmem_ld16_nowait(ts, y[0]);
+            tmem_ld16_nowait(ts + 32, y[1]);
+            ok = wait(vfull(j & 1), j >> 1) && ok;      // (V of step j + 2 waits for these weights)
+            tmem_wait_ld();
 #pragma unroll
-          for (int b = 0; b < 4; b++) {
-            const TileMeta d = meta[b];
-            f[b] = d.ks * scale;
-            lv[b] = d.lv;
-            kind[b] = d.kind;
-            pos0[b] = d.pos0;
-          }
-          tmem_wait_ld();
-          loaded32(s);
-          loaded32(s + 32);
-          if (kind[0] | kind[1] | kind[2] | kind[3]) {
+            for (int b = 0; b < 2; b++) {
+              const TileMeta d = meta[2 * b];
+              is[b] = d.kind != 4;
+              if (!is[b]) continue;
+              const uint32_t see = real ? sees(d.kind, d.pos0) : 0u;
+              const float f = d.ks * scale;
+              const uint4* kp = reinterpret_cast<const uint4*>(sm.kexp[j & (kT8Metas - 1)][2 * part + b]);
+              const float4* vp = reinterpret_cast<const float4*>(sm.vexp[j & 1][2 * part + b]);
 #pragma unroll
-            for (int b = 0; b < 4; b++) {
-              uint32_t see = kind[b] == 0 ? 0xffffu : 0u;
-              if (real && kind[b] == 1) see = sees_stored(a, it.N, node.depth, pos0[b]);
-              if (real && kind[b] == 2) {
-                const int w = pos0[b] >> 5;
-                see = (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (pos0[b] & 31);
+              for (int e = 0; e < 4; e++) {
+                const float4 x = vp[e];
+                v[b][4 * e] = x.x;
+                v[b][4 * e + 1] = x.y;
+                v[b][4 * e + 2] = x.z;
+                v[b][4 * e + 3] = x.w;
               }
 #pragma unroll
-              for (int e = 0; e < 16; e++) s[16 * b + e] = see & (1u << e) ? s[16 * b + e] : -INFINITY;
-            }
-          }
-          uint32_t p[32];
-          float sum;
-#pragma unroll 1
-          for (bool again = raise;; again = true) {
-            if (again) {
-              // (the maxima are not to be taken ahead of the question)
+              for (int e = 0; e < 2; e++) {
+                const uint4 x = kp[e];
+                const uint32_t k[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-              for (int e = 0; e < 64; e++) asm volatile("" : "+f"(s[e]));
-              // the rows' maxima over both parts
-              float yt = -INFINITY, xt = -INFINITY;
-#pragma unroll
-              for (int b = 0; b < 4; b++) {
-                float y0 = s[16 * b], y1 = s[16 * b + 1];
-#pragma unroll
-                for (int e = 2; e < 16; e += 2) {
-                  y0 = fmaxf(y0, s[16 * b + e]);
-                  y1 = fmaxf(y1, s[16 * b + e + 1]);
-                }
-                y0 = fmaxf(y0, y1) * f[b];
-                yt = fmaxf(yt, y0);
-                xt = fmaxf(xt, y0 + lv[b]);
-              }
-              sm.pair[told][part][r] = make_float2(yt, xt);
-              named_sync(pair_bar, 64);
-              const float2 other = sm.pair[told][part ^ 1][r];
-              told ^= 1;
-              const float nu = fmaxf(u, fmaxf(yt, other.x)), nm = fmaxf(mx, fmaxf(xt, other.y));
-              l *= nu == -INFINITY ? 1.0f : fast_exp2(u - nu);
-              if (!first) {        // O is still once the last product is done
-                ok = wait(pvdone((j - 1) & 3), (j - 1) >> 2) && ok;
-                tc_fence_after();
-                const float fo = nm == -INFINITY ? 1.0f : fast_exp2(mx - nm);
-#pragma unroll 1
-                for (int q = 0; q < 4; q++) {
-                  float o[16];
-                  tmem_ld16_nowait(t_o + tl + 64 * part + 16 * q, o);
-                  tmem_wait_ld();
-                  uint32_t w[16];
-#pragma unroll
-                  for (int e = 0; e < 16; e++) {
-                    asm volatile("" : "+f"(o[e]));
-                    w[e] = __float_as_uint(o[e] * fo);
-                  }
-                  tmem_st16(t_o + tl + 64 * part + 16 * q, w);
+                for (int z = 0; z < 8; z++) {
+                  float& o = y[b][8 * e + z];
+                  asm volatile("" : "+f"(o));
+                  o *= f * __uint_as_float(z & 1 ? k[z >> 1] & 0xffff0000u : k[z >> 1] << 16);
+                  o = see & (1u << (8 * e + z)) ? o : -INFINITY;
+                  yt = fmaxf(yt, o);
+                  xt = fmaxf(xt, o + v[b][8 * e + z]);
                 }
               }
-              mx = nm;
-              u = nu;
-              raise = __any_sync(0xffffffffu, real && u == -INFINITY);      // a row that has seen nothing so far
             }
-            // weights 2^(x - m + kT8Up), to be rounded to fp16; their sum of a tile over
-            // 2^(kT8Up + u - m) s_v is that of the probabilities under u, except where these
-            // are so far apart that one of them may vanish
+            raise_to(yt, xt, j, first, slack_x, slack_y);
             const float ur = u == -INFINITY ? 0.0f : u, mr = kT8Up - (mx == -INFINITY ? 0.0f : mx);
-            bool fits = true, far = false;
-            sum = 0.0f;
 #pragma unroll
-            for (int b = 0; b < 4; b++) {
-              const float up = lv[b] + mr;
-              const uint64_t f2 = f32x2(f[b], f[b]), up2 = f32x2(up, up);
-              uint64_t acc[2] = {0, 0};
+            for (int b = 0; b < 2; b++) {
+              if (!is[b]) continue;
+              uint32_t w[8];
 #pragma unroll
               for (int e = 0; e < 8; e++) {
-                const uint64_t y = fma_f32x2(f32x2(s[16 * b + 2 * e], s[16 * b + 2 * e + 1]), f2, up2);
-                const float w0 = fast_exp2(__uint_as_float((uint32_t)y)), w1 = fast_exp2(__uint_as_float((uint32_t)(y >> 32)));
-                acc[e & 1] = add_f32x2(acc[e & 1], f32x2(w0, w1));
-                p[8 * b + e] = pack_half2(w0, w1);
+                const float y0 = y[b][2 * e], y1 = y[b][2 * e + 1];
+                sum += fast_exp2(y0 - ur) + fast_exp2(y1 - ur);
+                w[e] = pack_half2(fast_exp2(y0 + v[b][2 * e] + mr), fast_exp2(y1 + v[b][2 * e + 1] + mr));
               }
-              acc[0] = add_f32x2(acc[0], acc[1]);
-              const float tile = __uint_as_float((uint32_t)acc[0]) + __uint_as_float((uint32_t)(acc[0] >> 32));
-              const float back = up + ur;
-              sum = fmaf(tile, fast_exp2(-back), sum);
-              fits = fits && tile <= kT8Most;
-              far = far || !(fabsf(back) <= kT8Far);      // (these rows take the longer way every time)
+              tmem_st8(ts + 16 * b, w);
             }
-            if (again) {
-              if (__any_sync(0xffffffffu, real && far)) {
-                sum = 0.0f;
+            l += sum;
+          } else {
+            float s[64];
+            tmem_ld32_nowait(ts, s);
+            tmem_ld32_nowait(ts + 32, s + 32);
+            float f[4], lv[4];
+            int kind[4], pos0[4];
 #pragma unroll
-                for (int e = 0; e < 64; e++) sum += fast_exp2(fmaf(s[e], f[e >> 4], -ur));
-              }
-              break;
+            for (int b = 0; b < 4; b++) {
+              const TileMeta d = meta[b];
+              f[b] = d.ks * scale;
+              lv[b] = d.lv;
+              kind[b] = d.kind;
+              pos0[b] = d.pos0;
             }
-            if (named_all(pair_bar, 64, (fits && !far) || !real)) break;
+            tmem_wait_ld();
+            loaded32(s);
+            loaded32(s + 32);
+            if (kind[0] | kind[1] | kind[2] | kind[3]) {
+#pragma unroll
+              for (int b = 0; b < 4; b++) {
+                const uint32_t see = real ? sees(kind[b], pos0[b]) : kind[b] == 0 ? 0xffffu : 0u;
+#pragma unroll
+                for (int e = 0; e < 16; e++) s[16 * b + e] = see & (1u << e) ? s[16 * b + e] : -INFINITY;
+              }
+            }
+            uint32_t p[32];
+#pragma unroll 1
+            for (bool again = raise || owned;; again = true) {
+              if (again) {
+                // (the maxima are not to be taken ahead of the question)
+#pragma unroll
+                for (int e = 0; e < 64; e++) asm volatile("" : "+f"(s[e]));
+                // the rows' maxima over both parts
+                float yt = -INFINITY, xt = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < 4; b++) {
+                  float y0 = s[16 * b], y1 = s[16 * b + 1];
+#pragma unroll
+                  for (int e = 2; e < 16; e += 2) {
+                    y0 = fmaxf(y0, s[16 * b + e]);
+                    y1 = fmaxf(y1, s[16 * b + e + 1]);
+                  }
+                  y0 = fmaxf(y0, y1) * f[b];
+                  yt = fmaxf(yt, y0);
+                  xt = fmaxf(xt, y0 + lv[b]);
+                }
+                raise_to(yt, xt, j, first, slack_x, slack_y);
+              }
+              // weights 2^(x - m + kT8Up), to be rounded to fp16; their sum of a tile over
+              // 2^(kT8Up + u - m) s_v is that of the probabilities under u, except where these
+              // are so far apart that one of them may vanish
+              const float ur = u == -INFINITY ? 0.0f : u, mr = kT8Up - (mx == -INFINITY ? 0.0f : mx);
+              bool fits = true, far = false;
+              sum = 0.0f;
+#pragma unroll
+              for (int b = 0; b < 4; b++) {
+                const float up = lv[b] + mr;
+                const uint64_t f2 = f32x2(f[b], f[b]), up2 = f32x2(up, up);
+                uint64_t acc[2] = {0, 0};
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                  const uint64_t y = fma_f32x2(f32x2(s[16 * b + 2 * e], s[16 * b + 2 * e + 1]), f2, up2);
+                  const float w0 = fast_exp2(__uint_as_float((uint32_t)y)), w1 = fast_exp2(__uint_as_float((uint32_t)(y >> 32)));
+                  acc[e & 1] = add_f32x2(acc[e & 1], f32x2(w0, w1));
+                  p[8 * b + e] = pack_half2(w0, w1);
+                }
+                acc[0] = add_f32x2(acc[0], acc[1]);
+                const float tile = __uint_as_float((uint32_t)acc[0]) + __uint_as_float((uint32_t)(acc[0] >> 32));
+                const float back = up + ur;
+                sum = fmaf(tile, fast_exp2(-back), sum);
+                fits = fits && tile <= kT8Most;
+                far = far || !(fabsf(back) <= kT8Far);      // (these rows take the longer way every time)
+              }
+              if (again) {
+                if (__any_sync(0xffffffffu, real && far)) {
+                  sum = 0.0f;
+#pragma unroll
+                  for (int e = 0; e < 64; e++) sum += fast_exp2(fmaf(s[e], f[e >> 4], -ur));
+                }
+                break;
+              }
+              if (named_all(pair_bar, 64, (fits && !far) || !real)) break;
+            }
+            l += sum;
+            tmem_st32(ts, p);
           }
-          l += sum;
-          tmem_st32(ts, p);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -1166,25 +1308,17 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
       for (int j = 0; ok && j < steps; j++) {
         const int slot = j & 1;
         const TileDesc* desc = sm.desc[j & (kT8Descs - 1)] + first;
-        // The softmax has to know V's exponents with S: K's warps find them themselves, from where
-        // the values lie, while the copies are on their way.
-        int ev = 0, ek = 0, out = 0;
-        if (ELEM == DKV_BF16 && op == 0) {
-          if (j % kT8Batch == 0) ok = wait(smem_u32(&sm.dfull[j / kT8Batch & 3]), j / kT8Batch >> 2);
-          if (ok && (desc->kind == 2 || desc->kind == 3)) ev = elems_exp(desc->vsrc, true, desc->kind == 3, desc->n, a.vs);
-        }
-        ok = ok && wait(rfull + 8 * slot, j >> 1);         // (the descriptors are there, too)
+        uint32_t out = 0;
+        ok = wait(rfull + 8 * slot, j >> 1);               // (the descriptors are there, too)
         if (ok && j >= kT8Slots) ok = wait(free + 8 * slot, (j >> 1) - 1);
         if (!ok) break;
         const uint32_t to0 = place(first) + slot * kT8Slot, to1 = place(first + 1) + slot * kT8Slot;
         const int kind = desc->kind;
         if (kind == 2 || kind == 3) {
           // (the second place is none)
-          int ex;
-          if (kind == 2) ex = put_tail<ELEM>(ring + slot * kT8Entry, op, desc->n, to0);
-          else ex = put_drafts<ELEM>(ring + slot * kT8Entry, op, desc->n, (op ? draft_place(first) : base + 2 * first * 1024) + slot * kT8Slot);
-          if (!op) ek = ex;
-          else out = ex;
+          const TileExps exps{sm.kexp[j & (kT8Metas - 1)][warp & 3], sm.vexp[slot][warp & 3]};
+          if (kind == 2) out = put_tail<ELEM>(ring + slot * kT8Entry, op, desc->n, to0, exps);
+          else out = put_drafts<ELEM>(ring + slot * kT8Entry, op, desc->n, (op ? draft_place(first) : base + 2 * first * 1024) + slot * kT8Slot, exps);
         } else {
 #pragma unroll 1
           for (int t = 0; t < 2; t++)
@@ -1210,14 +1344,12 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
             }
         }
         if (op && lane == 0) {
-          sm.taken[j & 15][warp & 3] = make_int2(desc->pos0, kind << 16 | out);
+          sm.taken[j & 15][warp & 3] = make_int2(desc->pos0, kind << 16 | (int)out);
           if (out) sm.any_taken = 1;
         }
         if (op == 0 && lane < 2) {
           const TileDesc* d = desc + lane;
-          const bool elems = ELEM == DKV_BF16 && (d->kind == 2 || d->kind == 3);
-          sm.meta[j & (kT8Metas - 1)][first + lane] =
-              TileMeta{elems ? kLogitScale * pow2(ek) : d->ks, elems ? (float)ev : d->lv, d->pos0, d->kind < 2 ? d->kind : d->kind - 1};
+          sm.meta[j & (kT8Metas - 1)][first + lane] = TileMeta{d->ks, d->lv, d->pos0, d->kind};
         }
         fence_proxy_async();
         __syncwarp();

@@ -616,8 +616,8 @@ int dkv_cache8_rotate(const dkv_cache8* cache, int32_t n_tok, const int32_t* pos
  * Sums are in fp32. Weights enter the value product rounded to fp16 (relative 2^-11;
  * below 2^-21 of the row's largest weighted scale, off by up to 2^-32 of it), the
  * sum of weights unrounded; bf16 queries, tail entries and drafts meet the products
- * as fp16 after division by a power of two (of a query row, or of the K or V of 16
- * tokens; what lies below 2^-24 of the largest is lost). What a row does
+ * as fp16 after division by a power of two (of a query row: what lies below 2^-25 of
+ * its largest is lost; of a token's K or V: below 2^-32). What a row does
  * not see never enters its result, whatever it holds: rows that come out infinite or
  * NaN, and rows that see a draft or tail entry with such a V, are computed again over what
  * they see (a row and 4096 tokens: 55 us, most rows at once; calls without such values pay
