@@ -64,6 +64,7 @@ constexpr int kT8Turn = 4;
 constexpr float kT8Up = 7.0f;       // log2 of a weight at its row's maximum
 constexpr float kT8Most = 32768.0f; // largest sum of a row's weights of one tile (fp16 holds 65504)
 constexpr float kT8Far = 60.0f;     // log2 of how far weights may be from probabilities
+constexpr float kT8Sum = 1.15292150460684698e18f;    // largest sum of probabilities under an earlier maximum, 2^kT8Far
 
 // A request of the call: N tokens stored, M drafts (0: padding).
 struct TreeReq {
@@ -513,8 +514,8 @@ struct TreeSmem {
   unsigned there[2 * kT8Descs];        // places of a step that hold a tile (the products are behind the conversion)
   TileMeta meta[kT8Metas][kT8Step];    // (K of step j comes when the softmax has read that of step j - 5)
   // of a step's tiles of 16 bits: K's powers of two, V's exponents (there with V, not with S)
-  uint16_t kexp[kT8Metas][kT8Step / 2][kSub];
-  float vexp[kT8Slots][kT8Step / 2][kSub];
+  alignas(16) uint16_t kexp[kT8Metas][kT8Step / 2][kSub];
+  alignas(16) float vexp[kT8Slots][kT8Step / 2][kSub];
   TreePlan plan;
   int parents[kMaxNodes];
   float2 pair[2][2][kT8Rows];      // what the two warps of a row tell each other
@@ -616,12 +617,12 @@ __device__ __forceinline__ TileDesc describe_tile(const Cache8View& c, const Tre
   return d;
 }
 
-// ---- powers of two: K and V of each bf16 token are divided by one of their own, which brings the
-// token's largest value to [128, 256). (One for the tile: what a row does not see would set the
-// power for what it does. A sibling's V 2^30 above the others left rows that do not see it wrong
-// by 25 %, one 2^60 above left zeros.) ----
-template <int ELEM>
-constexpr bool kT8Own = ELEM == DKV_BF16;
+// ---- powers of two: K of each bf16 token and V of each token of 16 bits are divided by one of their
+// own, which brings the token's largest value to [128, 256). (One for the tile: what a row does not
+// see would set the power for what it does. A sibling's V 2^30 above the others left rows that do
+// not see it wrong by 25 %, one 2^60 above left zeros. V in fp16 as it is: the weights of codes, which
+// carry their scale, lie 2^-20 below and lose their bits beside a heavier token of small V in the same
+// step; 64 codes beside a draft with V of 1e-4 were off by 7 times the bound of rounded weights.) ----
 // Largest finite magnitudes so far of the low and of the high values: with the exponent's last
 // bit added to the bits of the magnitudes, infinities and NaN are negative numbers of 16 bits.
 template <int ELEM>
@@ -640,15 +641,30 @@ __device__ __forceinline__ uint32_t swap_halves(uint32_t x) { return prmt(x, x, 
 template <int ELEM>
 __device__ __forceinline__ int exp_of(uint32_t top) {
   const uint32_t x = __float_as_uint(elem_float<ELEM>((uint16_t)((top & 0xffffu) - kT8Bias<ELEM>)));
-  return max(-120, (int)(x >> 23) - (127 + 7));
+  return max(ELEM == DKV_F16 ? -29 : -120, (int)(x >> 23) - (127 + 7));
+}
+// What brings two values there, by 2^-lo and 2^-hi: bf16 in fp32; fp16 in two steps, since one
+// factor of fp16 is 2^15 at most (the first of two that enlarge is exact).
+struct Factors {
+  uint32_t a, b;
+};
+template <int ELEM>
+__device__ __forceinline__ Factors factors(int lo, int hi) {
+  if (ELEM == DKV_BF16) return Factors{__float_as_uint(pow2(-lo)), __float_as_uint(pow2(-hi))};
+  const int l1 = min(-lo, 14), h1 = min(-hi, 14), l2 = min(-lo - l1, 15), h2 = min(-hi - h1, 15);
+  return Factors{(uint32_t)(15 + l1) << 10 | (uint32_t)(15 + h1) << 26, (uint32_t)(15 + l2) << 10 | (uint32_t)(15 + h2) << 26};
 }
 template <int ELEM>
-__device__ __forceinline__ uint32_t half_of(uint32_t w, float lo, float hi) {
-  return pack_half2(lo_elem<ELEM>(w) * lo, hi_elem<ELEM>(w) * hi);
+__device__ __forceinline__ uint32_t half_of(uint32_t w, const Factors& f) {
+  if (ELEM == DKV_BF16) return pack_half2(lo_elem<DKV_BF16>(w) * __uint_as_float(f.a), hi_elem<DKV_BF16>(w) * __uint_as_float(f.b));
+  uint32_t x;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(x) : "r"(w), "r"(f.a));
+  asm("mul.rn.f16x2 %0, %0, %1;\n" : "+r"(x) : "r"(f.b));
+  return x;
 }
-// What the softmax has to know of the 16 tokens: K's powers of two, V's exponents.
+// What the softmax has to know of the 16 tokens: K's powers of two (bf16), V's exponents.
 struct TileExps {
-  uint16_t* k;      // bf16
+  uint16_t* k;
   float* v;
 };
 __device__ __forceinline__ void put_exp(const TileExps& e, bool v, int token, int ex) {
@@ -688,6 +704,7 @@ __device__ __noinline__ uint32_t take_out(uint8_t* src, bool draft, int n) {
 template <int ELEM>
 __device__ __noinline__ uint32_t put_tail(uint8_t* src, bool v, int n, uint32_t at, TileExps exps) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const bool scaled = v || ELEM == DKV_BF16;         // (K in fp16 stays as it is)
   // The four 8 x 8 matrices of m-step f, of K the first eight features' first: even words are of token
   // g (K) or tokens 2t and 2t + 1 (V, low and high halves), odd ones of those eight tokens on. What
   // lies behind the valid tokens becomes 0 (0 times what it may hold is not).
@@ -699,7 +716,7 @@ __device__ __noinline__ uint32_t put_tail(uint8_t* src, bool v, int n, uint32_t 
   };
   uint32_t a = 0, b = 0, out = 0;
 #pragma unroll 1
-  while (v || ELEM == DKV_BF16) {          // (K in fp16 stays as it is)
+  while (scaled) {
     uint32_t acc = 0;
     a = b = kT8Bias<ELEM> * 0x10001u;
 #pragma unroll 2
@@ -715,8 +732,8 @@ __device__ __noinline__ uint32_t put_tail(uint8_t* src, bool v, int n, uint32_t 
     if (!v || __builtin_expect(!__any_sync(0xffffffffu, found_not_finite(acc)), 1)) break;
     out = take_out<ELEM>(src, false, n);
   }
-  float fa0 = 1.0f, fa1 = 1.0f, fb0 = 1.0f, fb1 = 1.0f;
-  if (kT8Own<ELEM>) {
+  Factors fa{}, fb{};
+  if (scaled) {
     if (!v) {
       a = max_s16x2(a, swap_halves(a));
       b = max_s16x2(b, swap_halves(b));
@@ -735,15 +752,13 @@ __device__ __noinline__ uint32_t put_tail(uint8_t* src, bool v, int n, uint32_t 
         put_exp(exps, v, 2 * t + 9, b1);
       }
     }
-    fa0 = pow2(-a0);
-    fa1 = pow2(-a1);
-    fb0 = pow2(-b0);
-    fb1 = pow2(-b1);
+    fa = factors<ELEM>(a0, a1);
+    fb = factors<ELEM>(b0, b1);
   }
 #pragma unroll 2
   for (int f = 0; f < 8; f++) {
     uint4 x = load(f);
-    if (kT8Own<ELEM>) x = make_uint4(half_of<ELEM>(x.x, fa0, fa1), half_of<ELEM>(x.y, fb0, fb1), half_of<ELEM>(x.z, fa0, fa1), half_of<ELEM>(x.w, fb0, fb1));
+    if (scaled) x = make_uint4(half_of<ELEM>(x.x, fa), half_of<ELEM>(x.y, fb), half_of<ELEM>(x.z, fa), half_of<ELEM>(x.w, fb));
     if (!v) stmatrix4((at + (f >> 2) * 16384) ^ ((f & 3) << 5), x.x, x.z, x.y, x.w);
     else stmatrix4(at + f * 2048, x.x, x.y, x.z, x.w);
   }
@@ -759,6 +774,7 @@ __device__ __noinline__ uint32_t put_tail(uint8_t* src, bool v, int n, uint32_t 
 template <int ELEM>
 __device__ __noinline__ uint32_t put_drafts(uint8_t* rows, bool v, int n, uint32_t to, TileExps exps) {
   const int lane = threadIdx.x & 31, row = lane & 15, half = lane >> 4, r = row & 7;
+  const bool scaled = v || ELEM == DKV_BF16;
   const uint32_t src = smem_u32(rows);
   // y -> column, such that r -> column and r -> column xor r are one to one
   const int turn = (r << 1 & 7) ^ (r & 4 ? 3 : 0);
@@ -770,7 +786,7 @@ __device__ __noinline__ uint32_t put_drafts(uint8_t* rows, bool v, int n, uint32
   };
   uint32_t top = 0, out = 0;
 #pragma unroll 1
-  while (v || ELEM == DKV_BF16) {
+  while (scaled) {
     uint32_t acc = 0;
     top = kT8Bias<ELEM> * 0x10001u;
 #pragma unroll 2
@@ -785,17 +801,17 @@ __device__ __noinline__ uint32_t put_drafts(uint8_t* rows, bool v, int n, uint32
     if (!v || __builtin_expect(!__any_sync(0xffffffffu, found_not_finite(acc)), 1)) break;
     out = take_out<ELEM>(rows, true, n);
   }
-  float f = 1.0f;
-  if (kT8Own<ELEM>) {
+  Factors f{};
+  if (scaled) {
     top = max_s16x2(top, swap_halves(top));
     const int ex = exp_of<ELEM>(max_s16x2(top, __shfl_xor_sync(0xffffffffu, top, 16)));
     if (half == 0) put_exp(exps, v, row, ex);
-    f = pow2(-ex);
+    f = factors<ELEM>(ex, ex);
   }
 #pragma unroll 2
   for (int y = 0; y < 8; y++) {
     uint4 x = load(y);
-    if (kT8Own<ELEM>) x = make_uint4(half_of<ELEM>(x.x, f, f), half_of<ELEM>(x.y, f, f), half_of<ELEM>(x.z, f, f), half_of<ELEM>(x.w, f, f));
+    if (scaled) x = make_uint4(half_of<ELEM>(x.x, f), half_of<ELEM>(x.y, f), half_of<ELEM>(x.z, f), half_of<ELEM>(x.w, f));
     sts128(v ? mine + ((y ^ turn) << 4) : to + half * 16384 + row * 128 + ((y ^ turn ^ r) << 4), x.x, x.y, x.z, x.w);
   }
   if (v) {
@@ -994,25 +1010,16 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         then = tree_item(c, a, sm.plan, pos, hi);
         if (real_of(then)) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(q_of(then)));
       }
-      // which tokens of a tile the row sees
-      auto sees = [&](int kind, int pos0) {
-        const int w = pos0 >> 5;
-        return kind == 0 ? 0xffffu : kind == 1 || kind == 2 ? sees_stored(a, it.N, node.depth, pos0) : kind != 3 ? 0u
-               : (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (pos0 & 31);
-      };
       float mx = -INFINITY, u = -INFINITY, l = 0.0f;
       const int end = j + it.n;
       bool first = true, raise = true;
-      // The running maxima take in yt, xt of a step: all of them where one row's would leave its
-      // own by more than the slack.
-      auto raise_to = [&](float yt, float xt, int j, bool first, float slack_x, float slack_y) {
+      // The rows' running maxima take in yt, xt of a step over both parts.
+      auto raise_to = [&](float yt, float xt, int j, bool first) {
         sm.pair[told][part][r] = make_float2(yt, xt);
         named_sync(pair_bar, 64);
         const float2 other = sm.pair[told][part ^ 1][r];
         told ^= 1;
         const float nu = fmaxf(u, fmaxf(yt, other.x)), nm = fmaxf(mx, fmaxf(xt, other.y));
-        // (the same for both warps of a row)
-        if (!__any_sync(0xffffffffu, nm > mx + slack_x || nu > u + slack_y)) return;
         l *= nu == -INFINITY ? 1.0f : fast_exp2(u - nu);
         if (!first) {        // O is still once the last product is done
           ok = wait(pvdone((j - 1) & 3), (j - 1) >> 2) && ok;
@@ -1044,16 +1051,11 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           const uint32_t ts = t_s(j & 1) + tl + 64 * part;
           const TileMeta* meta = sm.meta[j & (kT8Metas - 1)] + 4 * part;
           float sum = 0.0f;
-          // a step with tiles of 16 bits, whose tokens have exponents of their own: the maxima are
-          // taken ahead of the weights there, which may then exceed them by the slack (a tile's weights
-          // sum to 2^15 at most, its probabilities under u to 2^64)
-          const int place = kT8Step * (it.s0 + it.n - (end - j));
-          const bool owned = kT8Own<ELEM> && place + kT8Step > it.tiles.elems;
-          const float slack_x = owned ? 4.0f : 0.0f, slack_y = owned ? kT8Far : 0.0f;
-          if (owned && place + 4 * part >= it.tiles.elems) {
-            // this warp's part holds two of them
-            float y[2][16], v[2][16], yt = -INFINITY, xt = -INFINITY;
+          if (kT8Step * (it.s0 + it.n - (end - j)) + 4 * part >= it.tiles.elems) {
+            // two tiles of 16 bits, whose tokens have exponents of their own
+            float y[2][16];
             bool is[2];
+            auto vexp = [&](int b, int e) { return *reinterpret_cast<const ulonglong2*>(&sm.vexp[j & 1][2 * part + b][4 * e]); };
             tmem_ld16_nowait(ts, y[0]);
             tmem_ld16_nowait(ts + 32, y[1]);
             ok = wait(vfull(j & 1), j >> 1) && ok;      // (V of step j + 2 waits for these weights)
@@ -1063,46 +1065,73 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
               const TileMeta d = meta[2 * b];
               is[b] = d.kind != 4;
               if (!is[b]) continue;
-              const uint32_t see = real ? sees(d.kind, d.pos0) : 0u;
+              const int w = d.pos0 >> 5;
+              const uint32_t see = !real ? 0xffffu : d.kind == 2 ? sees_stored(a, it.N, node.depth, d.pos0)
+                                   : (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (d.pos0 & 31) & 0xffffu;
               const float f = d.ks * scale;
-              const uint4* kp = reinterpret_cast<const uint4*>(sm.kexp[j & (kT8Metas - 1)][2 * part + b]);
-              const float4* vp = reinterpret_cast<const float4*>(sm.vexp[j & 1][2 * part + b]);
-#pragma unroll
-              for (int e = 0; e < 4; e++) {
-                const float4 x = vp[e];
-                v[b][4 * e] = x.x;
-                v[b][4 * e + 1] = x.y;
-                v[b][4 * e + 2] = x.z;
-                v[b][4 * e + 3] = x.w;
-              }
+              const uint4* kp = reinterpret_cast<const uint4*>(sm.kexp[j & (kT8Metas - 1)][2 * part + b]);      // (bf16)
 #pragma unroll
               for (int e = 0; e < 2; e++) {
-                const uint4 x = kp[e];
+                const uint4 x = ELEM == DKV_BF16 ? kp[e] : make_uint4(0, 0, 0, 0);
                 const uint32_t k[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int z = 0; z < 8; z++) {
                   float& o = y[b][8 * e + z];
                   asm volatile("" : "+f"(o));
-                  o *= f * __uint_as_float(z & 1 ? k[z >> 1] & 0xffff0000u : k[z >> 1] << 16);
-                  o = see & (1u << (8 * e + z)) ? o : -INFINITY;
-                  yt = fmaxf(yt, o);
-                  xt = fmaxf(xt, o + v[b][8 * e + z]);
+                  o *= ELEM == DKV_BF16 ? f * __uint_as_float(z & 1 ? k[z >> 1] & 0xffff0000u : k[z >> 1] << 16) : f;
                 }
               }
-            }
-            raise_to(yt, xt, j, first, slack_x, slack_y);
-            const float ur = u == -INFINITY ? 0.0f : u, mr = kT8Up - (mx == -INFINITY ? 0.0f : mx);
+              if (!__all_sync(0xffffffffu, see == 0xffffu)) {
 #pragma unroll
-            for (int b = 0; b < 2; b++) {
-              if (!is[b]) continue;
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 8; e++) {
-                const float y0 = y[b][2 * e], y1 = y[b][2 * e + 1];
-                sum += fast_exp2(y0 - ur) + fast_exp2(y1 - ur);
-                w[e] = pack_half2(fast_exp2(y0 + v[b][2 * e] + mr), fast_exp2(y1 + v[b][2 * e + 1] + mr));
+                for (int e = 0; e < 16; e++) y[b][e] = see & (1u << e) ? y[b][e] : -INFINITY;
               }
-              tmem_st8(ts + 16 * b, w);
+            }
+#pragma unroll 1
+            for (bool again = raise;; again = true) {
+              if (again) {
+                float yt = -INFINITY, xt = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < 2; b++)
+                  if (is[b]) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) {
+                      const ulonglong2 v = vexp(b, e >> 2);
+#pragma unroll
+                      for (int z = 0; z < 4; z++) {
+                        asm volatile("" : "+f"(y[b][e + z]));
+                        const unsigned long long v2 = z & 2 ? v.y : v.x;
+                        yt = fmaxf(yt, y[b][e + z]);
+                        xt = fmaxf(xt, y[b][e + z] + __uint_as_float((uint32_t)(z & 1 ? v2 >> 32 : v2)));
+                      }
+                    }
+                  }
+                raise_to(yt, xt, j, first);
+              }
+              const float ur = u == -INFINITY ? 0.0f : u, mr = kT8Up - (mx == -INFINITY ? 0.0f : mx);
+              const uint64_t ur2 = f32x2(-ur, -ur), mr2 = f32x2(mr, mr);
+              bool fits = true;
+              uint64_t own = 0;         // probabilities under u: their exponentials by themselves
+#pragma unroll
+              for (int b = 0; b < 2; b++) {
+                if (!is[b]) continue;
+                uint64_t acc = 0;
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                  const ulonglong2 v = vexp(b, e >> 1);
+                  const uint64_t y2 = f32x2(y[b][2 * e], y[b][2 * e + 1]), t = add_f32x2(y2, ur2);
+                  const uint64_t x = add_f32x2(y2, add_f32x2(e & 1 ? v.y : v.x, mr2));
+                  own = add_f32x2(own, f32x2(fast_exp2(__uint_as_float((uint32_t)t)), fast_exp2(__uint_as_float((uint32_t)(t >> 32)))));
+                  const float w0 = fast_exp2(__uint_as_float((uint32_t)x)), w1 = fast_exp2(__uint_as_float((uint32_t)(x >> 32)));
+                  acc = add_f32x2(acc, f32x2(w0, w1));
+                  w[e] = pack_half2(w0, w1);
+                }
+                fits = fits && __uint_as_float((uint32_t)acc) + __uint_as_float((uint32_t)(acc >> 32)) <= kT8Most;
+                tmem_st8(ts + 16 * b, w);
+              }
+              sum = __uint_as_float((uint32_t)own) + __uint_as_float((uint32_t)(own >> 32));
+              fits = fits && sum <= kT8Sum;
+              if (again || named_all(pair_bar, 64, fits || !real)) break;
             }
             l += sum;
           } else {
@@ -1125,19 +1154,18 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
             if (kind[0] | kind[1] | kind[2] | kind[3]) {
 #pragma unroll
               for (int b = 0; b < 4; b++) {
-                const uint32_t see = real ? sees(kind[b], pos0[b]) : kind[b] == 0 ? 0xffffu : 0u;
+                const uint32_t see = kind[b] == 0 ? 0xffffu : real && kind[b] == 1 ? sees_stored(a, it.N, node.depth, pos0[b]) : 0u;
 #pragma unroll
                 for (int e = 0; e < 16; e++) s[16 * b + e] = see & (1u << e) ? s[16 * b + e] : -INFINITY;
               }
             }
             uint32_t p[32];
 #pragma unroll 1
-            for (bool again = raise || owned;; again = true) {
+            for (bool again = raise;; again = true) {
               if (again) {
                 // (the maxima are not to be taken ahead of the question)
 #pragma unroll
                 for (int e = 0; e < 64; e++) asm volatile("" : "+f"(s[e]));
-                // the rows' maxima over both parts
                 float yt = -INFINITY, xt = -INFINITY;
 #pragma unroll
                 for (int b = 0; b < 4; b++) {
@@ -1151,7 +1179,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
                   yt = fmaxf(yt, y0);
                   xt = fmaxf(xt, y0 + lv[b]);
                 }
-                raise_to(yt, xt, j, first, slack_x, slack_y);
+                raise_to(yt, xt, j, first);
               }
               // weights 2^(x - m + kT8Up), to be rounded to fp16; their sum of a tile over
               // 2^(kT8Up + u - m) s_v is that of the probabilities under u, except where these

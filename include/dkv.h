@@ -613,12 +613,14 @@ int dkv_cache8_rotate(const dkv_cache8* cache, int32_t n_tok, const int32_t* pos
  *            apart (multiples of 8); out contiguous, of elem_type, apart from them.
  *   workspace  device, 16-byte aligned, at least dkv_cache8_tree_workspace bytes; what
  *            it holds does not matter. Calls that may overlap need one each.
- * Sums are in fp32. Weights enter the value product rounded to fp16 (relative 2^-11;
- * below 2^-21 of the row's largest weighted scale, off by up to 2^-32 of it), the
- * sum of weights unrounded; bf16 queries, tail entries and drafts meet the products
- * as fp16 after division by a power of two (of a query row: what lies below 2^-25 of
- * its largest is lost; of a token's K or V: below 2^-32). What a row does
- * not see never enters its result, whatever it holds: rows that come out infinite or
+ * Sums are in fp32. Weights enter the value product rounded to fp16 (relative 2^-11; a
+ * weight whose product with its scale lies below 2^-21 of the row's largest such product
+ * is off by up to 2^-32 of that), the sum of weights unrounded. A code's scale is its
+ * block's. V of each tail entry and draft has a power of two of its own for a scale, and so
+ * have K of each such bf16 token and each row of bf16 queries, over which they meet the
+ * products as fp16 (what lies below 2^-32 of a token's largest value or 2^-25 of a query
+ * row's is lost). What a row does not see never enters its result, whatever it holds (but
+ * for the scale of a block that the row sees a part of): rows that come out infinite or
  * NaN, and rows that see a draft or tail entry with such a V, are computed again over what
  * they see (a row and 4096 tokens: 55 us, most rows at once; calls without such values pay
  * nothing). Means of finite values are finite. The same inputs give the same bits.

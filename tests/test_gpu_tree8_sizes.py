@@ -81,3 +81,88 @@ def test_queries_of_other_rows_do_not_matter():
     parents = [[-1] * M]
     out = run_tree(c, [n], parents, q, k, v)
     check_tree(c, out, [n], parents, q, k, v, [M], nodes={0, 2, 3, 4, 5, 7})
+
+
+# ------------------------------------------------------------------ values far from 1
+
+def close(got, q, k, v, size, elem):
+    """Attention of q [G][128] over k, v [n][128] in 64 bits and its bound: weights rounded
+    to fp16 (2^-11), and where they lie under 2^-21 of the row's largest weight times size
+    (a token's or its block's largest |v|) off by half of fp16's smallest step: weights
+    stand 2^7 above their place beside values of at most 448, the row's largest beside
+    one that came to 128 or more, so that is 2^-25 * 448 / (2^7 * 128) < 2^-30 of the largest
+    p * size for a token. Logits and exponentials as in cache8_ref.tolerance."""
+    s = q @ k.T / np.sqrt(128)
+    p = np.exp(s - s.max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    want, pv = p @ v, p @ np.abs(v)
+    qk = (np.abs(q) @ np.abs(k).T).max() / np.sqrt(128)
+    d = 2.0 ** -11 + 2 * 128 * 2.0 ** -23 * qk + 2.0 ** -21
+    tol = torch.finfo(elem).eps / 2 * np.abs(want) * (1 + d) + d * pv
+    tol += len(k) * 2.0 ** -30 * (p * size).max(axis=1, keepdims=True)
+    tol += torch.finfo(elem).tiny * torch.finfo(elem).eps / 2           # half of the type's smallest step
+    err = np.abs(got - want)
+    return (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("elem", [F16, BF16])
+@pytest.mark.parametrize("heavy", ["draft", "tail"])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -8, 2.0 ** -11, 2.0 ** -13, 300.0])
+@pytest.mark.parametrize("n,T,log", [(4100, 128, 14), (12100, 128, 14), (66, 64, 5.5), (66, 64, 7), (66, 64, 8.3), (65, 16, 7.5), (35, 32, 6)])
+def test_light_tokens_beside_a_heavy_one(elem, heavy, size, n, T, log):
+    """One token of 16 bits with 2^log times the weight of each of many codes, which hold a
+    good part of the mass all the same and round alike, also where they enter the products
+    together; values of any size around a mean."""
+    rng = np.random.default_rng(41)
+    G = 4
+    c = make(1, G, T, 1, n // T + 1, elem, E4M3, 1, seed=14)
+    q = torch.from_numpy(np.repeat(rng.standard_normal((1, 1, 128)), G, 1).astype(np.float32)).to(elem).cuda()
+    own = q[:, :1] * (log * np.log(2) * np.sqrt(128) / float((q[0, 0].double() ** 2).sum()))
+    value = lambda m: torch.from_numpy((size * (1 + 0.3 * rng.standard_normal((m, 1, 128)))).astype(np.float32)).to(elem).cuda()
+    k, v = torch.from_numpy((0.001 * rng.standard_normal((n, 1, 128))).astype(np.float32)).to(elem).cuda(), value(n)
+    if heavy == "tail":
+        k[n - 1] = own
+    c.append([0], [0], [n], k, v)
+    dk = own if heavy == "draft" else torch.zeros_like(own)
+    dv = value(1)
+    out = run_tree(c, [n], None, q, dk, dv)
+    torch.cuda.synchronize()
+    assert c.c.status_words.tolist() == [0, 0]
+    ks, vs = (np.concatenate([x, y.double().cpu().numpy()[0]]) for x, y in zip(c.ref.values(0, n, 0), (dk, dv)))
+    block = np.abs(vs).max(axis=1)
+    for b in range(n // T):
+        block[b * T:(b + 1) * T] = block[b * T:(b + 1) * T].max()
+    ok, worst = close(out[0].double().cpu().numpy(), q[0].double().cpu().numpy(), ks, vs, block, elem)
+    assert ok, worst
+
+
+@pytest.mark.parametrize("elem", [F16, BF16])
+@pytest.mark.parametrize("where", ["drafts", "tail"])
+def test_values_of_many_sizes_side_by_side(elem, where):
+    """Neighbouring tokens whose values lie many powers of two apart, seen one by one (chains
+    behind a short window): each row within the bound of what it sees."""
+    rng = np.random.default_rng(42)
+    M, T, n = 24, 64, 56
+    c = make(2, 2, T, 1, 1, elem, INT8, M, seed=15)
+    low, high = (-12, 12) if elem == F16 else (-90, 90)
+    powers = lambda m: torch.from_numpy(2.0 ** rng.integers(low, high, (m, 1, 1)).astype(np.float32)).cuda()
+    k, v = c.vec(rng, n, 2), c.vec(rng, n, 2)
+    if where == "tail":
+        v = (v.float() * powers(n)).to(elem)
+    c.append([0], [0], [n], k, v)
+    q, dk, dv = drafts(c, rng, 1, M)
+    if where == "drafts":
+        dv = (dv.float() * powers(M)).to(elem)
+    parents = [list(range(-1, M - 1))]
+    for window in (1, 2, 5, 0):
+        out = run_tree(c, [n], parents, q, dk, dv, window=window).double().cpu().numpy()
+        assert c.c.status_words.tolist() == [0, 0]
+        for h in range(2):
+            ks, vs = c.ref.values(0, n, h)
+            for m in range(M):
+                st, dr = tref.seen(parents[0], m, n, window, 0)
+                kk = np.concatenate([ks[st], dk.double().cpu().numpy()[dr, h]])
+                vv = np.concatenate([vs[st], dv.double().cpu().numpy()[dr, h]])
+                ok, worst = close(out[m, 2 * h:2 * h + 2], q.double().cpu().numpy()[m, 2 * h:2 * h + 2], kk, vv,
+                                  np.abs(vv).max(axis=1), elem)
+                assert ok, (window, h, m, worst)
