@@ -637,11 +637,12 @@ __device__ __forceinline__ uint32_t top_pair(uint32_t m, uint32_t w) {
   return max_s16x2(m, (w & 0x7fff7fffu) + kT8Bias<ELEM> * 0x10001u);
 }
 __device__ __forceinline__ uint32_t swap_halves(uint32_t x) { return prmt(x, x, 0x1032u); }
-// The exponent for one of the two.
+// The exponent for one of the two. Not below -112: results come back by that and kT8Up, which has
+// to stay a normal number; the smallest V then comes to 2^-14, where fp16 keeps what bf16 holds.
 template <int ELEM>
 __device__ __forceinline__ int exp_of(uint32_t top) {
   const uint32_t x = __float_as_uint(elem_float<ELEM>((uint16_t)((top & 0xffffu) - kT8Bias<ELEM>)));
-  return max(ELEM == DKV_F16 ? -29 : -120, (int)(x >> 23) - (127 + 7));
+  return max(ELEM == DKV_F16 ? -29 : -112, (int)(x >> 23) - (127 + 7));
 }
 // What brings two values there, by 2^-lo and 2^-hi: bf16 in fp32; fp16 in two steps, since one
 // factor of fp16 is 2^15 at most (the first of two that enlarge is exact).
@@ -1236,7 +1237,8 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         const float lsum = l + sm.pair[told][part ^ 1][r].x;
         told ^= 1;
         // a sum that left fp32's range: NaN, which the second kernel looks into
-        float f = lsum == 0.0f ? 0.0f : lsum < INFINITY ? __fdiv_rn(fast_exp2(mx - kT8Up - u), lsum) : __uint_as_float(0x7fffffffu);
+        float f = lsum == 0.0f ? 0.0f : lsum < INFINITY ? __fdiv_rn(1.0f, lsum) : __uint_as_float(0x7fffffffu);
+        const float fv = f == 0.0f ? 0.0f : fast_exp2(mx - kT8Up - u);       // (one after the other: the smallest values stay normal till the end)
         if (__builtin_expect(*(volatile int*)&sm.any_taken, 0)) {
           // tiles of 16 bits are a unit's last ones, in five steps at most
 #pragma unroll 1
@@ -1260,7 +1262,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 16; e++) {
             asm volatile("" : "+f"(o[e]));
-            o[e] *= f;
+            o[e] = o[e] * f * fv;
           }
         };
         if (whole) {

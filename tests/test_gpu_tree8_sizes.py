@@ -166,3 +166,32 @@ def test_values_of_many_sizes_side_by_side(elem, where):
                 ok, worst = close(out[m, 2 * h:2 * h + 2], q.double().cpu().numpy()[m, 2 * h:2 * h + 2], kk, vv,
                                   np.abs(vv).max(axis=1), elem)
                 assert ok, (window, h, m, worst)
+
+
+@pytest.mark.parametrize("up", [-100, -108, -114, -119, -123])
+@pytest.mark.parametrize("n", [0, 21, 150])
+def test_the_smallest_values_stay(up, n):
+    """bf16 values near the type's smallest normal number, and nothing else in sight: a window
+    of one and two positions over drafts, and what the tail holds."""
+    rng = np.random.default_rng(43)
+    M = 5
+    c = make(2, 3, 128, 1, 2, BF16, E4M3, M, seed=16)
+    k, v = c.vec(rng, max(n, 1), 2), c.vec(rng, max(n, 1), 2)
+    v[max(n, 128) - 128:] *= 2.0 ** up
+    if n:
+        c.append([0], [0], [n], k[:n], v[:n])
+    q, dk, dv = drafts(c, rng, 1, M)
+    dv *= 2.0 ** up
+    parents = [[-1, 0, 1, 0, -1]]
+    for window in (1, 2, 10):
+        out = run_tree(c, [n], parents, q, dk, dv, window=window).double().cpu().numpy()
+        assert c.c.status_words.tolist() == [0, 0]
+        qn, kn, vn = (x.double().cpu().numpy() for x in (q, dk, dv))
+        for h in range(2):
+            ks, vs = c.ref.values(0, n, h) if n else (np.zeros((0, 128)),) * 2
+            for m in range(M):
+                st, dr = tref.seen(parents[0], m, n, window, 0)
+                kk, vv = np.concatenate([ks[st], kn[dr, h]]), np.concatenate([vs[st], vn[dr, h]])
+                g = slice(3 * h, 3 * h + 3)
+                ok, worst = close(out[m, g], qn[m, g], kk, vv, np.abs(vv).max(axis=1), BF16)
+                assert ok, (window, h, m, worst)
