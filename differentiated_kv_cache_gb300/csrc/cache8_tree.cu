@@ -175,7 +175,9 @@ __device__ __forceinline__ uint32_t sees_stored(const Tree8Args& a, int N, int d
 // ---- one row by a block of the second kernel, from the formula in fp32, over what the row sees:
 // rows that came out infinite or NaN (a code that a row does not see may have met its weight of
 // 0). A warp takes every eighth tile, 32 of which it looks up at once, a lane each; the eight join.
-// 4096 tokens take a row 55 us; a warp a row, its code unrolled over all kinds of tiles, took 3300:
+// O is the mean so far, not a sum over weights of up to 1 each: bf16 values of the type's largest
+// size leave fp32's range as the sum of two.
+// 4096 tokens take a row 64 us (sums: 55); a warp a row, its code unrolled over all kinds of tiles, took 3300:
 // a tile was 100 KB of instructions. ----
 // A lane's share of a tile in the stored order: K of tokens g and g + 8, features
 // 16 m + 2 t + {0, 1, 8, 9}; V of features 16 m + g, + 8 and tokens 2t, 2t + 1, 2t + 8, 2t + 9.
@@ -317,20 +319,24 @@ struct Walk {
 #pragma unroll
         for (int d = 4; d <= 16; d <<= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
         if (now > top) {
-          const float f = fast_exp2(top - now);
-          l *= f;
-#pragma unroll
-          for (int e = 0; e < 16; e++) o[e] *= f;
+          l *= fast_exp2(top - now);
           top = now;
         }
         const float under = top == -INFINITY ? 0.0f : top;
         const float p0 = fast_exp2(y0 - under), p1 = fast_exp2(y1 - under);
-        l += p0 + p1;
+        float more = p0 + p1;            // lanes of one t hold the tokens once
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) more += __shfl_xor_sync(0xffffffffu, more, d);
+        const float before = l;
+        l += more;
+        const float part = l == 0.0f ? 0.0f : __frcp_rn(l), keep = before * part, scaled = part * vs;
+#pragma unroll
+        for (int e = 0; e < 16; e++) o[e] *= keep;
         float w[4];
-        w[0] = __shfl_sync(0xffffffffu, p0, 8 * tt) * vs;
-        w[1] = __shfl_sync(0xffffffffu, p0, 8 * tt + 4) * vs;
-        w[2] = __shfl_sync(0xffffffffu, p1, 8 * tt) * vs;
-        w[3] = __shfl_sync(0xffffffffu, p1, 8 * tt + 4) * vs;
+        w[0] = __shfl_sync(0xffffffffu, p0, 8 * tt) * scaled;
+        w[1] = __shfl_sync(0xffffffffu, p0, 8 * tt + 4) * scaled;
+        w[2] = __shfl_sync(0xffffffffu, p1, 8 * tt) * scaled;
+        w[3] = __shfl_sync(0xffffffffu, p1, 8 * tt + 4) * scaled;
         const uint32_t at = seen >> (2 * tt);
 #pragma unroll
         for (int f = 0; f < 16; f++) {            // features 16 (f / 2) + 8 (f % 2) + g
@@ -342,9 +348,7 @@ struct Walk {
         }
       }
     }
-    // lanes of one t hold the tokens once; lanes of one g a feature's tokens
-#pragma unroll
-    for (int d = 4; d <= 16; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    // lanes of one g hold a feature's tokens
 #pragma unroll
     for (int e = 0; e < 16; e++) {
       o[e] += __shfl_xor_sync(0xffffffffu, o[e], 1);
@@ -361,12 +365,13 @@ struct Walk {
 #pragma unroll
       for (int w = 0; w < kT8Walkers; w++) all = fmaxf(all, sm.top[w]);
 #pragma unroll
-      for (int w = 0; w < kT8Walkers; w++) {
-        const float f = sm.top[w] == all ? 1.0f : fast_exp2(sm.top[w] - all);
-        sum = fmaf(sm.sum[w], f, sum);
-        if (sm.top[w] > -INFINITY || sm.sum[w] != 0.0f) y = fmaf(sm.o[w][threadIdx.x], f, y);
-      }
-      reinterpret_cast<uint16_t*>(out)[threadIdx.x] = float_elem<ELEM>(in_range<ELEM>(__fdiv_rn(y, sum)));
+      for (int w = 0; w < kT8Walkers; w++) sum = fmaf(sm.sum[w], sm.top[w] == all ? 1.0f : fast_exp2(sm.top[w] - all), sum);
+#pragma unroll
+      for (int w = 0; w < kT8Walkers; w++)
+        if (sm.top[w] > -INFINITY || sm.sum[w] != 0.0f)
+          y = fmaf(sm.o[w][threadIdx.x], __fdiv_rn(sm.sum[w] * (sm.top[w] == all ? 1.0f : fast_exp2(sm.top[w] - all)), sum), y);
+      if (sum == 0.0f) y = __uint_as_float(0x7fffffffu);         // no logit above -Inf
+      reinterpret_cast<uint16_t*>(out)[threadIdx.x] = float_elem<ELEM>(in_range<ELEM>(y));
     }
   }
 };

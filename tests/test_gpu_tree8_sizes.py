@@ -195,3 +195,91 @@ def test_the_smallest_values_stay(up, n):
                 g = slice(3 * h, 3 * h + 3)
                 ok, worst = close(out[m, g], qn[m, g], kk, vv, np.abs(vv).max(axis=1), BF16)
                 assert ok, (window, h, m, worst)
+
+
+# ------------------------------------------------------------------ rows that are computed again
+
+def check_again(c, out, lens, parents, q, k, v, feature, window=0, sinks=0, nodes=None):
+    """All rows see an infinite V at one feature: infinite there, within the bound of
+    cache8_ref.tolerance everywhere else."""
+    torch.cuda.synchronize()
+    assert c.c.status_words.tolist() == [0, 0]
+    M, rest = len(parents[0]), np.arange(128) != feature
+    got, qn, kn, vn = (x.double().cpu().numpy() for x in (out, q, k, v))
+    assert np.isinf(got[..., feature]).all()
+    for i, n in enumerate(lens):
+        for h in range(c.hkv):
+            ks, vs = c.ref.values(i, n, h) if n else (np.zeros((0, 128)),) * 2
+            g = slice(h * c.G, (h + 1) * c.G)
+            for m in range(M) if nodes is None else nodes:
+                st, dr = tref.seen(parents[i], m, n, window, sinks)
+                rows = [i * M + x for x in dr]
+                kk, vv = np.concatenate([ks[st], kn[rows, h]]), np.concatenate([vs[st], vn[rows, h]])[:, rest]
+                s = qn[i * M + m, g] @ kk.T / np.sqrt(128)
+                p = np.exp(s - s.max(axis=1, keepdims=True))
+                p /= p.sum(axis=1, keepdims=True)
+                want, qk = p @ vv, float((np.abs(qn[i * M + m, g]) @ np.abs(kk).T).max() / np.sqrt(128))
+                tol = ref.tolerance(want, p @ np.abs(vv), qk, float(np.abs(vv).max()), len(kk), c.elem, 2.0 ** -11)
+                err = np.abs(got[i * M + m, g][:, rest] - want)
+                assert (err <= tol).all(), (i, h, m, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("elem,code", [(F16, E4M3), (F16, INT8), (BF16, E4M3), (BF16, INT8)])
+@pytest.mark.parametrize("T,window,sinks", [(16, 0, 0), (128, 0, 0), (32, 300, 5), (64, 4200, 20), (128, 70, 0)])
+def test_rows_computed_again(elem, code, T, window, sinks):
+    """From one token to more than 4096 (a second round of lookups), random logits, trees below
+    one root with an infinite feature."""
+    rng = np.random.default_rng(51)
+    lens, M = [4399, 150, 1, 0], 18
+    c = make(2, 3, T, len(lens), 4399 // T + 1, elem, code, M, seed=17, fill=NAN)
+    fill(c, rng, lens)
+    parents = [[-1] + [max(0, x) for x in tref.random_tree(rng, M)[1:]] for _ in lens]
+    q, k, v = drafts(c, rng, len(lens), M)
+    v[::M, :, 9] = float("inf")
+    out = run_tree(c, lens, parents, q, k, v, window=window, sinks=sinks)
+    check_again(c, out, lens, parents, q, k, v, 9, window, sinks, nodes=(0, 1, 5, M - 2, M - 1))
+
+
+@pytest.mark.parametrize("up", [-116, 116])
+def test_huge_and_tiny_logits_computed_again(up):
+    """bf16 keys of 2^116 (2^-116) and queries that bring them back, in rows that see the
+    infinite value."""
+    rng = np.random.default_rng(52)
+    n, M = 150, 6
+    c = make(1, 4, 32, 1, 8, BF16, E4M3, M, seed=11)
+    k, v = c.vec(rng, n, 1), c.vec(rng, n, 1)
+    if up > 0:
+        k *= 2.0 ** up
+    c.append([0], [0], [n], k, v)
+    q, dk, dv = drafts(c, rng, 1, M)
+    if up > 0:
+        q *= 2.0 ** -up
+        dk *= 2.0 ** up
+    else:
+        q[1] *= 2.0 ** up
+        dk[3] *= 2.0 ** up
+    parents = [[-1, 0, 0, 1, 1, 2]]
+    dv[0, :, 9] = float("inf")
+    check_again(c, run_tree(c, [n], parents, q, dk, dv), [n], parents, q, dk, dv, 9)
+
+
+@pytest.mark.parametrize("elem", [F16, BF16])
+@pytest.mark.parametrize("sign", ["plus", "both"])
+@pytest.mark.parametrize("n", [0, 90, 2000])
+def test_largest_values_computed_again(elem, sign, n):
+    """V of the type's largest size: means of finite values are finite in rows that are
+    computed again, too."""
+    rng = np.random.default_rng(53)
+    big, M = torch.finfo(elem).max, 7
+    c = make(1, 2, 32, 1, 2000 // 32 + 1, elem, INT8, M, seed=18)
+    signs = lambda m: torch.from_numpy(rng.choice([-1.0, 1.0], (m, 1, 128)) if sign == "both" else np.ones((m, 1, 128))).to(elem).cuda()
+    if n:
+        c.append([0], [0], [n], c.vec(rng, n, 1) * 0.05, big * signs(n))
+    q, k, v = drafts(c, rng, 1, M)
+    k *= 0.05
+    v = big * signs(M)
+    v[0, :, 9] = float("inf")
+    parents = [[-1, 0, 0, 1, 2, 2, 5]]
+    out = run_tree(c, [n], parents, q, k, v)
+    check_again(c, out, [n], parents, q, k, v, 9)
+    assert torch.isfinite(out[..., 10:].float()).all()
