@@ -135,14 +135,16 @@ __device__ __forceinline__ bool valid(const Cache8View& c, const Append8Args& a,
   return true;
 }
 
-// Slots given twice or outside the cache (one block, beside the others).
-__device__ void check_slots(const Cache8View& c, const Append8Args& a, int n_req, uint32_t* bits) {
-  if (!a.slots) return;
+// Slots given twice or outside the cache (one block, beside the others), but for
+// requests that are padding.
+template <typename Padding>
+__device__ void check_slots(const Cache8View& c, const int* slots, int n_req, uint32_t* bits, Padding padding) {
+  if (!slots) return;
   for (int x = threadIdx.x; x < (c.n_slots + 31) / 32; x += blockDim.x) bits[x] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < n_req; i += blockDim.x) {
-    const int s = a.slots[i];
-    if (a.before[i] < 0) continue;
+    const int s = slots[i];
+    if (padding(i)) continue;
     if ((unsigned)s >= (unsigned)c.n_slots) {
       c.latch(DKV_ERR_ARG, i);
       continue;
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(kStepThreads) k_append8_step(Cache8View c, App
   pdl_wait();
   const int i = blockIdx.x / c.hkv, h = blockIdx.x % c.hkv;
   if (i == n_req) {
-    if (!c.stopped()) check_slots(c, a, n_req, reinterpret_cast<uint32_t*>(sm));
+    if (!c.stopped()) check_slots(c, a.slots, n_req, reinterpret_cast<uint32_t*>(sm), [&](int x) { return a.before[x] < 0; });
     return;
   }
   const int r = threadIdx.x >> 4, j = threadIdx.x & 15;
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(512, 2)
   pdl_wait();
   if (c.stopped()) return;
   if ((int)blockIdx.x == call.blk0[n_req] * c.hkv) {
-    check_slots(c, a, n_req, reinterpret_cast<uint32_t*>(sm));
+    check_slots(c, a.slots, n_req, reinterpret_cast<uint32_t*>(sm), [&](int x) { return a.before[x] < 0; });
     return;
   }
   const int job = blockIdx.x / c.hkv, h = blockIdx.x % c.hkv;
@@ -451,14 +453,12 @@ __global__ void __launch_bounds__(kAcceptThreads) k_accept8(Cache8View c, Accept
   pdl_wait();
   if (c.stopped()) return;
   const int h = blockIdx.x % c.hkv, job = blockIdx.x / c.hkv, i = job / jobs, jb = job - i * jobs;
-  Append8Args slots_of;
-  slots_of.slots = a.slots;
-  slots_of.before = a.before;
+  auto tokens = [&](int x) { return a.n_path ? a.n_path[x] : a.width; };
   if (i == n_req) {
-    check_slots(c, slots_of, n_req, reinterpret_cast<uint32_t*>(sm));
+    check_slots(c, a.slots, n_req, reinterpret_cast<uint32_t*>(sm), [&](int x) { return a.before[x] < 0 || tokens(x) <= 0; });
     return;
   }
-  int n = a.n_path ? a.n_path[i] : a.width;
+  const int n = tokens(i);
   const int before = a.before[i], slot = a.slots ? a.slots[i] : i;
   if (before < 0 || n <= 0) return;
   int err = 0;

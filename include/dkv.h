@@ -637,8 +637,9 @@ int dkv_cache8_tree_workspace(const dkv_cache8* cache, int32_t max_nodes, int64_
 
 /* Append accepted drafts: request i's tokens path[i][0 .. n_path[i]) (node numbers
  * below max_nodes, device int32 [n_req][path_width], path_width <= 128; n_path device
- * int32 [n_req], NULL: path_width each, 0: none) lie in rows i * max_nodes + node of k
- * and v, the keys turned already, and follow the before[i] tokens stored so far.
+ * int32 [n_req], NULL: path_width each; 0 or less: none, its slot may be any number)
+ * lie in rows i * max_nodes + node of k and v, the keys turned already, and follow the
+ * before[i] tokens stored so far.
  * They leave the same state as an append of those rows to a cache without rotation.
  * Counts and paths are read on the device, so a captured step replays. Other
  * conditions as for dkv_cache8_append. Errors that only the device sees: also

@@ -842,3 +842,31 @@ def test_nothing_but_padding_then_something():
     check_tree(c, out, [70, 0, 16], parents, q, k, v, [0, 1, 0])
     # a node alone sees itself: its value
     assert torch.equal(out[M].view(2, 4, 128), v[M][:, None].expand(2, 4, 128))
+
+
+def test_requests_that_accept_nothing_need_no_slot():
+    """n_path of 0 or less: the slot may be any number, one of another request among them, as
+    a request without drafts may have in tree attention."""
+    rng = np.random.default_rng(22)
+    c = make(2, 2, 16, 3, 4, F16, E4M3, 4, seed=16, fill=NAN)
+    fill(c, rng, [20, 15, 9])
+    n, M = 6, 4
+    k, v = c.vec(rng, n * M, 2), c.vec(rng, n * M, 2)
+    before, slots, n_path = [20, 7, 15, 20, 3, 9], [0, -1, 1, 0, 1 << 30, 2], [2, 0, 3, 0, -4, 1]
+    path = [[1, 3, 0], [99, 0, 0], [0, 1, 2], [0, 0, 0], [0, 0, 0], [3, 0, 0]]
+    _dkv().dkv_cache8_accept(c.c, i32(before), k, v, i32(path), n_path=i32(n_path), slots=i32(slots))
+    kn, vn = ref.elem_np(k), ref.elem_np(v)
+    for i in range(n):
+        if n_path[i] > 0:
+            rows = [i * M + x for x in path[i][:n_path[i]]]
+            c.ref.append(slots[i], before[i], kn[rows], vn[rows])
+    c.check()
+    # a whole round with such requests, then one where two that accept share a slot
+    q, kd, vd = drafts(c, rng, n, M, [4, 0, 4, 0, 0, 4])
+    out = run_tree(c, before, None, q, kd, vd, [4, 0, 4, 0, -1, 4], slots)
+    torch.cuda.synchronize()
+    assert c.c.status_words.tolist() == [0, 0] and torch.isnan(out[M:2 * M].float()).all()
+    _dkv().dkv_cache8_accept(c.c, i32(before), k, v, i32(path), n_path=i32([2, 0, 1, 1, 0, 1]), slots=i32(slots))
+    torch.cuda.synchronize()
+    assert c.c.status_words[0] == -1
+    c.c.tensors[4].zero_()
