@@ -532,8 +532,9 @@ def dkv_cache8_tree(cache: dkv_cache8, seq_lens, parents, q, k, v, out, n_nodes=
                     slots=None, stream=None, check: bool = True) -> int:
     """Attention for trees of drafted tokens over a uniform 8-bit cache made with
     max_nodes: seq_lens (device int32 [n_req]) tokens are stored, q, k, v and out hold
-    max_nodes rows a request, of which n_nodes (device; None: all) are drafts; parents
-    (device int32 [n_req][max_nodes], -1: the last stored token; None: chains)."""
+    the same number of rows for each request (max_nodes at most), of which n_nodes (device;
+    None: all) are drafts; parents (device int32, one a row, -1: the last stored token;
+    None: chains)."""
     import torch
     _window8(window, sinks)
     i32, n_req = torch.int32, seq_lens.numel()
@@ -546,7 +547,10 @@ def dkv_cache8_tree(cache: dkv_cache8, seq_lens, parents, q, k, v, out, n_nodes=
                                 nodes, _on(cache, n_nodes, i32, "n_nodes", n_req), _on(cache, parents, i32, "parents", rows),
                                 qp, qs, kp, ks, vp, vs, _on(cache, out, cache.elem_dtype, "out", rows * cache.q_heads * 128),
                                 window, sinks, cache.tree_workspace, cache.tree_bytes, _stream8(cache, stream))
-    return _check(rc, "dkv_cache8_tree") if check else rc
+    if not check:
+        return rc
+    short = rc == DKV_ERR_SCRATCH or rc != DKV_OK and cache.tree_workspace is None
+    return _check(rc, f"dkv_cache8_tree: needs a cache made with max_nodes={nodes} or more" if short else "dkv_cache8_tree")
 
 
 def dkv_cache8_accept(cache: dkv_cache8, before, k, v, path, n_path=None, slots=None, stream=None, check: bool = True) -> int:

@@ -870,3 +870,13 @@ def test_requests_that_accept_nothing_need_no_slot():
     torch.cuda.synchronize()
     assert c.c.status_words[0] == -1
     c.c.tensors[4].zero_()
+
+
+def test_a_workspace_for_fewer_drafts_says_what_it_needs():
+    rng = np.random.default_rng(23)
+    c = make(2, 4, 16, 2, 4, F16, E4M3, 8, seed=17)
+    q, k, v = drafts(c, rng, 2, 20)
+    with pytest.raises(_dkv().DkvError, match="max_nodes=20") as e:
+        run_tree(c, [0, 0], None, q, k, v)
+    assert e.value.code == _dkv().DKV_ERR_SCRATCH
+    run_tree(c, [0, 0], None, q[:16], k[:16], v[:16])

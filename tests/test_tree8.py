@@ -138,3 +138,20 @@ def test_pair_axes_are_numbers_one_by_one():
             dkv.dkv._axes8(cache, pos, bad, 5)
     with pytest.raises(ValueError):
         dkv.dkv._axes8(cache, pos, want, 6)
+
+
+def test_a_cache_without_room_for_drafts_says_what_it_needs():
+    import torch
+    from types import SimpleNamespace
+    dkv.build.build()
+    c = cache(group_size=2)
+    c.dev, c.elem_dtype, c.heads, c.q_heads, c.pairs = -1, torch.float16, 2, 4, 0
+    c.address, c.tree_workspace, c.tree_bytes = C.addressof(c), None, 0
+    c.elem_type = dkv.dkv.DKV_F16
+    vec = lambda h: torch.zeros((6, h, 128), dtype=torch.float16)
+    lens, q, k = torch.zeros(2, dtype=torch.int32), vec(4), vec(2)
+    stream = SimpleNamespace(cuda_stream=0)
+    with pytest.raises(dkv.DkvError, match="max_nodes=3") as e:
+        dkv.dkv_cache8_tree(c, lens, None, q, k, vec(2), vec(4), stream=stream)
+    assert e.value.code == dkv.DKV_ERR_ARG
+    assert dkv.dkv_cache8_tree(c, lens, None, q, k, vec(2), vec(4), stream=stream, check=False) == dkv.DKV_ERR_ARG
