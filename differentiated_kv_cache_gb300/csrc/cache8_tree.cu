@@ -642,8 +642,8 @@ __device__ __forceinline__ uint32_t top_pair(uint32_t m, uint32_t w) {
   return max_s16x2(m, (w & 0x7fff7fffu) + kT8Bias<ELEM> * 0x10001u);
 }
 __device__ __forceinline__ uint32_t swap_halves(uint32_t x) { return prmt(x, x, 0x1032u); }
-// The exponent for one of the two. Not below -112: results come back by that and kT8Up, which has
-// to stay a normal number; the smallest V then comes to 2^-14, where fp16 keeps what bf16 holds.
+// The exponent for one of the two. Not below -112: results come back by that and kT8Up; the smallest
+// normal V then comes to 2^-14, where fp16 keeps what bf16 holds.
 template <int ELEM>
 __device__ __forceinline__ int exp_of(uint32_t top) {
   const uint32_t x = __float_as_uint(elem_float<ELEM>((uint16_t)((top & 0xffffu) - kT8Bias<ELEM>)));
@@ -1241,9 +1241,11 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         named_sync(pair_bar, 64);
         const float lsum = l + sm.pair[told][part ^ 1][r].x;
         told ^= 1;
-        // a sum that left fp32's range: NaN, which the second kernel looks into
-        float f = lsum == 0.0f ? 0.0f : lsum < INFINITY ? __fdiv_rn(1.0f, lsum) : __uint_as_float(0x7fffffffu);
-        const float fv = f == 0.0f ? 0.0f : fast_exp2(mx - kT8Up - u);       // (one after the other: the smallest values stay normal till the end)
+        // a sum that left fp32's range, or a factor that is not a normal number (only values below
+        // 2^-100 need one; two factors one after the other for every value: the chains 94 us, 90 so):
+        // NaN, which the second kernel looks into
+        float f = lsum == 0.0f ? 0.0f : __fdiv_rn(fast_exp2(mx - kT8Up - u), lsum);
+        if (lsum != 0.0f && !(f >= 1.17549435e-38f)) f = __uint_as_float(0x7fffffffu);
         if (__builtin_expect(*(volatile int*)&sm.any_taken, 0)) {
           // tiles of 16 bits are a unit's last ones, in five steps at most
 #pragma unroll 1
@@ -1267,7 +1269,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 16; e++) {
             asm volatile("" : "+f"(o[e]));
-            o[e] = o[e] * f * fv;
+            o[e] *= f;
           }
         };
         if (whole) {
