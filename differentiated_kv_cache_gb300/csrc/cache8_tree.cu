@@ -1243,9 +1243,10 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         told ^= 1;
         // a sum that left fp32's range, or a factor that is not a normal number (only values below
         // 2^-100 need one; two factors one after the other for every value: the chains 94 us, 90 so):
-        // NaN, which the second kernel looks into
+        // NaN, which the second kernel looks into; as is a row without a logit above -Inf
+        const bool whole = it.n == it.per;
         float f = lsum == 0.0f ? 0.0f : __fdiv_rn(fast_exp2(mx - kT8Up - u), lsum);
-        if (lsum != 0.0f && !(f >= 1.17549435e-38f)) f = __uint_as_float(0x7fffffffu);
+        if ((lsum != 0.0f || whole) && !(f >= 1.17549435e-38f)) f = __uint_as_float(0x7fffffffu);
         if (__builtin_expect(*(volatile int*)&sm.any_taken, 0)) {
           // tiles of 16 bits are a unit's last ones, in five steps at most
 #pragma unroll 1
@@ -1258,7 +1259,6 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
             if (see & d.y & 0xffffu) f = __uint_as_float(0x7fffffffu);
           }
         }
-        const bool whole = it.n == it.per;
         uint8_t* out = a.out + (((long long)it.i * a.max_nodes + m) * c.hkv * G + (size_t)it.h * G + (row - m * G)) * (2 * kD) + 128 * part;
         // a part: [feature / 4][row][4], whose lanes' stores are neighbours, then (u, l) of the rows
         float4* dst = reinterpret_cast<float4*>(a.part + (size_t)(2 * blockIdx.x + (it.s0 > 0 ? 0 : 1)) * part_rows * (kD + 2));
@@ -1646,7 +1646,9 @@ __global__ void __launch_bounds__(32 * kT8Walkers, 4) k_tree8_join(const __grid_
         more(make_float2(ot, os));
       }
     }
+    // (no logit above -Inf: no softmax)
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (sum == 0.0f) o.x = __uint_as_float(0x7fffffffu);
     auto add = [&](const float4& y, const float2& z) {
       const float f = z.y == 0.0f ? 0.0f : __fdiv_rn(z.y * (z.x == top ? 1.0f : fast_exp2(z.x - top)), sum);
       o.x = fmaf(y.x, f, o.x);

@@ -283,3 +283,26 @@ def test_largest_values_computed_again(elem, sign, n):
     out = run_tree(c, [n], parents, q, k, v)
     check_again(c, out, [n], parents, q, k, v, 9)
     assert torch.isfinite(out[..., 10:].float()).all()
+
+
+@pytest.mark.parametrize("elem", [F16, BF16])
+@pytest.mark.parametrize("n,M", [(0, 3), (20, 5), (120, 100)])
+def test_rows_of_nothing_but_minus_infinity(elem, n, M):
+    """Logits that are all -Inf have no softmax: NaN, in a unit of one block and in one that
+    several hold parts of; one finite logit beside them makes that token's value."""
+    rng = np.random.default_rng(54)
+    c = make(1, 2, 128, 1, 2, elem, E4M3, M, seed=19)
+    k, v = c.vec(rng, max(n, 1), 1), c.vec(rng, max(n, 1), 1)
+    k[..., 5] = float("-inf")
+    if n:
+        c.append([0], [0], [n], k, v)
+    q, dk, dv = drafts(c, rng, 1, M)
+    q[..., 5] = 1.0
+    dk[..., 5] = float("-inf")
+    dk[M - 1, :, 5] = 1.0
+    parents = [list(range(-1, M - 1))]
+    out = run_tree(c, [n], parents, q, dk, dv)
+    torch.cuda.synchronize()
+    assert c.c.status_words.tolist() == [0, 0]
+    assert torch.isnan(out[:M - 1].float()).all()
+    assert torch.equal(out[M - 1].float(), dv[M - 1].float().expand(2, 128))
