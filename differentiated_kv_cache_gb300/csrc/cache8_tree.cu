@@ -5,12 +5,12 @@
 // node's window and the drafts on its way to the root. All nodes of a request and all heads
 // of a group (M G query rows) read the same K and V, so the cache is read once for 128
 // rows; the products, 4 * 128 operations a row and token, go to tcgen05. Both take fp16
-// operands and sum in fp32: codes are exact in fp16; tails, drafts and queries in bf16 come
-// into its range by a power of two: one for a query's row, whose 8 bits stay down to 2^-17 of the
-// largest (what lies under 2^-25 of it is lost), one for each token's K and V, whose bits stay
-// down to 2^-24 (lost under 2^-32). K's scale joins the logits, V's joins the weights as an addend
-// of their exponent. Weights are rounded to
-// fp16 (2^-11), as probabilities are in the attention of single tokens.
+// operands and sum in fp32: codes are exact in fp16; queries in bf16 come into its range by a
+// power of two of their row, whose 8 bits stay down to 2^-17 of the largest (what lies under 2^-25
+// of it is lost), bf16 K and all V of tails and drafts by one of each token, whose bits stay down
+// to 2^-24 (lost under 2^-32). K's scale joins the logits, V's joins the weights as an addend of
+// their exponent. Weights are rounded to fp16 (2^-11), as probabilities are in the attention of
+// single tokens.
 //
 // Units (request, KV head, 128 rows) of steps (128 tokens) follow one another; the sequence
 // of all is cut into ranges of equal time, one for each SM, so ragged batches and one long
@@ -18,22 +18,26 @@
 // which the second kernel joins. The way of a step, of which several are in flight:
 //   lookups -> bulk copies of codes -> conversion to swizzled fp16 operands -> S = Q K^T
 //   -> weights -> O += P V, with Q, S, P and O in tensor memory.
-// What bounds a step of 128 rows (2400 cycles): its 16384 exponentials (4 cycles for a
-// warp's 32, a quarter of them for each quarter of an SM: 512 cycles; with sums, roundings and
-// masks 1300), and the wait from the weights through the products to the next S. Between two
-// units of a CTA lie 10000 cycles, ahead of the first step 20000: the launch, the plan, a
-// chain of four loads, and code that all SMs fetch at once. Measured:
-//   8 heads, G = 4, fp16, e4m3, 16 requests of 4096 tokens, 26 drafts    58 us (by bytes 21)
-//   8 heads, G = 8, bf16, int8, 8 of 32768, 64 drafts                   542 us, 1020 TFLOP/s
-//     (53 % of a plain matrix product's rate)
-//   4 heads, G = 7, bf16, e4m3, 32 of 1024 to 16384, window 4096         53 us
-//   8 heads, G = 5, fp16, int8, 64 of 1 to 3000, chains of 5             84 us
-//   8 heads, G = 4, fp16, e4m3, one of 300 tokens, 8 drafts              11.5 us
+// What bounds a step of 128 rows (2500 to 2600 cycles) are the softmax warps, busy for nine
+// tenths of it: logits out of tensor memory 400 cycles, weights 1300 (16384 exponentials, 4 cycles
+// for a warp's 32, a quarter of them for each quarter of an SM: 512; sums, roundings and masks),
+// weights into tensor memory 350, and 280 until the next S. All eight share a step, so none of
+// these hides another's; the products are done ahead of them. A step with tiles of 16 bits takes
+// 2000 to 5900: exponents of each token, a second exponential, V's conversion beside it. Between two
+// units of a CTA lie 5000 to 11000 cycles, ahead of the first weights 24000 to 35000: the launch,
+// the plan, a chain of four loads, queries, and code that all SMs fetch at once. Measured:
+//   8 heads, G = 4, fp16, e4m3, 16 requests of 4096 tokens, 26 drafts    59 us (by bytes 21)
+//   8 heads, G = 8, bf16, int8, 8 of 32768, 64 drafts                   551 us, 1000 TFLOP/s
+//     (52 % of a plain matrix product's rate)
+//   4 heads, G = 7, bf16, e4m3, 32 of 1024 to 16384, window 4096         55 us
+//   8 heads, G = 5, fp16, int8, 64 of 1 to 3000, chains of 5             90 us
+//   8 heads, G = 4, fp16, e4m3, one of 300 tokens, 8 drafts              11.4 us
 // Tried and slower: 64 tokens a step (the second: 0.92 ms); conversion by the softmax warps
 // (the chains: 196 us); maxima of each step ahead of its weights (the second: 0.66 ms; now
 // they are taken when a weight could leave fp16's range); conversion unrolled over its tiles
 // (0.62 ms: it leaves the instruction caches); ranges of equal steps (the chains: 126 us); the
-// tails' and drafts' largest values looked for ahead of all copies (the third: 68 us).
+// tails' and drafts' largest values looked for ahead of all copies (the third: 68 us); tiles of 16
+// bits through the body of the other steps, with exponents of tokens (the third: 70 us).
 #include <algorithm>
 
 #include "cache8.cuh"
@@ -59,7 +63,7 @@ constexpr int kT8Batch = 4;         // steps that are looked up at once
 constexpr int kT8Descs = 4 * kT8Batch;      // steps whose descriptors are kept, a ring
 constexpr int kT8Metas = 8;         // steps whose scales are kept for the softmax, a ring
 // steps in whose time a CTA goes from one unit to the next (2: 64 chains of 1 to 3000 tokens take
-// 90 us, 32 windows 56; 3: 85 and 54; 4: 84 and 53; 6: 85 and 53)
+// 96 us, 32 windows 57; 3: 91 and 54; 4: 91 and 55; 6: 92 and 55)
 constexpr int kT8Turn = 4;
 constexpr float kT8Up = 7.0f;       // log2 of a weight at its row's maximum
 constexpr float kT8Most = 32768.0f; // largest sum of a row's weights of one tile (fp16 holds 65504)
