@@ -8,7 +8,7 @@
 // operands and sum in fp32: codes are exact in fp16; queries in bf16 come into its range by a
 // power of two of their row, whose 8 bits stay down to 2^-17 of the largest (what lies under 2^-25
 // of it is lost), bf16 K and all V of tails and drafts by one of each token, whose bits stay down
-// to 2^-24 (lost under 2^-32). K's scale joins the logits, V's joins the weights as an addend of
+// to 2^-24 (lost under 2^-32), and so V of codes whose block some node sees a part of. K's scale joins the logits, V's joins the weights as an addend of
 // their exponent. Weights are rounded to fp16 (2^-11), as probabilities are in the attention of
 // single tokens.
 //
@@ -90,31 +90,47 @@ __device__ __forceinline__ TreeReq tree_req(const Cache8View& c, const Tree8Args
   return r;
 }
 
-// The 16-token tiles of a request in order: stored ones [0, head) and [win, end) of
-// which those from `full` on lie in the tail, then the drafts; `count` in all. A stored tile
-// is left out if no node of any depth sees a token of it. In the steps of the kernel below a
-// tile of 16-bit values takes two places (its copies need twice the room): places [0, codes)
-// hold the tiles of codes, which come first, those from `elems` on the others, every second one, so that the four
-// places of a softmax warp are of one kind.
+// The 16-token tiles of a request: stored ones [0, head) and [win, end), of which those from `full`
+// on lie in the tail, then the drafts; `count` in all. A stored tile is left out if no node of any
+// depth sees a token of it. Their order: `codes` tiles of blocks that every node sees all of, [0,
+// firsts) and [whole, full); other codes up to `tails`, whose block's scale may be set by what a node
+// does not see; the tail's; the drafts. In the steps of the kernel below places [0, codes) hold the
+// first kind; all others, whose tokens have exponents of their own (and, in 16 bits, whose copies
+// need twice the room), lie from `elems` on at every second place, so that the four places of a softmax
+// warp are of one sort.
 struct TreeTiles {
-  int head, win, end, full, stored, count;
-  int codes, elems, places;
-  __device__ __forceinline__ int tile(int x) const { return x < head ? x : x - head + win; }
+  int head, win, end, full, firsts, whole, stored, count;
+  int codes, tails, elems, places;
+  __device__ __forceinline__ int tile(int x) const {
+    if (x < codes) return x < firsts ? x : x - firsts + whole;
+    const int mid = min(head, full);
+    x -= codes;
+    if (x < mid - firsts) return x + firsts;
+    x -= mid - firsts;
+    if (x < whole - win) return x + win;
+    x -= whole - win;
+    return x < head - mid ? x + mid : x - (head - mid) + max(win, full);
+  }
 };
 __device__ __forceinline__ TreeTiles tree_tiles(int N, int M, int T, int window, int sinks) {
   TreeTiles t;
   t.end = (N + kSub - 1) / kSub;
   const int lt = __ffs(T) - 1;      // T is a power of two, at least 16
   t.full = N >> lt << (lt - 4);
-  t.head = t.win = 0;
+  t.head = t.win = t.firsts = t.whole = 0;
   if (window > 0 && window <= N) {          // a root (position N) sees those above N - window
     const int from = N - window + 1;
     t.win = from >= N ? t.end : from / kSub;
     t.head = min((min(sinks, N) + kSub - 1) / kSub, t.win);
+    t.firsts = min(sinks >> lt << (lt - 4), min(t.head, t.full));
   }
+  if (window > 0 && N + M > window)         // the deepest node may see those from N + M - window on
+    t.whole = (N + M - window + T - 1) >> lt << (lt - 4);
+  t.whole = min(max(t.whole, t.win), max(t.win, t.full));
   t.stored = t.head + t.end - t.win;
   t.count = t.stored + (M + kSub - 1) / kSub;
-  t.codes = t.full > t.win ? t.head + t.full - t.win : min(t.head, t.full);
+  t.codes = t.firsts + max(t.win, t.full) - t.whole;
+  t.tails = t.codes + min(t.head, t.full) - t.firsts + t.whole - t.win;
   t.elems = (t.codes + 3) & ~3;
   t.places = t.elems + 2 * (t.count - t.codes);
   return t;
@@ -499,8 +515,8 @@ struct __align__(16) TreeRecord {
   int flags, i, h, t, M, last, lo, hi;
 };
 
-// What is known of a tile. kind: of codes, of which every node sees every token (0) or not
-// (1), of the tail (2), drafts (3), none (4).
+// What is known of a tile. kind: codes of a block that every node sees all of (0), other codes (1),
+// the tail's (2), drafts (3), none (4).
 struct TileDesc {
   const uint8_t* src;       // (drafts: K)
   float ks;
@@ -522,7 +538,7 @@ struct TreeSmem {
   TileDesc desc[kT8Descs][kT8Step];
   unsigned there[2 * kT8Descs];        // places of a step that hold a tile (the products are behind the conversion)
   TileMeta meta[kT8Metas][kT8Step];    // (K of step j comes when the softmax has read that of step j - 5)
-  // of a step's tiles of 16 bits: K's powers of two, V's exponents (there with V, not with S)
+  // of a step's tiles from `elems` on: K's powers of two, V's exponents (there with V, not with S)
   alignas(16) uint16_t kexp[kT8Metas][kT8Step / 2][kSub];
   alignas(16) float vexp[kT8Slots][kT8Step / 2][kSub];
   TreePlan plan;
@@ -597,7 +613,10 @@ __device__ __forceinline__ TileDesc describe_tile(const Cache8View& c, const Tre
   const TreeItem it = tree_item(c, a, plan, pos, pos + 1);
   x = kT8Step * it.s0 + x % kT8Step;
   TileDesc d{nullptr, kLogitScale, {0.0f}, 0, 4, 0, nullptr};
-  if (x < it.tiles.codes) {
+  const bool own = x >= it.tiles.elems;
+  if (own ? x & 1 : x >= it.tiles.codes) return d;
+  if (own) x = it.tiles.codes + ((x - it.tiles.elems) >> 1);
+  if (x < it.tiles.tails) {
     const int tile = it.tiles.tile(x), per = __ffs(c.T) - 5;      // log2 of a block's tiles
     d.pos0 = tile * kSub;
     int page = c.table[(size_t)it.slot * c.width + (tile >> per)];
@@ -607,28 +626,26 @@ __device__ __forceinline__ TileDesc describe_tile(const Cache8View& c, const Tre
     }
     scales = reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * c.hkv + it.h));
     d.src = c.pages + c.page_head(page, it.h) + (size_t)(tile & ((1 << per) - 1)) * (2 * kTile);
-    // every depth sees all of it
-    d.kind = a.window <= 0 || d.pos0 >= it.N + it.M - a.window || d.pos0 + kSub <= a.sinks ? 0 : 1;
-  } else if (x >= it.tiles.elems && (x & 1) == 0) {
-    x = it.tiles.codes + ((x - it.tiles.elems) >> 1);
+    d.kind = own ? 1 : 0;
+  } else if (x < it.tiles.stored) {
+    const int tile = it.tiles.tile(x);
     d.req_head = it.i << 12 | it.h;
-    if (x < it.tiles.stored) {
-      const int tile = it.tiles.tile(x);
-      d.pos0 = tile * kSub;
-      d.src = c.tail + c.tail_head(it.slot, it.h) + (size_t)(tile - it.tiles.full) * (4 * kTile);
-      d.kind = 2;
-    } else if (x < it.tiles.count) {
-      d.pos0 = (x - it.tiles.stored) * kSub;
-      d.src = a.k + ((long long)it.i * a.max_nodes + d.pos0) * a.ks + it.h * (2 * kD);
-      d.kind = 3;
-    }
+    d.pos0 = tile * kSub;
+    d.src = c.tail + c.tail_head(it.slot, it.h) + (size_t)(tile - it.tiles.full) * (4 * kTile);
+    d.kind = 2;
+  } else if (x < it.tiles.count) {
+    d.req_head = it.i << 12 | it.h;
+    d.pos0 = (x - it.tiles.stored) * kSub;
+    d.src = a.k + ((long long)it.i * a.max_nodes + d.pos0) * a.ks + it.h * (2 * kD);
+    d.kind = 3;
   }
   return d;
 }
 
-// ---- powers of two: K of each bf16 token and V of each token of 16 bits are divided by one of their
-// own, which brings the token's largest value to [128, 256). (One for the tile: what a row does not
-// see would set the power for what it does. A sibling's V 2^30 above the others left rows that do
+// ---- powers of two: K of each bf16 token and V of each token of 16 bits, or of a block that some node
+// sees a part of only, are divided by one of their own, which brings the token's largest value to
+// [128, 256). (One for the tile, or the block's scale: what a row does not see would set the power for
+// what it does. A sibling's V 2^30 above the others left rows that do
 // not see it wrong by 25 %, one 2^60 above left zeros. V in fp16 as it is: the weights of codes, which
 // carry their scale, lie 2^-20 below and lose their bits beside a heavier token of small V in the same
 // step; 64 codes beside a draft with V of 1e-4 were off by 7 times the bound of rounded weights.) ----
@@ -707,40 +724,48 @@ __device__ __noinline__ uint32_t take_out(uint8_t* src, bool draft, int n) {
   __syncwarp();
   return __reduce_or_sync(0xffffffffu, bits) & below(n);
 }
-// A tile of the tail as fp16 operands, of which n tokens are valid; at: the lane's row of the first
-// four matrices. Returns the tokens whose V has values that are not finite. Two passes over the
+// A tile of the tail, or of codes (FMT: what they are read as; lv: log2 of V's scale), as fp16 operands,
+// of which n tokens are valid; at: the lane's row of the first four matrices. Returns the tokens of the
+// tail whose V has values that are not finite. Two passes over the
 // lane's 16 bytes of every m-step in short loops: this code runs once or twice a unit and comes from
 // far (unrolled, all eight m-steps at once: 59.9 us for the window, 57.3 so).
-template <int ELEM>
-__device__ __noinline__ uint32_t put_tail(uint8_t* src, bool v, int n, uint32_t at, TileExps exps) {
+template <int FMT, bool CODES, int CODE>
+__device__ __noinline__ uint32_t put_tile(uint8_t* src, bool v, int n, uint32_t at, TileExps exps, float lv) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const bool scaled = v || ELEM == DKV_BF16;         // (K in fp16 stays as it is)
+  const bool scaled = v || FMT == DKV_BF16;         // (K in fp16 stays as it is)
   // The four 8 x 8 matrices of m-step f, of K the first eight features' first: even words are of token
   // g (K) or tokens 2t and 2t + 1 (V, low and high halves), odd ones of those eight tokens on. What
   // lies behind the valid tokens becomes 0 (0 times what it may hold is not).
   const uint32_t valid_a = v ? (2 * t < n ? 0xffffu : 0u) | (2 * t + 1 < n ? 0xffff0000u : 0u) : g < n ? 0xffffffffu : 0u;
   const uint32_t valid_b = v ? (2 * t + 8 < n ? 0xffffu : 0u) | (2 * t + 9 < n ? 0xffff0000u : 0u) : g + 8 < n ? 0xffffffffu : 0u;
   auto load = [&](int f) {
-    const uint4 y = *reinterpret_cast<const uint4*>(src + 512 * f + 16 * lane);
+    uint4 y;
+    if (CODES) {
+      const uint2 w = *reinterpret_cast<const uint2*>(src + 512 * (f >> 1) + 16 * lane + 8 * (f & 1));
+      code_halves<CODE>(w.x, y.x, y.y);
+      code_halves<CODE>(w.y, y.z, y.w);
+    } else {
+      y = *reinterpret_cast<const uint4*>(src + 512 * f + 16 * lane);
+    }
     return make_uint4(y.x & valid_a, (v ? y.y : y.z) & valid_b, (v ? y.z : y.y) & valid_a, y.w & valid_b);
   };
   uint32_t a = 0, b = 0, out = 0;
 #pragma unroll 1
   while (scaled) {
     uint32_t acc = 0;
-    a = b = kT8Bias<ELEM> * 0x10001u;
+    a = b = kT8Bias<FMT> * 0x10001u;
 #pragma unroll 2
     for (int f = 0; f < 8; f++) {
       const uint4 x = load(f);
-      a = top_pair<ELEM>(top_pair<ELEM>(a, x.x), x.z);
-      b = top_pair<ELEM>(top_pair<ELEM>(b, x.y), x.w);
-      find_not_finite<ELEM>(acc, x.x);
-      find_not_finite<ELEM>(acc, x.y);
-      find_not_finite<ELEM>(acc, x.z);
-      find_not_finite<ELEM>(acc, x.w);
+      a = top_pair<FMT>(top_pair<FMT>(a, x.x), x.z);
+      b = top_pair<FMT>(top_pair<FMT>(b, x.y), x.w);
+      find_not_finite<FMT>(acc, x.x);
+      find_not_finite<FMT>(acc, x.y);
+      find_not_finite<FMT>(acc, x.z);
+      find_not_finite<FMT>(acc, x.w);
     }
-    if (!v || __builtin_expect(!__any_sync(0xffffffffu, found_not_finite(acc)), 1)) break;
-    out = take_out<ELEM>(src, false, n);
+    if (CODES || !v || __builtin_expect(!__any_sync(0xffffffffu, found_not_finite(acc)), 1)) break;
+    out = take_out<FMT>(src, false, n);
   }
   Factors fa{}, fb{};
   if (scaled) {
@@ -753,22 +778,29 @@ __device__ __noinline__ uint32_t put_tail(uint8_t* src, bool v, int n, uint32_t 
       a = max_s16x2(a, __shfl_xor_sync(0xffffffffu, a, d));
       b = max_s16x2(b, __shfl_xor_sync(0xffffffffu, b, d));
     }
-    const int a0 = exp_of<ELEM>(a), a1 = exp_of<ELEM>(a >> 16), b0 = exp_of<ELEM>(b), b1 = exp_of<ELEM>(b >> 16);
+    const int a0 = exp_of<FMT>(a), a1 = exp_of<FMT>(a >> 16), b0 = exp_of<FMT>(b), b1 = exp_of<FMT>(b >> 16);
     if (v ? g == 0 : t == 0) {
-      put_exp(exps, v, v ? 2 * t : g, a0);
-      put_exp(exps, v, v ? 2 * t + 8 : g + 8, b0);
+      // (a code is 0 or at least 2^-9; a token of zeros counts as one of the smallest scale)
+      auto put = [&](int token, int ex) {
+        if (CODES) exps.v[token] = ex < -16 ? -100.0f : (float)ex + lv;
+        else put_exp(exps, v, token, ex);
+      };
+      put(v ? 2 * t : g, a0);
+      put(v ? 2 * t + 8 : g + 8, b0);
       if (v) {
-        put_exp(exps, v, 2 * t + 1, a1);
-        put_exp(exps, v, 2 * t + 9, b1);
+        put(2 * t + 1, a1);
+        put(2 * t + 9, b1);
       }
     }
-    fa = factors<ELEM>(a0, a1);
-    fb = factors<ELEM>(b0, b1);
+    fa = factors<FMT>(a0, a1);
+    fb = factors<FMT>(b0, b1);
+  } else if (CODES && lane < kSub) {
+    put_exp(exps, false, lane, 0);
   }
 #pragma unroll 2
   for (int f = 0; f < 8; f++) {
     uint4 x = load(f);
-    if (scaled) x = make_uint4(half_of<ELEM>(x.x, fa), half_of<ELEM>(x.y, fb), half_of<ELEM>(x.z, fa), half_of<ELEM>(x.w, fb));
+    if (scaled) x = make_uint4(half_of<FMT>(x.x, fa), half_of<FMT>(x.y, fb), half_of<FMT>(x.z, fa), half_of<FMT>(x.w, fb));
     if (!v) stmatrix4((at + (f >> 2) * 16384) ^ ((f & 3) << 5), x.x, x.z, x.y, x.w);
     else stmatrix4(at + f * 2048, x.x, x.y, x.z, x.w);
   }
@@ -1062,7 +1094,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
           const TileMeta* meta = sm.meta[j & (kT8Metas - 1)] + 4 * part;
           float sum = 0.0f;
           if (kT8Step * (it.s0 + it.n - (end - j)) + 4 * part >= it.tiles.elems) {
-            // two tiles of 16 bits, whose tokens have exponents of their own
+            // two tiles whose tokens have exponents of their own
             float y[2][16];
             bool is[2];
             auto vexp = [&](int b, int e) { return *reinterpret_cast<const ulonglong2*>(&sm.vexp[j & 1][2 * part + b][4 * e]); };
@@ -1076,7 +1108,7 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
               is[b] = d.kind != 4;
               if (!is[b]) continue;
               const int w = d.pos0 >> 5;
-              const uint32_t see = !real ? 0xffffu : d.kind == 2 ? sees_stored(a, it.N, node.depth, d.pos0)
+              const uint32_t see = !real ? 0xffffu : d.kind != 3 ? sees_stored(a, it.N, node.depth, d.pos0)
                                    : (w == 0 ? node.over[0] : w == 1 ? node.over[1] : w == 2 ? node.over[2] : node.over[3]) >> (d.pos0 & 31) & 0xffffu;
               const float f = d.ks * scale;
               const uint4* kp = reinterpret_cast<const uint4*>(sm.kexp[j & (kT8Metas - 1)][2 * part + b]);      // (bf16)
@@ -1149,26 +1181,24 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
             tmem_ld32_nowait(ts, s);
             tmem_ld32_nowait(ts + 32, s + 32);
             float f[4], lv[4];
-            int kind[4], pos0[4];
+            int kind[4];
 #pragma unroll
             for (int b = 0; b < 4; b++) {
               const TileMeta d = meta[b];
               f[b] = d.ks * scale;
               lv[b] = d.lv;
               kind[b] = d.kind;
-              pos0[b] = d.pos0;
             }
             tmem_wait_ld();
             loaded32(s);
             loaded32(s + 32);
-            if (kind[0] | kind[1] | kind[2] | kind[3]) {
+            // (every node sees all of what there is)
 #pragma unroll
-              for (int b = 0; b < 4; b++) {
-                const uint32_t see = kind[b] == 0 ? 0xffffu : real && kind[b] == 1 ? sees_stored(a, it.N, node.depth, pos0[b]) : 0u;
+            for (int b = 1; b < 4; b++)
+              if (kind[b]) {
 #pragma unroll
-                for (int e = 0; e < 16; e++) s[16 * b + e] = see & (1u << e) ? s[16 * b + e] : -INFINITY;
+                for (int e = 0; e < 16; e++) s[16 * b + e] = -INFINITY;
               }
-            }
             uint32_t p[32];
 #pragma unroll 1
             for (bool again = raise;; again = true) {
@@ -1355,15 +1385,16 @@ __global__ void __launch_bounds__(kT8Threads, 1) k_tree8(const __grid_constant__
         if (!ok) break;
         const uint32_t to0 = place(first) + slot * kT8Slot, to1 = place(first + 1) + slot * kT8Slot;
         const int kind = desc->kind;
-        if (kind == 2 || kind == 3) {
+        if (kind >= 1 && kind <= 3) {
           // (the second place is none)
           const TileExps exps{sm.kexp[j & (kT8Metas - 1)][warp & 3], sm.vexp[slot][warp & 3]};
-          if (kind == 2) out = put_tail<ELEM>(ring + slot * kT8Entry, op, desc->n, to0, exps);
+          if (kind == 1) put_tile<DKV_F16, true, CODE>(ring + slot * kT8Entry, op, kSub, to0, exps, desc->lv);
+          else if (kind == 2) out = put_tile<ELEM, false, CODE>(ring + slot * kT8Entry, op, desc->n, to0, exps, 0.0f);
           else out = put_drafts<ELEM>(ring + slot * kT8Entry, op, desc->n, (op ? draft_place(first) : base + 2 * first * 1024) + slot * kT8Slot, exps);
         } else {
 #pragma unroll 1
           for (int t = 0; t < 2; t++)
-            if (desc[t].kind <= 1) {
+            if (desc[t].kind == 0) {
               const uint8_t* p = ring + slot * kT8Entry + t * kTile + 16 * lane;
               uint4 w[4];
 #pragma unroll

@@ -616,11 +616,11 @@ int dkv_cache8_rotate(const dkv_cache8* cache, int32_t n_tok, const int32_t* pos
  * Sums are in fp32. Weights enter the value product rounded to fp16 (relative 2^-11; a
  * weight whose product with its scale lies below 2^-21 of the row's largest such product
  * is off by up to 2^-32 of that), the sum of weights unrounded. A code's scale is its
- * block's. V of each tail entry and draft has a power of two of its own for a scale, and so
- * have K of each such bf16 token and each row of bf16 queries, over which they meet the
- * products as fp16 (what lies below 2^-32 of a token's largest value or 2^-25 of a query
- * row's is lost). What a row does not see never enters its result, whatever it holds (but
- * for the scale of a block that the row sees a part of): rows that come out infinite or
+ * block's where every node sees all of the block. V of each other token, tail entry and
+ * draft has a power of two of its own for a scale, and so have K of each bf16 tail entry and
+ * draft and each row of bf16 queries, over which they meet the products as fp16 (what lies
+ * below 2^-32 of a token's largest value or 2^-25 of a query row's is lost). What a row does
+ * not see never enters its result, whatever it holds: rows that come out infinite or
  * NaN, and rows that see a draft or tail entry with such a V, are computed again over what
  * they see (a row and 4096 tokens: 64 us, most rows at once; the look for such values
  * costs every call 2 to 4 %). An infinite value under a weight that rounds to 0 gives NaN. Means

@@ -306,3 +306,37 @@ def test_rows_of_nothing_but_minus_infinity(elem, n, M):
     assert c.c.status_words.tolist() == [0, 0]
     assert torch.isnan(out[:M - 1].float()).all()
     assert torch.equal(out[M - 1].float(), dv[M - 1].float().expand(2, 128))
+
+
+# ------------------------------------------------------------------ blocks that rows see a part of
+
+def hidden_sizes():
+    return [(e, c, w, x) for e in (F16, BF16) for c in (E4M3, INT8) for w, x in
+            (("k", 1e18), ("k", 3e4), ("v", 1e4), ("v", 1e9), ("v", 1e18), ("v", -3e38)) if abs(x) <= torch.finfo(e).max]
+
+
+@pytest.mark.parametrize("T,n,window,sinks", [(64, 300, 151, 0), (128, 700, 300, 20), (32, 200, 90, 40), (16, 333, 40, 3),
+                                              (128, 260, 5, 130), (64, 400, 395, 0)])
+@pytest.mark.parametrize("elem,code,what,size", hidden_sizes())
+def test_finite_codes_that_are_not_seen(elem, code, T, n, window, sinks, what, size):
+    """Stored tokens of any size that a window, or the first tokens, leave out of a block whose
+    rest rows see: they set the block's scale, with which the rest is stored, and no more. The
+    shallow nodes see some of them, which is their own affair."""
+    rng = np.random.default_rng(61)
+    M = 24
+    c = make(2, 3, T, 1, n // T + 1, elem, code, M, seed=20, fill=NAN)
+    k, v = c.vec(rng, n, 2), c.vec(rng, n, 2)
+    x = k if what == "k" else v
+    first = n - window + 1                   # a root sees those from here on
+    hidden = [j for j in (first - 1, first - 9, sinks, sinks + 5) if sinks <= j < first]
+    assert hidden
+    x[hidden] = size
+    deep = first + 3                         # seen by nodes of a depth up to 2
+    x[deep] = size
+    c.append([0], [0], [n], k, v)
+    parents = [list(range(-1, 11)) + [-1, 12, 13, 14, 2, 2, 16, 17, 18, 9, 9, 9]]
+    q, dk, dv = drafts(c, rng, 1, M)
+    out = run_tree(c, [n], parents, q, dk, dv, window=window, sinks=sinks)
+    assert c.c.status_words.tolist() == [0, 0]
+    depth = np.array(tref.depths(parents[0]))
+    check_tree(c, out, [n], parents, q, dk, dv, [M], window=window, sinks=sinks, nodes=set(np.flatnonzero(depth > 2).tolist()))
