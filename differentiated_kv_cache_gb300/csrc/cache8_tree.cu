@@ -19,19 +19,19 @@
 //   lookups -> bulk copies of codes -> conversion to swizzled fp16 operands -> S = Q K^T
 //   -> weights -> O += P V, with Q, S, P and O in tensor memory.
 // What bounds a step of 128 rows (2500 to 2600 cycles) are the softmax warps, busy for nine
-// tenths of it: logits out of tensor memory 400 cycles, weights 1300 (16384 exponentials, 4 cycles
-// for a warp's 32, a quarter of them for each quarter of an SM: 512; sums, roundings and masks),
-// weights into tensor memory 350, and 280 until the next S. All eight share a step, so none of
-// these hides another's; the products are done ahead of them. A step with tiles of 16 bits takes
-// 2000 to 5900: exponents of each token, a second exponential, V's conversion beside it. Between two
-// units of a CTA lie 5000 to 11000 cycles, ahead of the first weights 24000 to 35000: the launch,
+// tenths of it: logits out of tensor memory 390 cycles, weights 1350 (16384 exponentials, 4 cycles
+// for a warp's 32, a quarter of them for each quarter of an SM: 512; sums and roundings), weights
+// into tensor memory 350, and 300 until the next S. All eight share a step, so none of these
+// hides another's; the products are done ahead of them. A step with exponents for each token takes
+// 1800 to 6000: these, a second exponential, masks, V's conversion beside it. Between two units
+// of a CTA lie 6000 to 12000 cycles, ahead of the first weights 24000 to 32000: the launch,
 // the plan, a chain of four loads, queries, and code that all SMs fetch at once. Measured:
-//   8 heads, G = 4, fp16, e4m3, 16 requests of 4096 tokens, 26 drafts    59 us (by bytes 21)
-//   8 heads, G = 8, bf16, int8, 8 of 32768, 64 drafts                   551 us, 1000 TFLOP/s
+//   8 heads, G = 4, fp16, e4m3, 16 requests of 4096 tokens, 26 drafts    60 us (by bytes 21)
+//   8 heads, G = 8, bf16, int8, 8 of 32768, 64 drafts                   552 us, 1000 TFLOP/s
 //     (52 % of a plain matrix product's rate)
 //   4 heads, G = 7, bf16, e4m3, 32 of 1024 to 16384, window 4096         55 us
-//   8 heads, G = 5, fp16, int8, 64 of 1 to 3000, chains of 5             90 us
-//   8 heads, G = 4, fp16, e4m3, one of 300 tokens, 8 drafts              11.4 us
+//   8 heads, G = 5, fp16, int8, 64 of 1 to 3000, chains of 5             92 us
+//   8 heads, G = 4, fp16, e4m3, one of 300 tokens, 8 drafts              11.6 us
 // Tried and slower: 64 tokens a step (the second: 0.92 ms); conversion by the softmax warps
 // (the chains: 196 us); maxima of each step ahead of its weights (the second: 0.66 ms; now
 // they are taken when a weight could leave fp16's range); conversion unrolled over its tiles
