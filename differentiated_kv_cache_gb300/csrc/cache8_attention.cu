@@ -43,7 +43,8 @@
 // with; else s_v is the power of two that brings their largest |v| to
 // [128, 256), the size of codes, so that equal weights stand for equal
 // contributions; their values are divided by it (exact but for values 2^-20 and
-// less of the largest).
+// less of the largest). Codes that lie far under their scale in a block that the
+// window cuts are raised likewise (raise_codes).
 #include <algorithm>
 
 #include "cache8.cuh"
@@ -176,7 +177,43 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, uint4 (&w)[4]) {
   for (int j = 0; j < 4; j++) w[j] = *reinterpret_cast<const uint4*>(p + 512 * j);
 }
 
-// A tile of codes at p (K, then V); edge: some token may not be visible.
+// V codes whose largest lies 2^4 or more under what their block's scale allows, as in a block
+// that the window cuts, whose scale may be set by a token out of sight (left so, a hidden V
+// 2^23 above the others put their weights among fp16's subnormals): as codes 2^n times as large, exactly.
+// The exponent of 2 that joins V's scale lv; zeros count as of the smallest scale, 2^-100.
+template <int CODE>
+__device__ __forceinline__ float raise_codes(uint4 (&vw)[4], float lv) {
+  constexpr int kFull = CODE == DKV_E4M3 ? 7 : 6;        // the largest binade that codes fill (448, 127)
+  uint32_t* w = reinterpret_cast<uint32_t*>(vw);
+  uint32_t am = 0;          // magnitudes order like their bits
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    uint32_t a, b;
+    code_halves<CODE>(w[i], a, b);
+    am = __vmaxu2(am, __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu));
+  }
+  am = __reduce_max_sync(0xffffffffu, max(am & 0xffffu, am >> 16));
+  if (am == 0) return -100.0f - lv;
+  const int n = min(14, kFull + 15 - (int)(am >> 10));       // (the least code, 2^-9, is a normal number in fp16)
+  if (n < 4 || am >= 0x7c00u) return 0.0f;
+  const uint32_t f = (uint32_t)(15 + n) * 0x04000400u;
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    if (CODE == DKV_E4M3) {
+      asm("{\n .reg .b16 a, b;\n .reg .b32 x, y;\n mov.b32 {a, b}, %0;\n cvt.rn.f16x2.e4m3x2 x, a;\n cvt.rn.f16x2.e4m3x2 y, b;\n"
+          " mul.rn.f16x2 x, x, %1;\n mul.rn.f16x2 y, y, %1;\n cvt.rn.satfinite.e4m3x2.f16x2 a, x;\n"
+          " cvt.rn.satfinite.e4m3x2.f16x2 b, y;\n mov.b32 %0, {a, b};\n}\n"
+          : "+r"(w[i])
+          : "r"(f));
+    } else {
+      w[i] = w[i] << n & (0xffu << n & 0xffu) * 0x01010101u;
+    }
+  }
+  return -(float)n;
+}
+
+// A tile of codes at p (K, then V); edge: some token may not be visible, of the tile
+// or of its block.
 template <int CODE>
 __device__ __forceinline__ void code_tile(State& s, const uint32_t (&qf)[16], const uint8_t* p, bool edge,
                                           const See& see, const float (&ks)[2], float lv) {
@@ -207,6 +244,10 @@ __device__ __forceinline__ void code_tile(State& s, const uint32_t (&qf)[16], co
       vw[j].z &= see.v;
       vw[j].w &= see.v;
     }
+    const float more = raise_codes<CODE>(vw, lv);
+#pragma unroll
+    for (int e = 0; e < 4; e++) x[e] += more;
+    lv += more;
   }
   raise(s, x, lv, 0.0f);
   weights(s, x, lv);
@@ -707,6 +748,8 @@ __global__ void __launch_bounds__(kA8Warps * 32)
         }
         nxt.sc = *reinterpret_cast<const float2*>(c.scales + 2 * ((size_t)page * hkv + h));
         nxt.src = c.pages + c.page_head(page, h) + (size_t)(nxt.tile & ((1 << per) - 1)) * (2 * kTile);
+        const int start = nxt.tile >> per << (per + 4);        // of the block
+        nxt.edge = nxt.edge || (a.window > 0 && start < n - a.window && start + c.T > a.sinks);
       } else {
         nxt.src = c.tail + c.tail_head(slot, h) + (size_t)(nxt.tile - t.full) * (4 * kTile);
         nxt.tail = true;

@@ -1366,3 +1366,28 @@ def test_attention_of_bf16_queries_of_any_size(code, amp):
         out = c.attend(None, lens, q)
         assert torch.isfinite(out).all()
         c.check_attention(out, range(len(lens)), lens, q)
+
+
+@pytest.mark.parametrize("code", [E4M3, INT8])
+@pytest.mark.parametrize("elem,what,size", [(F16, "k", 6e4), (F16, "v", 6e4), (BF16, "k", 1e18), (BF16, "v", 3e4), (BF16, "v", 1e7),
+                                            (BF16, "v", 1e9), (BF16, "v", -3e38)])
+@pytest.mark.parametrize("T,G,sinks", [(128, 1, 0), (64, 4, 20), (32, 8, 5)])
+def test_decode_of_blocks_that_the_window_cuts(elem, code, what, size, T, G, sinks):
+    """Decode attention beside stored tokens of any size that are out of sight, where a warp has
+    many tiles (hundreds of requests over one slot)."""
+    rng = np.random.default_rng(62)
+    n, reqs = 1000, 200
+    c = Cache(1, G, T, 1, n // T + 1, elem, code, seed=21, fill=float("nan"))
+    k, v = c.vec(rng, n, 1), c.vec(rng, n, 1)
+    x = k if what == "k" else v
+    hidden = T + 9
+    x[[hidden, sinks + 1]] = size
+    c.append([0], [0], [n], k, v)
+    q = c.vec(rng, reqs, G)
+    c.c = _dkv().make_cache8(c.pages, c.scales, c.tail, c.table, group_size=G, max_req=reqs)
+    window = n - hidden - 1
+    out = c.attend([0] * reqs, [n] * reqs, q, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert c.c.status_words.tolist() == [0, 0]
+    rows = [0, 1, 77, 198, 199]
+    c.check_attention(out[rows], [0] * 5, [n] * 5, q[rows], window=window, sinks=sinks)
